@@ -425,6 +425,135 @@ int32_t tqd_op_attention_noalloc(const float* q, const float* K, const float* V,
                                  int32_t n_chunks, float* out, void* stream);
 size_t tqd_op_attention_noalloc_max_scratch(void);
 
+/* ------------------------------------------------------------------------
+ * Operators of a decode step in 4 bits: a paged cache of 4-bit keys and
+ * values, the attention that reads it, matrix-vector products with Q4_0
+ * weights, and the log probabilities of the resulting logits.  As the
+ * operator entry points above: device pointers owned by the caller, on
+ * `stream`, nothing allocated, every argument the host can see checked before
+ * anything is launched (BAD_ARG, with tqd_last_error()).  A call with no rows
+ * (n_tokens, n or rows 0) launches nothing.  Every call may be captured into a
+ * CUDA graph; a scratch may be shared by calls that do not overlap on the GPU
+ * (one stream, or graphs replayed one after the other) and needs no clearing.
+ * Results do not depend on the run: no sum's order is left to chance.
+ * ------------------------------------------------------------------------ */
+
+/* A paged cache in 4 bits for one layer.  Position p of sequence s lives in
+ * page page_table[s * table_stride + p / page_size], at position
+ * p % page_size.  A page holds n_kv_heads runs of page_size / 16 blocks; a block is
+ * 16 positions of one head, 18 * head_dim bytes:
+ *   K codes  [16][head_dim / 2] bytes: the row of position b (0..15) is row
+ *            8 * ((b / 2) % 2) + 2 * (b / 4) + b % 2; in a row, element d = 32 g
+ *            + 8 c + i is nibble i of the 32-bit word c * (head_dim / 32) + g;
+ *   K scales f16 [16][head_dim / 32];
+ *   V codes: element n + 8 i of position b is nibble i of a piece of
+ *            head_dim / 16 bytes at, for head_dim 128,
+ *            512 * ((b / 2) % 2) + 128 * (b / 4) + 16 * n + 8 * (b % 2), for 64
+ *            128 * (b / 4) + 16 * n + 4 * (b % 4);
+ *   V scales f16 [16][head_dim / 32].
+ * Codes and scales of a group of 32 consecutive elements y of a row: scale =
+ * f16(max|y| / 7), code = rint(7 y / max|y|) + 8 (1..15; 8 when all are 0), of the
+ * exact values; an element stands for (code - 8) * scale, so an error of at
+ * most half a step, max|y| / 14, and the scale's rounding.  A group that holds
+ * a NaN or an infinity, or whose scale passes the f16 range, has the scale
+ * 0x7E00 and codes of 8: it stands for NaN. */
+typedef struct tqd_kv_q4 {
+  uint8_t* pages;            /* [n_pages][tqd_kv_q4_page_bytes()], 16-byte aligned */
+  const int32_t* page_table; /* [n_seq][table_stride] page indices */
+  int32_t n_pages;
+  int32_t page_size;         /* positions per page, a multiple of 16 */
+  int32_t n_kv_heads;
+  int32_t head_dim;          /* 64 or 128 */
+  int32_t n_seq;
+  int32_t table_stride;      /* pages per sequence in the table */
+} tqd_kv_q4;
+
+/* Bytes of one page (0 for sizes the cache does not take). */
+size_t tqd_kv_q4_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_size);
+
+/* Rotate the query and key heads of n_tokens tokens by their positions and
+ * store the keys and values in the cache.  Token i is position positions[i]
+ * of sequence seqs[i] (seqs NULL: of sequence i; n_tokens <= n_seq then).
+ * k, v: f32 rows of n_kv_heads * head_dim, k_stride and v_stride floats apart;
+ * q, q_out: f32 rows of n_heads * head_dim (q NULL with n_heads 0: none), which
+ * may be the same rows; rows may be slices of one fused projection.
+ * rope_table: from tqd_op_rope_table with max_pos positions (NULL: no
+ * rotation); the rotation is the half-split one of tqd_op_rope, and the codes
+ * are those of the exactly rotated keys.
+ * A token whose sequence is outside [0, n_seq) or whose position is negative
+ * or (with a table) at or past max_pos is padding: nothing is written for it.
+ * A position past the page table, or a page outside [0, n_pages), stores no
+ * row (q is rotated all the same).  Two tokens of one call at one (sequence,
+ * position) leave that row unspecified. */
+int32_t tqd_op_kv_append_q4(const tqd_kv_q4* cache, const float* k, int64_t k_stride, const float* v,
+                            int64_t v_stride, const int32_t* positions, const int32_t* seqs, int32_t n_tokens,
+                            const float* rope_table, int32_t max_pos, const float* q, int64_t q_stride,
+                            int32_t n_heads, float* q_out, int64_t q_out_stride, void* stream);
+
+/* Read rows back as the f32 values they stand for (k_out or v_out may be
+ * NULL): e.g. to hand a paged sequence over to tqd_kv_upload.  Rows that are
+ * not in the cache (sequence, position or page out of range) read as NaN. */
+int32_t tqd_op_kv_read_q4(const tqd_kv_q4* cache, const int32_t* positions, const int32_t* seqs, int32_t n_tokens,
+                          float* k_out, int64_t k_stride, float* v_out, int64_t v_stride, void* stream);
+
+/* Attention of n_tokens query tokens over the cache: out = softmax(q . K /
+ * sqrt(head_dim)) V per head, query head h reading kv head
+ * h / (n_heads / n_kv_heads).  lens[s] (device) is the number of cached positions of
+ * sequence s.  q_start NULL: token s is the one query of sequence s, at
+ * position lens[s] - 1 (n_tokens == n_seq).  Otherwise q_start [n_seq + 1]
+ * (device, non-decreasing from 0): tokens q_start[s] .. q_start[s + 1] - 1 are the
+ * last positions of sequence s, and each sees the positions up to its own (a
+ * prompt's tile, or a draft's tokens).  A query that sees nothing (an empty
+ * sequence, or more queries than positions) gets zeros; rows at or past
+ * q_start[n_seq] stay as they were.  q, out: f32 rows of n_heads *
+ * head_dim, q_stride and out_stride floats apart; out may not overlap q.
+ * A page outside [0, n_pages), or a length past the page table, makes the
+ * queries that see it NaN.  At most 1024 sequences.  scratch: caller-owned
+ * device memory of tqd_attention_q4_scratch_bytes(head_dim) bytes, 16-byte
+ * aligned, whatever its contents. */
+int32_t tqd_op_attention_q4(const tqd_kv_q4* cache, const float* q, int64_t q_stride, const int32_t* lens,
+                            const int32_t* q_start, int32_t n_tokens, int32_t n_heads, float* out,
+                            int64_t out_stride, void* scratch, void* stream);
+size_t tqd_attention_q4_scratch_bytes(int32_t head_dim);
+
+/* Repack a Q4_0 matrix from 18-byte blocks (rows x cols / 32 of them: an f16
+ * scale d little-endian, then 16 bytes, byte j holding element j in its low
+ * nibble and element j + 16 in its high one; a weight is (nibble - 8) * d) into the
+ * library's tiles: tqd_q4_0_matrix_bytes(rows, cols) bytes, 16-byte aligned,
+ * [rows / 16 up][cols / 128 up] of 1152 bytes: the codes, 32-bit words
+ * [row % 16][c 0..3][group 0..3] of the eight codes 8 c .. 8 c + 7 of a
+ * group, then f16 scales [row % 16][group]; padding has scale 0.
+ * cols % 32 == 0, cols <= 16384. */
+int32_t tqd_op_q4_0_repack(const uint8_t* w_blocks, int64_t rows, int64_t cols, uint8_t* w_tiles, void* stream);
+size_t tqd_q4_0_matrix_bytes(int64_t rows, int64_t cols);
+
+/* y[j] = W x[j] for n vectors (n <= 64) over a repacked Q4_0 matrix: x f32
+ * [n][cols], y f32 [n][rows], their rows x_stride and y_stride floats apart.
+ * f32 accuracy: the weights are exact, x is carried to 22 bits below its
+ * largest element's exponent (or finer), sums are f32.  A scale that is NaN or
+ * infinite makes its row NaN (or infinite); so does an x that holds one. */
+int32_t tqd_op_q4_0_matvec(const uint8_t* w_tiles, int64_t rows, int64_t cols, const float* x, int32_t n,
+                           int64_t x_stride, float* y, int64_t y_stride, void* stream);
+
+/* Log probabilities of `rows` rows of logits, f32 [vocab] each, stride floats
+ * apart: with p = softmax(row),
+ *   logprob[r]          = log p[targets[r]] (NaN for a target outside [0, vocab));
+ *   entropy[r]          = -sum p log p;
+ *   top_ids[r][0..top_k)      the most likely tokens, descending, equal logits
+ *                             by ascending index (-1 past the last token whose
+ *                             logit is above -inf), top_k <= 32;
+ *   top_logprobs[r][0..top_k) their log p (-inf past the last).
+ * A NaN logit counts as -inf (as in the argmax and the sampler).  Logits of
+ * +inf share the probability.  A row with no logit above -inf has log p -inf
+ * everywhere and entropy 0.  targets and logprob go together and may be NULL,
+ * entropy may be NULL, top_k may be 0.  scratch: caller-owned device memory
+ * of tqd_logprobs_scratch_bytes(rows, vocab, top_k) bytes, 16-byte aligned,
+ * whatever its contents. */
+int32_t tqd_op_logprobs(const float* logits, int64_t stride, int32_t rows, int32_t vocab, const int32_t* targets,
+                        float* logprob, float* entropy, int32_t top_k, int32_t* top_ids, float* top_logprobs,
+                        void* scratch, void* stream);
+size_t tqd_logprobs_scratch_bytes(int32_t rows, int32_t vocab, int32_t top_k);
+
 #ifdef __cplusplus
 }
 #endif

@@ -51,6 +51,12 @@ class tqd_sampling(ctypes.Structure):
                 ("seed", ctypes.c_uint64)]
 
 
+class tqd_kv_q4(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("n_seq", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
 class TQDError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -111,6 +117,17 @@ def lib():
         "tqd_sample_scratch_bytes": (sz, [i32]),
         "tqd_op_attention_noalloc": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
         "tqd_op_attention_noalloc_max_scratch": (sz, []),
+        "tqd_kv_q4_page_bytes": (sz, [i32, i32, i32]),
+        "tqd_op_kv_append_q4": (i32, [P(tqd_kv_q4), vp, i64, vp, i64, vp, vp, i32, vp, i32, vp, i64, i32, vp, i64,
+                                      vp]),
+        "tqd_op_kv_read_q4": (i32, [P(tqd_kv_q4), vp, vp, i32, vp, i64, vp, i64, vp]),
+        "tqd_op_attention_q4": (i32, [P(tqd_kv_q4), vp, i64, vp, vp, i32, i32, vp, i64, vp, vp]),
+        "tqd_attention_q4_scratch_bytes": (sz, [i32]),
+        "tqd_op_q4_0_repack": (i32, [vp, i64, i64, vp, vp]),
+        "tqd_q4_0_matrix_bytes": (sz, [i64, i64]),
+        "tqd_op_q4_0_matvec": (i32, [vp, i64, i64, vp, i32, i64, vp, i64, vp]),
+        "tqd_op_logprobs": (i32, [vp, i64, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp]),
+        "tqd_logprobs_scratch_bytes": (sz, [i32, i32, i32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -131,6 +148,9 @@ def exported_symbols():
         "tqd_op_bf16_matvec", "tqd_op_rmsnorm", "tqd_op_rope_table", "tqd_op_rope", "tqd_op_attention",
         "tqd_attention_scratch_bytes", "tqd_op_wait_selftest", "tqd_op_silu_mul", "tqd_op_argmax", "tqd_argmax_scratch_bytes",
         "tqd_op_sample", "tqd_sample_scratch_bytes", "tqd_op_attention_noalloc", "tqd_op_attention_noalloc_max_scratch",
+        "tqd_kv_q4_page_bytes", "tqd_op_kv_append_q4", "tqd_op_kv_read_q4", "tqd_op_attention_q4",
+        "tqd_attention_q4_scratch_bytes", "tqd_op_q4_0_repack", "tqd_q4_0_matrix_bytes", "tqd_op_q4_0_matvec",
+        "tqd_op_logprobs", "tqd_logprobs_scratch_bytes",
     ]
 
 

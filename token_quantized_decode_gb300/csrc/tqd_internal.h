@@ -152,6 +152,40 @@ cudaError_t launch_sample(const DevSeq* seqs, int n, int V, int max_seq, const S
 // Validate the caller's sampling controls into a, and say whether they are greedy.
 int32_t sampling_args(const ::tqd_sampling* p, SampleArgs& a, bool* greedy);
 
+// The paged Q4 cache (tqd_q4_cache.cu, tqd_q4_attention.cu), Q4_0 weights
+// (tqd_q4_matvec.cu) and log probabilities (tqd_logprobs.cu): operator entry
+// points' kernels.  Row strides are in elements.
+struct Q4Cache;
+cudaError_t launch_kv_append_q4(const Q4Cache& c, int hd, const float* k, int64_t k_stride, const float* v,
+                                int64_t v_stride, const int32_t* positions, const int32_t* seqs, int n_tokens,
+                                const float2* rope, int max_pos, const float* q, int64_t q_stride, int n_heads,
+                                float* q_out, int64_t qo_stride, cudaStream_t st);
+cudaError_t launch_kv_read_q4(const Q4Cache& c, int hd, const int32_t* positions, const int32_t* seqs, int n_tokens,
+                              float* k_out, int64_t k_stride, float* v_out, int64_t v_stride, cudaStream_t st);
+struct Q4AttnArgs;
+constexpr int kQ4MaxSeqs = 1024;
+size_t attention_q4_scratch_bytes(int hd);
+cudaError_t launch_attention_q4(const Q4AttnArgs& a, int hd, cudaStream_t st);
+constexpr int kQ4MatvecMaxVectors = 64;
+constexpr int kQ4MatvecMaxCols = 16384;
+cudaError_t launch_q4_repack(const uint8_t* src, int64_t rows, int64_t cols, uint8_t* dst, cudaStream_t st);
+cudaError_t launch_q4_matvec(const uint8_t* w, int rows, int cols, const float* x, int n, int64_t x_stride, float* y,
+                             int64_t y_stride, cudaStream_t st);
+struct LogprobArgs {
+  const float* logits;
+  const int32_t* targets;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  void* scratch;
+  int64_t stride;
+  int rows, vocab, top_k;
+};
+constexpr int kLogprobMaxTopK = 32;
+size_t logprobs_scratch_bytes(int rows, int vocab, int top_k);
+cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st);
+
 // The bounded-wait self-test (tqd_op_wait_selftest): runs it on st and
 // returns the error bits its waits set.
 cudaError_t run_wait_selftest(uint32_t* err_bits, cudaStream_t st);

@@ -6,6 +6,7 @@
 
 #include "tqd.h"
 #include "tqd_internal.h"
+#include "tqd_q4.cuh"
 
 using namespace tqd;
 
@@ -21,6 +22,29 @@ size_t attn_scratch_floats_o(int32_t nq, int32_t hd, int32_t nch) {
   return static_cast<size_t>(nq) * nch * hd;
 }
 size_t attn_scratch_floats_ml(int32_t nq, int32_t nch) { return static_cast<size_t>(nq) * nch * 2; }
+
+int32_t refuse(const char* why) {
+  set_last_error(why);
+  return TQD_ERR_BAD_ARG;
+}
+
+size_t q4_page_bytes(int32_t n_kv, int32_t hd, int32_t page_size) {
+  if (n_kv <= 0 || (hd != 64 && hd != 128) || page_size <= 0 || page_size % kQ4Block || page_size > (1 << 20))
+    return 0;
+  return static_cast<size_t>(n_kv) * (page_size / kQ4Block) * q4_block_bytes(hd);
+}
+
+// The caller's cache descriptor as the kernels take it; TQD_OK or a refusal.
+int32_t q4_cache(const tqd_kv_q4* c, Q4Cache& o) {
+  if (!c || !c->pages || !c->page_table) return refuse("tqd_kv_q4: NULL cache, pages or page_table");
+  const size_t pb = q4_page_bytes(c->n_kv_heads, c->head_dim, c->page_size);
+  if (!pb) return refuse("tqd_kv_q4: n_kv_heads >= 1, head_dim 64 or 128, page_size a positive multiple of 16");
+  if (c->n_pages <= 0 || c->n_seq <= 0 || c->table_stride <= 0)
+    return refuse("tqd_kv_q4: n_pages, n_seq and table_stride must be positive");
+  if (reinterpret_cast<uintptr_t>(c->pages) % 16) return refuse("tqd_kv_q4: pages must be 16-byte aligned");
+  o = Q4Cache{c->pages, c->page_table, c->n_pages, c->page_size, c->n_kv_heads, c->n_seq, c->table_stride, pb};
+  return TQD_OK;
+}
 
 }  // namespace
 
@@ -164,6 +188,117 @@ int32_t tqd_op_sample(const float* logits, int32_t vocab, int32_t* tokens, int32
   if (e == cudaSuccess) e = cudaMemsetAsync(h.scnt, 0, 4 * v4, s);
   if (e == cudaSuccess) e = launch_sample(dseq, 1, vocab, n_inputs, a, s);
   return status_of(e);
+}
+
+size_t tqd_kv_q4_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_size) {
+  return q4_page_bytes(n_kv_heads, head_dim, page_size);
+}
+
+int32_t tqd_op_kv_append_q4(const tqd_kv_q4* cache, const float* k, int64_t k_stride, const float* v,
+                            int64_t v_stride, const int32_t* positions, const int32_t* seqs, int32_t n_tokens,
+                            const float* rope_table, int32_t max_pos, const float* q, int64_t q_stride,
+                            int32_t n_heads, float* q_out, int64_t q_out_stride, void* stream) {
+  Q4Cache c;
+  if (const int32_t rc = q4_cache(cache, c)) return rc;
+  if (!n_tokens) return TQD_OK;
+  if (!k || !v || !positions || n_tokens < 0 || (rope_table && max_pos <= 0))
+    return refuse("tqd_op_kv_append_q4: NULL k, v or positions, n_tokens < 0, or a table without positions");
+  if (!seqs && n_tokens > c.n_seq) return refuse("tqd_op_kv_append_q4: more tokens than sequences and no seqs");
+  if (q ? n_heads <= 0 || !q_out : n_heads != 0)
+    return refuse("tqd_op_kv_append_q4: q needs n_heads > 0 and q_out; without q n_heads must be 0");
+  const int64_t kvw = static_cast<int64_t>(c.n_kv) * cache->head_dim, qw = static_cast<int64_t>(n_heads) * cache->head_dim;
+  if (k_stride < kvw || v_stride < kvw || (q && (q_stride < qw || q_out_stride < qw)))
+    return refuse("tqd_op_kv_append_q4: a row stride shorter than the row");
+  if (static_cast<int64_t>(n_tokens) * (c.n_kv + static_cast<int64_t>(n_heads)) > (1ll << 33))
+    return refuse("tqd_op_kv_append_q4: n_tokens * (n_kv_heads + n_heads) above 2^33");
+  return status_of(launch_kv_append_q4(c, cache->head_dim, k, k_stride, v, v_stride, positions, seqs, n_tokens,
+                                       reinterpret_cast<const float2*>(rope_table), max_pos, q, q_stride, n_heads,
+                                       q_out, q_out_stride, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t tqd_op_kv_read_q4(const tqd_kv_q4* cache, const int32_t* positions, const int32_t* seqs, int32_t n_tokens,
+                          float* k_out, int64_t k_stride, float* v_out, int64_t v_stride, void* stream) {
+  Q4Cache c;
+  if (const int32_t rc = q4_cache(cache, c)) return rc;
+  if (!n_tokens) return TQD_OK;
+  if (!positions || (!k_out && !v_out) || n_tokens < 0)
+    return refuse("tqd_op_kv_read_q4: NULL positions, no output, or n_tokens < 0");
+  if (!seqs && n_tokens > c.n_seq) return refuse("tqd_op_kv_read_q4: more tokens than sequences and no seqs");
+  const int64_t kvw = static_cast<int64_t>(c.n_kv) * cache->head_dim;
+  if ((k_out && k_stride < kvw) || (v_out && v_stride < kvw))
+    return refuse("tqd_op_kv_read_q4: a row stride shorter than the row");
+  if (static_cast<int64_t>(n_tokens) * c.n_kv > (1ll << 33)) return refuse("tqd_op_kv_read_q4: n_tokens * n_kv_heads above 2^33");
+  return status_of(launch_kv_read_q4(c, cache->head_dim, positions, seqs, n_tokens, k_out, k_stride, v_out, v_stride,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t tqd_attention_q4_scratch_bytes(int32_t head_dim) {
+  return head_dim == 64 || head_dim == 128 ? attention_q4_scratch_bytes(head_dim) : 0;
+}
+
+int32_t tqd_op_attention_q4(const tqd_kv_q4* cache, const float* q, int64_t q_stride, const int32_t* lens,
+                            const int32_t* q_start, int32_t n_tokens, int32_t n_heads, float* out, int64_t out_stride,
+                            void* scratch, void* stream) {
+  Q4Cache c;
+  if (const int32_t rc = q4_cache(cache, c)) return rc;
+  if (!n_tokens && q_start) return TQD_OK;
+  if (!q || !lens || !out || !scratch || n_tokens < 0 || n_heads <= 0 || n_heads % c.n_kv)
+    return refuse("tqd_op_attention_q4: NULL pointer, n_tokens < 0, or n_heads no multiple of n_kv_heads");
+  if (c.n_seq > kQ4MaxSeqs) return refuse("tqd_op_attention_q4: more than 1024 sequences");
+  if (!q_start && n_tokens != c.n_seq) return refuse("tqd_op_attention_q4: without q_start one query per sequence");
+  const int64_t qw = static_cast<int64_t>(n_heads) * cache->head_dim;
+  if (q_stride < qw || out_stride < qw) return refuse("tqd_op_attention_q4: a row stride shorter than the row");
+  if (reinterpret_cast<uintptr_t>(scratch) % 16) return refuse("tqd_op_attention_q4: scratch must be 16-byte aligned");
+  if (static_cast<int64_t>(n_tokens) * n_heads > (1ll << 30))
+    return refuse("tqd_op_attention_q4: n_tokens * n_heads above 2^30");
+  const Q4AttnArgs a{c, q, out, lens, q_start, scratch, q_stride, out_stride, n_tokens, n_heads,
+                     cache->head_dim == 128 ? 0.08838834764831845f : 0.125f};
+  return status_of(launch_attention_q4(a, cache->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+size_t tqd_q4_0_matrix_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || cols % 32) return 0;
+  return static_cast<size_t>((rows + kQ4TileRows - 1) / kQ4TileRows) *
+         static_cast<size_t>((cols + kQ4TileCols - 1) / kQ4TileCols) * kQ4TileBytes;
+}
+
+int32_t tqd_op_q4_0_repack(const uint8_t* w_blocks, int64_t rows, int64_t cols, uint8_t* w_tiles, void* stream) {
+  if (!w_blocks || !w_tiles || rows <= 0 || rows > (1ll << 30) || cols <= 0 || cols % 32 || cols > kQ4MatvecMaxCols)
+    return refuse("tqd_op_q4_0_repack: NULL pointer, or cols no multiple of 32 up to 16384");
+  if (tqd_q4_0_matrix_bytes(rows, cols) / kQ4TileBytes > 0x7FFFFFFFull) return refuse("tqd_op_q4_0_repack: matrix too large");
+  if (reinterpret_cast<uintptr_t>(w_tiles) % 16) return refuse("tqd_op_q4_0_repack: w_tiles must be 16-byte aligned");
+  return status_of(launch_q4_repack(w_blocks, rows, cols, w_tiles, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t tqd_op_q4_0_matvec(const uint8_t* w_tiles, int64_t rows, int64_t cols, const float* x, int32_t n,
+                           int64_t x_stride, float* y, int64_t y_stride, void* stream) {
+  if (!n) return TQD_OK;
+  if (!w_tiles || !x || !y || rows <= 0 || rows > (1ll << 30) || cols <= 0 || cols % 32 || cols > kQ4MatvecMaxCols ||
+      n < 0 || n > kQ4MatvecMaxVectors)
+    return refuse("tqd_op_q4_0_matvec: NULL pointer, cols no multiple of 32 up to 16384, or n above 64");
+  if (n > 1 && (x_stride < cols || y_stride < rows)) return refuse("tqd_op_q4_0_matvec: a row stride shorter than the row");
+  if (reinterpret_cast<uintptr_t>(w_tiles) % 16) return refuse("tqd_op_q4_0_matvec: w_tiles must be 16-byte aligned");
+  return status_of(launch_q4_matvec(w_tiles, static_cast<int>(rows), static_cast<int>(cols), x, n, x_stride, y, y_stride,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+size_t tqd_logprobs_scratch_bytes(int32_t rows, int32_t vocab, int32_t top_k) {
+  if (rows <= 0 || vocab <= 0 || top_k < 0 || top_k > kLogprobMaxTopK) return 0;
+  return logprobs_scratch_bytes(rows, vocab, top_k);
+}
+
+int32_t tqd_op_logprobs(const float* logits, int64_t stride, int32_t rows, int32_t vocab, const int32_t* targets,
+                        float* logprob, float* entropy, int32_t top_k, int32_t* top_ids, float* top_logprobs,
+                        void* scratch, void* stream) {
+  if (!rows) return TQD_OK;
+  if (!logits || !scratch || rows < 0 || vocab <= 0 || stride < vocab || top_k < 0 || top_k > kLogprobMaxTopK)
+    return refuse("tqd_op_logprobs: NULL logits or scratch, rows < 0, vocab < 1, stride < vocab, or top_k above 32");
+  if (!targets != !logprob) return refuse("tqd_op_logprobs: targets and logprob go together");
+  if (top_k ? !top_ids || !top_logprobs : !logprob && !entropy)
+    return refuse("tqd_op_logprobs: top_k needs top_ids and top_logprobs; nothing else asked for");
+  if (reinterpret_cast<uintptr_t>(scratch) % 16) return refuse("tqd_op_logprobs: scratch must be 16-byte aligned");
+  const LogprobArgs a{logits, targets, logprob, entropy, top_ids, top_logprobs, scratch, stride, rows, vocab, top_k};
+  return status_of(launch_logprobs(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

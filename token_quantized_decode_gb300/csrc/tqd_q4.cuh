@@ -1,0 +1,66 @@
+// The 4-bit formats: the paged Q4 cache and the tiled Q4_0 weights (contracts
+// in tqd.h), and the tensor-core pieces the kernels over them share.
+//
+// Both keep the nibbles of one group of 32 where one mma.sync operand lane
+// needs them: a 32-bit word holds eight codes of a group, and
+//   word & 0x000F000F         codes 0 and 4 in the low bits of two f16
+//   word & 0x00F000F0         codes 1 and 5, times 16
+//   (word >> 8) & ...         codes 2, 6 and 3, 7
+// are f16 subnormals, code * 2^-24 and code * 2^-20 exactly, so a pair of
+// codes becomes a matrix operand in one instruction and no conversion.  The
+// factors are undone exactly: the 16 on the other operand, 2^24 on the sums.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "tqd_device.cuh"
+
+namespace tqd {
+
+constexpr int kQ4Block = 16;  // positions per cache block
+
+// Bytes of one cache block (16 positions of one head): K codes, K scales, V codes, V scales.
+__host__ __device__ constexpr int q4_block_bytes(int hd) { return 18 * hd; }
+__host__ __device__ constexpr int q4_ks_off(int hd) { return 8 * hd; }
+__host__ __device__ constexpr int q4_v_off(int hd) { return 9 * hd; }
+__host__ __device__ constexpr int q4_vs_off(int hd) { return 17 * hd; }
+
+// Byte offset inside the block of the K row of position b (0..15): rows are
+// stored in the order the score's tensor-core operand takes them.
+__host__ __device__ constexpr int q4_k_row(int b, int hd) {
+  return (((b >> 1) & 1) * 8 + (b >> 2) * 2 + (b & 1)) * (hd / 2);
+}
+// Byte offset (from the block's start) of the 2 * hd / 32 bytes that hold, for
+// position b, the codes of elements n, n + 8, n + 16, ... (nibble i: element n + 8 i).
+__host__ __device__ constexpr int q4_v_piece(int b, int n, int hd) {
+  return q4_v_off(hd) + (hd == 128 ? ((b >> 1) & 1) * 512 + (b >> 2) * 128 + n * 16 + (b & 1) * 8
+                                   : (b >> 2) * 128 + n * 16 + (b & 3) * 4);
+}
+
+struct Q4Cache {
+  uint8_t* pages;
+  const int32_t* table;
+  int n_pages, page_size, n_kv, n_seq, table_stride;
+  size_t page_bytes;
+};
+
+struct Q4AttnArgs {
+  Q4Cache c;
+  const float* q;
+  float* out;
+  const int32_t* lens;
+  const int32_t* q_start;  // [n_seq + 1], or null: one query per sequence
+  void* scratch;
+  int64_t q_stride, out_stride;
+  int n_tokens, n_heads;
+  float scale;             // 1 / sqrt(head_dim)
+};
+
+// Tiles of Q4_0 weights: 16 rows x 128 columns.
+constexpr int kQ4TileRows = 16;
+constexpr int kQ4TileCols = 128;
+constexpr int kQ4TileBytes = 1152;
+constexpr int kQ4TileScales = 1024;  // offset of the scales, f16 [16][4]
+
+}  // namespace tqd
