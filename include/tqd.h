@@ -529,14 +529,15 @@ size_t tqd_q4_0_matrix_bytes(int64_t rows, int64_t cols);
 
 /* y[j] = W x[j] for n vectors (n <= 64) over a repacked Q4_0 matrix: x f32
  * [n][cols], y f32 [n][rows], their rows x_stride and y_stride floats apart.
- * f32 accuracy: the weights are exact, x is carried to 22 bits below its
- * largest element's exponent (or finer), sums are f32.  A scale that is NaN or
- * infinite makes its row NaN (or infinite); so does an x that holds one. */
+ * f32 accuracy: the weights are exact, each 32 elements of x are carried to 22
+ * bits below their largest one's exponent (or finer), sums are f32.  A scale
+ * that is NaN or infinite makes its row NaN (or infinite); an x with an
+ * element that is NaN, infinite or of magnitude 2^113 or more gives NaN. */
 int32_t tqd_op_q4_0_matvec(const uint8_t* w_tiles, int64_t rows, int64_t cols, const float* x, int32_t n,
                            int64_t x_stride, float* y, int64_t y_stride, void* stream);
 
-/* Log probabilities of `rows` rows of logits, f32 [vocab] each, stride floats
- * apart: with p = softmax(row),
+/* Log probabilities of `rows` rows of logits, f32 [vocab <= 2^30] each, stride
+ * floats apart: with p = softmax(row),
  *   logprob[r]          = log p[targets[r]] (NaN for a target outside [0, vocab));
  *   entropy[r]          = -sum p log p;
  *   top_ids[r][0..top_k)      the most likely tokens, descending, equal logits

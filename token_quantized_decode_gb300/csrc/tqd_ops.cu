@@ -283,7 +283,7 @@ int32_t tqd_op_q4_0_matvec(const uint8_t* w_tiles, int64_t rows, int64_t cols, c
 }
 
 size_t tqd_logprobs_scratch_bytes(int32_t rows, int32_t vocab, int32_t top_k) {
-  if (rows <= 0 || vocab <= 0 || top_k < 0 || top_k > kLogprobMaxTopK) return 0;
+  if (rows <= 0 || vocab <= 0 || vocab > (1 << 30) || top_k < 0 || top_k > kLogprobMaxTopK) return 0;
   return logprobs_scratch_bytes(rows, vocab, top_k);
 }
 
@@ -291,11 +291,12 @@ int32_t tqd_op_logprobs(const float* logits, int64_t stride, int32_t rows, int32
                         float* logprob, float* entropy, int32_t top_k, int32_t* top_ids, float* top_logprobs,
                         void* scratch, void* stream) {
   if (!rows) return TQD_OK;
-  if (!logits || !scratch || rows < 0 || vocab <= 0 || stride < vocab || top_k < 0 || top_k > kLogprobMaxTopK)
-    return refuse("tqd_op_logprobs: NULL logits or scratch, rows < 0, vocab < 1, stride < vocab, or top_k above 32");
+  if (!logits || !scratch || rows < 0 || vocab <= 0 || vocab > (1 << 30) || stride < vocab || top_k < 0 || top_k > kLogprobMaxTopK)
+    return refuse("tqd_op_logprobs: NULL logits or scratch, rows < 0, vocab outside 1 .. 2^30, stride < vocab, or top_k above 32");
   if (!targets != !logprob) return refuse("tqd_op_logprobs: targets and logprob go together");
   if (top_k ? !top_ids || !top_logprobs : !logprob && !entropy)
     return refuse("tqd_op_logprobs: top_k needs top_ids and top_logprobs; nothing else asked for");
+  if (rows * static_cast<int64_t>(vocab) > (1ll << 40)) return refuse("tqd_op_logprobs: more than 2^40 logits");
   if (reinterpret_cast<uintptr_t>(scratch) % 16) return refuse("tqd_op_logprobs: scratch must be 16-byte aligned");
   const LogprobArgs a{logits, targets, logprob, entropy, top_ids, top_logprobs, scratch, stride, rows, vocab, top_k};
   return status_of(launch_logprobs(a, static_cast<cudaStream_t>(stream)));

@@ -7,7 +7,9 @@
 // p = 2^(score - ref) the row is (sum p v) / (sum p), rescaled when M or the V
 // scale grows past a slack of 2 octaves.  K and V elements are (code - 8) * scale,
 // so  q . k = sum over groups scale_g (sum_d q_d code_d - 8 sum_d q_d)  and
-// sum_t p_t v_t = sum_t (p_t scale_t) code_t - 8 sum_t (p_t scale_t).
+// sum_t p_t v_t = sum_t (p_t scale_t) (code_t - 8).  (The second is not split like
+// the first: over many positions sum p code is 8 sum p but for a small rest,
+// and the rest is the result.)
 //
 // Both contractions run on the tensor cores by mma.sync m16n8k16 with f16
 // operands: codes are exact (a masked word is an operand, tqd_q4.cuh), q and
@@ -56,22 +58,10 @@ struct Ring {
 // A partial result: R rows of HD sums, then the 8 operand rows' ref and sum p.
 __host__ __device__ constexpr int partial_floats(int hd) { return 8 * hd + 16; }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // x0, x1 as two f16 parts each: hi = f16(x), lo = f16(x - hi).
@@ -297,36 +287,33 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
 
     // ---- the query rows as operands
     uint32_t qa[NG][2][4];
-    float zq[NS][2], rowfac;
+    float zq[NS][2], fac[NS];
     {
       const float* q = a.q + token * a.q_stride + static_cast<int64_t>(head) * HD;
-      float x[NS][8], m = 0.f;
-#pragma unroll
-      for (int t = 0; t < NS; ++t)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[t][i] = q[(gv * NS + t) * 32 + 8 * c + i] * a.scale;
-          m = fmaxf(m, fabsf(x[t][i]));
-        }
-#pragma unroll
-      for (int o = 1; o < 4 * GV; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      // A power of two brings the row's largest element to 2^9 .. 2^10; the high
-      // part is then the nearest whole number, so that a group's sum of high
-      // parts times codes is exact in the tensor cores' f32, which truncate
+      // A power of two for each group of 32 brings its largest element to 2^10
+      // .. 2^11; the high part is then the nearest whole number, so that a group's sum
+      // of high parts times codes is exact in the tensor cores' f32, which truncate
       // (f16 parts with their own exponents cost four times the error).
-      // (The clip of rowfac is met past 2^113, where distinct scores differ by
+      // (The clip of fac is met past 2^113, where distinct scores differ by
       // more than 2^80 however they are scaled.)
-      const int e = max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100);
-      const float f = __uint_as_float(static_cast<uint32_t>(127 + 9 - e) << 23);
-      rowfac = __uint_as_float(static_cast<uint32_t>(min(127 + 24 - 9 + e, 254)) << 23);
 #pragma unroll
       for (int t = 0; t < NS; ++t) {
-        float zh = 0.f, zl = 0.f;
+        float x[8], m = 0.f, zh = 0.f, zl = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[t][i] *= f;
-          zh += rintf(x[t][i]);
-          zl += x[t][i] - rintf(x[t][i]);
+          x[i] = q[(gv * NS + t) * 32 + 8 * c + i] * a.scale;
+          m = fmaxf(m, fabsf(x[i]));
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const int e = max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100);
+        const float f = pow2(10 - e);
+        fac[t] = pow2(min(24 - 10 + e, 127));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] *= f;
+          zh += rintf(x[i]);
+          zl += round_f16(x[i] - rintf(x[i]));  // what the operand holds
         }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
@@ -341,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
           const float on = k == gv ? 1.f : 0.f;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            const float y0 = on * x[t][2 * w], y1 = on * x[t][2 * w + 4];
-            const float y2 = on * x[t][2 * w + 1], y3 = on * x[t][2 * w + 5];
+            const float y0 = on * x[2 * w], y1 = on * x[2 * w + 4];
+            const float y2 = on * x[2 * w + 1], y3 = on * x[2 * w + 5];
             const float i0 = rintf(y0), i1 = rintf(y1), i2 = rintf(y2), i3 = rintf(y3);
             qa[g][w][0] = pack_f16(i0, i1);
             qa[g][w][1] = pack_f16(y0 - i0, y1 - i1);
@@ -409,16 +396,16 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
             const uint32_t w = kw[g] >> 8;
             mma_f16(d, qa[g][1], w & 0x000F000Fu, w & 0x00F000F0u);
           }
-          p0 += ks[2 * j][t] * (d[0] + d[2]);
-          p1 += ks[2 * j + 1][t] * (d[1] + d[3]);
+          p0 += ks[2 * j][t] * (fac[t] * (d[0] + d[2]));
+          p1 += ks[2 * j + 1][t] * (fac[t] * (d[1] + d[3]));
         }
 #pragma unroll
         for (int x = 4; x < 4 * GV; x <<= 1) {
           p0 += __shfl_xor_sync(0xFFFFFFFFu, p0, x);
           p1 += __shfl_xor_sync(0xFFFFFFFFu, p1, x);
         }
-        sc[2 * j] = p0 * rowfac;
-        sc[2 * j + 1] = p1 * rowfac;
+        sc[2 * j] = p0;
+        sc[2 * j + 1] = p1;
       }
       if (t0 + kQ4Block > min_seen) {
 #pragma unroll

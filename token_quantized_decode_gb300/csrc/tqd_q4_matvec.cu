@@ -40,25 +40,263 @@ __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t r
   reinterpret_cast<uint32_t*>(dst + tile * kQ4TileBytes)[w] = word;
 }
 
-// One warp per (row, vector).
-__global__ void __launch_bounds__(256) k_q4_matvec(const uint8_t* w, int rows, int cols, int strips, const float* x,
-                                                   int64_t x_stride, int n, float* y, int64_t y_stride) {
-  const int lane = threadIdx.x & 31;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t row = task / n;
-  if (row >= rows) return;
-  const int vec = static_cast<int>(task - row * n);
-  const int r = static_cast<int>(row & 15);
-  float s = 0.f;
-  for (int g = 0; g < cols / 32; ++g) {
-    const uint8_t* tile = w + (row / 16 * strips + g / 4) * kQ4TileBytes;
-    const uint32_t word = reinterpret_cast<const uint32_t*>(tile)[r * 16 + (lane >> 3) * 4 + (g & 3)];
-    const float d = __half2float(reinterpret_cast<const __half*>(tile + kQ4TileScales)[r * 4 + (g & 3)]);
-    const float q = static_cast<float>(static_cast<int>((word >> (4 * (lane & 7))) & 15u) - 8);
-    s += q * d * x[vec * x_stride + g * 32 + lane];
+constexpr int kMvWarps = 8;
+constexpr int kMvThreads = 32 * kMvWarps;
+constexpr int kMvXBytes = 73728;  // staged vectors: two CTAs fit an SM
+// Stages (strips) of a warp's ring.
+__host__ __device__ constexpr int mv_stages(int nt) { return nt == 4 ? 3 : 4; }
+
+struct MatvecQ4Args {
+  const uint8_t* w;
+  const float* x;
+  float* y;
+  int64_t xs, ys;
+  int rows, groups, n;   // groups: columns / 32
+  int row_tiles, strips;
+  int slab;              // strips whose x is staged at a time
+  int wk;                // warps that share a row tile's strips (1, 2, 4, 8)
+  int per_slot;          // row tiles of one warp (of wk warps)
+};
+
+// y = W x for up to 4 NT vectors (ONE: a single one).
+//
+// A tile's 16 rows are the tensor cores' 16 operand rows, its masked words the
+// operand itself (tqd_q4.cuh); the vectors are columns, two for each: a group of
+// 32 elements is scaled by a power of two that brings its largest to 2^10
+// .. 2^11 and split into the nearest whole number and the rest in f16, so that the
+// group's sums of whole parts times codes are exact in the f32 accumulators
+// (which truncate) and the rest carries 11 bits more; one power of two for a
+// whole vector costs the small elements of a vector with outliers too many.
+// sum_k (code_k - 8) x_k starts from -8 sum_k x_k, staged with x; each
+// group's two column sums are added, scaled by the group's power of two and
+// the row's f16 scale and summed over groups in f32.
+//
+// HBM bounds it: 4.5 bits a weight.  A weight costs 0.6 instructions of
+// unpacking and 1/4 MMA lane, where unpacking to f32 and a packed FMA cost over 2;
+// up to 16 vectors share them.  Each warp streams its row tiles' strips, one
+// contiguous run, through a ring of bulk copies of its own; where there are too
+// few row tiles for the GPU's warps, 2, 4 or 8 warps share a tile's strips and
+// add their sums in shared memory.
+template <int NT, bool ONE>
+__global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
+  constexpr int NC = ONE ? 2 : 8 * NT;  // staged columns: high and low part of each vector
+  constexpr int kMvStages = mv_stages(NT), kStage = kQ4TileBytes;
+  extern __shared__ __align__(128) unsigned char sm[];
+  unsigned char* ring = sm;
+  float* red = reinterpret_cast<float*>(ring + kMvWarps * kMvStages * kStage);  // [warps][2 NT][32]
+  auto* bars = reinterpret_cast<uint64_t*>(red + kMvWarps * 2 * NT * 32);
+  // [groups of a slab][NC / 2]: start of the high and of the low part's sum, the vector's factor
+  float4* zs = reinterpret_cast<float4*>(bars + kMvWarps * kMvStages);
+  unsigned char* xs = reinterpret_cast<unsigned char*>(zs + a.slab * 4 * (NC / 2));  // [groups][NC][4][16 bytes]
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r8 = lane >> 2, c = lane & 3;
+  const int wk = warp % a.wk;
+  const int slot = blockIdx.x * (kMvWarps / a.wk) + warp / a.wk;
+  const int tile0 = slot * a.per_slot, tile1 = min(tile0 + a.per_slot, a.row_tiles);
+  const int v0 = blockIdx.y * 16, nv = min(a.n - v0, ONE ? 1 : 4 * NT);
+  const float* x = a.x + v0 * a.xs;
+  float* y = a.y + v0 * a.ys;
+  const int slabs = (a.strips + a.slab - 1) / a.slab;
+
+  uint64_t* bar = bars + warp * kMvStages;
+  unsigned char* my_ring = ring + warp * kMvStages * kStage;
+  if (lane < kMvStages) mbar_init(&bar[lane], 1);
+  fence_mbar_init();
+  __syncwarp();
+
+  // this warp's strips of a slab
+  auto share = [&](int slab, int& b, int& e) {
+    const int s0 = slab * a.slab, n = min(a.slab, a.strips - s0);
+    b = s0 + n * wk / a.wk;
+    e = s0 + n * (wk + 1) / a.wk;
+  };
+  // the ring's next copy: slab by slab, tile by tile, strip by strip
+  int pslab = 0, ptile = tile0, pstrip, pend, issued = 0;
+  share(0, pstrip, pend);
+  auto issue = [&] {
+    while (pstrip >= pend) {  // a share without strips (fewer strips than warps), or one that is done
+      if (++ptile >= tile1) {
+        ptile = tile0;
+        if (++pslab >= slabs) break;
+      }
+      share(pslab, pstrip, pend);
+      if (pstrip >= pend) ptile = tile1 - 1;
+    }
+    if (pslab >= slabs || tile0 >= tile1) return;
+    const int st = issued % kMvStages;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bar[st], kStage);
+      bulk_g2s(my_ring + st * kStage, a.w + (static_cast<size_t>(ptile) * a.strips + pstrip) * kStage, kStage, &bar[st]);
+    }
+    ++pstrip;
+    ++issued;
+  };
+  if (tile0 < tile1)
+    for (int i = 0; i < kMvStages - 1; ++i) issue();
+
+  int taken = 0;
+  bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
+  for (int slab = 0; slab < slabs; ++slab) {
+    // ---- the slab's part of the vectors
+    const int g0 = slab * a.slab * 4, ng = min(a.slab, a.strips - slab * a.slab) * 4;
+    if (slab) __syncthreads();
+    const int octs = ng * 4;
+    const int real = min(a.groups - g0, ng) * 4;
+    // (whole warps: octs is a multiple of 16, and a group's four octets are neighbouring lanes)
+    for (int i0 = warp * 32; i0 < octs * (NC / 2); i0 += kMvThreads) {
+      const int i = i0 + lane, v = i / octs, o = i - v * octs;
+      float f[8], m = 0.f, zh = 0.f, zl = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      if (v < nv && o < real) {
+        const float* p = x + v * a.xs + static_cast<int64_t>(g0) * 32 + o * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = p[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+#pragma unroll
+      for (int s = 1; s < 4; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+      const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127, up = 10 - e;
+      const float f1 = pow2(up / 2), f2 = pow2(up - up / 2);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = e > 112 ? __int_as_float(0x7FC00000) : f[j] * f1 * f2;
+      float hi[8], lo[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        hi[j] = rintf(f[j]);
+        lo[j] = round_f16(f[j] - hi[j]);  // (rounded here: the start of the sum counts what the operand holds)
+        zh += hi[j];
+        zl += lo[j];
+      }
+#pragma unroll
+      for (int s = 1; s < 4; s <<= 1) {
+        zh += __shfl_xor_sync(0xFFFFFFFFu, zh, s);
+        zl += __shfl_xor_sync(0xFFFFFFFFu, zl, s);
+      }
+      if (v >= NC / 2) continue;
+      const int g = o >> 2, oc = o & 3;
+      if (oc == 0)
+        zs[g * (NC / 2) + v] = make_float4(-8.f * 0x1p-24f * zh, -8.f * 0x1p-24f * zl, pow2(min(24 - up, 127)), 0.f);
+      uint4 q;
+      unsigned char* d = xs + ((g * NC + 2 * v) * 4 + oc) * 16;
+      q.x = pack_f16(hi[0], hi[4]);
+      q.y = pack_f16(0.0625f * hi[1], 0.0625f * hi[5]);
+      q.z = pack_f16(hi[2], hi[6]);
+      q.w = pack_f16(0.0625f * hi[3], 0.0625f * hi[7]);
+      *reinterpret_cast<uint4*>(d) = q;
+      q.x = pack_f16(lo[0], lo[4]);
+      q.y = pack_f16(0.0625f * lo[1], 0.0625f * lo[5]);
+      q.z = pack_f16(lo[2], lo[6]);
+      q.w = pack_f16(0.0625f * lo[3], 0.0625f * lo[7]);
+      *reinterpret_cast<uint4*>(d + 64) = q;
+    }
+    __syncthreads();
+
+    // ---- this warp's row tiles
+    int b, e;
+    share(slab, b, e);
+    for (int k = 0; k < a.per_slot; ++k) {
+      const int tile = tile0 + k;
+      float acc[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = 0.f;
+      if (tile < tile1) {
+        for (int strip = b; strip < e; ++strip) {
+          issue();
+          const int st = taken % kMvStages;
+          if (!dead) dead = !mbar_wait_bounded(&bar[st], (taken / kMvStages) & 1, nullptr);
+          ++taken;
+          const unsigned char* tl = my_ring + st * kStage;
+          const uint4 w0 = *reinterpret_cast<const uint4*>(tl + lane * 16);
+          const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + lane * 16);
+          const uint2 s0 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + r8 * 8);
+          const uint2 s1 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + 64 + r8 * 8);
+          const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w}, wb[4] = {w1.x, w1.y, w1.z, w1.w};
+          const int gl = strip * 4 - g0;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t p = wa[g], q = wb[g], p8 = p >> 8, q8 = q >> 8;
+            const uint32_t a0[4] = {p & 0x000F000Fu, q & 0x000F000Fu, p & 0x00F000F0u, q & 0x00F000F0u};
+            const uint32_t a1[4] = {p8 & 0x000F000Fu, q8 & 0x000F000Fu, p8 & 0x00F000F0u, q8 & 0x00F000F0u};
+            const uint32_t sw0 = g < 2 ? s0.x : s0.y, sw1 = g < 2 ? s1.x : s1.y;
+            const float d0 = __half2float(__ushort_as_half(static_cast<unsigned short>(g & 1 ? sw0 >> 16 : sw0 & 0xFFFFu)));
+            const float d1 = __half2float(__ushort_as_half(static_cast<unsigned short>(g & 1 ? sw1 >> 16 : sw1 & 0xFFFFu)));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const int col = ONE ? r8 & 1 : t * 8 + r8;  // (one vector: the other columns repeat its two)
+              const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl + g) * NC + col) * 4 + c) * 16);
+              const float4 z = zs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
+              float d[4] = {z.x, z.y, z.x, z.y};
+              mma_f16(d, a0, xv.x, xv.y);
+              mma_f16(d, a1, xv.z, xv.w);
+              acc[t][0] += d0 * (z.z * (d[0] + d[1]));
+              acc[t][1] += d1 * (z.z * (d[2] + d[3]));
+            }
+          }
+          __syncwarp();  // every lane has read the stage before it is filled again
+        }
+        if (dead)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = __int_as_float(0x7FC00000);
+      }
+      if (a.wk > 1) {
+        float* mine = red + warp * 2 * NT * 32 + lane;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mine[(2 * t) * 32] = acc[t][0];
+          mine[(2 * t + 1) * 32] = acc[t][1];
+        }
+        __syncthreads();
+        if (wk == 0)
+          for (int j = 1; j < a.wk; ++j)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              acc[t][0] += mine[(j * NT + t) * 64];
+              acc[t][1] += mine[(j * NT + t) * 64 + 32];
+            }
+        __syncthreads();
+      }
+      if (tile < tile1 && wk == 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int v = t * 4 + c;
+          if (v >= nv) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = tile * 16 + h * 8 + r8;
+            if (r >= a.rows) continue;
+            float* p = y + v * a.ys + r;
+            *p = slab ? *p + acc[t][h] : acc[t][h];
+          }
+        }
+      }
+    }
   }
-  s = warp_sum(s);
-  if (lane == 0) y[vec * y_stride + row] = s;
+}
+
+template <int NT, bool ONE>
+cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
+  constexpr int NC = ONE ? 2 : 8 * NT;
+  const int most = kMvXBytes / ((NC * 64 + NC / 2 * 16) * 4);  // strips whose vectors fit
+  const int slabs = (a.strips + most - 1) / most;
+  a.slab = (a.strips + slabs - 1) / slabs;
+  const size_t smem = static_cast<size_t>(kMvWarps) * mv_stages(NT) * (kQ4TileBytes + 8) +
+                      static_cast<size_t>(kMvWarps) * 2 * NT * 128 + static_cast<size_t>(a.slab) * 4 * (NC * 64 + NC / 2 * 16);
+  // a warp a row tile where that keeps eight warps on each SM busy, else 2, 4 or 8
+  a.wk = 1;
+  while (a.wk < kMvWarps && static_cast<int64_t>(a.row_tiles) * a.wk < 152 * kMvWarps && a.wk * 2 <= a.slab) a.wk *= 2;
+  const int slots = kMvWarps / a.wk;
+  int blocks = (a.row_tiles + slots - 1) / slots;
+  if (blocks > 304) blocks = 304;
+  a.per_slot = (a.row_tiles + blocks * slots - 1) / (blocks * slots);
+  blocks = (a.row_tiles + a.per_slot * slots - 1) / (a.per_slot * slots);
+  const cudaError_t e = cudaFuncSetAttribute(k_q4_matvec<NT, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  k_q4_matvec<NT, ONE><<<dim3(blocks, (a.n + 15) / 16), kMvThreads, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -72,10 +310,21 @@ cudaError_t launch_q4_repack(const uint8_t* src, int64_t rows, int64_t cols, uin
 
 cudaError_t launch_q4_matvec(const uint8_t* w, int rows, int cols, const float* x, int n, int64_t x_stride, float* y,
                              int64_t y_stride, cudaStream_t st) {
-  const int64_t warps = static_cast<int64_t>(rows) * n;
-  k_q4_matvec<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, st>>>(w, rows, cols, (cols + 127) / 128, x, x_stride, n,
-                                                                      y, y_stride);
-  return cudaGetLastError();
+  MatvecQ4Args a{};
+  a.w = w;
+  a.x = x;
+  a.y = y;
+  a.xs = x_stride;
+  a.ys = y_stride;
+  a.rows = rows;
+  a.groups = cols / 32;
+  a.n = n;
+  a.row_tiles = (rows + kQ4TileRows - 1) / kQ4TileRows;
+  a.strips = (cols + kQ4TileCols - 1) / kQ4TileCols;
+  if (n == 1) return launch_mv<1, true>(a, st);
+  if (n <= 4) return launch_mv<1, false>(a, st);
+  if (n <= 8) return launch_mv<2, false>(a, st);
+  return launch_mv<4, false>(a, st);
 }
 
 }  // namespace tqd
