@@ -12,25 +12,25 @@
 // and the rest is the result.)
 //
 // Both contractions run on the tensor cores by mma.sync m16n8k16 with f16
-// operands: codes are exact (a masked word is an operand, tqd_q4.cuh), q and
+// operands, the cache as the 16-row operand: codes are exact (a masked word is
+// an operand, tqd_q4.cuh; V's are made signed by one packed operation), q and
 // p * scale are split into two f16 parts (22 bits; 2^-11 would show in f32
-// outputs), one in rows 0-7 of the 16-row operand and one in rows 8-15, so the
-// split costs no instruction more; sums are f32.  tcgen05 does not fit here:
-// its weight-side operand would have to pass through shared memory as f16, four
-// times the bytes that the cache holds, and that is more than shared memory
-// moves at the rate HBM delivers the codes.
+// outputs) in two of the 8 columns, so the split costs no instruction more;
+// sums are f32.  p * scale passes from the scores' layout to the operand's by
+// movmatrix.  tcgen05 does not fit here: the cache would have to pass through
+// shared memory as f16, four times the bytes that HBM delivers, and that is
+// more than shared memory moves at HBM's rate.
 //
-// Few query rows share a kv head (G = 2 to 8), and the operand has 8.  The free
-// rows carry other groups: with GV groups side by side, row (h, gv) holds
-// query row h for group gv only, one chain of MMAs sums each group in its own
-// row, and a p * scale operand is made once instead of GV times.  GV is 4 for up
-// to 2 rows, 2 for up to 4, 1 otherwise.
+// 8 columns hold 4 query rows.  Where fewer share a kv head, GV groups lie side
+// by side: column pair (h, gv) holds row h for group gv only, one chain of MMAs
+// sums each group in its own column, and a p * scale operand is made once
+// instead of GV times.  GV is 4 for one row, 2 for two; for more than four rows
+// (NT = 2) two column tiles share the unpacked cache.
 //
 // Split.  The unit is a block of 16 positions of one (sequence, kv head, tile
-// of query rows); units are laid end to end and each CTA takes an equal run of
-// them (kCtas at three per SM), its 4 warps every fourth unit with a running
-// softmax each, whatever the lengths.  Rows that one CTA finishes are written
-// out; where a run begins or ends inside a row's units the CTA leaves a partial
+// of query rows); units are laid end to end and each CTA (two an SM) takes an
+// equal run of them, its warps every W-th unit with a running softmax each,
+// whatever the lengths.  Rows that one CTA finishes are written out; where a run begins or ends inside a row's units the CTA leaves a partial
 // (ref, sum p, sum p v) and a second kernel, already launched (programmatic
 // dependent launch), joins them.  The order of every sum is fixed by the sizes.
 #include <cuda_runtime.h>
@@ -41,21 +41,28 @@
 namespace tqd {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kCtas = 456;      // three per SM
+constexpr int kCtas = 304;      // two per SM
 constexpr int kSegment = 16;    // units that beginning and ending a segment is counted as
 constexpr int kCombine = 512;   // threads of the joining kernel
 constexpr float kNaN = __builtin_nanf("");
 
-// Stages of a warp's ring of blocks.
-template <int HD>
-struct Ring {
-  static constexpr int stages = HD == 128 ? 5 : 8;
-  static constexpr int bytes = q4_block_bytes(HD);
+// One instantiation: head size, column tiles, groups side by side.
+template <int HD, int NT, int GV>
+struct Cfg {
+  static constexpr int NG = HD / 32;      // groups of a row
+  static constexpr int NS = NG / GV;      // chains: column pair gv holds groups gv * NS + 0 .. NS - 1
+  static constexpr int P = 4 * NT;        // column pairs
+  static constexpr int R = P / GV;        // query rows of a tile
+  static constexpr int W = NT == 1 ? 8 : 6;  // warps: what the registers leave room for twice an SM
+  static constexpr int T = 32 * W;
+  static constexpr int ST = HD == 128 ? 4 : 6;  // stages of a warp's ring of blocks
+  static constexpr int BB = q4_block_bytes(HD);
+  static constexpr int LD = HD + 8;       // floats of a row in the merge buffer
+  static constexpr size_t smem = static_cast<size_t>(W) * ST * (BB + 12) + static_cast<size_t>(W) * (R * LD + 2 * P) * 4;
+  static_assert(NT == 1 || GV == 1, "groups side by side only where columns are free");
 };
 
-// A partial result: R rows of HD sums, then the 8 operand rows' ref and sum p.
+// A partial result: R rows of HD sums, then the column pairs' ref and sum p.
 __host__ __device__ constexpr int partial_floats(int hd) { return 8 * hd + 16; }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -64,12 +71,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// x0, x1 as two f16 parts each: hi = f16(x), lo = f16(x - hi).
-__device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x0, x1);
-  const float2 f = __half22float2(h);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = pack_f16(x0 - f.x, x1 - f.y);
+// x as two f16 parts in one word: the leading 11 bits low, the rest high.
+__device__ __forceinline__ uint32_t split_f16(float x) {
+  const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
+  return pack_f16(hi, x - hi);
+}
+
+// Element (i, j) of an 8 x 8 matrix of f16 (lane 4 i + j / 2, half j % 2) to (j, i).
+__device__ __forceinline__ uint32_t transpose_f16(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // The codes in bits 0-3 (lo) or 4-7 (hi) of each half of x as f16 pairs of
@@ -135,7 +147,7 @@ __device__ __forceinline__ int q_first(const Q4AttnArgs& a, int s) { return a.q_
 
 // Build the plan: every thread of the block calls it; blocks of up to 32 warps.
 // Shared memory: pre [n_seq + 1] u64, len [n_seq], nq [n_seq], warp sums.
-__device__ Plan make_plan(const Q4AttnArgs& a, int R, int ctas, unsigned char* smem) {
+__device__ Plan make_plan(const Q4AttnArgs& a, int R, int W, int ctas, unsigned char* smem) {
   __shared__ unsigned long long wsum[33];
   Plan p;
   const int n = a.c.n_seq, t = threadIdx.x, nt = blockDim.x;
@@ -180,47 +192,48 @@ __device__ Plan make_plan(const Q4AttnArgs& a, int R, int ctas, unsigned char* s
   __syncthreads();
   p.total = total;
   const unsigned long long per = (total + ctas - 1) / ctas;
-  p.per = (per + kWarps - 1) / kWarps * kWarps;
-  if (p.per == 0) p.per = kWarps;
+  p.per = max((per + W - 1) / W * W, static_cast<unsigned long long>(W));
   return p;
 }
 
 size_t plan_bytes(int n_seq) { return (static_cast<size_t>(n_seq) * 16 + 8 + 15) / 16 * 16; }
 
-template <int HD, int GV>
-__global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
-  constexpr int NG = HD / 32, NS = NG / GV, R = 8 / GV;
-  constexpr int ST = Ring<HD>::stages, BB = Ring<HD>::bytes;
+template <int HD, int NT, int GV>
+__global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnArgs a) {
+  using C = Cfg<HD, NT, GV>;
+  constexpr int NG = C::NG, NS = C::NS, P = C::P, R = C::R, W = C::W, ST = C::ST, BB = C::BB, LD = C::LD;
   extern __shared__ __align__(128) unsigned char sm[];
   unsigned char* ring = sm;
-  float* merge = reinterpret_cast<float*>(ring + kWarps * ST * BB);  // [warps][R * HD], then [warps][8] ref, l
-  float* mref = merge + kWarps * R * HD;
-  float* ml = mref + kWarps * 8;
-  auto* bars = reinterpret_cast<uint64_t*>(ml + kWarps * 8);  // [warps][ST]
-  int* flags = reinterpret_cast<int*>(bars + kWarps * ST);    // [warps][ST] 0 block, 1 no such page, 2 not seen
-  unsigned char* plan_mem = reinterpret_cast<unsigned char*>(flags + kWarps * ST);
+  float* merge = reinterpret_cast<float*>(ring + W * ST * BB);  // [W][R][LD], then [W][P] ref, sum p
+  float* mref = merge + W * R * LD;
+  float* ml = mref + W * P;
+  auto* bars = reinterpret_cast<uint64_t*>(ml + W * P);  // [W][ST]
+  int* flags = reinterpret_cast<int*>(bars + W * ST);    // [W][ST] 0 block, 1 no such page, 2 not seen
+  unsigned char* plan_mem = reinterpret_cast<unsigned char*>(flags + W * ST);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r8 = lane >> 2, c = lane & 3, h = r8 / GV, gv = r8 % GV;
+  const int r = lane >> 2, c = lane & 3;  // operand row (and r + 8), and column pair of the sums
+  const int h = c / GV, gv = c % GV;      // the pair's query row in its tile and first group's chain
   pdl_launch_dependents();
   uint64_t* bar = bars + warp * ST;
   int* flag = flags + warp * ST;
   if (lane < ST) mbar_init(&bar[lane], 1);
   fence_mbar_init();
-  const Plan plan = make_plan(a, R, gridDim.x, plan_mem);
+  const Plan plan = make_plan(a, R, W, gridDim.x, plan_mem);
 
   // sequences without positions: their queries see nothing
   for (int s = blockIdx.x; s < plan.n_seq; s += gridDim.x) {
     if (plan.len[s] > 0) continue;
-    const int64_t width = static_cast<int64_t>(a.n_heads) * HD, first = q_first(a, s);
-    for (int64_t i = threadIdx.x; i < plan.nq[s] * width; i += kThreads)
-      a.out[(first + i / width) * a.out_stride + i % width] = 0.f;
+    const int64_t first = q_first(a, s);
+    for (int q = 0; q < plan.nq[s]; ++q)
+      for (int i = threadIdx.x; i < a.n_heads * HD; i += C::T) a.out[(first + q) * a.out_stride + i] = 0.f;
   }
 
   const unsigned long long u0 = blockIdx.x * plan.per;
   if (u0 >= plan.total) return;
   const unsigned long long u1 = min(u0 + plan.per, plan.total);
-  const int n_it = static_cast<int>((u1 - u0 - warp + kWarps - 1) / kWarps) * (u0 + warp < u1);
+  const int n_units = static_cast<int>(u1 - u0);
+  const int n_it = n_units > warp ? (n_units - warp + W - 1) / W : 0;
   unsigned char* my_ring = ring + warp * ST * BB;
   const int ppb = a.c.page_size / kQ4Block;  // blocks per page
 
@@ -229,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
   const uint8_t* src = nullptr;
   int src_flag = 0;
   auto locate = [&](int i) {
-    const unsigned long long u = u0 + warp + static_cast<unsigned long long>(i) * kWarps;
-    if (u >= u1) return;
+    if (i >= n_it) return;
+    const unsigned long long u = u0 + warp + static_cast<unsigned long long>(i) * W;
     const int s = plan.seq_of(u);
     const unsigned long long uq = u - plan.pre[s];
     const int nb = plan.blocks(s);
@@ -239,33 +252,29 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
     int kvh;
     const int rt = plan.tile_of(s, seg, &kvh);
     const int last = min(rt * R + R, plan.nq[s] * plan.G) - 1;
-    if (blk * kQ4Block >= plan.seen(s, last)) {
-      src_flag = 2;
-      return;
-    }
+    src_flag = 2;
+    if (blk * kQ4Block >= plan.seen(s, last)) return;
     const int slot = blk / ppb;
     const int page = slot < a.c.table_stride ? a.c.table[static_cast<size_t>(s) * a.c.table_stride + slot] : -1;
     src_flag = page < 0 || page >= a.c.n_pages;
     src = a.c.pages + static_cast<size_t>(page) * a.c.page_bytes +
           (static_cast<size_t>(kvh) * ppb + (blk - slot * ppb)) * BB;
   };
-  auto issue = [&](int i) {
-    if (i >= n_it) return;
-    if ((i & 31) == 0) locate(i + lane);
-    if (lane == (i & 31)) {
-      const int st = i % ST;
-      flag[st] = src_flag;
-      if (src_flag == 0) {
-        mbar_arrive_expect_tx(&bar[st], BB);
-        bulk_g2s(my_ring + st * BB, src, BB, &bar[st]);
-      } else {
-        mbar_arrive_expect_tx(&bar[st], 0);
-      }
+  int issued = 0, issue_st = 0;
+  auto issue = [&] {
+    if (issued >= n_it) return;
+    if ((issued & 31) == 0) locate(issued + lane);
+    if (lane == (issued & 31)) {
+      flag[issue_st] = src_flag;
+      mbar_arrive_expect_tx(&bar[issue_st], src_flag ? 0 : BB);
+      if (!src_flag) bulk_g2s(my_ring + issue_st * BB, src, BB, &bar[issue_st]);
     }
+    ++issued;
+    issue_st = issue_st + 1 == ST ? 0 : issue_st + 1;
   };
-  for (int i = 0; i < ST - 1; ++i) issue(i);
+  for (int i = 0; i < ST - 1; ++i) issue();
 
-  int it = 0;
+  int rel = warp, st = 0, phase = 0;  // the warp's next unit, counted from u0, and its stage
   bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
   int s = plan.seq_of(u0);
   unsigned long long u = u0;
@@ -276,213 +285,256 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
     const unsigned long long seg = udiv(u - plan.pre[s], nb);
     const unsigned long long seg0 = plan.pre[s] + seg * nb, seg1 = seg0 + nb;
     const unsigned long long uend = min(seg1, u1);
+    const int rel_end = static_cast<int>(uend - u0);
+    const int blk0 = static_cast<int>(static_cast<long long>(u0 - seg0));  // block of unit rel: rel + blk0
     int kvh;
     const int rt = plan.tile_of(s, seg, &kvh);
     const int n_rows = min(R, plan.nq[s] * plan.G - rt * R);
     const int min_seen = plan.seen(s, rt * R);
-    const int row = rt * R + min(h, n_rows - 1);  // rows past the last repeat it
-    const int seen = plan.seen(s, row);
-    const int head = kvh * plan.G + row % plan.G;
-    const int64_t token = q_first(a, s) + row / plan.G;
 
-    // ---- the query rows as operands
-    uint32_t qa[NG][2][4];
-    float zq[NS][2], fac[NS];
+    // ---- the query rows as column operands
+    int seen[NT];
+    uint32_t qb[NT][NG][2][2];
+    float zh[NT][NS], zl[NT][NS], fac[NT][NS];
     {
-      const float* q = a.q + token * a.q_stride + static_cast<int64_t>(head) * HD;
-      // A power of two for each group of 32 brings its largest element to 2^10
-      // .. 2^11; the high part is then the nearest whole number, so that a group's sum
-      // of high parts times codes is exact in the tensor cores' f32, which truncate
-      // (f16 parts with their own exponents cost four times the error).
-      // (The clip of fac is met past 2^113, where distinct scores differ by
-      // more than 2^80 however they are scaled.)
+      const int pair = lane >> 3, part = (lane >> 2) & 1;  // this lane's operand column: pair's high or low part
 #pragma unroll
-      for (int t = 0; t < NS; ++t) {
-        float x[8], m = 0.f, zh = 0.f, zl = 0.f;
+      for (int t = 0; t < NT; ++t) {
+        const int row = rt * R + min(t * 4 + pair / GV, n_rows - 1);  // rows past the last repeat it
+        seen[t] = plan.seen(s, rt * R + min(t * 4 + h, n_rows - 1));
+        const float* q = a.q + (q_first(a, s) + row / plan.G) * a.q_stride +
+                         static_cast<int64_t>(kvh * plan.G + row % plan.G) * HD;
+        // A power of two for each group of 32 brings its largest element to 2^10
+        // .. 2^11; the high part is then the nearest whole number, so that a
+        // group's sum of high parts times codes is exact in the tensor cores' f32,
+        // which truncate (f16 parts with their own exponents cost four times
+        // the error).  (The clip of fac is met past 2^113, where distinct
+        // scores differ by more than 2^80 however they are scaled.)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = q[(gv * NS + t) * 32 + 8 * c + i] * a.scale;
-          m = fmaxf(m, fabsf(x[i]));
-        }
+        for (int k = 0; k < NS; ++k) {
+          float x[8], m = 0.f, z = 0.f;
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const int e = max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100);
-        const float f = pow2(10 - e);
-        fac[t] = pow2(min(24 - 10 + e, 127));
+          for (int i = 0; i < 8; ++i) {
+            x[i] = q[((pair % GV) * NS + k) * 32 + 8 * c + i] * a.scale;
+            m = fmaxf(m, fabsf(x[i]));
+          }
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const int e = max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100);
+          const float f = pow2(10 - e);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] *= f;
-          zh += rintf(x[i]);
-          zl += round_f16(x[i] - rintf(x[i]));  // what the operand holds
-        }
+          for (int i = 0; i < 8; ++i) {
+            x[i] *= f;
+            x[i] = part ? round_f16(x[i] - rintf(x[i])) : rintf(x[i]);
+            z += x[i];  // (counts what the operand holds)
+          }
+          z += __shfl_xor_sync(0xFFFFFFFFu, z, 1);
+          z += __shfl_xor_sync(0xFFFFFFFFu, z, 2);
+          z *= -8.f * 0x1p-24f;
+          zh[t][k] = __shfl_sync(0xFFFFFFFFu, z, c * 8);
+          zl[t][k] = __shfl_sync(0xFFFFFFFFu, z, c * 8 + 4);
+          fac[t][k] = __shfl_sync(0xFFFFFFFFu, pow2(min(24 - 10 + e, 127)), c * 8);
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          zh += __shfl_xor_sync(0xFFFFFFFFu, zh, o);
-          zl += __shfl_xor_sync(0xFFFFFFFFu, zl, o);
-        }
-        zq[t][0] = -8.f * 0x1p-24f * zh;
-        zq[t][1] = -8.f * 0x1p-24f * zl;
+          for (int v = 0; v < GV; ++v) {
+            const float on = v == pair % GV ? 1.f : 0.f;
 #pragma unroll
-        for (int k = 0; k < GV; ++k) {
-          const int g = k * NS + t;
-          const float on = k == gv ? 1.f : 0.f;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const float y0 = on * x[2 * w], y1 = on * x[2 * w + 4];
-            const float y2 = on * x[2 * w + 1], y3 = on * x[2 * w + 5];
-            const float i0 = rintf(y0), i1 = rintf(y1), i2 = rintf(y2), i3 = rintf(y3);
-            qa[g][w][0] = pack_f16(i0, i1);
-            qa[g][w][1] = pack_f16(y0 - i0, y1 - i1);
-            qa[g][w][2] = pack_f16(0.0625f * i2, 0.0625f * i3);
-            qa[g][w][3] = pack_f16(0.0625f * (y2 - i2), 0.0625f * (y3 - i3));
+            for (int w = 0; w < 2; ++w) {
+              qb[t][v * NS + k][w][0] = pack_f16(on * x[2 * w], on * x[2 * w + 4]);
+              qb[t][v * NS + k][w][1] = pack_f16(on * 0.0625f * x[2 * w + 1], on * 0.0625f * x[2 * w + 5]);
+            }
           }
         }
       }
     }
 
-    float o[NG * 4][4], l = 0.f, M = -INFINITY, S = 0.f, ref = 0.f;
+    float o[NT][NG * 2][4], l[NT], M[NT], ref[NT], S = 0.f;
 #pragma unroll
-    for (int i = 0; i < NG * 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int t = 0; t < NT; ++t) {
+      l[t] = 0.f;
+      M[t] = -INFINITY;
+      ref[t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NG * 2; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+    }
 
     // ---- this warp's units of it
-    for (;; ++it) {
-      const unsigned long long ui = u0 + warp + static_cast<unsigned long long>(it) * kWarps;
-      if (ui >= uend) break;
-      issue(it + ST - 1);
+    for (; rel < rel_end; rel += W) {
+      issue();
       __syncwarp();
-      const int st = it % ST;
-      if (!dead) dead = !mbar_wait_bounded(&bar[st], (it / ST) & 1, nullptr);
-      const int t0 = static_cast<int>(ui - seg0) * kQ4Block;
+      if (!dead) dead = !mbar_wait_bounded(&bar[st], phase, nullptr);
+      const int t0 = (rel + blk0) * kQ4Block;
       const int fl = flag[st];
+      const unsigned char* blk = my_ring + st * BB;
+      if (++st == ST) {
+        st = 0;
+        phase ^= 1;
+      }
       if (fl || dead) {
-        if (fl != 2 && t0 < seen) l = kNaN;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (fl != 2 && t0 < seen[t]) l[t] = kNaN;
         __syncwarp();
         continue;
       }
-      const unsigned char* blk = my_ring + st * BB;
 
-      // scales of positions 4c .. 4c + 3, this row's groups
-      float ks[4][NS], vs[4][NS];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int t = 0; t < NS; ++t) {
-          const int at = ((4 * c + i) * NG + gv * NS + t) * 2;
-          ks[i][t] = __half2float(*reinterpret_cast<const __half*>(blk + q4_ks_off(HD) + at));
-          vs[i][t] = __half2float(*reinterpret_cast<const __half*>(blk + q4_vs_off(HD) + at));
-        }
-
-      // scores of positions 4c .. 4c + 3
-      float sc[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t kw[NG];
-        const unsigned char* kr = blk + (j * 8 + r8) * (HD / 2) + c * (4 * NG);
-        if constexpr (HD == 128) {
-          const uint4 v = *reinterpret_cast<const uint4*>(kr);
-          kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
+      // positions of operand rows r and r + 8, their scales for this pair's groups
+      const int b0 = 4 * (r >> 1) + (r & 1), b1 = b0 + 2;
+      float ks0[NS], ks1[NS], vs0[NS], vs1[NS];
+      __half2 vmax;
+      auto scales = [&](int off, int b, float (&d)[NS]) {
+        const unsigned char* p = blk + off + (b * NG + gv * NS) * 2;
+        __half2 top;
+        if constexpr (NS == 4) {
+          const uint2 w = *reinterpret_cast<const uint2*>(p);
+          const __half2 x = *reinterpret_cast<const __half2*>(&w.x), y = *reinterpret_cast<const __half2*>(&w.y);
+          d[0] = __low2float(x); d[1] = __high2float(x); d[2] = __low2float(y); d[3] = __high2float(y);
+          top = __hmax2(x, y);
+        } else if constexpr (NS == 2) {
+          top = *reinterpret_cast<const __half2*>(p);
+          d[0] = __low2float(top); d[1] = __high2float(top);
         } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(kr);
-          kw[0] = v.x; kw[1] = v.y;
+          top = __half2half2(*reinterpret_cast<const __half*>(p));
+          d[0] = __low2float(top);
         }
-        float p0 = 0.f, p1 = 0.f;
+        return top;
+      };
+      scales(q4_ks_off(HD), b0, ks0);
+      scales(q4_ks_off(HD), b1, ks1);
+      vmax = __hmax2(scales(q4_vs_off(HD), b0, vs0), scales(q4_vs_off(HD), b1, vs1));
+
+      // scores of the two positions
+      float sc[NT][2];
+      {
+        uint32_t k0[NG], k1[NG];
+        const unsigned char* kr = blk + r * (HD / 2) + c * (4 * NG);
+        if constexpr (HD == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(kr), w = *reinterpret_cast<const uint4*>(kr + 512);
+          k0[0] = v.x; k0[1] = v.y; k0[2] = v.z; k0[3] = v.w;
+          k1[0] = w.x; k1[1] = w.y; k1[2] = w.z; k1[3] = w.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(kr), w = *reinterpret_cast<const uint2*>(kr + 256);
+          k0[0] = v.x; k0[1] = v.y;
+          k1[0] = w.x; k1[1] = w.y;
+        }
+        float d[NT][NS][4];
 #pragma unroll
-        for (int t = 0; t < NS; ++t) {
-          float d[4] = {zq[t][0], zq[t][0], zq[t][1], zq[t][1]};
+        for (int g = 0; g < NG; ++g) {
+          const int k = g % NS;
+          const uint32_t p = k0[g], q = k1[g], p8 = p >> 8, q8 = q >> 8;
+          const uint32_t a0[4] = {p & 0x000F000Fu, q & 0x000F000Fu, p & 0x00F000F0u, q & 0x00F000F0u};
+          const uint32_t a1[4] = {p8 & 0x000F000Fu, q8 & 0x000F000Fu, p8 & 0x00F000F0u, q8 & 0x00F000F0u};
 #pragma unroll
-          for (int k = 0; k < GV; ++k) {
-            const int g = k * NS + t;
-            mma_f16(d, qa[g][0], kw[g] & 0x000F000Fu, kw[g] & 0x00F000F0u);
-            const uint32_t w = kw[g] >> 8;
-            mma_f16(d, qa[g][1], w & 0x000F000Fu, w & 0x00F000F0u);
+          for (int t = 0; t < NT; ++t) {
+            if (g < NS)
+              mma_f16(d[t][k], a0, qb[t][g][0][0], qb[t][g][0][1], zh[t][k], zl[t][k], zh[t][k], zl[t][k]);
+            else
+              mma_f16(d[t][k], a0, qb[t][g][0][0], qb[t][g][0][1]);
+            mma_f16(d[t][k], a1, qb[t][g][1][0], qb[t][g][1][1]);
           }
-          p0 += ks[2 * j][t] * (fac[t] * (d[0] + d[2]));
-          p1 += ks[2 * j + 1][t] * (fac[t] * (d[1] + d[3]));
         }
 #pragma unroll
-        for (int x = 4; x < 4 * GV; x <<= 1) {
-          p0 += __shfl_xor_sync(0xFFFFFFFFu, p0, x);
-          p1 += __shfl_xor_sync(0xFFFFFFFFu, p1, x);
+        for (int t = 0; t < NT; ++t) {
+          sc[t][0] = sc[t][1] = 0.f;
+#pragma unroll
+          for (int k = 0; k < NS; ++k) {
+            sc[t][0] = fmaf(ks0[k], fac[t][k] * (d[t][k][0] + d[t][k][1]), sc[t][0]);
+            sc[t][1] = fmaf(ks1[k], fac[t][k] * (d[t][k][2] + d[t][k][3]), sc[t][1]);
+          }
+#pragma unroll
+          for (int x = 1; x < GV; x <<= 1) {
+            sc[t][0] += __shfl_xor_sync(0xFFFFFFFFu, sc[t][0], x);
+            sc[t][1] += __shfl_xor_sync(0xFFFFFFFFu, sc[t][1], x);
+          }
         }
-        sc[2 * j] = p0;
-        sc[2 * j + 1] = p1;
       }
-      if (t0 + kQ4Block > min_seen) {
+      const bool masked = t0 + kQ4Block > min_seen;
+      float bs = fmaxf(__low2float(vmax), __high2float(vmax));
+      if (masked) {
+        int most = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (t0 + 4 * c + i >= seen) {
-            sc[i] = -INFINITY;
+        for (int t = 0; t < NT; ++t) {
+          if (t0 + b0 >= seen[t]) sc[t][0] = -INFINITY;
+          if (t0 + b1 >= seen[t]) sc[t][1] = -INFINITY;
+          most = max(most, seen[t]);
+        }
+        // scales behind the end of every row: bytes that no position wrote
+        bs = 0.f;
 #pragma unroll
-            for (int t = 0; t < NS; ++t) vs[i][t] = 0.f;  // a NaN scale behind the end weighs nothing
-          }
+        for (int k = 0; k < NS; ++k) {
+          if (t0 + b0 >= most) vs0[k] = 0.f;
+          if (t0 + b1 >= most) vs1[k] = 0.f;
+          bs = fmaxf(bs, fmaxf(vs0[k], vs1[k]));
+        }
       }
 
       // the reference: kept while neither the scores nor the V scales grow past the slack
-      const float bm = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-      float bs = 0.f;
+      bool grow = bs > 4.f * S;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int t = 0; t < NT; ++t) grow |= fmaxf(sc[t][0], sc[t][1]) > M[t] + 2.f;
+      if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
-        for (int t = 0; t < NS; ++t) bs = fmaxf(bs, vs[i][t]);
-      if (__any_sync(0xFFFFFFFFu, bm > M + 2.f || bs > 4.f * S)) {
-        float m2 = bm, s2 = bs;
-#pragma unroll
-        for (int x = 1; x < 4; x <<= 1) {
-          m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, x));
-          s2 = fmaxf(s2, __shfl_xor_sync(0xFFFFFFFFu, s2, x));
-        }
-        m2 = fmaxf(m2, M);
-        S = fmaxf(s2, S);
+        for (int x = 4; x < 32; x <<= 1) bs = fmaxf(bs, __shfl_xor_sync(0xFFFFFFFFu, bs, x));
+        S = fmaxf(bs, S);
         const int ex = max(static_cast<int>(__float_as_uint(S) >> 23) - 126, -24);
-        const float nref = m2 == -INFINITY ? 0.f : m2 + static_cast<float>(ex - 11);
-        const float k = M == -INFINITY ? 1.f : ex2(ref - nref);
-        M = m2;
-        ref = nref;
-        l *= k;
 #pragma unroll
-        for (int i = 0; i < NG * 4; ++i) {
-          o[i][0] *= k; o[i][1] *= k; o[i][2] *= k; o[i][3] *= k;
+        for (int t = 0; t < NT; ++t) {
+          float m2 = fmaxf(sc[t][0], sc[t][1]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, x));
+          m2 = fmaxf(m2, M[t]);
+          const float nref = m2 == -INFINITY ? 0.f : m2 + static_cast<float>(ex - 11);
+          const float k = M[t] == -INFINITY ? 1.f : ex2(ref[t] - nref);
+          M[t] = m2;
+          ref[t] = nref;
+          l[t] *= k;
+#pragma unroll
+          for (int i = 0; i < NG * 2; ++i) {
+            o[t][i][0] *= k; o[t][i][1] *= k; o[t][i][2] *= k; o[t][i][3] *= k;
+          }
         }
       }
 
-      float p[4];
+      // p * scale as column operands
+      uint32_t pb[NT][NS][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = ex2(sc[i] - ref);
-      l += (p[0] + p[1]) + (p[2] + p[3]);
-
-      uint4 v0, v1;
-      if constexpr (HD == 128) {
-        v0 = *reinterpret_cast<const uint4*>(blk + q4_v_off(HD) + c * 128 + r8 * 16);
-        v1 = *reinterpret_cast<const uint4*>(blk + q4_v_off(HD) + 512 + c * 128 + r8 * 16);
-      } else {
-        v0 = *reinterpret_cast<const uint4*>(blk + q4_v_off(HD) + c * 128 + r8 * 16);
-      }
+      for (int t = 0; t < NT; ++t) {
+        const float p0 = ex2(sc[t][0] - ref[t]), p1 = ex2(sc[t][1] - ref[t]);
+        l[t] += p0 + p1;
 #pragma unroll
-      for (int t = 0; t < NS; ++t) {
-        float w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = p[i] * vs[i][t];
-        uint32_t pa[4];
-        split_f16(w[0], w[1], pa[0], pa[1]);
-        split_f16(w[2], w[3], pa[2], pa[3]);
-#pragma unroll
-        for (int k = 0; k < GV; ++k) {
-          const int g = k * NS + t;
-          const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-          uint32_t x0, x1;
-          if constexpr (HD == 128) {
-            x0 = __byte_perm(g < 2 ? v0.x : v0.y, g < 2 ? v0.z : v0.w, sel);
-            x1 = __byte_perm(g < 2 ? v1.x : v1.y, g < 2 ? v1.z : v1.w, sel);
-          } else {
-            x0 = __byte_perm(v0.x, v0.y, sel);
-            x1 = __byte_perm(v0.z, v0.w, sel);
+        for (int k = 0; k < NS; ++k) {
+          float w0 = p0 * vs0[k], w1 = p1 * vs1[k];
+          if (masked) {  // a NaN scale of a position that this row does not see
+            if (t0 + b0 >= seen[t]) w0 = 0.f;
+            if (t0 + b1 >= seen[t]) w1 = 0.f;
           }
-          mma_f16(o[4 * g], pa, signed_lo(x0), signed_lo(x1));
-          mma_f16(o[4 * g + 1], pa, signed_hi(x0), signed_hi(x1));
-          x0 >>= 8;
-          x1 >>= 8;
-          mma_f16(o[4 * g + 2], pa, signed_lo(x0), signed_lo(x1));
-          mma_f16(o[4 * g + 3], pa, signed_hi(x0), signed_hi(x1));
+          pb[t][k][0] = transpose_f16(split_f16(w0));
+          pb[t][k][1] = transpose_f16(split_f16(w1));
+        }
+      }
+
+      // sums of V
+      uint4 v0, v1;
+      v0 = *reinterpret_cast<const uint4*>(blk + q4_v_off(HD) + c * 128 + r * 16);
+      if constexpr (HD == 128) v1 = *reinterpret_cast<const uint4*>(blk + q4_v_off(HD) + 512 + c * 128 + r * 16);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+        uint32_t x0, x1;
+        if constexpr (HD == 128) {
+          x0 = __byte_perm(g < 2 ? v0.x : v0.y, g < 2 ? v0.z : v0.w, sel);
+          x1 = __byte_perm(g < 2 ? v1.x : v1.y, g < 2 ? v1.z : v1.w, sel);
+        } else {
+          x0 = __byte_perm(v0.x, v0.y, sel);
+          x1 = __byte_perm(v0.z, v0.w, sel);
+        }
+        const uint32_t a0[4] = {signed_lo(x0), signed_hi(x0), signed_lo(x1), signed_hi(x1)};
+        x0 >>= 8;
+        x1 >>= 8;
+        const uint32_t a1[4] = {signed_lo(x0), signed_hi(x0), signed_lo(x1), signed_hi(x1)};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mma_f16(o[t][2 * g], a0, pb[t][g % NS][0], pb[t][g % NS][1]);
+          mma_f16(o[t][2 * g + 1], a1, pb[t][g % NS][0], pb[t][g % NS][1]);
         }
       }
       __syncwarp();  // every lane has read the stage before it is filled again
@@ -490,38 +542,42 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
 
     // ---- the warps' sums into one
 #pragma unroll
-    for (int x = 1; x < 4; x <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
-    float* mo = merge + warp * R * HD + h * HD;
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-      if (g / NS == gv) {
+      for (int x = 4; x < 32; x <<= 1) l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], x);
+      float* mo = merge + (warp * R + t * 4 + h) * LD;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const float (&d)[4] = o[4 * g + tt];
-          *reinterpret_cast<float2*>(mo + 32 * g + 8 * tt + 2 * c) = make_float2(d[0] + d[2], d[1] + d[3]);
+      for (int g = 0; g < NG; ++g)
+        if (g / NS == gv) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float (&d)[4] = o[t][2 * g + i];
+            mo[32 * g + 16 * i + r] = d[0] + d[1];
+            mo[32 * g + 16 * i + r + 8] = d[2] + d[3];
+          }
         }
+      if (r == 0) {
+        mref[warp * P + t * 4 + c] = M[t] == -INFINITY && l[t] == 0.f ? -INFINITY : ref[t];
+        ml[warp * P + t * 4 + c] = l[t];
       }
-    if (c == 0) {
-      mref[warp * 8 + r8] = M == -INFINITY && l == 0.f ? -INFINITY : ref;
-      ml[warp * 8 + r8] = l;
     }
     __syncthreads();
     const bool whole = u0 <= seg0 && seg1 <= u1;
     // slot 0: the units from the CTA's first on; slot 1: those up to its last
     float* part = static_cast<float*>(a.scratch) +
                   (static_cast<size_t>(blockIdx.x) * 2 + (u == u0 ? 0 : 1)) * partial_floats(HD);
-    for (int i = threadIdx.x; i < R * HD; i += kThreads) {
-      const int hr = i / HD, d = i % HD, r = hr * GV + d / 32 / NS;
-      float ref2 = -INFINITY;
+    for (int i = threadIdx.x; i < R * HD; i += C::T) {
+      const int hr = i / HD, d = i % HD, pr = hr * GV + d / 32 / NS;
+      float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) ref2 = fmaxf(ref2, mref[w * 8 + r]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, mref[w * P + pr]);
       float acc = 0.f, ls = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if (mref[w * 8 + r] > -INFINITY) {
-          const float k = ex2(mref[w * 8 + r] - ref2);
-          acc += k * merge[w * R * HD + i];
-          ls += k * ml[w * 8 + r];
+      for (int w = 0; w < W; ++w)
+        if (mref[w * P + pr] > -INFINITY) {
+          const float k = ex2(mref[w * P + pr] - top);
+          acc += k * merge[(w * R + hr) * LD + d];
+          ls += k * ml[w * P + pr];
         }
       if (whole) {
         if (hr < n_rows) {
@@ -532,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
       } else {
         part[i] = acc;
         if (d % (32 * NS) == 0) {
-          part[8 * HD + r] = ref2;
-          part[8 * HD + 8 + r] = ls;
+          part[8 * HD + pr] = top;
+          part[8 * HD + 8 + pr] = ls;
         }
       }
     }
@@ -544,11 +600,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_attention_q4(Q4AttnArgs a) {
 
 // Joins the partials of the rows that a CTA's run of units begins and does not
 // end: block i looks at the last segment of run i.
-template <int HD, int GV>
+template <int HD, int NT, int GV>
 __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
-  constexpr int NG = HD / 32, NS = NG / GV, R = 8 / GV;
+  using C = Cfg<HD, NT, GV>;
+  constexpr int NS = C::NS, R = C::R;
   extern __shared__ __align__(128) unsigned char sm[];
-  const Plan plan = make_plan(a, R, gridDim.x, sm);
+  const Plan plan = make_plan(a, R, C::W, gridDim.x, sm);
   pdl_wait();
   const unsigned long long u0 = blockIdx.x * plan.per, u1 = u0 + plan.per;
   if (u1 >= plan.total) return;  // nothing behind this run
@@ -565,10 +622,10 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
                        (static_cast<size_t>(blockIdx.x) * 2 + (seg0 == u0 ? 0 : 1)) * partial_floats(HD);
   const float* rest = static_cast<const float*>(a.scratch) + static_cast<size_t>(blockIdx.x) * 2 * partial_floats(HD);
   auto part = [&](int k) { return k ? rest + static_cast<size_t>(k) * 2 * partial_floats(HD) : first; };
-  __shared__ float wt[kCtas * 8], lsum[8];  // each partial's weight; a row's sum p
+  __shared__ float wt[kCtas * 8], lsum[8];  // each partial's weight; a pair's sum p
   __shared__ float4 red[kCombine];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < 8) {  // a warp per operand row
+  if (warp < C::P) {  // a warp per column pair
     float ref = -INFINITY, ls = 0.f;
     for (int k = lane; k < runs; k += 32) ref = fmaxf(ref, part(k)[8 * HD + warp]);
     ref = warp_max(ref);
@@ -617,16 +674,14 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   }
 }
 
-template <int HD, int GV>
+template <int HD, int NT, int GV>
 cudaError_t launch(const Q4AttnArgs& a, cudaStream_t st) {
-  constexpr int R = 8 / GV;
-  const size_t plan_b = plan_bytes(a.c.n_seq);
-  const size_t smem = static_cast<size_t>(kWarps) * Ring<HD>::stages * (Ring<HD>::bytes + 12) +
-                      static_cast<size_t>(kWarps) * (R * HD + 16) * 4 + plan_b;
-  cudaError_t e = cudaFuncSetAttribute(k_attention_q4<HD, GV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = Cfg<HD, NT, GV>;
+  const size_t plan_b = plan_bytes(a.c.n_seq), smem = C::smem + plan_b;
+  cudaError_t e = cudaFuncSetAttribute(k_attention_q4<HD, NT, GV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  k_attention_q4<HD, GV><<<kCtas, kThreads, smem, st>>>(a);
+  k_attention_q4<HD, NT, GV><<<kCtas, C::T, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -639,7 +694,7 @@ cudaError_t launch(const Q4AttnArgs& a, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attention_q4_join<HD, GV>, a);
+  return cudaLaunchKernelEx(&cfg, k_attention_q4_join<HD, NT, GV>, a);
 }
 
 }  // namespace
@@ -652,11 +707,14 @@ cudaError_t launch_attention_q4(const Q4AttnArgs& args, int hd, cudaStream_t st)
   // rows that share a kv head; with q_start their number is on the device
   const int rows = a.q_start ? 8 : a.n_heads / a.c.n_kv;
   if (hd == 128) {
-    if (rows <= 2) return launch<128, 4>(a, st);
-    if (rows <= 4) return launch<128, 2>(a, st);
-    return launch<128, 1>(a, st);
+    if (rows == 1) return launch<128, 1, 4>(a, st);
+    if (rows == 2) return launch<128, 1, 2>(a, st);
+    if (rows <= 4) return launch<128, 1, 1>(a, st);
+    return launch<128, 2, 1>(a, st);
   }
-  return rows <= 4 ? launch<64, 2>(a, st) : launch<64, 1>(a, st);
+  if (rows <= 2) return launch<64, 1, 2>(a, st);
+  if (rows <= 4) return launch<64, 1, 1>(a, st);
+  return launch<64, 2, 1>(a, st);
 }
 
 }  // namespace tqd
