@@ -27,13 +27,15 @@
 // instead of GV times.  GV is 4 for one row, 2 for two; for more than four rows
 // (NT = 2) two column tiles share the unpacked cache.
 //
-// Split.  The unit is a block of 16 positions of one (sequence, kv head, tile
-// of query rows); units are laid end to end and each CTA (two an SM) takes an
+// Split.  The unit is 32 positions of one (sequence, kv head, tile of query
+// rows); units are laid end to end and each CTA (two an SM) takes an
 // equal run of them, its warps every W-th unit with a running softmax each,
 // whatever the lengths.  Rows that one CTA finishes are written out; where a run begins or ends inside a row's units the CTA leaves a partial
 // (ref, sum p, sum p v) and a second kernel, already launched (programmatic
 // dependent launch), joins them.  The order of every sum is fixed by the sizes.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "tqd_internal.h"
 #include "tqd_q4.cuh"
@@ -42,7 +44,8 @@ namespace tqd {
 namespace {
 
 constexpr int kCtas = 304;      // two per SM
-constexpr int kSegment = 16;    // units that beginning and ending a segment is counted as
+constexpr int kUnit = 32;       // positions of a unit: two blocks
+constexpr int kSegment = 8;     // units that beginning and ending a segment is counted as
 constexpr int kCombine = 512;   // threads of the joining kernel
 constexpr float kNaN = __builtin_nanf("");
 
@@ -55,10 +58,11 @@ struct Cfg {
   static constexpr int R = P / GV;        // query rows of a tile
   static constexpr int W = NT == 1 ? 8 : 6;  // warps: what the registers leave room for twice an SM
   static constexpr int T = 32 * W;
-  static constexpr int ST = HD == 128 ? 4 : 6;  // stages of a warp's ring of blocks
   static constexpr int BB = q4_block_bytes(HD);
+  static constexpr int JB = NT == 1 ? 2 : 1;  // blocks of a unit taken at once: two where the registers hold them
+  static constexpr int ST = HD == 64 ? 4 : NT == 1 ? 2 : 3;  // stages (units) of a warp's ring
   static constexpr int LD = HD + 8;       // floats of a row in the merge buffer
-  static constexpr size_t smem = static_cast<size_t>(W) * ST * (BB + 12) + static_cast<size_t>(W) * (R * LD + 2 * P) * 4;
+  static constexpr size_t smem = static_cast<size_t>(W) * ST * (2 * BB + 16) + static_cast<size_t>(W) * (R * LD + 2 * P) * 4;
   static_assert(NT == 1 || GV == 1, "groups side by side only where columns are free");
 };
 
@@ -84,18 +88,33 @@ __device__ __forceinline__ uint32_t transpose_f16(uint32_t x) {
   return y;
 }
 
-// The codes in bits 0-3 (lo) or 4-7 (hi) of each half of x as f16 pairs of
-// code - 8: 1024 + code and 1024 + 16 code are exact f16, so is the result.
-__device__ __forceinline__ uint32_t signed_lo(uint32_t x) {
-  const uint32_t v = (x & 0x000F000Fu) | 0x64006400u;
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t signed_hi(uint32_t x) {
-  const uint32_t v = (x & 0x00F000F0u) | 0x64006400u;
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
+// The constants of unpacking V, kept in registers (as immediates they cost an
+// instruction each: a logic operation takes one).
+struct Unpack {
+  uint32_t lo, hi, magic, off, sixteenth, off_hi;
+  __device__ Unpack() {
+    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(lo));
+    asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(hi));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+    off = 0xE408E408u;        // -1032
+    sixteenth = 0x2C002C00u;
+    off_hi = 0xD480D480u;     // -72
+  }
+  // The codes in bits 0-3 (low) or 4-7 (high) of each half of x as f16 pairs of
+  // code - 8: 1024 + code and 1024 + 16 code are exact f16, so is the result.
+  __device__ __forceinline__ uint32_t low(uint32_t x) const {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(lo), "r"(magic));
+    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(off));
+    return v;
+  }
+  __device__ __forceinline__ uint32_t high(uint32_t x) const {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(hi), "r"(magic));
+    asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(v) : "r"(sixteenth), "r"(off_hi));
+    return v;
+  }
+};
 
 __device__ __forceinline__ unsigned long long udiv(unsigned long long a, unsigned b) {
   return a >> 32 ? a / b : static_cast<unsigned>(a) / b;
@@ -109,10 +128,10 @@ struct Plan {
   unsigned long long total, per;  // units, and units of one CTA
   int n_seq, n_kv, G, R;
 
-  // Units of a segment: its blocks, and kSegment more that stand for the cost
+  // Units of a segment: those of its positions, and kSegment more that stand for the cost
   // of beginning and ending it.
-  __device__ int blocks(int s) const {
-    return len[s] > 0 ? (len[s] + kQ4Block - 1) / kQ4Block + kSegment : 0;
+  __device__ int units(int s) const {
+    return len[s] > 0 ? (len[s] + kUnit - 1) / kUnit + kSegment : 0;
   }
   __device__ int tiles(int s) const { return static_cast<int>((static_cast<long long>(nq[s]) * G + R - 1) / R); }
   // Sequence of unit u < total.
@@ -172,7 +191,7 @@ __device__ Plan make_plan(const Q4AttnArgs& a, int R, int W, int ctas, unsigned 
     }
     nq[s] = q;
     pre[s] = mine;
-    mine += static_cast<unsigned long long>(p.n_kv) * p.tiles(s) * p.blocks(s);
+    mine += static_cast<unsigned long long>(p.n_kv) * p.tiles(s) * p.units(s);
   }
   unsigned long long run = mine;
 #pragma unroll
@@ -201,15 +220,15 @@ size_t plan_bytes(int n_seq) { return (static_cast<size_t>(n_seq) * 16 + 8 + 15)
 template <int HD, int NT, int GV>
 __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnArgs a) {
   using C = Cfg<HD, NT, GV>;
-  constexpr int NG = C::NG, NS = C::NS, P = C::P, R = C::R, W = C::W, ST = C::ST, BB = C::BB, LD = C::LD;
+  constexpr int NG = C::NG, NS = C::NS, P = C::P, R = C::R, W = C::W, ST = C::ST, BB = C::BB, LD = C::LD, JB = C::JB;
   extern __shared__ __align__(128) unsigned char sm[];
   unsigned char* ring = sm;
-  float* merge = reinterpret_cast<float*>(ring + W * ST * BB);  // [W][R][LD], then [W][P] ref, sum p
+  float* merge = reinterpret_cast<float*>(ring + W * ST * 2 * BB);  // [W][R][LD], then [W][P] ref, sum p
   float* mref = merge + W * R * LD;
   float* ml = mref + W * P;
   auto* bars = reinterpret_cast<uint64_t*>(ml + W * P);  // [W][ST]
-  int* flags = reinterpret_cast<int*>(bars + W * ST);    // [W][ST] 0 block, 1 no such page, 2 not seen
-  unsigned char* plan_mem = reinterpret_cast<unsigned char*>(flags + W * ST);
+  int* flags = reinterpret_cast<int*>(bars + W * ST);    // [W][ST] 1, 2: no page for the first, second block; 4: not seen
+  unsigned char* plan_mem = reinterpret_cast<unsigned char*>(flags + W * ST * 2);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;  // operand row (and r + 8), and column pair of the sums
@@ -234,31 +253,39 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   const unsigned long long u1 = min(u0 + plan.per, plan.total);
   const int n_units = static_cast<int>(u1 - u0);
   const int n_it = n_units > warp ? (n_units - warp + W - 1) / W : 0;
-  unsigned char* my_ring = ring + warp * ST * BB;
+  unsigned char* my_ring = ring + warp * ST * 2 * BB;
   const int ppb = a.c.page_size / kQ4Block;  // blocks per page
 
   // Issue unit number i of this warp: lane i % 32 knows its address (found for
   // 32 units at a time, a lane each).
-  const uint8_t* src = nullptr;
+  const uint8_t *src0 = nullptr, *src1 = nullptr;
   int src_flag = 0;
   auto locate = [&](int i) {
     if (i >= n_it) return;
     const unsigned long long u = u0 + warp + static_cast<unsigned long long>(i) * W;
     const int s = plan.seq_of(u);
     const unsigned long long uq = u - plan.pre[s];
-    const int nb = plan.blocks(s);
+    const int nb = plan.units(s);
     const unsigned long long seg = udiv(uq, nb);
-    const int blk = static_cast<int>(uq - seg * nb);
+    const int t0 = static_cast<int>(uq - seg * nb) * kUnit;
     int kvh;
     const int rt = plan.tile_of(s, seg, &kvh);
-    const int last = min(rt * R + R, plan.nq[s] * plan.G) - 1;
-    src_flag = 2;
-    if (blk * kQ4Block >= plan.seen(s, last)) return;
-    const int slot = blk / ppb;
-    const int page = slot < a.c.table_stride ? a.c.table[static_cast<size_t>(s) * a.c.table_stride + slot] : -1;
-    src_flag = page < 0 || page >= a.c.n_pages;
-    src = a.c.pages + static_cast<size_t>(page) * a.c.page_bytes +
-          (static_cast<size_t>(kvh) * ppb + (blk - slot * ppb)) * BB;
+    const int seen = plan.seen(s, min(rt * R + R, plan.nq[s] * plan.G) - 1);
+    src0 = src1 = nullptr;
+    src_flag = t0 < seen ? 0 : 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int t = t0 + j * kQ4Block;
+      if (t >= seen) break;
+      const int slot = t / a.c.page_size;
+      const int page = slot < a.c.table_stride ? a.c.table[static_cast<size_t>(s) * a.c.table_stride + slot] : -1;
+      if (page < 0 || page >= a.c.n_pages) {
+        src_flag |= 1 << j;
+        continue;
+      }
+      (j ? src1 : src0) = a.c.pages + static_cast<size_t>(page) * a.c.page_bytes +
+                          (static_cast<size_t>(kvh) * ppb + (t - slot * a.c.page_size) / kQ4Block) * BB;
+    }
   };
   int issued = 0, issue_st = 0;
   auto issue = [&] {
@@ -266,14 +293,21 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
     if ((issued & 31) == 0) locate(issued + lane);
     if (lane == (issued & 31)) {
       flag[issue_st] = src_flag;
-      mbar_arrive_expect_tx(&bar[issue_st], src_flag ? 0 : BB);
-      if (!src_flag) bulk_g2s(my_ring + issue_st * BB, src, BB, &bar[issue_st]);
+      unsigned char* to = my_ring + issue_st * 2 * BB;
+      mbar_arrive_expect_tx(&bar[issue_st], (src0 ? BB : 0) + (src1 ? BB : 0));
+      if (src1 == src0 + BB && src0) {
+        bulk_g2s(to, src0, 2 * BB, &bar[issue_st]);
+      } else {
+        if (src0) bulk_g2s(to, src0, BB, &bar[issue_st]);
+        if (src1) bulk_g2s(to + BB, src1, BB, &bar[issue_st]);
+      }
     }
     ++issued;
     issue_st = issue_st + 1 == ST ? 0 : issue_st + 1;
   };
   for (int i = 0; i < ST - 1; ++i) issue();
 
+  const Unpack unpack;
   int rel = warp, st = 0, phase = 0;  // the warp's next unit, counted from u0, and its stage
   bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
   int s = plan.seq_of(u0);
@@ -281,12 +315,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   while (u < u1) {
     // ---- the segment of unit u: one (sequence, kv head, tile of rows)
     while (plan.pre[s + 1] <= u) ++s;
-    const int nb = plan.blocks(s);
+    const int nb = plan.units(s);
     const unsigned long long seg = udiv(u - plan.pre[s], nb);
     const unsigned long long seg0 = plan.pre[s] + seg * nb, seg1 = seg0 + nb;
     const unsigned long long uend = min(seg1, u1);
     const int rel_end = static_cast<int>(uend - u0);
-    const int blk0 = static_cast<int>(static_cast<long long>(u0 - seg0));  // block of unit rel: rel + blk0
+    const int unit0 = static_cast<int>(static_cast<long long>(u0 - seg0));  // unit rel is the segment's rel + unit0
     int kvh;
     const int rt = plan.tile_of(s, seg, &kvh);
     const int n_rows = min(R, plan.nq[s] * plan.G - rt * R);
@@ -334,6 +368,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           zh[t][k] = __shfl_sync(0xFFFFFFFFu, z, c * 8);
           zl[t][k] = __shfl_sync(0xFFFFFFFFu, z, c * 8 + 4);
           fac[t][k] = __shfl_sync(0xFFFFFFFFu, pow2(min(24 - 10 + e, 127)), c * 8);
+          zl[t][k] *= fac[t][k];
 #pragma unroll
           for (int v = 0; v < GV; ++v) {
             const float on = v == pair % GV ? 1.f : 0.f;
@@ -358,31 +393,13 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
     }
 
     // ---- this warp's units of it
-    for (; rel < rel_end; rel += W) {
-      issue();
-      __syncwarp();
-      if (!dead) dead = !mbar_wait_bounded(&bar[st], phase, nullptr);
-      const int t0 = (rel + blk0) * kQ4Block;
-      const int fl = flag[st];
-      const unsigned char* blk = my_ring + st * BB;
-      if (++st == ST) {
-        st = 0;
-        phase ^= 1;
-      }
-      if (fl || dead) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (fl != 2 && t0 < seen[t]) l[t] = kNaN;
-        __syncwarp();
-        continue;
-      }
-
-      // positions of operand rows r and r + 8, their scales for this pair's groups
-      const int b0 = 4 * (r >> 1) + (r & 1), b1 = b0 + 2;
-      float ks0[NS], ks1[NS], vs0[NS], vs1[NS];
-      __half2 vmax;
-      auto scales = [&](int off, int b, float (&d)[NS]) {
-        const unsigned char* p = blk + off + (b * NG + gv * NS) * 2;
+    // positions of operand rows r and r + 8 in a block
+    const int b0 = 4 * (r >> 1) + (r & 1), b1 = b0 + 2;
+    auto blocks = [&](auto masked_c, const unsigned char* from, int t0, int bad) {
+      constexpr bool masked = decltype(masked_c)::value;
+      float sc[NT][2 * JB], vs[2 * JB][NS];  // positions b0, b1 of each block
+      __half2 vmax = __float2half2_rn(0.f);
+      auto scales = [&](const unsigned char* p, float (&d)[NS]) {
         __half2 top;
         if constexpr (NS == 4) {
           const uint2 w = *reinterpret_cast<const uint2*>(p);
@@ -398,13 +415,14 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
         }
         return top;
       };
-      scales(q4_ks_off(HD), b0, ks0);
-      scales(q4_ks_off(HD), b1, ks1);
-      vmax = __hmax2(scales(q4_vs_off(HD), b0, vs0), scales(q4_vs_off(HD), b1, vs1));
-
-      // scores of the two positions
-      float sc[NT][2];
-      {
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        const unsigned char* blk = from + j * BB;
+        // scores of the block's two positions
+        float ks0[NS], ks1[NS];
+        const int at0 = (b0 * NG + gv * NS) * 2, at1 = (b1 * NG + gv * NS) * 2;
+        scales(blk + q4_ks_off(HD) + at0, ks0);
+        scales(blk + q4_ks_off(HD) + at1, ks1);
         uint32_t k0[NG], k1[NG];
         const unsigned char* kr = blk + r * (HD / 2) + c * (4 * NG);
         if constexpr (HD == 128) {
@@ -421,12 +439,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
         for (int g = 0; g < NG; ++g) {
           const int k = g % NS;
           const uint32_t p = k0[g], q = k1[g], p8 = p >> 8, q8 = q >> 8;
-          const uint32_t a0[4] = {p & 0x000F000Fu, q & 0x000F000Fu, p & 0x00F000F0u, q & 0x00F000F0u};
-          const uint32_t a1[4] = {p8 & 0x000F000Fu, q8 & 0x000F000Fu, p8 & 0x00F000F0u, q8 & 0x00F000F0u};
+          const uint32_t a0[4] = {p & unpack.lo, q & unpack.lo, p & unpack.hi, q & unpack.hi};
+          const uint32_t a1[4] = {p8 & unpack.lo, q8 & unpack.lo, p8 & unpack.hi, q8 & unpack.hi};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (g < NS)
-              mma_f16(d[t][k], a0, qb[t][g][0][0], qb[t][g][0][1], zh[t][k], zl[t][k], zh[t][k], zl[t][k]);
+              mma_f16(d[t][k], a0, qb[t][g][0][0], qb[t][g][0][1], 0.f, 0.f, 0.f, 0.f);
             else
               mma_f16(d[t][k], a0, qb[t][g][0][0], qb[t][g][0][1]);
             mma_f16(d[t][k], a1, qb[t][g][1][0], qb[t][g][1][1]);
@@ -434,43 +452,52 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          sc[t][0] = sc[t][1] = 0.f;
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int k = 0; k < NS; ++k) {
-            sc[t][0] = fmaf(ks0[k], fac[t][k] * (d[t][k][0] + d[t][k][1]), sc[t][0]);
-            sc[t][1] = fmaf(ks1[k], fac[t][k] * (d[t][k][2] + d[t][k][3]), sc[t][1]);
+            // (the high parts' sum and its -8 sum q are whole: their difference is exact)
+            s0 = fmaf(ks0[k], fmaf(fac[t][k], d[t][k][0] + zh[t][k] + d[t][k][1], zl[t][k]), s0);
+            s1 = fmaf(ks1[k], fmaf(fac[t][k], d[t][k][2] + zh[t][k] + d[t][k][3], zl[t][k]), s1);
           }
 #pragma unroll
           for (int x = 1; x < GV; x <<= 1) {
-            sc[t][0] += __shfl_xor_sync(0xFFFFFFFFu, sc[t][0], x);
-            sc[t][1] += __shfl_xor_sync(0xFFFFFFFFu, sc[t][1], x);
+            s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, x);
+            s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, x);
           }
+          if (masked) {
+            if (t0 + j * kQ4Block + b0 >= seen[t] || (bad >> j & 1)) s0 = -INFINITY;
+            if (t0 + j * kQ4Block + b1 >= seen[t] || (bad >> j & 1)) s1 = -INFINITY;
+          }
+          sc[t][2 * j] = s0;
+          sc[t][2 * j + 1] = s1;
         }
+        vmax = __hmax2(vmax, __hmax2(scales(blk + q4_vs_off(HD) + at0, vs[2 * j]),
+                                     scales(blk + q4_vs_off(HD) + at1, vs[2 * j + 1])));
       }
-      const bool masked = t0 + kQ4Block > min_seen;
       float bs = fmaxf(__low2float(vmax), __high2float(vmax));
-      if (masked) {
+      if (masked) {  // scales behind the end of every row: bytes that no position wrote
         int most = 0;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t0 + b0 >= seen[t]) sc[t][0] = -INFINITY;
-          if (t0 + b1 >= seen[t]) sc[t][1] = -INFINITY;
-          most = max(most, seen[t]);
-        }
-        // scales behind the end of every row: bytes that no position wrote
+        for (int t = 0; t < NT; ++t) most = max(most, seen[t]);
         bs = 0.f;
 #pragma unroll
-        for (int k = 0; k < NS; ++k) {
-          if (t0 + b0 >= most) vs0[k] = 0.f;
-          if (t0 + b1 >= most) vs1[k] = 0.f;
-          bs = fmaxf(bs, fmaxf(vs0[k], vs1[k]));
-        }
+        for (int i = 0; i < 2 * JB; ++i)
+#pragma unroll
+          for (int k = 0; k < NS; ++k) {
+            if (t0 + (i >> 1) * kQ4Block + (i & 1 ? b1 : b0) >= most || (bad >> (i >> 1) & 1)) vs[i][k] = 0.f;
+            bs = fmaxf(bs, vs[i][k]);
+          }
       }
 
       // the reference: kept while neither the scores nor the V scales grow past the slack
       bool grow = bs > 4.f * S;
+      float bm[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) grow |= fmaxf(sc[t][0], sc[t][1]) > M[t] + 2.f;
+      for (int t = 0; t < NT; ++t) {
+        bm[t] = fmaxf(sc[t][0], sc[t][1]);
+        if constexpr (JB == 2) bm[t] = fmaxf(bm[t], fmaxf(sc[t][2], sc[t][3]));
+        grow |= bm[t] > M[t] + 2.f;
+      }
       if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) bs = fmaxf(bs, __shfl_xor_sync(0xFFFFFFFFu, bs, x));
@@ -478,7 +505,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
         const int ex = max(static_cast<int>(__float_as_uint(S) >> 23) - 126, -24);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float m2 = fmaxf(sc[t][0], sc[t][1]);
+          float m2 = bm[t];
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, x));
           m2 = fmaxf(m2, M[t]);
@@ -494,47 +521,76 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
         }
       }
 
-      // p * scale as column operands
-      uint32_t pb[NT][NS][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float p0 = ex2(sc[t][0] - ref[t]), p1 = ex2(sc[t][1] - ref[t]);
-        l[t] += p0 + p1;
-#pragma unroll
-        for (int k = 0; k < NS; ++k) {
-          float w0 = p0 * vs0[k], w1 = p1 * vs1[k];
-          if (masked) {  // a NaN scale of a position that this row does not see
-            if (t0 + b0 >= seen[t]) w0 = 0.f;
-            if (t0 + b1 >= seen[t]) w1 = 0.f;
-          }
-          pb[t][k][0] = transpose_f16(split_f16(w0));
-          pb[t][k][1] = transpose_f16(split_f16(w1));
-        }
-      }
-
-      // sums of V
-      uint4 v0, v1;
-      v0 = *reinterpret_cast<const uint4*>(blk + q4_v_off(HD) + c * 128 + r * 16);
-      if constexpr (HD == 128) v1 = *reinterpret_cast<const uint4*>(blk + q4_v_off(HD) + 512 + c * 128 + r * 16);
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
-        uint32_t x0, x1;
-        if constexpr (HD == 128) {
-          x0 = __byte_perm(g < 2 ? v0.x : v0.y, g < 2 ? v0.z : v0.w, sel);
-          x1 = __byte_perm(g < 2 ? v1.x : v1.y, g < 2 ? v1.z : v1.w, sel);
-        } else {
-          x0 = __byte_perm(v0.x, v0.y, sel);
-          x1 = __byte_perm(v0.z, v0.w, sel);
-        }
-        const uint32_t a0[4] = {signed_lo(x0), signed_hi(x0), signed_lo(x1), signed_hi(x1)};
-        x0 >>= 8;
-        x1 >>= 8;
-        const uint32_t a1[4] = {signed_lo(x0), signed_hi(x0), signed_lo(x1), signed_hi(x1)};
+      for (int j = 0; j < JB; ++j) {
+        // p * scale as column operands
+        uint32_t pb[NT][NS][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma_f16(o[t][2 * g], a0, pb[t][g % NS][0], pb[t][g % NS][1]);
-          mma_f16(o[t][2 * g + 1], a1, pb[t][g % NS][0], pb[t][g % NS][1]);
+          const float p0 = ex2(sc[t][2 * j] - ref[t]), p1 = ex2(sc[t][2 * j + 1] - ref[t]);
+          l[t] += p0 + p1;
+#pragma unroll
+          for (int k = 0; k < NS; ++k) {
+            float w0 = p0 * vs[2 * j][k], w1 = p1 * vs[2 * j + 1][k];
+            if (masked) {  // a NaN scale of a position that this row does not see
+              if (t0 + j * kQ4Block + b0 >= seen[t]) w0 = 0.f;
+              if (t0 + j * kQ4Block + b1 >= seen[t]) w1 = 0.f;
+            }
+            pb[t][k][0] = transpose_f16(split_f16(w0));
+            pb[t][k][1] = transpose_f16(split_f16(w1));
+          }
+        }
+        // sums of V
+        const unsigned char* vr = from + j * BB + q4_v_off(HD) + c * 128 + r * 16;
+        const uint4 v0 = *reinterpret_cast<const uint4*>(vr);
+        uint4 v1 = v0;
+        if constexpr (HD == 128) v1 = *reinterpret_cast<const uint4*>(vr + 512);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+          uint32_t x0, x1;
+          if constexpr (HD == 128) {
+            x0 = __byte_perm(g < 2 ? v0.x : v0.y, g < 2 ? v0.z : v0.w, sel);
+            x1 = __byte_perm(g < 2 ? v1.x : v1.y, g < 2 ? v1.z : v1.w, sel);
+          } else {
+            x0 = __byte_perm(v0.x, v0.y, sel);
+            x1 = __byte_perm(v0.z, v0.w, sel);
+          }
+          const uint32_t a0[4] = {unpack.low(x0), unpack.high(x0), unpack.low(x1), unpack.high(x1)};
+          x0 >>= 8;
+          x1 >>= 8;
+          const uint32_t a1[4] = {unpack.low(x0), unpack.high(x0), unpack.low(x1), unpack.high(x1)};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma_f16(o[t][2 * g], a0, pb[t][g % NS][0], pb[t][g % NS][1]);
+            mma_f16(o[t][2 * g + 1], a1, pb[t][g % NS][0], pb[t][g % NS][1]);
+          }
+        }
+      }
+    };
+    for (; rel < rel_end; rel += W) {
+      issue();
+      __syncwarp();
+      if (!dead) dead = !mbar_wait_bounded(&bar[st], phase, nullptr);
+      const int t0 = (rel + unit0) * kUnit;
+      const int fl = flag[st];
+      const unsigned char* at = my_ring + st * 2 * BB;
+      if (++st == ST) {
+        st = 0;
+        phase ^= 1;
+      }
+      if (fl || dead) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (((fl & 1 || dead) && t0 < seen[t]) || (fl & 2 && t0 + kQ4Block < seen[t])) l[t] = kNaN;
+      }
+      if (fl < 4 && !dead) {  // (a block without a page counts as behind the end: rows that see it are NaN already)
+#pragma unroll 1
+        for (int j = 0; j < 2; j += JB) {
+          if (fl || t0 + kUnit > min_seen)
+            blocks(std::true_type{}, at + j * BB, t0 + j * kQ4Block, fl >> j);
+          else
+            blocks(std::false_type{}, at + j * BB, t0 + j * kQ4Block, 0);
         }
       }
       __syncwarp();  // every lane has read the stage before it is filled again
@@ -610,7 +666,7 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   const unsigned long long u0 = blockIdx.x * plan.per, u1 = u0 + plan.per;
   if (u1 >= plan.total) return;  // nothing behind this run
   const int s = plan.seq_of(u1 - 1);
-  const int nb = plan.blocks(s);
+  const int nb = plan.units(s);
   const unsigned long long seg = udiv(u1 - 1 - plan.pre[s], nb);
   const unsigned long long seg0 = plan.pre[s] + seg * nb, seg1 = seg0 + nb;
   if (seg0 < u0 || seg1 <= u1) return;  // begun by an earlier run, or ended by this one

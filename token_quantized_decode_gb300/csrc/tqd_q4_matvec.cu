@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t r
 
 constexpr int kMvWarps = 8;
 constexpr int kMvThreads = 32 * kMvWarps;
-constexpr int kMvXBytes = 73728;  // staged vectors: two CTAs fit an SM
+constexpr int kMvXBytes = 75776;  // staged vectors: two CTAs fit an SM
 // Stages (strips) of a warp's ring.
 __host__ __device__ constexpr int mv_stages(int nt) { return nt == 4 ? 3 : 4; }
 
@@ -85,9 +85,10 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   unsigned char* ring = sm;
   float* red = reinterpret_cast<float*>(ring + kMvWarps * kMvStages * kStage);  // [warps][2 NT][32]
   auto* bars = reinterpret_cast<uint64_t*>(red + kMvWarps * 2 * NT * 32);
-  // [groups of a slab][NC / 2]: start of the high and of the low part's sum, the vector's factor
+  // [groups of a slab][NC / 2]: start of the sums of the high and low parts (of two rows); the vector's factor
   float4* zs = reinterpret_cast<float4*>(bars + kMvWarps * kMvStages);
-  unsigned char* xs = reinterpret_cast<unsigned char*>(zs + a.slab * 4 * (NC / 2));  // [groups][NC][4][16 bytes]
+  float* fs = reinterpret_cast<float*>(zs + a.slab * 4 * (NC / 2));
+  unsigned char* xs = reinterpret_cast<unsigned char*>(fs + a.slab * 4 * (NC / 2));  // [groups][NC][4][16 bytes]
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r8 = lane >> 2, c = lane & 3;
@@ -177,8 +178,12 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
       }
       if (v >= NC / 2) continue;
       const int g = o >> 2, oc = o & 3;
-      if (oc == 0)
-        zs[g * (NC / 2) + v] = make_float4(-8.f * 0x1p-24f * zh, -8.f * 0x1p-24f * zl, pow2(min(24 - up, 127)), 0.f);
+      if (oc == 0) {
+        zh *= -8.f * 0x1p-24f;
+        zl *= -8.f * 0x1p-24f;
+        zs[g * (NC / 2) + v] = make_float4(zh, zl, zh, zl);
+        fs[g * (NC / 2) + v] = pow2(min(24 - up, 127));
+      }
       uint4 q;
       unsigned char* d = xs + ((g * NC + 2 * v) * 4 + oc) * 16;
       q.x = pack_f16(hi[0], hi[4]);
@@ -228,11 +233,12 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
               const int col = ONE ? r8 & 1 : t * 8 + r8;  // (one vector: the other columns repeat its two)
               const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl + g) * NC + col) * 4 + c) * 16);
               const float4 z = zs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
-              float d[4] = {z.x, z.y, z.x, z.y};
-              mma_f16(d, a0, xv.x, xv.y);
+              const float f = fs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
+              float d[4];
+              mma_f16(d, a0, xv.x, xv.y, z.x, z.y, z.z, z.w);
               mma_f16(d, a1, xv.z, xv.w);
-              acc[t][0] += d0 * (z.z * (d[0] + d[1]));
-              acc[t][1] += d1 * (z.z * (d[2] + d[3]));
+              acc[t][0] += d0 * (f * (d[0] + d[1]));
+              acc[t][1] += d1 * (f * (d[2] + d[3]));
             }
           }
           __syncwarp();  // every lane has read the stage before it is filled again
@@ -279,11 +285,11 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
 template <int NT, bool ONE>
 cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   constexpr int NC = ONE ? 2 : 8 * NT;
-  const int most = kMvXBytes / ((NC * 64 + NC / 2 * 16) * 4);  // strips whose vectors fit
+  const int most = kMvXBytes / ((NC * 64 + NC / 2 * 20) * 4);  // strips whose vectors fit
   const int slabs = (a.strips + most - 1) / most;
   a.slab = (a.strips + slabs - 1) / slabs;
   const size_t smem = static_cast<size_t>(kMvWarps) * mv_stages(NT) * (kQ4TileBytes + 8) +
-                      static_cast<size_t>(kMvWarps) * 2 * NT * 128 + static_cast<size_t>(a.slab) * 4 * (NC * 64 + NC / 2 * 16);
+                      static_cast<size_t>(kMvWarps) * 2 * NT * 128 + static_cast<size_t>(a.slab) * 4 * (NC * 64 + NC / 2 * 20);
   // a warp a row tile where that keeps eight warps on each SM busy, else 2, 4 or 8
   a.wk = 1;
   while (a.wk < kMvWarps && static_cast<int64_t>(a.row_tiles) * a.wk < 152 * kMvWarps && a.wk * 2 <= a.slab) a.wk *= 2;
