@@ -152,6 +152,10 @@ cudaError_t launch_sample(const DevSeq* seqs, int n, int V, int max_seq, const S
 // Validate the caller's sampling controls into a, and say whether they are greedy.
 int32_t sampling_args(const ::tqd_sampling* p, SampleArgs& a, bool* greedy);
 
+// Let a kernel use `bytes` of dynamic shared memory: asked of the driver once
+// per kernel and device (`done`, one bit a device), then known.
+cudaError_t allow_smem(const void* kernel, size_t bytes, unsigned long long* done);
+
 // The paged Q4 cache (tqd_q4_cache.cu, tqd_q4_attention.cu), Q4_0 weights
 // (tqd_q4_matvec.cu) and log probabilities (tqd_logprobs.cu): operator entry
 // points' kernels.  Row strides are in elements.

@@ -734,8 +734,9 @@ template <int HD, int NT, int GV>
 cudaError_t launch(const Q4AttnArgs& a, cudaStream_t st) {
   using C = Cfg<HD, NT, GV>;
   const size_t plan_b = plan_bytes(a.c.n_seq), smem = C::smem + plan_b;
-  cudaError_t e = cudaFuncSetAttribute(k_attention_q4<HD, NT, GV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static unsigned long long done = 0;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_attention_q4<HD, NT, GV>),
+                             C::smem + plan_bytes(kQ4MaxSeqs), &done);
   if (e != cudaSuccess) return e;
   k_attention_q4<HD, NT, GV><<<kCtas, C::T, smem, st>>>(a);
   e = cudaGetLastError();

@@ -42,9 +42,13 @@ __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t r
 
 constexpr int kMvWarps = 8;
 constexpr int kMvThreads = 32 * kMvWarps;
-constexpr int kMvXBytes = 75776;  // staged vectors: two CTAs fit an SM
 // Stages (strips) of a warp's ring.
 __host__ __device__ constexpr int mv_stages(int nt) { return nt == 4 ? 3 : 4; }
+// Shared memory of a CTA: at most what lets two of them share an SM; the rings
+// and the warps' sums, then the staged vectors.
+constexpr int kMvSmem = 113 * 1024;
+constexpr int mv_fixed_smem(int nt) { return kMvWarps * (mv_stages(nt) * (kQ4TileBytes + 8) + 2 * nt * 128); }
+constexpr int mv_strip_smem(int cols) { return 4 * (cols * 64 + cols / 2 * 20); }
 
 struct MatvecQ4Args {
   const uint8_t* w;
@@ -285,11 +289,10 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
 template <int NT, bool ONE>
 cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   constexpr int NC = ONE ? 2 : 8 * NT;
-  const int most = kMvXBytes / ((NC * 64 + NC / 2 * 20) * 4);  // strips whose vectors fit
+  constexpr int most = (kMvSmem - mv_fixed_smem(NT)) / mv_strip_smem(NC);  // strips whose vectors fit
   const int slabs = (a.strips + most - 1) / most;
   a.slab = (a.strips + slabs - 1) / slabs;
-  const size_t smem = static_cast<size_t>(kMvWarps) * mv_stages(NT) * (kQ4TileBytes + 8) +
-                      static_cast<size_t>(kMvWarps) * 2 * NT * 128 + static_cast<size_t>(a.slab) * 4 * (NC * 64 + NC / 2 * 20);
+  const size_t smem = static_cast<size_t>(mv_fixed_smem(NT)) + static_cast<size_t>(a.slab) * mv_strip_smem(NC);
   // a warp a row tile where that keeps eight warps on each SM busy, else 2, 4 or 8
   a.wk = 1;
   while (a.wk < kMvWarps && static_cast<int64_t>(a.row_tiles) * a.wk < 152 * kMvWarps && a.wk * 2 <= a.slab) a.wk *= 2;
@@ -298,8 +301,8 @@ cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   if (blocks > 304) blocks = 304;
   a.per_slot = (a.row_tiles + blocks * slots - 1) / (blocks * slots);
   blocks = (a.row_tiles + a.per_slot * slots - 1) / (a.per_slot * slots);
-  const cudaError_t e = cudaFuncSetAttribute(k_q4_matvec<NT, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+  static unsigned long long done = 0;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_q4_matvec<NT, ONE>), kMvSmem, &done);
   if (e != cudaSuccess) return e;
   k_q4_matvec<NT, ONE><<<dim3(blocks, (a.n + 15) / 16), kMvThreads, smem, st>>>(a);
   return cudaGetLastError();
