@@ -1,22 +1,29 @@
 // Log probabilities of given tokens, entropy and top alternatives, from one
 // pass over the logits.
 //
-// Mathematics.  With m the largest logit so far, s = sum e^(x - m) and
-// t = sum e^(x - m) (x - m), rescaled when m grows: log p = (x - m) - log s and
-// the entropy is log s - t / s.  d = x - m is clamped to [-200, 0], which also
-// settles the special values: (-inf) - m becomes a term of 0, inf - inf (NaN)
-// becomes a term of 1, so infinite logits share the probability.
+// Mathematics, in units of log2.  With m the largest logit so far and
+// ref = f32(m log2 e), s = sum 2^(x log2 e - ref) and t = sum 2^(x log2 e - ref)
+// (x log2 e - ref), rescaled when m grows: log2 p = (x log2 e - ref) - log2 s and
+// the entropy is log2 s - t / s.  x log2 e - ref is one fused operation; ref is the
+// same number in every term, so its rounding cancels.  The exponent is kept at
+// -300 or more, which makes NaN and -inf logits terms of 0.  Where m is 2^20 or more
+// in magnitude (ref's rounding would no longer be small) a term is
+// 2^((x - m) log2 e), of two operations, and 1 where x = m: infinite logits share
+// the probability.
 //
 // Alternatives are ordered by a 64-bit key (the logit's bits in integer order,
 // then the complement of the index), which no two tokens share, so the result
 // does not depend on the order of insertion.  A block keeps a list of
-// candidates in shared memory and a threshold, the k-th best logit of its
-// earlier tiles: a thread compares its largest new logit with it, and on most tiles that
-// is all.  The first tile's threshold is the k-th largest of the threads' own
-// maxima (at least k tokens reach it, and about k do).
+// candidates in shared memory and a threshold, the k-th best logit of the
+// groups of tiles behind it: a thread compares its largest new logit with it, and on most
+// tiles that is all.  The first group, and one that overflows the list, is
+// read again (from L2) with a threshold of its own: the k-th largest of the threads'
+// maxima over it, which at least k and, but for equal logits, at most 32 k tokens
+// reach.
 //
-// HBM bounds it: 4 bytes a logit and about ten instructions.  A tile is 8
-// logits a thread, the next one's loads issued before the current one's work.
+// HBM bounds it: 4 bytes a logit and about seven instructions (a fused
+// multiply-add, a maximum, an exponential, two sums; half a maximum).  A tile is
+// 8 logits a thread, the next one's loads issued before the current one's work.
 // Few rows are cut into slices of whole tiles, one block each, whose partial
 // (m, s, t) and alternatives a second kernel joins (programmatic dependent launch).
 #include <cuda_runtime.h>
@@ -29,8 +36,10 @@ namespace {
 constexpr int kLT = 256;         // threads of a block
 constexpr int kEach = 8;         // logits of a thread per tile
 constexpr int kTile = kLT * kEach;
-constexpr int kCap = 512;        // candidates a block holds
-constexpr int kFull = 160;       // candidates at which it keeps the k best only
+constexpr int kGroup = 4;        // tiles between looks at the list
+constexpr int kCap = 1024;       // candidates a block holds: kGroup * kEach * kLogprobMaxTopK
+constexpr int kFull = 128;       // candidates at which it keeps the k best only
+static_assert(kCap == kGroup * kEach * kLogprobMaxTopK, "a group's candidates fit but for equal logits");
 constexpr int kJoinCap = kLogprobMaxTopK * kLogprobMaxTopK;
 constexpr int kMaxSlices = 256;
 
@@ -49,24 +58,37 @@ __device__ __forceinline__ float key_logit(Key k) {
 }
 __device__ __forceinline__ int key_index(Key k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
 
-// x - m for a term of the sums, see above; m > -inf.
-__device__ __forceinline__ float term(float x, float m) { return fmaxf(fminf(x - m, 0.f), -200.f); }
-__device__ __forceinline__ float exp_of(float d) {
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
+// Whether sums with largest logit m are relative to ref_of(m), or to m itself.
+__device__ __forceinline__ bool by_ref(float m) { return fabsf(m) < 1048576.f; }
+// (A rounded product wherever it is made: left to itself the compiler fuses it into what uses it.)
+__device__ __forceinline__ float ref_of(float m) { return __fmul_rn(m, kLog2e); }
+// log2 of how far above 2^0 the largest logit's own term is.
+__device__ __forceinline__ float over_of(float m) { return by_ref(m) ? fmaf(m, kLog2e, -ref_of(m)) : 0.f; }
+// The exponent that takes sums with largest logit a to those with b >= a > -inf.
+__device__ __forceinline__ float gap(float a, float b) {
+  if (a == b) return 0.f;
+  const float d = by_ref(a) && by_ref(b) ? ref_of(a) - ref_of(b) : (a - b) * kLog2e - over_of(a) + over_of(b);
+  return fmaxf(d, -300.f);
+}
+
 struct Sums {
-  float m, s, t;
+  float m, s, t;  // largest logit; sums of terms, and of terms times their exponents
 };
 
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   Sums r;
   r.m = fmaxf(a.m, b.m);
   if (r.m == -INFINITY) return a;
-  const float da = term(a.m, r.m), db = term(b.m, r.m);
-  const float wa = exp_of(da), wb = exp_of(db);
+  const float da = gap(a.m, r.m), db = gap(b.m, r.m);
+  const float wa = ex2(da), wb = ex2(db);
   r.s = wa * a.s + wb * b.s;
   r.t = wa * (a.t + a.s * da) + wb * (b.t + b.s * db);
   return r;
@@ -102,7 +124,8 @@ __device__ void keep_best(const Key* keys, int n, int k, Key* out) {
 }
 
 struct RowOut {
-  float m, log_s;
+  float m, log_s;  // log_s: log sum e^(x - m)
+  __device__ RowOut(const Sums& v) : m(v.m), log_s(kLn2 * (log2f(v.s) - over_of(v.m))) {}
   __device__ float logprob(float x) const {
     return !(x > -INFINITY) ? -INFINITY : (x == m ? 0.f : x - m) - log_s;
   }
@@ -110,7 +133,7 @@ struct RowOut {
 
 // The row's results from its sums and its n <= k best keys.
 __device__ void write_row(const LogprobArgs& a, int64_t row, const Sums& v, const Key* best, int n) {
-  const RowOut o{v.m, logf(v.s)};
+  const RowOut o(v);
   const int t = threadIdx.x;
   if (t < a.top_k) {
     const Key k = t < n ? best[t] : 0ull;
@@ -121,18 +144,18 @@ __device__ void write_row(const LogprobArgs& a, int64_t row, const Sums& v, cons
     const int id = a.targets[row];
     a.logprob[row] = id < 0 || id >= a.vocab ? __int_as_float(0x7FC00000) : o.logprob(a.logits[row * a.stride + id]);
   }
-  if (t == 64 && a.entropy) a.entropy[row] = v.m > -INFINITY ? o.log_s - v.t / v.s : 0.f;
+  if (t == 64 && a.entropy) a.entropy[row] = v.m > -INFINITY ? kLn2 * (log2f(v.s) - v.t / v.s) : 0.f;
 }
 
 // One slice's partial in scratch: (m, s, t, alternatives' number), top_k keys.
 __host__ __device__ constexpr size_t partial_bytes(int top_k) { return 16 + static_cast<size_t>(top_k + (top_k & 1)) * 8; }
 
-__global__ void __launch_bounds__(kLT, 4) k_logprobs(LogprobArgs a, int slices, int tiles_each) {
-  __shared__ Key buf[kCap];
+__global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, int tiles_each) {
+  __shared__ __align__(16) Key buf[kCap];
   __shared__ Key best[kLogprobMaxTopK];
   __shared__ __align__(16) float heads[kLT];
   __shared__ Sums sm[kLT / 32];
-  __shared__ int count;
+  __shared__ int counts[3];  // insertions of a group, of the next, of the one after
   __shared__ float floor_;
   const int tid = threadIdx.x, k = a.top_k;
   pdl_launch_dependents();
@@ -143,107 +166,143 @@ __global__ void __launch_bounds__(kLT, 4) k_logprobs(LogprobArgs a, int slices, 
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
   const int tiles = (a.vocab + off + kTile - 1) / kTile;
   const int tile0 = slice * tiles_each, tile1 = min(tile0 + tiles_each, tiles);
-  if (tid == 0) {
-    count = 0;
-    floor_ = -INFINITY;
-  }
+  if (tid < 3) counts[tid] = 0;
 
   auto index_of = [&](int tile, int j) { return tile * kTile - off + (j >> 2) * (kLT * 4) + tid * 4 + (j & 3); };
   auto load = [&](int tile, float (&v)[kEach]) {
+    const int i = index_of(tile, 0);
+    if (tile * kTile >= off && (tile + 1) * kTile - off <= a.vocab) {  // a whole tile
 #pragma unroll
-    for (int h = 0; h < kEach / 4; ++h) {
-      const int i = index_of(tile, h * 4);
-      if (i >= 0 && i + 3 < a.vocab) {
-        const float4 q = __ldcs(reinterpret_cast<const float4*>(x + i));
+      for (int h = 0; h < kEach / 4; ++h) {
+        const float4 q = *reinterpret_cast<const float4*>(x + i + h * (kLT * 4));
         v[4 * h] = q.x; v[4 * h + 1] = q.y; v[4 * h + 2] = q.z; v[4 * h + 3] = q.w;
-      } else {
+      }
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * h + j] = i + j >= 0 && i + j < a.vocab ? x[i + j] : -INFINITY;
+      for (int h = 0; h < kEach; ++h) {
+        const int at = index_of(tile, h);
+        v[h] = at >= 0 && at < a.vocab ? x[at] : -INFINITY;
       }
     }
   };
+  int held = 0, turn = 0;  // the list's length at the group's start (every thread's), and the group's counter
+  auto insert = [&](float v, int i) {
+    const int p = held + atomicAdd(&counts[turn], 1);
+    if (p < kCap) buf[p] = logit_key(v, i);
+    return p;
+  };
 
   Sums own{-INFINITY, 0.f, 0.f};
-  float floor_r = -INFINITY;
+  float ref = 0.f;
+  float least = INFINITY;  // the first group is read again with a threshold of its own
   float nx[kEach];
   if (tile0 < tile1) load(tile0, nx);
   __syncthreads();
-  for (int tile = tile0; tile < tile1; ++tile) {
-    float v[kEach];
+  for (int group = tile0; group < tile1; group += kGroup) {
+    const int end = min(group + kGroup, tile1);
+    const bool first = group == tile0;
+    // (the counter of the next group was last read before the barrier behind the group before this one)
+    if (tid == 0) counts[turn == 2 ? 0 : turn + 1] = 0;
+    float gm = -INFINITY;
+    bool want = first;
+    for (int tile = group; tile < end; ++tile) {
+      float v[kEach];
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) v[j] = fmaxf(nx[j], -INFINITY);  // NaN counts as -inf
-    if (tile + 1 < tile1) load(tile + 1, nx);
-    float lm = v[0];
+      for (int j = 0; j < kEach; ++j) v[j] = nx[j];
+      if (tile + 1 < tile1) load(tile + 1, nx);
+      float lm = v[0];
 #pragma unroll
-    for (int j = 1; j < kEach; ++j) lm = fmaxf(lm, v[j]);
-    if (lm > own.m) {
-      const float d = term(own.m, lm), w = exp_of(d);
-      own.t = w * (own.t + own.s * d);
-      own.s *= w;
-      own.m = lm;
-    }
-    if (own.m > -INFINITY) {
+      for (int j = 1; j < kEach; ++j) lm = fmaxf(lm, v[j]);
+      lm = fmaxf(lm, -INFINITY);  // (eight NaN)
+      gm = fmaxf(gm, lm);
+      if (lm > own.m) {
+        const float d = gap(own.m, lm), w = ex2(d);
+        own.t = w * (own.t + own.s * d);
+        own.s *= w;
+        own.m = lm;
+        ref = ref_of(lm);
+      }
+      if (by_ref(own.m)) {
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        const float d = term(v[j], own.m), e = exp_of(d);
-        own.s += e;
-        own.t = fmaf(e, d, own.t);
+        for (int j = 0; j < kEach; ++j) {
+          const float d = fmaxf(fmaf(v[j], kLog2e, -ref), -300.f), e = ex2(d);
+          own.s += e;
+          own.t = fmaf(e, d, own.t);
+        }
+      } else if (own.m > -INFINITY) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const float d = v[j] == own.m ? 0.f : fmaxf((v[j] - own.m) * kLog2e, -300.f), e = ex2(d);
+          own.s += e;
+          own.t = fmaf(e, d, own.t);
+        }
+      }
+      if (lm > least) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (v[j] > least) want |= insert(v[j], index_of(tile, j)) >= kFull;
       }
     }
     if (k == 0) continue;
+    const bool merge = __syncthreads_or(want) || end == tile1;
+    int n = held + counts[turn];
+    if (!merge) {
+      held = n;
+      turn = turn == 2 ? 0 : turn + 1;
+      continue;
+    }
 
-    // ---- candidates
-    const bool first = tile == tile0;
-    float least = floor_r;
-    if (first) {
-      heads[tid] = lm;
+    // ---- keep the k best
+    if (first || n > kCap) {
+      // The group again: the tokens that reach the k-th largest of the threads'
+      // maxima, and those that the earlier list holds.  (Of this group's own
+      // first insertions none are kept: they began at `held`.)
+      heads[tid] = gm;
       __syncthreads();
+      if (tid == 0) {
+        counts[turn] = 0;
+        floor_ = -INFINITY;
+      }
       int rank = 0;
 #pragma unroll 8
       for (int j = 0; j < kLT; j += 4) {
         const float4 h = *reinterpret_cast<const float4*>(heads + j);
-        rank += (h.x > lm || (h.x == lm && j < tid)) + (h.y > lm || (h.y == lm && j + 1 < tid)) +
-                (h.z > lm || (h.z == lm && j + 2 < tid)) + (h.w > lm || (h.w == lm && j + 3 < tid));
+        rank += (h.x > gm || (h.x == gm && j < tid)) + (h.y > gm || (h.y == gm && j + 1 < tid)) +
+                (h.z > gm || (h.z == gm && j + 2 < tid)) + (h.w > gm || (h.w == gm && j + 3 < tid));
       }
-      if (rank == k - 1) floor_ = lm;
       __syncthreads();
-      least = floor_;
+      if (rank == k - 1) floor_ = gm;
+      __syncthreads();
+      const float reach = floor_, above = first ? -INFINITY : least;
+      if (gm >= reach && gm > above)
+        for (int tile = group; tile < end; ++tile)
+          for (int j = 0; j < kEach; ++j) {
+            const int i = index_of(tile, j);
+            const float v = i >= 0 && i < a.vocab ? x[i] : -INFINITY;
+            if (v >= reach && v > above) insert(v, i);
+          }
+      __syncthreads();
+      n = held + counts[turn];
     }
-    bool want_merge = first;
-    if (first ? lm >= least && lm > -INFINITY : lm > least) {
-#pragma unroll
-      for (int j = 0; j < kEach; ++j)
-        if (first ? v[j] >= least && v[j] > -INFINITY : v[j] > least) {
-          const int p = atomicAdd(&count, 1);
-          if (p < kCap) buf[p] = logit_key(v[j], index_of(tile, j));
-          want_merge |= p >= kFull;
-        }
-    }
-    if (!__syncthreads_or(want_merge) && tile + 1 < tile1) continue;
-
-    // ---- keep the k best (all threads are here; the count is final)
-    int n = count;
     if (n > kCap) {
-      // More tokens passed than the list holds (many equal logits, or ascending
-      // ones): the tile's own k best one by one, with the earlier list's.
-      // The list before this tile held at most kFull + (a tile's last inserts),
-      // and what fitted of this tile is found again, so equal keys are dropped.
+      // Too many equal logits: the group's k best one by one, from it and the earlier list.
       Key below = ~0ull;
+      Key* hk = reinterpret_cast<Key*>(heads);
       for (int r = 0; r < k; ++r) {
         Key top = 0ull;
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-          const Key key = logit_key(v[j], index_of(tile, j));
-          if (key < below && key > top) top = key;
-        }
-        for (int j = tid; j < kCap; j += kLT)
+        for (int tile = group; tile < end; ++tile)
+          for (int j = 0; j < kEach; ++j) {
+            const int i = index_of(tile, j);
+            const Key key = i >= 0 && i < a.vocab ? logit_key(x[i], i) : 0ull;
+            if (key < below && key > top) top = key;
+          }
+        for (int j = tid; j < held; j += kLT)
           if (buf[j] < below && buf[j] > top) top = buf[j];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           const Key w = __shfl_xor_sync(0xFFFFFFFFu, top, o);
           if (w > top) top = w;
         }
-        Key* hk = reinterpret_cast<Key*>(heads);
         if ((tid & 31) == 0) hk[tid >> 5] = top;
         __syncthreads();
         top = hk[0];
@@ -253,19 +312,20 @@ __global__ void __launch_bounds__(kLT, 4) k_logprobs(LogprobArgs a, int slices, 
         below = top;
         __syncthreads();
       }
-      n = k;  // (keys of 0: fewer than k above -inf, impossible with a full list)
+      n = k;  // (there are more than kCap >= k)
     } else {
       keep_best(buf, n, k, best);
       n = min(n, k);
     }
     if (tid < n) buf[tid] = best[tid];
-    if (tid == 0) count = n;
-    floor_r = n == k ? key_logit(best[k - 1]) : -INFINITY;
+    held = n;
+    turn = turn == 2 ? 0 : turn + 1;
+    least = n == k ? key_logit(best[k - 1]) : -INFINITY;
     __syncthreads();
   }
 
   const Sums all = block_join(own, sm);
-  const int n = k ? count : 0;
+  const int n = held;
   if (slices == 1) {
     write_row(a, row, all, best, n);
     return;

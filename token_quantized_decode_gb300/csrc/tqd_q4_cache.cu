@@ -20,8 +20,8 @@ __device__ __forceinline__ uint8_t* q4_block_of(const Q4Cache& c, int seq, int p
          (static_cast<size_t>(h) * (c.page_size / kQ4Block) + in_page / kQ4Block) * q4_block_bytes(hd);
 }
 
-// One group of 32 (a lane's element each): the codes are rint(7 y / max|y|)
-// and the scale f16(max|y| / 7) of the exact rotated values.
+// Codes and scale of one group of 32, a lane's element each: rint(7 y / max|y|)
+// + 8 and f16(max|y| / 7) of the exact values.
 struct Q4Code {
   uint32_t code;   // 1..15 (8: zero)
   uint32_t scale;  // f16 bits, the same in every lane
@@ -38,42 +38,42 @@ __device__ __noinline__ Q4Code q4_code_exact(double y) {
   return r;
 }
 
-// y: the lane's element in f32; e: |x0| + |x1| of the rotation that made it
-// (0: y is exact).  exact(): the element in f64, called by whole warps only.
+// The same in f32, and whether the result is sure.  M: the group's largest
+// |x0| + |x1| of the rotation that made y (0: y is exact).
 //
-// The f32 rotation is off by at most 2^-23 e, so 7 y / max|y| by at most
-// 2^-19 (M / max|y| + 1) with M the largest e of the group; where a code lies
-// closer than that to the border between two, or the scale to the border
-// between two f16, the group is coded again from f64.  That happens to about
-// one group in 3,000; coding every group in f64 would bound the kernel by the
-// f64 units (about two operations a clock per SM).
-template <class F>
-__device__ __forceinline__ Q4Code q4_code(float y, float e, F exact) {
+// The f32 rotation is off by at most 2^-23 M, so 7 y / max|y| by at most
+// 2^-19 (M / max|y| + 1), the approximate reciprocal's 2^-23 included; where a
+// code lies closer than that to the border between two, or the scale to the
+// border between two f16, the group is coded again from f64.  That happens to
+// about one group in 2,000; coding every group in f64 would bound the kernel by
+// the f64 units (about two operations a clock per SM).
+__device__ __forceinline__ Q4Code q4_code(float y, float M, bool& unsure) {
   const float a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(y))));
-  const float M = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(e)));
-  const float d = __fdiv_rn(a, 7.f);
-  Q4Code r;
-  // a NaN or an infinity in the group, or a scale past the f16 range: the
-  // scale is NaN, so the group stands for NaN
-  if (!(d < 65520.f)) {
-    r.code = 8u;
-    r.scale = 0x7E00u;
-    return r;
-  }
-  const float rel = a > 0.f ? M / a : 0.f;
-  const float t = y * __fdiv_rn(7.f, a);
+  // a / 7 rounded: one step from a times the nearest f32 to 1 / 7
+  float d = a * 0.14285715f;
+  d = fmaf(fmaf(-7.f, d, a), 0.14285715f, d);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(a));
+  const float rel = M * inv;
+  const float t = y * (7.f * inv);
   const float q = rintf(t);
-  const float band = 1.9073486e-6f * (rel + 1.f);  // 2^-19
-  const float slack = d * (2.3841858e-7f * (rel + 1.f));  // 2^-22
-  bool unsure = fabsf(t - q) > 0.5f - band;
+  Q4Code r;
+  const __half h = __float2half_rn(d);
+  r.scale = __half_as_ushort(h);
+  r.code = static_cast<uint32_t>(static_cast<int>(q) + 8);
+  unsure = fabsf(t - q) > fmaf(rel, -1.9073486e-6f, 0.49999809f);  // 1/2 - 2^-19 (rel + 1)
   if (M > 0.f) {
-    const uint16_t lo = __half_as_ushort(__float2half_rn(d - slack)), hi = __half_as_ushort(__float2half_rn(d + slack));
-    unsure |= lo != hi || rel > 256.f;
+    const float slack = d * fmaf(rel, 2.3841858e-7f, 2.3841858e-7f);  // 2^-22
+    unsure |= __half_as_ushort(__float2half_rn(d - slack)) != __half_as_ushort(__float2half_rn(d + slack)) || rel > 256.f;
   }
-  unsure |= a < 1e-30f && (a > 0.f || M > 0.f);
-  if (__any_sync(0xFFFFFFFFu, unsure)) return q4_code_exact(exact());
-  r.code = a > 0.f ? static_cast<uint32_t>(static_cast<int>(q) + 8) : 8u;
-  r.scale = __half_as_ushort(__float2half_rn(d));
+  if (!(a > 1e-30f && d < 65520.f)) {
+    // All 0; so small that the steps above lose bits; or a NaN or an infinity
+    // in the group, or a scale past the f16 range: the scale is NaN, so the
+    // group stands for NaN.
+    unsure = d < 65520.f && (a > 0.f || M > 0.f);
+    r.code = 8u;
+    r.scale = d < 65520.f ? 0u : 0x7E00u;
+  }
   return r;
 }
 
@@ -136,42 +136,93 @@ __global__ void __launch_bounds__(256) k_kv_append_q4(AppendArgs a) {
   if (!blk) return;
 
   const int b = (pos % a.c.page_size) % kQ4Block;
-  uint32_t kword = 0, ksc[2] = {0u, 0u}, vsc[2] = {0u, 0u}, vpiece[2] = {0u, 0u};
+  uint32_t kcode[NG], vcode[NG], ksc[NG], vsc[NG], again = 0;
+  float M[NG / 2];
+#pragma unroll
+  for (int p = 0; p < NG / 2; ++p)
+    M[p] = a.rope ? __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(x[p]) + fabsf(x[p + NG / 2]))))
+                  : 0.f;
 #pragma unroll
   for (int j = 0; j < NG; ++j) {
-    const int p = j % (NG / 2);
-    const bool second = j >= NG / 2;
-    const Q4Code kc = q4_code(y[j], a.rope ? fabsf(x[p]) + fabsf(x[p + NG / 2]) : 0.f, [&] {
-      if (!a.rope) return static_cast<double>(x[j]);
-      const double x0 = x[p], x1 = x[p + NG / 2], c = cs[p], s = sn[p];
-      return second ? x1 * c + x0 * s : x0 * c - x1 * s;
-    });
-    // the eight codes of an octet of lanes into one word; lane i of the octet keeps group i's
-    uint32_t w = kc.code << (4 * (lane & 7));
-    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2);
-    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
-    if ((lane & 7) == j) kword = w;
-    ksc[j >> 1] |= kc.scale << (16 * (j & 1));
-
-    const Q4Code vc = q4_code(vx[j], 0.f, [&] { return static_cast<double>(vx[j]); });
-    // elements n, n + 8, n + 16, n + 24 of the group into 16 bits at lane n
-    uint32_t u = vc.code << (4 * (lane >> 3));
-    u |= __shfl_xor_sync(0xFFFFFFFFu, u, 8);
-    u |= __shfl_xor_sync(0xFFFFFFFFu, u, 16);
-    vpiece[j >> 1] |= u << (16 * (j & 1));
-    vsc[j >> 1] |= vc.scale << (16 * (j & 1));
+    bool unsure;
+    const Q4Code kc = q4_code(y[j], M[j % (NG / 2)], unsure);
+    kcode[j] = kc.code;
+    ksc[j] = kc.scale;
+    again |= unsure ? 1u << j : 0u;
+    const Q4Code vc = q4_code(vx[j], 0.f, unsure);
+    vcode[j] = vc.code;
+    vsc[j] = vc.scale;
+    again |= unsure ? 256u << j : 0u;
   }
-  if ((lane & 7) < NG)
-    *reinterpret_cast<uint32_t*>(blk + q4_k_row(b, HD) + (lane >> 3) * (4 * NG) + (lane & 7) * 4) = kword;
+  again = __reduce_or_sync(0xFFFFFFFFu, again);
+  if (again) {
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+      if (again >> j & 1u) {
+        const int p = j % (NG / 2);
+        const double x0 = x[p], x1 = x[p + NG / 2], c = cs[p], s = sn[p];
+        const Q4Code r = q4_code_exact(!a.rope ? static_cast<double>(x[j]) : j < NG / 2 ? x0 * c - x1 * s : x1 * c + x0 * s);
+        kcode[j] = r.code;
+        ksc[j] = r.scale;
+      }
+      if (again >> j & 256u) {
+        const Q4Code r = q4_code_exact(static_cast<double>(vx[j]));
+        vcode[j] = r.code;
+        vsc[j] = r.scale;
+      }
+    }
+  }
+
+  // K: an octet's eight codes of a group are a word.  In three exchanges each
+  // lane gives away the groups that its partner keeps and ends with one group's word.
+  const bool l2 = lane & 2, l4 = lane & 4;
+  uint32_t kword;
+  {
+    uint32_t u = 0;  // byte g: codes of lanes 2 i, 2 i + 1 of group g
+#pragma unroll
+    for (int j = 0; j < NG; ++j) u |= kcode[j] << (8 * j + 4 * (lane & 1));
+    u |= __shfl_xor_sync(0xFFFFFFFFu, u, 1);
+    if constexpr (NG == 4) {
+      // lane bit 1 keeps groups 2, 3 or 0, 1; then bit 2 keeps the odd or the even one
+      uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, l2 ? u : u >> 16, 2) & 0xFFFFu;
+      const uint32_t mine = l2 ? u >> 16 : u & 0xFFFFu;
+      // halves: codes of the quad for the lower and the higher group kept
+      const uint32_t lo4 = l2 ? got : mine, hi4 = l2 ? mine : got;  // lanes 0, 1 of the quad first
+      const uint32_t even = (lo4 & 0xFFu) | (hi4 & 0xFFu) << 8, odd = lo4 >> 8 | (hi4 & 0xFF00u);
+      got = __shfl_xor_sync(0xFFFFFFFFu, l4 ? even : odd, 4);
+      kword = l4 ? got | odd << 16 : even | got << 16;
+    } else {
+      uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, l2 ? u : u >> 8, 2) & 0xFFu;
+      const uint32_t mine = l2 ? u >> 8 & 0xFFu : u & 0xFFu;
+      const uint32_t quad = l2 ? got | mine << 8 : mine | got << 8;
+      got = __shfl_xor_sync(0xFFFFFFFFu, quad, 4);
+      kword = l4 ? got | quad << 16 : quad | got << 16;
+    }
+  }
+  // V: the codes of elements n + 8 i in nibble i of the piece of lane n
+  uint32_t vpiece[2] = {0u, 0u}, ks2[2] = {0u, 0u}, vs2[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < NG; ++j) {
+    vpiece[j >> 1] |= vcode[j] << (16 * (j & 1) + 4 * (lane >> 3));
+    ks2[j >> 1] |= ksc[j] << (16 * (j & 1));
+    vs2[j >> 1] |= vsc[j] << (16 * (j & 1));
+  }
+#pragma unroll
+  for (int h = 0; h < NG / 2; ++h) {
+    vpiece[h] |= __shfl_xor_sync(0xFFFFFFFFu, vpiece[h], 8);
+    vpiece[h] |= __shfl_xor_sync(0xFFFFFFFFu, vpiece[h], 16);
+  }
+  const int g = NG == 4 ? (l2 ? 2 : 0) + (l4 ? 1 : 0) : (l2 ? 1 : 0);
+  if (NG == 4 ? !(lane & 1) : !(lane & 5))
+    *reinterpret_cast<uint32_t*>(blk + q4_k_row(b, HD) + (lane >> 3) * (4 * NG) + g * 4) = kword;
   if (HD == 128) {
     if (lane < 8) *reinterpret_cast<uint2*>(blk + q4_v_piece(b, lane, HD)) = make_uint2(vpiece[0], vpiece[1]);
-    if (lane == 8) *reinterpret_cast<uint2*>(blk + q4_ks_off(HD) + b * 8) = make_uint2(ksc[0], ksc[1]);
-    if (lane == 9) *reinterpret_cast<uint2*>(blk + q4_vs_off(HD) + b * 8) = make_uint2(vsc[0], vsc[1]);
+    if (lane == 8) *reinterpret_cast<uint2*>(blk + q4_ks_off(HD) + b * 8) = make_uint2(ks2[0], ks2[1]);
+    if (lane == 9) *reinterpret_cast<uint2*>(blk + q4_vs_off(HD) + b * 8) = make_uint2(vs2[0], vs2[1]);
   } else {
     if (lane < 8) *reinterpret_cast<uint32_t*>(blk + q4_v_piece(b, lane, HD)) = vpiece[0];
-    if (lane == 8) *reinterpret_cast<uint32_t*>(blk + q4_ks_off(HD) + b * 4) = ksc[0];
-    if (lane == 9) *reinterpret_cast<uint32_t*>(blk + q4_vs_off(HD) + b * 4) = vsc[0];
+    if (lane == 8) *reinterpret_cast<uint32_t*>(blk + q4_ks_off(HD) + b * 4) = ks2[0];
+    if (lane == 9) *reinterpret_cast<uint32_t*>(blk + q4_vs_off(HD) + b * 4) = vs2[0];
   }
 }
 
