@@ -152,6 +152,24 @@ cudaError_t launch_sample(const DevSeq* seqs, int n, int V, int max_seq, const S
 // Validate the caller's sampling controls into a, and say whether they are greedy.
 int32_t sampling_args(const ::tqd_sampling* p, SampleArgs& a, bool* greedy);
 
+// Launch with programmatic dependent launch: the kernel may start while the one
+// before it on the stream ends, and waits for that one's end (pdl_wait) before
+// it touches global memory.
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Let a kernel use `bytes` of dynamic shared memory: asked of the driver once
 // per kernel and device (`done`, one bit a device), then known.
 cudaError_t allow_smem(const void* kernel, size_t bytes, unsigned long long* done);

@@ -1,15 +1,15 @@
 // Log probabilities of given tokens, entropy and top alternatives, from one
 // pass over the logits.
 //
-// Mathematics, in units of log2.  With m the largest logit so far and
-// ref = f32(m log2 e), s = sum 2^(x log2 e - ref) and t = sum 2^(x log2 e - ref)
-// (x log2 e - ref), rescaled when m grows: log2 p = (x log2 e - ref) - log2 s and
-// the entropy is log2 s - t / s.  x log2 e - ref is one fused operation; ref is the
-// same number in every term, so its rounding cancels.  The exponent is kept at
-// -300 or more, which makes NaN and -inf logits terms of 0.  Where m is 2^20 or more
-// in magnitude (ref's rounding would no longer be small) a term is
-// 2^((x - m) log2 e), of two operations, and 1 where x = m: infinite logits share
-// the probability.
+// Mathematics, in units of log2.  A thread keeps a whole number ref near its
+// largest logit times log2 e and s = sum 2^(x log2 e - ref), t = sum 2^(x log2 e -
+// ref) (x log2 e - ref).  x log2 e - ref is one fused operation, changes of ref are exact
+// powers of two, and ref may stay up to 16 behind, so it hardly ever changes.
+// With ref = rint(max log2 e) at the end: log2 p = (x log2 e - ref) - log2 s, and the
+// entropy is log2 s - t / s.  The exponent is kept at -300 or more, which makes NaN
+// and -inf logits terms of 0.  A row (or slice) whose largest logit is infinite
+// or beyond 2^19 in magnitude is read again with terms 2^((x - max) log2 e), 1 where
+// x = max: infinite logits share the probability.
 //
 // Alternatives are ordered by a 64-bit key (the logit's bits in integer order,
 // then the complement of the index), which no two tokens share, so the result
@@ -67,10 +67,9 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Whether sums with largest logit m are relative to ref_of(m), or to m itself.
-__device__ __forceinline__ bool by_ref(float m) { return fabsf(m) < 1048576.f; }
-// (A rounded product wherever it is made: left to itself the compiler fuses it into what uses it.)
-__device__ __forceinline__ float ref_of(float m) { return __fmul_rn(m, kLog2e); }
-// log2 of how far above 2^0 the largest logit's own term is.
+__device__ __forceinline__ bool by_ref(float m) { return fabsf(m) < 524288.f; }
+__device__ __forceinline__ float ref_of(float m) { return rintf(m * kLog2e); }
+// log2 of the largest logit's own term.
 __device__ __forceinline__ float over_of(float m) { return by_ref(m) ? fmaf(m, kLog2e, -ref_of(m)) : 0.f; }
 // The exponent that takes sums with largest logit a to those with b >= a > -inf.
 __device__ __forceinline__ float gap(float a, float b) {
@@ -158,10 +157,11 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
   __shared__ int counts[3];  // insertions of a group, of the next, of the one after
   __shared__ float floor_;
   const int tid = threadIdx.x, k = a.top_k;
+  pdl_wait();
   pdl_launch_dependents();
-  const int64_t row = blockIdx.x / slices;
+  const unsigned row = blockIdx.x / static_cast<unsigned>(slices);
   const int slice = static_cast<int>(blockIdx.x - row * slices);
-  const float* x = a.logits + row * a.stride;
+  const float* x = a.logits + static_cast<int64_t>(row) * a.stride;
   // 16-byte loads from the aligned address at or before the row; what lies outside the row is not read
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
   const int tiles = (a.vocab + off + kTile - 1) / kTile;
@@ -169,12 +169,13 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
   if (tid < 3) counts[tid] = 0;
 
   auto index_of = [&](int tile, int j) { return tile * kTile - off + (j >> 2) * (kLT * 4) + tid * 4 + (j & 3); };
+  const int whole0 = off ? 1 : 0, whole1 = (a.vocab + off) / kTile;  // tiles that lie inside the row
   auto load = [&](int tile, float (&v)[kEach]) {
-    const int i = index_of(tile, 0);
-    if (tile * kTile >= off && (tile + 1) * kTile - off <= a.vocab) {  // a whole tile
+    if (tile >= whole0 && tile < whole1) {
+      const float* p = x + index_of(tile, 0);
 #pragma unroll
       for (int h = 0; h < kEach / 4; ++h) {
-        const float4 q = *reinterpret_cast<const float4*>(x + i + h * (kLT * 4));
+        const float4 q = *reinterpret_cast<const float4*>(p + h * (kLT * 4));
         v[4 * h] = q.x; v[4 * h + 1] = q.y; v[4 * h + 2] = q.z; v[4 * h + 3] = q.w;
       }
     } else {
@@ -192,8 +193,9 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
     return p;
   };
 
-  Sums own{-INFINITY, 0.f, 0.f};
-  float ref = 0.f;
+  constexpr float kRefMin = -1048576.f;
+  float ref = kRefMin, rise = -INFINITY;  // rise: a logit above it moves the reference
+  float rs = 0.f, rt = 0.f, rm = -INFINITY;
   float least = INFINITY;  // the first group is read again with a threshold of its own
   float nx[kEach];
   if (tile0 < tile1) load(tile0, nx);
@@ -210,32 +212,23 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
 #pragma unroll
       for (int j = 0; j < kEach; ++j) v[j] = nx[j];
       if (tile + 1 < tile1) load(tile + 1, nx);
-      float lm = v[0];
+      float lm = fmaxf(v[0], -INFINITY);  // (eight NaN)
 #pragma unroll
       for (int j = 1; j < kEach; ++j) lm = fmaxf(lm, v[j]);
-      lm = fmaxf(lm, -INFINITY);  // (eight NaN)
       gm = fmaxf(gm, lm);
-      if (lm > own.m) {
-        const float d = gap(own.m, lm), w = ex2(d);
-        own.t = w * (own.t + own.s * d);
-        own.s *= w;
-        own.m = lm;
-        ref = ref_of(lm);
+      if (lm > rise) {
+        const float nref = fminf(fmaxf(rintf(lm * kLog2e), kRefMin), -kRefMin);
+        const float d = fmaxf(ref - nref, -300.f), w = ex2(d);
+        rt = w * (rt + rs * d);
+        rs *= w;
+        ref = nref;
+        rise = (nref + 16.f) * kLn2;
       }
-      if (by_ref(own.m)) {
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-          const float d = fmaxf(fmaf(v[j], kLog2e, -ref), -300.f), e = ex2(d);
-          own.s += e;
-          own.t = fmaf(e, d, own.t);
-        }
-      } else if (own.m > -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-          const float d = v[j] == own.m ? 0.f : fmaxf((v[j] - own.m) * kLog2e, -300.f), e = ex2(d);
-          own.s += e;
-          own.t = fmaf(e, d, own.t);
-        }
+      for (int j = 0; j < kEach; ++j) {
+        const float d = fmaxf(fmaf(v[j], kLog2e, -ref), -300.f), e = ex2(d);
+        rs += e;
+        rt = fmaf(e, d, rt);
       }
       if (lm > least) {
 #pragma unroll
@@ -243,6 +236,7 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
           if (v[j] > least) want |= insert(v[j], index_of(tile, j)) >= kFull;
       }
     }
+    rm = fmaxf(rm, gm);
     if (k == 0) continue;
     const bool merge = __syncthreads_or(want) || end == tile1;
     int n = held + counts[turn];
@@ -324,6 +318,28 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
     __syncthreads();
   }
 
+  // ---- the block's sums, relative to its own largest logit
+  float bm = rm;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
+  if ((tid & 31) == 0) heads[tid >> 5] = bm;
+  __syncthreads();
+  for (int w = 0; w < kLT / 32; ++w) bm = fmaxf(bm, heads[w]);
+  Sums own{bm, 0.f, 0.f};
+  if (by_ref(bm)) {
+    const float d = fmaxf(ref - ref_of(bm), -300.f), w = ex2(d);
+    own.t = w * (rt + rs * d);
+    own.s = w * rs;
+  } else if (bm > -INFINITY) {
+    for (int tile = tile0; tile < tile1; ++tile)
+      for (int j = 0; j < kEach; ++j) {
+        const int i = index_of(tile, j);
+        const float v = i >= 0 && i < a.vocab ? x[i] : -INFINITY;
+        const float d = v == bm ? 0.f : fmaxf((v - bm) * kLog2e, -300.f), e = ex2(d);
+        own.s += e;
+        own.t = fmaf(e, d, own.t);
+      }
+  }
   const Sums all = block_join(own, sm);
   const int n = held;
   if (slices == 1) {
@@ -351,6 +367,7 @@ __global__ void __launch_bounds__(kLT) k_logprobs_join(LogprobArgs a, int slices
     floor_ = 1ull;
   }
   pdl_wait();
+  pdl_launch_dependents();
   Sums own{-INFINITY, 0.f, 0.f};
   Key head = 0ull;
   if (tid < slices) {
@@ -403,19 +420,9 @@ cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
   const int slices = slices_of(a.rows, a.vocab);
   const int tiles = (a.vocab + 3 + kTile - 1) / kTile;
   const int each = (tiles + slices - 1) / slices;
-  k_logprobs<<<static_cast<unsigned>(a.rows) * slices, kLT, 0, st>>>(a, slices, each);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(k_logprobs, dim3(static_cast<unsigned>(a.rows) * slices), kLT, 0, st, a, slices, each);
   if (e != cudaSuccess || slices == 1) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.rows);
-  cfg.blockDim = dim3(kLT);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_logprobs_join, a, slices);
+  return launch_pdl(k_logprobs_join, dim3(a.rows), kLT, 0, st, a, slices);
 }
 
 }  // namespace tqd

@@ -209,8 +209,8 @@ int32_t tqd_op_kv_append_q4(const tqd_kv_q4* cache, const float* k, int64_t k_st
   const int64_t kvw = static_cast<int64_t>(c.n_kv) * cache->head_dim, qw = static_cast<int64_t>(n_heads) * cache->head_dim;
   if (k_stride < kvw || v_stride < kvw || (q && (q_stride < qw || q_out_stride < qw)))
     return refuse("tqd_op_kv_append_q4: a row stride shorter than the row");
-  if (static_cast<int64_t>(n_tokens) * (c.n_kv + static_cast<int64_t>(n_heads)) > (1ll << 33))
-    return refuse("tqd_op_kv_append_q4: n_tokens * (n_kv_heads + n_heads) above 2^33");
+  if (static_cast<int64_t>(n_tokens) * c.n_kv > (1ll << 30) || kvw > (1 << 24) || qw > (1 << 24))
+    return refuse("tqd_op_kv_append_q4: n_tokens * n_kv_heads above 2^30, or rows above 2^24 floats");
   return status_of(launch_kv_append_q4(c, cache->head_dim, k, k_stride, v, v_stride, positions, seqs, n_tokens,
                                        reinterpret_cast<const float2*>(rope_table), max_pos, q, q_stride, n_heads,
                                        q_out, q_out_stride, static_cast<cudaStream_t>(stream)));
@@ -227,7 +227,7 @@ int32_t tqd_op_kv_read_q4(const tqd_kv_q4* cache, const int32_t* positions, cons
   const int64_t kvw = static_cast<int64_t>(c.n_kv) * cache->head_dim;
   if ((k_out && k_stride < kvw) || (v_out && v_stride < kvw))
     return refuse("tqd_op_kv_read_q4: a row stride shorter than the row");
-  if (static_cast<int64_t>(n_tokens) * c.n_kv > (1ll << 33)) return refuse("tqd_op_kv_read_q4: n_tokens * n_kv_heads above 2^33");
+  if (static_cast<int64_t>(n_tokens) * c.n_kv > (1ll << 30)) return refuse("tqd_op_kv_read_q4: n_tokens * n_kv_heads above 2^30");
   return status_of(launch_kv_read_q4(c, cache->head_dim, positions, seqs, n_tokens, k_out, k_stride, v_out, v_stride,
                                      static_cast<cudaStream_t>(stream)));
 }

@@ -183,10 +183,10 @@ __device__ Plan make_plan(const Q4AttnArgs& a, int R, int W, int ctas, unsigned 
   const int each = (n + nt - 1) / nt, s0 = t * each;
   unsigned long long mine = 0;
   for (int s = s0; s < s0 + each && s < n; ++s) {
-    len[s] = max(a.lens[s], 0);
+    len[s] = max(__ldcg(a.lens + s), 0);
     int q = 1;
     if (a.q_start) {  // clipped to the query rows there are
-      const int b = a.q_start[s], e = a.q_start[s + 1];
+      const int b = __ldcg(a.q_start + s), e = __ldcg(a.q_start + s + 1);
       q = b >= 0 && b <= a.n_tokens && e > b ? min(e, a.n_tokens) - b : 0;
     }
     nq[s] = q;
@@ -233,11 +233,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;  // operand row (and r + 8), and column pair of the sums
   const int h = c / GV, gv = c % GV;      // the pair's query row in its tile and first group's chain
-  pdl_launch_dependents();
   uint64_t* bar = bars + warp * ST;
   int* flag = flags + warp * ST;
   if (lane < ST) mbar_init(&bar[lane], 1);
   fence_mbar_init();
+  pdl_wait();
+  pdl_launch_dependents();
   const Plan plan = make_plan(a, R, W, gridDim.x, plan_mem);
 
   // sequences without positions: their queries see nothing
@@ -663,6 +664,7 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   extern __shared__ __align__(128) unsigned char sm[];
   const Plan plan = make_plan(a, R, C::W, gridDim.x, sm);
   pdl_wait();
+  pdl_launch_dependents();
   const unsigned long long u0 = blockIdx.x * plan.per, u1 = u0 + plan.per;
   if (u1 >= plan.total) return;  // nothing behind this run
   const int s = plan.seq_of(u1 - 1);
@@ -738,20 +740,9 @@ cudaError_t launch(const Q4AttnArgs& a, cudaStream_t st) {
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_attention_q4<HD, NT, GV>),
                              C::smem + plan_bytes(kQ4MaxSeqs), &done);
   if (e != cudaSuccess) return e;
-  k_attention_q4<HD, NT, GV><<<kCtas, C::T, smem, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_pdl(k_attention_q4<HD, NT, GV>, dim3(kCtas), C::T, smem, st, a);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCtas);
-  cfg.blockDim = dim3(kCombine);
-  cfg.dynamicSmemBytes = plan_b;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attention_q4_join<HD, NT, GV>, a);
+  return launch_pdl(k_attention_q4_join<HD, NT, GV>, dim3(kCtas), kCombine, plan_b, st, a);
 }
 
 }  // namespace

@@ -16,6 +16,7 @@ __device__ __forceinline__ uint8_t* q4_block_of(const Q4Cache& c, int seq, int p
   const int page = c.table[static_cast<size_t>(seq) * c.table_stride + slot];
   if (page < 0 || page >= c.n_pages) return nullptr;
   const int in_page = pos - slot * c.page_size;
+  // (a page is a multiple of 16 positions: the position in its block is pos % 16)
   return c.pages + static_cast<size_t>(page) * c.page_bytes +
          (static_cast<size_t>(h) * (c.page_size / kQ4Block) + in_page / kQ4Block) * q4_block_bytes(hd);
 }
@@ -90,52 +91,71 @@ struct AppendArgs {
   int n_tokens, n_heads, max_pos;
 };
 
-// One warp per (token, head): the first n_kv heads are the cache's (the key
-// rotated, both rows coded and stored), the others rotate a query head.  A
-// lane holds elements lane + 32 j, so a group of 32 is one element per lane
-// and its maximum one redux instruction; loads are whole 128-byte lines
-// whatever the rows' alignment.
+// One warp per (token, kv head): it rotates that head's key and its share of the
+// query heads, and codes and stores the key and the value.  A lane holds
+// elements lane + 32 j, so a group of 32 is one element per lane and its maximum
+// one redux instruction; loads are whole 128-byte lines whatever the rows'
+// alignment.  All rows are loaded before the first is used: the kernel is bound
+// by that latency for a few tokens and by instructions for many (a row of K and V costs
+// about 450).
 template <int HD>
 __global__ void __launch_bounds__(256) k_kv_append_q4(AppendArgs a) {
   constexpr int NG = HD / 32;
   const int lane = threadIdx.x & 31;
-  const int per = a.c.n_kv + a.n_heads;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t token = task / per;
-  if (token >= a.n_tokens) return;
-  const int item = static_cast<int>(task - token * per);
+  const unsigned task = blockIdx.x * 8 + (threadIdx.x >> 5);  // (at most 2^30)
+  const unsigned token = task / static_cast<unsigned>(a.c.n_kv);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (token >= static_cast<unsigned>(a.n_tokens)) return;
+  const int item = static_cast<int>(task - token * a.c.n_kv);
   const int pos = a.positions[token];
   const int seq = a.seqs ? a.seqs[token] : static_cast<int>(token);
-  if (pos < 0 || seq < 0 || seq >= a.c.n_seq || (a.rope && pos >= a.max_pos)) return;  // padding
-
-  const bool is_kv = item < a.c.n_kv;
-  const float* src = is_kv ? a.k + token * a.k_stride + static_cast<int64_t>(item) * HD
-                           : a.q + token * a.q_stride + static_cast<int64_t>(item - a.c.n_kv) * HD;
-  float x[NG], y[NG], cs[NG / 2], sn[NG / 2];
+  const float* ksrc = a.k + token * a.k_stride + item * HD + lane;
+  const float* vsrc = a.v + token * a.v_stride + item * HD + lane;
+  float x[NG], y[NG], vx[NG], cs[NG / 2], sn[NG / 2];
 #pragma unroll
-  for (int j = 0; j < NG; ++j) x[j] = src[lane + 32 * j];
+  for (int j = 0; j < NG; ++j) x[j] = ksrc[32 * j];
+#pragma unroll
+  for (int j = 0; j < NG; ++j) vx[j] = vsrc[32 * j];
+  if (pos < 0 || seq < 0 || seq >= a.c.n_seq || (a.rope && pos >= a.max_pos)) return;  // padding
 #pragma unroll
   for (int j = 0; j < NG / 2; ++j) {
     const float2 w = a.rope ? a.rope[static_cast<size_t>(pos) * (HD / 2) + lane + 32 * j] : make_float2(1.f, 0.f);
     cs[j] = w.x;
     sn[j] = w.y;
-    y[j] = a.rope ? fmaf(x[j], w.x, -__fmul_rn(x[j + NG / 2], w.y)) : x[j];
-    y[j + NG / 2] = a.rope ? fmaf(x[j + NG / 2], w.x, __fmul_rn(x[j], w.y)) : x[j + NG / 2];
   }
-  if (!is_kv) {
-    float* dst = a.q_out + token * a.qo_stride + static_cast<int64_t>(item - a.c.n_kv) * HD;
+  auto rotate = [&](const float (&in)[NG], float (&out)[NG]) {
 #pragma unroll
-    for (int j = 0; j < NG; ++j) dst[lane + 32 * j] = y[j];
-    return;
-  }
-  const float* vsrc = a.v + token * a.v_stride + static_cast<int64_t>(item) * HD;
-  float vx[NG];
-#pragma unroll
-  for (int j = 0; j < NG; ++j) vx[j] = vsrc[lane + 32 * j];
+    for (int j = 0; j < NG / 2; ++j) {
+      out[j] = a.rope ? fmaf(in[j], cs[j], -__fmul_rn(in[j + NG / 2], sn[j])) : in[j];
+      out[j + NG / 2] = a.rope ? fmaf(in[j + NG / 2], cs[j], __fmul_rn(in[j], sn[j])) : in[j + NG / 2];
+    }
+  };
   uint8_t* blk = q4_block_of(a.c, seq, pos, item, HD);
+  for (int h = item; h < a.n_heads; h += 2 * a.c.n_kv) {  // two query heads at a time
+    const bool two = h + a.c.n_kv < a.n_heads;
+    const float* q = a.q + token * a.q_stride + static_cast<int64_t>(h) * HD + lane;
+    float* o = a.q_out + token * a.qo_stride + static_cast<int64_t>(h) * HD + lane;
+    const int64_t next = static_cast<int64_t>(a.c.n_kv) * HD;
+    float q0[NG], q1[NG], r[NG];
+#pragma unroll
+    for (int j = 0; j < NG; ++j) q0[j] = q[32 * j];
+    if (two)
+#pragma unroll
+      for (int j = 0; j < NG; ++j) q1[j] = q[next + 32 * j];
+    rotate(q0, r);
+#pragma unroll
+    for (int j = 0; j < NG; ++j) o[32 * j] = r[j];
+    if (two) {
+      rotate(q1, r);
+#pragma unroll
+      for (int j = 0; j < NG; ++j) o[next + 32 * j] = r[j];
+    }
+  }
+  rotate(x, y);
   if (!blk) return;
 
-  const int b = (pos % a.c.page_size) % kQ4Block;
+  const int b = pos % kQ4Block;
   uint32_t kcode[NG], vcode[NG], ksc[NG], vsc[NG], again = 0;
   float M[NG / 2];
 #pragma unroll
@@ -241,15 +261,17 @@ template <int HD>
 __global__ void __launch_bounds__(256) k_kv_read_q4(ReadArgs a) {
   constexpr int NG = HD / 32;
   const int lane = threadIdx.x & 31;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t token = task / a.c.n_kv;
-  if (token >= a.n_tokens) return;
+  const unsigned task = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const unsigned token = task / static_cast<unsigned>(a.c.n_kv);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (token >= static_cast<unsigned>(a.n_tokens)) return;
   const int h = static_cast<int>(task - token * a.c.n_kv);
   const int pos = a.positions[token];
   const int seq = a.seqs ? a.seqs[token] : static_cast<int>(token);
   const uint8_t* blk = q4_block_of(a.c, seq, pos, h, HD);
   const float nan = __int_as_float(0x7FC00000);
-  const int b = pos >= 0 ? (pos % a.c.page_size) % kQ4Block : 0;
+  const int b = pos & (kQ4Block - 1);
 #pragma unroll
   for (int j = 0; j < NG; ++j) {
     float kv = nan, vv = nan;
@@ -285,25 +307,17 @@ cudaError_t launch_kv_append_q4(const Q4Cache& c, int hd, const float* k, int64_
                                 float* q_out, int64_t qo_stride, cudaStream_t st) {
   AppendArgs a{c, k, v, q, q_out, k_stride, v_stride, q_stride, qo_stride, positions, seqs, rope, n_tokens, n_heads,
                max_pos};
-  const int64_t warps = static_cast<int64_t>(n_tokens) * (c.n_kv + n_heads);
-  const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
-  if (hd == 128)
-    k_kv_append_q4<128><<<blocks, 256, 0, st>>>(a);
-  else
-    k_kv_append_q4<64><<<blocks, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(n_tokens) * c.n_kv + 7) / 8);
+  return hd == 128 ? launch_pdl(k_kv_append_q4<128>, dim3(blocks), 256, 0, st, a)
+                   : launch_pdl(k_kv_append_q4<64>, dim3(blocks), 256, 0, st, a);
 }
 
 cudaError_t launch_kv_read_q4(const Q4Cache& c, int hd, const int32_t* positions, const int32_t* seqs, int n_tokens,
                               float* k_out, int64_t k_stride, float* v_out, int64_t v_stride, cudaStream_t st) {
   ReadArgs a{c, positions, seqs, k_out, v_out, k_stride, v_stride, n_tokens};
-  const int64_t warps = static_cast<int64_t>(n_tokens) * c.n_kv;
-  const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
-  if (hd == 128)
-    k_kv_read_q4<128><<<blocks, 256, 0, st>>>(a);
-  else
-    k_kv_read_q4<64><<<blocks, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(n_tokens) * c.n_kv + 7) / 8);
+  return hd == 128 ? launch_pdl(k_kv_read_q4<128>, dim3(blocks), 256, 0, st, a)
+                   : launch_pdl(k_kv_read_q4<64>, dim3(blocks), 256, 0, st, a);
 }
 
 }  // namespace tqd

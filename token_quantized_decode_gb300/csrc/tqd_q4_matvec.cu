@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   fence_mbar_init();
   __syncwarp();
 
+  pdl_wait();
+  pdl_launch_dependents();
   // this warp's strips of a slab
   auto share = [&](int slab, int& b, int& e) {
     const int s0 = slab * a.slab, n = min(a.slab, a.strips - s0);
@@ -117,30 +119,37 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
     e = s0 + n * (wk + 1) / a.wk;
   };
   // the ring's next copy: slab by slab, tile by tile, strip by strip
-  int pslab = 0, ptile = tile0, pstrip, pend, issued = 0;
-  share(0, pstrip, pend);
+  const uint8_t* src = nullptr;
+  int left = 0, ptile = tile1 - 1, pslab = -1, pst = 0;
   auto issue = [&] {
-    while (pstrip >= pend) {  // a share without strips (fewer strips than warps), or one that is done
-      if (++ptile >= tile1) {
-        ptile = tile0;
-        if (++pslab >= slabs) break;
-      }
-      share(pslab, pstrip, pend);
-      if (pstrip >= pend) ptile = tile1 - 1;
+    if (left == 0) {  // the next tile, or the next slab, with strips for this warp
+      int b = 0, e = 0;
+      do {
+        if (++ptile >= tile1) {
+          ptile = tile0;
+          if (++pslab >= slabs) {
+            pslab = slabs;
+            return;
+          }
+        }
+        share(pslab, b, e);
+        if (b == e) ptile = tile1 - 1;  // (fewer strips than warps)
+      } while (b == e);
+      left = e - b;
+      src = a.w + (static_cast<size_t>(ptile) * a.strips + b) * kStage;
     }
-    if (pslab >= slabs || tile0 >= tile1) return;
-    const int st = issued % kMvStages;
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bar[st], kStage);
-      bulk_g2s(my_ring + st * kStage, a.w + (static_cast<size_t>(ptile) * a.strips + pstrip) * kStage, kStage, &bar[st]);
+      mbar_arrive_expect_tx(&bar[pst], kStage);
+      bulk_g2s(my_ring + pst * kStage, src, kStage, &bar[pst]);
     }
-    ++pstrip;
-    ++issued;
+    pst = pst + 1 == kMvStages ? 0 : pst + 1;
+    src += kStage;
+    --left;
   };
   if (tile0 < tile1)
     for (int i = 0; i < kMvStages - 1; ++i) issue();
 
-  int taken = 0;
+  int st = 0, phase = 0;
   bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
   for (int slab = 0; slab < slabs; ++slab) {
     // ---- the slab's part of the vectors
@@ -214,10 +223,12 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
       if (tile < tile1) {
         for (int strip = b; strip < e; ++strip) {
           issue();
-          const int st = taken % kMvStages;
-          if (!dead) dead = !mbar_wait_bounded(&bar[st], (taken / kMvStages) & 1, nullptr);
-          ++taken;
+          if (!dead) dead = !mbar_wait_bounded(&bar[st], phase, nullptr);
           const unsigned char* tl = my_ring + st * kStage;
+          if (++st == kMvStages) {
+            st = 0;
+            phase ^= 1;
+          }
           const uint4 w0 = *reinterpret_cast<const uint4*>(tl + lane * 16);
           const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + lane * 16);
           const uint2 s0 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + r8 * 8);
@@ -230,8 +241,8 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
             const uint32_t a0[4] = {p & 0x000F000Fu, q & 0x000F000Fu, p & 0x00F000F0u, q & 0x00F000F0u};
             const uint32_t a1[4] = {p8 & 0x000F000Fu, q8 & 0x000F000Fu, p8 & 0x00F000F0u, q8 & 0x00F000F0u};
             const uint32_t sw0 = g < 2 ? s0.x : s0.y, sw1 = g < 2 ? s1.x : s1.y;
-            const float d0 = __half2float(__ushort_as_half(static_cast<unsigned short>(g & 1 ? sw0 >> 16 : sw0 & 0xFFFFu)));
-            const float d1 = __half2float(__ushort_as_half(static_cast<unsigned short>(g & 1 ? sw1 >> 16 : sw1 & 0xFFFFu)));
+            const __half2 h0 = *reinterpret_cast<const __half2*>(&sw0), h1 = *reinterpret_cast<const __half2*>(&sw1);
+            const float d0 = g & 1 ? __high2float(h0) : __low2float(h0), d1 = g & 1 ? __high2float(h1) : __low2float(h1);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               const int col = ONE ? r8 & 1 : t * 8 + r8;  // (one vector: the other columns repeat its two)
@@ -304,8 +315,7 @@ cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   static unsigned long long done = 0;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_q4_matvec<NT, ONE>), kMvSmem, &done);
   if (e != cudaSuccess) return e;
-  k_q4_matvec<NT, ONE><<<dim3(blocks, (a.n + 15) / 16), kMvThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(k_q4_matvec<NT, ONE>, dim3(blocks, (a.n + 15) / 16), kMvThreads, smem, st, a);
 }
 
 }  // namespace
