@@ -46,7 +46,7 @@ namespace {
 constexpr int kCtas = 304;      // two per SM
 constexpr int kUnit = 32;       // positions of a unit: two blocks
 constexpr int kSegment = 8;     // units that beginning and ending a segment is counted as
-constexpr int kCombine = 512;   // threads of the joining kernel
+constexpr int kCombine = 256;   // threads of the joining kernel
 constexpr float kNaN = __builtin_nanf("");
 
 // One instantiation: head size, column tiles, groups side by side.
@@ -656,64 +656,79 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
 }
 
 // Joins the partials of the rows that a CTA's run of units begins and does not
-// end: block i looks at the last segment of run i.
+// end: blocks R i .. R i + R - 1 look at the last segment of run i, a row each.
 template <int HD, int NT, int GV>
 __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   using C = Cfg<HD, NT, GV>;
   constexpr int NS = C::NS, R = C::R;
   extern __shared__ __align__(128) unsigned char sm[];
-  const Plan plan = make_plan(a, R, C::W, gridDim.x, sm);
+  const int run = blockIdx.x / R, hr = blockIdx.x % R;
+  const Plan plan = make_plan(a, R, C::W, kCtas, sm);
+  const unsigned long long u0 = run * plan.per, u1 = u0 + plan.per;
+  bool mine = u1 < plan.total;  // something behind this run
+  int s = 0, nb = 1;
+  unsigned long long seg = 0, seg0 = 0, seg1 = 0;
+  if (mine) {
+    s = plan.seq_of(u1 - 1);
+    nb = plan.units(s);
+    seg = udiv(u1 - 1 - plan.pre[s], nb);
+    seg0 = plan.pre[s] + seg * nb;
+    seg1 = seg0 + nb;
+    mine = seg0 >= u0 && seg1 > u1;  // else begun by an earlier run, or ended by this one
+  }
   pdl_wait();
   pdl_launch_dependents();
-  const unsigned long long u0 = blockIdx.x * plan.per, u1 = u0 + plan.per;
-  if (u1 >= plan.total) return;  // nothing behind this run
-  const int s = plan.seq_of(u1 - 1);
-  const int nb = plan.units(s);
-  const unsigned long long seg = udiv(u1 - 1 - plan.pre[s], nb);
-  const unsigned long long seg0 = plan.pre[s] + seg * nb, seg1 = seg0 + nb;
-  if (seg0 < u0 || seg1 <= u1) return;  // begun by an earlier run, or ended by this one
-  const int runs = static_cast<int>((seg1 - 1) / plan.per) - static_cast<int>(blockIdx.x) + 1;
+  if (!mine) return;
   int kvh;
   const int rt = plan.tile_of(s, seg, &kvh);
-  const int n_rows = min(R, plan.nq[s] * plan.G - rt * R);
+  const int row = rt * R + hr;
+  if (row >= plan.nq[s] * plan.G) return;
+  const int runs = static_cast<int>((seg1 - 1) / plan.per) - run + 1;
   const float* first = static_cast<const float*>(a.scratch) +
-                       (static_cast<size_t>(blockIdx.x) * 2 + (seg0 == u0 ? 0 : 1)) * partial_floats(HD);
-  const float* rest = static_cast<const float*>(a.scratch) + static_cast<size_t>(blockIdx.x) * 2 * partial_floats(HD);
+                       (static_cast<size_t>(run) * 2 + (seg0 == u0 ? 0 : 1)) * partial_floats(HD);
+  const float* rest = static_cast<const float*>(a.scratch) + static_cast<size_t>(run) * 2 * partial_floats(HD);
   auto part = [&](int k) { return k ? rest + static_cast<size_t>(k) * 2 * partial_floats(HD) : first; };
-  __shared__ float wt[kCtas * 8], lsum[8];  // each partial's weight; a pair's sum p
+  __shared__ float wt[kCtas * GV], lsum[GV];  // each partial's weight; the row's sum p, for each group pair
   __shared__ float4 red[kCombine];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < C::P) {  // a warp per column pair
+  if (warp < GV) {  // a warp per column pair
+    const int pr = hr * GV + warp;
     float ref = -INFINITY, ls = 0.f;
-    for (int k = lane; k < runs; k += 32) ref = fmaxf(ref, part(k)[8 * HD + warp]);
+    for (int k = lane; k < runs; k += 32) ref = fmaxf(ref, part(k)[8 * HD + pr]);
     ref = warp_max(ref);
     for (int k = lane; k < runs; k += 32) {
-      const float pr = part(k)[8 * HD + warp];
-      const float w = pr > -INFINITY ? ex2(pr - ref) : 0.f;
-      wt[k * 8 + warp] = w;
-      if (pr > -INFINITY) ls += w * part(k)[8 * HD + 8 + warp];
+      const float pf = part(k)[8 * HD + pr];
+      const float w = pf > -INFINITY ? ex2(pf - ref) : 0.f;
+      wt[k * GV + warp] = w;
+      if (pf > -INFINITY) ls += w * part(k)[8 * HD + 8 + pr];
     }
     ls = warp_sum(ls);
     if (lane == 0) lsum[warp] = ls;
   }
+  // four elements a thread, the partials dealt over the threads left; loaded before their weights are known
+  constexpr int kQuads = HD / 4, kDeal = kCombine / kQuads, kAhead = 8;
+  const int i = threadIdx.x % kQuads * 4, deal = threadIdx.x / kQuads, pair = i / 32 / NS;
+  float4 ahead[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (deal + j * kDeal < runs) ahead[j] = *reinterpret_cast<const float4*>(part(deal + j * kDeal) + hr * HD + i);
   __syncthreads();
-  // four elements a thread, the partials dealt over the threads left
-  constexpr int kQuads = R * HD / 4, kDeal = kCombine / kQuads;
-  const int i = threadIdx.x % kQuads * 4, deal = threadIdx.x / kQuads;
-  const int hr = i / HD, d = i % HD, r = hr * GV + d / 32 / NS;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = deal; k < runs; k += kDeal) {
-    const float w = wt[k * 8 + r];
-    const float4 v = *reinterpret_cast<const float4*>(part(k) + i);
+  auto add = [&](int k, const float4& v) {
+    const float w = wt[k * GV + pair];
     acc.x += w * v.x;
     acc.y += w * v.y;
     acc.z += w * v.z;
     acc.w += w * v.w;
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (deal + j * kDeal < runs) add(deal + j * kDeal, ahead[j]);
+  for (int k = deal + kAhead * kDeal; k < runs; k += kDeal)
+    add(k, *reinterpret_cast<const float4*>(part(k) + hr * HD + i));
   red[threadIdx.x] = acc;
   __syncthreads();
-  if (deal == 0 && hr < n_rows) {
+  if (deal == 0) {
 #pragma unroll
     for (int k = 1; k < kDeal; ++k) {
       const float4 v = red[k * kQuads + threadIdx.x];
@@ -722,9 +737,9 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
       acc.z += v.z;
       acc.w += v.w;
     }
-    const int rr = rt * R + hr;
-    const float ls = lsum[r];
-    float* out = a.out + (q_first(a, s) + rr / plan.G) * a.out_stride + static_cast<int64_t>(kvh * plan.G + rr % plan.G) * HD + d;
+    const float ls = lsum[pair];
+    float* out = a.out + (q_first(a, s) + row / plan.G) * a.out_stride +
+                 static_cast<int64_t>(kvh * plan.G + row % plan.G) * HD + i;
     out[0] = ls == 0.f ? 0.f : acc.x / ls;
     out[1] = ls == 0.f ? 0.f : acc.y / ls;
     out[2] = ls == 0.f ? 0.f : acc.z / ls;
@@ -742,7 +757,7 @@ cudaError_t launch(const Q4AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_attention_q4<HD, NT, GV>, dim3(kCtas), C::T, smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_attention_q4_join<HD, NT, GV>, dim3(kCtas), kCombine, plan_b, st, a);
+  return launch_pdl(k_attention_q4_join<HD, NT, GV>, dim3(kCtas * C::R), kCombine, plan_b, st, a);
 }
 
 }  // namespace

@@ -42,12 +42,13 @@ __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t r
 
 constexpr int kMvWarps = 8;
 constexpr int kMvThreads = 32 * kMvWarps;
-// Stages (strips) of a warp's ring.
-__host__ __device__ constexpr int mv_stages(int nt) { return nt == 4 ? 3 : 4; }
+// Strips of a stage, and stages of a warp's ring.
+__host__ __device__ constexpr int mv_chunk(int nt) { return nt == 4 ? 1 : 2; }
+__host__ __device__ constexpr int mv_stages(int nt) { return nt == 4 ? 3 : 2; }
 // Shared memory of a CTA: at most what lets two of them share an SM; the rings
 // and the warps' sums, then the staged vectors.
 constexpr int kMvSmem = 113 * 1024;
-constexpr int mv_fixed_smem(int nt) { return kMvWarps * (mv_stages(nt) * (kQ4TileBytes + 8) + 2 * nt * 128); }
+constexpr int mv_fixed_smem(int nt) { return kMvWarps * (mv_stages(nt) * (mv_chunk(nt) * kQ4TileBytes + 8) + 2 * nt * 128); }
 constexpr int mv_strip_smem(int cols) { return 4 * (cols * 64 + cols / 2 * 20); }
 
 struct MatvecQ4Args {
@@ -84,7 +85,7 @@ struct MatvecQ4Args {
 template <int NT, bool ONE>
 __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   constexpr int NC = ONE ? 2 : 8 * NT;  // staged columns: high and low part of each vector
-  constexpr int kMvStages = mv_stages(NT), kStage = kQ4TileBytes;
+  constexpr int kMvStages = mv_stages(NT), kChunk = mv_chunk(NT), kStage = kChunk * kQ4TileBytes;
   extern __shared__ __align__(128) unsigned char sm[];
   unsigned char* ring = sm;
   float* red = reinterpret_cast<float*>(ring + kMvWarps * kMvStages * kStage);  // [warps][2 NT][32]
@@ -136,15 +137,16 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
         if (b == e) ptile = tile1 - 1;  // (fewer strips than warps)
       } while (b == e);
       left = e - b;
-      src = a.w + (static_cast<size_t>(ptile) * a.strips + b) * kStage;
+      src = a.w + (static_cast<size_t>(ptile) * a.strips + b) * kQ4TileBytes;
     }
+    const int n = min(left, kChunk);
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bar[pst], kStage);
-      bulk_g2s(my_ring + pst * kStage, src, kStage, &bar[pst]);
+      mbar_arrive_expect_tx(&bar[pst], n * kQ4TileBytes);
+      bulk_g2s(my_ring + pst * kStage, src, n * kQ4TileBytes, &bar[pst]);
     }
     pst = pst + 1 == kMvStages ? 0 : pst + 1;
     src += kStage;
-    --left;
+    left -= n;
   };
   if (tile0 < tile1)
     for (int i = 0; i < kMvStages - 1; ++i) issue();
@@ -221,39 +223,44 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = 0.f;
       if (tile < tile1) {
-        for (int strip = b; strip < e; ++strip) {
+        for (int strip0 = b; strip0 < e; strip0 += kChunk) {
           issue();
           if (!dead) dead = !mbar_wait_bounded(&bar[st], phase, nullptr);
-          const unsigned char* tl = my_ring + st * kStage;
+          const unsigned char* stage = my_ring + st * kStage;
           if (++st == kMvStages) {
             st = 0;
             phase ^= 1;
           }
-          const uint4 w0 = *reinterpret_cast<const uint4*>(tl + lane * 16);
-          const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + lane * 16);
-          const uint2 s0 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + r8 * 8);
-          const uint2 s1 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + 64 + r8 * 8);
-          const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w}, wb[4] = {w1.x, w1.y, w1.z, w1.w};
-          const int gl = strip * 4 - g0;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t p = wa[g], q = wb[g], p8 = p >> 8, q8 = q >> 8;
-            const uint32_t a0[4] = {p & 0x000F000Fu, q & 0x000F000Fu, p & 0x00F000F0u, q & 0x00F000F0u};
-            const uint32_t a1[4] = {p8 & 0x000F000Fu, q8 & 0x000F000Fu, p8 & 0x00F000F0u, q8 & 0x00F000F0u};
-            const uint32_t sw0 = g < 2 ? s0.x : s0.y, sw1 = g < 2 ? s1.x : s1.y;
-            const __half2 h0 = *reinterpret_cast<const __half2*>(&sw0), h1 = *reinterpret_cast<const __half2*>(&sw1);
-            const float d0 = g & 1 ? __high2float(h0) : __low2float(h0), d1 = g & 1 ? __high2float(h1) : __low2float(h1);
+          for (int u = 0; u < kChunk; ++u) {
+            if (u && strip0 + u >= e) break;
+            const unsigned char* tl = stage + u * kQ4TileBytes;
+            const uint4 w0 = *reinterpret_cast<const uint4*>(tl + lane * 16);
+            const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + lane * 16);
+            const uint2 s0 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + r8 * 8);
+            const uint2 s1 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + 64 + r8 * 8);
+            const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w}, wb[4] = {w1.x, w1.y, w1.z, w1.w};
+            const int gl = (strip0 + u) * 4 - g0;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const int col = ONE ? r8 & 1 : t * 8 + r8;  // (one vector: the other columns repeat its two)
-              const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl + g) * NC + col) * 4 + c) * 16);
-              const float4 z = zs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
-              const float f = fs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
-              float d[4];
-              mma_f16(d, a0, xv.x, xv.y, z.x, z.y, z.z, z.w);
-              mma_f16(d, a1, xv.z, xv.w);
-              acc[t][0] += d0 * (f * (d[0] + d[1]));
-              acc[t][1] += d1 * (f * (d[2] + d[3]));
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t p = wa[g], q = wb[g], p8 = p >> 8, q8 = q >> 8;
+              const uint32_t a0[4] = {p & 0x000F000Fu, q & 0x000F000Fu, p & 0x00F000F0u, q & 0x00F000F0u};
+              const uint32_t a1[4] = {p8 & 0x000F000Fu, q8 & 0x000F000Fu, p8 & 0x00F000F0u, q8 & 0x00F000F0u};
+              const uint32_t sw0 = g < 2 ? s0.x : s0.y, sw1 = g < 2 ? s1.x : s1.y;
+              const __half2 h0 = *reinterpret_cast<const __half2*>(&sw0), h1 = *reinterpret_cast<const __half2*>(&sw1);
+              const float d0 = g & 1 ? __high2float(h0) : __low2float(h0), d1 = g & 1 ? __high2float(h1) : __low2float(h1);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                const int col = ONE ? r8 & 1 : t * 8 + r8;  // (one vector: the other columns repeat its two)
+                const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl + g) * NC + col) * 4 + c) * 16);
+                const float4 z = zs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
+                const float f = fs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
+                float d[4];
+                mma_f16(d, a0, xv.x, xv.y, z.x, z.y, z.z, z.w);
+                mma_f16(d, a1, xv.z, xv.w);
+                acc[t][0] += d0 * (f * (d[0] + d[1]));
+                acc[t][1] += d1 * (f * (d[2] + d[3]));
+              }
             }
           }
           __syncwarp();  // every lane has read the stage before it is filled again
