@@ -27,12 +27,14 @@
 // instead of GV times.  GV is 4 for one row, 2 for two; for more than four rows
 // (NT = 2) two column tiles share the unpacked cache.
 //
-// Split.  The unit is 32 positions of one (sequence, kv head, tile of query
-// rows); units are laid end to end and each CTA (two an SM) takes an
-// equal run of them, its warps every W-th unit with a running softmax each,
-// whatever the lengths.  Rows that one CTA finishes are written out; where a run begins or ends inside a row's units the CTA leaves a partial
-// (ref, sum p, sum p v) and a second kernel, already launched (programmatic
-// dependent launch), joins them.  The order of every sum is fixed by the sizes.
+// Split.  The unit is 32 positions of one segment: (sequence, kv head, tile of
+// query rows).  Units are laid end to end and each warp takes an equal run of
+// them, whatever the lengths, with a running softmax for each segment it meets.
+// A segment inside a warp's run is written out by the warp alone; the partial
+// results (ref, sum p, sum p v) of one that several warps of a CTA share are
+// joined in shared memory at the CTA's end, and those of one that several CTAs
+// share by a second kernel, already launched (programmatic dependent launch).  The
+// order of every sum is fixed by the sizes.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -45,7 +47,6 @@ namespace {
 
 constexpr int kCtas = 304;      // two per SM
 constexpr int kUnit = 32;       // positions of a unit: two blocks
-constexpr int kSegment = 8;     // units that beginning and ending a segment is counted as
 constexpr int kCombine = 256;   // threads of the joining kernel
 constexpr float kNaN = __builtin_nanf("");
 
@@ -56,13 +57,16 @@ struct Cfg {
   static constexpr int NS = NG / GV;      // chains: column pair gv holds groups gv * NS + 0 .. NS - 1
   static constexpr int P = 4 * NT;        // column pairs
   static constexpr int R = P / GV;        // query rows of a tile
+  static constexpr int B = R == 1 ? 1 : 2;  // blocks that join a run
   static constexpr int W = NT == 1 ? 8 : 6;  // warps: what the registers leave room for twice an SM
   static constexpr int T = 32 * W;
   static constexpr int BB = q4_block_bytes(HD);
   static constexpr int JB = NT == 1 ? 2 : 1;  // blocks of a unit taken at once: two where the registers hold them
   static constexpr int ST = HD == 64 ? 4 : NT == 1 ? 2 : 3;  // stages (units) of a warp's ring
   static constexpr int LD = HD + 8;       // floats of a row in the merge buffer
-  static constexpr size_t smem = static_cast<size_t>(W) * ST * (2 * BB + 16) + static_cast<size_t>(W) * (R * LD + 2 * P) * 4;
+  static constexpr int PART = R * LD + 2 * P;  // floats of a warp's partial result
+  static constexpr size_t smem = static_cast<size_t>(W) * ST * (2 * BB + 16) + static_cast<size_t>(W) * PART * 4;
+  static_assert(PART * 4 <= ST * 2 * BB, "a partial result fits a warp's ring");
   static_assert(NT == 1 || GV == 1, "groups side by side only where columns are free");
 };
 
@@ -125,15 +129,15 @@ struct Plan {
   const unsigned long long* pre;  // [n_seq + 1] units before each sequence (shared memory)
   const int* len;                 // [n_seq] cached positions, >= 0
   const int* nq;                  // [n_seq] queries
-  unsigned long long total, per;  // units, and units of one CTA
-  int n_seq, n_kv, G, R;
+  unsigned long long total, per;  // units, and units of one warp
+  int n_seq, n_kv, G, rbits;      // 2^rbits rows of a tile
+  int most;                       // positions of the page table, and a unit
 
-  // Units of a segment: those of its positions, and kSegment more that stand for the cost
-  // of beginning and ending it.
-  __device__ int units(int s) const {
-    return len[s] > 0 ? (len[s] + kUnit - 1) / kUnit + kSegment : 0;
-  }
-  __device__ int tiles(int s) const { return static_cast<int>((static_cast<long long>(nq[s]) * G + R - 1) / R); }
+  // Units of a segment: its positions', and where they pass the page table one
+  // behind the table's end (which makes the rows that see it NaN).
+  __device__ int units(int s) const { return (min(len[s], most) + kUnit - 1) / kUnit; }
+  // (rows are at most tokens * heads, 2^30)
+  __device__ int tiles(int s) const { return (nq[s] * G + (1 << rbits) - 1) >> rbits; }
   // Sequence of unit u < total.
   __device__ int seq_of(unsigned long long u) const {
     int lo = 0, hi = n_seq - 1;
@@ -152,9 +156,11 @@ struct Plan {
     *kvh = static_cast<int>(k);
     return i & 1 ? rt - 1 - (i >> 1) : i >> 1;
   }
+  // Query of row `row` (a division only where there are several).
+  __device__ int query(int row) const { return row < G ? 0 : row / G; }
   // Positions that query row `row` of sequence s sees (0 for a row past the last).
   __device__ int seen(int s, int row) const {
-    const int q = row / G;
+    const int q = query(row);
     if (q >= nq[s]) return 0;
     const int v = len[s] - nq[s] + q + 1;
     return v > 0 ? v : 0;
@@ -179,56 +185,82 @@ __device__ Plan make_plan(const Q4AttnArgs& a, int R, int W, int ctas, unsigned 
   p.n_seq = n;
   p.n_kv = a.c.n_kv;
   p.G = a.n_heads / a.c.n_kv;
-  p.R = R;
-  const int each = (n + nt - 1) / nt, s0 = t * each;
-  unsigned long long mine = 0;
-  for (int s = s0; s < s0 + each && s < n; ++s) {
-    len[s] = max(__ldcg(a.lens + s), 0);
+  p.most = static_cast<int>(min(static_cast<long long>(a.c.table_stride) * a.c.page_size, 1ll << 30)) + kUnit;
+  p.rbits = R == 8 ? 3 : R == 4 ? 2 : R == 2 ? 1 : 0;
+  auto sizes = [&](int s) {  // fills in a sequence's entries, returns its units
+    len[s] = min(max(__ldcg(a.lens + s), 0), 1 << 30);
     int q = 1;
     if (a.q_start) {  // clipped to the query rows there are
       const int b = __ldcg(a.q_start + s), e = __ldcg(a.q_start + s + 1);
       q = b >= 0 && b <= a.n_tokens && e > b ? min(e, a.n_tokens) - b : 0;
     }
     nq[s] = q;
-    pre[s] = mine;
-    mine += static_cast<unsigned long long>(p.n_kv) * p.tiles(s) * p.units(s);
-  }
-  unsigned long long run = mine;
+    return static_cast<unsigned long long>(p.n_kv) * p.tiles(s) * p.units(s);
+  };
+  auto scan = [&](unsigned long long v) {  // inclusive, over a warp
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long v = __shfl_up_sync(0xFFFFFFFFu, run, o);
-    if ((t & 31) >= o) run += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if ((t & 31) >= o) v += u;
+    }
+    return v;
+  };
+  if (n <= 32) {  // one warp does it
+    if (t < 32) {
+      const unsigned long long mine = t < n ? sizes(t) : 0, run = scan(mine);
+      if (t < n) pre[t] = run - mine;
+      if (t == 31) pre[n] = run;
+    }
+    __syncthreads();
+  } else {
+    const int each = (n + nt - 1) / nt, s0 = t * each;
+    unsigned long long mine = 0;
+    for (int s = s0; s < s0 + each && s < n; ++s) {
+      pre[s] = mine;
+      mine += sizes(s);
+    }
+    const unsigned long long run = scan(mine);
+    if ((t & 31) == 31) wsum[t >> 5] = run;
+    __syncthreads();
+    unsigned long long before = run - mine, total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+      if (w < (t >> 5)) before += wsum[w];
+      total += wsum[w];
+    }
+    for (int s = s0; s < s0 + each && s < n; ++s) pre[s] += before;
+    if (t == 0) pre[n] = total;
+    __syncthreads();
   }
-  if ((t & 31) == 31) wsum[t >> 5] = run;
-  __syncthreads();
-  unsigned long long before = run - mine, total = 0;
-  for (int w = 0; w < nt / 32; ++w) {
-    if (w < (t >> 5)) before += wsum[w];
-    total += wsum[w];
-  }
-  for (int s = s0; s < s0 + each && s < n; ++s) pre[s] += before;
-  if (t == 0) pre[n] = total;
-  __syncthreads();
-  p.total = total;
-  const unsigned long long per = (total + ctas - 1) / ctas;
-  p.per = max((per + W - 1) / W * W, static_cast<unsigned long long>(W));
+  p.total = pre[n];
+  const unsigned warps = static_cast<unsigned>(ctas * W);
+  p.per = max(udiv(p.total + warps - 1, warps), 1ull);
   return p;
 }
 
 size_t plan_bytes(int n_seq) { return (static_cast<size_t>(n_seq) * 16 + 8 + 15) / 16 * 16; }
 
+// A segment whose parts the warps of a CTA join at its end.
+struct Shared {
+  unsigned long long seg0, seg1;
+  int64_t token;            // first query token of its sequence
+  int n_rows, row0, head0;  // rows of the tile, its first row, first query head of the kv head
+};
+
 template <int HD, int NT, int GV>
 __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnArgs a) {
   using C = Cfg<HD, NT, GV>;
-  constexpr int NG = C::NG, NS = C::NS, P = C::P, R = C::R, W = C::W, ST = C::ST, BB = C::BB, LD = C::LD, JB = C::JB;
+  constexpr int NG = C::NG, NS = C::NS, P = C::P, R = C::R, W = C::W, ST = C::ST, BB = C::BB, LD = C::LD, JB = C::JB, PART = C::PART;
   extern __shared__ __align__(128) unsigned char sm[];
   unsigned char* ring = sm;
-  float* merge = reinterpret_cast<float*>(ring + W * ST * 2 * BB);  // [W][R][LD], then [W][P] ref, sum p
-  float* mref = merge + W * R * LD;
-  float* ml = mref + W * P;
-  auto* bars = reinterpret_cast<uint64_t*>(ml + W * P);  // [W][ST]
+  // A warp's partial result of the segment that it shares with the warp before
+  // it; that of one shared with the warp behind it goes to its ring, done with by then.
+  float* parts = reinterpret_cast<float*>(ring + W * ST * 2 * BB);  // [W][PART]: [R][LD], [P] ref, [P] sum p
+  auto* bars = reinterpret_cast<uint64_t*>(parts + W * PART);      // [W][ST]
   int* flags = reinterpret_cast<int*>(bars + W * ST);    // [W][ST] 1, 2: no page for the first, second block; 4: not seen
   unsigned char* plan_mem = reinterpret_cast<unsigned char*>(flags + W * ST * 2);
+
+  __shared__ int ends[W];
+  __shared__ Shared shared[W + 1];  // the last segment of each warp's run, and the CTA's first one
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c = lane & 3;  // operand row (and r + 8), and column pair of the sums
@@ -249,11 +281,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       for (int i = threadIdx.x; i < a.n_heads * HD; i += C::T) a.out[(first + q) * a.out_stride + i] = 0.f;
   }
 
-  const unsigned long long u0 = blockIdx.x * plan.per;
-  if (u0 >= plan.total) return;
-  const unsigned long long u1 = min(u0 + plan.per, plan.total);
-  const int n_units = static_cast<int>(u1 - u0);
-  const int n_it = n_units > warp ? (n_units - warp + W - 1) / W : 0;
+  const unsigned long long c0 = blockIdx.x * plan.per * W;  // the CTA's run
+  if (c0 >= plan.total) return;
+  const unsigned long long c1 = min(c0 + plan.per * W, plan.total);
+  const unsigned long long u0 = min(c0 + warp * plan.per, c1), u1 = min(u0 + plan.per, c1);  // the warp's
+  const int n_it = static_cast<int>(u1 - u0);
   unsigned char* my_ring = ring + warp * ST * 2 * BB;
   const int ppb = a.c.page_size / kQ4Block;  // blocks per page
 
@@ -263,7 +295,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   int src_flag = 0;
   auto locate = [&](int i) {
     if (i >= n_it) return;
-    const unsigned long long u = u0 + warp + static_cast<unsigned long long>(i) * W;
+    const unsigned long long u = u0 + i;
     const int s = plan.seq_of(u);
     const unsigned long long uq = u - plan.pre[s];
     const int nb = plan.units(s);
@@ -309,10 +341,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   for (int i = 0; i < ST - 1; ++i) issue();
 
   const Unpack unpack;
-  int rel = warp, st = 0, phase = 0;  // the warp's next unit, counted from u0, and its stage
+  int rel = 0, st = 0, phase = 0;  // the warp's next unit, counted from u0, and its stage
   bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
-  int s = plan.seq_of(u0);
+  int goes_on = 0;
+  bool begun = false;
   unsigned long long u = u0;
+  int s = u < u1 ? plan.seq_of(u) : 0;
   while (u < u1) {
     // ---- the segment of unit u: one (sequence, kv head, tile of rows)
     while (plan.pre[s + 1] <= u) ++s;
@@ -337,8 +371,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       for (int t = 0; t < NT; ++t) {
         const int row = rt * R + min(t * 4 + pair / GV, n_rows - 1);  // rows past the last repeat it
         seen[t] = plan.seen(s, rt * R + min(t * 4 + h, n_rows - 1));
-        const float* q = a.q + (q_first(a, s) + row / plan.G) * a.q_stride +
-                         static_cast<int64_t>(kvh * plan.G + row % plan.G) * HD;
+        const float* q = a.q + (q_first(a, s) + plan.query(row)) * a.q_stride +
+                         static_cast<int64_t>(kvh * plan.G + (row - plan.query(row) * plan.G)) * HD;
         // A power of two for each group of 32 brings its largest element to 2^10
         // .. 2^11; the high part is then the nearest whole number, so that a
         // group's sum of high parts times codes is exact in the tensor cores' f32,
@@ -569,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
         }
       }
     };
-    for (; rel < rel_end; rel += W) {
+    for (; rel < rel_end; ++rel) {
       issue();
       __syncwarp();
       if (!dead) dead = !mbar_wait_bounded(&bar[st], phase, nullptr);
@@ -597,74 +631,123 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       __syncwarp();  // every lane has read the stage before it is filled again
     }
 
-    // ---- the warps' sums into one
+    // ---- the end of the segment, or of the run
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], x);
-      float* mo = merge + (warp * R + t * 4 + h) * LD;
+    if (u0 <= seg0 && seg1 <= u1) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-        if (g / NS == gv) {
+      for (int t = 0; t < NT; ++t) {
+        if (t * 4 + h >= n_rows) continue;
+        const int row = rt * R + t * 4 + h;
+        float* out = a.out + (q_first(a, s) + plan.query(row)) * a.out_stride +
+                     static_cast<int64_t>(kvh * plan.G + (row - plan.query(row) * plan.G)) * HD + r;
+        const float inv = l[t] == 0.f ? 0.f : 1.f / l[t];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float (&d)[4] = o[t][2 * g + i];
-            mo[32 * g + 16 * i + r] = d[0] + d[1];
-            mo[32 * g + 16 * i + r + 8] = d[2] + d[3];
+        for (int g = 0; g < NG; ++g)
+          if (g / NS == gv) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float (&d)[4] = o[t][2 * g + i];
+              out[32 * g + 16 * i] = inv == 0.f && l[t] == 0.f ? 0.f : (d[0] + d[1]) * inv;
+              out[32 * g + 16 * i + 8] = inv == 0.f && l[t] == 0.f ? 0.f : (d[2] + d[3]) * inv;
+            }
           }
+      }
+    } else {
+      if (lane == 0) {
+        const Shared sh{seg0, seg1, q_first(a, s), n_rows, rt * R, kvh * plan.G};
+        shared[warp] = sh;
+        if (u == c0) shared[W] = sh;
+      }
+      goes_on = u0 <= seg0;  // (else it is the run's first, begun before it)
+      begun |= u == c0 && seg0 < c0;
+      float* part = u0 <= seg0 ? reinterpret_cast<float*>(my_ring) : parts + warp * PART;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float* mo = part + (t * 4 + h) * LD + r;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          if (g / NS == gv) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float (&d)[4] = o[t][2 * g + i];
+              mo[32 * g + 16 * i] = d[0] + d[1];
+              mo[32 * g + 16 * i + 8] = d[2] + d[3];
+            }
+          }
+        if (r == 0) {
+          part[R * LD + t * 4 + c] = M[t] == -INFINITY && l[t] == 0.f ? -INFINITY : ref[t];
+          part[R * LD + P + t * 4 + c] = l[t];
         }
-      if (r == 0) {
-        mref[warp * P + t * 4 + c] = M[t] == -INFINITY && l[t] == 0.f ? -INFINITY : ref[t];
-        ml[warp * P + t * 4 + c] = l[t];
       }
     }
-    __syncthreads();
-    const bool whole = u0 <= seg0 && seg1 <= u1;
-    // slot 0: the units from the CTA's first on; slot 1: those up to its last
-    float* part = static_cast<float*>(a.scratch) +
-                  (static_cast<size_t>(blockIdx.x) * 2 + (u == u0 ? 0 : 1)) * partial_floats(HD);
+    u = uend;
+  }
+  // bit 0: the warp's run ends inside a segment that began in it; bit 1: the CTA's begins inside one
+  if (lane == 0) ends[warp] = goes_on | (warp == 0 && begun ? 2 : 0);
+  __syncthreads();
+  unsigned last_shared = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) last_shared |= (ends[w] & 1) << w;
+  const bool first_shared = ends[0] & 2;
+
+  // ---- segments that several warps share, or that another CTA shares: the one
+  // that began before the CTA's run, and those that begin in a warp's run and go on behind it
+  for (int w = -1; w < W; ++w) {
+    const int w_ = max(w, 0);
+    const unsigned long long w0 = c0 + w_ * plan.per, w1 = min(w0 + plan.per, c1);
+    if (w0 >= c1) break;
+    const Shared sh = shared[w < 0 ? W : w];
+    if (w < 0 ? !first_shared : !(last_shared >> w & 1)) continue;
+    const int last = static_cast<int>(udiv(min(sh.seg1, c1) - 1 - c0, static_cast<unsigned>(plan.per)));
+    const bool whole = c0 <= sh.seg0 && sh.seg1 <= c1;
+    const float* head = w >= 0 ? reinterpret_cast<const float*>(ring + w * ST * 2 * BB) : parts;
+    // slot 0: a segment of the CTA's first unit; slot 1: one that begins later
+    float* to = static_cast<float*>(a.scratch) +
+                (static_cast<size_t>(blockIdx.x) * 2 + (sh.seg0 <= c0 ? 0 : 1)) * partial_floats(HD);
     for (int i = threadIdx.x; i < R * HD; i += C::T) {
       const int hr = i / HD, d = i % HD, pr = hr * GV + d / 32 / NS;
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < W; ++w) top = fmaxf(top, mref[w * P + pr]);
+      float top = head[R * LD + pr];
+      for (int k = w_ + 1; k <= last; ++k) top = fmaxf(top, parts[k * PART + R * LD + pr]);
       float acc = 0.f, ls = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-        if (mref[w * P + pr] > -INFINITY) {
-          const float k = ex2(mref[w * P + pr] - top);
-          acc += k * merge[(w * R + hr) * LD + d];
-          ls += k * ml[w * P + pr];
+      for (int k = w_; k <= last; ++k) {
+        const float* part = k == w_ ? head : parts + k * PART;
+        const float pf = part[R * LD + pr];
+        if (pf > -INFINITY) {
+          const float f = ex2(pf - top);
+          acc += f * part[hr * LD + d];
+          ls += f * part[R * LD + P + pr];
         }
+      }
       if (whole) {
-        if (hr < n_rows) {
-          const int rr = rt * R + hr;
-          a.out[(q_first(a, s) + rr / plan.G) * a.out_stride + static_cast<int64_t>(kvh * plan.G + rr % plan.G) * HD + d] =
+        if (hr < sh.n_rows) {
+          const int row = sh.row0 + hr;
+          a.out[(sh.token + plan.query(row)) * a.out_stride + static_cast<int64_t>(sh.head0 + (row - plan.query(row) * plan.G)) * HD + d] =
               ls == 0.f ? 0.f : acc / ls;
         }
       } else {
-        part[i] = acc;
+        to[i] = acc;
         if (d % (32 * NS) == 0) {
-          part[8 * HD + pr] = top;
-          part[8 * HD + 8 + pr] = ls;
+          to[8 * HD + pr] = top;
+          to[8 * HD + 8 + pr] = ls;
         }
       }
     }
-    __syncthreads();
-    u = uend;
   }
 }
 
-// Joins the partials of the rows that a CTA's run of units begins and does not
-// end: blocks R i .. R i + R - 1 look at the last segment of run i, a row each.
+// Joins the partials of the segment that a CTA's run of units begins and does
+// not end: two blocks for each run (one where a tile has one row), half the rows each.
 template <int HD, int NT, int GV>
 __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   using C = Cfg<HD, NT, GV>;
-  constexpr int NS = C::NS, R = C::R;
+  constexpr int NS = C::NS, R = C::R, B = C::B, RB = R / B;
   extern __shared__ __align__(128) unsigned char sm[];
-  const int run = blockIdx.x / R, hr = blockIdx.x % R;
+  const int run = blockIdx.x / B, row0 = blockIdx.x % B * RB;
   const Plan plan = make_plan(a, R, C::W, kCtas, sm);
-  const unsigned long long u0 = run * plan.per, u1 = u0 + plan.per;
+  const unsigned long long per = plan.per * C::W, u0 = run * per, u1 = u0 + per;
   bool mine = u1 < plan.total;  // something behind this run
   int s = 0, nb = 1;
   unsigned long long seg = 0, seg0 = 0, seg1 = 0;
@@ -681,41 +764,43 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   if (!mine) return;
   int kvh;
   const int rt = plan.tile_of(s, seg, &kvh);
-  const int row = rt * R + hr;
-  if (row >= plan.nq[s] * plan.G) return;
-  const int runs = static_cast<int>((seg1 - 1) / plan.per) - run + 1;
+  const int n_rows = plan.nq[s] * plan.G - rt * R - row0;
+  if (n_rows <= 0) return;
+  const int runs = static_cast<int>((seg1 - 1) / per) - run + 1;
   const float* first = static_cast<const float*>(a.scratch) +
                        (static_cast<size_t>(run) * 2 + (seg0 == u0 ? 0 : 1)) * partial_floats(HD);
   const float* rest = static_cast<const float*>(a.scratch) + static_cast<size_t>(run) * 2 * partial_floats(HD);
   auto part = [&](int k) { return k ? rest + static_cast<size_t>(k) * 2 * partial_floats(HD) : first; };
-  __shared__ float wt[kCtas * GV], lsum[GV];  // each partial's weight; the row's sum p, for each group pair
+  constexpr int PB = RB * GV;
+  __shared__ float wt[kCtas * PB], lsum[PB];  // each partial's weight and the sum p, for the block's column pairs
   __shared__ float4 red[kCombine];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < GV) {  // a warp per column pair
-    const int pr = hr * GV + warp;
+  if (warp < PB) {  // a warp per column pair
+    const int pr = row0 * GV + warp;
     float ref = -INFINITY, ls = 0.f;
     for (int k = lane; k < runs; k += 32) ref = fmaxf(ref, part(k)[8 * HD + pr]);
     ref = warp_max(ref);
     for (int k = lane; k < runs; k += 32) {
       const float pf = part(k)[8 * HD + pr];
       const float w = pf > -INFINITY ? ex2(pf - ref) : 0.f;
-      wt[k * GV + warp] = w;
+      wt[k * PB + warp] = w;
       if (pf > -INFINITY) ls += w * part(k)[8 * HD + 8 + pr];
     }
     ls = warp_sum(ls);
     if (lane == 0) lsum[warp] = ls;
   }
   // four elements a thread, the partials dealt over the threads left; loaded before their weights are known
-  constexpr int kQuads = HD / 4, kDeal = kCombine / kQuads, kAhead = 8;
-  const int i = threadIdx.x % kQuads * 4, deal = threadIdx.x / kQuads, pair = i / 32 / NS;
+  constexpr int kQuads = RB * HD / 4, kDeal = kCombine / kQuads, kAhead = 8;
+  const int i = threadIdx.x % kQuads * 4, deal = threadIdx.x / kQuads;
+  const int hr = i / HD, d = i % HD, pair = hr * GV + d / 32 / NS;
   float4 ahead[kAhead];
 #pragma unroll
   for (int j = 0; j < kAhead; ++j)
-    if (deal + j * kDeal < runs) ahead[j] = *reinterpret_cast<const float4*>(part(deal + j * kDeal) + hr * HD + i);
+    if (deal + j * kDeal < runs) ahead[j] = *reinterpret_cast<const float4*>(part(deal + j * kDeal) + row0 * HD + i);
   __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](int k, const float4& v) {
-    const float w = wt[k * GV + pair];
+    const float w = wt[k * PB + pair];
     acc.x += w * v.x;
     acc.y += w * v.y;
     acc.z += w * v.z;
@@ -725,10 +810,10 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   for (int j = 0; j < kAhead; ++j)
     if (deal + j * kDeal < runs) add(deal + j * kDeal, ahead[j]);
   for (int k = deal + kAhead * kDeal; k < runs; k += kDeal)
-    add(k, *reinterpret_cast<const float4*>(part(k) + hr * HD + i));
+    add(k, *reinterpret_cast<const float4*>(part(k) + row0 * HD + i));
   red[threadIdx.x] = acc;
   __syncthreads();
-  if (deal == 0) {
+  if (deal == 0 && hr < n_rows) {
 #pragma unroll
     for (int k = 1; k < kDeal; ++k) {
       const float4 v = red[k * kQuads + threadIdx.x];
@@ -738,8 +823,9 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
       acc.w += v.w;
     }
     const float ls = lsum[pair];
-    float* out = a.out + (q_first(a, s) + row / plan.G) * a.out_stride +
-                 static_cast<int64_t>(kvh * plan.G + row % plan.G) * HD + i;
+    const int row = rt * R + row0 + hr;
+    float* out = a.out + (q_first(a, s) + plan.query(row)) * a.out_stride +
+                 static_cast<int64_t>(kvh * plan.G + (row - plan.query(row) * plan.G)) * HD + d;
     out[0] = ls == 0.f ? 0.f : acc.x / ls;
     out[1] = ls == 0.f ? 0.f : acc.y / ls;
     out[2] = ls == 0.f ? 0.f : acc.z / ls;
@@ -757,7 +843,7 @@ cudaError_t launch(const Q4AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_attention_q4<HD, NT, GV>, dim3(kCtas), C::T, smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_attention_q4_join<HD, NT, GV>, dim3(kCtas * C::R), kCombine, plan_b, st, a);
+  return launch_pdl(k_attention_q4_join<HD, NT, GV>, dim3(kCtas * C::B), kCombine, plan_b, st, a);
 }
 
 }  // namespace
