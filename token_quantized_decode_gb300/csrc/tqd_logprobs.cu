@@ -115,8 +115,12 @@ __device__ Sums block_join(Sums v, Sums* sm) {
 __device__ void keep_best(const Key* keys, int n, int k, Key* out) {
   for (int i = threadIdx.x; i < n; i += kLT) {
     const Key mine = keys[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > mine;
+    int rank = 0, j = 0;
+    for (; j + 4 <= n; j += 4) {
+      const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(keys + j), q = *reinterpret_cast<const ulonglong2*>(keys + j + 2);
+      rank += (p.x > mine) + (p.y > mine) + (q.x > mine) + (q.y > mine);
+    }
+    for (; j < n; ++j) rank += keys[j] > mine;
     if (rank < k) out[rank] = mine;
   }
   __syncthreads();
@@ -269,12 +273,13 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
       __syncthreads();
       const float reach = floor_, above = first ? -INFINITY : least;
       if (gm >= reach && gm > above)
-        for (int tile = group; tile < end; ++tile)
-          for (int j = 0; j < kEach; ++j) {
-            const int i = index_of(tile, j);
-            const float v = i >= 0 && i < a.vocab ? x[i] : -INFINITY;
-            if (v >= reach && v > above) insert(v, i);
-          }
+        for (int tile = group; tile < end; ++tile) {
+          float v[kEach];
+          load(tile, v);
+#pragma unroll
+          for (int j = 0; j < kEach; ++j)
+            if (v[j] >= reach && v[j] > above) insert(v[j], index_of(tile, j));
+        }
       __syncthreads();
       n = held + counts[turn];
     }
@@ -284,12 +289,15 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
       Key* hk = reinterpret_cast<Key*>(heads);
       for (int r = 0; r < k; ++r) {
         Key top = 0ull;
-        for (int tile = group; tile < end; ++tile)
+        for (int tile = group; tile < end; ++tile) {
+          float v[kEach];
+          load(tile, v);
+#pragma unroll
           for (int j = 0; j < kEach; ++j) {
-            const int i = index_of(tile, j);
-            const Key key = i >= 0 && i < a.vocab ? logit_key(x[i], i) : 0ull;
+            const Key key = logit_key(v[j], index_of(tile, j));
             if (key < below && key > top) top = key;
           }
+        }
         for (int j = tid; j < held; j += kLT)
           if (buf[j] < below && buf[j] > top) top = buf[j];
 #pragma unroll
@@ -331,14 +339,16 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
     own.t = w * (rt + rs * d);
     own.s = w * rs;
   } else if (bm > -INFINITY) {
-    for (int tile = tile0; tile < tile1; ++tile)
+    for (int tile = tile0; tile < tile1; ++tile) {
+      float v[kEach];
+      load(tile, v);
+#pragma unroll
       for (int j = 0; j < kEach; ++j) {
-        const int i = index_of(tile, j);
-        const float v = i >= 0 && i < a.vocab ? x[i] : -INFINITY;
-        const float d = v == bm ? 0.f : fmaxf((v - bm) * kLog2e, -300.f), e = ex2(d);
+        const float d = v[j] == bm ? 0.f : fmaxf((v[j] - bm) * kLog2e, -300.f), e = ex2(d);
         own.s += e;
         own.t = fmaf(e, d, own.t);
       }
+    }
   }
   const Sums all = block_join(own, sm);
   const int n = held;
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
 
 // One block per row joins its slices.
 __global__ void __launch_bounds__(kLT) k_logprobs_join(LogprobArgs a, int slices) {
-  __shared__ Key buf[kJoinCap];
+  __shared__ __align__(16) Key buf[kJoinCap];
   __shared__ Key best[kLogprobMaxTopK];
   __shared__ Key heads[kMaxSlices];
   __shared__ Sums sm[kLT / 32];

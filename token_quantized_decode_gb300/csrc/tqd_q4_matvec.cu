@@ -159,58 +159,78 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
     if (slab) __syncthreads();
     const int octs = ng * 4;
     const int real = min(a.groups - g0, ng) * 4;
-    // (whole warps: octs is a multiple of 16, and a group's four octets are neighbouring lanes)
-    for (int i0 = warp * 32; i0 < octs * (NC / 2); i0 += kMvThreads) {
-      const int i = i0 + lane, v = i / octs, o = i - v * octs;
-      float f[8], m = 0.f, zh = 0.f, zl = 0.f;
+    // Octets of columns: kBatch of them loaded before the first is used.  (Whole
+    // warps: octs is a multiple of 16, and a group's four octets are neighbouring lanes.)
+    constexpr int kBatch = ONE ? 2 : 4;
+    const bool wide = (reinterpret_cast<uintptr_t>(x) % 16 | a.xs % 4) == 0;
+    for (int i0 = warp * 32; i0 < octs * (NC / 2); i0 += kBatch * kMvThreads) {
+      float fs_[kBatch][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.f;
-      if (v < nv && o < real) {
-        const float* p = x + v * a.xs + static_cast<int64_t>(g0) * 32 + o * 8;
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kMvThreads + lane, v = i / octs, o = i - v * octs;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = p[j];
+        for (int j = 0; j < 8; ++j) fs_[k][j] = 0.f;
+        if (v < nv && o < real) {
+          const float* p = x + v * a.xs + static_cast<int64_t>(g0) * 32 + o * 8;
+          if (wide) {
+            const float4 lo4 = *reinterpret_cast<const float4*>(p), hi4 = *reinterpret_cast<const float4*>(p + 4);
+            fs_[k][0] = lo4.x; fs_[k][1] = lo4.y; fs_[k][2] = lo4.z; fs_[k][3] = lo4.w;
+            fs_[k][4] = hi4.x; fs_[k][5] = hi4.y; fs_[k][6] = hi4.z; fs_[k][7] = hi4.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) fs_[k][j] = p[j];
+          }
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kMvThreads + lane, v = i / octs, o = i - v * octs;
+        if (i - lane >= octs * (NC / 2)) break;
+        float (&f)[8] = fs_[k];
+        float m = 0.f, zh = 0.f, zl = 0.f;
 #pragma unroll
-      for (int s = 1; s < 4; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-      const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127, up = 10 - e;
-      const float f1 = pow2(up / 2), f2 = pow2(up - up / 2);
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = e > 112 ? __int_as_float(0x7FC00000) : f[j] * f1 * f2;
-      float hi[8], lo[8];
+        for (int s = 1; s < 4; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+        const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127, up = 10 - e;
+        const float f1 = pow2(up / 2), f2 = pow2(up - up / 2);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        hi[j] = rintf(f[j]);
-        lo[j] = round_f16(f[j] - hi[j]);  // (rounded here: the start of the sum counts what the operand holds)
-        zh += hi[j];
-        zl += lo[j];
+        for (int j = 0; j < 8; ++j) f[j] = e > 112 ? __int_as_float(0x7FC00000) : f[j] * f1 * f2;
+        float hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          hi[j] = rintf(f[j]);
+          lo[j] = round_f16(f[j] - hi[j]);  // (rounded here: the start of the sum counts what the operand holds)
+          zh += hi[j];
+          zl += lo[j];
+        }
+#pragma unroll
+        for (int s = 1; s < 4; s <<= 1) {
+          zh += __shfl_xor_sync(0xFFFFFFFFu, zh, s);
+          zl += __shfl_xor_sync(0xFFFFFFFFu, zl, s);
+        }
+        if (v < NC / 2) {
+          const int g = o >> 2, oc = o & 3;
+          if (oc == 0) {
+            zh *= -8.f * 0x1p-24f;
+            zl *= -8.f * 0x1p-24f;
+            zs[g * (NC / 2) + v] = make_float4(zh, zl, zh, zl);
+            fs[g * (NC / 2) + v] = pow2(min(24 - up, 127));
+          }
+          uint4 q;
+          unsigned char* d = xs + ((g * NC + 2 * v) * 4 + oc) * 16;
+          q.x = pack_f16(hi[0], hi[4]);
+          q.y = pack_f16(0.0625f * hi[1], 0.0625f * hi[5]);
+          q.z = pack_f16(hi[2], hi[6]);
+          q.w = pack_f16(0.0625f * hi[3], 0.0625f * hi[7]);
+          *reinterpret_cast<uint4*>(d) = q;
+          q.x = pack_f16(lo[0], lo[4]);
+          q.y = pack_f16(0.0625f * lo[1], 0.0625f * lo[5]);
+          q.z = pack_f16(lo[2], lo[6]);
+          q.w = pack_f16(0.0625f * lo[3], 0.0625f * lo[7]);
+          *reinterpret_cast<uint4*>(d + 64) = q;
+        }
       }
-#pragma unroll
-      for (int s = 1; s < 4; s <<= 1) {
-        zh += __shfl_xor_sync(0xFFFFFFFFu, zh, s);
-        zl += __shfl_xor_sync(0xFFFFFFFFu, zl, s);
-      }
-      if (v >= NC / 2) continue;
-      const int g = o >> 2, oc = o & 3;
-      if (oc == 0) {
-        zh *= -8.f * 0x1p-24f;
-        zl *= -8.f * 0x1p-24f;
-        zs[g * (NC / 2) + v] = make_float4(zh, zl, zh, zl);
-        fs[g * (NC / 2) + v] = pow2(min(24 - up, 127));
-      }
-      uint4 q;
-      unsigned char* d = xs + ((g * NC + 2 * v) * 4 + oc) * 16;
-      q.x = pack_f16(hi[0], hi[4]);
-      q.y = pack_f16(0.0625f * hi[1], 0.0625f * hi[5]);
-      q.z = pack_f16(hi[2], hi[6]);
-      q.w = pack_f16(0.0625f * hi[3], 0.0625f * hi[7]);
-      *reinterpret_cast<uint4*>(d) = q;
-      q.x = pack_f16(lo[0], lo[4]);
-      q.y = pack_f16(0.0625f * lo[1], 0.0625f * lo[5]);
-      q.z = pack_f16(lo[2], lo[6]);
-      q.w = pack_f16(0.0625f * lo[3], 0.0625f * lo[7]);
-      *reinterpret_cast<uint4*>(d + 64) = q;
     }
     __syncthreads();
 
