@@ -14,18 +14,22 @@
 // Alternatives are ordered by a 64-bit key (the logit's bits in integer order,
 // then the complement of the index), which no two tokens share, so the result
 // does not depend on the order of insertion.  A block keeps a list of
-// candidates in shared memory and a threshold, the k-th best logit of the
-// groups of tiles behind it: a thread compares its largest new logit with it, and on most
-// tiles that is all.  The first group, and one that overflows the list, is
-// read again (from L2) with a threshold of its own: the k-th largest of the threads'
-// maxima over it, which at least k and, but for equal logits, at most 32 k tokens
-// reach.
+// candidates in shared memory and a threshold, the k-th best logit so far,
+// brought up to date after 4, 16, 64, ... tiles (about 3 k insertions each time,
+// and no other barrier while a row streams): a thread compares its largest new logit
+// with it, and on most tiles that is all.  The first 4 tiles are read again (from
+// L2) with the k-th largest of the threads' maxima, which at least k tokens reach
+// and about k do.  A list that overflows (many equal logits, or ascending ones) is
+// dropped, and at the end all threads read again what lies with the threads
+// whose largest logit reaches the k-th largest; where more than 64 do, the equal
+// logits are taken in order of index.
 //
 // HBM bounds it: 4 bytes a logit and about seven instructions (a fused
-// multiply-add, a maximum, an exponential, two sums; half a maximum).  A tile is
-// 8 logits a thread, the next one's loads issued before the current one's work.
-// Few rows are cut into slices of whole tiles, one block each, whose partial
-// (m, s, t) and alternatives a second kernel joins (programmatic dependent launch).
+// multiply-add, a maximum, an exponential, two sums; half a maximum).  A tile
+// is 8 logits a thread, the next one's loads
+// issued before the current one's work.  Few rows are cut into slices of whole
+// tiles, one block each, whose partial (m, s, t) and alternatives a second kernel
+// joins (programmatic dependent launch).
 #include <cuda_runtime.h>
 
 #include "tqd_internal.h"
@@ -36,26 +40,29 @@ namespace {
 constexpr int kLT = 256;         // threads of a block
 constexpr int kEach = 8;         // logits of a thread per tile
 constexpr int kTile = kLT * kEach;
-constexpr int kGroup = 4;        // tiles between looks at the list
-constexpr int kCap = 1024;       // candidates a block holds: kGroup * kEach * kLogprobMaxTopK
-constexpr int kFull = 128;       // candidates at which it keeps the k best only
-static_assert(kCap == kGroup * kEach * kLogprobMaxTopK, "a group's candidates fit but for equal logits");
+constexpr int kCap = 1024;       // candidates a block holds
+constexpr int kFirst = 4;        // tiles before the list is first looked at
+constexpr int kMost = 64;        // threads whose logits are read again
 constexpr int kJoinCap = kLogprobMaxTopK * kLogprobMaxTopK;
 constexpr int kMaxSlices = 256;
 
 using Key = unsigned long long;
 
+// An f32's bits in integer order (-0 as 0), and back.
+__device__ __forceinline__ uint32_t order_bits(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float bits_order(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+
 // 0 for NaN and -inf, which are no alternatives.
 __device__ __forceinline__ Key logit_key(float x, int i) {
   if (!(x > -INFINITY)) return 0ull;
-  const uint32_t b = __float_as_uint(x + 0.f);
-  const uint32_t u = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return (static_cast<Key>(u) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
+  return (static_cast<Key>(order_bits(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
 }
-__device__ __forceinline__ float key_logit(Key k) {
-  const uint32_t u = static_cast<uint32_t>(k >> 32);
-  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
-}
+__device__ __forceinline__ float key_logit(Key k) { return bits_order(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ int key_index(Key k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -158,9 +165,10 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
   __shared__ Key best[kLogprobMaxTopK];
   __shared__ __align__(16) float heads[kLT];
   __shared__ Sums sm[kLT / 32];
-  __shared__ int counts[3];  // insertions of a group, of the next, of the one after
-  __shared__ float floor_;
-  const int tid = threadIdx.x, k = a.top_k;
+  __shared__ int count, found, members;
+  __shared__ uint8_t member[kLT];
+  __shared__ uint32_t floor_;
+  const int tid = threadIdx.x, lane = tid & 31, k = a.top_k;
   pdl_wait();
   pdl_launch_dependents();
   const unsigned row = blockIdx.x / static_cast<unsigned>(slices);
@@ -170,13 +178,23 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
   const int tiles = (a.vocab + off + kTile - 1) / kTile;
   const int tile0 = slice * tiles_each, tile1 = min(tile0 + tiles_each, tiles);
-  if (tid < 3) counts[tid] = 0;
-
-  auto index_of = [&](int tile, int j) { return tile * kTile - off + (j >> 2) * (kLT * 4) + tid * 4 + (j & 3); };
   const int whole0 = off ? 1 : 0, whole1 = (a.vocab + off) / kTile;  // tiles that lie inside the row
+
+  // the four logits of quad `quad` of a tile (thread t holds quads t and kLT + t), and the index of the first
+  auto quad_index = [&](int tile, int quad) { return tile * kTile - off + quad * 4; };
+  auto load_quad = [&](int tile, int quad) {
+    const int i = quad_index(tile, quad);
+    if (tile >= whole0 && tile < whole1) return *reinterpret_cast<const float4*>(x + i);
+    float4 q;
+    q.x = i >= 0 && i < a.vocab ? x[i] : -INFINITY;
+    q.y = i + 1 >= 0 && i + 1 < a.vocab ? x[i + 1] : -INFINITY;
+    q.z = i + 2 >= 0 && i + 2 < a.vocab ? x[i + 2] : -INFINITY;
+    q.w = i + 3 >= 0 && i + 3 < a.vocab ? x[i + 3] : -INFINITY;
+    return q;
+  };
   auto load = [&](int tile, float (&v)[kEach]) {
     if (tile >= whole0 && tile < whole1) {
-      const float* p = x + index_of(tile, 0);
+      const float* p = x + quad_index(tile, tid);
 #pragma unroll
       for (int h = 0; h < kEach / 4; ++h) {
         const float4 q = *reinterpret_cast<const float4*>(p + h * (kLT * 4));
@@ -184,155 +202,119 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
       }
     } else {
 #pragma unroll
-      for (int h = 0; h < kEach; ++h) {
-        const int at = index_of(tile, h);
-        v[h] = at >= 0 && at < a.vocab ? x[at] : -INFINITY;
+      for (int h = 0; h < kEach / 4; ++h) {
+        const float4 q = load_quad(tile, h * kLT + tid);
+        v[4 * h] = q.x; v[4 * h + 1] = q.y; v[4 * h + 2] = q.z; v[4 * h + 3] = q.w;
       }
     }
   };
-  int held = 0, turn = 0;  // the list's length at the group's start (every thread's), and the group's counter
   auto insert = [&](float v, int i) {
-    const int p = held + atomicAdd(&counts[turn], 1);
+    const int p = atomicAdd(&count, 1);
     if (p < kCap) buf[p] = logit_key(v, i);
-    return p;
+  };
+  auto index_of = [&](int tile, int j) { return quad_index(tile, (j >> 2) * kLT + tid) + (j & 3); };
+  // The k-th largest of the threads' largest logits (in heads; this thread's is mine), -inf where fewer than k
+  // are above it.  floor_ holds ~0 before.
+  auto kth_head = [&](float mine) {
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < kLT; j += 4) {
+      const float4 h = *reinterpret_cast<const float4*>(heads + j);
+      above += h.x > mine;
+      above += h.y > mine;
+      above += h.z > mine;
+      above += h.w > mine;
+    }
+    if (above < k) atomicMin(&floor_, order_bits(mine));
+    __syncthreads();
+    return bits_order(floor_);
   };
 
+  // ---- one pass: sums, and the thread's largest logit
   constexpr float kRefMin = -1048576.f;
   float ref = kRefMin, rise = -INFINITY;  // rise: a logit above it moves the reference
   float rs = 0.f, rt = 0.f, rm = -INFINITY;
-  float least = INFINITY;  // the first group is read again with a threshold of its own
+  float least = INFINITY;  // a logit above it is a candidate
+  int check = k ? min(tile0 + kFirst, tile1) : tile1 + 1, n = 0;  // the tile before which the list is looked at; its length then
+  bool over = false, first = true;
   float nx[kEach];
+  if (tid == 0) {
+    count = found = members = 0;
+    floor_ = ~0u;
+  }
   if (tile0 < tile1) load(tile0, nx);
-  __syncthreads();
-  for (int group = tile0; group < tile1; group += kGroup) {
-    const int end = min(group + kGroup, tile1);
-    const bool first = group == tile0;
-    // (the counter of the next group was last read before the barrier behind the group before this one)
-    if (tid == 0) counts[turn == 2 ? 0 : turn + 1] = 0;
-    float gm = -INFINITY;
-    bool want = first;
-    for (int tile = group; tile < end; ++tile) {
-      float v[kEach];
+  for (int tile = tile0; tile < tile1; ++tile) {
+    float v[kEach];
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) v[j] = nx[j];
-      if (tile + 1 < tile1) load(tile + 1, nx);
-      float lm = fmaxf(v[0], -INFINITY);  // (eight NaN)
+    for (int j = 0; j < kEach; ++j) v[j] = nx[j];
+    if (tile + 1 < tile1) load(tile + 1, nx);
+    float lm = fmaxf(v[0], -INFINITY);  // (eight NaN)
 #pragma unroll
-      for (int j = 1; j < kEach; ++j) lm = fmaxf(lm, v[j]);
-      gm = fmaxf(gm, lm);
-      if (lm > rise) {
-        const float nref = fminf(fmaxf(rintf(lm * kLog2e), kRefMin), -kRefMin);
-        const float d = fmaxf(ref - nref, -300.f), w = ex2(d);
-        rt = w * (rt + rs * d);
-        rs *= w;
-        ref = nref;
-        rise = (nref + 16.f) * kLn2;
-      }
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        const float d = fmaxf(fmaf(v[j], kLog2e, -ref), -300.f), e = ex2(d);
-        rs += e;
-        rt = fmaf(e, d, rt);
-      }
-      if (lm > least) {
-#pragma unroll
-        for (int j = 0; j < kEach; ++j)
-          if (v[j] > least) want |= insert(v[j], index_of(tile, j)) >= kFull;
-      }
+    for (int j = 1; j < kEach; ++j) lm = fmaxf(lm, v[j]);
+    rm = fmaxf(rm, lm);
+    if (lm > rise) {
+      const float nref = fminf(fmaxf(rintf(lm * kLog2e), kRefMin), -kRefMin);
+      const float d = fmaxf(ref - nref, -300.f), w = ex2(d);
+      rt = w * (rt + rs * d);
+      rs *= w;
+      ref = nref;
+      rise = (nref + 16.f) * kLn2;
     }
-    rm = fmaxf(rm, gm);
-    if (k == 0) continue;
-    const bool merge = __syncthreads_or(want) || end == tile1;
-    int n = held + counts[turn];
-    if (!merge) {
-      held = n;
-      turn = turn == 2 ? 0 : turn + 1;
-      continue;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const float d = fmaxf(fmaf(v[j], kLog2e, -ref), -300.f), e = ex2(d);
+      rs += e;
+      rt = fmaf(e, d, rt);
     }
+    if (lm > least) {
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)
+        if (v[j] > least) insert(v[j], index_of(tile, j));
+    }
+    if (tile + 1 != check) continue;
 
-    // ---- keep the k best
-    if (first || n > kCap) {
-      // The group again: the tokens that reach the k-th largest of the threads'
-      // maxima, and those that the earlier list holds.  (Of this group's own
-      // first insertions none are kept: they began at `held`.)
-      heads[tid] = gm;
+    // ---- the list is brought up to date
+    if (first) {  // these tiles again
+      first = false;
+      heads[tid] = rm;
       __syncthreads();
-      if (tid == 0) {
-        counts[turn] = 0;
-        floor_ = -INFINITY;
-      }
-      int rank = 0;
-#pragma unroll 8
-      for (int j = 0; j < kLT; j += 4) {
-        const float4 h = *reinterpret_cast<const float4*>(heads + j);
-        rank += (h.x > gm || (h.x == gm && j < tid)) + (h.y > gm || (h.y == gm && j + 1 < tid)) +
-                (h.z > gm || (h.z == gm && j + 2 < tid)) + (h.w > gm || (h.w == gm && j + 3 < tid));
-      }
-      __syncthreads();
-      if (rank == k - 1) floor_ = gm;
-      __syncthreads();
-      const float reach = floor_, above = first ? -INFINITY : least;
-      if (gm >= reach && gm > above)
-        for (int tile = group; tile < end; ++tile) {
-          float v[kEach];
-          load(tile, v);
+      const float reach = kth_head(rm);
+      if (rm >= reach && rm > -INFINITY)
+        for (int t = tile0; t < check; ++t) {
+          float w[kEach];
+          load(t, w);
 #pragma unroll
           for (int j = 0; j < kEach; ++j)
-            if (v[j] >= reach && v[j] > above) insert(v[j], index_of(tile, j));
+            if (w[j] >= reach && w[j] > -INFINITY) insert(w[j], index_of(t, j));
         }
-      __syncthreads();
-      n = held + counts[turn];
     }
-    if (n > kCap) {
-      // Too many equal logits: the group's k best one by one, from it and the earlier list.
-      Key below = ~0ull;
-      Key* hk = reinterpret_cast<Key*>(heads);
-      for (int r = 0; r < k; ++r) {
-        Key top = 0ull;
-        for (int tile = group; tile < end; ++tile) {
-          float v[kEach];
-          load(tile, v);
-#pragma unroll
-          for (int j = 0; j < kEach; ++j) {
-            const Key key = logit_key(v[j], index_of(tile, j));
-            if (key < below && key > top) top = key;
-          }
-        }
-        for (int j = tid; j < held; j += kLT)
-          if (buf[j] < below && buf[j] > top) top = buf[j];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const Key w = __shfl_xor_sync(0xFFFFFFFFu, top, o);
-          if (w > top) top = w;
-        }
-        if ((tid & 31) == 0) hk[tid >> 5] = top;
-        __syncthreads();
-        top = hk[0];
-        for (int w = 1; w < kLT / 32; ++w)
-          if (hk[w] > top) top = hk[w];
-        if (tid == 0) best[r] = top;
-        below = top;
-        __syncthreads();
-      }
-      n = k;  // (there are more than kCap >= k)
+    __syncthreads();
+    n = count;
+    over |= n > kCap;
+    __syncthreads();
+    if (over) {
+      least = INFINITY;
     } else {
       keep_best(buf, n, k, best);
       n = min(n, k);
+      if (tid < n) buf[tid] = best[tid];
+      least = n == k ? key_logit(best[k - 1]) : -INFINITY;
     }
-    if (tid < n) buf[tid] = best[tid];
-    held = n;
-    turn = turn == 2 ? 0 : turn + 1;
-    least = n == k ? key_logit(best[k - 1]) : -INFINITY;
+    if (tid == 0) count = over ? 0 : n;
+    check = check == tile1 ? tile1 + 1 : min(tile0 + 4 * (check - tile0), tile1);
     __syncthreads();
   }
 
   // ---- the block's sums, relative to its own largest logit
-  float bm = rm;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, o));
-  if ((tid & 31) == 0) heads[tid >> 5] = bm;
+  heads[tid] = rm;
+  if (tid == 0) {
+    count = 0;
+    floor_ = ~0u;
+  }
   __syncthreads();
-  for (int w = 0; w < kLT / 32; ++w) bm = fmaxf(bm, heads[w]);
+  float bm = fmaxf(fmaxf(heads[lane], heads[lane + 32]), fmaxf(heads[lane + 64], heads[lane + 96]));
+  bm = fmaxf(bm, fmaxf(fmaxf(heads[lane + 128], heads[lane + 160]), fmaxf(heads[lane + 192], heads[lane + 224])));
+  bm = warp_max(bm);
   Sums own{bm, 0.f, 0.f};
   if (by_ref(bm)) {
     const float d = fmaxf(ref - ref_of(bm), -300.f), w = ex2(d);
@@ -350,8 +332,134 @@ __global__ void __launch_bounds__(kLT, 5) k_logprobs(LogprobArgs a, int slices, 
       }
     }
   }
-  const Sums all = block_join(own, sm);
-  const int n = held;
+  // (all relative to the same logit: plain sums)
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    own.s += __shfl_xor_sync(0xFFFFFFFFu, own.s, o);
+    own.t += __shfl_xor_sync(0xFFFFFFFFu, own.t, o);
+  }
+  if (lane == 0) sm[tid >> 5] = own;
+
+  // ---- the k best, where the list overflowed
+  if (over) {
+    const float reach = kth_head(rm);  // -inf: fewer than k threads hold a logit above it
+    const int reaching = __syncthreads_count(rm > -INFINITY && rm >= reach);
+    const bool ties = reaching > kMost;
+    if (rm > -INFINITY && (ties ? rm > reach : rm >= reach)) member[atomicAdd(&members, 1)] = static_cast<uint8_t>(tid);
+    __syncthreads();
+    const int m = members;
+    const int items = (tile1 - tile0) * (kEach / 4) * m;  // quads to read again
+    auto take = [&](float v, int i) {
+      if (ties ? v > reach : v >= reach && v > -INFINITY) {
+        const int p = atomicAdd(&count, 1);
+        if (p < kCap) buf[p] = logit_key(v, i);
+      }
+    };
+    for (int i0 = tid; i0 < items; i0 += 4 * kLT) {
+      float4 q[4];
+      int at[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kLT;
+        q[u] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (i < items) {
+          const int part = i / m, tile = tile0 + part / (kEach / 4);
+          const int quad = part % (kEach / 4) * kLT + member[i - part * m];
+          at[u] = quad_index(tile, quad);
+          q[u] = load_quad(tile, quad);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        take(q[u].x, at[u]);
+        take(q[u].y, at[u] + 1);
+        take(q[u].z, at[u] + 2);
+        take(q[u].w, at[u] + 3);
+      }
+    }
+    __syncthreads();
+    n = count;
+    if (ties && n < k) {
+      // the first k - n tokens at the threshold, in order of index: quads of a
+      // tile in the threads' order, each thread's place from the counts before it
+      for (int tile = tile0; tile < tile1 && n + found < k; ++tile)
+        for (int h = 0; h < kEach / 4; ++h) {
+          const float4 q = load_quad(tile, h * kLT + tid);
+          const int mine = (q.x == reach) + (q.y == reach) + (q.z == reach) + (q.w == reach);
+          int run = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, run, o);
+            if (lane >= o) run += u;
+          }
+          if (lane == 31) heads[tid >> 5] = __int_as_float(run);
+          __syncthreads();
+          int place = n + found + run - mine, all = 0;
+          for (int w = 0; w < kLT / 32; ++w) {
+            const int c = __float_as_int(heads[w]);
+            if (w < (tid >> 5)) place += c;
+            all += c;
+          }
+          const float v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (v[j] == reach) {
+              if (place < k) buf[place] = logit_key(v[j], quad_index(tile, h * kLT + tid) + j);
+              ++place;
+            }
+          __syncthreads();
+          if (tid == 0) found += all;
+          __syncthreads();
+        }
+      n = min(n + found, k);
+    }
+    if (n > kCap) {
+      // More than the list holds (a few threads hold most large logits): one by one.
+      Key below = ~0ull;
+      Key* hk = reinterpret_cast<Key*>(heads);
+      for (int r = 0; r < k; ++r) {
+        Key top = 0ull;
+        for (int tile = tile0; tile < tile1; ++tile) {
+#pragma unroll
+          for (int h = 0; h < kEach / 4; ++h) {
+            const float4 q = load_quad(tile, h * kLT + tid);
+            const int i = quad_index(tile, h * kLT + tid);
+            const Key keys[4] = {logit_key(q.x, i), logit_key(q.y, i + 1), logit_key(q.z, i + 2), logit_key(q.w, i + 3)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (keys[j] < below && keys[j] > top) top = keys[j];
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const Key w = __shfl_xor_sync(0xFFFFFFFFu, top, o);
+          if (w > top) top = w;
+        }
+        __syncthreads();
+        if (lane == 0) hk[tid >> 5] = top;
+        __syncthreads();
+        top = hk[0];
+        for (int w = 1; w < kLT / 32; ++w)
+          if (hk[w] > top) top = hk[w];
+        if (tid == 0) best[r] = top;
+        below = top;
+      }
+      n = k;  // (there are more than kCap >= k)
+      __syncthreads();
+    } else {
+      keep_best(buf, n, k, best);
+      n = min(n, k);
+    }
+  } else {
+    __syncthreads();
+  }
+
+  Sums all{bm, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < kLT / 32; ++w) {
+    all.s += sm[w].s;
+    all.t += sm[w].t;
+  }
   if (slices == 1) {
     write_row(a, row, all, best, n);
     return;
@@ -396,12 +504,20 @@ __global__ void __launch_bounds__(kLT) k_logprobs_join(LogprobArgs a, int slices
       if (tid < slices && head && rank == k - 1) floor_ = head;
       __syncthreads();
     }
-    if (head >= floor_)
-      for (int j = 0; j < k; ++j) {
-        const Key key = reinterpret_cast<const Key*>(part + tid * partial_bytes(k) + 16)[j];
-        if (key < floor_) break;
-        buf[atomicAdd(&count, 1)] = key;
+    const Key reach = floor_;
+    for (int i0 = tid; i0 < slices * k; i0 += 4 * kLT) {
+      Key key[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kLT, sl = i / k;
+        key[u] = i < slices * k && heads[sl] >= reach
+                     ? reinterpret_cast<const Key*>(part + sl * partial_bytes(k) + 16)[i - sl * k]
+                     : 0ull;
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (key[u] >= reach) buf[atomicAdd(&count, 1)] = key[u];
+    }
     __syncthreads();
     keep_best(buf, count, k, best);
     n = min(count, k);
@@ -409,25 +525,37 @@ __global__ void __launch_bounds__(kLT) k_logprobs_join(LogprobArgs a, int slices
   write_row(a, row, all, best, n);
 }
 
-// Slices of a row: whole tiles, so that about 152 x 4 blocks run.
-int slices_of(int rows, int vocab) {
-  const int tiles = (vocab + 3 + kTile - 1) / kTile;
-  int want = (608 + rows - 1) / rows;
-  if (want > tiles) want = tiles;
-  if (want > kMaxSlices) want = kMaxSlices;
-  const int each = (tiles + want - 1) / want;
+// Slices of a row, of whole tiles: what makes the waves of 5 blocks an SM
+// shortest, a block being counted as its tiles and, for its beginning, end and
+// list, 8 more (2 without alternatives).
+int slices_of(int rows, int vocab, int top_k) {
+  constexpr int64_t kWave = 5 * 152;
+  const int tiles = (vocab + 3 + kTile - 1) / kTile, fixed = top_k ? 8 : 2;
+  const int most = tiles < kMaxSlices ? tiles : kMaxSlices;
+  int best = 1;
+  int64_t least = -1;
+  for (int s = 1; s <= most; ++s) {
+    const int each = (tiles + s - 1) / s;
+    const int64_t cost = (static_cast<int64_t>(rows) * s + kWave - 1) / kWave * (each + fixed);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = s;
+    }
+    if (static_cast<int64_t>(rows) * s >= 4 * kWave) break;
+  }
+  const int each = (tiles + best - 1) / best;
   return (tiles + each - 1) / each;
 }
 
 }  // namespace
 
 size_t logprobs_scratch_bytes(int rows, int vocab, int top_k) {
-  const int s = slices_of(rows, vocab);
+  const int s = slices_of(rows, vocab, top_k);
   return s == 1 ? 16 : static_cast<size_t>(rows) * s * partial_bytes(top_k);
 }
 
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
-  const int slices = slices_of(a.rows, a.vocab);
+  const int slices = slices_of(a.rows, a.vocab, a.top_k);
   const int tiles = (a.vocab + 3 + kTile - 1) / kTile;
   const int each = (tiles + slices - 1) / slices;
   const cudaError_t e = launch_pdl(k_logprobs, dim3(static_cast<unsigned>(a.rows) * slices), kLT, 0, st, a, slices, each);
