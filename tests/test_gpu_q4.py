@@ -60,11 +60,13 @@ def rope_table(ops, hd, n, theta=1e6):
 class Host:
     """A cache on the host: pages as bytes, a shuffled table, and the rows that were stored."""
 
-    def __init__(self, rng, n_seq, n_kv, hd, page, positions, spare=1):
+    def __init__(self, rng, n_seq, n_kv, hd, page, positions, spare=1, room=0):
         self.hd, self.n_kv, self.page, self.n_seq = hd, n_kv, page, n_seq
         self.per_seq = max(1, -(-positions // page))
         self.n_pages = n_seq * self.per_seq + spare
         self.table = rng.permutation(self.n_pages)[:n_seq * self.per_seq].reshape(n_seq, -1).astype(np.int32)
+        # room: positions that the table has beyond, without pages (the attention goes by the table's size)
+        self.table = np.concatenate([self.table, np.full((n_seq, -(-room // page)), -1, dtype=np.int32)], 1)
         # bytes that no call wrote: any codes, scales that are NaN
         self.pages = np.full((self.n_pages, q4.page_bytes(n_kv, hd, page)), 0xFF, dtype=np.uint8)
 
@@ -270,6 +272,55 @@ def test_attention_ragged_lengths(ops, heads, n_kv, hd, page):
     check_attention(got, q, host.K, host.V, lens, [1] * len(lens), hd)
 
 
+@pytest.mark.parametrize("heads,n_kv,hd", HEADS)
+@pytest.mark.parametrize("room", [0, 100000])
+def test_attention_by_clusters_and_by_runs(ops, heads, n_kv, hd, room):
+    """The same lengths with a short page table (a cluster for each row tile) and a long one (equal runs)."""
+    rng = np.random.default_rng(heads * 7 + hd)
+    lens = [0, 700, 1, 33, 64, 1023, 480]
+    host = Host(rng, len(lens), n_kv, hd, 32, max(lens), room=room)
+    host.fill(rng, lens)
+    q = rng.normal(size=(len(lens), heads * hd)).astype(np.float32)
+    got = attend(ops, host.device(ops), q, lens)
+    check_attention(got, q, host.K, host.V, lens, [1] * len(lens), hd)
+
+
+def test_attention_pages_outside_the_pool_by_runs(ops):
+    rng = np.random.default_rng(25)
+    hd, page = 128, 16
+    host = Host(rng, 4, 2, hd, page, 96, room=50000)
+    host.fill(rng, [90, 90, 90, 96])
+    host.table[1, 3] = -7
+    host.table[2, 5] = host.n_pages
+    q = rng.normal(size=(4, 4 * hd)).astype(np.float32)
+    got = attend(ops, host.device(ops), q, [90, 90, 90, 97])
+    assert np.all(np.isnan(got[1:]))
+    check_attention(got[:1], q[:1], host.K[:1], host.V[:1], [90], [1], hd)
+    got = attend(ops, host.device(ops), q, [90, 48, 80, 96])
+    check_attention(got, q, host.K, host.V, [90, 48, 80, 96], [1] * 4, hd)
+    got = attend(ops, host.device(ops), q, [90, 48, 2**31 - 1, -2**31])
+    check_attention(got[:2], q[:2], host.K[:2], host.V[:2], [90, 48], [1] * 2, hd)
+    assert np.all(np.isnan(got[2])) and np.all(got[3] == 0)
+
+
+def test_attention_lengths_of_any_size(ops):
+    """Lengths up to int32's ends, over a short table and with several queries: the queries that see no position
+    past the table keep their values."""
+    rng = np.random.default_rng(26)
+    hd, page = 64, 16
+    host = Host(rng, 3, 1, hd, page, 32)
+    host.fill(rng, [32, 32, 32])
+    q = rng.normal(size=(12, 2 * hd)).astype(np.float32)
+    got = attend(ops, host.device(ops), q[:3], [2**31 - 1, 20, -2**31])
+    assert np.all(np.isnan(got[0])) and np.all(got[2] == 0)
+    check_attention(got[1:2], q[1:2], host.K[1:2], host.V[1:2], [20], [1], hd)
+    # sequence 1's queries are positions 29 .. 33 of 34, of which 32 are in the table
+    got = attend(ops, host.device(ops), q, [32, 34, 2**31 - 1], [0, 4, 9, 12])
+    check_attention(got[:4], q[:4], host.K[:1], host.V[:1], [32], [4], hd)
+    check_attention(got[4:7], q[4:7], [host.K[1]], [host.V[1]], [32], [3], hd)
+    assert np.all(np.isnan(got[7:]))
+
+
 @pytest.mark.parametrize("heads,n_kv,hd", [(16, 8, 128), (15, 5, 64), (4, 1, 128), (12, 1, 128)])
 def test_attention_of_several_queries(ops, heads, n_kv, hd):
     rng = np.random.default_rng(heads * 3 + hd)
@@ -359,7 +410,6 @@ def test_attention_nan_keys_and_values(ops, heads):
     host.fill(rng, [n, n])
     bad = rng.normal(size=(1, hd))
     bad[0, 40] = np.nan
-    fine = rng.normal(size=(1, hd))
     for p in range(n, n + 5):
         host.store(0, p, bad, bad)
     host.store(0, 30, bad, host.V[0][30])
@@ -377,7 +427,6 @@ def test_attention_nan_keys_and_values(ops, heads):
                 assert np.all(np.isnan(g))
             else:
                 assert np.all(np.isnan(g[:, 32:64])) and np.all(np.isfinite(g[:, :32])) and np.all(np.isfinite(g[:, 64:]))
-    del fine
 
 
 def test_attention_pages_outside_the_pool_and_lengths_past_the_table(ops):

@@ -154,20 +154,28 @@ int32_t sampling_args(const ::tqd_sampling* p, SampleArgs& a, bool* greedy);
 
 // Launch with programmatic dependent launch: the kernel may start while the one
 // before it on the stream ends, and waits for that one's end (pdl_wait) before
-// it touches global memory.
+// it touches global memory.  cluster: CTAs of a cluster.
 template <class... P, class... A>
-cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+cudaError_t launch_pdl_clusters(void (*kernel)(P...), unsigned cluster, dim3 grid, unsigned block, size_t smem,
+                                cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+  return launch_pdl_clusters(kernel, 1u, grid, block, smem, st, args...);
 }
 
 // Let a kernel use `bytes` of dynamic shared memory: asked of the driver once

@@ -35,6 +35,11 @@
 // joined in shared memory at the CTA's end, and those of one that several CTAs
 // share by a second kernel, already launched (programmatic dependent launch).  The
 // order of every sum is fixed by the sizes.
+//
+// Where every sequence has one query and the page table holds few positions
+// (use_clusters), a cluster of 1 to 8 CTAs takes a segment instead, and joins its
+// parts through distributed shared memory: no plan and no second kernel, half the time of a
+// short call.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -246,8 +251,21 @@ struct Shared {
   int n_rows, row0, head0;  // rows of the tile, its first row, first query head of the kv head
 };
 
-template <int HD, int NT, int GV>
-__global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnArgs a) {
+// A float of another CTA of the cluster, at the address that it has in this one.
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+  float v;
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// CL: clusters of `cluster` CTAs, one a segment; else equal runs of units.
+template <int HD, int NT, int GV, bool CL>
+__global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnArgs a, int cluster) {
   using C = Cfg<HD, NT, GV>;
   constexpr int NG = C::NG, NS = C::NS, P = C::P, R = C::R, W = C::W, ST = C::ST, BB = C::BB, LD = C::LD, JB = C::JB, PART = C::PART;
   extern __shared__ __align__(128) unsigned char sm[];
@@ -271,20 +289,38 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   fence_mbar_init();
   pdl_wait();
   pdl_launch_dependents();
-  const Plan plan = make_plan(a, R, W, gridDim.x, plan_mem);
-
-  // sequences without positions: their queries see nothing
-  for (int s = blockIdx.x; s < plan.n_seq; s += gridDim.x) {
-    if (plan.len[s] > 0) continue;
-    const int64_t first = q_first(a, s);
-    for (int q = 0; q < plan.nq[s]; ++q)
-      for (int i = threadIdx.x; i < a.n_heads * HD; i += C::T) a.out[(first + q) * a.out_stride + i] = 0.f;
+  Plan plan;
+  unsigned long long c0 = 0, c1, u0, u1;  // the CTA's run of units, and the warp's
+  int cl_s = 0, cl_kvh = 0, cl_rt = 0, cl_len = 0;
+  if constexpr (CL) {
+    plan.G = a.n_heads / a.c.n_kv;
+    const int tiles = (plan.G + R - 1) / R;
+    const int seg = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    cl_s = seg / (a.c.n_kv * tiles);
+    cl_kvh = seg / tiles - cl_s * a.c.n_kv;
+    cl_rt = seg % tiles;
+    cl_len = min(max(a.lens[cl_s], 0), 1 << 30);
+    const int most = static_cast<int>(min(static_cast<long long>(a.c.table_stride) * a.c.page_size, 1ll << 30)) + kUnit;
+    const unsigned units = (min(cl_len, most) + kUnit - 1) / kUnit, warps = cluster * W;
+    plan.per = (units + warps - 1) / warps;
+    c1 = units;
+    u0 = min((rank * W + warp) * plan.per, c1);
+    u1 = min(u0 + plan.per, c1);
+  } else {
+    plan = make_plan(a, R, W, gridDim.x, plan_mem);
+    // sequences without positions: their queries see nothing
+    for (int s = blockIdx.x; s < plan.n_seq; s += gridDim.x) {
+      if (plan.len[s] > 0) continue;
+      const int64_t first = q_first(a, s);
+      for (int q = 0; q < plan.nq[s]; ++q)
+        for (int i = threadIdx.x; i < a.n_heads * HD; i += C::T) a.out[(first + q) * a.out_stride + i] = 0.f;
+    }
+    c0 = blockIdx.x * plan.per * W;
+    if (c0 >= plan.total) return;
+    c1 = min(c0 + plan.per * W, plan.total);
+    u0 = min(c0 + warp * plan.per, c1);
+    u1 = min(u0 + plan.per, c1);
   }
-
-  const unsigned long long c0 = blockIdx.x * plan.per * W;  // the CTA's run
-  if (c0 >= plan.total) return;
-  const unsigned long long c1 = min(c0 + plan.per * W, plan.total);
-  const unsigned long long u0 = min(c0 + warp * plan.per, c1), u1 = min(u0 + plan.per, c1);  // the warp's
   const int n_it = static_cast<int>(u1 - u0);
   unsigned char* my_ring = ring + warp * ST * 2 * BB;
   const int ppb = a.c.page_size / kQ4Block;  // blocks per page
@@ -296,14 +332,19 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   auto locate = [&](int i) {
     if (i >= n_it) return;
     const unsigned long long u = u0 + i;
-    const int s = plan.seq_of(u);
-    const unsigned long long uq = u - plan.pre[s];
-    const int nb = plan.units(s);
-    const unsigned long long seg = udiv(uq, nb);
-    const int t0 = static_cast<int>(uq - seg * nb) * kUnit;
-    int kvh;
-    const int rt = plan.tile_of(s, seg, &kvh);
-    const int seen = plan.seen(s, min(rt * R + R, plan.nq[s] * plan.G) - 1);
+    int s = cl_s, kvh = cl_kvh, t0, seen;
+    if constexpr (CL) {
+      t0 = static_cast<int>(u) * kUnit;
+      seen = cl_len;
+    } else {
+      s = plan.seq_of(u);
+      const unsigned long long uq = u - plan.pre[s];
+      const int nb = plan.units(s);
+      const unsigned long long seg = udiv(uq, nb);
+      t0 = static_cast<int>(uq - seg * nb) * kUnit;
+      const int rt = plan.tile_of(s, seg, &kvh);
+      seen = plan.seen(s, min(rt * R + R, plan.nq[s] * plan.G) - 1);
+    }
     src0 = src1 = nullptr;
     src_flag = t0 < seen ? 0 : 4;
 #pragma unroll
@@ -346,20 +387,26 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   int goes_on = 0;
   bool begun = false;
   unsigned long long u = u0;
-  int s = u < u1 ? plan.seq_of(u) : 0;
+  int s = cl_s;
+  if constexpr (!CL) s = u < u1 ? plan.seq_of(u) : 0;
   while (u < u1) {
     // ---- the segment of unit u: one (sequence, kv head, tile of rows)
-    while (plan.pre[s + 1] <= u) ++s;
-    const int nb = plan.units(s);
-    const unsigned long long seg = udiv(u - plan.pre[s], nb);
-    const unsigned long long seg0 = plan.pre[s] + seg * nb, seg1 = seg0 + nb;
+    unsigned long long seg0 = 0, seg1 = c1;
+    int kvh = cl_kvh, rt = cl_rt, rows = plan.G, min_seen = cl_len;
+    if constexpr (!CL) {
+      while (plan.pre[s + 1] <= u) ++s;
+      const int nb = plan.units(s);
+      const unsigned long long seg = udiv(u - plan.pre[s], nb);
+      seg0 = plan.pre[s] + seg * nb;
+      seg1 = seg0 + nb;
+      rt = plan.tile_of(s, seg, &kvh);
+      rows = plan.nq[s] * plan.G;
+      min_seen = plan.seen(s, rt * R);
+    }
     const unsigned long long uend = min(seg1, u1);
     const int rel_end = static_cast<int>(uend - u0);
     const int unit0 = static_cast<int>(static_cast<long long>(u0 - seg0));  // unit rel is the segment's rel + unit0
-    int kvh;
-    const int rt = plan.tile_of(s, seg, &kvh);
-    const int n_rows = min(R, plan.nq[s] * plan.G - rt * R);
-    const int min_seen = plan.seen(s, rt * R);
+    const int n_rows = min(R, rows - rt * R);
 
     // ---- the query rows as column operands
     int seen[NT];
@@ -370,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int row = rt * R + min(t * 4 + pair / GV, n_rows - 1);  // rows past the last repeat it
-        seen[t] = plan.seen(s, rt * R + min(t * 4 + h, n_rows - 1));
+        seen[t] = CL ? cl_len : plan.seen(s, rt * R + min(t * 4 + h, n_rows - 1));
         const float* q = a.q + (q_first(a, s) + plan.query(row)) * a.q_stride +
                          static_cast<int64_t>(kvh * plan.G + (row - plan.query(row) * plan.G)) * HD;
         // A power of two for each group of 32 brings its largest element to 2^10
@@ -578,7 +625,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
         // sums of V
         const unsigned char* vr = from + j * BB + q4_v_off(HD) + c * 128 + r * 16;
         const uint4 v0 = *reinterpret_cast<const uint4*>(vr);
-        uint4 v1 = v0;
+        [[maybe_unused]] uint4 v1 = v0;
         if constexpr (HD == 128) v1 = *reinterpret_cast<const uint4*>(vr + 512);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -636,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], x);
-    if (u0 <= seg0 && seg1 <= u1) {
+    if (!CL && u0 <= seg0 && seg1 <= u1) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (t * 4 + h >= n_rows) continue;
@@ -656,14 +703,14 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           }
       }
     } else {
-      if (lane == 0) {
+      if (!CL && lane == 0) {
         const Shared sh{seg0, seg1, q_first(a, s), n_rows, rt * R, kvh * plan.G};
         shared[warp] = sh;
         if (u == c0) shared[W] = sh;
       }
       goes_on = u0 <= seg0;  // (else it is the run's first, begun before it)
       begun |= u == c0 && seg0 < c0;
-      float* part = u0 <= seg0 ? reinterpret_cast<float*>(my_ring) : parts + warp * PART;
+      float* part = !CL && u0 <= seg0 ? reinterpret_cast<float*>(my_ring) : parts + warp * PART;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float* mo = part + (t * 4 + h) * LD + r;
@@ -684,6 +731,70 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       }
     }
     u = uend;
+  }
+  if constexpr (CL) {
+    // ---- the cluster's parts into one: the CTA's warps' first, in its ring
+    // (done with by all of them), then each CTA a share of the outputs
+    if (u0 >= u1 && lane < P) parts[warp * PART + R * LD + lane] = -INFINITY;
+    __syncthreads();
+    float* mine = reinterpret_cast<float*>(ring);  // [R][HD], [P] ref, [P] sum p
+    auto emit = [&](int i, float v, float ls) {
+      const int hr = i / HD, row = cl_rt * R + hr;
+      if (row < plan.G)
+        a.out[cl_s * a.out_stride + static_cast<int64_t>(cl_kvh * plan.G + row) * HD + i % HD] = ls == 0.f ? 0.f : v / ls;
+    };
+    for (int i = threadIdx.x; i < R * HD; i += C::T) {
+      const int hr = i / HD, d = i % HD, pr = hr * GV + d / 32 / NS;
+      float top = -INFINITY, acc = 0.f, ls = 0.f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) top = fmaxf(top, parts[k * PART + R * LD + pr]);
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float* part = parts + k * PART;
+        const float pf = part[R * LD + pr];
+        if (pf > -INFINITY) {
+          const float f = ex2(pf - top);
+          acc += f * part[hr * LD + d];
+          ls += f * part[R * LD + P + pr];
+        }
+      }
+      if (cluster == 1) {
+        emit(i, acc, ls);
+      } else {
+        mine[i] = acc;
+        if (d % (32 * NS) == 0) {
+          mine[R * HD + pr] = top;
+          mine[R * HD + P + pr] = ls;
+        }
+      }
+    }
+    if (cluster == 1) return;
+    cluster_sync();
+    const int share = R * HD / cluster, rank = blockIdx.x % cluster;
+    for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += C::T) {
+      const int pr = i / HD * GV + i % HD / 32 / NS;
+      float ref[8], sum[8], val[8], top = -INFINITY, acc = 0.f, ls = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < cluster) {
+          ref[k] = ld_cluster(mine + R * HD + pr, k);
+          sum[k] = ld_cluster(mine + R * HD + P + pr, k);
+          val[k] = ld_cluster(mine + i, k);
+        }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < cluster) top = fmaxf(top, ref[k]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < cluster && ref[k] > -INFINITY) {
+          const float f = ex2(ref[k] - top);
+          acc += f * val[k];
+          ls += f * sum[k];
+        }
+      emit(i, acc, ls);
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+    return;
   }
   // bit 0: the warp's run ends inside a segment that began in it; bit 1: the CTA's begins inside one
   if (lane == 0) ends[warp] = goes_on | (warp == 0 && begun ? 2 : 0);
@@ -833,15 +944,38 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   }
 }
 
+// CTAs of a cluster for each segment, or 0 for equal runs of units.  The lengths
+// are on the device: what the host knows is how many positions the table holds.
+// Clusters win up to four units a warp (16/8 heads of 128, us, clusters and
+// runs: 1 x 4096 7.9 and 11.9, 33 ragged to 1024 10.7 and 15.0, 64 x 1024 22.4
+// and 27.8), runs behind that, the more the less equal the lengths are (33 ragged
+// to 4160: 29 and 19; 1 x 16384: 14.7 and 14.3).
+int use_clusters(const Q4AttnArgs& a, int rows, int warps) {
+  if (a.q_start) return 0;
+  const int64_t segments = static_cast<int64_t>(a.c.n_seq) * a.c.n_kv * ((a.n_heads / a.c.n_kv + rows - 1) / rows);
+  const int64_t units = (static_cast<int64_t>(a.c.table_stride) * a.c.page_size + kUnit - 1) / kUnit;
+  int x = 8;
+  while (x > 1 && segments * x > kCtas) x /= 2;
+  return segments <= 4 * kCtas && units <= 4 * x * warps ? x : 0;
+}
+
 template <int HD, int NT, int GV>
 cudaError_t launch(const Q4AttnArgs& a, cudaStream_t st) {
+  const int clusters = use_clusters(a, Cfg<HD, NT, GV>::R, Cfg<HD, NT, GV>::W);
   using C = Cfg<HD, NT, GV>;
   const size_t plan_b = plan_bytes(a.c.n_seq), smem = C::smem + plan_b;
-  static unsigned long long done = 0;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_attention_q4<HD, NT, GV>),
+  static unsigned long long done = 0, done_cl = 0;
+  if (clusters) {
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_attention_q4<HD, NT, GV, true>), C::smem, &done_cl);
+    if (e != cudaSuccess) return e;
+    const int segments = a.c.n_seq * a.c.n_kv * ((a.n_heads / a.c.n_kv + C::R - 1) / C::R);
+    return launch_pdl_clusters(k_attention_q4<HD, NT, GV, true>, clusters, dim3(segments * clusters), C::T, C::smem, st, a,
+                               clusters);
+  }
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_attention_q4<HD, NT, GV, false>),
                              C::smem + plan_bytes(kQ4MaxSeqs), &done);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k_attention_q4<HD, NT, GV>, dim3(kCtas), C::T, smem, st, a);
+  e = launch_pdl(k_attention_q4<HD, NT, GV, false>, dim3(kCtas), C::T, smem, st, a, 0);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_attention_q4_join<HD, NT, GV>, dim3(kCtas * C::B), kCombine, plan_b, st, a);
 }
