@@ -45,6 +45,18 @@ __device__ __forceinline__ float round_f16(float x) { return __half2float(__floa
 // 2^e as f32, e in -126 .. 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
+// A float of another CTA of the cluster, at the address that it has in this one.
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+  float v;
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 constexpr int kQ4Block = 16;  // positions per cache block
 
 // Bytes of one cache block (16 positions of one head): K codes, K scales, V codes, V scales.

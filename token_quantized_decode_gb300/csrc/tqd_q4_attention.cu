@@ -251,18 +251,6 @@ struct Shared {
   int n_rows, row0, head0;  // rows of the tile, its first row, first query head of the kv head
 };
 
-// A float of another CTA of the cluster, at the address that it has in this one.
-__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
-  float v;
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // CL: clusters of `cluster` CTAs, one a segment; else equal runs of units.
 template <int HD, int NT, int GV, bool CL>
 __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnArgs a, int cluster) {

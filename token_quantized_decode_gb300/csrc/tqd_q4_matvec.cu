@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t r
 }
 
 constexpr int kMvWarps = 8;
+constexpr int kMvCtas = 304;  // two per SM
 constexpr int kMvThreads = 32 * kMvWarps;
 // Strips of a stage, and stages of a warp's ring.
 __host__ __device__ constexpr int mv_chunk(int nt) { return nt == 4 ? 1 : 2; }
@@ -60,6 +61,7 @@ struct MatvecQ4Args {
   int row_tiles, strips;
   int slab;              // strips whose x is staged at a time
   int wk;                // warps that share a row tile's strips (1, 2, 4, 8)
+  int cluster;           // CTAs of a cluster, each with a part of the strips (1, 2, 4, 8)
   int per_slot;          // row tiles of one warp (of wk warps)
 };
 
@@ -79,9 +81,11 @@ struct MatvecQ4Args {
 // HBM bounds it: 4.5 bits a weight.  A weight costs 0.6 instructions of
 // unpacking and 1/4 MMA lane, where unpacking to f32 and a packed FMA cost over 2;
 // up to 16 vectors share them.  Each warp streams its row tiles' strips, one
-// contiguous run, through a ring of bulk copies of its own; where there are too
-// few row tiles for the GPU's warps, 2, 4 or 8 warps share a tile's strips and
-// add their sums in shared memory.
+// contiguous run, through a ring of bulk copies of its own.  Where there are too
+// few row tiles for the GPU's warps, or staging the vectors would take too long, a cluster
+// of 2, 4 or 8 CTAs shares the strips (so each stages a part of the vectors) and adds
+// its sums through distributed shared memory; with less than 8 row tiles the
+// warps of a CTA share them too.
 template <int NT, bool ONE>
 __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   constexpr int NC = ONE ? 2 : 8 * NT;  // staged columns: high and low part of each vector
@@ -98,12 +102,15 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r8 = lane >> 2, c = lane & 3;
   const int wk = warp % a.wk;
-  const int slot = blockIdx.x * (kMvWarps / a.wk) + warp / a.wk;
+  const int rank = blockIdx.x % a.cluster, slots = kMvWarps / a.wk;
+  const int cta0 = blockIdx.x / a.cluster * slots;  // the cluster's first slot
+  const int slot = cta0 + warp / a.wk;
+  const int cs0 = a.strips * rank / a.cluster, cs1 = a.strips * (rank + 1) / a.cluster;  // the CTA's strips
   const int tile0 = slot * a.per_slot, tile1 = min(tile0 + a.per_slot, a.row_tiles);
   const int v0 = blockIdx.y * 16, nv = min(a.n - v0, ONE ? 1 : 4 * NT);
   const float* x = a.x + v0 * a.xs;
   float* y = a.y + v0 * a.ys;
-  const int slabs = (a.strips + a.slab - 1) / a.slab;
+  const int slabs = ((a.strips + a.cluster - 1) / a.cluster + a.slab - 1) / a.slab;  // the same in every CTA
 
   uint64_t* bar = bars + warp * kMvStages;
   unsigned char* my_ring = ring + warp * kMvStages * kStage;
@@ -115,7 +122,7 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   pdl_launch_dependents();
   // this warp's strips of a slab
   auto share = [&](int slab, int& b, int& e) {
-    const int s0 = slab * a.slab, n = min(a.slab, a.strips - s0);
+    const int s0 = cs0 + slab * a.slab, n = max(min(a.slab, cs1 - s0), 0);
     b = s0 + n * wk / a.wk;
     e = s0 + n * (wk + 1) / a.wk;
   };
@@ -155,10 +162,10 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
   for (int slab = 0; slab < slabs; ++slab) {
     // ---- the slab's part of the vectors
-    const int g0 = slab * a.slab * 4, ng = min(a.slab, a.strips - slab * a.slab) * 4;
+    const int g0 = (cs0 + slab * a.slab) * 4, ng = max(min(a.slab * 4, cs1 * 4 - g0), 0);
     if (slab) __syncthreads();
     const int octs = ng * 4;
-    const int real = min(a.groups - g0, ng) * 4;
+    const int real = max(min(a.groups - g0, ng), 0) * 4;
     // Octets of columns: kBatch of them loaded before the first is used.  (Whole
     // warps: octs is a multiple of 16, and a group's four octets are neighbouring lanes.)
     constexpr int kBatch = ONE ? 2 : 4;
@@ -289,37 +296,46 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = __int_as_float(0x7FC00000);
       }
-      if (a.wk > 1) {
-        float* mine = red + warp * 2 * NT * 32 + lane;
+      auto store = [&](int row_tile, int t, int h, int l, float sum) {  // lane l's sum for vectors t * 4 .. of half h
+        const int v = t * 4 + (l & 3), r = row_tile * 16 + h * 8 + (l >> 2);
+        if (v >= nv || r >= a.rows || row_tile >= a.row_tiles) return;
+        float* p = y + v * a.ys + r;
+        *p = slab ? *p + sum : sum;
+      };
+      if (a.wk * a.cluster == 1) {
+        if (tile < tile1)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          mine[(2 * t) * 32] = acc[t][0];
-          mine[(2 * t + 1) * 32] = acc[t][1];
-        }
-        __syncthreads();
-        if (wk == 0)
-          for (int j = 1; j < a.wk; ++j)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              acc[t][0] += mine[(j * NT + t) * 64];
-              acc[t][1] += mine[(j * NT + t) * 64 + 32];
-            }
-        __syncthreads();
-      }
-      if (tile < tile1 && wk == 0) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int v = t * 4 + c;
-          if (v >= nv) continue;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = tile * 16 + h * 8 + r8;
-            if (r >= a.rows) continue;
-            float* p = y + v * a.ys + r;
-            *p = slab ? *p + acc[t][h] : acc[t][h];
+          for (int t = 0; t < NT; ++t) {
+            store(tile, t, 0, lane, acc[t][0]);
+            store(tile, t, 1, lane, acc[t][1]);
           }
-        }
+        continue;
       }
+      float* mine = red + warp * 2 * NT * 32 + lane;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mine[(2 * t) * 32] = acc[t][0];
+        mine[(2 * t + 1) * 32] = acc[t][1];
+      }
+      if (a.cluster == 1)
+        __syncthreads();
+      else
+        cluster_sync();
+      // the sums of each slot's tile: 64 NT values, dealt over the cluster's threads
+      for (int i = rank * kMvThreads + threadIdx.x; i < slots * 2 * NT * 32; i += a.cluster * kMvThreads) {
+        const int sl = i / (2 * NT * 32), e2 = i % (2 * NT * 32);
+        const float* from = red + sl * a.wk * 2 * NT * 32 + e2;
+        float sum = 0.f;
+        for (int q = 0; q < a.cluster; ++q)
+          for (int j = 0; j < a.wk; ++j)
+            sum += a.cluster == 1 ? from[j * 2 * NT * 32] : ld_cluster(from + j * 2 * NT * 32, q);
+        const int row_tile = (cta0 + sl) * a.per_slot + k;
+        store(row_tile, e2 / 64, e2 / 32 % 2, e2 % 32, sum);
+      }
+      if (a.cluster == 1)
+        __syncthreads();
+      else
+        cluster_sync();
     }
   }
 }
@@ -328,21 +344,36 @@ template <int NT, bool ONE>
 cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   constexpr int NC = ONE ? 2 : 8 * NT;
   constexpr int most = (kMvSmem - mv_fixed_smem(NT)) / mv_strip_smem(NC);  // strips whose vectors fit
-  const int slabs = (a.strips + most - 1) / most;
-  a.slab = (a.strips + slabs - 1) / slabs;
-  const size_t smem = static_cast<size_t>(mv_fixed_smem(NT)) + static_cast<size_t>(a.slab) * mv_strip_smem(NC);
-  // a warp a row tile where that keeps eight warps on each SM busy, else 2, 4 or 8
+  // With less than eight row tiles the warps of a CTA share a tile's strips.  The
+  // cluster is the one that costs a warp the fewest instructions: about 50 for
+  // each octet of columns that it stages, 110 + 60 NT a strip, 500 to add a row tile's
+  // sums through distributed shared memory.
   a.wk = 1;
-  while (a.wk < kMvWarps && static_cast<int64_t>(a.row_tiles) * a.wk < 152 * kMvWarps && a.wk * 2 <= a.slab) a.wk *= 2;
+  while (a.wk < kMvWarps && a.row_tiles * a.wk < kMvWarps && a.wk * 2 <= a.strips) a.wk *= 2;
+  const int sweep = a.n < 16 ? a.n : 16, ctas = (a.row_tiles * a.wk + kMvWarps - 1) / kMvWarps;
+  int64_t least = 0;
+  for (int x = 1; x <= 8 && x * a.wk <= a.strips; x *= 2) {
+    const int sweeps = (a.n + 15) / 16, room = kMvCtas / (x * sweeps);  // (sweeps run side by side; at most 4)
+    const int64_t rounds = (ctas + room - 1) / room, each = (a.strips + x * a.wk - 1) / (x * a.wk);
+    const int64_t cost = static_cast<int64_t>(sweep) * a.strips * 6 / x + rounds * (each * (110 + 60 * NT) + (x > 1 ? 500 : 0));
+    if (x == 1 || cost < least) {
+      least = cost;
+      a.cluster = x;
+    }
+  }
+  const int strips = (a.strips + a.cluster - 1) / a.cluster, slabs = (strips + most - 1) / most;
+  a.slab = (strips + slabs - 1) / slabs;
+  const size_t smem = static_cast<size_t>(mv_fixed_smem(NT)) + static_cast<size_t>(a.slab) * mv_strip_smem(NC);
   const int slots = kMvWarps / a.wk;
   int blocks = (a.row_tiles + slots - 1) / slots;
-  if (blocks > 304) blocks = 304;
+  if (blocks > kMvCtas / a.cluster) blocks = kMvCtas / a.cluster;
   a.per_slot = (a.row_tiles + blocks * slots - 1) / (blocks * slots);
   blocks = (a.row_tiles + a.per_slot * slots - 1) / (a.per_slot * slots);
   static unsigned long long done = 0;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_q4_matvec<NT, ONE>), kMvSmem, &done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_q4_matvec<NT, ONE>, dim3(blocks, (a.n + 15) / 16), kMvThreads, smem, st, a);
+  return launch_pdl_clusters(k_q4_matvec<NT, ONE>, a.cluster, dim3(blocks * a.cluster, (a.n + 15) / 16), kMvThreads, smem,
+                             st, a);
 }
 
 }  // namespace
