@@ -63,11 +63,14 @@ struct Cfg {
   static constexpr int P = 4 * NT;        // column pairs
   static constexpr int R = P / GV;        // query rows of a tile
   static constexpr int B = R == 1 ? 1 : 2;  // blocks that join a run
-  static constexpr int W = NT == 1 ? 8 : 6;  // warps: what the registers leave room for twice an SM
+  // Warps: what the registers leave room for twice an SM.  (Eight warps and 128
+  // registers spill where a warp keeps four groups' sums of 128 elements: 131072
+  // positions of 32/8 heads took 51 us so, 45 with six.)
+  static constexpr int W = NT == 1 && (HD == 64 || GV > 1) ? 8 : 6;
   static constexpr int T = 32 * W;
   static constexpr int BB = q4_block_bytes(HD);
   static constexpr int JB = NT == 1 ? 2 : 1;  // blocks of a unit taken at once: two where the registers hold them
-  static constexpr int ST = HD == 64 ? 4 : NT == 1 ? 2 : 3;  // stages (units) of a warp's ring
+  static constexpr int ST = HD == 64 ? 4 : W == 8 ? 2 : 3;  // stages (units) of a warp's ring
   static constexpr int LD = HD + 8;       // floats of a row in the merge buffer
   static constexpr int PART = R * LD + 2 * P;  // floats of a warp's partial result
   static constexpr size_t smem = static_cast<size_t>(W) * ST * (2 * BB + 16) + static_cast<size_t>(W) * PART * 4;
@@ -591,10 +594,10 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
         }
       }
 
+      // p * scale as column operands
+      uint32_t pb[JB][NT][NS][2];
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
-        // p * scale as column operands
-        uint32_t pb[NT][NS][2];
+      for (int j = 0; j < JB; ++j)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const float p0 = ex2(sc[t][2 * j] - ref[t]), p1 = ex2(sc[t][2 * j + 1] - ref[t]);
@@ -603,28 +606,36 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           for (int k = 0; k < NS; ++k) {
             float w0 = p0 * vs[2 * j][k], w1 = p1 * vs[2 * j + 1][k];
             if (masked) {  // a NaN scale of a position that this row does not see
-              if (t0 + j * kQ4Block + b0 >= seen[t]) w0 = 0.f;
-              if (t0 + j * kQ4Block + b1 >= seen[t]) w1 = 0.f;
+              if (t0 + j * kQ4Block + b0 >= seen[t] || (bad >> j & 1)) w0 = 0.f;
+              if (t0 + j * kQ4Block + b1 >= seen[t] || (bad >> j & 1)) w1 = 0.f;
             }
-            pb[t][k][0] = transpose_f16(split_f16(w0));
-            pb[t][k][1] = transpose_f16(split_f16(w1));
+            pb[j][t][k][0] = transpose_f16(split_f16(w0));
+            pb[j][t][k][1] = transpose_f16(split_f16(w1));
           }
         }
-        // sums of V
-        const unsigned char* vr = from + j * BB + q4_v_off(HD) + c * 128 + r * 16;
-        const uint4 v0 = *reinterpret_cast<const uint4*>(vr);
-        [[maybe_unused]] uint4 v1 = v0;
-        if constexpr (HD == 128) v1 = *reinterpret_cast<const uint4*>(vr + 512);
+      // Sums of V: those of the blocks at hand by MMA, to the running ones by
+      // rounded adds (the MMA truncates: 100 in a row lose 2e-6 of a long average).
+      uint4 v0[JB];
+      [[maybe_unused]] uint4 v1[JB];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+      for (int j = 0; j < JB; ++j) {
+        const unsigned char* vr = from + j * BB + q4_v_off(HD) + c * 128 + r * 16;
+        v0[j] = *reinterpret_cast<const uint4*>(vr);
+        if constexpr (HD == 128) v1[j] = *reinterpret_cast<const uint4*>(vr + 512);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        float d[NT][2][4];
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
           const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
           uint32_t x0, x1;
           if constexpr (HD == 128) {
-            x0 = __byte_perm(g < 2 ? v0.x : v0.y, g < 2 ? v0.z : v0.w, sel);
-            x1 = __byte_perm(g < 2 ? v1.x : v1.y, g < 2 ? v1.z : v1.w, sel);
+            x0 = __byte_perm(g < 2 ? v0[j].x : v0[j].y, g < 2 ? v0[j].z : v0[j].w, sel);
+            x1 = __byte_perm(g < 2 ? v1[j].x : v1[j].y, g < 2 ? v1[j].z : v1[j].w, sel);
           } else {
-            x0 = __byte_perm(v0.x, v0.y, sel);
-            x1 = __byte_perm(v0.z, v0.w, sel);
+            x0 = __byte_perm(v0[j].x, v0[j].y, sel);
+            x1 = __byte_perm(v0[j].z, v0[j].w, sel);
           }
           const uint32_t a0[4] = {unpack.low(x0), unpack.high(x0), unpack.low(x1), unpack.high(x1)};
           x0 >>= 8;
@@ -632,10 +643,23 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           const uint32_t a1[4] = {unpack.low(x0), unpack.high(x0), unpack.low(x1), unpack.high(x1)};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma_f16(o[t][2 * g], a0, pb[t][g % NS][0], pb[t][g % NS][1]);
-            mma_f16(o[t][2 * g + 1], a1, pb[t][g % NS][0], pb[t][g % NS][1]);
+            const uint32_t q0 = pb[j][t][g % NS][0], q1 = pb[j][t][g % NS][1];
+            if (j == 0) {
+              mma_f16(d[t][0], a0, q0, q1, 0.f, 0.f, 0.f, 0.f);
+              mma_f16(d[t][1], a1, q0, q1, 0.f, 0.f, 0.f, 0.f);
+            } else {
+              mma_f16(d[t][0], a0, q0, q1);
+              mma_f16(d[t][1], a1, q0, q1);
+            }
           }
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[t][2 * g][i] += d[t][0][i];
+            o[t][2 * g + 1][i] += d[t][1][i];
+          }
       }
     };
     for (; rel < rel_end; ++rel) {
