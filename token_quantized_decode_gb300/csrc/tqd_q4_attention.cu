@@ -63,10 +63,10 @@ struct Cfg {
   static constexpr int P = 4 * NT;        // column pairs
   static constexpr int R = P / GV;        // query rows of a tile
   static constexpr int B = R == 1 ? 1 : 2;  // blocks that join a run
-  // Warps: what the registers leave room for twice an SM.  (Eight warps and 128
-  // registers spill where a warp keeps four groups' sums of 128 elements: 131072
-  // positions of 32/8 heads took 51 us so, 45 with six.)
-  static constexpr int W = NT == 1 && (HD == 64 || GV > 1) ? 8 : 6;
+  // Warps: what the registers leave room for twice an SM.  Spills cost more than
+  // warps: 131072 positions of 32/8 heads of 128 took 51 us with eight warps of 128
+  // registers, 45 with six of 168; of 64/8 heads 101 us with six, 66 with four of 255.
+  static constexpr int W = HD == 64 ? (NT == 1 ? 8 : 6) : NT == 2 ? 4 : GV == 1 ? 6 : 8;
   static constexpr int T = 32 * W;
   static constexpr int BB = q4_block_bytes(HD);
   static constexpr int JB = NT == 1 ? 2 : 1;  // blocks of a unit taken at once: two where the registers hold them
