@@ -385,6 +385,32 @@ def test_attention_small_values_next_to_large_ones(ops):
     check_attention(attend(ops, host.device(ops), q, [n]), q, [K], [V], [n], [1], hd)
 
 
+def test_attention_scales_of_either_sign(ops):
+    """Pages that a program wrote itself: any finite f16 is a scale, and a negative one can be the largest by far."""
+    rng = np.random.default_rng(27)
+    n_kv, n = 2, 150
+    for hd, heads in ((64, 2), (128, 4), (128, 8), (64, 16)):
+        host = Host(rng, 1, n_kv, hd, 16, n)
+        K, V = [], []
+        for p in range(n):
+            kc, ks = q4.quantise_groups(rng.normal(size=(n_kv, hd)))
+            vc, vs = q4.quantise_groups(rng.normal(size=(n_kv, hd)) * 2.0 ** (p // 8))
+            ks, vs = -ks if p % 3 == 0 else ks, -vs if p % 8 else vs
+            for h in range(n_kv):
+                q4.store_row(host.pages, host.table[0, p // 16], h, p % 16, 16, kc[h], ks[h], vc[h], vs[h])
+            K.append(q4.group_values(kc, ks))
+            V.append(q4.group_values(vc, vs))
+        for scale in (1.0, -1.0):
+            q = rng.normal(size=(1, heads * hd)).astype(np.float32) * np.float32(scale)
+            cache = host.device(ops)
+            for visible in (40, 136):
+                check_attention(attend(ops, cache, q, [visible]), q, [np.array(K)], [np.array(V)], [visible], [1], hd)
+            # from 2^18 * 1.75 a group's scale passes f16 and stands for NaN
+            got = attend(ops, cache, q, [n]).reshape(heads, hd)
+            want = q4.attention(q[0].reshape(heads, hd).astype(np.float64), np.array(K), np.array(V), n)
+            assert np.any(np.isnan(want)) and np.all(np.isnan(got[np.isnan(want)]))
+
+
 def test_attention_extreme_queries(ops):
     """Queries of any f32 size: tiny ones weigh all positions alike, huge ones pick the largest score."""
     rng = np.random.default_rng(13)

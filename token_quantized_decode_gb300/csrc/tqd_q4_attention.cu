@@ -478,13 +478,15 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           const uint2 w = *reinterpret_cast<const uint2*>(p);
           const __half2 x = *reinterpret_cast<const __half2*>(&w.x), y = *reinterpret_cast<const __half2*>(&w.y);
           d[0] = __low2float(x); d[1] = __high2float(x); d[2] = __low2float(y); d[3] = __high2float(y);
-          top = __hmax2(x, y);
+          top = __hmax2(__habs2(x), __habs2(y));
         } else if constexpr (NS == 2) {
-          top = *reinterpret_cast<const __half2*>(p);
-          d[0] = __low2float(top); d[1] = __high2float(top);
+          const __half2 x = *reinterpret_cast<const __half2*>(p);
+          d[0] = __low2float(x); d[1] = __high2float(x);
+          top = __habs2(x);
         } else {
-          top = __half2half2(*reinterpret_cast<const __half*>(p));
-          d[0] = __low2float(top);
+          const __half2 x = __half2half2(*reinterpret_cast<const __half*>(p));
+          d[0] = __low2float(x);
+          top = __habs2(x);
         }
         return top;
       };
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
 #pragma unroll
           for (int k = 0; k < NS; ++k) {
             if (t0 + (i >> 1) * kQ4Block + (i & 1 ? b1 : b0) >= most || (bad >> (i >> 1) & 1)) vs[i][k] = 0.f;
-            bs = fmaxf(bs, vs[i][k]);
+            bs = fmaxf(bs, fabsf(vs[i][k]));
           }
       }
 
