@@ -370,20 +370,10 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
     ++issued;
     issue_st = issue_st + 1 == ST ? 0 : issue_st + 1;
   };
-  for (int i = 0; i < ST - 1; ++i) issue();
-
-  const Unpack unpack;
-  int rel = 0, st = 0, phase = 0;  // the warp's next unit, counted from u0, and its stage
-  bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
-  int goes_on = 0;
-  bool begun = false;
-  unsigned long long u = u0;
-  int s = cl_s;
-  if constexpr (!CL) s = u < u1 ? plan.seq_of(u) : 0;
-  while (u < u1) {
-    // ---- the segment of unit u: one (sequence, kv head, tile of rows)
-    unsigned long long seg0 = 0, seg1 = c1;
-    int kvh = cl_kvh, rt = cl_rt, rows = plan.G, min_seen = cl_len;
+  // ---- the segment of unit u: one (sequence, kv head, tile of rows)
+  unsigned long long u = u0, seg0 = 0, seg1 = c1;
+  int s = cl_s, kvh = cl_kvh, rt = cl_rt, rows = plan.G, min_seen = cl_len, n_rows = 0;
+  auto segment = [&] {
     if constexpr (!CL) {
       while (plan.pre[s + 1] <= u) ++s;
       const int nb = plan.units(s);
@@ -394,23 +384,47 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       rows = plan.nq[s] * plan.G;
       min_seen = plan.seen(s, rt * R);
     }
+    n_rows = min(R, rows - rt * R);
+  };
+  // A lane's operand column is a pair's high or low part; its elements of query row
+  // (rows past the last repeat it) t:
+  const int pair = lane >> 3, part = (lane >> 2) & 1;
+  auto row_of = [&](int t) {
+    const int row = rt * R + min(t * 4 + pair / GV, n_rows - 1);
+    return a.q + (q_first(a, s) + plan.query(row)) * a.q_stride +
+           static_cast<int64_t>(kvh * plan.G + (row - plan.query(row) * plan.G)) * HD + pair % GV * NS * 32 + 8 * c;
+  };
+  if (u < u1) {  // on their way while the first units' pages are looked up and their copies issued
+    if constexpr (!CL) s = plan.seq_of(u);
+    segment();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float* q = row_of(t);
+#pragma unroll
+      for (int k = 0; k < NS; ++k) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + k * 32));
+    }
+  }
+  for (int i = 0; i < ST - 1; ++i) issue();
+
+  const Unpack unpack;
+  int rel = 0, st = 0, phase = 0;  // the warp's next unit, counted from u0, and its stage
+  bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
+  int goes_on = 0;
+  bool begun = false;
+  while (u < u1) {
     const unsigned long long uend = min(seg1, u1);
     const int rel_end = static_cast<int>(uend - u0);
     const int unit0 = static_cast<int>(static_cast<long long>(u0 - seg0));  // unit rel is the segment's rel + unit0
-    const int n_rows = min(R, rows - rt * R);
 
     // ---- the query rows as column operands
     int seen[NT];
     uint32_t qb[NT][NG][2][2];
     float zh[NT][NS], zl[NT][NS], fac[NT][NS];
     {
-      const int pair = lane >> 3, part = (lane >> 2) & 1;  // this lane's operand column: pair's high or low part
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int row = rt * R + min(t * 4 + pair / GV, n_rows - 1);  // rows past the last repeat it
+        const float* q = row_of(t);
         seen[t] = CL ? cl_len : plan.seen(s, rt * R + min(t * 4 + h, n_rows - 1));
-        const float* q = a.q + (q_first(a, s) + plan.query(row)) * a.q_stride +
-                         static_cast<int64_t>(kvh * plan.G + (row - plan.query(row) * plan.G)) * HD;
         // A power of two for each group of 32 brings its largest element to 2^10
         // .. 2^11; the high part is then the nearest whole number, so that a
         // group's sum of high parts times codes is exact in the tensor cores' f32,
@@ -422,7 +436,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           float x[8], m = 0.f, z = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            x[i] = q[((pair % GV) * NS + k) * 32 + 8 * c + i] * a.scale;
+            x[i] = q[k * 32 + i] * a.scale;
             m = fmaxf(m, fabsf(x[i]));
           }
           m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
@@ -431,8 +445,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           const float f = pow2(10 - e);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            x[i] *= f;
-            x[i] = part ? round_f16(x[i] - rintf(x[i])) : rintf(x[i]);
+            const float y = x[i] * f;
+            x[i] = part ? round_f16(y - rintf(y)) : rintf(y);
             z += x[i];  // (counts what the operand holds)
           }
           z += __shfl_xor_sync(0xFFFFFFFFu, z, 1);
@@ -724,10 +738,10 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       }
       goes_on = u0 <= seg0;  // (else it is the run's first, begun before it)
       begun |= u == c0 && seg0 < c0;
-      float* part = !CL && u0 <= seg0 ? reinterpret_cast<float*>(my_ring) : parts + warp * PART;
+      float* to = !CL && u0 <= seg0 ? reinterpret_cast<float*>(my_ring) : parts + warp * PART;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float* mo = part + (t * 4 + h) * LD + r;
+        float* mo = to + (t * 4 + h) * LD + r;
 #pragma unroll
         for (int g = 0; g < NG; ++g)
           if (g / NS == gv) {
@@ -739,12 +753,13 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
             }
           }
         if (r == 0) {
-          part[R * LD + t * 4 + c] = M[t] == -INFINITY && l[t] == 0.f ? -INFINITY : ref[t];
-          part[R * LD + P + t * 4 + c] = l[t];
+          to[R * LD + t * 4 + c] = M[t] == -INFINITY && l[t] == 0.f ? -INFINITY : ref[t];
+          to[R * LD + P + t * 4 + c] = l[t];
         }
       }
     }
     u = uend;
+    if (!CL && u < u1) segment();
   }
   if constexpr (CL) {
     // ---- the cluster's parts into one: the CTA's warps' first, in its ring
@@ -820,40 +835,52 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
 
   // ---- segments that several warps share, or that another CTA shares: the one
   // that began before the CTA's run, and those that begin in a warp's run and go on behind it
-  for (int w = -1; w < W; ++w) {
+  // (four elements a thread, the segments dealt over the threads left)
+  constexpr int kQuads = R * HD / 4, kDeal = C::T / kQuads > 1 ? C::T / kQuads : 1;
+  for (int w = -1 + static_cast<int>(threadIdx.x) / kQuads % kDeal; w < W; w += kDeal) {
     const int w_ = max(w, 0);
-    const unsigned long long w0 = c0 + w_ * plan.per, w1 = min(w0 + plan.per, c1);
+    const unsigned long long w0 = c0 + w_ * plan.per;
     if (w0 >= c1) break;
-    const Shared sh = shared[w < 0 ? W : w];
     if (w < 0 ? !first_shared : !(last_shared >> w & 1)) continue;
+    const Shared sh = shared[w < 0 ? W : w];
     const int last = static_cast<int>(udiv(min(sh.seg1, c1) - 1 - c0, static_cast<unsigned>(plan.per)));
     const bool whole = c0 <= sh.seg0 && sh.seg1 <= c1;
     const float* head = w >= 0 ? reinterpret_cast<const float*>(ring + w * ST * 2 * BB) : parts;
     // slot 0: a segment of the CTA's first unit; slot 1: one that begins later
     float* to = static_cast<float*>(a.scratch) +
                 (static_cast<size_t>(blockIdx.x) * 2 + (sh.seg0 <= c0 ? 0 : 1)) * partial_floats(HD);
-    for (int i = threadIdx.x; i < R * HD; i += C::T) {
+    for (int i = (kDeal > 1 ? threadIdx.x % kQuads : threadIdx.x) * 4; i < R * HD; i += (kDeal > 1 ? kQuads : C::T) * 4) {
       const int hr = i / HD, d = i % HD, pr = hr * GV + d / 32 / NS;
       float top = head[R * LD + pr];
       for (int k = w_ + 1; k <= last; ++k) top = fmaxf(top, parts[k * PART + R * LD + pr]);
-      float acc = 0.f, ls = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ls = 0.f;
       for (int k = w_; k <= last; ++k) {
-        const float* part = k == w_ ? head : parts + k * PART;
-        const float pf = part[R * LD + pr];
+        const float* from = k == w_ ? head : parts + k * PART;
+        const float pf = from[R * LD + pr];
+        const float4 v = *reinterpret_cast<const float4*>(from + hr * LD + d);
+        const float sum = from[R * LD + P + pr];
         if (pf > -INFINITY) {
           const float f = ex2(pf - top);
-          acc += f * part[hr * LD + d];
-          ls += f * part[R * LD + P + pr];
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
+          ls += f * sum;
         }
       }
       if (whole) {
         if (hr < sh.n_rows) {
           const int row = sh.row0 + hr;
-          a.out[(sh.token + plan.query(row)) * a.out_stride + static_cast<int64_t>(sh.head0 + (row - plan.query(row) * plan.G)) * HD + d] =
-              ls == 0.f ? 0.f : acc / ls;
+          float* out = a.out + (sh.token + plan.query(row)) * a.out_stride +
+                       static_cast<int64_t>(sh.head0 + (row - plan.query(row) * plan.G)) * HD + d;
+          out[0] = ls == 0.f ? 0.f : acc.x / ls;
+          out[1] = ls == 0.f ? 0.f : acc.y / ls;
+          out[2] = ls == 0.f ? 0.f : acc.z / ls;
+          out[3] = ls == 0.f ? 0.f : acc.w / ls;
         }
       } else {
-        to[i] = acc;
+        *reinterpret_cast<float4*>(to + i) = acc;
         if (d % (32 * NS) == 0) {
           to[8 * HD + pr] = top;
           to[8 * HD + 8 + pr] = ls;
@@ -902,15 +929,26 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp < PB) {  // a warp per column pair
     const int pr = row0 * GV + warp;
-    float ref = -INFINITY, ls = 0.f;
-    for (int k = lane; k < runs; k += 32) ref = fmaxf(ref, part(k)[8 * HD + pr]);
+    float ref = -INFINITY, ls = 0.f, refs[4], sums[4];  // (128 runs at once)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool on = lane + 32 * j < runs;
+      refs[j] = on ? part(lane + 32 * j)[8 * HD + pr] : -INFINITY;
+      sums[j] = on ? part(lane + 32 * j)[8 * HD + 8 + pr] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ref = fmaxf(ref, refs[j]);
+    for (int k = lane + 128; k < runs; k += 32) ref = fmaxf(ref, part(k)[8 * HD + pr]);
     ref = warp_max(ref);
-    for (int k = lane; k < runs; k += 32) {
-      const float pf = part(k)[8 * HD + pr];
+    auto weigh = [&](int k, float pf, float sum) {
       const float w = pf > -INFINITY ? ex2(pf - ref) : 0.f;
       wt[k * PB + warp] = w;
-      if (pf > -INFINITY) ls += w * part(k)[8 * HD + 8 + pr];
-    }
+      if (pf > -INFINITY) ls += w * sum;
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane + 32 * j < runs) weigh(lane + 32 * j, refs[j], sums[j]);
+    for (int k = lane + 128; k < runs; k += 32) weigh(k, part(k)[8 * HD + pr], part(k)[8 * HD + 8 + pr]);
     ls = warp_sum(ls);
     if (lane == 0) lsum[warp] = ls;
   }
