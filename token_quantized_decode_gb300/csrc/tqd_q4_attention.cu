@@ -87,6 +87,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two sums by one instruction.
+__device__ __forceinline__ void add_f32x2(float& x0, float& x1, float y0, float y1) {
+  asm("{\n.reg .b64 x, y;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %3};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1));
+}
+
 // x as two f16 parts in one word: the leading 11 bits low, the rest high.
 __device__ __forceinline__ uint32_t split_f16(float x) {
   const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
@@ -672,9 +679,9 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[t][2 * g][i] += d[t][0][i];
-            o[t][2 * g + 1][i] += d[t][1][i];
+          for (int i = 0; i < 4; i += 2) {
+            add_f32x2(o[t][2 * g][i], o[t][2 * g][i + 1], d[t][0][i], d[t][0][i + 1]);
+            add_f32x2(o[t][2 * g + 1][i], o[t][2 * g + 1][i + 1], d[t][1][i], d[t][1][i + 1]);
           }
       }
     };
