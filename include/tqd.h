@@ -532,7 +532,8 @@ size_t tqd_q4_0_matrix_bytes(int64_t rows, int64_t cols);
  * f32 accuracy: the weights are exact, each 32 elements of x are carried to 22
  * bits below their largest one's exponent (or finer), sums are f32.  A scale
  * that is NaN or infinite makes its row NaN (or infinite); an x with an
- * element that is NaN, infinite or of magnitude 2^113 or more gives NaN. */
+ * element that is NaN, infinite or of magnitude 2^113 or more gives NaN.  y may
+ * not overlap x. */
 int32_t tqd_op_q4_0_matvec(const uint8_t* w_tiles, int64_t rows, int64_t cols, const float* x, int32_t n,
                            int64_t x_stride, float* y, int64_t y_stride, void* stream);
 

