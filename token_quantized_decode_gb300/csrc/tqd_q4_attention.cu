@@ -28,8 +28,8 @@
 // (NT = 2) two column tiles share the unpacked cache.
 //
 // Split.  The unit is 32 positions of one segment: (sequence, kv head, tile of
-// query rows).  Units are laid end to end and each warp takes an equal run of
-// them, whatever the lengths, with a running softmax for each segment it meets.
+// query rows).  Units, and a few empty ones at each segment's beginning for what that
+// costs, are laid end to end and each warp takes an equal run of them, whatever the lengths, with a running softmax for each segment it meets.
 // A segment inside a warp's run is written out by the warp alone; the partial
 // results (ref, sum p, sum p v) of one that several warps of a CTA share are
 // joined in shared memory at the CTA's end, and those of one that several CTAs
@@ -41,15 +41,15 @@
 // parts through distributed shared memory: no plan and no second kernel, half the time of a
 // short call.
 //
-// What it measures (GB300, 1.9 GHz).  131072 positions of 32/8 heads of 128: 43 us for 151 MB
-// (3.5 TB/s; 22 us at a copy's rate), of which a warp's instructions take most: 740
+// What it measures (GB300, 1.9 GHz).  131072 positions of 32/8 heads of 128: 42 us for 151 MB
+// (3.6 TB/s; 22 us at a copy's rate), of which a warp's instructions take most: 740
 // for each unit of 32 positions and 4 rows, 40,000 a scheduler, 20 us at one a cycle;
 // the three warps that the registers leave a scheduler reach 0.7 of that between
-// the copies' arrival and the last unit (31 us), and 12 us are the beginning
-// (lengths, pages, queries: 6 us) and the two joins (3 and 3).  The same 12 us bound
-// short calls by runs; 1 x 575 positions by clusters take 6.6 us, a launch and one
-// chain of loads.  Prompts' tiles are bound by the same instructions (2048 queries
-// of 16/8 heads of 128: 281 us, 61 TFLOP/s).
+// the copies' arrival and the last unit, and 12 us are the beginning (lengths, pages,
+// queries: 6 us) and the two joins (3 and 3).  The same 12 us bound short calls by
+// runs (33 ragged to 4160 positions of 16/8 heads: 18.6 us); 1 x 575 positions by
+// clusters take 6.7 us, a launch and one chain of loads.  Prompts' tiles are
+// bound by the same instructions (2048 queries of 16/8 heads of 128: 288 us, 60 TFLOP/s).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -82,6 +82,13 @@ struct Cfg {
   static constexpr int BB = q4_block_bytes(HD);
   static constexpr int JB = NT == 1 ? 2 : 1;  // blocks of a unit taken at once: two where the registers hold them
   static constexpr int ST = HD == 64 ? 4 : W == 8 ? 2 : 3;  // stages (units) of a warp's ring
+  // Empty units that a segment begins with in the plan: about what a warp loses at a
+  // segment's beginning and end.  Without them the warps that meet two or more
+  // segments ended 5 us after the others: 40 ragged batches (20 of one query, 20 of 8
+  // to 400 a sequence) took 20.9 and 38.5 us in the geometric mean with none, 18.7
+  // and 34.8 with two, 19.3 and 34.0 with four (33 ragged to 4160: 22.4, 18.6, 20.0; 2048
+  // queries of 16/8 heads of 128, where all runs are long: 280, 285, 288).
+  static constexpr int LEAD = NT == 1 ? 2 : 4;
   static constexpr int LD = HD + 8;       // floats of a row in the merge buffer
   static constexpr int PART = R * LD + 2 * P;  // floats of a warp's partial result
   static constexpr size_t smem = static_cast<size_t>(W) * ST * (2 * BB + 16) + static_cast<size_t>(W) * PART * 4;
@@ -158,10 +165,11 @@ struct Plan {
   unsigned long long total, per;  // units, and units of one warp
   int n_seq, n_kv, G, rbits;      // 2^rbits rows of a tile
   int most;                       // positions of the page table, and a unit
+  int lead;                       // empty units that a segment begins with
 
-  // Units of a segment: its positions', and where they pass the page table one
-  // behind the table's end (which makes the rows that see it NaN).
-  __device__ int units(int s) const { return (min(len[s], most) + kUnit - 1) / kUnit; }
+  // Units of a segment: the empty ones, its positions', and where they pass the page
+  // table one behind the table's end (which makes the rows that see it NaN).
+  __device__ int units(int s) const { return len[s] > 0 ? lead + (min(len[s], most) + kUnit - 1) / kUnit : 0; }
   // (rows are at most tokens * heads, 2^30)
   __device__ int tiles(int s) const { return (nq[s] * G + (1 << rbits) - 1) >> rbits; }
   // Sequence of unit u < total.
@@ -198,7 +206,7 @@ __device__ __forceinline__ int q_first(const Q4AttnArgs& a, int s) { return a.q_
 
 // Build the plan: every thread of the block calls it; blocks of up to 32 warps.
 // Shared memory: pre [n_seq + 1] u64, len [n_seq], nq [n_seq], warp sums.
-__device__ Plan make_plan(const Q4AttnArgs& a, int R, int W, int ctas, unsigned char* smem) {
+__device__ Plan make_plan(const Q4AttnArgs& a, int R, int W, int lead, int ctas, unsigned char* smem) {
   __shared__ unsigned long long wsum[33];
   Plan p;
   const int n = a.c.n_seq, t = threadIdx.x, nt = blockDim.x;
@@ -209,6 +217,7 @@ __device__ Plan make_plan(const Q4AttnArgs& a, int R, int W, int ctas, unsigned 
   p.len = len;
   p.nq = nq;
   p.n_seq = n;
+  p.lead = lead;
   p.n_kv = a.c.n_kv;
   p.G = a.n_heads / a.c.n_kv;
   p.most = static_cast<int>(min(static_cast<long long>(a.c.table_stride) * a.c.page_size, 1ll << 30)) + kUnit;
@@ -316,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
     u0 = min((rank * W + warp) * plan.per, c1);
     u1 = min(u0 + plan.per, c1);
   } else {
-    plan = make_plan(a, R, W, gridDim.x, plan_mem);
+    plan = make_plan(a, R, W, C::LEAD, gridDim.x, plan_mem);
     // sequences without positions: their queries see nothing
     for (int s = blockIdx.x; s < plan.n_seq; s += gridDim.x) {
       if (plan.len[s] > 0) continue;
@@ -350,16 +359,16 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       const unsigned long long uq = u - plan.pre[s];
       const int nb = plan.units(s);
       const unsigned long long seg = udiv(uq, nb);
-      t0 = static_cast<int>(uq - seg * nb) * kUnit;
+      t0 = (static_cast<int>(uq - seg * nb) - C::LEAD) * kUnit;
       const int rt = plan.tile_of(s, seg, &kvh);
       seen = plan.seen(s, min(rt * R + R, plan.nq[s] * plan.G) - 1);
     }
     src0 = src1 = nullptr;
-    src_flag = t0 < seen ? 0 : 4;
+    src_flag = t0 >= 0 && t0 < seen ? 0 : 4;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = t0 + j * kQ4Block;
-      if (t >= seen) break;
+      if (t < 0 || t >= seen) break;
       const int slot = t / a.c.page_size;
       const int page = slot < a.c.table_stride ? a.c.table[static_cast<size_t>(s) * a.c.table_stride + slot] : -1;
       if (page < 0 || page >= a.c.n_pages) {
@@ -432,13 +441,13 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   while (u < u1) {
     const unsigned long long uend = min(seg1, u1);
     const int rel_end = static_cast<int>(uend - u0);
-    const int unit0 = static_cast<int>(static_cast<long long>(u0 - seg0));  // unit rel is the segment's rel + unit0
+    const int unit0 = static_cast<int>(static_cast<long long>(u0 - seg0)) - (CL ? 0 : C::LEAD);  // unit rel is the segment's rel + unit0
 
     // ---- the query rows as column operands
     int seen[NT];
     uint32_t qb[NT][NG][2][2];
     float zh[NT][NS], zl[NT][NS], fac[NT][NS];
-    {
+    if (CL || uend > seg0 + C::LEAD) {  // (else the run ends before the segment's first positions)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float* q = row_of(t);
@@ -916,7 +925,7 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
   constexpr int NS = C::NS, R = C::R, B = C::B, RB = R / B;
   extern __shared__ __align__(128) unsigned char sm[];
   const int run = blockIdx.x / B, row0 = blockIdx.x % B * RB;
-  const Plan plan = make_plan(a, R, C::W, kCtas, sm);
+  const Plan plan = make_plan(a, R, C::W, C::LEAD, kCtas, sm);
   const unsigned long long per = plan.per * C::W, u0 = run * per, u1 = u0 + per;
   bool mine = u1 < plan.total;  // something behind this run
   int s = 0, nb = 1;
@@ -1016,17 +1025,18 @@ __global__ void __launch_bounds__(kCombine) k_attention_q4_join(Q4AttnArgs a) {
 
 // CTAs of a cluster for each segment, or 0 for equal runs of units.  The lengths
 // are on the device: what the host knows is how many positions the table holds.
-// Clusters win up to four units a warp (16/8 heads of 128, us, clusters and
-// runs: 1 x 575 7.2 and 10.0, 1 x 4096 8.5 and 11.8, 33 ragged to 1024 11.1 and
-// 14.3, 64 x 1024 24.0 and 28.2), runs behind that, the more the less equal the
-// lengths are (1 x 16384 16.0 and 14.5, 33 ragged to 4160 33.6 and 21.5).
+// Clusters win up to about six units a warp (us, clusters and runs; 16/8 heads of 128:
+// 1 x 575 7.2 and 10.1, 1 x 8192 11.1 and 12.4, 33 ragged to 1024 11.2 and 14.2, 64 x
+// 1024 24.2 and 28.8; 32/8: 33 ragged to 1024 13.3 and 17.8), runs behind that, the
+// more the less equal the lengths are (16/8: 1 x 16384 16.1 and 14.6, 33 ragged to
+// 4160 33.4 and 18.7).
 int use_clusters(const Q4AttnArgs& a, int rows, int warps) {
   if (a.q_start) return 0;
   const int64_t segments = static_cast<int64_t>(a.c.n_seq) * a.c.n_kv * ((a.n_heads / a.c.n_kv + rows - 1) / rows);
   const int64_t units = (static_cast<int64_t>(a.c.table_stride) * a.c.page_size + kUnit - 1) / kUnit;
   int x = 8;
   while (x > 1 && segments * x > kCtas) x /= 2;
-  return segments <= 4 * kCtas && units <= 4 * x * warps ? x : 0;
+  return segments <= 4 * kCtas && units <= 6 * x * warps ? x : 0;
 }
 
 template <int HD, int NT, int GV>
