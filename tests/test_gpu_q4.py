@@ -129,6 +129,28 @@ def test_append_stores_the_oracles_bytes(ops, heads, n_kv, hd, page, gain):
     assert np.array_equal(v_out.cpu().numpy().astype(np.float64), V.reshape(n, -1))
 
 
+@pytest.mark.parametrize("heads,n_kv,hd", [(16, 8, 128), (15, 5, 64), (40, 2, 64), (7, 1, 128)])
+def test_append_rows_on_any_boundary(ops, heads, n_kv, hd):
+    """The same rows on 16-byte boundaries and off them: the same bytes and the same queries."""
+    rng = np.random.default_rng(heads + 2 * hd)
+    n, width = 37, (heads + 2 * n_kv) * hd
+    rows = rng.normal(size=(n, width)).astype(np.float32)
+    pos = np.arange(n)
+    table = rope_table(ops, hd, n)
+    got = []
+    for stride, start in ((width, 0), (width + 4, 4), (width + 1, 0), (width + 4, 1), (width + 2, 2)):
+        d = torch.zeros(n, stride + start, device="cuda")[:, start:start + width]
+        d.copy_(dev(rows))
+        host = Host(np.random.default_rng(1), 1, n_kv, hd, 16, n)
+        cache = host.device(ops)
+        q = d[:, :heads * hd]
+        ops.tqd_op_kv_append_q4(cache, d[:, heads * hd:(heads + n_kv) * hd], d[:, (heads + n_kv) * hd:], i32(pos),
+                                i32(np.zeros(n)), table, q, q)  # in place
+        got.append((cache.pages.cpu().numpy(), q.cpu().numpy()))
+    for pages, q in got[1:]:
+        assert np.array_equal(pages, got[0][0]) and np.array_equal(q, got[0][1])
+
+
 def test_append_codes_values_next_to_a_border_exactly(ops):
     """Elements at (k + 1/2) / 7 of the largest and one f32 step to either side, and rotated keys whose
     exact value lies within f32 rounding of such a border."""
@@ -522,6 +544,22 @@ def test_attention_strides_streams_graphs_and_a_shared_scratch(ops):
         check_attention(o1.cpu().numpy(), q.cpu().numpy(), host.K, host.V, new, [1] * 4, hd)
         check_attention(o2.cpu().numpy(), q3.cpu().numpy(), host.K, host.V, new, [3, 1, 0, 5], hd)
     assert torch.equal(o1, ref)
+
+
+@pytest.mark.parametrize("heads,n_kv,hd", [(16, 8, 128), (15, 5, 64), (4, 1, 128), (8, 1, 64), (2, 2, 128)])
+@pytest.mark.parametrize("many", [False, True])
+def test_attention_of_short_sequences_by_runs(ops, heads, n_kv, hd, many):
+    """A long page table over many sequences of a few positions, and one long one among them: a warp's run takes
+    several whole segments, ends before the positions of one, or begins at its first."""
+    rng = np.random.default_rng(heads + hd + many)
+    lens = [int(x) for x in rng.integers(0, 4, size=240 if many else 7)]
+    lens[3] = 700
+    lens[-1] = 33
+    host = Host(rng, len(lens), n_kv, hd, 16, max(lens), room=100000)
+    host.fill(rng, lens)
+    q = rng.normal(size=(len(lens), heads * hd)).astype(np.float32)
+    got = attend(ops, host.device(ops), q, lens)
+    check_attention(got, q, host.K, host.V, lens, [1] * len(lens), hd)
 
 
 def test_attention_many_sequences(ops):
