@@ -1,5 +1,5 @@
 """The 4-bit decode operators and the log probabilities in 64 bits (numpy),
-from the formulas and byte layouts that include/tqd.h states.  The checker of
+from the formulas and byte layouts that include/tqd.h states.  The oracle of
 the operator tests; the library never uses it."""
 from __future__ import annotations
 
