@@ -619,6 +619,19 @@ def test_q4_matvec(ops, rows, cols, n):
     check_matvec(y.cpu().numpy(), codes, d, x)
 
 
+@pytest.mark.parametrize("rows,cols", [(9713, 160), (9729, 32), (9744, 1184), (9760, 2080)])
+@pytest.mark.parametrize("n", [9, 16, 30])
+def test_q4_matvec_many_rows(ops, rows, cols, n):
+    """Row tiles in twos: an odd number of them, a last one in part, one strip and several slabs."""
+    rng = np.random.default_rng(rows + cols)
+    codes, d = q4_matrix(rng, rows, cols)
+    x = rng.normal(size=(n, cols)).astype(np.float32)
+    y = torch.full((n + 1, rows), 3.0, device="cuda")
+    ops.tqd_op_q4_0_matvec(tiles_of(ops, codes, d), rows, cols, dev(x), y[:n])
+    check_matvec(y[:n].cpu().numpy(), codes, d, x)
+    assert bool((y[n] == 3.0).all())
+
+
 @pytest.mark.parametrize("n", [17, 33, 64])
 def test_q4_matvec_more_vectors_than_a_sweep(ops, n):
     rng = np.random.default_rng(n)

@@ -43,13 +43,15 @@ __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t r
 constexpr int kMvWarps = 8;
 constexpr int kMvCtas = 304;  // two per SM
 constexpr int kMvThreads = 32 * kMvWarps;
-// Strips of a stage, and stages of a warp's ring.
+// Strips of a stage, and stages of a warp's ring (nt: tiles of 8 columns, rt: row tiles at once).
 __host__ __device__ constexpr int mv_chunk(int nt) { return nt == 4 ? 1 : 2; }
-__host__ __device__ constexpr int mv_stages(int nt) { return nt == 4 ? 3 : 2; }
+__host__ __device__ constexpr int mv_stages(int nt, int rt) { return nt == 4 && rt == 1 ? 3 : 2; }
 // Shared memory of a CTA: at most what lets two of them share an SM; the rings
 // and the warps' sums, then the staged vectors.
 constexpr int kMvSmem = 113 * 1024;
-constexpr int mv_fixed_smem(int nt) { return kMvWarps * (mv_stages(nt) * (mv_chunk(nt) * kQ4TileBytes + 8) + 2 * nt * 128); }
+constexpr int mv_fixed_smem(int nt, int rt) {
+  return kMvWarps * (mv_stages(nt, rt) * (rt * mv_chunk(nt) * kQ4TileBytes + 8) + rt * 2 * nt * 128);
+}
 constexpr int mv_strip_smem(int cols) { return 4 * (cols * 64 + cols / 2 * 20); }
 
 struct MatvecQ4Args {
@@ -58,7 +60,8 @@ struct MatvecQ4Args {
   float* y;
   int64_t xs, ys;
   int rows, groups, n;   // groups: columns / 32
-  int row_tiles, strips;
+  int row_tiles, strips; // of 16 rows, of 128 columns
+  int tiles;             // RT row tiles each
   int slab;              // strips whose x is staged at a time
   int wk;                // warps that share a row tile's strips (1, 2, 4, 8)
   int cluster;           // CTAs of a cluster, each with a part of the strips (1, 2, 4, 8)
@@ -82,21 +85,25 @@ struct MatvecQ4Args {
 // unpacking and 1/4 MMA lane, where unpacking to f32 and a packed FMA cost over 2;
 // up to 16 vectors share them.  151936 x 1024 of one vector: 18.9 us for 88 MB (4.6
 // TB/s, 69 % of a copy's rate: 5 us are the launch, the vector and the last tiles'
-// sums); 16 vectors 57 us, bound by the instructions for sums and scales (16384 x
-// 8192 of 16: 75 us, 57 TFLOP/s); 1024 x 1024 5.8 us, a launch.  Each warp streams its row tiles' strips, one
-// contiguous run, through a ring of bulk copies of its own.  Where there are too
-// few row tiles for the GPU's warps, or staging the vectors would take too long, a cluster
-// of 2, 4 or 8 CTAs shares the strips (so each stages a part of the vectors) and adds
-// its sums through distributed shared memory; with less than 8 row tiles the
-// warps of a CTA share them too.
-template <int NT, bool ONE>
+// sums); 16 vectors 51 us, bound by the reads of the staged vectors, the matrix
+// pipe and the sums' instructions in turn (16384 x 8192 of 16: 67 us, 64 TFLOP/s);
+// 1024 x 1024 5.8 us, a launch.
+//
+// Each warp streams its row tiles' strips, one contiguous run, through a ring of
+// bulk copies of its own.  Where there are too few row tiles for the GPU's warps, or
+// staging the vectors would take too long, a cluster of 2, 4 or 8 CTAs shares the
+// strips (so each stages a part of the vectors) and adds its sums through
+// distributed shared memory; with less than 8 row tiles the warps of a CTA share
+// them too.
+template <int NT, int RT, bool ONE>
 __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   constexpr int NC = ONE ? 2 : 8 * NT;  // staged columns: high and low part of each vector
-  constexpr int kMvStages = mv_stages(NT), kChunk = mv_chunk(NT), kStage = kChunk * kQ4TileBytes;
+  constexpr int NS = RT * 2 * NT;  // a lane's sums
+  constexpr int kMvStages = mv_stages(NT, RT), kChunk = mv_chunk(NT), kStage = RT * kChunk * kQ4TileBytes;
   extern __shared__ __align__(128) unsigned char sm[];
   unsigned char* ring = sm;
-  float* red = reinterpret_cast<float*>(ring + kMvWarps * kMvStages * kStage);  // [warps][2 NT][32]
-  auto* bars = reinterpret_cast<uint64_t*>(red + kMvWarps * 2 * NT * 32);
+  float* red = reinterpret_cast<float*>(ring + kMvWarps * kMvStages * kStage);  // [warps][NS][32]
+  auto* bars = reinterpret_cast<uint64_t*>(red + kMvWarps * NS * 32);
   // [groups of a slab][NC / 2]: start of the sums of the high and low parts (of two rows); the vector's factor
   float4* zs = reinterpret_cast<float4*>(bars + kMvWarps * kMvStages);
   float* fs = reinterpret_cast<float*>(zs + a.slab * 4 * (NC / 2));
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   const int cta0 = blockIdx.x / a.cluster * slots;  // the cluster's first slot
   const int slot = cta0 + warp / a.wk;
   const int cs0 = a.strips * rank / a.cluster, cs1 = a.strips * (rank + 1) / a.cluster;  // the CTA's strips
-  const int tile0 = slot * a.per_slot, tile1 = min(tile0 + a.per_slot, a.row_tiles);
+  const int tile0 = slot * a.per_slot, tile1 = min(tile0 + a.per_slot, a.tiles);
   const int v0 = blockIdx.y * 16, nv = min(a.n - v0, ONE ? 1 : 4 * NT);
   const float* x = a.x + v0 * a.xs;
   float* y = a.y + v0 * a.ys;
@@ -147,15 +154,20 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
         if (b == e) ptile = tile1 - 1;  // (fewer strips than warps)
       } while (b == e);
       left = e - b;
-      src = a.w + (static_cast<size_t>(ptile) * a.strips + b) * kQ4TileBytes;
+      src = a.w + (static_cast<size_t>(ptile) * RT * a.strips + b) * kQ4TileBytes;
     }
     const int n = min(left, kChunk);
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bar[pst], n * kQ4TileBytes);
-      bulk_g2s(my_ring + pst * kStage, src, n * kQ4TileBytes, &bar[pst]);
+      const int has = min(RT, a.row_tiles - ptile * RT);  // (what lies behind the last row tile is not stored)
+      mbar_arrive_expect_tx(&bar[pst], has * n * kQ4TileBytes);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        if (rt < has)
+          bulk_g2s(my_ring + pst * kStage + rt * kChunk * kQ4TileBytes, src + static_cast<size_t>(rt) * a.strips * kQ4TileBytes,
+                   n * kQ4TileBytes, &bar[pst]);
     }
     pst = pst + 1 == kMvStages ? 0 : pst + 1;
-    src += kStage;
+    src += kChunk * kQ4TileBytes;
     left -= n;
   };
   if (tile0 < tile1)
@@ -249,9 +261,11 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
     share(slab, b, e);
     for (int k = 0; k < a.per_slot; ++k) {
       const int tile = tile0 + k;
-      float acc[NT][2];
+      float acc[RT][NT][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = 0.f;
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[rt][t][0] = acc[rt][t][1] = 0.f;
       if (tile < tile1) {
         for (int strip0 = b; strip0 < e; strip0 += kChunk) {
           issue();
@@ -264,32 +278,50 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
 #pragma unroll
           for (int u = 0; u < kChunk; ++u) {
             if (u && strip0 + u >= e) break;
-            const unsigned char* tl = stage + u * kQ4TileBytes;
-            const uint4 w0 = *reinterpret_cast<const uint4*>(tl + lane * 16);
-            const uint4 w1 = *reinterpret_cast<const uint4*>(tl + 512 + lane * 16);
-            const uint2 s0 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + r8 * 8);
-            const uint2 s1 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + 64 + r8 * 8);
-            const uint32_t wa[4] = {w0.x, w0.y, w0.z, w0.w}, wb[4] = {w1.x, w1.y, w1.z, w1.w};
+            uint4 w[RT][2];
+            uint2 sc[RT][2];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              const unsigned char* tl = stage + (rt * kChunk + u) * kQ4TileBytes;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                w[rt][h] = *reinterpret_cast<const uint4*>(tl + h * 512 + lane * 16);
+                sc[rt][h] = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + h * 64 + r8 * 8);
+              }
+            }
             const int gl = (strip0 + u) * 4 - g0;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              const uint32_t p = wa[g], q = wb[g], p8 = p >> 8, q8 = q >> 8;
-              const uint32_t a0[4] = {p & 0x000F000Fu, q & 0x000F000Fu, p & 0x00F000F0u, q & 0x00F000F0u};
-              const uint32_t a1[4] = {p8 & 0x000F000Fu, q8 & 0x000F000Fu, p8 & 0x00F000F0u, q8 & 0x00F000F0u};
-              const uint32_t sw0 = g < 2 ? s0.x : s0.y, sw1 = g < 2 ? s1.x : s1.y;
-              const __half2 h0 = *reinterpret_cast<const __half2*>(&sw0), h1 = *reinterpret_cast<const __half2*>(&sw1);
-              const float d0 = g & 1 ? __high2float(h0) : __low2float(h0), d1 = g & 1 ? __high2float(h1) : __low2float(h1);
+              uint32_t a0[RT][4], a1[RT][4];
+              float ds[RT][2];
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint4& v = w[rt][h];
+                  const uint32_t p = g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w, p8 = p >> 8;
+                  a0[rt][h] = p & 0x000F000Fu;
+                  a0[rt][2 + h] = p & 0x00F000F0u;
+                  a1[rt][h] = p8 & 0x000F000Fu;
+                  a1[rt][2 + h] = p8 & 0x00F000F0u;
+                  const uint32_t sw = g < 2 ? sc[rt][h].x : sc[rt][h].y;
+                  const __half2 hs = *reinterpret_cast<const __half2*>(&sw);
+                  ds[rt][h] = g & 1 ? __high2float(hs) : __low2float(hs);
+                }
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 const int col = ONE ? r8 & 1 : t * 8 + r8;  // (one vector: the other columns repeat its two)
                 const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl + g) * NC + col) * 4 + c) * 16);
                 const float4 z = zs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
                 const float f = fs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
-                float d[4];
-                mma_f16(d, a0, xv.x, xv.y, z.x, z.y, z.z, z.w);
-                mma_f16(d, a1, xv.z, xv.w);
-                acc[t][0] += d0 * (f * (d[0] + d[1]));
-                acc[t][1] += d1 * (f * (d[2] + d[3]));
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                  float d[4];
+                  mma_f16(d, a0[rt], xv.x, xv.y, z.x, z.y, z.z, z.w);
+                  mma_f16(d, a1[rt], xv.z, xv.w);
+                  acc[rt][t][0] += ds[rt][0] * (f * (d[0] + d[1]));
+                  acc[rt][t][1] += ds[rt][1] * (f * (d[2] + d[3]));
+                }
               }
             }
           }
@@ -297,43 +329,39 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
         }
         if (dead)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = __int_as_float(0x7FC00000);
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[rt][t][0] = acc[rt][t][1] = __int_as_float(0x7FC00000);
       }
-      auto store = [&](int row_tile, int t, int h, int l, float sum) {  // lane l's sum for vectors t * 4 .. of half h
-        const int v = t * 4 + (l & 3), r = row_tile * 16 + h * 8 + (l >> 2);
-        if (v >= nv || r >= a.rows || row_tile >= a.row_tiles) return;
+      auto store = [&](int of, int i, int l, float sum) {  // sum i of lane l: [row tile][4 vectors][half of the rows]
+        const int v = i / 2 % NT * 4 + (l & 3);
+        const int64_t r = (static_cast<int64_t>(of) * RT + i / (2 * NT)) * 16 + i % 2 * 8 + (l >> 2);
+        if (v >= nv || r >= a.rows) return;
         float* p = y + v * a.ys + r;
         *p = slab ? *p + sum : sum;
       };
       if (a.wk * a.cluster == 1) {
         if (tile < tile1)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            store(tile, t, 0, lane, acc[t][0]);
-            store(tile, t, 1, lane, acc[t][1]);
-          }
+          for (int i = 0; i < NS; ++i) store(tile, i, lane, acc[i / (2 * NT)][i / 2 % NT][i % 2]);
         continue;
       }
-      float* mine = red + warp * 2 * NT * 32 + lane;
+      float* mine = red + warp * NS * 32 + lane;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        mine[(2 * t) * 32] = acc[t][0];
-        mine[(2 * t + 1) * 32] = acc[t][1];
-      }
+      for (int i = 0; i < NS; ++i) mine[i * 32] = acc[i / (2 * NT)][i / 2 % NT][i % 2];
       if (a.cluster == 1)
         __syncthreads();
       else
         cluster_sync();
-      // the sums of each slot's tile: 64 NT values, dealt over the cluster's threads
-      for (int i = rank * kMvThreads + threadIdx.x; i < slots * 2 * NT * 32; i += a.cluster * kMvThreads) {
-        const int sl = i / (2 * NT * 32), e2 = i % (2 * NT * 32);
-        const float* from = red + sl * a.wk * 2 * NT * 32 + e2;
+      // the sums of each slot's tile, dealt over the cluster's threads
+      for (int i = rank * kMvThreads + threadIdx.x; i < slots * NS * 32; i += a.cluster * kMvThreads) {
+        const int sl = i / (NS * 32), e2 = i % (NS * 32);
+        const float* from = red + sl * a.wk * NS * 32 + e2;
         float sum = 0.f;
         for (int q = 0; q < a.cluster; ++q)
           for (int j = 0; j < a.wk; ++j)
-            sum += a.cluster == 1 ? from[j * 2 * NT * 32] : ld_cluster(from + j * 2 * NT * 32, q);
-        const int row_tile = (cta0 + sl) * a.per_slot + k;
-        store(row_tile, e2 / 64, e2 / 32 % 2, e2 % 32, sum);
+            sum += a.cluster == 1 ? from[j * NS * 32] : ld_cluster(from + j * NS * 32, q);
+        store((cta0 + sl) * a.per_slot + k, e2 / 32, e2 % 32, sum);
       }
       if (a.cluster == 1)
         __syncthreads();
@@ -343,22 +371,23 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   }
 }
 
-template <int NT, bool ONE>
+template <int NT, int RT, bool ONE>
 cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   constexpr int NC = ONE ? 2 : 8 * NT;
-  constexpr int most = (kMvSmem - mv_fixed_smem(NT)) / mv_strip_smem(NC);  // strips whose vectors fit
+  constexpr int most = (kMvSmem - mv_fixed_smem(NT, RT)) / mv_strip_smem(NC);  // strips whose vectors fit
   // With less than eight row tiles the warps of a CTA share a tile's strips.  The
   // cluster is the one that costs a warp the fewest instructions: about 50 for
   // each octet of columns that it stages, 110 + 60 NT a strip, 500 to add a row tile's
   // sums through distributed shared memory.
+  a.tiles = (a.row_tiles + RT - 1) / RT;
   a.wk = 1;
-  while (a.wk < kMvWarps && a.row_tiles * a.wk < kMvWarps && a.wk * 2 <= a.strips) a.wk *= 2;
-  const int sweep = a.n < 16 ? a.n : 16, ctas = (a.row_tiles * a.wk + kMvWarps - 1) / kMvWarps;
+  while (a.wk < kMvWarps && a.tiles * a.wk < kMvWarps && a.wk * 2 <= a.strips) a.wk *= 2;
+  const int sweep = a.n < 16 ? a.n : 16, ctas = (a.tiles * a.wk + kMvWarps - 1) / kMvWarps;
   int64_t least = 0;
   for (int x = 1; x <= 8 && x * a.wk <= a.strips; x *= 2) {
     const int sweeps = (a.n + 15) / 16, room = kMvCtas / (x * sweeps);  // (sweeps run side by side; at most 4)
     const int64_t rounds = (ctas + room - 1) / room, each = (a.strips + x * a.wk - 1) / (x * a.wk);
-    const int64_t cost = static_cast<int64_t>(sweep) * a.strips * 6 / x + rounds * (each * (110 + 60 * NT) + (x > 1 ? 500 : 0));
+    const int64_t cost = static_cast<int64_t>(sweep) * a.strips * 6 / x + rounds * (each * RT * (110 + 60 * NT) + (x > 1 ? 500 : 0));
     if (x == 1 || cost < least) {
       least = cost;
       a.cluster = x;
@@ -366,16 +395,16 @@ cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   }
   const int strips = (a.strips + a.cluster - 1) / a.cluster, slabs = (strips + most - 1) / most;
   a.slab = (strips + slabs - 1) / slabs;
-  const size_t smem = static_cast<size_t>(mv_fixed_smem(NT)) + static_cast<size_t>(a.slab) * mv_strip_smem(NC);
+  const size_t smem = static_cast<size_t>(mv_fixed_smem(NT, RT)) + static_cast<size_t>(a.slab) * mv_strip_smem(NC);
   const int slots = kMvWarps / a.wk;
-  int blocks = (a.row_tiles + slots - 1) / slots;
+  int blocks = (a.tiles + slots - 1) / slots;
   if (blocks > kMvCtas / a.cluster) blocks = kMvCtas / a.cluster;
-  a.per_slot = (a.row_tiles + blocks * slots - 1) / (blocks * slots);
-  blocks = (a.row_tiles + a.per_slot * slots - 1) / (a.per_slot * slots);
+  a.per_slot = (a.tiles + blocks * slots - 1) / (blocks * slots);
+  blocks = (a.tiles + a.per_slot * slots - 1) / (a.per_slot * slots);
   static unsigned long long done = 0;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_q4_matvec<NT, ONE>), kMvSmem, &done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_q4_matvec<NT, RT, ONE>), kMvSmem, &done);
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(k_q4_matvec<NT, ONE>, a.cluster, dim3(blocks * a.cluster, (a.n + 15) / 16), kMvThreads, smem,
+  return launch_pdl_clusters(k_q4_matvec<NT, RT, ONE>, a.cluster, dim3(blocks * a.cluster, (a.n + 15) / 16), kMvThreads, smem,
                              st, a);
 }
 
@@ -401,10 +430,14 @@ cudaError_t launch_q4_matvec(const uint8_t* w, int rows, int cols, const float* 
   a.n = n;
   a.row_tiles = (rows + kQ4TileRows - 1) / kQ4TileRows;
   a.strips = (cols + kQ4TileCols - 1) / kQ4TileCols;
-  if (n == 1) return launch_mv<1, true>(a, st);
-  if (n <= 4) return launch_mv<1, false>(a, st);
-  if (n <= 8) return launch_mv<2, false>(a, st);
-  return launch_mv<4, false>(a, st);
+  if (n == 1) return launch_mv<1, 1, true>(a, st);
+  if (n <= 4) return launch_mv<1, 1, false>(a, st);
+  if (n <= 8) return launch_mv<2, 1, false>(a, st);
+  // Two row tiles a warp read the staged vectors once for both: with two for every
+  // CTA, 151936 x 1024 of 16 took 51 us instead of 57, 16384 x 8192 67 instead of 76; with
+  // fewer, 4096 x 16384 64 instead of 44 and 1024 x 1024 9.2 instead of 7.6.
+  if (a.row_tiles < 2 * kMvCtas) return launch_mv<4, 1, false>(a, st);
+  return launch_mv<4, 2, false>(a, st);
 }
 
 }  // namespace tqd
