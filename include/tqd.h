@@ -550,7 +550,8 @@ int32_t tqd_op_q4_0_matvec(const uint8_t* w_tiles, int64_t rows, int64_t cols, c
  * everywhere and entropy 0.  targets and logprob go together and may be NULL,
  * entropy may be NULL, top_k may be 0.  scratch: caller-owned device memory
  * of tqd_logprobs_scratch_bytes(rows, vocab, top_k) bytes, 16-byte aligned,
- * whatever its contents. */
+ * whatever its contents.  The size never falls as one of the three grows: a
+ * scratch for the largest call serves every smaller one. */
 int32_t tqd_op_logprobs(const float* logits, int64_t stride, int32_t rows, int32_t vocab, const int32_t* targets,
                         float* logprob, float* entropy, int32_t top_k, int32_t* top_ids, float* top_logprobs,
                         void* scratch, void* stream);

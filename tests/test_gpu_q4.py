@@ -825,6 +825,29 @@ def test_logprobs_repeat_to_the_bit_and_in_a_graph(ops):
         assert torch.equal(p, q)
 
 
+def test_logprobs_with_the_scratch_of_a_larger_call(ops):
+    """One scratch, sized for the largest batch, serves calls of fewer rows, which are cut into more slices; what
+    lies behind it stays as it was."""
+    rng = np.random.default_rng(31)
+    v, k, rows = 20011, 20, 2053
+    size, guard = ops.tqd_logprobs_scratch_bytes(rows, v, k), 4 << 20
+    mem = torch.full((size + guard,), 0x5A, dtype=torch.uint8, device="cuda")
+    x = (rng.normal(size=(rows, v)) * 3).astype(np.float32)
+    d, targets = dev(x), rng.integers(0, v, size=rows)
+    for n in (1, 8, 40, 333, 700, rows):
+        lp, ent = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        ids, tops = torch.empty(n, k, dtype=torch.int32, device="cuda"), torch.empty(n, k, device="cuda")
+        ops.tqd_op_logprobs(d[:n], i32(targets[:n]), lp, ent, ids, tops, mem[:size])
+        for r in {0, n // 2, n - 1}:
+            a, h, i, t, e1, e2 = q4.logprobs(x[r], targets[r], k)
+            tol = 4 * U * (1 + e1)
+            assert abs(float(lp[r]) - a) <= 4 * U * (1 + 3 * abs(a)) + tol
+            assert abs(float(ent[r]) - h) <= 4 * U * (2 + h + e1 + e2) + tol
+            assert np.array_equal(ids[r].cpu().numpy(), i)
+            assert np.all(np.abs(tops[r].cpu().numpy() - t) <= 4 * U * (1 + 3 * np.abs(t)) + tol)
+    assert bool((mem[size:] == 0x5A).all())
+
+
 # ------------------------------------------------------------------ refusals of the wrappers
 
 def test_wrapper_refusals(ops, TQDError):

@@ -93,6 +93,21 @@ def test_sizes(L):
     assert L.tqd_logprobs_scratch_bytes(1, 100, 33) == L.tqd_logprobs_scratch_bytes(0, 100, 1) == 0
 
 
+@pytest.mark.parametrize("vocab", [1, 1000, 2045, 2046, 9001, 151936, 1 << 20])
+def test_a_logprob_scratch_serves_every_smaller_call(L, vocab):
+    """The size never falls as rows, vocabulary or alternatives grow (a program keeps one for its largest batch)."""
+    rows = sorted({1, 2, 3, 7, 8, 9, 40, 41, 512, 700, 759, 760, 761, 1000, 1519, 1520, 2053, 3039, 3040, 3041, 6080,
+                   6081, 100000, *range(10, 400, 13)})
+    sizes = {k: [L.tqd_logprobs_scratch_bytes(r, vocab, k) for r in rows] for k in (0, 1, 2, 5, 20, 31, 32)}
+    for a in sizes.values():
+        assert a == sorted(a)
+    for a, b in zip(list(sizes.values()), list(sizes.values())[1:]):
+        assert all(x <= y for x, y in zip(a, b))
+    for r in (1, 8, 512, 760, 2053):
+        by_vocab = [L.tqd_logprobs_scratch_bytes(r, v, 20) for v in (1, 2045, 2046, 4094, 9001, 49152, 151936, 1 << 20)]
+        assert by_vocab == sorted(by_vocab)
+
+
 def test_cache_struct_matches_the_header():
     cls = _lib.tqd_kv_q4
     fields = [f[0] for f in cls._fields_]

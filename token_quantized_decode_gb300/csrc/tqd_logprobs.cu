@@ -527,13 +527,17 @@ __global__ void __launch_bounds__(kLT) k_logprobs_join(LogprobArgs a, int slices
   write_row(a, row, all, best, n);
 }
 
+constexpr int64_t kWave = 5 * 152;  // blocks that run at once
+
+int tiles_of(int vocab) { return (vocab + 3 + kTile - 1) / kTile; }
+int most_slices(int vocab) { return tiles_of(vocab) < kMaxSlices ? tiles_of(vocab) : kMaxSlices; }
+
 // Slices of a row, of whole tiles: what makes the waves of 5 blocks an SM
 // shortest, a block being counted as its tiles and, for its beginning, end and
-// list, 8 more (2 without alternatives).
+// list, 8 more (2 without alternatives).  More than one only where one slice
+// less leaves fewer than 4 waves of blocks.
 int slices_of(int rows, int vocab, int top_k) {
-  constexpr int64_t kWave = 5 * 152;
-  const int tiles = (vocab + 3 + kTile - 1) / kTile, fixed = top_k ? 8 : 2;
-  const int most = tiles < kMaxSlices ? tiles : kMaxSlices;
+  const int tiles = tiles_of(vocab), most = most_slices(vocab), fixed = top_k ? 8 : 2;
   int best = 1;
   int64_t least = -1;
   for (int s = 1; s <= most; ++s) {
@@ -551,14 +555,18 @@ int slices_of(int rows, int vocab, int top_k) {
 
 }  // namespace
 
+// Room for a call of these sizes and of any smaller ones.  Fewer rows are cut into more
+// slices, so what a call needs does not grow with its rows; but with s > 1 slices
+// rows * (s - 1) < 4 kWave, hence rows < 4 kWave and rows * s < 4 kWave + rows.
 size_t logprobs_scratch_bytes(int rows, int vocab, int top_k) {
-  const int s = slices_of(rows, vocab, top_k);
-  return s == 1 ? 16 : static_cast<size_t>(rows) * s * partial_bytes(top_k);
+  const int most = most_slices(vocab);
+  if (most == 1) return 16;
+  const int64_t all = static_cast<int64_t>(rows) * most, cut = 4 * kWave + (rows < 4 * kWave ? rows : 4 * kWave);
+  return static_cast<size_t>(all < cut ? all : cut) * partial_bytes(top_k);
 }
 
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st) {
-  const int slices = slices_of(a.rows, a.vocab, a.top_k);
-  const int tiles = (a.vocab + 3 + kTile - 1) / kTile;
+  const int slices = slices_of(a.rows, a.vocab, a.top_k), tiles = tiles_of(a.vocab);
   const int each = (tiles + slices - 1) / slices;
   const cudaError_t e = launch_pdl(k_logprobs, dim3(static_cast<unsigned>(a.rows) * slices), kLT, 0, st, a, slices, each);
   if (e != cudaSuccess || slices == 1) return e;
