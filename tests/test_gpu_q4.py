@@ -848,6 +848,12 @@ def test_logprobs_with_the_scratch_of_a_larger_call(ops):
     assert bool((mem[size:] == 0x5A).all())
 
 
+def test_lanes_of_a_warp_agree_about_a_wait_that_runs_out_in_some(ops):
+    """A phase that completes between two lanes' limits: the attention and the products go on with whole warps."""
+    status, bits = ops.tqd_op_wait_selftest()
+    assert status != 0 and not bits & 4
+
+
 # ------------------------------------------------------------------ refusals of the wrappers
 
 def test_wrapper_refusals(ops, TQDError):

@@ -69,17 +69,40 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Wait for phase `parity` of the barrier to complete; false (and the error
-// bit set) if it does not within kWaitLimitNs.
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint32_t* err) {
+// bit set) if it does not within the limit.
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint32_t* err,
+                                                  uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity)) {
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
+    if (global_timer_ns() - t0 > limit_ns) {
       if (err) atomicOr(err, kErrMbarrier);
       return false;
     }
   }
   return true;
+}
+
+// The same by all lanes of a warp, for code that goes on with the whole warp:
+// each lane reads the timer for itself, so a phase that completes as the limit
+// passes is seen by some of them only; false in every lane then.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, nullptr, limit_ns));
+}
+
+// After a wait that ran out at stage st of a warp's ring: every stage's copy
+// that may still be under way gets the limit once more, so that none lands in
+// shared memory that serves something else by then.  (A stage without a copy costs its
+// limit: at most a few seconds, on a GPU that has stopped copying.)
+__device__ __forceinline__ void mbar_ring_drain(uint64_t* bars, int stages, int st, uint32_t phase) {
+#pragma unroll 1
+  for (int i = 0; i < stages; ++i) {
+    mbar_wait_warp(&bars[st], phase);
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1u;
+    }
+  }
 }
 
 // Global -> shared bulk copy completing on `bar` (both addresses 16-byte

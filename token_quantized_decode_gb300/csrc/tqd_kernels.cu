@@ -456,15 +456,18 @@ cudaError_t launch_op_argmax(const float* x, int64_t n, int32_t* out, float* can
 // arrives at (the bounded wait the ring and tensor-core kernels use); thread 32
 // polls a counter nothing increments, the way a grid barrier does.  Both give
 // up after kWaitLimitNs, set their error bits and return, and the context
-// stays usable.
+// stays usable.  Warp 2 checks that a warp's wait has one answer for all lanes.
+constexpr uint32_t kWaitLanes = 4u;
 __device__ uint32_t g_wait_err;
 __device__ unsigned long long g_wait_ctr;  // never incremented
 
 __global__ void k_wait_selftest() {
-  __shared__ __align__(8) uint64_t bar;
+  __shared__ __align__(8) uint64_t bar, late[2];
   if (threadIdx.x == 0) {
     g_wait_err = 0u;
     mbar_init(&bar, 1);
+    mbar_init(&late[0], 1);
+    mbar_init(&late[1], 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -481,11 +484,25 @@ __global__ void k_wait_selftest() {
         break;
       }
     }
+  } else if (threadIdx.x >= 64 && threadIdx.x < 96) {
+    // two barriers that complete late, after 0.2 and 0.4 s: half of the lanes stop waiting
+    // after a millisecond, so on its own each lane may answer for itself, the warp's wait not
+    const uint64_t limit = threadIdx.x < 80 ? 1000000ull : kWaitLimitNs;
+    const bool own = mbar_wait_bounded(&late[0], 0u, nullptr, limit);
+    const bool mixed = __any_sync(0xFFFFFFFFu, own) && !__all_sync(0xFFFFFFFFu, own);
+    const bool together = __any_sync(0xFFFFFFFFu, mbar_wait_warp(&late[1], 0u, limit));
+    if (threadIdx.x == 64 && (!mixed || together)) atomicOr(&g_wait_err, kWaitLanes);
+  } else if (threadIdx.x == 96) {
+    const uint64_t t0 = global_timer_ns();
+    for (int i = 0; i < 2; ++i) {
+      while (global_timer_ns() - t0 < (i + 1) * 200000000ull) __nanosleep(1000000);
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&late[i])) : "memory");
+    }
   }
 }
 
 cudaError_t run_wait_selftest(uint32_t* err_bits, cudaStream_t st) {
-  k_wait_selftest<<<1, 64, 0, st>>>();
+  k_wait_selftest<<<1, 128, 0, st>>>();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = cudaMemcpyFromSymbolAsync(err_bits, g_wait_err, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, st);

@@ -379,9 +379,10 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
                           (static_cast<size_t>(kvh) * ppb + (t - slot * a.c.page_size) / kQ4Block) * BB;
     }
   };
+  bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
   int issued = 0, issue_st = 0;
   auto issue = [&] {
-    if (issued >= n_it) return;
+    if (issued >= n_it || dead) return;
     if ((issued & 31) == 0) locate(issued + lane);
     if (lane == (issued & 31)) {
       flag[issue_st] = src_flag;
@@ -435,7 +436,6 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
 
   const Unpack unpack;
   int rel = 0, st = 0, phase = 0;  // the warp's next unit, counted from u0, and its stage
-  bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
   int goes_on = 0;
   bool begun = false;
   while (u < u1) {
@@ -708,7 +708,10 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
     for (; rel < rel_end; ++rel) {
       issue();
       __syncwarp();
-      if (!dead) dead = !mbar_wait_bounded(&bar[st], phase, nullptr);
+      if (!dead && !mbar_wait_warp(&bar[st], phase)) {
+        dead = true;
+        mbar_ring_drain(bar, ST, st, phase);
+      }
       const int t0 = (rel + unit0) * kUnit;
       const int fl = flag[st];
       const unsigned char* at = my_ring + st * 2 * BB;

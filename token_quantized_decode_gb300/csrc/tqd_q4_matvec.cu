@@ -139,7 +139,10 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   // the ring's next copy: slab by slab, tile by tile, strip by strip
   const uint8_t* src = nullptr;
   int left = 0, ptile = tile1 - 1, pslab = -1, pst = 0;
+  bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
+  bool stopped = false;  // the warp knows of it
   auto issue = [&] {
+    if (dead) return;
     if (left == 0) {  // the next tile, or the next slab, with strips for this warp
       int b = 0, e = 0;
       do {
@@ -174,7 +177,6 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
     for (int i = 0; i < kMvStages - 1; ++i) issue();
 
   int st = 0, phase = 0;
-  bool dead = false;  // a copy that did not arrive within the wait's limit: the rows become NaN
   for (int slab = 0; slab < slabs; ++slab) {
     // ---- the slab's part of the vectors
     const int g0 = (cs0 + slab * a.slab) * 4, ng = max(min(a.slab * 4, cs1 * 4 - g0), 0);
@@ -327,11 +329,15 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
           }
           __syncwarp();  // every lane has read the stage before it is filled again
         }
-        if (dead)
+        // (each lane read the timer for itself: one that ran out speaks for the warp, whose sums hold its share)
+        if (__any_sync(0xFFFFFFFFu, dead)) {
+          if (!stopped) mbar_ring_drain(bar, kMvStages, st, phase);
+          dead = stopped = true;
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[rt][t][0] = acc[rt][t][1] = __int_as_float(0x7FC00000);
+        }
       }
       auto store = [&](int of, int i, int l, float sum) {  // sum i of lane l: [row tile][4 vectors][half of the rows]
         const int v = i / 2 % NT * 4 + (l & 3);
