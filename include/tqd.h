@@ -530,8 +530,9 @@ size_t tqd_q4_0_matrix_bytes(int64_t rows, int64_t cols);
 
 /* y[j] = W x[j] for n vectors (n <= 64) over a repacked Q4_0 matrix: x f32
  * [n][cols], y f32 [n][rows], their rows x_stride and y_stride floats apart.
- * f32 accuracy: the weights are exact, each 32 elements of x are carried to 22
- * bits below their largest one's exponent (or finer), sums are f32.  A scale
+ * Accuracy: the weights are exact; of an element of x at most 2^-22 is lost, or
+ * 2^-40 of the largest of its aligned group of 32 where that is more; sums are f32,
+ * and zero weights add nothing to them.  A scale
  * that is NaN or infinite makes its row NaN (or infinite); an x with an
  * element that is NaN, infinite or of magnitude 2^113 or more gives NaN.  y may
  * not overlap x. */

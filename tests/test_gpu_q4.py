@@ -686,6 +686,54 @@ def test_q4_matvec_extremes(ops):
     assert np.isnan(y[7]) and np.all(np.isfinite(np.delete(y, 7)))
 
 
+@pytest.mark.parametrize("ratio", [1, 20, 100, 1000, 5000, 2**20])
+@pytest.mark.parametrize("n", [1, 3, 8, 16])
+def test_q4_matvec_large_elements_that_meet_zero_weights(ops, ratio, n):
+    """One element of each group of 32 is far larger than the rest and its weights are 0 (code 8), so that nothing of
+    the result hides what the rest lost beside it.  Terms of the tolerance are the products themselves, |w x|: f32's
+    16 u sqrt(sum T^2) + 4 u |sum| (the file's head), and an element off by up to 2^-40 of its group's largest (four
+    times the root sum square)."""
+    rng = np.random.default_rng(ratio + n)
+    rows, cols = 2000, 1024
+    codes, d = q4_matrix(rng, rows, cols)
+    x = rng.normal(size=(n, cols)).astype(np.float32)
+    at = 32 * np.arange(cols // 32) + rng.integers(0, 32, size=cols // 32)
+    x[:, at] = (ratio * rng.uniform(0.7, 1.4, size=(n, at.size)) * rng.choice([-1, 1], size=(n, at.size)))
+    codes[:, at] = 8
+    y = torch.empty(n, rows, device="cuda")
+    ops.tqd_op_q4_0_matvec(tiles_of(ops, codes, d), rows, cols, dev(x), y)
+    w, x64 = q4.q4_0_values(codes, d), x.astype(np.float64)
+    want = x64 @ w.T
+    top = np.repeat(np.abs(x64).reshape(n, -1, 32).max(-1), 32, axis=1)
+    off = 4 * np.sqrt((top * 2.0**-40) ** 2 @ (w**2).T)
+    tol = 16 * U * np.sqrt((x64**2) @ (w**2).T) + 4 * U * np.abs(want) + off
+    err = np.abs(y.cpu().numpy() - want)
+    assert np.all(err <= tol), float((err / tol).max())
+
+
+def test_q4_matvec_groups_of_every_shape(ops):
+    """Groups of equal elements, at the ends of an octave, of one large element and 31 small ones, all codes 0, all 15
+    and mixed: sums at their longest, and terms of very unequal size."""
+    rng = np.random.default_rng(77)
+    cols = 256
+    top = np.float32(2.0) - np.float32(2.0**-23)
+    groups = [np.full(32, top), np.full(32, 1.0), np.full(32, top) * rng.choice([-1, 1], 32),
+              np.r_[top, np.full(31, 2.0**-5)], np.r_[1.0, np.full(31, 2.0**-12 * 1.7)],
+              np.r_[top, np.full(31, 2.0**-20 * 1.3)], np.full(32, 2.0**-40 * 1.1), np.r_[-top, np.full(31, top)]]
+    x = np.concatenate(groups).astype(np.float32)
+    x = np.stack([x, x * np.float32(1 / 3), -x * np.float32(1.7)])
+    codes = np.concatenate([np.zeros((3, cols)), np.full((3, cols), 15), rng.choice([0, 15], size=(26, cols)),
+                            rng.integers(0, 16, size=(8, cols))]).astype(np.uint8)
+    d = np.exp2(rng.integers(-3, 4, size=(40, cols // 32))).astype(np.float16)
+    y = torch.empty(3, 40, device="cuda")
+    ops.tqd_op_q4_0_matvec(tiles_of(ops, codes, d), 40, cols, dev(x), y)
+    w, x64 = q4.q4_0_values(codes, d), x.astype(np.float64)
+    want = x64 @ w.T
+    tol = 16 * U * np.sqrt((x64**2) @ (w**2).T) + 4 * U * np.abs(want)
+    err = np.abs(y.cpu().numpy() - want)
+    assert np.all(err <= tol), float((err / tol).max())
+
+
 def test_q4_matvec_in_a_graph_and_on_a_stream(ops):
     rng = np.random.default_rng(6)
     rows, cols = 1000, 1056

@@ -6,9 +6,10 @@
 //   word & 0x000F000F         codes 0 and 4 in the low bits of two f16
 //   word & 0x00F000F0         codes 1 and 5, times 16
 //   (word >> 8) & ...         codes 2, 6 and 3, 7
-// are f16 subnormals, code * 2^-24 and code * 2^-20 exactly, so a pair of
-// codes becomes a matrix operand in one instruction and no conversion.  The
-// factors are undone exactly: the 16 on the other operand, 2^24 on the sums.
+// V's and the weights become pairs of code - 8 by one packed operation more
+// (Unpack).  K's are operands as they are: f16 subnormals, code * 2^-24 and code *
+// 2^-20 exactly, the factors undone exactly (the 16 on the other operand, 2^24
+// on the sums) and 8 sum q taken off.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -39,11 +40,42 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The two f16 of a word as f32.
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+
 // x rounded to f16.
 __device__ __forceinline__ float round_f16(float x) { return __half2float(__float2half_rn(x)); }
 
 // 2^e as f32, e in -126 .. 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// The constants of unpacking codes to signed f16, kept in registers (as immediates they cost an
+// instruction each: a logic operation takes one).
+struct Unpack {
+  uint32_t lo, hi, magic, off, sixteenth, off_hi;
+  __device__ Unpack() {
+    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(lo));
+    asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(hi));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
+    off = 0xE408E408u;        // -1032
+    sixteenth = 0x2C002C00u;
+    off_hi = 0xD480D480u;     // -72
+  }
+  // The codes in bits 0-3 (low) or 4-7 (high) of each half of x as f16 pairs of
+  // code - 8: 1024 + code and 1024 + 16 code are exact f16, so is the result.
+  __device__ __forceinline__ uint32_t low(uint32_t x) const {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(lo), "r"(magic));
+    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(off));
+    return v;
+  }
+  __device__ __forceinline__ uint32_t high(uint32_t x) const {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(hi), "r"(magic));
+    asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(v) : "r"(sixteenth), "r"(off_hi));
+    return v;
+  }
+};
 
 // A float of another CTA of the cluster, at the address that it has in this one.
 __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {

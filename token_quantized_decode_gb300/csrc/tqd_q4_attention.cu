@@ -125,34 +125,6 @@ __device__ __forceinline__ uint32_t transpose_f16(uint32_t x) {
   return y;
 }
 
-// The constants of unpacking V, kept in registers (as immediates they cost an
-// instruction each: a logic operation takes one).
-struct Unpack {
-  uint32_t lo, hi, magic, off, sixteenth, off_hi;
-  __device__ Unpack() {
-    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(lo));
-    asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(hi));
-    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-    off = 0xE408E408u;        // -1032
-    sixteenth = 0x2C002C00u;
-    off_hi = 0xD480D480u;     // -72
-  }
-  // The codes in bits 0-3 (low) or 4-7 (high) of each half of x as f16 pairs of
-  // code - 8: 1024 + code and 1024 + 16 code are exact f16, so is the result.
-  __device__ __forceinline__ uint32_t low(uint32_t x) const {
-    uint32_t v;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(lo), "r"(magic));
-    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(off));
-    return v;
-  }
-  __device__ __forceinline__ uint32_t high(uint32_t x) const {
-    uint32_t v;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(hi), "r"(magic));
-    asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(v) : "r"(sixteenth), "r"(off_hi));
-    return v;
-  }
-};
-
 __device__ __forceinline__ unsigned long long udiv(unsigned long long a, unsigned b) {
   return a >> 32 ? a / b : static_cast<unsigned>(a) / b;
 }

@@ -43,8 +43,11 @@ __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t r
 constexpr int kMvWarps = 8;
 constexpr int kMvCtas = 304;  // two per SM
 constexpr int kMvThreads = 32 * kMvWarps;
-// Strips of a stage, and stages of a warp's ring (nt: tiles of 8 columns, rt: row tiles at once).
-__host__ __device__ constexpr int mv_chunk(int nt) { return nt == 4 ? 1 : 2; }
+// Strips of a stage, and stages of a warp's ring (nt: tiles of 8 columns, rt: row
+// tiles at once).  Four strips a stage for few columns (151936 x 1024 of one vector 18.7
+// us, with two 20.1; 151936 x 8192 109 and 123), fewer where the staged vectors
+// need the room.
+__host__ __device__ constexpr int mv_chunk(int nt) { return nt == 4 ? 1 : nt == 1 ? 4 : 2; }
 __host__ __device__ constexpr int mv_stages(int nt, int rt) { return nt == 4 && rt == 1 ? 3 : 2; }
 // Shared memory of a CTA: at most what lets two of them share an SM; the rings
 // and the warps' sums, then the staged vectors.
@@ -52,7 +55,7 @@ constexpr int kMvSmem = 113 * 1024;
 constexpr int mv_fixed_smem(int nt, int rt) {
   return kMvWarps * (mv_stages(nt, rt) * (rt * mv_chunk(nt) * kQ4TileBytes + 8) + rt * 2 * nt * 128);
 }
-constexpr int mv_strip_smem(int cols) { return 4 * (cols * 64 + cols / 2 * 20); }
+constexpr int mv_strip_smem(int cols) { return 4 * (cols * 64 + cols / 2 * 4); }
 
 struct MatvecQ4Args {
   const uint8_t* w;
@@ -70,24 +73,26 @@ struct MatvecQ4Args {
 
 // y = W x for up to 4 NT vectors (ONE: a single one).
 //
-// A tile's 16 rows are the tensor cores' 16 operand rows, its masked words the
-// operand itself (tqd_q4.cuh); the vectors are columns, two for each: a group of
-// 32 elements is scaled by a power of two that brings its largest to 2^10
-// .. 2^11 and split into the nearest whole number and the rest in f16, so that the
-// group's sums of whole parts times codes are exact in the f32 accumulators
-// (which truncate) and the rest carries 11 bits more; one power of two for a
-// whole vector costs the small elements of a vector with outliers too many.
-// sum_k (code_k - 8) x_k starts from -8 sum_k x_k, staged with x; each
+// A tile's 16 rows are the tensor cores' 16 operand rows, its codes unpacked to
+// f16 pairs of code - 8; the vectors are columns, two for each: a group of
+// 32 elements is scaled by a power of two that brings its largest to 2^14
+// .. 2^15 and each element split into its leading 11 bits and the rest in f16, so
+// an element keeps 22 bits down to 2^-17 of its group's largest.  Each
 // group's two column sums are added, scaled by the group's power of two and
 // the row's f16 scale and summed over groups in f32.
+// (Codes as they are, masked words that count as f16 subnormals, with 8 sum x taken off,
+// save the unpacking's packed operations; but a product with a zero weight is then 8 x and
+// not 0, and the tensor cores align the products of a subnormal as if it were 2^-14.
+// What that loses stays where a large element meets a zero weight: 1e-4
+// of the result for elements 1000 times the rest, where f32 products have 7e-7.)
 //
-// HBM bounds it: 4.5 bits a weight.  A weight costs 0.6 instructions of
+// HBM bounds it: 4.5 bits a weight.  A weight costs 1.1 instructions of
 // unpacking and 1/4 MMA lane, where unpacking to f32 and a packed FMA cost over 2;
-// up to 16 vectors share them.  151936 x 1024 of one vector: 18.9 us for 88 MB (4.6
-// TB/s, 69 % of a copy's rate: 5 us are the launch, the vector and the last tiles'
-// sums); 16 vectors 51 us, bound by the reads of the staged vectors, the matrix
-// pipe and the sums' instructions in turn (16384 x 8192 of 16: 67 us, 64 TFLOP/s);
-// 1024 x 1024 5.8 us, a launch.
+// up to 16 vectors share them.  151936 x 1024 of one vector: 17.7 us for 88 MB (5.0
+// TB/s, 73 % of a copy's rate: 5 us are the launch, the vector and the last tiles'
+// sums); 16 vectors 46 us, bound by the reads of the staged vectors, the matrix
+// pipe and the instructions of unpacking and sums in turn (16384 x 8192 of 16: 62
+// us, 69 TFLOP/s); 1024 x 1024 5.7 us, a launch.
 //
 // Each warp streams its row tiles' strips, one contiguous run, through a ring of
 // bulk copies of its own.  Where there are too few row tiles for the GPU's warps, or
@@ -104,10 +109,11 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   unsigned char* ring = sm;
   float* red = reinterpret_cast<float*>(ring + kMvWarps * kMvStages * kStage);  // [warps][NS][32]
   auto* bars = reinterpret_cast<uint64_t*>(red + kMvWarps * NS * 32);
-  // [groups of a slab][NC / 2]: start of the sums of the high and low parts (of two rows); the vector's factor
-  float4* zs = reinterpret_cast<float4*>(bars + kMvWarps * kMvStages);
-  float* fs = reinterpret_cast<float*>(zs + a.slab * 4 * (NC / 2));
+  float* fs = reinterpret_cast<float*>(bars + kMvWarps * kMvStages);  // [groups of a slab][NC / 2]: the vectors' factors
   unsigned char* xs = reinterpret_cast<unsigned char*>(fs + a.slab * 4 * (NC / 2));  // [groups][NC][4][16 bytes]
+
+  __shared__ uint4 none;  // a column of zeros
+  if (ONE && threadIdx.x == 0) none = make_uint4(0u, 0u, 0u, 0u);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r8 = lane >> 2, c = lane & 3;
@@ -176,6 +182,7 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   if (tile0 < tile1)
     for (int i = 0; i < kMvStages - 1; ++i) issue();
 
+  const Unpack unpack;
   int st = 0, phase = 0;
   for (int slab = 0; slab < slabs; ++slab) {
     // ---- the slab's part of the vectors
@@ -211,48 +218,28 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
         const int i = i0 + k * kMvThreads + lane, v = i / octs, o = i - v * octs;
         if (i - lane >= octs * (NC / 2)) break;
         float (&f)[8] = fs_[k];
-        float m = 0.f, zh = 0.f, zl = 0.f;
+        float m = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
 #pragma unroll
         for (int s = 1; s < 4; s <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-        const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127, up = 10 - e;
+        const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127, up = min(14 - e, 126);
         const float f1 = pow2(up / 2), f2 = pow2(up - up / 2);
+        uint32_t hi[4], lo[4];  // elements j and j + 4, their leading bits and the rest
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = e > 112 ? __int_as_float(0x7FC00000) : f[j] * f1 * f2;
-        float hi[8], lo[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          hi[j] = rintf(f[j]);
-          lo[j] = round_f16(f[j] - hi[j]);  // (rounded here: the start of the sum counts what the operand holds)
-          zh += hi[j];
-          zl += lo[j];
-        }
-#pragma unroll
-        for (int s = 1; s < 4; s <<= 1) {
-          zh += __shfl_xor_sync(0xFFFFFFFFu, zh, s);
-          zl += __shfl_xor_sync(0xFFFFFFFFu, zl, s);
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = e > 112 ? __int_as_float(0x7FC00000) : f[j] * f1 * f2;
+          const float x1 = e > 112 ? __int_as_float(0x7FC00000) : f[j + 4] * f1 * f2;
+          hi[j] = pack_f16(x0, x1);
+          const float2 h = unpack_f16(hi[j]);
+          lo[j] = pack_f16(x0 - h.x, x1 - h.y);
         }
         if (v < NC / 2) {
           const int g = o >> 2, oc = o & 3;
-          if (oc == 0) {
-            zh *= -8.f * 0x1p-24f;
-            zl *= -8.f * 0x1p-24f;
-            zs[g * (NC / 2) + v] = make_float4(zh, zl, zh, zl);
-            fs[g * (NC / 2) + v] = pow2(min(24 - up, 127));
-          }
-          uint4 q;
+          if (oc == 0) fs[g * (NC / 2) + v] = pow2(-up);
           unsigned char* d = xs + ((g * NC + 2 * v) * 4 + oc) * 16;
-          q.x = pack_f16(hi[0], hi[4]);
-          q.y = pack_f16(0.0625f * hi[1], 0.0625f * hi[5]);
-          q.z = pack_f16(hi[2], hi[6]);
-          q.w = pack_f16(0.0625f * hi[3], 0.0625f * hi[7]);
-          *reinterpret_cast<uint4*>(d) = q;
-          q.x = pack_f16(lo[0], lo[4]);
-          q.y = pack_f16(0.0625f * lo[1], 0.0625f * lo[5]);
-          q.z = pack_f16(lo[2], lo[6]);
-          q.w = pack_f16(0.0625f * lo[3], 0.0625f * lo[7]);
-          *reinterpret_cast<uint4*>(d + 64) = q;
+          *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(d + 64) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
     }
@@ -280,6 +267,33 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
 #pragma unroll
           for (int u = 0; u < kChunk; ++u) {
             if (u && strip0 + u >= e) break;
+            const int gl = (strip0 + u) * 4 - g0;
+            if constexpr (ONE) {
+              // the strip's four groups in the four column pairs, so that a lane takes the sums of
+              // one of them, group c, and not of all four
+              const unsigned char* tl = stage + u * kQ4TileBytes;
+              const uint4 w0 = *reinterpret_cast<const uint4*>(tl + lane * 16), w1 = *reinterpret_cast<const uint4*>(tl + 512 + lane * 16);
+              const unsigned char* scale = tl + kQ4TileScales + r8 * 8 + c * 2;
+              const unsigned char* own = xs + (((gl + (r8 >> 1)) * 2 + (r8 & 1)) * 4 + c) * 16;
+              float d[4];
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const uint32_t p = g == 0 ? w0.x : g == 1 ? w0.y : g == 2 ? w0.z : w0.w;
+                const uint32_t q = g == 0 ? w1.x : g == 1 ? w1.y : g == 2 ? w1.z : w1.w;
+                const uint32_t a0[4] = {unpack.low(p), unpack.low(q), unpack.high(p), unpack.high(q)};
+                const uint32_t a1[4] = {unpack.low(p >> 8), unpack.low(q >> 8), unpack.high(p >> 8), unpack.high(q >> 8)};
+                const uint4 xv = *reinterpret_cast<const uint4*>(r8 >> 1 == g ? own : reinterpret_cast<const unsigned char*>(&none));
+                if (g == 0)
+                  mma_f16(d, a0, xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
+                else
+                  mma_f16(d, a0, xv.x, xv.y);
+                mma_f16(d, a1, xv.z, xv.w);
+              }
+              const float f = fs[gl + c];
+              acc[0][0][0] += __half2float(*reinterpret_cast<const __half*>(scale)) * (f * (d[0] + d[1]));
+              acc[0][0][1] += __half2float(*reinterpret_cast<const __half*>(scale + 64)) * (f * (d[2] + d[3]));
+              continue;
+            }
             uint4 w[RT][2];
             uint2 sc[RT][2];
 #pragma unroll
@@ -291,7 +305,6 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
                 sc[rt][h] = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + h * 64 + r8 * 8);
               }
             }
-            const int gl = (strip0 + u) * 4 - g0;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               uint32_t a0[RT][4], a1[RT][4];
@@ -302,24 +315,22 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
                 for (int h = 0; h < 2; ++h) {
                   const uint4& v = w[rt][h];
                   const uint32_t p = g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w, p8 = p >> 8;
-                  a0[rt][h] = p & 0x000F000Fu;
-                  a0[rt][2 + h] = p & 0x00F000F0u;
-                  a1[rt][h] = p8 & 0x000F000Fu;
-                  a1[rt][2 + h] = p8 & 0x00F000F0u;
+                  a0[rt][h] = unpack.low(p);
+                  a0[rt][2 + h] = unpack.high(p);
+                  a1[rt][h] = unpack.low(p8);
+                  a1[rt][2 + h] = unpack.high(p8);
                   const uint32_t sw = g < 2 ? sc[rt][h].x : sc[rt][h].y;
                   const __half2 hs = *reinterpret_cast<const __half2*>(&sw);
                   ds[rt][h] = g & 1 ? __high2float(hs) : __low2float(hs);
                 }
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                const int col = ONE ? r8 & 1 : t * 8 + r8;  // (one vector: the other columns repeat its two)
-                const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl + g) * NC + col) * 4 + c) * 16);
-                const float4 z = zs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
-                const float f = fs[(gl + g) * (NC / 2) + (ONE ? 0 : t * 4 + c)];
+                const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl + g) * NC + t * 8 + r8) * 4 + c) * 16);
+                const float f = fs[(gl + g) * (NC / 2) + t * 4 + c];
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                   float d[4];
-                  mma_f16(d, a0[rt], xv.x, xv.y, z.x, z.y, z.z, z.w);
+                  mma_f16(d, a0[rt], xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
                   mma_f16(d, a1[rt], xv.z, xv.w);
                   acc[rt][t][0] += ds[rt][0] * (f * (d[0] + d[1]));
                   acc[rt][t][1] += ds[rt][1] * (f * (d[2] + d[3]));
@@ -328,6 +339,13 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
             }
           }
           __syncwarp();  // every lane has read the stage before it is filled again
+        }
+        if constexpr (ONE) {  // (the groups' sums, the same in the four lanes of a row)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            acc[0][0][h] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][0][h], 1);
+            acc[0][0][h] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][0][h], 2);
+          }
         }
         // (each lane read the timer for itself: one that ran out speaks for the warp, whose sums hold its share)
         if (__any_sync(0xFFFFFFFFu, dead)) {
