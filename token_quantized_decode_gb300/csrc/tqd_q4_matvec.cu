@@ -43,17 +43,16 @@ __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t r
 constexpr int kMvWarps = 8;
 constexpr int kMvCtas = 304;  // two per SM
 constexpr int kMvThreads = 32 * kMvWarps;
-// Strips of a stage, and stages of a warp's ring (nt: tiles of 8 columns, rt: row
-// tiles at once).  Four strips a stage for few columns (151936 x 1024 of one vector 18.7
-// us, with two 20.1; 151936 x 8192 109 and 123), fewer where the staged vectors
-// need the room.
+// Strips of a stage, and stages of a warp's ring (nt: tiles of 8 columns).  Four
+// strips a stage for few columns (151936 x 1024 of one vector 18.7 us, with two 20.1;
+// 151936 x 8192 109 and 123), fewer where the staged vectors need the room.
 __host__ __device__ constexpr int mv_chunk(int nt) { return nt == 4 ? 1 : nt == 1 ? 4 : 2; }
-__host__ __device__ constexpr int mv_stages(int nt, int rt) { return nt == 4 && rt == 1 ? 3 : 2; }
+__host__ __device__ constexpr int mv_stages(int nt) { return nt == 4 ? 3 : 2; }
 // Shared memory of a CTA: at most what lets two of them share an SM; the rings
 // and the warps' sums, then the staged vectors.
 constexpr int kMvSmem = 113 * 1024;
-constexpr int mv_fixed_smem(int nt, int rt) {
-  return kMvWarps * (mv_stages(nt, rt) * (rt * mv_chunk(nt) * kQ4TileBytes + 8) + rt * 2 * nt * 128);
+constexpr int mv_fixed_smem(int nt) {
+  return kMvWarps * (mv_stages(nt) * (mv_chunk(nt) * kQ4TileBytes + 8) + 2 * nt * 128);
 }
 constexpr int mv_strip_smem(int cols) { return 4 * (cols * 64 + cols / 2 * 4); }
 
@@ -64,7 +63,6 @@ struct MatvecQ4Args {
   int64_t xs, ys;
   int rows, groups, n;   // groups: columns / 32
   int row_tiles, strips; // of 16 rows, of 128 columns
-  int tiles;             // RT row tiles each
   int slab;              // strips whose x is staged at a time
   int wk;                // warps that share a row tile's strips (1, 2, 4, 8)
   int cluster;           // CTAs of a cluster, each with a part of the strips (1, 2, 4, 8)
@@ -100,11 +98,11 @@ struct MatvecQ4Args {
 // strips (so each stages a part of the vectors) and adds its sums through
 // distributed shared memory; with less than 8 row tiles the warps of a CTA share
 // them too.
-template <int NT, int RT, bool ONE>
+template <int NT, bool ONE>
 __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   constexpr int NC = ONE ? 2 : 8 * NT;  // staged columns: high and low part of each vector
-  constexpr int NS = RT * 2 * NT;  // a lane's sums
-  constexpr int kMvStages = mv_stages(NT, RT), kChunk = mv_chunk(NT), kStage = RT * kChunk * kQ4TileBytes;
+  constexpr int NS = 2 * NT;  // a lane's sums
+  constexpr int kMvStages = mv_stages(NT), kChunk = mv_chunk(NT), kStage = kChunk * kQ4TileBytes;
   extern __shared__ __align__(128) unsigned char sm[];
   unsigned char* ring = sm;
   float* red = reinterpret_cast<float*>(ring + kMvWarps * kMvStages * kStage);  // [warps][NS][32]
@@ -122,7 +120,7 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   const int cta0 = blockIdx.x / a.cluster * slots;  // the cluster's first slot
   const int slot = cta0 + warp / a.wk;
   const int cs0 = a.strips * rank / a.cluster, cs1 = a.strips * (rank + 1) / a.cluster;  // the CTA's strips
-  const int tile0 = slot * a.per_slot, tile1 = min(tile0 + a.per_slot, a.tiles);
+  const int tile0 = slot * a.per_slot, tile1 = min(tile0 + a.per_slot, a.row_tiles);
   const int v0 = blockIdx.y * 16, nv = min(a.n - v0, ONE ? 1 : 4 * NT);
   const float* x = a.x + v0 * a.xs;
   float* y = a.y + v0 * a.ys;
@@ -163,17 +161,12 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
         if (b == e) ptile = tile1 - 1;  // (fewer strips than warps)
       } while (b == e);
       left = e - b;
-      src = a.w + (static_cast<size_t>(ptile) * RT * a.strips + b) * kQ4TileBytes;
+      src = a.w + (static_cast<size_t>(ptile) * a.strips + b) * kQ4TileBytes;
     }
     const int n = min(left, kChunk);
     if (lane == 0) {
-      const int has = min(RT, a.row_tiles - ptile * RT);  // (what lies behind the last row tile is not stored)
-      mbar_arrive_expect_tx(&bar[pst], has * n * kQ4TileBytes);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        if (rt < has)
-          bulk_g2s(my_ring + pst * kStage + rt * kChunk * kQ4TileBytes, src + static_cast<size_t>(rt) * a.strips * kQ4TileBytes,
-                   n * kQ4TileBytes, &bar[pst]);
+      mbar_arrive_expect_tx(&bar[pst], n * kQ4TileBytes);
+      bulk_g2s(my_ring + pst * kStage, src, n * kQ4TileBytes, &bar[pst]);
     }
     pst = pst + 1 == kMvStages ? 0 : pst + 1;
     src += kChunk * kQ4TileBytes;
@@ -250,11 +243,9 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
     share(slab, b, e);
     for (int k = 0; k < a.per_slot; ++k) {
       const int tile = tile0 + k;
-      float acc[RT][NT][2];
+      float acc[NT][2];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[rt][t][0] = acc[rt][t][1] = 0.f;
+      for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = 0.f;
       if (tile < tile1) {
         for (int strip0 = b; strip0 < e; strip0 += kChunk) {
           issue();
@@ -268,20 +259,31 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
           for (int u = 0; u < kChunk; ++u) {
             if (u && strip0 + u >= e) break;
             const int gl = (strip0 + u) * 4 - g0;
+            const unsigned char* tl = stage + u * kQ4TileBytes;
+            const uint4 w0 = *reinterpret_cast<const uint4*>(tl + lane * 16), w1 = *reinterpret_cast<const uint4*>(tl + 512 + lane * 16);
+            // the operands of a group: rows r8 and r8 + 8
+            auto operands = [&](int g, uint32_t (&a0)[4], uint32_t (&a1)[4]) {
+              const uint32_t p = g == 0 ? w0.x : g == 1 ? w0.y : g == 2 ? w0.z : w0.w;
+              const uint32_t q = g == 0 ? w1.x : g == 1 ? w1.y : g == 2 ? w1.z : w1.w;
+              a0[0] = unpack.low(p);
+              a0[1] = unpack.low(q);
+              a0[2] = unpack.high(p);
+              a0[3] = unpack.high(q);
+              a1[0] = unpack.low(p >> 8);
+              a1[1] = unpack.low(q >> 8);
+              a1[2] = unpack.high(p >> 8);
+              a1[3] = unpack.high(q >> 8);
+            };
             if constexpr (ONE) {
               // the strip's four groups in the four column pairs, so that a lane takes the sums of
               // one of them, group c, and not of all four
-              const unsigned char* tl = stage + u * kQ4TileBytes;
-              const uint4 w0 = *reinterpret_cast<const uint4*>(tl + lane * 16), w1 = *reinterpret_cast<const uint4*>(tl + 512 + lane * 16);
               const unsigned char* scale = tl + kQ4TileScales + r8 * 8 + c * 2;
               const unsigned char* own = xs + (((gl + (r8 >> 1)) * 2 + (r8 & 1)) * 4 + c) * 16;
               float d[4];
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
-                const uint32_t p = g == 0 ? w0.x : g == 1 ? w0.y : g == 2 ? w0.z : w0.w;
-                const uint32_t q = g == 0 ? w1.x : g == 1 ? w1.y : g == 2 ? w1.z : w1.w;
-                const uint32_t a0[4] = {unpack.low(p), unpack.low(q), unpack.high(p), unpack.high(q)};
-                const uint32_t a1[4] = {unpack.low(p >> 8), unpack.low(q >> 8), unpack.high(p >> 8), unpack.high(q >> 8)};
+                uint32_t a0[4], a1[4];
+                operands(g, a0, a1);
                 const uint4 xv = *reinterpret_cast<const uint4*>(r8 >> 1 == g ? own : reinterpret_cast<const unsigned char*>(&none));
                 if (g == 0)
                   mma_f16(d, a0, xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
@@ -290,51 +292,27 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
                 mma_f16(d, a1, xv.z, xv.w);
               }
               const float f = fs[gl + c];
-              acc[0][0][0] += __half2float(*reinterpret_cast<const __half*>(scale)) * (f * (d[0] + d[1]));
-              acc[0][0][1] += __half2float(*reinterpret_cast<const __half*>(scale + 64)) * (f * (d[2] + d[3]));
+              acc[0][0] += __half2float(*reinterpret_cast<const __half*>(scale)) * (f * (d[0] + d[1]));
+              acc[0][1] += __half2float(*reinterpret_cast<const __half*>(scale + 64)) * (f * (d[2] + d[3]));
               continue;
             }
-            uint4 w[RT][2];
-            uint2 sc[RT][2];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              const unsigned char* tl = stage + (rt * kChunk + u) * kQ4TileBytes;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                w[rt][h] = *reinterpret_cast<const uint4*>(tl + h * 512 + lane * 16);
-                sc[rt][h] = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + h * 64 + r8 * 8);
-              }
-            }
+            const uint2 sc0 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + r8 * 8);
+            const uint2 sc1 = *reinterpret_cast<const uint2*>(tl + kQ4TileScales + 64 + r8 * 8);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              uint32_t a0[RT][4], a1[RT][4];
-              float ds[RT][2];
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint4& v = w[rt][h];
-                  const uint32_t p = g == 0 ? v.x : g == 1 ? v.y : g == 2 ? v.z : v.w, p8 = p >> 8;
-                  a0[rt][h] = unpack.low(p);
-                  a0[rt][2 + h] = unpack.high(p);
-                  a1[rt][h] = unpack.low(p8);
-                  a1[rt][2 + h] = unpack.high(p8);
-                  const uint32_t sw = g < 2 ? sc[rt][h].x : sc[rt][h].y;
-                  const __half2 hs = *reinterpret_cast<const __half2*>(&sw);
-                  ds[rt][h] = g & 1 ? __high2float(hs) : __low2float(hs);
-                }
+              uint32_t a0[4], a1[4];
+              operands(g, a0, a1);
+              const float2 s0 = unpack_f16(g < 2 ? sc0.x : sc0.y), s1 = unpack_f16(g < 2 ? sc1.x : sc1.y);
+              const float ds0 = g & 1 ? s0.y : s0.x, ds1 = g & 1 ? s1.y : s1.x;
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
                 const uint4 xv = *reinterpret_cast<const uint4*>(xs + (((gl + g) * NC + t * 8 + r8) * 4 + c) * 16);
                 const float f = fs[(gl + g) * (NC / 2) + t * 4 + c];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                  float d[4];
-                  mma_f16(d, a0[rt], xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
-                  mma_f16(d, a1[rt], xv.z, xv.w);
-                  acc[rt][t][0] += ds[rt][0] * (f * (d[0] + d[1]));
-                  acc[rt][t][1] += ds[rt][1] * (f * (d[2] + d[3]));
-                }
+                float d[4];
+                mma_f16(d, a0, xv.x, xv.y, 0.f, 0.f, 0.f, 0.f);
+                mma_f16(d, a1, xv.z, xv.w);
+                acc[t][0] += ds0 * (f * (d[0] + d[1]));
+                acc[t][1] += ds1 * (f * (d[2] + d[3]));
               }
             }
           }
@@ -343,8 +321,8 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
         if constexpr (ONE) {  // (the groups' sums, the same in the four lanes of a row)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            acc[0][0][h] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][0][h], 1);
-            acc[0][0][h] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][0][h], 2);
+            acc[0][h] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][h], 1);
+            acc[0][h] += __shfl_xor_sync(0xFFFFFFFFu, acc[0][h], 2);
           }
         }
         // (each lane read the timer for itself: one that ran out speaks for the warp, whose sums hold its share)
@@ -352,14 +330,12 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
           if (!stopped) mbar_ring_drain(bar, kMvStages, st, phase);
           dead = stopped = true;
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[rt][t][0] = acc[rt][t][1] = __int_as_float(0x7FC00000);
+          for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = __int_as_float(0x7FC00000);
         }
       }
-      auto store = [&](int of, int i, int l, float sum) {  // sum i of lane l: [row tile][4 vectors][half of the rows]
-        const int v = i / 2 % NT * 4 + (l & 3);
-        const int64_t r = (static_cast<int64_t>(of) * RT + i / (2 * NT)) * 16 + i % 2 * 8 + (l >> 2);
+      auto store = [&](int of, int i, int l, float sum) {  // sum i of lane l: [4 vectors][half of the rows]
+        const int v = i / 2 * 4 + (l & 3);
+        const int64_t r = static_cast<int64_t>(of) * 16 + i % 2 * 8 + (l >> 2);
         if (v >= nv || r >= a.rows) return;
         float* p = y + v * a.ys + r;
         *p = slab ? *p + sum : sum;
@@ -367,12 +343,12 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
       if (a.wk * a.cluster == 1) {
         if (tile < tile1)
 #pragma unroll
-          for (int i = 0; i < NS; ++i) store(tile, i, lane, acc[i / (2 * NT)][i / 2 % NT][i % 2]);
+          for (int i = 0; i < NS; ++i) store(tile, i, lane, acc[i / 2][i % 2]);
         continue;
       }
       float* mine = red + warp * NS * 32 + lane;
 #pragma unroll
-      for (int i = 0; i < NS; ++i) mine[i * 32] = acc[i / (2 * NT)][i / 2 % NT][i % 2];
+      for (int i = 0; i < NS; ++i) mine[i * 32] = acc[i / 2][i % 2];
       if (a.cluster == 1)
         __syncthreads();
       else
@@ -395,23 +371,22 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
   }
 }
 
-template <int NT, int RT, bool ONE>
+template <int NT, bool ONE>
 cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   constexpr int NC = ONE ? 2 : 8 * NT;
-  constexpr int most = (kMvSmem - mv_fixed_smem(NT, RT)) / mv_strip_smem(NC);  // strips whose vectors fit
+  constexpr int most = (kMvSmem - mv_fixed_smem(NT)) / mv_strip_smem(NC);  // strips whose vectors fit
   // With less than eight row tiles the warps of a CTA share a tile's strips.  The
   // cluster is the one that costs a warp the fewest instructions: about 50 for
   // each octet of columns that it stages, 110 + 60 NT a strip, 500 to add a row tile's
   // sums through distributed shared memory.
-  a.tiles = (a.row_tiles + RT - 1) / RT;
   a.wk = 1;
-  while (a.wk < kMvWarps && a.tiles * a.wk < kMvWarps && a.wk * 2 <= a.strips) a.wk *= 2;
-  const int sweep = a.n < 16 ? a.n : 16, ctas = (a.tiles * a.wk + kMvWarps - 1) / kMvWarps;
+  while (a.wk < kMvWarps && a.row_tiles * a.wk < kMvWarps && a.wk * 2 <= a.strips) a.wk *= 2;
+  const int sweep = a.n < 16 ? a.n : 16, ctas = (a.row_tiles * a.wk + kMvWarps - 1) / kMvWarps;
   int64_t least = 0;
   for (int x = 1; x <= 8 && x * a.wk <= a.strips; x *= 2) {
     const int sweeps = (a.n + 15) / 16, room = kMvCtas / (x * sweeps);  // (sweeps run side by side; at most 4)
     const int64_t rounds = (ctas + room - 1) / room, each = (a.strips + x * a.wk - 1) / (x * a.wk);
-    const int64_t cost = static_cast<int64_t>(sweep) * a.strips * 6 / x + rounds * (each * RT * (110 + 60 * NT) + (x > 1 ? 500 : 0));
+    const int64_t cost = static_cast<int64_t>(sweep) * a.strips * 6 / x + rounds * (each * (110 + 60 * NT) + (x > 1 ? 500 : 0));
     if (x == 1 || cost < least) {
       least = cost;
       a.cluster = x;
@@ -419,16 +394,16 @@ cudaError_t launch_mv(MatvecQ4Args a, cudaStream_t st) {
   }
   const int strips = (a.strips + a.cluster - 1) / a.cluster, slabs = (strips + most - 1) / most;
   a.slab = (strips + slabs - 1) / slabs;
-  const size_t smem = static_cast<size_t>(mv_fixed_smem(NT, RT)) + static_cast<size_t>(a.slab) * mv_strip_smem(NC);
+  const size_t smem = static_cast<size_t>(mv_fixed_smem(NT)) + static_cast<size_t>(a.slab) * mv_strip_smem(NC);
   const int slots = kMvWarps / a.wk;
-  int blocks = (a.tiles + slots - 1) / slots;
+  int blocks = (a.row_tiles + slots - 1) / slots;
   if (blocks > kMvCtas / a.cluster) blocks = kMvCtas / a.cluster;
-  a.per_slot = (a.tiles + blocks * slots - 1) / (blocks * slots);
-  blocks = (a.tiles + a.per_slot * slots - 1) / (a.per_slot * slots);
+  a.per_slot = (a.row_tiles + blocks * slots - 1) / (blocks * slots);
+  blocks = (a.row_tiles + a.per_slot * slots - 1) / (a.per_slot * slots);
   static unsigned long long done = 0;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_q4_matvec<NT, RT, ONE>), kMvSmem, &done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_q4_matvec<NT, ONE>), kMvSmem, &done);
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(k_q4_matvec<NT, RT, ONE>, a.cluster, dim3(blocks * a.cluster, (a.n + 15) / 16), kMvThreads, smem,
+  return launch_pdl_clusters(k_q4_matvec<NT, ONE>, a.cluster, dim3(blocks * a.cluster, (a.n + 15) / 16), kMvThreads, smem,
                              st, a);
 }
 
@@ -454,14 +429,10 @@ cudaError_t launch_q4_matvec(const uint8_t* w, int rows, int cols, const float* 
   a.n = n;
   a.row_tiles = (rows + kQ4TileRows - 1) / kQ4TileRows;
   a.strips = (cols + kQ4TileCols - 1) / kQ4TileCols;
-  if (n == 1) return launch_mv<1, 1, true>(a, st);
-  if (n <= 4) return launch_mv<1, 1, false>(a, st);
-  if (n <= 8) return launch_mv<2, 1, false>(a, st);
-  // Two row tiles a warp read the staged vectors once for both: with two for every
-  // CTA, 151936 x 1024 of 16 took 51 us instead of 57, 16384 x 8192 67 instead of 76; with
-  // fewer, 4096 x 16384 64 instead of 44 and 1024 x 1024 9.2 instead of 7.6.
-  if (a.row_tiles < 2 * kMvCtas) return launch_mv<4, 1, false>(a, st);
-  return launch_mv<4, 2, false>(a, st);
+  if (n == 1) return launch_mv<1, true>(a, st);
+  if (n <= 4) return launch_mv<1, false>(a, st);
+  if (n <= 8) return launch_mv<2, false>(a, st);
+  return launch_mv<4, false>(a, st);
 }
 
 }  // namespace tqd
