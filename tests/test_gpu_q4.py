@@ -179,6 +179,34 @@ def test_append_codes_values_next_to_a_border_exactly(ops):
     assert np.array_equal(cache.pages.cpu().numpy(), host.pages)
 
 
+def test_append_scales_next_to_the_end_of_f16(ops):
+    """Rotated keys whose f32 rotation passes the largest scale (max / 7 = 65520) while the exact one does not, or the
+    other way round: by cancelling from far larger elements, or by lying within f32 rounding of it."""
+    rng = np.random.default_rng(29)
+    n, hd, page = 4096, 64, 16
+    host = Host(rng, 1, 1, hd, page, n, spare=0)
+    cache = host.device(ops)
+    table = rope_table(ops, hd, n)
+    t = table.cpu().numpy().astype(np.float64)
+    pos = np.arange(n)
+    c, s = t[:, :, 0], t[:, :, 1]
+    y = rng.normal(size=(n, hd)) * 1e4
+    i = rng.integers(0, 32, size=n)
+    far = rng.random(n) < 0.6
+    # one pair of a token: its first element becomes small or next to the end, the second large
+    y[pos, i] = np.where(far, 0.0, 7 * 65520.0 * (1 + rng.uniform(-3, 3, size=n) * 2.0**-24)) * rng.choice([-1, 1], n)
+    y[pos, i + 32] = np.where(far, 10.0 ** rng.uniform(11.5, 14, size=n), rng.choice([0.0, 4e5], n)) * rng.choice([-1, 1], n)
+    k = np.concatenate([y[:, :32] * c + y[:, 32:] * s, y[:, 32:] * c - y[:, :32] * s], 1).astype(np.float32)
+    v = rng.normal(size=(n, hd)).astype(np.float32)
+    v[:, 5] = (7 * 65520.0 * (1 + rng.integers(-3, 4, size=n) * 2.0**-24)).astype(np.float32)
+    ops.tqd_op_kv_append_q4(cache, dev(k), dev(v), i32(pos), i32(np.zeros(n)), table)
+    rk = q4.rotate(k[:, None].astype(np.float64), pos, table.cpu().numpy())
+    for p in range(n):
+        host.store(0, p, rk[p], v[p][None])
+    got, want = cache.pages.cpu().numpy(), host.pages
+    assert np.array_equal(got, want), int((got != want).any(1).sum())
+
+
 def test_append_without_rotation_padding_and_pages_outside_the_pool(ops):
     rng = np.random.default_rng(5)
     hd, n_kv, page = 128, 2, 16

@@ -32,15 +32,15 @@ __device__ __noinline__ Q4Code q4_code_exact(double y0, double y1, double y2, do
   double a = fmax(fmax(fabs(y0), fabs(y1)), fmax(fabs(y2), fabs(y3)));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) a = fmax(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+  const float d = __double2float_rn(a / 7.0);
   Q4Code r;
   r.codes = 0x8888u;
-  if (a > 0.0) {
+  if (a > 0.0 && d < 65520.f) {
     r.codes = static_cast<uint32_t>(__double2int_rn(7.0 * y0 / a) + 8);
     r.codes |= static_cast<uint32_t>(__double2int_rn(7.0 * y1 / a) + 8) << 4;
     r.codes |= static_cast<uint32_t>(__double2int_rn(7.0 * y2 / a) + 8) << 8;
     r.codes |= static_cast<uint32_t>(__double2int_rn(7.0 * y3 / a) + 8) << 12;
   }
-  const float d = __double2float_rn(a / 7.0);
   r.scale = d < 65520.f ? __half_as_ushort(__float2half_rn(d)) : 0x7E00u;
   return r;
 }
@@ -82,15 +82,16 @@ __device__ __forceinline__ Q4Code q4_code(const float (&y)[4], float M, bool& un
     r.codes |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * e);
   }
   unsure = far > edge;
+  const float slack = d * fmaf(rel, 2.3841858e-7f, 2.3841858e-7f);  // 2^-22 d (rel + 1)
   if (M > 0.f) {
-    const float slack = d * fmaf(rel, 2.3841858e-7f, 2.3841858e-7f);  // 2^-22
     unsure |= __half_as_ushort(__float2half_rn(d - slack)) != __half_as_ushort(__float2half_rn(d + slack)) || rel > 256.f;
   }
   if (!(a > 1e-30f && d < 65520.f)) {
     // All 0; so small that the steps above lose bits; or a NaN or an infinity
     // in the group, or a scale past the f16 range: the scale is NaN, so the
-    // group stands for NaN.
-    unsure = d < 65520.f && (a > 0.f || M > 0.f);
+    // group stands for NaN.  (A scale that the rotation's error may have taken
+    // past it is looked at again; that of a NaN or an infinity compares false.)
+    unsure = d < 65520.f ? a > 0.f || M > 0.f : M > 0.f && d - slack < 65520.f;
     r.codes = 0x8888u;
     r.scale = d < 65520.f ? 0u : 0x7E00u;
   }
