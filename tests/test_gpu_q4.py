@@ -435,6 +435,52 @@ def test_attention_small_values_next_to_large_ones(ops):
     check_attention(attend(ops, host.device(ops), q, [n]), q, [K], [V], [n], [1], hd)
 
 
+def check_weighted(got, q, K, V, hd):
+    """got [heads, hd] against 64 bits with the terms that an element's sum has: the error of a weight (the file's head:
+    2 * its score's error + 16 u) times sum_i p_i 7 scale_i over the element's own group."""
+    heads, n_kv = q.shape[0], K.shape[1]
+    for h in range(heads):
+        k, v = K[:, h // (heads // n_kv)], V[:, h // (heads // n_kv)]
+        sk = np.repeat(np.abs(k.reshape(len(k), -1, 32)).max(-1) / 7, 32, axis=1)
+        sv = np.repeat(np.abs(v.reshape(len(v), -1, 32)).max(-1) / 7, 32, axis=1)
+        s = k @ q[h] / math.sqrt(hd)
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        score = 16 * U * np.sqrt(((15 * sk * q[h]) ** 2).sum(-1)).max() / math.sqrt(hd) + 4 * U * np.abs(s).max()
+        tol = p @ (7 * sv) * (2 * score + 16 * U) + 1e-30
+        err = np.abs(got[h] - p @ v)
+        assert np.all(err <= tol), (h, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("heads,n_kv,hd", [(1, 1, 64), (1, 1, 128), (2, 1, 128), (4, 1, 128), (8, 1, 128), (3, 1, 64),
+                                           (8, 1, 64)])
+@pytest.mark.parametrize("room", [0, 100000])
+@pytest.mark.parametrize("large", [0, 40, 299])
+def test_attention_large_values_of_no_weight(ops, heads, n_kv, hd, room, large):
+    """A position with values 2^24 times the others' that the queries hardly see (weights of 2^-60): the others keep
+    their accuracy, wherever it lies.  And the other way round: the position that has nearly all the weight has values
+    2^-20 of the others', or none (scale 0)."""
+    rng = np.random.default_rng(heads + hd + large)
+    n = 300
+    key = rng.choice([-1.0, 1.0], size=hd)
+    cases = [(-1.0, 2.0**24, 2.0**-12), (1.0, 2.0**-20, 1.0), (1.0, 0.0, 1.0)]
+    host = Host(rng, len(cases), n_kv, hd, 16, n, room=room)
+    K, V = [], []
+    for s, (sign, gain, base) in enumerate(cases):
+        rows = []
+        for p in range(n):
+            k = key * sign if p == large else rng.normal(size=hd) * 0.1
+            v = rng.normal(size=hd) * base * (gain if p == large else 1.0)
+            rows.append(host.store(s, p, k[None], v[None]))
+        K.append(np.array([r[0] for r in rows]))
+        V.append(np.array([r[1] for r in rows]))
+    q = np.concatenate([np.tile(key * 41.6 / math.sqrt(hd), heads)[None] * (1.0 if s == 0 else 0.5)
+                        for s in range(len(cases))]).astype(np.float32)
+    got = attend(ops, host.device(ops), q, [n] * len(cases))
+    for s in range(len(cases)):
+        check_weighted(got[s].reshape(heads, hd), q[s].reshape(heads, hd).astype(np.float64), K[s], V[s], hd)
+
+
 def test_attention_scales_of_either_sign(ops):
     """Pages that a program wrote itself: any finite f16 is a scale, and a negative one can be the largest by far."""
     rng = np.random.default_rng(27)

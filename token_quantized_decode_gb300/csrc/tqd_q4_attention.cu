@@ -2,11 +2,13 @@
 // several queries per sequence.
 //
 // Mathematics.  Scores are kept in units of log2 (q is multiplied by
-// log2(e) / sqrt(hd)), the running reference of a row is ref = M + ex - 11 with M
-// its largest score so far and 2^ex above the largest V scale so far, and with
-// p = 2^(score - ref) the row is (sum p v) / (sum p), rescaled when M or the V
-// scale grows past a slack of 2 octaves.  K and V elements are (code - 8) * scale,
-// so  q . k = sum over groups scale_g (sum_d q_d code_d - 8 sum_d q_d)  and
+// log2(e) / sqrt(hd)), and with p = 2^(score - ref) a row is (sum p v) / (sum p).  The
+// running reference of a row goes by its largest product p * V scale so far,
+// which it keeps between 2^12 and 2^15; all sums are rescaled when it moves.  (By
+// the largest score and the largest scale, which may be of two positions, a
+// position of no weight with values 2^24 times the others' left these 11 bits; it
+// costs 1 % at 131072 positions.)  K and V elements are (code - 8) * scale, so
+// q . k = sum over groups scale_g (sum_d q_d code_d - 8 sum_d q_d)  and
 // sum_t p_t v_t = sum_t (p_t scale_t) (code_t - 8).  (The second is not split like
 // the first: over many positions sum p code is 8 sum p but for a small rest,
 // and the rest is the result.)
@@ -28,9 +30,10 @@
 // (NT = 2) two column tiles share the unpacked cache.
 //
 // Split.  The unit is 32 positions of one segment: (sequence, kv head, tile of
-// query rows).  Units, and a few empty ones at each segment's beginning for what that
-// costs, are laid end to end and each warp takes an equal run of them, whatever the lengths, with a running softmax for each segment it meets.
-// A segment inside a warp's run is written out by the warp alone; the partial
+// query rows).  Units, and a few empty ones at each segment's beginning for what
+// that costs, are laid end to end and each warp takes an equal run of them,
+// whatever the lengths, with a running softmax for each segment it meets.  A
+// segment inside a warp's run is written out by the warp alone; the partial
 // results (ref, sum p, sum p v) of one that several warps of a CTA share are
 // joined in shared memory at the CTA's end, and those of one that several CTAs
 // share by a second kernel, already launched (programmatic dependent launch).  The
@@ -64,6 +67,7 @@ constexpr int kCtas = 304;      // two per SM
 constexpr int kUnit = 32;       // positions of a unit: two blocks
 constexpr int kCombine = 256;   // threads of the joining kernel
 constexpr float kNaN = __builtin_nanf("");
+constexpr float kNoRef = -3.402823466e38f;  // the reference of a row that has seen no position
 
 // One instantiation: head size, column tiles, groups side by side.
 template <int HD, int NT, int GV>
@@ -110,6 +114,18 @@ __device__ __forceinline__ void add_f32x2(float& x0, float& x1, float y0, float 
   asm("{\n.reg .b64 x, y;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %3};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
       : "+f"(x0), "+f"(x1)
       : "f"(y0), "f"(y1));
+}
+
+// Two products, and two sums of squares, by one instruction.
+__device__ __forceinline__ void mul_f32x2(float& x0, float& x1, float a0, float a1, float b0, float b1) {
+  asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
+      : "=f"(x0), "=f"(x1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void square_f32x2(float& s0, float& s1, float x0, float x1) {
+  asm("{\n.reg .b64 x, y;\nmov.b64 x, {%0, %1};\nmov.b64 y, {%2, %3};\nfma.rn.f32x2 x, y, y, x;\nmov.b64 {%0, %1}, x;\n}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(x0), "f"(x1));
 }
 
 // x as two f16 parts in one word: the leading 11 bits low, the rest high.
@@ -468,12 +484,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       }
     }
 
-    float o[NT][NG * 2][4], l[NT], M[NT], ref[NT], S = 0.f;
+    float o[NT][NG * 2][4], l[NT], ref[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       l[t] = 0.f;
-      M[t] = -INFINITY;
-      ref[t] = 0.f;
+      ref[t] = kNoRef;
 #pragma unroll
       for (int i = 0; i < NG * 2; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
     }
@@ -483,34 +498,41 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
     const int b0 = 4 * (r >> 1) + (r & 1), b1 = b0 + 2;
     auto blocks = [&](auto masked_c, const unsigned char* from, int t0, int bad) {
       constexpr bool masked = decltype(masked_c)::value;
-      float sc[NT][2 * JB], vs[2 * JB][NS];  // positions b0, b1 of each block
-      __half2 vmax = __float2half2_rn(0.f);
-      auto scales = [&](const unsigned char* p, float (&d)[NS]) {
-        __half2 top;
+      float sc[NT][2 * JB];  // positions b0, b1 of each block
+      const int at0 = (b0 * NG + gv * NS) * 2, at1 = (b1 * NG + gv * NS) * 2;  // their scales
+      constexpr int SW = NS == 4 ? 2 : 1;  // words of a position's scales
+      auto scale_words = [&](const unsigned char* p, uint32_t (&w)[SW]) {
         if constexpr (NS == 4) {
-          const uint2 w = *reinterpret_cast<const uint2*>(p);
-          const __half2 x = *reinterpret_cast<const __half2*>(&w.x), y = *reinterpret_cast<const __half2*>(&w.y);
-          d[0] = __low2float(x); d[1] = __high2float(x); d[2] = __low2float(y); d[3] = __high2float(y);
-          top = __hmax2(__habs2(x), __habs2(y));
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          w[0] = v.x;
+          w[1] = v.y;
         } else if constexpr (NS == 2) {
-          const __half2 x = *reinterpret_cast<const __half2*>(p);
-          d[0] = __low2float(x); d[1] = __high2float(x);
-          top = __habs2(x);
+          w[0] = *reinterpret_cast<const uint32_t*>(p);
         } else {
-          const __half2 x = __half2half2(*reinterpret_cast<const __half*>(p));
-          d[0] = __low2float(x);
-          top = __habs2(x);
+          w[0] = *reinterpret_cast<const uint16_t*>(p);
         }
-        return top;
       };
+      auto scales = [&](const uint32_t (&w)[SW], float (&d)[NS]) {
+#pragma unroll
+        for (int i = 0; i < SW; ++i) {
+          const float2 x = unpack_f16(w[i]);
+          d[2 * i] = x.x;
+          if constexpr (NS > 1) d[2 * i + 1] = x.y;
+        }
+      };
+      uint32_t vw[2 * JB][SW];  // the V scales as they lie
 #pragma unroll
       for (int j = 0; j < JB; ++j) {
         const unsigned char* blk = from + j * BB;
         // scores of the block's two positions
         float ks0[NS], ks1[NS];
-        const int at0 = (b0 * NG + gv * NS) * 2, at1 = (b1 * NG + gv * NS) * 2;
-        scales(blk + q4_ks_off(HD) + at0, ks0);
-        scales(blk + q4_ks_off(HD) + at1, ks1);
+        uint32_t kw0[SW], kw1[SW];
+        scale_words(blk + q4_ks_off(HD) + at0, kw0);
+        scale_words(blk + q4_ks_off(HD) + at1, kw1);
+        scales(kw0, ks0);
+        scales(kw1, ks1);
+        scale_words(blk + q4_vs_off(HD) + at0, vw[2 * j]);
+        scale_words(blk + q4_vs_off(HD) + at1, vw[2 * j + 1]);
         uint32_t k0[NG], k1[NG];
         const unsigned char* kr = blk + r * (HD / 2) + c * (4 * NG);
         if constexpr (HD == 128) {
@@ -559,48 +581,69 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           sc[t][2 * j] = s0;
           sc[t][2 * j + 1] = s1;
         }
-        vmax = __hmax2(vmax, __hmax2(scales(blk + q4_vs_off(HD) + at0, vs[2 * j]),
-                                     scales(blk + q4_vs_off(HD) + at1, vs[2 * j + 1])));
-      }
-      float bs = fmaxf(__low2float(vmax), __high2float(vmax));
-      if (masked) {  // scales behind the end of every row: bytes that no position wrote
-        int most = 0;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) most = max(most, seen[t]);
-        bs = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * JB; ++i)
-#pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            if (t0 + (i >> 1) * kQ4Block + (i & 1 ? b1 : b0) >= most || (bad >> (i >> 1) & 1)) vs[i][k] = 0.f;
-            bs = fmaxf(bs, fabsf(vs[i][k]));
-          }
       }
 
-      // the reference: kept while neither the scores nor the V scales grow past the slack
-      bool grow = bs > 4.f * S;
-      float bm[NT];
+      // p * scale as column operands.  The reference stays while a lane's products have
+      // a sum of squares up to 2^30, so each is at most 2^15 (f16 ends at 2^16), and no
+      // sum of p passes 2^100; else it moves to where the largest product is 2^12, or to
+      // 60 below the largest score where that is more (a position whose scale is 0
+      // has a p too).  Squares, two to an operation, cost less than maxima.
+      uint32_t pb[JB][NT][NS][2];
+      float sum[NT];
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        // (converted within the loop: as f32 they would take more registers on the other path)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        bm[t] = fmaxf(sc[t][0], sc[t][1]);
-        if constexpr (JB == 2) bm[t] = fmaxf(bm[t], fmaxf(sc[t][2], sc[t][3]));
-        grow |= bm[t] > M[t] + 2.f;
-      }
-      if (__any_sync(0xFFFFFFFFu, grow)) {
+        for (int i = 0; i < 2 * JB * SW; ++i) asm volatile("" : "+r"(vw[i / SW][i % SW]));
+        float top0 = 0.f, top1 = 0.f;
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) bs = fmaxf(bs, __shfl_xor_sync(0xFFFFFFFFu, bs, x));
-        S = fmaxf(bs, S);
-        const int ex = max(static_cast<int>(__float_as_uint(S) >> 23) - 126, -24);
+        for (int t = 0; t < NT; ++t) sum[t] = l[t];
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+          float vs0[NS], vs1[NS];
+          scales(vw[2 * j], vs0);
+          scales(vw[2 * j + 1], vs1);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float p0 = ex2(sc[t][2 * j] - ref[t]), p1 = ex2(sc[t][2 * j + 1] - ref[t]);
+            sum[t] += p0 + p1;
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+              float w0, w1;
+              mul_f32x2(w0, w1, p0, p1, vs0[k], vs1[k]);
+              if (masked) {  // a NaN scale of a position that this row does not see
+                if (t0 + j * kQ4Block + b0 >= seen[t] || (bad >> j & 1)) w0 = 0.f;
+                if (t0 + j * kQ4Block + b1 >= seen[t] || (bad >> j & 1)) w1 = 0.f;
+              }
+              square_f32x2(top0, top1, w0, w1);
+              pb[j][t][k][0] = transpose_f16(split_f16(w0));
+              pb[j][t][k][1] = transpose_f16(split_f16(w1));
+            }
+          }
+        }
+        bool grow = !(top0 + top1 <= 0x1p30f);  // (a NaN may hide another one)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) grow |= sum[t] > 0x1p100f;
+        if (!__any_sync(0xFFFFFFFFu, grow) || again) break;
+        float best[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) best[t] = ref[t];
+#pragma unroll
+        for (int i = 0; i < 2 * JB; ++i) {
+          float v[NS], size = 0.f;
+          scales(vw[i], v);
+#pragma unroll
+          for (int k = 0; k < NS; ++k) size = fmaxf(size, fabsf(v[k]) <= 65504.f ? fabsf(v[k]) : 0.f);  // (not NaN or infinite)
+          const float high = fmaxf(__log2f(size) - 12.f, -60.f);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) best[t] = fmaxf(best[t], sc[t][i] + high);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float m2 = bm[t];
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, x));
-          m2 = fmaxf(m2, M[t]);
-          const float nref = m2 == -INFINITY ? 0.f : m2 + static_cast<float>(ex - 11);
-          const float k = M[t] == -INFINITY ? 1.f : ex2(ref[t] - nref);
-          M[t] = m2;
-          ref[t] = nref;
+          for (int x = 4; x < 32; x <<= 1) best[t] = fmaxf(best[t], __shfl_xor_sync(0xFFFFFFFFu, best[t], x));
+          const float k = ex2(ref[t] - best[t]);
+          ref[t] = best[t];
           l[t] *= k;
 #pragma unroll
           for (int i = 0; i < NG * 2; ++i) {
@@ -608,26 +651,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
           }
         }
       }
-
-      // p * scale as column operands
-      uint32_t pb[JB][NT][NS][2];
 #pragma unroll
-      for (int j = 0; j < JB; ++j)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float p0 = ex2(sc[t][2 * j] - ref[t]), p1 = ex2(sc[t][2 * j + 1] - ref[t]);
-          l[t] += p0 + p1;
-#pragma unroll
-          for (int k = 0; k < NS; ++k) {
-            float w0 = p0 * vs[2 * j][k], w1 = p1 * vs[2 * j + 1][k];
-            if (masked) {  // a NaN scale of a position that this row does not see
-              if (t0 + j * kQ4Block + b0 >= seen[t] || (bad >> j & 1)) w0 = 0.f;
-              if (t0 + j * kQ4Block + b1 >= seen[t] || (bad >> j & 1)) w1 = 0.f;
-            }
-            pb[j][t][k][0] = transpose_f16(split_f16(w0));
-            pb[j][t][k][1] = transpose_f16(split_f16(w1));
-          }
-        }
+      for (int t = 0; t < NT; ++t) l[t] = sum[t];
       // Sums of V: those of the blocks at hand by MMA, to the running ones by
       // rounded adds (the MMA truncates: 100 in a row lose 2e-6 of a long average).
       uint4 v0[JB];
@@ -755,7 +780,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
             }
           }
         if (r == 0) {
-          to[R * LD + t * 4 + c] = M[t] == -INFINITY && l[t] == 0.f ? -INFINITY : ref[t];
+          to[R * LD + t * 4 + c] = ref[t] == kNoRef && l[t] == 0.f ? -INFINITY : ref[t];
           to[R * LD + P + t * 4 + c] = l[t];
         }
       }
