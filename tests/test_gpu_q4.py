@@ -648,6 +648,72 @@ def test_attention_many_sequences(ops):
     check_attention(got, q, host.K, host.V, lens, [1] * n_seq, hd)
 
 
+def random_blocks(g, n, hd):
+    """n cache blocks [n, 18 * hd] of any codes, with scales of either size: K's 0.05 .. 0.15, V's 0.01 .. 1."""
+    b = torch.randint(0, 256, (n, 18 * hd), generator=g, device="cuda", dtype=torch.uint8)
+    ks = 0.05 + 0.1 * torch.rand(n, hd // 2, generator=g, device="cuda")
+    vs = 10.0 ** (-2 * torch.rand(n, hd // 2, generator=g, device="cuda"))
+    b[:, 8 * hd:9 * hd] = ks.half().view(torch.uint8)
+    b[:, 17 * hd:] = vs.half().view(torch.uint8)
+    return b
+
+
+def block_values(b, hd):
+    """K and V values f64 [n, 16, hd] of blocks [n, 18 * hd]."""
+    def f16(at):
+        at = torch.from_numpy(at).cuda()
+        return torch.stack([b[:, at], b[:, at + 1]], -1).view(torch.float16)[..., 0].double().repeat_interleave(32, 1)
+    K, V = [], []
+    for p in range(16):
+        (kb, ksh), (vb, vsh), ksb, vsb = q4._nibble_places(p, hd)
+        for out, at, sh, sc in ((K, kb, ksh, ksb), (V, vb, vsh, vsb)):
+            code = (b[:, torch.from_numpy(at).cuda()].int() >> torch.from_numpy(sh).cuda().int()) & 15
+            out.append((code - 8).double() * f16(sc))
+    return torch.stack(K, 1), torch.stack(V, 1)
+
+
+@pytest.mark.parametrize("heads,n_kv,hd,n_seq,length,nq", [
+    (8, 1, 128, 1, 131067, 1), (8, 1, 64, 1, 131067, 1), (8, 1, 128, 1, 131067, 3), (4, 1, 128, 1, 131072, 1),
+    (2, 1, 128, 1, 130000, 1), (1, 1, 128, 1, 131041, 1), (3, 1, 64, 1, 131072, 2),
+    (32, 8, 128, 64, 8190, 1), (64, 8, 128, 64, 8190, 1), (32, 8, 64, 64, 8190, 1), (16, 8, 128, 64, 8190, 2),
+    (32, 4, 64, 64, 8190, 3)])
+def test_attention_of_long_runs(ops, heads, n_kv, hd, n_seq, length, nq):
+    """A warp's run of more than 32 units (its pages are looked up 32 at a time), and segments that over 250 CTAs
+    share.  Pages are filled on the device and shared by the sequences; some heads are compared."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(heads * 1000 + hd + length + nq)
+    page, G = 64, heads // n_kv
+    n_pages = 2100 if n_seq == 1 else 600
+    blocks = random_blocks(g, n_pages * n_kv * (page // 16), hd)
+    per_seq = -(-length // page)
+    table = torch.stack([torch.randperm(n_pages, generator=g, device="cuda")[:per_seq] for _ in range(n_seq)]).to(torch.int32)
+    cache = ops.kv_q4(blocks.view(n_pages, -1), table.contiguous(), n_kv, hd, page)
+    lens = [length - 3 * (s % 7) for s in range(n_seq)]
+    q = torch.randn(n_seq * nq, heads * hd, generator=g, device="cuda") * (3.0 if nq == 1 else 1.0)
+    start = None if nq == 1 else [nq * s for s in range(n_seq + 1)]
+    got = torch.from_numpy(attend(ops, cache, q, lens, start)).cuda()
+    rng = np.random.default_rng(length)
+    for s in {0, n_seq - 1, *rng.integers(0, n_seq, size=3).tolist()}:
+        h = int(rng.integers(n_kv))
+        at = (table[s].long()[:, None] * n_kv + h) * (page // 16) + torch.arange(page // 16, device="cuda")
+        k, v = block_values(blocks[at.reshape(-1)], hd)
+        k, v = k.reshape(-1, hd), v.reshape(-1, hd)
+        for i in range(nq):
+            seen = lens[s] - nq + i + 1
+            K, V = k[:seen], v[:seen]
+            size = lambda x: x.abs().view(seen, -1, 32).amax(-1).repeat_interleave(32, 1)  # noqa: E731
+            for row in range(G):
+                at0 = (h * G + row) * hd
+                qr = q[s * nq + i, at0:at0 + hd].double()
+                sc = K @ qr / math.sqrt(hd)
+                p = torch.softmax(sc, 0)
+                # the tolerance of check_weighted
+                score = 16 * U * (15 / 7 * size(K) * qr).square().sum(-1).sqrt().max() / math.sqrt(hd) + 4 * U * sc.abs().max()
+                tol = (p @ size(V)) * (2 * score + 16 * U)
+                err = (got[s * nq + i, at0:at0 + hd] - p @ V).abs()
+                assert bool((err <= tol).all()), (s, h, i, row, float((err / tol).max()))
+
+
 # ------------------------------------------------------------------ matvec
 
 def q4_matrix(rng, rows, cols, sigma=0.02):
@@ -900,6 +966,67 @@ def test_logprobs_ties_masks_and_order(ops, v):
     targets[6], targets[3] = v - 1, 0
     check_logprobs(ops, x, targets, 32)
     check_logprobs(ops, x, targets, 7, pad=1)
+
+
+def hard_rows(rng, v, off, k):
+    """Rows whose alternatives a block finds on each of its paths when it streams a whole row; off: how far the row
+    lies past a 16-byte boundary.  Thread t of a block holds the logits i with (i + off) / 4 % 256 == t."""
+    thread = (np.arange(v) + off) // 4 % 256
+    rows = {"random": rng.normal(size=v) * 2}
+    rows["ascending"] = np.sort(rng.normal(size=v))          # a list that overflows after its first look
+    rows["descending"] = rows["ascending"][::-1]
+    rows["equal"] = np.zeros(v)
+    rows["last"] = rng.normal(size=v)                        # the best lie in the last tile
+    rows["last"][-40:] += 30
+    rows["late"] = rng.normal(size=v)                        # and behind the second look
+    rows["late"][v * 3 // 5:v * 3 // 5 + 50] += 30
+    rows["few"] = rng.integers(-3, 4, size=v)
+    rows["steps"] = np.floor(np.arange(v) / 777.0)           # ascending in groups of equal ones
+    # fewer threads than alternatives hold thousands of values above what all others have in common
+    rows["columns"] = np.where(np.isin(thread, rng.permutation(256)[:15]), rng.uniform(1, 2, size=v), 0.0)
+    # and one thread less than alternatives, 30 threads of equal values behind them, the rest below
+    pick = rng.permutation(256)
+    rows["two levels"] = np.where(np.isin(thread, pick[:k - 1]), rng.uniform(10, 11, size=v), rng.uniform(-9, -8, size=v))
+    rows["two levels"] = np.where(np.isin(thread, pick[k - 1:k + 29]), 5.0, rows["two levels"])
+    rows["masked"] = np.where(rng.random(v) < 0.9, -np.inf, rng.normal(size=v))
+    rows["ten"] = np.full(v, -np.inf)
+    rows["ten"][rng.permutation(v)[:10]] = rng.normal(size=10)
+    rows["infinite"] = np.sort(rng.normal(size=v))
+    rows["infinite"][[v // 3, v - 5]] = np.inf
+    return {k: np.asarray(r, dtype=np.float32) for k, r in rows.items()}
+
+
+@pytest.mark.parametrize("v,pad", [(151936, 0), (40961, 1), (200003, 2)])
+@pytest.mark.parametrize("k", [20, 32])
+def test_logprobs_of_rows_streamed_whole(ops, v, pad, k):
+    """760 rows are a block each (20 to 98 tiles): candidates above a threshold, lists looked at after 4, 16 and 64
+    tiles and at the end, lists that overflow between looks, and what is read again then."""
+    rng = np.random.default_rng(v + k)
+    n = 760
+    wide = torch.randn(n, v + pad, device="cuda") * 2
+    picked = {}
+    for i, where in enumerate((0, 300, 301, 302, 303)):      # at every place of a 16-byte boundary
+        off = where * (v + pad) % 4
+        for j, (name, row) in enumerate(hard_rows(rng, v, off, k).items()):
+            r = where + 20 * j if i == 0 else where + 4 * (j + 1) + 4 * 13 * (i - 1)
+            while r in picked or r * (v + pad) % 4 != off:
+                r += 1
+            picked[r] = name, row
+            wide[r, :v] = dev(row)
+    logits = wide[:, :v]
+    targets = rng.integers(0, v, size=n)
+    lp, ent = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    ids, tops = torch.empty(n, k, dtype=torch.int32, device="cuda"), torch.empty(n, k, device="cuda")
+    scratch = torch.full((ops.tqd_logprobs_scratch_bytes(n, v, k),), 0xFF, dtype=torch.uint8, device="cuda")
+    ops.tqd_op_logprobs(logits, i32(targets), lp, ent, ids, tops, scratch)
+    picked |= {r: ("plain", logits[r].cpu().numpy()) for r in (5, 758, 759)}
+    for r, (name, row) in picked.items():
+        a, h, i, t, e1, e2 = q4.logprobs(row, targets[r], k)
+        near = lambda got, want: got == want if not math.isfinite(want) else (  # noqa: E731
+            abs(got - want) <= 4 * U * (1 + 3 * abs(want)) + 4 * U * (1 + e1))
+        assert np.array_equal(ids[r].cpu().numpy(), i), (r, name)
+        assert near(float(lp[r]), a) and all(map(near, tops[r].tolist(), t.tolist())), (r, name)
+        assert abs(float(ent[r]) - h) <= 4 * U * (2 + h + e1 + e2) + 4 * U * (1 + e1), (r, name, float(ent[r]), h)
 
 
 def test_logprobs_infinite_logits_and_targets_outside(ops):
