@@ -1153,6 +1153,18 @@ def test_wrapper_refusals(ops, TQDError):
     ops.tqd_op_logprobs(e(0, 100), none, e(0), None, None, None, scratch)
 
 
+def test_logprob_alternatives_go_together(ops, TQDError):
+    """top_logprobs of another shape than top_ids would be filled with another stride, and alone with nothing."""
+    f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    x, ids = f(2, 100), torch.zeros(2, 5, dtype=torch.int32, device="cuda")
+    scratch = torch.zeros(ops.tqd_logprobs_scratch_bytes(2, 100, 5), dtype=torch.uint8, device="cuda")
+    for top_ids, tops in ((ids, f(2, 10)), (ids, f(10)), (ids, f(3, 5)), (ids, None), (None, f(2, 5))):
+        with pytest.raises(TQDError, match="top_"):
+            ops.tqd_op_logprobs(x, None, None, f(2), top_ids, tops, scratch)
+    ops.tqd_op_logprobs(x, None, None, f(2), ids, f(2, 5), scratch)
+    ops.tqd_op_logprobs(x, None, None, f(2), ids[:, :0], f(2, 0), scratch)
+
+
 # ------------------------------------------------------------------ a decode step of them together
 
 def test_a_decode_step_in_four_bits(ops):

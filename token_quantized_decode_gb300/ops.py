@@ -314,10 +314,12 @@ def tqd_op_logprobs(logits, targets, logprob, entropy, top_ids, top_logprobs, sc
         ep = _ptr(entropy, _F32, n, dev, where, "entropy")
     if top_ids is not None and top_ids.shape[-1]:
         k = top_ids.shape[-1]
-        if top_ids.shape != (n, k) or top_logprobs is None:
-            _refuse(where, "top_ids: [rows, top_k], with top_logprobs")
+        if top_ids.shape != (n, k) or top_logprobs is None or top_logprobs.shape != (n, k):
+            _refuse(where, "top_ids and top_logprobs: [rows, top_k] both")
         ip = _ptr(top_ids, _I32, n * k, dev, where, "top_ids")
         kp = _ptr(top_logprobs, _F32, n * k, dev, where, "top_logprobs")
+    elif top_ids is None and top_logprobs is not None:
+        _refuse(where, "top_logprobs needs top_ids")
     L = lib()
     status = L.tqd_op_logprobs(
         lp, ls, n, v, tp, op, ep, k, ip, kp,
