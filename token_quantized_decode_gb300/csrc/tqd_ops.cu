@@ -8,6 +8,21 @@
 #include "tqd_internal.h"
 #include "tqd_q4.cuh"
 
+namespace tqd {
+
+cudaError_t allow_smem(const void* kernel, size_t bytes, unsigned long long* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (__atomic_load_n(done, __ATOMIC_RELAXED) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess && dev < 64) __atomic_fetch_or(done, bit, __ATOMIC_RELAXED);
+  return e;
+}
+
+}  // namespace tqd
+
 using namespace tqd;
 
 namespace {

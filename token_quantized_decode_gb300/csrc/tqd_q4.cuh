@@ -49,8 +49,8 @@ __device__ __forceinline__ float round_f16(float x) { return __half2float(__floa
 // 2^e as f32, e in -126 .. 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// The constants of unpacking codes to signed f16, kept in registers (as immediates they cost an
-// instruction each: a logic operation takes one).
+// The constants of unpacking codes to signed f16, kept in registers (as immediates
+// they cost an instruction each: a logic operation takes one).
 struct Unpack {
   uint32_t lo, hi, magic, off, sixteenth, off_hi;
   __device__ Unpack() {
@@ -62,7 +62,9 @@ struct Unpack {
     off_hi = 0xD480D480u;     // -72
   }
   // The codes in bits 0-3 (low) or 4-7 (high) of each half of x as f16 pairs of
-  // code - 8: 1024 + code and 1024 + 16 code are exact f16, so is the result.
+  // code - 8: 1024 + code and 1024 + 16 code are exact f16, so is the result.  (Whole
+  // numbers under an f16 exponent: Kim, Henry, Fahim and Awadalla, "Who Says Elephants
+  // Can't Run: Bringing Large Scale MoE Models into Cloud Scale Production", 2022.)
   __device__ __forceinline__ uint32_t low(uint32_t x) const {
     uint32_t v;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(lo), "r"(magic));

@@ -95,8 +95,9 @@ struct Cfg {
   static constexpr int LEAD = NT == 1 ? 2 : 4;
   static constexpr int LD = HD + 8;       // floats of a row in the merge buffer
   static constexpr int PART = R * LD + 2 * P;  // floats of a warp's partial result
-  static constexpr size_t smem = static_cast<size_t>(W) * ST * (2 * BB + 16) + static_cast<size_t>(W) * PART * 4;
+  static constexpr size_t smem = static_cast<size_t>(W) * ST * (2 * BB + 12) + static_cast<size_t>(W) * PART * 4;
   static_assert(PART * 4 <= ST * 2 * BB, "a partial result fits a warp's ring");
+  static_assert(W * ST % 2 == 0, "the plan behind the flags starts on 8 bytes");
   static_assert(NT == 1 || GV == 1, "groups side by side only where columns are free");
 };
 
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
   float* parts = reinterpret_cast<float*>(ring + W * ST * 2 * BB);  // [W][PART]: [R][LD], [P] ref, [P] sum p
   auto* bars = reinterpret_cast<uint64_t*>(parts + W * PART);      // [W][ST]
   int* flags = reinterpret_cast<int*>(bars + W * ST);    // [W][ST] 1, 2: no page for the first, second block; 4: not seen
-  unsigned char* plan_mem = reinterpret_cast<unsigned char*>(flags + W * ST * 2);
+  unsigned char* plan_mem = reinterpret_cast<unsigned char*>(flags + W * ST);
 
   __shared__ int ends[W];
   __shared__ Shared shared[W + 1];  // the last segment of each warp's run, and the CTA's first one

@@ -311,17 +311,6 @@ __global__ void __launch_bounds__(256) k_kv_read_q4(ReadArgs a) {
 
 }  // namespace
 
-cudaError_t allow_smem(const void* kernel, size_t bytes, unsigned long long* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (dev < 64 && (__atomic_load_n(done, __ATOMIC_RELAXED) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess && dev < 64) __atomic_fetch_or(done, bit, __ATOMIC_RELAXED);
-  return e;
-}
-
 cudaError_t launch_kv_append_q4(const Q4Cache& c, int hd, const float* k, int64_t k_stride, const float* v,
                                 int64_t v_stride, const int32_t* positions, const int32_t* seqs, int n_tokens,
                                 const float2* rope, int max_pos, const float* q, int64_t q_stride, int n_heads,
