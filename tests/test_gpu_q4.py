@@ -1029,6 +1029,34 @@ def test_logprobs_of_rows_streamed_whole(ops, v, pad, k):
         assert abs(float(ent[r]) - h) <= 4 * U * (2 + h + e1 + e2) + 4 * U * (1 + e1), (r, name, float(ent[r]), h)
 
 
+@pytest.mark.parametrize("peaks", [False, True])
+def test_logprobs_entropy_keeps_f32(ops, peaks):
+    """The entropy of long rows, (log2 s - t / s) ln 2 with s = sum 2^d and t = sum d 2^d, d relative to the largest
+    logit: four f32 roundings of log2 s, t / s and twice their difference, each u / sqrt(3) of its value in the root
+    mean square.  Over 760 rows the error's root mean square stays below three times theirs, which leaves the sums
+    of 151936 terms two of the three: small terms may not be lost one by one beside large ones."""
+    n, v = 760, 151936
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8 + peaks)
+    x = 2 * torch.randn(n, v, generator=g, device="cuda")
+    if peaks:
+        x.scatter_add_(1, torch.randint(0, v, (n, 8), generator=g, device="cuda"),
+                       6 + 6 * torch.rand(n, 8, generator=g, device="cuda"))
+    ent = torch.empty(n, device="cuda")
+    scratch = torch.empty(ops.tqd_logprobs_scratch_bytes(n, v, 0), dtype=torch.uint8, device="cuda")
+    ops.tqd_op_logprobs(x, None, None, ent, None, None, scratch)
+    parts = []
+    for rows, got in zip(x.split(38), ent.split(38)):
+        d = (rows.double() - rows.double().amax(1, keepdim=True)) / math.log(2)
+        e = torch.exp2(d)
+        a, b = torch.log2(e.sum(1)), (e * d).sum(1) / e.sum(1)
+        h = (a - b) * math.log(2)
+        scale = U / math.sqrt(3) * math.log(2) * torch.sqrt(a**2 + b**2 + 2 * (a - b) ** 2)
+        parts.append((got.double() - h) / scale)
+    rms = float(torch.cat(parts).square().mean().sqrt())
+    assert rms <= 3, rms
+
+
 def test_logprobs_infinite_logits_and_targets_outside(ops):
     x = np.random.default_rng(1).normal(size=(4, 5000)).astype(np.float32)
     x[0, [17, 4000]] = np.inf
