@@ -481,6 +481,64 @@ def test_attention_large_values_of_no_weight(ops, heads, n_kv, hd, room, large):
         check_weighted(got[s].reshape(heads, hd), q[s].reshape(heads, hd).astype(np.float64), K[s], V[s], hd)
 
 
+@pytest.mark.parametrize("heads,hd", [(1, 64), (1, 128), (2, 128), (4, 128), (8, 128), (3, 64), (8, 64)])
+@pytest.mark.parametrize("ratio", [1, 30, 1000])
+def test_attention_large_query_elements_that_meet_zero_keys(ops, heads, hd, ratio):
+    """One element of each group of a query is far larger than the rest, and every key is 0 there (code 8): what the
+    rest keeps beside it is what the header states, 2^-22 of the largest of the group.  A score's tolerance: its
+    products' 16 u sqrt(sum T^2) + 4 u |sum|, four times the root sum square of |k| 2^-22 max|q|, and the tensor cores'
+    truncation of a group's 32 low parts times codes, 2^-20 max|q| scale.  A weight's: twice that and 16 u."""
+    rng = np.random.default_rng(heads + hd + ratio)
+    n = 400
+    host = Host(rng, 1, 1, hd, 16, n)
+    at = 32 * np.arange(hd // 32) + rng.integers(0, 32, size=hd // 32)
+    keys = rng.normal(size=(n, hd))
+    keys[:, at] = 0
+    rows = [host.store(0, p, keys[p][None], rng.normal(size=(1, hd))) for p in range(n)]
+    K, V = np.array([r[0][0] for r in rows]), np.array([r[1][0] for r in rows])
+    q = rng.normal(size=(heads, hd)).astype(np.float32)
+    q[:, at] = ratio * rng.uniform(0.7, 1.4, size=(heads, at.size)) * rng.choice([-1, 1], size=(heads, at.size))
+    got = attend(ops, host.device(ops), q.reshape(1, -1), [n]).reshape(heads, hd)
+    step = lambda x: np.abs(x.reshape(n, -1, 32)).max(-1) / 7  # noqa: E731
+    for h in range(heads):
+        x = q[h].astype(np.float64)
+        top = np.abs(x.reshape(-1, 32)).max(-1)
+        s = K @ x / math.sqrt(hd)
+        hold = 4 * np.sqrt(((K * np.repeat(top, 32) * 2.0**-22) ** 2).sum(-1)) + 2.0**-20 * step(K) @ top
+        score = (16 * U * np.sqrt(((K * x) ** 2).sum(-1)) + hold) / math.sqrt(hd) + 4 * U * np.abs(s)
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        tol = (p * (2 * score.max() + 16 * U)) @ (7 * np.repeat(step(V), 32, axis=1))
+        err = np.abs(got[h] - p @ V)
+        assert np.all(err <= tol), (h, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("heads,hd", [(1, 64), (1, 128), (2, 128), (4, 128), (8, 128), (8, 64)])
+@pytest.mark.parametrize("octaves", [8, 16, 24])
+def test_attention_groups_of_very_unequal_values(ops, heads, hd, octaves):
+    """The groups of 32 of one head's values differ by 2^8 to 2^24: a group far below the largest keeps what the header
+    states, each product of weight and scale to 2^-22 of itself or 2^-37 of the head's largest product (times codes up
+    to 8, with random signs: four times the root of their number)."""
+    rng = np.random.default_rng(heads + hd + octaves)
+    n = 500
+    host = Host(rng, 1, 1, hd, 16, n)
+    gain = np.repeat(2.0 ** (12 - octaves * np.arange(hd // 32) / (hd // 32 - 1)), 32)
+    rows = [host.store(0, p, rng.normal(size=(1, hd)), rng.normal(size=(1, hd)) * gain) for p in range(n)]
+    K, V = np.array([r[0][0] for r in rows]), np.array([r[1][0] for r in rows])
+    q = rng.normal(size=(heads, hd)).astype(np.float32)
+    got = attend(ops, host.device(ops), q.reshape(1, -1), [n]).reshape(heads, hd)
+    step = lambda x: np.repeat(np.abs(x.reshape(n, -1, 32)).max(-1) / 7, 32, axis=1)  # noqa: E731
+    for h in range(heads):
+        x = q[h].astype(np.float64)
+        s = K @ x / math.sqrt(hd)
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        score = 16 * U * np.sqrt(((15 * step(K) * x) ** 2).sum(-1)).max() / math.sqrt(hd) + 4 * U * np.abs(s).max()
+        tol = p @ (7 * step(V)) * (2 * score + 16 * U) + 4 * math.sqrt(n) * 8 * 2.0**-37 * (p[:, None] * step(V)).max()
+        err = np.abs(got[h] - p @ V)
+        assert np.all(err <= tol), (h, float((err / tol).max()))
+
+
 def test_attention_scales_of_either_sign(ops):
     """Pages that a program wrote itself: any finite f16 is a scale, and a negative one can be the largest by far."""
     rng = np.random.default_rng(27)
