@@ -27,11 +27,11 @@
 // HBM bounds it: 4 bytes a logit and about seven instructions (a fused
 // multiply-add, a maximum, an exponential, two sums; half a maximum).  A tile
 // is 8 logits a thread, the next one's loads issued before the current one's
-// work.  2053 rows of 151936 take 195 us without alternatives (1.25 GB: 6.4 TB/s,
-// 95 % of a copy's rate), 217 with 20 (85 %): the lists' barriers and the last
+// work.  2053 rows of 151936 take 193 us without alternatives (1.25 GB: 6.5 TB/s,
+// 95 % of a copy's rate), 216 with 20 (85 %): the lists' barriers and the last
 // wave of blocks.  Few rows are cut into slices of whole tiles, one block each,
 // whose partial (m, s, t) and alternatives a second kernel joins (programmatic
-// dependent launch): one row takes 10.5 us, two launches.
+// dependent launch): one row takes 10.8 us, two launches.
 #include <cuda_runtime.h>
 
 #include "tqd_internal.h"

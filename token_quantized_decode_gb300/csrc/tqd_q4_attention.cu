@@ -44,15 +44,15 @@
 // parts through distributed shared memory: no plan and no second kernel, half the time of a
 // short call.
 //
-// What it measures (GB300, 1.9 GHz).  131072 positions of 32/8 heads of 128: 42 us for 151 MB
-// (3.6 TB/s; 22 us at a copy's rate), of which a warp's instructions take most: 740
-// for each unit of 32 positions and 4 rows, 40,000 a scheduler, 20 us at one a cycle;
-// the three warps that the registers leave a scheduler reach 0.7 of that between
+// What it measures (GB300, 1.9 GHz).  131071 positions of 32/8 heads of 128: 42.0 us for
+// 151 MB (3.6 TB/s; 22 us at a copy's rate), of which a warp's instructions take most:
+// 752 for each unit of 32 positions and 4 rows, 40,500 a scheduler, 21 us at one a
+// cycle; the three warps that the registers leave a scheduler reach 0.7 of that between
 // the copies' arrival and the last unit, and 12 us are the beginning (lengths, pages,
 // queries: 6 us) and the two joins (3 and 3).  The same 12 us bound short calls by
-// runs (33 ragged to 4160 positions of 16/8 heads: 18.6 us); 1 x 575 positions by
+// runs (33 ragged to 4160 positions of 16/8 heads: 18.5 us); 1 x 575 positions by
 // clusters take 6.7 us, a launch and one chain of loads.  Prompts' tiles are
-// bound by the same instructions (2048 queries of 16/8 heads of 128: 288 us, 60 TFLOP/s).
+// bound by the same instructions (2048 queries of 16/8 heads of 128: 295 us, 58 TFLOP/s).
 #include <cuda_runtime.h>
 
 #include <type_traits>

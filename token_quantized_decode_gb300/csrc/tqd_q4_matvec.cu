@@ -8,7 +8,9 @@
 namespace tqd {
 namespace {
 
-// One thread per 32-bit word of a tile's codes or scales.
+// One thread per 32-bit word of a tile's codes or scales.  Run once per matrix when a
+// model is loaded: 151936 x 1024 takes 99 us (175 MB, 1.8 TB/s; single-byte loads
+// from the 18-byte blocks bound it).
 __global__ void __launch_bounds__(288) k_q4_repack(const uint8_t* src, int64_t rows, int64_t groups, int64_t strips,
                                                    uint8_t* dst) {
   const int64_t tile = blockIdx.x, rt = tile / strips, st = tile - rt * strips;
