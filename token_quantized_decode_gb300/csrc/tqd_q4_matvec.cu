@@ -51,8 +51,9 @@ constexpr int kMvThreads = 32 * kMvWarps;
 __host__ __device__ constexpr int mv_chunk(int nt) { return nt == 4 ? 1 : nt == 1 ? 4 : 2; }
 __host__ __device__ constexpr int mv_stages(int nt) { return nt == 4 ? 3 : 2; }
 // Shared memory of a CTA: at most what lets two of them share an SM; the rings
-// and the warps' sums, then the staged vectors.
-constexpr int kMvSmem = 113 * 1024;
+// and the warps' sums, then the staged vectors.  (228 KB hold two of 113 KB, 1 KB of
+// the system's and 128 bytes that are not dynamic.)
+constexpr int kMvSmem = 113 * 1024 - 128;
 constexpr int mv_fixed_smem(int nt) {
   return kMvWarps * (mv_stages(nt) * (mv_chunk(nt) * kQ4TileBytes + 8) + 2 * nt * 128);
 }
