@@ -477,7 +477,8 @@ size_t tqd_kv_q4_page_bytes(int32_t n_kv_heads, int32_t head_dim, int32_t page_s
  * of sequence seqs[i] (seqs NULL: of sequence i; n_tokens <= n_seq then).
  * k, v: f32 rows of n_kv_heads * head_dim, k_stride and v_stride floats apart;
  * q, q_out: f32 rows of n_heads * head_dim (q NULL with n_heads 0: none), which
- * may be the same rows; rows may be slices of one fused projection.
+ * may be the same rows but not overlap otherwise, nor q_out k or v; rows may be
+ * slices of one fused projection.
  * rope_table: from tqd_op_rope_table with max_pos positions (NULL: no
  * rotation); the rotation is the half-split one of tqd_op_rope, and the codes
  * are those of the exactly rotated keys.

@@ -1239,6 +1239,39 @@ def test_wrapper_refusals(ops, TQDError):
     ops.tqd_op_logprobs(e(0, 100), none, e(0), None, None, None, scratch)
 
 
+def test_rows_between_one_anothers(ops, TQDError):
+    """Outputs as slices of one buffer with strides of any kind: read where they do not overlap, refused where they do."""
+    rng = np.random.default_rng(33)
+    host = Host(rng, 1, 1, 64, 16, 16)
+    host.fill(rng, [8])
+    cache = host.device(ops)
+    taken = 0
+    for _ in range(400):
+        n, sk, sv = int(rng.integers(1, 6)), int(rng.integers(64, 300)), int(rng.integers(64, 300))
+        if rng.random() < 0.5:
+            sv = sk
+        at = int(rng.integers(-1400, 1400))
+        buf = torch.full((6000,), 7.0, device="cuda")
+        k, v = buf.as_strided((n, 64), (sk, 1), 2000), buf.as_strided((n, 64), (sv, 1), 2000 + at)
+        mine = [{2000 + o + s * i + j for i in range(n) for j in range(64)} for o, s in ((0, sk), (at, sv))]
+        pos = i32(np.arange(n))
+        seqs = i32(np.zeros(n))
+        if mine[0] & mine[1]:
+            with pytest.raises(TQDError, match="overlap"):
+                ops.tqd_op_kv_read_q4(cache, pos, seqs, k, v)
+            continue
+        taken += 1
+        ops.tqd_op_kv_read_q4(cache, pos, seqs, k, v)
+        assert np.array_equal(k.cpu().numpy(), host.K[0][:n, 0]) and np.array_equal(v.cpu().numpy(), host.V[0][:n, 0])
+        assert int((buf != 7.0).sum()) <= 128 * n
+    assert taken > 100
+    x = torch.randn(4, 160, device="cuda")  # x and y side by side in one tensor
+    t = tiles_of(ops, *q4_matrix(rng, 32, 96))
+    ops.tqd_op_q4_0_matvec(t, 32, 96, x[:, :96], x[:, 100:132])
+    with pytest.raises(TQDError, match="overlap"):
+        ops.tqd_op_q4_0_matvec(t, 32, 96, x[:, :96], x[:, 95:127])
+
+
 def test_logprob_alternatives_go_together(ops, TQDError):
     """top_logprobs of another shape than top_ids would be filled with another stride, and alone with nothing."""
     f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731

@@ -175,6 +175,50 @@ def test_matvec_refusals(L):
         assert L.tqd_op_q4_0_repack(*bad, None) == BAD, bad
 
 
+def test_overlapping_rows_are_refused(L):
+    """Outputs that would be read as inputs while they are written."""
+    f = lambda i: P + 4 * i  # noqa: E731
+    app = dict(c=cache(), k=f(256), ks=512, v=f(384), vs=512, pos=P, seqs=P, n=3, rope=None, max_pos=0, q=f(0), qs=512,
+               heads=4, out=f(0), os=512, st=None)
+    for bad in (dict(out=f(1)), dict(out=f(512)), dict(os=511), dict(out=f(128)), dict(out=f(300)), dict(out=f(512 + 256)),
+                dict(out=f(100000), k=f(100000 + 255)), dict(out=f(4000), os=1024, v=f(4000 + 2048 - 127))):
+        assert L.tqd_op_kv_append_q4(*{**app, **bad}.values()) == BAD, bad
+        assert b"overlap" in L.tqd_last_error()
+    assert L.tqd_op_kv_read_q4(cache(), P, P, 3, f(0), 128, f(127), 128, None) == BAD
+    att = dict(c=cache(), q=f(0), qs=512, lens=P, start=P, n=4, heads=4, out=f(0), os=512, scratch=P, st=None)
+    for bad in (dict(), dict(out=f(255)), dict(out=f(512 * 3)), dict(out=f(512 * 3 + 255)), dict(out=f(-255)),
+                dict(out=f(300), os=600), dict(out=f(260), os=256), dict(n=1 << 20, out=f(512 * (1 << 19) + 3))):
+        assert L.tqd_op_attention_q4(*{**att, **bad}.values()) == BAD, bad
+        assert b"overlap" in L.tqd_last_error(), bad
+    mv = dict(w=P, rows=20, cols=96, x=f(0), n=2, xs=96, y=f(0), ys=20, st=None)
+    for bad in (dict(), dict(y=f(95)), dict(y=f(191)), dict(y=f(-39)), dict(n=1, y=f(95), xs=0, ys=0)):
+        assert L.tqd_op_q4_0_matvec(*{**mv, **bad}.values()) == BAD, bad
+        assert b"overlap" in L.tqd_last_error(), bad
+
+
+def _meet(a, sa, wa, b, sb, wb, n):
+    rows = lambda p, s, w: {(p + s * i + j) for i in range(n) for j in range(w)}  # noqa: E731
+    return bool(rows(a, sa, wa) & rows(b, sb, wb))
+
+
+def test_overlaps_of_rows_of_any_stride_are_found(L):
+    """Against sets of addresses.  (Rows that lie between one another's without an overlap are taken: a call with them
+    would launch, so they are tested with memory behind them.)"""
+    rng = np.random.default_rng(0)
+    c = cache(n_kv_heads=1, n_seq=8)
+    hits = 0
+    for _ in range(3000):
+        n, sk, sv = int(rng.integers(1, 6)), int(rng.integers(64, 300)), int(rng.integers(64, 300))
+        if rng.random() < 0.4:
+            sv = sk
+        at = int(rng.integers(-1400, 1400))
+        if _meet(0, sk, 64, at, sv, 64, n):
+            hits += 1
+            assert L.tqd_op_kv_read_q4(c, P, P, n, P + 65536, sk, P + 65536 + 4 * at, sv, None) == BAD
+            assert b"overlap" in L.tqd_last_error()
+    assert hits > 500
+
+
 def test_logprob_refusals(L):
     good = dict(x=P, stride=100, rows=2, vocab=100, t=P, lp=P, ent=P, k=3, ids=P, tops=P, scratch=P, st=None)
     for bad in (dict(x=None), dict(stride=99), dict(rows=-1), dict(vocab=0), dict(t=None), dict(lp=None), dict(k=-1),

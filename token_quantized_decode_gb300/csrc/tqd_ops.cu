@@ -43,6 +43,32 @@ int32_t refuse(const char* why) {
   return TQD_ERR_BAD_ARG;
 }
 
+// n rows of `width` floats, `stride` floats apart (no less than width where n > 1).
+struct FloatRows {
+  const float* p;
+  int64_t stride, width;
+};
+
+// Whether n rows of a and n rows of b share memory (rows may lie between one another's, as slices
+// of one tensor's columns do).
+bool overlap(const FloatRows& a, const FloatRows& b, int64_t n) {
+  using Wide = __int128;  // strides and row numbers are the caller's
+  const Wide d = static_cast<Wide>(reinterpret_cast<uintptr_t>(b.p)) - static_cast<Wide>(reinterpret_cast<uintptr_t>(a.p));
+  const Wide wa = a.width * static_cast<Wide>(4), wb = b.width * static_cast<Wide>(4), last = n - 1;
+  const Wide sa = n > 1 ? a.stride * static_cast<Wide>(4) : wa, sb = n > 1 ? b.stride * static_cast<Wide>(4) : wb;
+  if (d >= last * sa + wa || -d >= last * sb + wb) return false;
+  auto floor_div = [](Wide x, Wide y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
+  // row i of a, from offset `at`, meets the rows of b from lo to hi
+  auto meets = [&](Wide at, Wide first) {
+    const Wide lo = floor_div(at - wb - d, sb) + 1, hi = -floor_div(-(at + wa - d), sb) - 1;
+    return (lo > first ? lo : first) <= (hi < last ? hi : last);
+  };
+  if (sa == sb) return meets(0, -last);  // the same for every row but for which rows there are
+  for (Wide i = 0; i <= last; ++i)
+    if (meets(i * sa, 0)) return true;
+  return false;
+}
+
 size_t q4_page_bytes(int32_t n_kv, int32_t hd, int32_t page_size) {
   if (n_kv <= 0 || (hd != 64 && hd != 128) || page_size <= 0 || page_size % kQ4Block || page_size > (1 << 20))
     return 0;
@@ -226,6 +252,13 @@ int32_t tqd_op_kv_append_q4(const tqd_kv_q4* cache, const float* k, int64_t k_st
     return refuse("tqd_op_kv_append_q4: a row stride shorter than the row");
   if (static_cast<int64_t>(n_tokens) * c.n_kv > (1ll << 30) || kvw > (1 << 24) || qw > (1 << 24))
     return refuse("tqd_op_kv_append_q4: n_tokens * n_kv_heads above 2^30, or rows above 2^24 floats");
+  if (q) {
+    const FloatRows in{q, q_stride, qw}, to{q_out, q_out_stride, qw};
+    const bool same = q == q_out && (q_stride == q_out_stride || n_tokens == 1);
+    if ((!same && overlap(in, to, n_tokens)) || overlap(to, {k, k_stride, kvw}, n_tokens) ||
+        overlap(to, {v, v_stride, kvw}, n_tokens))
+      return refuse("tqd_op_kv_append_q4: q_out overlaps k, v, or q without being the same rows");
+  }
   return status_of(launch_kv_append_q4(c, cache->head_dim, k, k_stride, v, v_stride, positions, seqs, n_tokens,
                                        reinterpret_cast<const float2*>(rope_table), max_pos, q, q_stride, n_heads,
                                        q_out, q_out_stride, static_cast<cudaStream_t>(stream)));
@@ -243,6 +276,8 @@ int32_t tqd_op_kv_read_q4(const tqd_kv_q4* cache, const int32_t* positions, cons
   if ((k_out && k_stride < kvw) || (v_out && v_stride < kvw))
     return refuse("tqd_op_kv_read_q4: a row stride shorter than the row");
   if (static_cast<int64_t>(n_tokens) * c.n_kv > (1ll << 30)) return refuse("tqd_op_kv_read_q4: n_tokens * n_kv_heads above 2^30");
+  if (k_out && v_out && overlap({k_out, k_stride, kvw}, {v_out, v_stride, kvw}, n_tokens))
+    return refuse("tqd_op_kv_read_q4: k_out overlaps v_out");
   return status_of(launch_kv_read_q4(c, cache->head_dim, positions, seqs, n_tokens, k_out, k_stride, v_out, v_stride,
                                      static_cast<cudaStream_t>(stream)));
 }
@@ -266,6 +301,7 @@ int32_t tqd_op_attention_q4(const tqd_kv_q4* cache, const float* q, int64_t q_st
   if (reinterpret_cast<uintptr_t>(scratch) % 16) return refuse("tqd_op_attention_q4: scratch must be 16-byte aligned");
   if (static_cast<int64_t>(n_tokens) * n_heads > (1ll << 30))
     return refuse("tqd_op_attention_q4: n_tokens * n_heads above 2^30");
+  if (overlap({q, q_stride, qw}, {out, out_stride, qw}, n_tokens)) return refuse("tqd_op_attention_q4: out overlaps q");
   const Q4AttnArgs a{c, q, out, lens, q_start, scratch, q_stride, out_stride, n_tokens, n_heads,
                      cache->head_dim == 128 ? 0.08838834764831845f : 0.125f};
   return status_of(launch_attention_q4(a, cache->head_dim, static_cast<cudaStream_t>(stream)));
@@ -293,6 +329,7 @@ int32_t tqd_op_q4_0_matvec(const uint8_t* w_tiles, int64_t rows, int64_t cols, c
     return refuse("tqd_op_q4_0_matvec: NULL pointer, cols no multiple of 32 up to 16384, or n above 64");
   if (n > 1 && (x_stride < cols || y_stride < rows)) return refuse("tqd_op_q4_0_matvec: a row stride shorter than the row");
   if (reinterpret_cast<uintptr_t>(w_tiles) % 16) return refuse("tqd_op_q4_0_matvec: w_tiles must be 16-byte aligned");
+  if (overlap({x, x_stride, cols}, {y, y_stride, rows}, n)) return refuse("tqd_op_q4_0_matvec: y overlaps x");
   return status_of(launch_q4_matvec(w_tiles, static_cast<int>(rows), static_cast<int>(cols), x, n, x_stride, y, y_stride,
                                     static_cast<cudaStream_t>(stream)));
 }
