@@ -581,6 +581,29 @@ def test_attention_extreme_queries(ops):
     assert np.max(np.abs(got[1] - host.V[0][top, 0])) < 1e-5 * vmax
 
 
+@pytest.mark.parametrize("heads,hd", [(1, 128), (2, 128), (4, 128), (8, 128), (2, 64), (8, 64)])
+@pytest.mark.parametrize("room", [0, 100000])
+def test_attention_scores_far_below_and_above_zero(ops, heads, hd, room):
+    """Scores of one sign up to 1e34: the largest one takes all the weight, the one nearest to zero where all are
+    negative; also where the first positions score 1e30 less than later ones, and the other way round."""
+    rng = np.random.default_rng(heads + hd)
+    n = 200
+    host = Host(rng, 2, 1, hd, 16, n, room=room)
+    key = rng.choice([-1.0, 1.0], size=hd)
+    size = np.stack([rng.permutation(np.linspace(1, 6, n)), np.where(np.arange(n) < 90, 1.0, 5.0) + rng.permutation(n) / n])
+    rows = [[host.store(s, p, (key * size[s, p])[None], rng.normal(size=(1, hd))) for p in range(n)] for s in range(2)]
+    cache = host.device(ops)
+    for gain in (1e5, -1e5, 1e20, -1e20, 3e32, -3e32):
+        q = np.tile(key, (2, heads)) * gain * rng.uniform(0.5, 1, size=(2, heads)).repeat(hd, 1)
+        got = attend(ops, cache, q.astype(np.float32), [n, n]).reshape(2, heads, hd)
+        for s in range(2):
+            K = np.array([r[0][0] for r in rows[s]])
+            score = K @ key * (1 if gain > 0 else -1)
+            top = np.flatnonzero(score == score.max())
+            want = np.mean([rows[s][p][1][0] for p in top], 0)
+            assert np.all(np.abs(got[s] - want) <= 1e-5), (gain, s)
+
+
 @pytest.mark.parametrize("heads", [1, 4, 8])
 def test_attention_nan_keys_and_values(ops, heads):
     """A NaN in a position reaches the queries that see it and no other; NaN scales behind the end reach none."""
