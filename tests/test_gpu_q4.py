@@ -1365,3 +1365,68 @@ def test_a_decode_step_in_four_bits(ops):
             a, ent_w, id_w, top_w, *_ = q4.logprobs(logits[i].cpu().numpy(), targets[i], 5)
             assert abs(float(lp[i]) - a) < 1e-5 and abs(float(ent[i]) - ent_w) < 1e-5
             assert np.array_equal(ids[i].cpu().numpy(), id_w) and np.max(np.abs(tops[i].cpu().numpy() - top_w)) < 1e-5
+
+
+def test_a_captured_decode_step_repeats_the_eager_one(ops):
+    """The whole step as one graph, replayed with positions, lengths and inputs that change on the device, beside the
+    same calls made one by one on a copy of the cache: the same bits, over steps that cross pages and blocks."""
+    rng = np.random.default_rng(34)
+    hidden, heads, n_kv, hd, vocab, n_seq, page, k = 256, 8, 2, 64, 3001, 5, 16, 6
+    qw, kvw = heads * hd, n_kv * hd
+    tiles = {n: tiles_of(ops, *q4_matrix(rng, r, c, 0.06)) for n, (r, c) in
+             {"qkv": (qw + 2 * kvw, hidden), "o": (hidden, qw), "head": (vocab, hidden)}.items()}
+    table = rope_table(ops, hd, 128)
+    first = [0, 13, 31, 3, 70]
+    host = Host(rng, n_seq, n_kv, hd, page, 112)
+    host.fill(rng, first)
+
+    class Step:
+        def __init__(self):
+            e = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+            self.cache = host.device(ops)
+            self.scratch = torch.zeros(ops.tqd_attention_q4_scratch_bytes(hd), dtype=torch.uint8, device="cuda")
+            self.lscratch = torch.zeros(ops.tqd_logprobs_scratch_bytes(n_seq, vocab, k), dtype=torch.uint8, device="cuda")
+            self.x, self.qkv, self.att = e(n_seq, hidden), e(n_seq, qw + 2 * kvw), e(n_seq, qw)
+            self.h, self.logits = e(n_seq, hidden), e(n_seq, vocab)
+            self.lp, self.ent, self.tops = e(n_seq), e(n_seq), e(n_seq, k)
+            self.ids = torch.zeros(n_seq, k, dtype=torch.int32, device="cuda")
+            self.pos, self.lens, self.targets = i32(first), i32([f + 1 for f in first]), i32([1, 2, 3, 4, 5])
+
+        def run(self):
+            q, kk, v = self.qkv.split([qw, kvw, kvw], 1)
+            ops.tqd_op_q4_0_matvec(tiles["qkv"], qw + 2 * kvw, hidden, self.x, self.qkv)
+            ops.tqd_op_kv_append_q4(self.cache, kk, v, self.pos, None, table, q, q)
+            ops.tqd_op_attention_q4(self.cache, q, self.lens, None, self.att, self.scratch)
+            ops.tqd_op_q4_0_matvec(tiles["o"], hidden, qw, self.att, self.h)
+            ops.tqd_op_q4_0_matvec(tiles["head"], vocab, hidden, self.h, self.logits)
+            ops.tqd_op_logprobs(self.logits, self.targets, self.lp, self.ent, self.ids, self.tops, self.lscratch)
+
+        def advance(self, x):
+            self.x.copy_(x)
+            self.pos += 1
+            self.lens += 1
+
+        def results(self):
+            return [t.clone() for t in (self.cache.pages, self.qkv, self.att, self.logits, self.lp, self.ent, self.ids,
+                                        self.tops)]
+
+    eager, captured = Step(), Step()
+    warm = Step()  # (every kernel once before the capture)
+    warm.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured.run()
+    for step in range(40):
+        x = torch.randn(n_seq, hidden, device="cuda")
+        for s in (eager, captured):
+            if step:
+                s.advance(x)
+            else:
+                s.x.copy_(x)
+        eager.run()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager.results(), captured.results()):
+            assert torch.equal(a, b), step
+    assert bool(torch.isfinite(eager.logits).all()) and eager.lens.tolist() == [f + 40 for f in first]
