@@ -510,8 +510,9 @@ int32_t tqd_op_kv_read_q4(const tqd_kv_q4* cache, const int32_t* positions, cons
  * q_start[n_seq] stay as they were.  q, out: f32 rows of n_heads *
  * head_dim, q_stride and out_stride floats apart; out may not overlap q.
  * Accuracy: codes and scales are exact; of a query's element at most 2^-22 of the
- * largest of its aligned group of 32 is lost, of a product of weight and V scale
- * 2^-22 or 2^-37 of the largest of its row and kv head, and sums are f32.
+ * largest of its aligned group of 32 is lost, of a product of softmax weight and V
+ * scale 2^-22, or 2^-37 of the largest of its row and kv head, or 2^-85, and sums
+ * are f32.
  * A page outside [0, n_pages), or a length past the page table, makes the
  * queries that see it NaN.  At most 1024 sequences.  scratch: caller-owned
  * device memory of tqd_attention_q4_scratch_bytes(head_dim) bytes, 16-byte
