@@ -90,19 +90,14 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, nullptr, limit_ns));
 }
 
-// After a wait that ran out at stage st of a warp's ring: every stage's copy
-// that may still be under way gets the limit once more, so that none lands in
-// shared memory that serves something else by then.  (A stage without a copy costs its
-// limit: at most a few seconds, on a GPU that has stopped copying.)
-__device__ __forceinline__ void mbar_ring_drain(uint64_t* bars, int stages, int st, uint32_t phase) {
+// After a wait that ran out: every copy of a warp's ring that may still be under
+// way gets half a second more, so that none lands in shared memory that serves
+// something else by then.  A barrier's phase at hand has one of the two parities,
+// the other one's is over and answers at once; a stage without a copy costs the
+// half second, on a GPU that has stopped copying.
+__device__ __forceinline__ void mbar_ring_drain(uint64_t* bars, int stages) {
 #pragma unroll 1
-  for (int i = 0; i < stages; ++i) {
-    mbar_wait_warp(&bars[st], phase);
-    if (++st == stages) {
-      st = 0;
-      phase ^= 1u;
-    }
-  }
+  for (int i = 0; i < 2 * stages; ++i) mbar_wait_warp(&bars[i >> 1], i & 1, kWaitLimitNs / 4);
 }
 
 // Global -> shared bulk copy completing on `bar` (both addresses 16-byte

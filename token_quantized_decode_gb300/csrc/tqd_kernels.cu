@@ -462,12 +462,11 @@ __device__ uint32_t g_wait_err;
 __device__ unsigned long long g_wait_ctr;  // never incremented
 
 __global__ void k_wait_selftest() {
-  __shared__ __align__(8) uint64_t bar, late[2];
+  __shared__ __align__(8) uint64_t bar, late[4];
   if (threadIdx.x == 0) {
     g_wait_err = 0u;
     mbar_init(&bar, 1);
-    mbar_init(&late[0], 1);
-    mbar_init(&late[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&late[i], 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -485,16 +484,23 @@ __global__ void k_wait_selftest() {
       }
     }
   } else if (threadIdx.x >= 64 && threadIdx.x < 96) {
-    // two barriers that complete late, after 0.2 and 0.4 s: half of the lanes stop waiting
-    // after a millisecond, so on its own each lane may answer for itself, the warp's wait not
+    // barriers that complete late, after 0.2, 0.4 and 0.6 s: half of the lanes stop waiting
+    // after a millisecond, so on its own each lane may answer for itself, the warp's wait not;
+    // and what is under way when the wait is given up has arrived when the ring is drained
+    // (late[2] in its second phase, late[3] a stage without a copy)
     const uint64_t limit = threadIdx.x < 80 ? 1000000ull : kWaitLimitNs;
     const bool own = mbar_wait_bounded(&late[0], 0u, nullptr, limit);
     const bool mixed = __any_sync(0xFFFFFFFFu, own) && !__all_sync(0xFFFFFFFFu, own);
     const bool together = __any_sync(0xFFFFFFFFu, mbar_wait_warp(&late[1], 0u, limit));
-    if (threadIdx.x == 64 && (!mixed || together)) atomicOr(&g_wait_err, kWaitLanes);
+    if (threadIdx.x == 64) mbar_arrive_expect_tx(&late[2], 0);
+    __syncwarp();
+    const bool given_up = mbar_wait_warp(&late[2], 0u) && !mbar_wait_warp(&late[2], 1u, 1000000ull);
+    mbar_ring_drain(&late[2], 2);
+    const bool arrived = mbar_try_wait(&late[2], 1u);
+    if (threadIdx.x == 64 && (!mixed || together || !given_up || !arrived)) atomicOr(&g_wait_err, kWaitLanes);
   } else if (threadIdx.x == 96) {
     const uint64_t t0 = global_timer_ns();
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       while (global_timer_ns() - t0 < (i + 1) * 200000000ull) __nanosleep(1000000);
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&late[i])) : "memory");
     }

@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, GV>::T, 2) k_attention_q4(Q4AttnAr
       __syncwarp();
       if (!dead && !mbar_wait_warp(&bar[st], phase)) {
         dead = true;
-        mbar_ring_drain(bar, ST, st, phase);
+        mbar_ring_drain(bar, ST);
       }
       const int t0 = (rel + unit0) * kUnit;
       const int fl = flag[st];

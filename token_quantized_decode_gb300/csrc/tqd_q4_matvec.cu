@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_q4_matvec(MatvecQ4Args a) {
         }
         // (each lane read the timer for itself: one that ran out speaks for the warp, whose sums hold its share)
         if (__any_sync(0xFFFFFFFFu, dead)) {
-          if (!stopped) mbar_ring_drain(bar, kMvStages, st, phase);
+          if (!stopped) mbar_ring_drain(bar, kMvStages);
           dead = stopped = true;
 #pragma unroll
           for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = __int_as_float(0x7FC00000);
