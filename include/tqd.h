@@ -564,6 +564,88 @@ int32_t tqd_op_logprobs(const float* logits, int64_t stride, int32_t rows, int32
                         void* scratch, void* stream);
 size_t tqd_logprobs_scratch_bytes(int32_t rows, int32_t vocab, int32_t top_k);
 
+/* ------------------------------------------------------------------------
+ * Rows of 8-bit codes: activations and weights as int8 with one scale a row, the
+ * norm and the SwiGLU product that end in such rows, and the product of two such
+ * matrices; and the rotation of many tokens' heads.  The conventions are those of
+ * the operators in 4 bits above: refusals before any launch, no rows no
+ * launch, capturable, nothing allocated, the same result in every run.
+ *
+ * A row y of n values is held as scale = f32(max|y| / 127) and codes q = rint(127 y /
+ * max|y|), ties to even, of the exact values (for rmsnorm: of h g, as 1 / rms is the
+ * same for the whole row): an element stands for q * scale.  A row of zeros has scale 0
+ * and codes 0.  A row with a NaN or an infinity, or whose largest value passes the f32
+ * range, has scale NaN and codes 0: it stands for NaN, and so does what a product
+ * makes of it.  rows <= 2^28, n <= 16384.  Row strides are in elements;
+ * outputs may not overlap inputs or one another, but for what is said below.
+ * Elements between n and a row's stride are neither read nor written.
+ * ------------------------------------------------------------------------ */
+
+/* Codes of x [rows][n] as they are (an attention's output; a weight's rows). */
+int32_t tqd_op_rows_i8(const float* x, int64_t x_stride, int32_t rows, int32_t n, int8_t* q, int64_t q_stride,
+                       float* scale, void* stream);
+
+/* h = x + add, rounded to f32 (add NULL: h = x), written to sum (which may be the
+ * rows of x or of add; NULL: not kept); then codes of h * (mean(h^2) + eps)^(-1/2) * g. */
+int32_t tqd_op_rmsnorm_i8(const float* x, int64_t x_stride, const float* add, int64_t add_stride, const float* g,
+                          int32_t rows, int32_t n, float eps, float* sum, int64_t sum_stride, int8_t* q,
+                          int64_t q_stride, float* scale, void* stream);
+
+/* Codes of silu(gate) * up, silu(z) = z / (1 + e^-z); both may be slices of one
+ * projection's rows. */
+int32_t tqd_op_silu_mul_i8(const float* gate, int64_t gate_stride, const float* up, int64_t up_stride, int32_t rows,
+                           int32_t n, int8_t* q, int64_t q_stride, float* scale, void* stream);
+
+/* The f32 values that rows of codes stand for. */
+int32_t tqd_op_rows_i8_read(const int8_t* q, int64_t q_stride, const float* scale, int32_t rows, int32_t n, float* out,
+                            int64_t out_stride, void* stream);
+
+/* y[j][r] = x_scale[j] * w_scale[r] * sum_c x[j][c] w[r][c] for n tokens over a matrix w
+ * [rows][cols] of codes (any int8 values), y f32 [n][rows].  The sum is exact; it is rounded to f32,
+ * multiplied by x_scale[j], then by w_scale[r].  cols % 32 == 0, cols <= 16384, rows <= 2^24,
+ * n <= 2^20; w contiguous and 16-byte aligned, the rows of x 16-byte aligned (x_stride % 16 == 0).
+ * scratch: tqd_i8_matmul_scratch_bytes(rows, cols, n) bytes, 16-byte aligned, whatever its contents
+ * (may be NULL where that is 0).  The size never falls as one of the three grows. */
+int32_t tqd_op_i8_matmul(const int8_t* w, const float* w_scale, int32_t rows, int32_t cols, const int8_t* x,
+                         int64_t x_stride, const float* x_scale, int32_t n, float* y, int64_t y_stride, void* scratch,
+                         void* stream);
+size_t tqd_i8_matmul_scratch_bytes(int32_t rows, int32_t cols, int32_t n);
+
+/* How a table's angles are scaled for contexts longer than the training's.  With
+ * f_i = theta^(-2 i / rotary_dim) and keep in [0, 1] (limited to it), pair i turns by f_i (keep +
+ * (1 - keep) / factor) a position:
+ *   TQD_ROPE_UNSCALED      keep = 1;
+ *   TQD_ROPE_LINEAR        keep = 0: positions divided by the factor;
+ *   TQD_ROPE_BY_ROTATIONS  keep = (r - low_rotations) / (high_rotations - low_rotations), r =
+ *                          original_len f_i / 2 pi, the pair's turns over the original length;
+ *   TQD_ROPE_BY_INDEX      keep falls linearly over the index i from 1 at `from` to 0 at `to`, the
+ *                          indices whose pairs turn high_rotations times (rounded down, not below
+ *                          0) and low_rotations times (rounded up, not above rotary_dim - 1).
+ * cos and sin are multiplied by attention_factor (1: none). */
+enum { TQD_ROPE_UNSCALED = 0, TQD_ROPE_LINEAR = 1, TQD_ROPE_BY_ROTATIONS = 2, TQD_ROPE_BY_INDEX = 3 };
+typedef struct tqd_rope_scaling {
+  int32_t kind;             /* TQD_ROPE_* */
+  float factor;
+  int32_t original_len;     /* positions of the original length */
+  float low_rotations;
+  float high_rotations;
+  float attention_factor;
+} tqd_rope_scaling;
+
+/* Fill table [max_pos][rotary_dim / 2] of (cos a, sin a) f32 pairs, angles in f64
+ * (scaling NULL: unscaled, as tqd_op_rope_table). */
+int32_t tqd_op_rope_table_scaled(float theta, int32_t rotary_dim, int32_t max_pos, const tqd_rope_scaling* scaling,
+                                 float* table, void* stream);
+
+/* Rotate the first rotary_dim elements of each of n_heads heads of n_tokens rows of x, f32
+ * [n_tokens][n_heads * head_dim <= 65536], by the tokens' positions: pairs (i, i + rotary_dim / 2),
+ * or with interleaved (2 i, 2 i + 1); (a, b) -> (a cos - b sin, b cos + a sin).  The rest of a
+ * head is copied.  out may be the rows of x, and may not overlap them otherwise.  A token whose
+ * position is negative or at or past max_pos is padding: nothing is written for it. */
+int32_t tqd_op_rope_rows(const float* x, int64_t x_stride, const int32_t* positions, int32_t n_tokens, int32_t n_heads,
+                         int32_t head_dim, const float* table, int32_t max_pos, int32_t rotary_dim, int32_t interleaved,
+                         float* out, int64_t out_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,7 @@ for _i, _n in enumerate(STATUS_NAMES):
 TQD_WEIGHT_Q8_0, TQD_WEIGHT_BF16 = 0, 1
 TQD_SCHED_GRAPH, TQD_SCHED_PERSISTENT = 0, 1
 TQD_KV_F32, TQD_KV_F16 = 0, 1
+TQD_ROPE_UNSCALED, TQD_ROPE_LINEAR, TQD_ROPE_BY_ROTATIONS, TQD_ROPE_BY_INDEX = 0, 1, 2, 3
 
 
 class tqd_config(ctypes.Structure):
@@ -55,6 +56,12 @@ class tqd_kv_q4(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("n_seq", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
+class tqd_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_float), ("original_len", ctypes.c_int32),
+                ("low_rotations", ctypes.c_float), ("high_rotations", ctypes.c_float),
+                ("attention_factor", ctypes.c_float)]
 
 
 class TQDError(RuntimeError):
@@ -128,6 +135,14 @@ def lib():
         "tqd_op_q4_0_matvec": (i32, [vp, i64, i64, vp, i32, i64, vp, i64, vp]),
         "tqd_op_logprobs": (i32, [vp, i64, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp]),
         "tqd_logprobs_scratch_bytes": (sz, [i32, i32, i32]),
+        "tqd_op_rows_i8": (i32, [vp, i64, i32, i32, vp, i64, vp, vp]),
+        "tqd_op_rmsnorm_i8": (i32, [vp, i64, vp, i64, vp, i32, i32, ctypes.c_float, vp, i64, vp, i64, vp, vp]),
+        "tqd_op_silu_mul_i8": (i32, [vp, i64, vp, i64, i32, i32, vp, i64, vp, vp]),
+        "tqd_op_rows_i8_read": (i32, [vp, i64, vp, i32, i32, vp, i64, vp]),
+        "tqd_op_i8_matmul": (i32, [vp, vp, i32, i32, vp, i64, vp, i32, vp, i64, vp, vp]),
+        "tqd_i8_matmul_scratch_bytes": (sz, [i32, i32, i32]),
+        "tqd_op_rope_table_scaled": (i32, [ctypes.c_float, i32, i32, P(tqd_rope_scaling), vp, vp]),
+        "tqd_op_rope_rows": (i32, [vp, i64, vp, i32, i32, i32, vp, i32, i32, i32, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -151,6 +166,8 @@ def exported_symbols():
         "tqd_kv_q4_page_bytes", "tqd_op_kv_append_q4", "tqd_op_kv_read_q4", "tqd_op_attention_q4",
         "tqd_attention_q4_scratch_bytes", "tqd_op_q4_0_repack", "tqd_q4_0_matrix_bytes", "tqd_op_q4_0_matvec",
         "tqd_op_logprobs", "tqd_logprobs_scratch_bytes",
+        "tqd_op_rows_i8", "tqd_op_rmsnorm_i8", "tqd_op_silu_mul_i8", "tqd_op_rows_i8_read", "tqd_op_i8_matmul",
+        "tqd_i8_matmul_scratch_bytes", "tqd_op_rope_table_scaled", "tqd_op_rope_rows",
     ]
 
 

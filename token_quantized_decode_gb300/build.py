@@ -21,7 +21,8 @@ LIB = os.path.join(BUILD, "libtqd.so")
 SYNTH_SRC = os.path.join(ROOT, "synth", "tqd_synth.c")
 
 SOURCES = ["tqd_kernels.cu", "tqd_persist.cu", "tqd_persist_bf16.cu", "tqd_engine.cu", "tqd_ops.cu", "tqd_noalloc.cu", "tqd_batch.cu",
-           "tqd_sample.cu", "tqd_q4_cache.cu", "tqd_q4_attention.cu", "tqd_q4_matvec.cu", "tqd_logprobs.cu"]
+           "tqd_sample.cu", "tqd_q4_cache.cu", "tqd_q4_attention.cu", "tqd_q4_matvec.cu", "tqd_logprobs.cu",
+           "tqd_i8_rows.cu", "tqd_i8_matmul.cu", "tqd_rope_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]

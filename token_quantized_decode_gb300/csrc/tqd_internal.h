@@ -216,6 +216,22 @@ constexpr int kLogprobMaxTopK = 32;
 size_t logprobs_scratch_bytes(int rows, int vocab, int top_k);
 cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t st);
 
+// Rows of 8-bit codes (tqd_i8_rows.cu), their products (tqd_i8_matmul.cu) and the
+// rotation of many tokens' heads (tqd_rope_rows.cu); arguments in tqd_i8.cuh.
+constexpr int kI8MaxCols = 16384;
+struct I8RowsArgs;
+cudaError_t launch_rows_i8(int kind, const I8RowsArgs& a, cudaStream_t st);
+cudaError_t launch_rows_i8_read(const int8_t* q, int64_t q_stride, const float* scale, int rows, int n, float* out,
+                                int64_t out_stride, cudaStream_t st);
+struct I8MatmulArgs;
+size_t i8_matmul_scratch_bytes(int rows, int cols, int n);
+cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st);
+struct RopeScaling;
+struct RopeRowsArgs;
+cudaError_t launch_rope_table_scaled(double theta, int rotary, int max_pos, const RopeScaling& sc, float2* table,
+                                     cudaStream_t st);
+cudaError_t launch_rope_rows(const RopeRowsArgs& a, bool interleaved, cudaStream_t st);
+
 // The bounded-wait self-test (tqd_op_wait_selftest): runs it on st and
 // returns the error bits its waits set.
 cudaError_t run_wait_selftest(uint32_t* err_bits, cudaStream_t st);

@@ -3,8 +3,10 @@
 // piece can be checked on its own, as in the inferno.rs blog's "The
 // correctness ladder", rung one.
 #include <cuda_runtime.h>
+#include <stdio.h>
 
 #include "tqd.h"
+#include "tqd_i8.cuh"
 #include "tqd_internal.h"
 #include "tqd_q4.cuh"
 
@@ -43,31 +45,39 @@ int32_t refuse(const char* why) {
   return TQD_ERR_BAD_ARG;
 }
 
-// n rows of `width` floats, `stride` floats apart (no less than width where n > 1).
+// n rows of `width` bytes, `stride` bytes apart (no less than width where n > 1): the
+// numbers are the caller's, so their products may pass 64 bits.
+using Wide = __int128;
+struct MemRows {
+  const void* p;
+  Wide stride, width;
+};
+// The same in floats.
 struct FloatRows {
   const float* p;
   int64_t stride, width;
+  operator MemRows() const { return {p, static_cast<Wide>(stride) * 4, static_cast<Wide>(width) * 4}; }
 };
 
-// Whether n rows of a and n rows of b share memory (rows may lie between one another's, as slices
+// Whether na rows of a and nb rows of b share memory (rows may lie between one another's, as slices
 // of one tensor's columns do).
-bool overlap(const FloatRows& a, const FloatRows& b, int64_t n) {
-  using Wide = __int128;  // strides and row numbers are the caller's
+bool meet(const MemRows& a, int64_t na, const MemRows& b, int64_t nb) {
   const Wide d = static_cast<Wide>(reinterpret_cast<uintptr_t>(b.p)) - static_cast<Wide>(reinterpret_cast<uintptr_t>(a.p));
-  const Wide wa = a.width * static_cast<Wide>(4), wb = b.width * static_cast<Wide>(4), last = n - 1;
-  const Wide sa = n > 1 ? a.stride * static_cast<Wide>(4) : wa, sb = n > 1 ? b.stride * static_cast<Wide>(4) : wb;
-  if (d >= last * sa + wa || -d >= last * sb + wb) return false;
+  const Wide wa = a.width, wb = b.width, la = na - 1, lb = nb - 1;
+  const Wide sa = na > 1 ? a.stride : wa, sb = nb > 1 ? b.stride : wb;
+  if (d >= la * sa + wa || -d >= lb * sb + wb) return false;
   auto floor_div = [](Wide x, Wide y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
   // row i of a, from offset `at`, meets the rows of b from lo to hi
   auto meets = [&](Wide at, Wide first) {
     const Wide lo = floor_div(at - wb - d, sb) + 1, hi = -floor_div(-(at + wa - d), sb) - 1;
-    return (lo > first ? lo : first) <= (hi < last ? hi : last);
+    return (lo > first ? lo : first) <= (hi < lb ? hi : lb);
   };
-  if (sa == sb) return meets(0, -last);  // the same for every row but for which rows there are
-  for (Wide i = 0; i <= last; ++i)
+  if (sa == sb && la == lb) return meets(0, -la);  // the same for every row but for which rows there are
+  for (Wide i = 0; i <= la; ++i)
     if (meets(i * sa, 0)) return true;
   return false;
 }
+bool overlap(const FloatRows& a, const FloatRows& b, int64_t n) { return meet(a, n, b, n); }
 
 size_t q4_page_bytes(int32_t n_kv, int32_t hd, int32_t page_size) {
   if (n_kv <= 0 || (hd != 64 && hd != 128) || page_size <= 0 || page_size % kQ4Block || page_size > (1 << 20))
@@ -85,6 +95,23 @@ int32_t q4_cache(const tqd_kv_q4* c, Q4Cache& o) {
   if (reinterpret_cast<uintptr_t>(c->pages) % 16) return refuse("tqd_kv_q4: pages must be 16-byte aligned");
   o = Q4Cache{c->pages, c->page_table, c->n_pages, c->page_size, c->n_kv_heads, c->n_seq, c->table_stride, pb};
   return TQD_OK;
+}
+
+constexpr int kI8MaxRows = 1 << 24, kI8MaxTokens = 1 << 20, kRopeMaxRow = 65536;
+
+// Sizes of rows of 8-bit codes; `where` begins with the call's name.
+int32_t i8_rows_size(const char* where, int32_t rows, int32_t n) {
+  if (rows > 0 && rows <= (1 << 28) && n > 0 && n <= kI8MaxCols) return TQD_OK;
+  static thread_local char text[128];
+  snprintf(text, sizeof(text), "%s: rows outside 1 .. 2^28, or n outside 1 .. 16384", where);
+  return refuse(text);
+}
+
+// Whether codes or scales of 8-bit rows share memory with `in` (n_in rows) or with one another.
+bool i8_rows_meet(const MemRows& in, int64_t n_in, const int8_t* q, int64_t q_stride, int32_t n, const float* scale,
+                  int32_t rows) {
+  const MemRows codes{q, q_stride, n}, scales = FloatRows{scale, rows, rows};
+  return meet(in, n_in, codes, rows) || meet(scales, 1, in, n_in) || meet(scales, 1, codes, rows);
 }
 
 }  // namespace
@@ -352,6 +379,144 @@ int32_t tqd_op_logprobs(const float* logits, int64_t stride, int32_t rows, int32
   if (reinterpret_cast<uintptr_t>(scratch) % 16) return refuse("tqd_op_logprobs: scratch must be 16-byte aligned");
   const LogprobArgs a{logits, targets, logprob, entropy, top_ids, top_logprobs, scratch, stride, rows, vocab, top_k};
   return status_of(launch_logprobs(a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t tqd_op_rows_i8(const float* x, int64_t x_stride, int32_t rows, int32_t n, int8_t* q, int64_t q_stride,
+                       float* scale, void* stream) {
+  if (!rows) return TQD_OK;
+  if (!x || !q || !scale) return refuse("tqd_op_rows_i8: NULL pointer");
+  if (const int32_t rc = i8_rows_size("tqd_op_rows_i8", rows, n)) return rc;
+  if (x_stride < n || q_stride < n) return refuse("tqd_op_rows_i8: a row stride shorter than the row");
+  const FloatRows in{x, x_stride, n};
+  if (i8_rows_meet(in, rows, q, q_stride, n, scale, rows)) return refuse("tqd_op_rows_i8: q or scale overlaps x or one another");
+  const I8RowsArgs a{x, nullptr, nullptr, nullptr, q, scale, x_stride, 0, 0, q_stride, rows, n, 0.f};
+  return status_of(launch_rows_i8(kI8Rows, a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t tqd_op_rmsnorm_i8(const float* x, int64_t x_stride, const float* add, int64_t add_stride, const float* g,
+                          int32_t rows, int32_t n, float eps, float* sum, int64_t sum_stride, int8_t* q,
+                          int64_t q_stride, float* scale, void* stream) {
+  if (!rows) return TQD_OK;
+  if (!x || !g || !q || !scale) return refuse("tqd_op_rmsnorm_i8: NULL x, g, q or scale");
+  if (const int32_t rc = i8_rows_size("tqd_op_rmsnorm_i8", rows, n)) return rc;
+  if (!(eps >= 0.f) || !(eps < 1e30f)) return refuse("tqd_op_rmsnorm_i8: eps must be a finite number >= 0");
+  if (x_stride < n || (add && add_stride < n) || (sum && sum_stride < n) || q_stride < n)
+    return refuse("tqd_op_rmsnorm_i8: a row stride shorter than the row");
+  const FloatRows in{x, x_stride, n}, to{sum, sum_stride, n}, more{add, add_stride, n}, gain{g, n, n};
+  if (sum) {
+    auto same = [&](const float* p, int64_t stride) { return p == sum && (stride == sum_stride || rows == 1); };
+    if ((!same(x, x_stride) && overlap(in, to, rows)) || (add && !same(add, add_stride) && overlap(more, to, rows)) ||
+        meet(gain, 1, to, rows))
+      return refuse("tqd_op_rmsnorm_i8: sum overlaps g, or x or add without being the same rows");
+    if (i8_rows_meet(to, rows, q, q_stride, n, scale, rows)) return refuse("tqd_op_rmsnorm_i8: q or scale overlaps sum or one another");
+  }
+  if (i8_rows_meet(in, rows, q, q_stride, n, scale, rows) || (add && i8_rows_meet(more, rows, q, q_stride, n, scale, rows)) ||
+      i8_rows_meet(gain, 1, q, q_stride, n, scale, rows))
+    return refuse("tqd_op_rmsnorm_i8: q or scale overlaps an input or one another");
+  const I8RowsArgs a{x, add, g, sum, q, scale, x_stride, add_stride, sum_stride, q_stride, rows, n, eps};
+  return status_of(launch_rows_i8(kI8Norm, a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t tqd_op_silu_mul_i8(const float* gate, int64_t gate_stride, const float* up, int64_t up_stride, int32_t rows,
+                           int32_t n, int8_t* q, int64_t q_stride, float* scale, void* stream) {
+  if (!rows) return TQD_OK;
+  if (!gate || !up || !q || !scale) return refuse("tqd_op_silu_mul_i8: NULL pointer");
+  if (const int32_t rc = i8_rows_size("tqd_op_silu_mul_i8", rows, n)) return rc;
+  if (gate_stride < n || up_stride < n || q_stride < n) return refuse("tqd_op_silu_mul_i8: a row stride shorter than the row");
+  const FloatRows ga{gate, gate_stride, n}, ua{up, up_stride, n};
+  if (i8_rows_meet(ga, rows, q, q_stride, n, scale, rows) || i8_rows_meet(ua, rows, q, q_stride, n, scale, rows))
+    return refuse("tqd_op_silu_mul_i8: q or scale overlaps an input or one another");
+  const I8RowsArgs a{gate, up, nullptr, nullptr, q, scale, gate_stride, up_stride, 0, q_stride, rows, n, 0.f};
+  return status_of(launch_rows_i8(kI8Silu, a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t tqd_op_rows_i8_read(const int8_t* q, int64_t q_stride, const float* scale, int32_t rows, int32_t n, float* out,
+                            int64_t out_stride, void* stream) {
+  if (!rows) return TQD_OK;
+  if (!q || !scale || !out) return refuse("tqd_op_rows_i8_read: NULL pointer");
+  if (const int32_t rc = i8_rows_size("tqd_op_rows_i8_read", rows, n)) return rc;
+  if (q_stride < n || out_stride < n) return refuse("tqd_op_rows_i8_read: a row stride shorter than the row");
+  const FloatRows to{out, out_stride, n};
+  if (meet(MemRows{q, q_stride, n}, rows, to, rows) || meet(FloatRows{scale, rows, rows}, 1, to, rows))
+    return refuse("tqd_op_rows_i8_read: out overlaps q or scale");
+  return status_of(launch_rows_i8_read(q, q_stride, scale, rows, n, out, out_stride, static_cast<cudaStream_t>(stream)));
+}
+
+size_t tqd_i8_matmul_scratch_bytes(int32_t rows, int32_t cols, int32_t n) {
+  if (rows <= 0 || rows > kI8MaxRows || cols <= 0 || cols % 32 || cols > kI8MaxCols || n <= 0 || n > kI8MaxTokens) return 0;
+  return i8_matmul_scratch_bytes(rows, cols, n);
+}
+
+int32_t tqd_op_i8_matmul(const int8_t* w, const float* w_scale, int32_t rows, int32_t cols, const int8_t* x,
+                         int64_t x_stride, const float* x_scale, int32_t n, float* y, int64_t y_stride, void* scratch,
+                         void* stream) {
+  if (!n) return TQD_OK;
+  if (!w || !w_scale || !x || !x_scale || !y) return refuse("tqd_op_i8_matmul: NULL pointer");
+  if (rows <= 0 || rows > kI8MaxRows || cols <= 0 || cols % 32 || cols > kI8MaxCols || n < 0 || n > kI8MaxTokens)
+    return refuse("tqd_op_i8_matmul: rows outside 1 .. 2^24, cols no multiple of 32 up to 16384, or n above 2^20");
+  if (n > 1 && (x_stride < cols || y_stride < rows)) return refuse("tqd_op_i8_matmul: a row stride shorter than the row");
+  if (reinterpret_cast<uintptr_t>(w) % 16 || reinterpret_cast<uintptr_t>(x) % 16 || (n > 1 && x_stride % 16))
+    return refuse("tqd_op_i8_matmul: w and every row of x must be 16-byte aligned");
+  const int64_t need = static_cast<int64_t>(i8_matmul_scratch_bytes(rows, cols, n));
+  if (need && (!scratch || reinterpret_cast<uintptr_t>(scratch) % 16))
+    return refuse("tqd_op_i8_matmul: scratch of tqd_i8_matmul_scratch_bytes, 16-byte aligned, is needed");
+  const FloatRows to{y, y_stride, rows};
+  const MemRows matrix{w, static_cast<Wide>(rows) * cols, static_cast<Wide>(rows) * cols}, tokens{x, x_stride, cols};
+  if (meet(tokens, n, to, n) || meet(matrix, 1, to, n) || meet(FloatRows{w_scale, rows, rows}, 1, to, n) ||
+      meet(FloatRows{x_scale, n, n}, 1, to, n))
+    return refuse("tqd_op_i8_matmul: y overlaps an input");
+  if (need) {
+    const MemRows room{scratch, need, need};
+    if (meet(room, 1, to, n) || meet(room, 1, tokens, n) || meet(room, 1, matrix, 1) ||
+        meet(room, 1, FloatRows{w_scale, rows, rows}, 1) || meet(room, 1, FloatRows{x_scale, n, n}, 1))
+      return refuse("tqd_op_i8_matmul: scratch overlaps another argument");
+  }
+  const I8MatmulArgs a{w, w_scale, x, x_scale, y, scratch, x_stride, y_stride, rows, cols, n};
+  return status_of(launch_i8_matmul(a, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t tqd_op_rope_table_scaled(float theta, int32_t rotary_dim, int32_t max_pos, const tqd_rope_scaling* scaling,
+                                 float* table, void* stream) {
+  if (!table || !(theta > 0.f) || !(theta < 1e30f) || rotary_dim <= 0 || rotary_dim % 2 || rotary_dim > kRopeMaxRow || max_pos <= 0)
+    return refuse("tqd_op_rope_table_scaled: NULL table, theta not positive and finite, rotary_dim odd or outside 2 .. 65536, or no positions");
+  RopeScaling s{kRopeUnscaled, 1.0, 0.0, 0.0, 0.0, 1.0};
+  if (scaling) {
+    s = RopeScaling{scaling->kind, scaling->factor, static_cast<double>(scaling->original_len), scaling->low_rotations,
+                    scaling->high_rotations, scaling->attention_factor};
+    if (s.kind < kRopeUnscaled || s.kind > kRopeByIndex) return refuse("tqd_op_rope_table_scaled: unknown kind of scaling");
+    if (!(s.attention > 0.0 && s.attention < 1e30)) return refuse("tqd_op_rope_table_scaled: attention_factor must be positive and finite");
+    if (s.kind != kRopeUnscaled && !(s.factor > 0.0 && s.factor < 1e30))
+      return refuse("tqd_op_rope_table_scaled: factor must be positive and finite");
+    if (s.kind >= kRopeByRotations && !(s.original > 0.0 && s.low > 0.0 && s.high > s.low && s.high < 1e30))
+      return refuse("tqd_op_rope_table_scaled: original_len > 0 and 0 < low_rotations < high_rotations are needed");
+    if (s.kind == kRopeByIndex && !(theta > 1.f)) return refuse("tqd_op_rope_table_scaled: scaling by index needs theta above 1");
+  }
+  return status_of(launch_rope_table_scaled(static_cast<double>(theta), rotary_dim, max_pos, s,
+                                            reinterpret_cast<float2*>(table), static_cast<cudaStream_t>(stream)));
+}
+
+int32_t tqd_op_rope_rows(const float* x, int64_t x_stride, const int32_t* positions, int32_t n_tokens, int32_t n_heads,
+                         int32_t head_dim, const float* table, int32_t max_pos, int32_t rotary_dim, int32_t interleaved,
+                         float* out, int64_t out_stride, void* stream) {
+  if (!n_tokens) return TQD_OK;
+  if (!x || !positions || !table || !out || n_tokens < 0 || max_pos <= 0)
+    return refuse("tqd_op_rope_rows: NULL pointer, n_tokens < 0, or a table without positions");
+  if (n_heads <= 0 || head_dim <= 0 || rotary_dim <= 0 || rotary_dim % 2 || rotary_dim > head_dim ||
+      static_cast<int64_t>(n_heads) * head_dim > kRopeMaxRow)
+    return refuse("tqd_op_rope_rows: rotary_dim must be even and at most head_dim, and a row at most 65536 floats");
+  if (interleaved != 0 && interleaved != 1) return refuse("tqd_op_rope_rows: interleaved is 0 or 1");
+  const int64_t w = static_cast<int64_t>(n_heads) * head_dim;
+  if (n_tokens > 1 && (x_stride < w || out_stride < w)) return refuse("tqd_op_rope_rows: a row stride shorter than the row");
+  if (reinterpret_cast<uintptr_t>(table) % 8) return refuse("tqd_op_rope_rows: table must be 8-byte aligned");
+  const FloatRows in{x, x_stride, w}, to{out, out_stride, w};
+  const int64_t entries = static_cast<int64_t>(max_pos) * rotary_dim;
+  const bool same = x == out && (x_stride == out_stride || n_tokens == 1);
+  if ((!same && overlap(in, to, n_tokens)) || meet(FloatRows{table, entries, entries}, 1, to, n_tokens) ||
+      meet(FloatRows{reinterpret_cast<const float*>(positions), n_tokens, n_tokens}, 1, to, n_tokens))
+    return refuse("tqd_op_rope_rows: out overlaps table or positions, or x without being the same rows");
+  const RopeRowsArgs a{x, out, positions, reinterpret_cast<const float2*>(table), x_stride, out_stride, n_tokens,
+                       n_heads, head_dim, rotary_dim, max_pos};
+  return status_of(launch_rope_rows(a, interleaved != 0, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

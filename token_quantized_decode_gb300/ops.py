@@ -5,16 +5,16 @@ from __future__ import annotations
 
 from ctypes import byref
 
-from ._lib import TQDError, check, lib, tqd_kv_q4
+from ._lib import TQDError, check, lib, tqd_kv_q4, tqd_rope_scaling
 
 
 torch = None  # bound at the first call (the rest of the package does not need it)
 
 
 def _bind():
-    global torch, _stream_of, _device, _F32, _I32, _U8
+    global torch, _stream_of, _device, _F32, _I32, _U8, _I8
     import torch as t
-    _F32, _I32, _U8 = t.float32, t.int32, t.uint8
+    _F32, _I32, _U8, _I8 = t.float32, t.int32, t.uint8, t.int8
     # (without a GPU no tensor is on device 0, and every call is refused)
     _device = t.cuda.current_device if t.cuda.is_available() else lambda: 0
     raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
@@ -135,12 +135,12 @@ def _ptr(t, dtype, n, dev, where, name):
                    f"device) is needed, got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _rows(t, n, width, dev, where, name):
-    """Pointer and row stride of an f32 tensor [n, width] with contiguous rows ([width] when n is 1)."""
+def _rows(t, n, width, dev, where, name, dtype=None):
+    """Pointer and row stride of an f32 (or dtype) tensor [n, width] with contiguous rows ([width] when n is 1)."""
     shape = t.shape
-    if t.dtype is not _F32 or t.get_device() != dev or not (shape == (n, width) or (n == 1 and shape == (width,))):
-        _refuse(where, f"{name}: an f32 tensor [{n}, {width}] on cuda:{dev} (the current CUDA device) is needed, got "
-                       f"{tuple(shape)} {t.dtype} on {t.device}")
+    if t.dtype is not (dtype or _F32) or t.get_device() != dev or not (shape == (n, width) or (n == 1 and shape == (width,))):
+        _refuse(where, f"{name}: a {dtype or _F32} tensor [{n}, {width}] on cuda:{dev} (the current CUDA device) is needed, "
+                       f"got {tuple(shape)} {t.dtype} on {t.device}")
     if n == 1 or not n:
         if width > 1 and n and t.stride(-1) != 1:
             _refuse(where, f"{name}: the elements of a row must be contiguous")
@@ -325,5 +325,137 @@ def tqd_op_logprobs(logits, targets, logprob, entropy, top_ids, top_logprobs, sc
         lp, ls, n, v, tp, op, ep, k, ip, kp,
         _ptr(scratch, _U8, L.tqd_logprobs_scratch_bytes(n, v, k), dev, where, "scratch"),
         _stream_of(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, where)
+
+
+# ------------------------------------------------------------------ rows of 8-bit codes, rotation of many rows
+
+def _shape(t, where, name):
+    """(rows, width) of [rows, width], or of [width] as one row."""
+    if torch is None:
+        _bind()
+    shape = t.shape
+    if len(shape) == 2:
+        return shape
+    if len(shape) != 1:
+        _refuse(where, f"{name}: [rows, width], or [width] for one row")
+    return 1, shape[0]
+
+
+def tqd_op_rows_i8(x, q, scale, stream=None):
+    """Codes of x [rows, n] into q (int8, the same shape), scales into scale [rows]."""
+    where = "tqd_op_rows_i8"
+    n, w = _shape(x, where, "x")
+    dev = _device()
+    xp, xs = _rows(x, n, w, dev, where, "x")
+    qp, qs = _rows(q, n, w, dev, where, "q", _I8)
+    status = lib().tqd_op_rows_i8(xp, xs, n, w, qp, qs, _ptr(scale, _F32, n, dev, where, "scale"),
+                                  _stream_of(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, where)
+
+
+def tqd_op_rmsnorm_i8(x, add, g, eps: float, sum_out, q, scale, stream=None):
+    """h = x + add [rows, n] (add None: x), kept in sum_out (may be x or add; None: not); codes of its RMSNorm with
+    gains g [n] into q, scales into scale."""
+    where = "tqd_op_rmsnorm_i8"
+    n, w = _shape(x, where, "x")
+    dev = _device()
+    xp, xs = _rows(x, n, w, dev, where, "x")
+    ap, as_ = (None, 0) if add is None else _rows(add, n, w, dev, where, "add")
+    sp, ss = (None, 0) if sum_out is None else _rows(sum_out, n, w, dev, where, "sum_out")
+    qp, qs = _rows(q, n, w, dev, where, "q", _I8)
+    status = lib().tqd_op_rmsnorm_i8(xp, xs, ap, as_, _ptr(g, _F32, w, dev, where, "g"), n, w, eps, sp, ss, qp, qs,
+                                     _ptr(scale, _F32, n, dev, where, "scale"),
+                                     _stream_of(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, where)
+
+
+def tqd_op_silu_mul_i8(gate, up, q, scale, stream=None):
+    """Codes of silu(gate) * up [rows, n] into q, scales into scale (gate and up may be slices of one tensor)."""
+    where = "tqd_op_silu_mul_i8"
+    n, w = _shape(gate, where, "gate")
+    dev = _device()
+    gp, gs = _rows(gate, n, w, dev, where, "gate")
+    up_, us = _rows(up, n, w, dev, where, "up")
+    qp, qs = _rows(q, n, w, dev, where, "q", _I8)
+    status = lib().tqd_op_silu_mul_i8(gp, gs, up_, us, n, w, qp, qs, _ptr(scale, _F32, n, dev, where, "scale"),
+                                      _stream_of(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, where)
+
+
+def tqd_op_rows_i8_read(q, scale, out, stream=None):
+    """The values that rows of codes stand for, f32 [rows, n]."""
+    where = "tqd_op_rows_i8_read"
+    n, w = _shape(q, where, "q")
+    dev = _device()
+    qp, qs = _rows(q, n, w, dev, where, "q", _I8)
+    op, os_ = _rows(out, n, w, dev, where, "out")
+    status = lib().tqd_op_rows_i8_read(qp, qs, _ptr(scale, _F32, n, dev, where, "scale"), n, w, op, os_,
+                                       _stream_of(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, where)
+
+
+def tqd_i8_matmul_scratch_bytes(rows: int, cols: int, n: int) -> int:
+    return int(lib().tqd_i8_matmul_scratch_bytes(rows, cols, n))
+
+
+def tqd_op_i8_matmul(w, w_scale, x, x_scale, y, scratch=None, stream=None):
+    """y [n, rows] = (x [n, cols] * x_scale [n]) (w [rows, cols] * w_scale [rows])^T over codes.  scratch: uint8 of
+    tqd_i8_matmul_scratch_bytes(rows, cols, n) (None where that is 0)."""
+    where = "tqd_op_i8_matmul"
+    n, cols = _shape(x, where, "x")
+    if w.dim() != 2 or w.shape[1] != cols:
+        _refuse(where, "w: [rows, cols] with the columns of x")
+    dev = _device()
+    rows = w.shape[0]
+    L = lib()
+    xp, xs = _rows(x, n, cols, dev, where, "x", _I8)
+    yp, ys = _rows(y, n, rows, dev, where, "y")
+    need = L.tqd_i8_matmul_scratch_bytes(rows, cols, n)
+    if need and scratch is None:
+        _refuse(where, f"scratch of {need} bytes is needed")
+    status = L.tqd_op_i8_matmul(_ptr(w, _I8, rows * cols, dev, where, "w"), _ptr(w_scale, _F32, rows, dev, where, "w_scale"),
+                                rows, cols, xp, xs, _ptr(x_scale, _F32, n, dev, where, "x_scale"), n, yp, ys,
+                                _ptr(scratch, _U8, need, dev, where, "scratch") if need else None,
+                                _stream_of(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, where)
+
+
+def rope_scaling(kind: int, factor: float = 1.0, original_len: int = 0, low_rotations: float = 1.0,
+                 high_rotations: float = 32.0, attention_factor: float = 1.0) -> tqd_rope_scaling:
+    """How a table's angles are scaled for long contexts (TQD_ROPE_*)."""
+    return tqd_rope_scaling(kind, factor, original_len, low_rotations, high_rotations, attention_factor)
+
+
+def tqd_op_rope_table_scaled(theta: float, rotary_dim: int, max_pos: int, scaling, table, stream=None):
+    """(cos, sin) of max_pos positions into table (f32, max_pos * rotary_dim); scaling: rope_scaling(...) or None."""
+    where = "tqd_op_rope_table_scaled"
+    if torch is None:
+        _bind()
+    dev = _device()
+    check(lib().tqd_op_rope_table_scaled(theta, rotary_dim, max_pos, None if scaling is None else byref(scaling),
+                                         _ptr(table, _F32, max_pos * rotary_dim, dev, where, "table"), _s(stream)), where)
+
+
+def tqd_op_rope_rows(x, positions, table, head_dim: int, rotary_dim: int, interleaved: bool, out, stream=None):
+    """Rotate the first rotary_dim elements of every head of x [n, heads * head_dim] by positions [n] into out (may be
+    x).  table: tqd_op_rope_table_scaled's, whole rows of rotary_dim floats."""
+    where = "tqd_op_rope_rows"
+    n, w = _shape(x, where, "x")
+    if head_dim <= 0 or w % head_dim or rotary_dim <= 0 or table.numel() % rotary_dim:
+        _refuse(where, "x: whole heads of head_dim; table: whole rows of rotary_dim")
+    dev = _device()
+    xp, xs = _rows(x, n, w, dev, where, "x")
+    op, os_ = _rows(out, n, w, dev, where, "out")
+    status = lib().tqd_op_rope_rows(xp, xs, _ptr(positions, _I32, n, dev, where, "positions"), n, w // head_dim, head_dim,
+                                    _ptr(table, _F32, rotary_dim, dev, where, "table"), table.numel() // rotary_dim,
+                                    rotary_dim, 1 if interleaved else 0, op, os_,
+                                    _stream_of(dev) if stream is None else stream.cuda_stream)
     if status:
         check(status, where)
