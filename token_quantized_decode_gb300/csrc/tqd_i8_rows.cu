@@ -4,10 +4,9 @@
 //
 // The codes are those of the exact values.  In f32 the quotient t = 127 y / max|y| is
 // known to within kBand; where t lies that near to a border between two codes,
-// and only there, it is taken again in f64, with the row's largest value in f64
-// too (found among the elements whose code is 127 in magnitude).  A row whose
-// largest value or sum of squares leaves the middle of the f32 range is done in
-// f64 as a whole, so neither squares nor products overflow or vanish.  The norm's
+// and only there, it is taken again in f64, with the row's largest value in f64 too.
+// A row whose largest value or sum of squares leaves the middle of the f32 range
+// is done in f64 as a whole, so neither squares nor products overflow or vanish.  The norm's
 // 1 / rms multiplies every element alike: it is in the scale and not in the codes.
 #include <cuda_runtime.h>
 #include <float.h>
@@ -19,16 +18,44 @@
 namespace tqd {
 namespace {
 
+constexpr int kSms = 152;
+
 // The relative errors that reach t, in units of 2^-24, times 127: of y (exact for
 // rows; the product h g, 1; expf 4, 1 + e, the quotient and the product with up 3), of the
 // largest y the same, of 127 / max and of the product with it 1 each.  2 * 127 * 2^-24 =
 // 2^-16, 4 * 127 * 2^-24 = 2^-15, 16 * 127 * 2^-24 = 2^-13.
 template <int kKind>
-constexpr float kBand = kKind == kI8Silu ? 0x1p-12f : 0x1p-14f;
+constexpr float kBand = kKind == kI8Rows ? 0x1p-16f : kKind == kI8Norm ? 0x1p-15f : 0x1p-13f;
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it leaves the nearest whole number in the low bits
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
+
+// silu(g) u in f64 to 2^-40, for gates whose e^-g is within f32: of a row whose largest |y| is at least 2^-40
+// and whose |u| are at most 2^40, elements of at least a 2^8th of the largest have g > -62.  The f64 pipe does a
+// warp's instruction in 15 clocks, so this takes the reduction to |r| <= ln 2 / 2 with ln 2 in two parts (Cody and
+// Waite), ten terms of the Taylor series, and one step of Newton's iteration from the f32 reciprocal in place of
+// exp and a division.
+constexpr double kLn2High = 0.6931471804855391, kLn2Low = 7.440617110012397e-11;  // 33 bits after the point, and the rest
+__device__ __noinline__ double near_silu(float g, float u) {
+  const double x = fmax(-static_cast<double>(g), -64.0);  // (e^-64 is nothing beside 1)
+  const double k = rint(x * 1.4426950408889634);
+  const double r = fma(k, -kLn2Low, fma(k, -kLn2High, x));
+  double e = 1.0 / 3628800;
+  e = fma(e, r, 1.0 / 362880);
+  e = fma(e, r, 1.0 / 40320);
+  e = fma(e, r, 1.0 / 5040);
+  e = fma(e, r, 1.0 / 720);
+  e = fma(e, r, 1.0 / 120);
+  e = fma(e, r, 1.0 / 24);
+  e = fma(e, r, 1.0 / 6);
+  e = fma(e, r, 0.5);
+  e = fma(e, r, 1.0);
+  e = fma(e, r, 1.0);
+  const double d = 1.0 + e * __hiloint2double((1023 + static_cast<int>(k)) << 20, 0);
+  const double q = 1.f / static_cast<float>(d);
+  return fma(fma(-d, q, 1.0), q, q) * g * u;
+}
 
 // Element i of a row in f64, from memory again (the norm: without 1 / rms; h is its sum in f32).
 template <int kKind>
@@ -46,6 +73,16 @@ __device__ __noinline__ double exact_element(const I8RowsArgs& a, int64_t row, i
   return x / (1.0 + exp(-static_cast<double>(x))) * u;
 }
 
+// The code of y in a row whose largest value is `most`.
+__device__ __noinline__ float exact_code(double y, double most) { return static_cast<float>(rint(127.0 * y / most)); }
+
+// The largest of a and |b|, |c|; NaN where one of them is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <bool kVec>
 __device__ __forceinline__ void load4(const float* p, int i, int n, float (&v)[4]) {
   if (kVec) {
@@ -58,19 +95,25 @@ __device__ __forceinline__ void load4(const float* p, int i, int n, float (&v)[4
   }
 }
 
+// Elements i to i + 3 of a row into 16 bytes of shared memory, zeros past the row's end.
+template <bool kVec>
+__device__ __forceinline__ void fetch4(float4* to, const float* p, int i, int n) {
+  const uint32_t dst = smem_addr(to);
+  if (kVec) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p + (i < n ? i : 0)), "r"(i < n ? 16 : 0)
+                 : "memory");
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * j), "l"(p + (i + j < n ? i + j : 0)),
+                   "r"(i + j < n ? 4 : 0)
+                   : "memory");
+  }
+}
+
 // Reductions over the kT threads of a row: one warp, or the whole block.
 template <int kT>
 struct RowGroup {
-  static __device__ __forceinline__ uint32_t max_u32(uint32_t v, uint32_t* sh) {
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    if (kT == 32) return v;
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sh[0];
-#pragma unroll
-    for (int w = 1; w < kT / 32; ++w) v = max(v, sh[w]);
-    return v;
-  }
   static __device__ __forceinline__ bool any(bool p) {
     return kT == 32 ? __any_sync(0xFFFFFFFFu, p) : __syncthreads_or(p) != 0;
   }
@@ -88,141 +131,231 @@ struct RowGroup {
   }
 };
 
-// kT threads a row, kE groups of four elements a thread.  kVec: every row of every tensor
-// begins on a 16-byte boundary (codes: 4) and is whole groups of four.
-template <int kKind, int kT, int kE, bool kVec>
-__global__ void __launch_bounds__(kT < 128 ? 128 : kT) k_rows_i8(const I8RowsArgs a) {
-  __shared__ uint32_t sh_max[32];
-  __shared__ float sh_sum[32];
-  __shared__ double sh_d[32];
-  const int t = threadIdx.x % kT;
-  const int64_t row = kT < 128 ? static_cast<int64_t>(blockIdx.x) * (128 / kT) + threadIdx.x / kT : blockIdx.x;
-  if (row >= a.rows) return;  // whole warps, of blocks without barriers
-  const int n = a.n;
-  const float* x = a.x + row * a.x_stride;
-  const float* other = a.other ? a.other + row * a.other_stride : nullptr;
-
-  float v[kE][4], w[kE][4];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) load4<kVec>(x, (e * kT + t) * 4, n, v[e]);
-  if (kKind == kI8Silu || (kKind == kI8Norm && other)) {
-#pragma unroll
-    for (int e = 0; e < kE; ++e) load4<kVec>(other, (e * kT + t) * 4, n, w[e]);
+// The codes of the elements of `near` (bit 4 e + j: group e of the thread, element j) again, in f64.  Rows as they are
+// know their largest value m; of the others it is found among the elements of `tops`, by the whole row's threads.
+template <int kKind, int kT>
+__device__ __noinline__ void codes_again(const I8RowsArgs& a, int64_t row, int t, uint32_t near, uint32_t tops, float m,
+                                         unsigned long long* sh_most) {
+  auto place = [&](uint32_t bits) {
+    const int b = __ffs(bits) - 1;
+    return (b / 4 * kT + t) * 4 + b % 4;
+  };
+  auto element = [&](int i) {
+    double h;
+    if (kKind == kI8Silu) return near_silu(a.x[row * a.x_stride + i], a.other[row * a.other_stride + i]);
+    return exact_element<kKind>(a, row, i, h);
+  };
+  double most = m;
+  if (kKind != kI8Rows) {
+    most = 0.0;
+    for (; tops; tops &= tops - 1) most = fmax(most, fabs(element(place(tops))));
+    if (kT == 32) {
+      most = RowGroup<kT>::all(most, nullptr, [](double p, double q) { return fmax(p, q); });
+    } else {
+      if (most > 0.0) atomicMax(sh_most, static_cast<unsigned long long>(__double_as_longlong(most)));
+      __syncthreads();
+      most = __longlong_as_double(static_cast<long long>(*sh_most));
+    }
   }
-  uint32_t top = 0u;  // the largest |y|, as bits: a NaN or an infinity is above all
-  float ss = 0.f;
+  int8_t* q = a.q + row * a.q_stride;
+  for (; near; near &= near - 1) {
+    const int i = place(near);
+    q[i] = static_cast<int8_t>(exact_code(element(i), most));
+  }
+}
+
+// A row in f64 as a whole.
+template <int kKind, int kT>
+__device__ __noinline__ void whole_row(const I8RowsArgs& a, int64_t row, int t, double* sh) {
+  const int n = a.n;
+  double most = 0.0, squares = 0.0, h;
+  bool lost = false;
+  for (int i = t; i < n; i += kT) {
+    const double y = exact_element<kKind>(a, row, i, h);
+    lost = lost || !(fabs(y) <= DBL_MAX);
+    most = fmax(most, fabs(y));
+    squares += h * h;
+  }
+  most = RowGroup<kT>::all(most, sh, [](double p, double q) { return fmax(p, q); });
+  lost = RowGroup<kT>::any(lost);
+  double top = most;
+  if (kKind == kI8Norm) {
+    squares = RowGroup<kT>::all(squares, sh, [](double p, double q) { return p + q; });
+    const double at = squares / n + a.eps;
+    top = at > 0.0 ? most / sqrt(at) : 0.0;
+  }
+  if (!isfinite(static_cast<float>(top))) lost = true;
+  int8_t* q = a.q + row * a.q_stride;
+  for (int i = t; i < n; i += kT)
+    q[i] = lost || most == 0.0 ? 0 : static_cast<int8_t>(exact_code(exact_element<kKind>(a, row, i, h), most));
+  if (t == 0) a.scale[row] = lost ? __uint_as_float(0x7FC00000u) : static_cast<float>(top / 127.0);
+}
+
+// How many rows' inputs a thread has under way, and CTAs an SM.
+template <int kKind, int kT, int kE>
+struct RowsCfg {
+  static constexpr int block = kT < 128 ? 128 : kT;
+  static constexpr int inputs = kKind == kI8Rows ? 1 : 2, ahead = kKind == kI8Rows ? 2 : 1;
+  static constexpr int smem = block * kE * 16 * inputs * ahead;
+  static constexpr int ctas = kT >= 1024 ? 1 : kT == 512 ? 2 : kT == 256 ? (kE == 4 ? 3 : kKind == kI8Rows ? 5 : 4)
+                              : kE == 4 ? 5 : kKind == kI8Rows ? 8 : 7;
+  static constexpr bool keep_gains = kE <= 2;  // in registers, from row to row
+};
+
+// kT threads a row, kE groups of four elements a thread.  kVec: every row of every tensor
+// begins on a 16-byte boundary (codes: 4) and is whole groups of four.  CTAs go from row to
+// row; a thread copies its elements of the next row into its own part of shared memory
+// while it works on this one, so that loads are always under way.
+template <int kKind, int kT, int kE, bool kVec>
+__global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, kT, kE>::ctas)
+    k_rows_i8(const __grid_constant__ I8RowsArgs a) {
+  using Cfg = RowsCfg<kKind, kT, kE>;
+  extern __shared__ float4 next_rows[];  // [ahead][inputs][kE][block]
+  __shared__ uint32_t sh_max[2][32];     // the largest |y| of each warp, as bits
+  __shared__ float sh_sum[2][32];
+  __shared__ double sh_d[32];
+  __shared__ unsigned long long sh_most[2];
+  const int t = threadIdx.x % kT, lane = threadIdx.x & 31, n = a.n;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (Cfg::block / kT);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * (Cfg::block / kT) + threadIdx.x / kT;
+  const bool two = kKind == kI8Silu || (kKind == kI8Norm && a.other);
+  auto fetch = [&](int at, int64_t r) {  // (a row past the last: nothing, but a group of its own)
+    float4* to = next_rows + at * (Cfg::inputs * kE * Cfg::block) + threadIdx.x;
+    if (r < a.rows) {
+#pragma unroll(kVec ? kE : 1)
+      for (int e = 0; e < kE; ++e) fetch4<kVec>(to + e * Cfg::block, a.x + r * a.x_stride, (e * kT + t) * 4, n);
+      if (two) {
+#pragma unroll(kVec ? kE : 1)
+        for (int e = 0; e < kE; ++e)
+          fetch4<kVec>(to + (kE + e) * Cfg::block, a.other + r * a.other_stride, (e * kT + t) * 4, n);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < Cfg::ahead; ++i) fetch(i, row + i * step);
+  float gains[Cfg::keep_gains && kKind == kI8Norm ? kE : 1][4];
+  if (Cfg::keep_gains && kKind == kI8Norm) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) load4<kVec>(a.g, (e * kT + t) * 4, n, gains[e]);
+  }
+#pragma unroll 1
+  for (int turn = 0; row < a.rows; row += step, ++turn) {
+  const int odd = turn & 1;
+  float v[kE][4], w[kE][4];  // y; what else came in (the norm: then h)
+  asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::ahead - 1) : "memory");
+  {
+    const float4* from = next_rows + turn % Cfg::ahead * (Cfg::inputs * kE * Cfg::block) + threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const float4 f = from[e * Cfg::block];
+      v[e][0] = f.x, v[e][1] = f.y, v[e][2] = f.z, v[e][3] = f.w;
+      if (two) {
+        const float4 o = from[(kE + e) * Cfg::block];
+        w[e][0] = o.x, w[e][1] = o.y, w[e][2] = o.z, w[e][3] = o.w;
+      }
+    }
+  }
+  fetch(turn % Cfg::ahead, row + Cfg::ahead * step);
+  float top = 0.f, ss = 0.f;  // the largest |y| (a NaN or an infinity is above all), the sum of h^2
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
     const int i = (e * kT + t) * 4;
     if (kKind == kI8Silu) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[e][j] = silu(v[e][j]) * w[e][j];
+      for (int j = 0; j < 4; ++j) {
+        v[e][j] = silu(v[e][j]) * w[e][j];
+        if (fabsf(w[e][j]) > 0x1p40f) top = INFINITY;  // silu may be below f32's range, and count: the row in f64
+      }
     }
     if (kKind == kI8Norm) {
-      if (other) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[e][j] += w[e][j];
-      }
+      for (int j = 0; j < 4; ++j) w[e][j] = two ? v[e][j] + w[e][j] : v[e][j];
       if (a.sum) {
         float* s = a.sum + row * a.sum_stride + i;
         if (kVec) {
-          if (i < n) *reinterpret_cast<float4*>(s) = make_float4(v[e][0], v[e][1], v[e][2], v[e][3]);
+          if (i < n) *reinterpret_cast<float4*>(s) = make_float4(w[e][0], w[e][1], w[e][2], w[e][3]);
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (i + j < n) s[j] = v[e][j];
+            if (i + j < n) s[j] = w[e][j];
         }
       }
       float g[4];
-      load4<kVec>(a.g, i, n, g);
+      if (!Cfg::keep_gains) load4<kVec>(a.g, i, n, g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        ss = fmaf(v[e][j], v[e][j], ss);
-        v[e][j] *= g[j];
+        ss = fmaf(w[e][j], w[e][j], ss);
+        v[e][j] = w[e][j] * (Cfg::keep_gains ? gains[Cfg::keep_gains ? e : 0][j] : g[j]);
       }
     }
+    top = max_abs(max_abs(top, v[e][0], v[e][1]), v[e][2], v[e][3]);
+  }
+  uint32_t high = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top) & 0x7FFFFFFFu);
+  if (kKind == kI8Norm) ss = warp_sum(ss);
+  if (kT > 32) {
+    if (lane == 0) {
+      sh_max[odd][threadIdx.x >> 5] = high;
+      if (kKind == kI8Norm) sh_sum[odd][threadIdx.x >> 5] = ss;
+      if (kKind != kI8Rows && threadIdx.x == 0) sh_most[odd] = 0ull;
+    }
+    __syncthreads();
+    ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(v[e][j]) & 0x7FFFFFFFu);
+    for (int i = 0; i < kT / 32; ++i) {
+      high = max(high, sh_max[odd][i]);
+      if (kKind == kI8Norm) ss += sh_sum[odd][i];
+    }
   }
-  if (kKind == kI8Norm) {
-    ss = warp_sum(ss);
-    if (kT > 32 && (threadIdx.x & 31) == 0) sh_sum[threadIdx.x >> 5] = ss;
-  }
-  const float m = __uint_as_float(RowGroup<kT>::max_u32(top, sh_max));
-  if (kKind == kI8Norm && kT > 32) {
-    ss = sh_sum[0];
-#pragma unroll
-    for (int i = 1; i < kT / 32; ++i) ss += sh_sum[i];
-  }
+  const float m = __uint_as_float(high);
 
   // (false for NaN; zeros of rows as they are need nothing)
-  bool whole = !(m >= 0x1p-60f && m <= 0x1p60f);
+  bool whole = !(m >= (kKind == kI8Silu ? 0x1p-40f : 0x1p-60f) && m <= 0x1p60f);
   if (kKind == kI8Rows && m == 0.f) whole = false;
   if (kKind == kI8Norm) whole = whole || !(ss >= 0x1p-60f && ss <= 0x1p100f);
-  float scale = m / 127.f;
-  if (kKind == kI8Norm) scale = m * (1.f / sqrtf(ss / n + a.eps)) / 127.f;
+  if (whole) {
+    whole_row<kKind, kT>(a, row, t, sh_d);
+    continue;
+  }
   const float inv = m > 0.f ? 127.f / m : 0.f;
-  uint32_t near = 0u;  // elements whose quotient is next to a border
+  float c[kE][4], far = 0.f;  // kMagic + code; the largest distance of a quotient from its code
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
+    float d[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float q = v[e][j] * inv;
-      v[e][j] = q + kMagic;
-      if (fabsf(q - (v[e][j] - kMagic)) > 0.5f - kBand<kKind>) near |= 1u << (e * 4 + j);
+      c[e][j] = fmaf(v[e][j], inv, kMagic);
+      d[j] = fmaf(v[e][j], inv, kMagic - c[e][j]);
     }
+    far = max_abs(max_abs(far, d[0], d[1]), d[2], d[3]);
   }
-  if (RowGroup<kT>::any(near != 0u || whole)) {
-    double most = 0.0, squares = 0.0, h;
-    bool lost = false;
+  // One bit for each element whose quotient is next to a border, and for each that may be the largest (those that
+  // f32 cannot tell from it: silu 7 units each): the codes of the former are taken again below.
+  uint32_t near = 0u, tops = 0u;
+  if (far > 0.5f - kBand<kKind>) {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
+    for (int e = 0; e < kE; ++e)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = (e * kT + t) * 4 + j;
-        if (i < n && (whole || fabsf(v[e][j] - kMagic) > 126.f)) {
-          const double y = exact_element<kKind>(a, row, i, h);
-          lost = lost || !(fabs(y) <= DBL_MAX);
-          most = fmax(most, fabs(y));
-          squares += h * h;
-        }
-      }
-    }
-    most = RowGroup<kT>::all(most, sh_d, [](double p, double q) { return fmax(p, q); });
-    if (whole) {
-      lost = RowGroup<kT>::any(lost);
-      if (kKind == kI8Norm) {
-        squares = RowGroup<kT>::all(squares, sh_d, [](double p, double q) { return p + q; });
-        const double at = squares / n + a.eps;
-        scale = at > 0.0 ? static_cast<float>(most / sqrt(at) / 127.0) : 0.f;
-        if (at > 0.0 && !isfinite(static_cast<float>(most / sqrt(at)))) lost = true;
-      } else {
-        scale = static_cast<float>(most / 127.0);
-        if (!isfinite(static_cast<float>(most))) lost = true;
-      }
-      if (lost) scale = __uint_as_float(0x7FC00000u);
-    }
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = (e * kT + t) * 4 + j;
-        if (i < n && (whole || ((near >> (e * 4 + j)) & 1u))) {
-          double c = 0.0;
-          if (!lost && most > 0.0) c = rint(127.0 * exact_element<kKind>(a, row, i, h) / most);
-          v[e][j] = static_cast<float>(c) + kMagic;
-        }
-      }
-    }
+      for (int j = 0; j < 4; ++j)
+        if (fabsf(fmaf(v[e][j], inv, kMagic - c[e][j])) > 0.5f - kBand<kKind>) near |= 1u << (e * 4 + j);
   }
+  if (kKind != kI8Rows && __float_as_uint(top) >= high - (kKind == kI8Silu ? 32u : 0u)) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (fabsf(c[e][j] - kMagic) > 126.f) tops |= 1u << (e * 4 + j);
+  }
+  float scale = m / 127.f;
+  if (kKind == kI8Norm) scale = m * (1.f / sqrtf(ss / n + a.eps)) / 127.f;
   int8_t* q = a.q + row * a.q_stride;
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
     const int i = (e * kT + t) * 4;
-    if (i >= n) break;
+    if (i >= n) continue;
     uint32_t b[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(v[e][j]);
+    for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(c[e][j]);
     if (kVec) {
       *reinterpret_cast<uint32_t*>(q + i) = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     } else {
@@ -232,14 +365,22 @@ __global__ void __launch_bounds__(kT < 128 ? 128 : kT) k_rows_i8(const I8RowsArg
     }
   }
   if (t == 0) a.scale[row] = scale;
+  if (kKind == kI8Rows ? near != 0u : RowGroup<kT>::any(near != 0u))
+    codes_again<kKind, kT>(a, row, t, near, tops, m, &sh_most[odd]);
+  }
 }
 
 template <int kKind, int kT, int kE>
 cudaError_t launch_rows(const I8RowsArgs& a, bool vec, cudaStream_t st) {
-  const unsigned per = kT < 128 ? 128 / kT : 1, grid = static_cast<unsigned>((a.rows + per - 1) / per);
-  const unsigned block = kT < 128 ? 128 : kT;
-  if (vec) k_rows_i8<kKind, kT, kE, true><<<grid, block, 0, st>>>(a);
-  else k_rows_i8<kKind, kT, kE, false><<<grid, block, 0, st>>>(a);
+  using Cfg = RowsCfg<kKind, kT, kE>;
+  const auto kernel = vec ? k_rows_i8<kKind, kT, kE, true> : k_rows_i8<kKind, kT, kE, false>;
+  if (Cfg::smem > 48 * 1024) {
+    static unsigned long long done[2] = {0, 0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Cfg::smem, &done[vec]);
+    if (e != cudaSuccess) return e;
+  }
+  const int per = Cfg::block / kT, blocks = (a.rows + per - 1) / per, most = kSms * Cfg::ctas;
+  kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), Cfg::block, Cfg::smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -251,11 +392,13 @@ cudaError_t launch_kind(const I8RowsArgs& a, cudaStream_t st) {
   const bool vec = a.n % 4 == 0 && on16(a.x, a.x_stride) && on16(a.other, a.other_stride) && on16(a.g, 0) &&
                    on16(a.sum, a.sum_stride) && reinterpret_cast<uintptr_t>(a.q) % 4 == 0 &&
                    (a.rows == 1 || a.q_stride % 4 == 0);
-  if (a.n <= 1024 && a.rows > 1024) return launch_rows<kKind, 32, 8>(a, vec, st);
+  if (a.n <= 128) return launch_rows<kKind, 32, 1>(a, vec, st);
+  if (a.n <= 512) return launch_rows<kKind, 32, 4>(a, vec, st);
+  if (a.n <= 1024) return launch_rows<kKind, 128, 2>(a, vec, st);
   if (a.n <= 2048) return launch_rows<kKind, 256, 2>(a, vec, st);
   if (a.n <= 4096) return launch_rows<kKind, 256, 4>(a, vec, st);
-  if (a.n <= 8192) return launch_rows<kKind, 256, 8>(a, vec, st);
-  return launch_rows<kKind, 512, 8>(a, vec, st);
+  if (a.n <= 8192) return launch_rows<kKind, 512, 4>(a, vec, st);
+  return launch_rows<kKind, 1024, 4>(a, vec, st);
 }
 
 // The values that rows of codes stand for: four a thread and step.
