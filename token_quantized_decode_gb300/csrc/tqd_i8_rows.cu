@@ -31,30 +31,32 @@ constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it leaves the neares
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
-// silu(g) u in f64 to 2^-40, for gates whose e^-g is within f32: of a row whose largest |y| is at least 2^-40
+// silu(g) u to 2^-38, for gates whose e^-g is within f32: of a row whose largest |y| is at least 2^-40
 // and whose |u| are at most 2^40, elements of at least a 2^8th of the largest have g > -62.  The f64 pipe does a
 // warp's instruction in 15 clocks, so this takes the reduction to |r| <= ln 2 / 2 with ln 2 in two parts (Cody and
-// Waite), ten terms of the Taylor series, and one step of Newton's iteration from the f32 reciprocal in place of
-// exp and a division.
+// Waite), the Taylor series with the terms from r^6 on in f32 (less than 2^-18 of the whole), and one step of
+// Newton's iteration from the f32 reciprocal in place of exp and a division.
 constexpr double kLn2High = 0.6931471804855391, kLn2Low = 7.440617110012397e-11;  // 33 bits after the point, and the rest
-__device__ __noinline__ double near_silu(float g, float u) {
-  const double x = fmax(-static_cast<double>(g), -64.0);  // (e^-64 is nothing beside 1)
-  const double k = rint(x * 1.4426950408889634);
-  const double r = fma(k, -kLn2Low, fma(k, -kLn2High, x));
-  double e = 1.0 / 3628800;
-  e = fma(e, r, 1.0 / 362880);
-  e = fma(e, r, 1.0 / 40320);
-  e = fma(e, r, 1.0 / 5040);
-  e = fma(e, r, 1.0 / 720);
+__device__ __forceinline__ double near_silu(float g, float u) {
+  const float xf = fmaxf(-g, -64.f);  // (e^-64 is nothing beside 1)
+  const float kf = rintf(xf * 1.44269504f);
+  const double k = kf, r = fma(k, -kLn2Low, fma(k, -kLn2High, static_cast<double>(xf)));
+  const float rf = static_cast<float>(r);
+  float h = 1.f / 3628800;
+  h = fmaf(h, rf, 1.f / 362880);
+  h = fmaf(h, rf, 1.f / 40320);
+  h = fmaf(h, rf, 1.f / 5040);
+  h = fmaf(h, rf, 1.f / 720);
+  double e = h;
   e = fma(e, r, 1.0 / 120);
   e = fma(e, r, 1.0 / 24);
   e = fma(e, r, 1.0 / 6);
   e = fma(e, r, 0.5);
   e = fma(e, r, 1.0);
   e = fma(e, r, 1.0);
-  const double d = 1.0 + e * __hiloint2double((1023 + static_cast<int>(k)) << 20, 0);
+  const double d = fma(e, __hiloint2double((1023 + static_cast<int>(kf)) << 20, 0), 1.0);
   const double q = 1.f / static_cast<float>(d);
-  return fma(fma(-d, q, 1.0), q, q) * g * u;
+  return fma(fma(-d, q, 1.0), q, q) * (static_cast<double>(g) * u);
 }
 
 // Element i of a row in f64, from memory again (the norm: without 1 / rms; h is its sum in f32).
@@ -145,7 +147,8 @@ __device__ __noinline__ void codes_again(const I8RowsArgs& a, int64_t row, int t
     if (kKind == kI8Silu) return near_silu(a.x[row * a.x_stride + i], a.other[row * a.other_stride + i]);
     return exact_element<kKind>(a, row, i, h);
   };
-  double most = m;
+  double most = m, y = 0.0;
+  if (near) y = element(place(near));
   if (kKind != kI8Rows) {
     most = 0.0;
     for (; tops; tops &= tops - 1) most = fmax(most, fabs(element(place(tops))));
@@ -158,9 +161,15 @@ __device__ __noinline__ void codes_again(const I8RowsArgs& a, int64_t row, int t
     }
   }
   int8_t* q = a.q + row * a.q_stride;
-  for (; near; near &= near - 1) {
+  while (near) {
+    // the border, and the side of it that 127 y / most lies on (on it: the even code)
     const int i = place(near);
-    q[i] = static_cast<int8_t>(exact_code(element(i), most));
+    const float low = floorf(static_cast<float>(y) * (127.f / m));
+    const double side = fma(127.0, y, -(low + 0.5) * most);
+    const int c = static_cast<int>(low);
+    q[i] = static_cast<int8_t>(side > 0.0 || (side == 0.0 && (c & 1)) ? c + 1 : c);
+    near &= near - 1;
+    if (near) y = element(place(near));
   }
 }
 
@@ -199,8 +208,7 @@ struct RowsCfg {
   static constexpr int smem = block * kE * 16 * inputs * ahead;
   static constexpr int ctas = kT >= 1024 ? 1 : kT == 512 ? 2 : kT == 256 ? (kE == 4 ? 3 : kKind == kI8Rows ? 5 : 4)
                               : kE == 4 ? 5 : kKind == kI8Rows ? 8 : 7;
-  static constexpr bool keep_gains = kE <= 2;  // in registers, from row to row
-};
+  };
 
 // kT threads a row, kE groups of four elements a thread.  kVec: every row of every tensor
 // begins on a 16-byte boundary (codes: 4) and is whole groups of four.  CTAs go from row to
@@ -234,11 +242,6 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
   };
 #pragma unroll
   for (int i = 0; i < Cfg::ahead; ++i) fetch(i, row + i * step);
-  float gains[Cfg::keep_gains && kKind == kI8Norm ? kE : 1][4];
-  if (Cfg::keep_gains && kKind == kI8Norm) {
-#pragma unroll
-    for (int e = 0; e < kE; ++e) load4<kVec>(a.g, (e * kT + t) * 4, n, gains[e]);
-  }
 #pragma unroll 1
   for (int turn = 0; row < a.rows; row += step, ++turn) {
   const int odd = turn & 1;
@@ -282,11 +285,11 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
         }
       }
       float g[4];
-      if (!Cfg::keep_gains) load4<kVec>(a.g, i, n, g);
+      load4<kVec>(a.g, i, n, g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         ss = fmaf(w[e][j], w[e][j], ss);
-        v[e][j] = w[e][j] * (Cfg::keep_gains ? gains[Cfg::keep_gains ? e : 0][j] : g[j]);
+        v[e][j] = w[e][j] * g[j];
       }
     }
     top = max_abs(max_abs(top, v[e][0], v[e][1]), v[e][2], v[e][3]);
