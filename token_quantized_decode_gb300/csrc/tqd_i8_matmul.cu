@@ -8,6 +8,8 @@
 // they are split, changes nothing.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <stdio.h>
+#include <stdlib.h>
 
 #include "tqd_device.cuh"
 #include "tqd_i8.cuh"
@@ -16,185 +18,212 @@
 namespace tqd {
 namespace {
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+constexpr int kSms = 152;
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at `p`'s place in CTA `rank` of the cluster.
+__device__ __forceinline__ int ld_rank(const int* p, int rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
 }
 
-// ---------------------------------------------------------------- few tokens
+// -------------------------------------------------------------- up to 8 tokens
 //
-// The weights pass once through registers: a warp takes 16 rows, lane (g, c) = (lane / 4,
-// lane % 4) sixteen bytes of rows g and g + 8, which are its share of four 16 x 16
-// operands (the columns' order within a unit of 64 does not matter, as long as both operands have
-// the same).  The tokens' codes stand in shared memory as f16 operands, per unit and eight
-// tokens 1 KB.  kw warps share 16 rows, each with every kw-th pair of units.
+// A warp takes 16 rows; lane (g, c) = (lane / 4, lane % 4) holds sixteen bytes of rows g and g + 8 and of
+// token g, which are its share of two 16 x 8 x 32 int8 instructions (the columns' order within 64 does
+// not matter, as long as both operands have the same).  Eight columns of the instruction are all that is
+// needed here, and its rate, 32 bytes of weights a clock and SM, is above what memory brings (24): nothing is
+// converted.  Each lane copies its own bytes into a ring of its own, so that no barrier
+// stands between a copy and its use.  A step is 128 columns.  kw warps of a CTA and cs CTAs of a
+// cluster share 16 rows: piece p of the kw cs has the steps p, p + kw cs, ...
+constexpr int kFewMost = 8;
 constexpr int kFewWarps = 8;
-constexpr int kFewCtas = 304;         // two an SM
-constexpr int kFewStage = 64 * 1024;  // bytes of operands in shared memory
+constexpr int kFewCtas = 2 * kSms;
+constexpr int kFewDepth = 4;                     // steps of the ring
+constexpr int kFewSlot = kFewWarps * 32 * 6;     // 16-byte words of one: [half][row g, row g + 8, token][thread]
 
-template <int kNT>
-__global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs a, int kw, int groups) {
-  extern __shared__ uint4 xs[];                 // [unit][tile of 8][2][lane]
-  __shared__ int sums[kFewWarps][kNT * 4][32];  // of the warps that share rows
-  constexpr int kUnits = kFewStage / (kNT * 1024);
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},{%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs a, int kw, int cs, int groups) {
+  extern __shared__ uint4 few_smem[];
+  __shared__ int sums[kFewWarps][4][32];  // of the warps that share rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int units = (a.cols + 63) / 64, share = kFewWarps / kw, part = warp % kw;
-  const int j0 = blockIdx.y * (kNT * 8);
+  const int share = kFewWarps / kw, part = warp % kw, rank = blockIdx.x % cs, pieces = kw * cs, piece = rank * kw + part;
+  const int steps = ((a.cols + 127) / 128 + pieces - 1) / pieces;
+  const int first = blockIdx.x / cs, stride = gridDim.x / cs;
+  uint4* ring = few_smem + threadIdx.x;
+  const int8_t* x = a.x + min(g, a.n - 1) * a.x_stride;
 
-  for (int group = blockIdx.x; group < groups; group += gridDim.x) {
-    const int r0 = (group * share + warp / kw) * 16 + g;
-    const int8_t* w0 = a.w + static_cast<int64_t>(min(r0, a.rows - 1)) * a.cols + c * 16;
-    const int8_t* w1 = a.w + static_cast<int64_t>(min(r0 + 8, a.rows - 1)) * a.cols + c * 16;
-    int total[kNT][4];
-    float acc[kNT][4];
-#pragma unroll
-    for (int t = 0; t < kNT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) total[t][i] = 0, acc[t][i] = 0.f;
-    int run = 0;  // units in acc
-
-    uint4 now[2][2], next[2][2];  // [unit][row]
-    auto load = [&](uint4(&v)[2][2], int u) {
+  // the next step to copy: of this CTA's row groups in turn
+  int f_group = first, f_step = 0, f_slot = 0;
+  auto fetch = [&]() {
+    if (f_group < groups) {
+      const int r = (f_group * share + warp / kw) * 16 + g, col = (f_step * pieces + piece) * 128 + c * 16;
+      const int8_t* w0 = a.w + static_cast<int64_t>(min(r, a.rows - 1)) * a.cols;
+      const int8_t* w1 = a.w + static_cast<int64_t>(min(r + 8, a.rows - 1)) * a.cols;
+      uint4* to = ring + f_slot * kFewSlot;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const bool in = (u + k) * 64 + c * 16 < a.cols;
-        v[k][0] = in ? ld_weights16(w0 + (u + k) * 64) : make_uint4(0u, 0u, 0u, 0u);
-        v[k][1] = in ? ld_weights16(w1 + (u + k) * 64) : make_uint4(0u, 0u, 0u, 0u);
+        const int at = col + k * 64;
+        const uint32_t size = at < a.cols ? 16 : 0, dst = smem_addr(to + k * (3 * 32 * kFewWarps));
+        constexpr uint32_t next = 32 * kFewWarps * 16;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(w0 + (size ? at : 0)), "r"(size) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + next), "l"(w1 + (size ? at : 0)), "r"(size) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 2 * next), "l"(x + (size ? at : 0)),
+                     "r"(g < a.n ? size : 0)
+                     : "memory");
       }
-    };
-    load(now, 2 * part);
-    for (int u0 = 0; u0 < units; u0 += kUnits) {
-      const int here = min(kUnits, units - u0);
-      if (units > kUnits || group == static_cast<int>(blockIdx.x)) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < here * kNT * 32; i += 32 * kFewWarps) {
-          const int l = i & 31, t = (i >> 5) % kNT, u = (i >> 5) / kNT;
-          const int j = j0 + t * 8 + (l >> 2), col = (u0 + u) * 64 + (l & 3) * 16;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (j < a.n && col < a.cols) v = *reinterpret_cast<const uint4*>(a.x + j * a.x_stride + col);
-          uint4 p, q;
-          i8x4_to_f16(v.x, p.x, p.y);
-          i8x4_to_f16(v.y, p.z, p.w);
-          i8x4_to_f16(v.z, q.x, q.y);
-          i8x4_to_f16(v.w, q.z, q.w);
-          xs[(u * kNT + t) * 64 + l] = p;
-          xs[(u * kNT + t) * 64 + 32 + l] = q;
-        }
-        __syncthreads();
+      if (++f_step == steps) f_step = 0, f_group += stride;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++f_slot == kFewDepth) f_slot = 0;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kFewDepth; ++i) fetch();
+  float sx[2];  // scales of this lane's tokens, and (below) of its rows
+#pragma unroll
+  for (int i = 0; i < 2; ++i) sx[i] = __ldg(a.x_scale + min(2 * c + i, a.n - 1));
+  int slot = 0;
+  for (int group = first; group < groups; group += stride) {
+    const int r0 = (group * share + warp / kw) * 16 + g;
+    const float sw[2] = {__ldg(a.w_scale + min(r0, a.rows - 1)), __ldg(a.w_scale + min(r0 + 8, a.rows - 1))};
+    int total[4] = {0, 0, 0, 0}, other[4] = {0, 0, 0, 0};
+    for (int s = 0; s < steps; ++s) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kFewDepth - 1) : "memory");
+      uint4 v[2][3];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[k][i] = ring[slot * kFewSlot + (k * 3 + i) * 32 * kFewWarps];
+      if (++slot == kFewDepth) slot = 0;
+      fetch();  // into the place just read
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        mma_s8(total, v[k][0].x, v[k][1].x, v[k][0].y, v[k][1].y, v[k][2].x, v[k][2].y);
+        mma_s8(other, v[k][0].z, v[k][1].z, v[k][0].w, v[k][1].w, v[k][2].z, v[k][2].w);
       }
-      for (int u = 2 * part; u < here; u += 2 * kw) {
-        // the next pair of units, which may be of the next stage
-        load(next, u + 2 * kw < kUnits ? u0 + u + 2 * kw : u0 + kUnits + 2 * part);
+    }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (u + k < here) {
-            const uint32_t r0w[4] = {now[k][0].x, now[k][0].y, now[k][0].z, now[k][0].w};
-            const uint32_t r1w[4] = {now[k][1].x, now[k][1].y, now[k][1].z, now[k][1].w};
-            uint32_t op[4][4];
+    for (int e = 0; e < 4; ++e) total[e] += other[e];
+    if (pieces > 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              i8x4_to_f16(r0w[i], op[i][0], op[i][2]);
-              i8x4_to_f16(r1w[i], op[i][1], op[i][3]);
-            }
+      for (int e = 0; e < 4; ++e) sums[warp][e][lane] = total[e];
+      __syncthreads();
+      if (cs > 1) {  // the CTA's sums in the place of its first warp's, then the cluster's
 #pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-              const uint4 p = xs[((u + k) * kNT + t) * 64 + lane], q = xs[((u + k) * kNT + t) * 64 + 32 + lane];
-              mma16816(acc[t], op[0], p.x, p.y);
-              mma16816(acc[t], op[1], p.z, p.w);
-              mma16816(acc[t], op[2], q.x, q.y);
-              mma16816(acc[t], op[3], q.z, q.w);
-            }
+        for (int e = 0; e < 4; ++e) {
+          if (kw > 1 && e % kw == part) {
+            int s = 0;
+            for (int w = warp - part; w < warp - part + kw; ++w) s += sums[w][e][lane];
+            sums[warp - part][e][lane] = s;
           }
         }
-        run += 2;
-        if (run == 16) {
-          run = 0;
-#pragma unroll
-          for (int t = 0; t < kNT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) total[t][i] += __float2int_rn(acc[t][i]), acc[t][i] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) now[k][0] = next[k][0], now[k][1] = next[k][1];
+        cluster_barrier();
       }
     }
+    // of the sums of 16 rows, piece p writes every (kw cs)-th
 #pragma unroll
-    for (int t = 0; t < kNT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) total[t][i] += __float2int_rn(acc[t][i]);
-    if (kw > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < kNT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums[warp][t * 4 + i][lane] = total[t][i];
-      __syncthreads();
-    }
-    // warp `part` of those that share rows writes every kw-th of their sums
-#pragma unroll
-    for (int t = 0; t < kNT; ++t) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (kw > 1 && (t * 4 + i) % kw != part) continue;
-        int s = total[t][i];
-        if (kw > 1) {
-          s = 0;
-          for (int w = warp - part; w < warp - part + kw; ++w) s += sums[w][t * 4 + i][lane];
-        }
-        const int r = r0 + (i >> 1) * 8, j = j0 + t * 8 + 2 * c + (i & 1);
-        if (r < a.rows && j < a.n)
-          a.y[j * a.y_stride + r] = static_cast<float>(s) * a.x_scale[j] * a.w_scale[r];
+    for (int e = 0; e < 4; ++e) {
+      if (pieces > 1 && e % pieces != piece) continue;
+      int s = total[e];
+      if (cs > 1) {
+        s = 0;
+        for (int q = 0; q < cs; ++q) s += ld_rank(&sums[warp - part][e][lane], q);
+      } else if (kw > 1) {
+        s = 0;
+        for (int w = warp - part; w < warp - part + kw; ++w) s += sums[w][e][lane];
       }
+      const int r = r0 + (e >> 1) * 8, j = 2 * c + (e & 1);
+      if (r < a.rows && j < a.n) a.y[j * a.y_stride + r] = static_cast<float>(s) * sx[e & 1] * sw[e >> 1];
     }
+    // (no sum is overwritten, nor a CTA's memory gone, while another reads it)
+    if (cs > 1) cluster_barrier();
+    else if (kw > 1) __syncthreads();
   }
 }
 
-template <int kNT>
+cudaError_t launch_clusters(const void* kernel, int cs, unsigned grid, unsigned block, size_t smem, cudaStream_t st, void** args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
 cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
+  constexpr int kMost = kFewDepth * kFewSlot * 16;
   static unsigned long long done = 0;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_few<kNT>), kFewStage, &done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_few), kMost, &done);
   if (e != cudaSuccess) return e;
-  // how many warps share 16 rows: what makes the busiest CTA's share least
-  const int tiles = (a.rows + 15) / 16, pairs = (a.cols + 127) / 128, blocks = (a.n + kNT * 8 - 1) / (kNT * 8);
-  int kw = 1, groups = 0;
-  int64_t best = -1;
-  for (int k = 1; k <= kFewWarps; k *= 2) {
-    const int gr = (tiles + kFewWarps / k - 1) / (kFewWarps / k);
-    const int64_t waves = (static_cast<int64_t>(gr) * blocks + kFewCtas - 1) / kFewCtas;
-    const int64_t cost = waves * ((pairs + k - 1) / k + 1);
-    if (best < 0 || cost < best) best = cost, kw = k, groups = gr;
+  // How many warps and CTAs share 16 rows: what makes the busiest CTA's share least.
+  const int tiles = (a.rows + 15) / 16, pairs = (a.cols + 127) / 128;
+  int kw = 1, cs = 1, groups = 0;
+  float best = 0.f;
+  for (int c = 1; c <= 8; c *= 2) {
+    for (int k = 1; k <= kFewWarps; k *= 2) {
+      const int gr = (tiles + kFewWarps / k - 1) / (kFewWarps / k);
+      const int64_t ctas = static_cast<int64_t>(gr) * c;
+      const int64_t waves = (ctas + kFewCtas / c * c - 1) / (kFewCtas / c * c);
+      const int steps = (pairs + k * c - 1) / (k * c);
+      const float cost = waves * (steps * (ctas > kFewCtas / 2 ? 1.f : 0.6f) + 1.f) + (c > 1 ? 2.f : 0.f);
+      if (groups == 0 || cost < best) best = cost, kw = k, cs = c, groups = gr;
+    }
   }
-  const int units = (a.cols + 63) / 64;
-  const size_t smem = units * kNT * 1024 < kFewStage ? units * kNT * 1024 : kFewStage;
-  const dim3 grid(static_cast<unsigned>(groups < kFewCtas ? groups : kFewCtas), static_cast<unsigned>(blocks));
-  k_i8_few<kNT><<<grid, 32 * kFewWarps, smem, st>>>(a, kw, groups);
-  return cudaGetLastError();
+  if (const char* f = getenv("FEW")) sscanf(f, "%d,%d", &kw, &cs), groups = (tiles + kFewWarps / kw - 1) / (kFewWarps / kw);
+  const int most = kFewCtas / cs, clusters = groups < most ? groups : most;
+  const int steps = (pairs + kw * cs - 1) / (kw * cs) * ((groups + clusters - 1) / clusters);
+  I8MatmulArgs args = a;
+  void* p[] = {&args, &kw, &cs, &groups};
+  return launch_clusters(reinterpret_cast<const void*>(k_i8_few), cs, static_cast<unsigned>(clusters * cs), 32 * kFewWarps,
+                         (steps < kFewDepth ? steps : kFewDepth) * kFewSlot * 16, st, p);
 }
 
-// --------------------------------------------------------------- many tokens
+// ------------------------------------------------------------ 9 tokens and more
 //
-// A CTA per SM goes over tiles of 128 rows of w by kTN tokens on the fifth-generation
-// tensor cores.  In a step of 64 columns the rows' codes come by a tensor copy as they are,
-// four warps make them f16 and put them into tensor memory as operand A (a lane is a
-// row), and the tokens' come as f16 from an image in the scratch, laid out by k_i8_image in the
-// order of shared memory, so that one bulk copy brings them.  Sixteen warps take the sums out
-// of tensor memory after every 16 steps (1024 columns), add them up as whole numbers, and
-// write the tile's results while the next one's sums are made.
-constexpr int kBigThreads = 24 * 32;  // copies, MMAs, two idle; four that convert; sixteen that read sums
+// A CTA per SM makes tiles of 128 rows of w by kTN tokens on the fifth-generation tensor
+// cores.  In a step of 64 columns the rows' codes come by a tensor copy as they are, and
+// groups of four warps, a step each in turn, make them f16 and put them into tensor memory as
+// operand A (a lane is a row).  The tokens, operand B, are f16 in shared memory: up to 64 are
+// made so by the same warps, more come by a bulk copy from an image that k_i8_image laid out in the
+// scratch in the order of shared memory.  Other warps take the sums out of tensor memory
+// after every 16 steps (1024 columns) and add them up as whole numbers; they write a tile's results
+// while the next one's sums are made.  Where there are few tiles a cluster of cs CTAs shares a
+// tile's steps, and each adds up and writes a part of its tokens.
 constexpr int kBigM = 128, kBigK = 64, kBigRun = 16;
-constexpr int kBigCtas = 152;
-constexpr uint32_t kBigRaw = kBigM * kBigK;  // bytes of codes in a stage
+constexpr uint32_t kBigRaw = kBigM * kBigK;  // bytes of the rows' codes in a stage
 
 template <int kTN>
 struct BigCfg {
-  static constexpr uint32_t image = kTN * kBigK * 2;  // bytes of f16 tokens in a stage
-  static constexpr int stages = kTN == 256 ? 5 : kTN == 128 ? 8 : 12;
-  static constexpr int sums = kTN == 256 ? 1 : 2;  // accumulators in turn
-  static constexpr uint32_t a_col = sums * kTN;    // operand A's columns: 32 a stage
-  static constexpr size_t smem = stages * (kBigRaw + image) + 1024;
-  static_assert(a_col + stages * 32 <= 512, "tensor memory");
+  static constexpr bool raw_tokens = kTN <= 64;
+  static constexpr int converters = kTN <= 128 ? 2 : 1;              // groups of four warps
+  static constexpr int readers = kTN <= 32 ? 4 : kTN <= 128 ? 8 : 16;  // warps that read sums (TN 192: 48 columns each)
+  static constexpr int threads = 32 * (4 + 4 * converters + readers);  // copies, MMAs, two idle; then these
+  static constexpr uint32_t image = kTN * kBigK * 2;                 // bytes of f16 tokens in a stage
+  static constexpr uint32_t raw = raw_tokens ? kTN * kBigK : 0;      // bytes of their codes
+  static constexpr uint32_t stage = kBigRaw + image + raw;
+  static constexpr int stages = kTN == 192 ? 6 : kTN == 128 ? 8 : kTN == 64 ? 10 : 12;
+  static constexpr int a_stages = kTN == 192 ? 4 : stages;  // of operand A, 32 columns each
+  static constexpr uint32_t a_col = 2 * kTN;                // behind two accumulators, in turn
+  static constexpr size_t smem = stages * stage + 1024;
+  static_assert(a_col + a_stages * 32 <= 512, "tensor memory");
+  static_assert(static_cast<size_t>(kTN) * kBigM * 4 <= stages * stage, "a cluster's sums take the stages' place");
 };
 
 __device__ __forceinline__ uint64_t image_desc(const void* p) {
@@ -242,22 +271,31 @@ __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int 
       "l"(map), "r"(col), "r"(row), "r"(smem_addr(bar))
       : "memory");
 }
+// True in one lane of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Wait for a phase; false once any wait of the CTA ran out of time (which *dead says).
+// Wait for a phase; false once any wait of the CTA ran out of time (which *dead says).  The
+// timer takes longer to read than most waits last: it is read after 64 tries, and then every 64.
 __device__ __forceinline__ bool big_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (i % 64) continue;
     if (*dead) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
+    const uint64_t now = global_timer_ns();
+    if (!t0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
       *dead = 1;
       return false;
     }
   }
-  return true;
 }
 
 struct BigArgs {
@@ -265,11 +303,12 @@ struct BigArgs {
   const float *x_scale, *w_scale;
   float* y;
   int64_t y_stride;
-  int rows, n, n16, steps, row_tiles, token_tiles;
+  int rows, n, n16, steps, row_tiles, token_tiles, cs;
 };
 
 template <int kTN>
-__global__ void __launch_bounds__(kBigThreads, 1) k_i8_big(const __grid_constant__ CUtensorMap map, const BigArgs a) {
+__global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
+    k_i8_big(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map, const BigArgs a) {
   using Cfg = BigCfg<kTN>;
   extern __shared__ uint8_t big_smem[];
   __shared__ uint64_t full[Cfg::stages], ready[Cfg::stages], empty[Cfg::stages], sums_full[2], sums_empty[2], done;
@@ -277,8 +316,9 @@ __global__ void __launch_bounds__(kBigThreads, 1) k_i8_big(const __grid_constant
   __shared__ int dead_word;
   volatile int* dead = &dead_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* raw = big_smem + (1024u - (smem_addr(big_smem) & 1023u)) % 1024u;
-  uint8_t* tokens = raw + Cfg::stages * kBigRaw;
+  uint8_t* raw = big_smem + (1024u - (smem_addr(big_smem) & 1023u)) % 1024u;  // [stage] codes of the rows,
+  uint8_t* tokens = raw + Cfg::stages * kBigRaw;                             // f16 of the tokens,
+  uint8_t* raw_x = tokens + Cfg::stages * Cfg::image;                        // codes of the tokens
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::stages; ++s) {
@@ -288,7 +328,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) k_i8_big(const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sums_full[i], 1);
-      mbar_init(&sums_empty[i], 16);
+      mbar_init(&sums_empty[i], Cfg::readers);
     }
     mbar_init(&done, 1);
     dead_word = 0;
@@ -302,91 +342,134 @@ __global__ void __launch_bounds__(kBigThreads, 1) k_i8_big(const __grid_constant
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_at;
-  const int tiles = a.row_tiles * a.token_tiles;
+  // this CTA's tiles, and its steps of each
+  const int tiles = a.row_tiles * a.token_tiles, rank = blockIdx.x % a.cs, first = blockIdx.x / a.cs, stride = gridDim.x / a.cs;
+  const int from = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.cs);
+  const int steps = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / a.cs) - from;
 
+  // The copying and the multiplying warp go through their loops whole, so that what they compute stays uniform; one
+  // elected lane issues.
   if (warp == 0) {
-    if (lane == 0) {
-      int g = 0;  // steps issued
-      bool image_there = false, ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        const int row0 = tile / a.token_tiles * kBigM, j0 = tile % a.token_tiles * kTN;
-        const uint32_t bytes = min(kTN, a.n16 - j0) * kBigK * 2;
-        for (int k = 0; k < a.steps; ++k, ++g) {
-          const int s = g % Cfg::stages;
-          if (g >= Cfg::stages) ok = big_wait(&empty[s], (g / Cfg::stages - 1) & 1, dead);
-          if (!ok) break;
+    int s = 0, issued = 0;
+    uint32_t phase = 0;
+    bool image_there = Cfg::raw_tokens, ok = true;
+    for (int tile = first; ok && tile < tiles; tile += stride) {
+      const int row0 = tile / a.token_tiles * kBigM, j0 = tile % a.token_tiles * kTN;
+      const uint32_t bytes = Cfg::raw_tokens ? Cfg::raw : min(kTN, a.n16 - j0) * kBigK * 2;
+      for (int k = from; k < from + steps; ++k) {
+        if (issued >= Cfg::stages) ok = __all_sync(0xFFFFFFFFu, big_wait(&empty[s], phase ^ 1, dead));
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&full[s], kBigRaw + bytes);
-          copy_box(raw + s * kBigRaw, &map, k * kBigK, row0, &full[s]);
-          if (!image_there) pdl_wait();  // the kernel before this one writes the image
-          image_there = true;
-          bulk_g2s(tokens + s * Cfg::image, a.image + (static_cast<int64_t>(k) * a.n16 + j0) * (kBigK * 2), bytes, &full[s]);
+          copy_box(raw + s * kBigRaw, &w_map, k * kBigK, row0, &full[s]);
+          if (Cfg::raw_tokens) {
+            copy_box(raw_x + s * Cfg::raw, &x_map, k * kBigK, j0, &full[s]);
+          } else {
+            if (!image_there) pdl_wait();  // the kernel before this one writes the image
+            bulk_g2s(tokens + s * Cfg::image, a.image + (static_cast<int64_t>(k) * a.n16 + j0) * (kBigK * 2), bytes, &full[s]);
+          }
         }
+        image_there = true;
+        if (issued < Cfg::stages) ++issued;
+        if (++s == Cfg::stages) s = 0, phase ^= 1;
       }
-      // whatever the others do, what is still under way lands before the CTA ends
-      for (int i = max(0, g - Cfg::stages); i < g; ++i)
-        mbar_wait_bounded(&full[i % Cfg::stages], (i / Cfg::stages) & 1, nullptr, kWaitLimitNs / 4);
+    }
+    // whatever the others do, what is still under way lands before the CTA ends
+    for (int i = 0; i < issued; ++i) {
+      if (--s < 0) s = Cfg::stages - 1, phase ^= 1;
+      mbar_wait_warp(&full[s], phase, kWaitLimitNs / 4);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int g = 0, run = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        const int width = min(kTN, a.n16 - tile % a.token_tiles * kTN);
-        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kBigM >> 4) << 24);
-        for (int k0 = 0; ok && k0 < a.steps; k0 += kBigRun, ++run) {
-          const int b = run % Cfg::sums;
-          if (run >= Cfg::sums) ok = big_wait(&sums_empty[b], (run / Cfg::sums - 1) & 1, dead);
-          const int end = min(a.steps, k0 + kBigRun);
-          for (int k = k0; ok && k < end; ++k, ++g) {
-            const int s = g % Cfg::stages;
-            const uint32_t phase = (g / Cfg::stages) & 1;
-            ok = big_wait(&full[s], phase, dead) && big_wait(&ready[s], phase, dead);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    int s = 0, at = 0, run = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = first; ok && tile < tiles; tile += stride) {
+      const int width = min(kTN, a.n16 - tile % a.token_tiles * kTN);
+      const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kBigM >> 4) << 24);
+      for (int k0 = 0; ok && k0 < steps; k0 += kBigRun, ++run) {
+        const int b = run & 1;
+        if (run >= 2) ok = __all_sync(0xFFFFFFFFu, big_wait(&sums_empty[b], (run / 2 - 1) & 1, dead));
+        const int end = min(steps, k0 + kBigRun);
+        for (int k = k0; ok && k < end; ++k) {
+          // (ready follows full, but this warp has to see the image's bytes itself)
+          ok = __all_sync(0xFFFFFFFFu, big_wait(&ready[s], phase, dead) && big_wait(&full[s], phase, dead));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (elect_one()) {
             const uint64_t bd = image_desc(tokens + s * Cfg::image);
 #pragma unroll
             for (int i = 0; i < kBigK / 16; ++i)
-              mma_ts(tmem + b * kTN, tmem + Cfg::a_col + s * 32 + i * 8, bd + i * 16, idesc, k > k0 || i > 0);
+              mma_ts(tmem + b * kTN, tmem + Cfg::a_col + at * 32 + i * 8, bd + i * 16, idesc, k > k0 || i > 0);
             mma_commit(&empty[s]);
+            if (k + 1 == end) mma_commit(&sums_full[b]);
           }
-          if (ok) mma_commit(&sums_full[b]);
+          if (++s == Cfg::stages) s = 0, phase ^= 1;
+          if (++at == Cfg::a_stages) at = 0;
         }
       }
-      mma_commit(&done);  // tensor memory is given back once every MMA is over
-      mbar_wait_bounded(&done, 0, nullptr, kWaitLimitNs / 4);
     }
-  } else if (warp >= 4 && warp < 8) {
-    const int row = (warp - 4) * 32 + lane;
+    if (elect_one()) mma_commit(&done);  // tensor memory is given back once every MMA is over
+    mbar_wait_warp(&done, 0, kWaitLimitNs / 4);
+  } else if (warp >= 4 && warp < 4 + 4 * Cfg::converters) {
+    const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t turn = ((row >> 1) & 3) * 16;
-    int g = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-      for (int k = 0; k < a.steps; ++k, ++g) {
-        const int s = g % Cfg::stages;
-        ok = __all_sync(0xFFFFFFFFu, big_wait(&full[s], (g / Cfg::stages) & 1, dead));
-        if (!ok) break;
-        uint32_t v[32];
+    const int total = (tiles - first + stride - 1) / stride * steps;  // (first < tiles)
+    int held = -1;  // a stage whose operand is on its way into tensor memory
+    auto hand_over = [&]() {
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      if (Cfg::raw_tokens) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready[held]);
+      held = -1;
+    };
+    for (int g = warp / 4 - 1; g < total; g += Cfg::converters) {
+      const int s = g % Cfg::stages, at = g % Cfg::a_stages;
+      const uint32_t phase = (g / Cfg::stages) & 1;
+      if (held >= 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait(&full[s], phase))) hand_over();
+      if (!__all_sync(0xFFFFFFFFu, big_wait(&full[s], phase, dead))) break;
+      uint4 w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(raw + s * kBigRaw + row * 64 + ((c * 16) ^ turn));
-          i8x4_to_f16(w.x, v[c * 8], v[c * 8 + 1]);
-          i8x4_to_f16(w.y, v[c * 8 + 2], v[c * 8 + 3]);
-          i8x4_to_f16(w.z, v[c * 8 + 4], v[c * 8 + 5]);
-          i8x4_to_f16(w.w, v[c * 8 + 6], v[c * 8 + 7]);
-        }
-        tmem_st32(tmem + Cfg::a_col + s * 32 + (static_cast<uint32_t>((warp - 4) * 32) << 16), v);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ready[s]);
+      for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + s * kBigRaw + row * 64 + ((c * 16) ^ turn));
+      if (held >= 0) hand_over();
+      if (Cfg::a_stages < Cfg::stages && g >= Cfg::a_stages) {  // the operand that stood there has been used
+        const int before = g - Cfg::a_stages;
+        if (!__all_sync(0xFFFFFFFFu, big_wait(&empty[before % Cfg::stages], (before / Cfg::stages) & 1, dead))) break;
       }
+      if (Cfg::raw_tokens) {
+        // 16 codes a thread: token j, piece c of four
+#pragma unroll
+        for (int q = quad * 32 + lane; q < kTN * 4; q += 128) {
+          const int c = (q >> 3) & 3, j = (q >> 5) * 8 + (q & 7);
+          const uint4 v = *reinterpret_cast<const uint4*>(raw_x + s * Cfg::raw + j * 64 + ((c * 16) ^ (((j >> 1) & 3) * 16)));
+          uint4 lo, hi;
+          i8x4_to_f16(v.x, lo.x, lo.y);
+          i8x4_to_f16(v.y, lo.z, lo.w);
+          i8x4_to_f16(v.z, hi.x, hi.y);
+          i8x4_to_f16(v.w, hi.z, hi.w);
+          uint4* to = reinterpret_cast<uint4*>(tokens + s * Cfg::image + (j >> 3) * 1024 + c * 256 + (j & 7) * 16);
+          to[0] = lo;
+          to[8] = hi;
+        }
+      }
+      uint32_t v[32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        i8x4_to_f16(w[c].x, v[c * 8], v[c * 8 + 1]);
+        i8x4_to_f16(w[c].y, v[c * 8 + 2], v[c * 8 + 3]);
+        i8x4_to_f16(w[c].z, v[c * 8 + 4], v[c * 8 + 5]);
+        i8x4_to_f16(w[c].w, v[c * 8 + 6], v[c * 8 + 7]);
+      }
+      tmem_st32(tmem + Cfg::a_col + at * 32 + (static_cast<uint32_t>(quad * 32) << 16), v);
+      held = s;
     }
-  } else if (warp >= 8) {
-    constexpr int kCols = kTN / 4;  // a warp's columns: those of its quarter
-    const int quad = warp & 3, c0 = (warp - 8) / 4 * kCols;
+    if (held >= 0) hand_over();
+  } else if (warp >= 4 + 4 * Cfg::converters) {
+    constexpr int kCols = kTN / (Cfg::readers / 4);  // a warp's columns
+    const int quad = warp & 3, c0 = (warp - 4 - 4 * Cfg::converters) / 4 * kCols;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     int run = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (int tile = first; tile < tiles; tile += stride) {
       const int row = tile / a.token_tiles * kBigM + quad * 32 + lane, j0 = tile % a.token_tiles * kTN;
       const int width = min(kTN, a.n16 - j0);
       const float sw = row < a.rows ? a.w_scale[row] : 0.f;
@@ -394,9 +477,9 @@ __global__ void __launch_bounds__(kBigThreads, 1) k_i8_big(const __grid_constant
 #pragma unroll
       for (int i = 0; i < kCols; ++i) total[i] = 0;
       bool ok = true;
-      for (int k0 = 0; k0 < a.steps; k0 += kBigRun, ++run) {
-        const int b = run % Cfg::sums;
-        ok = __all_sync(0xFFFFFFFFu, big_wait(&sums_full[b], (run / Cfg::sums) & 1, dead)) && ok;
+      for (int k0 = 0; k0 < steps; k0 += kBigRun, ++run) {
+        const int b = run & 1;
+        ok = __all_sync(0xFFFFFFFFu, big_wait(&sums_full[b], (run / 2) & 1, dead)) && ok;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
@@ -411,14 +494,20 @@ __global__ void __launch_bounds__(kBigThreads, 1) k_i8_big(const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&sums_empty[b]);
       }
-      // (after a wait that ran out: NaN)
-      const float w_scale = ok ? sw : __uint_as_float(0x7FC00000u);
-      float* y = a.y + (j0 + c0) * a.y_stride + row;
+      if (a.cs > 1) {  // the stages are done with: the only tile's sums take their place, [token][row]
+        int* sums = reinterpret_cast<int*>(raw);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        const int j = j0 + c0 + i;
-        if (j < a.n && row < a.rows) *y = static_cast<float>(total[i]) * __ldg(a.x_scale + j) * w_scale;
-        y += a.y_stride;
+        for (int i = 0; i < kCols; ++i) sums[(c0 + i) * kBigM + quad * 32 + lane] = total[i];
+      } else {
+        // (after a wait that ran out: NaN)
+        const float w_scale = ok ? sw : __uint_as_float(0x7FC00000u);
+        float* y = a.y + (j0 + c0) * a.y_stride + row;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          const int j = j0 + c0 + i;
+          if (j < a.n && row < a.rows) *y = static_cast<float>(total[i]) * __ldg(a.x_scale + j) * w_scale;
+          y += a.y_stride;
+        }
       }
     }
   }
@@ -428,6 +517,23 @@ __global__ void __launch_bounds__(kBigThreads, 1) k_i8_big(const __grid_constant
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+  if (a.cs > 1) {
+    cluster_barrier();
+    const int* sums = reinterpret_cast<const int*>(raw);
+    const int row0 = first / a.token_tiles * kBigM, j0 = first % a.token_tiles * kTN, width = min(kTN, a.n - j0);
+    int gone = 0;  // a wait ran out in one of the CTAs
+    for (int q = 0; q < a.cs; ++q) gone |= ld_rank(&dead_word, q);
+    // token i of the tile by CTA i mod cs: a thread takes one row of it
+    for (int e = threadIdx.x; e < (width - rank + a.cs - 1) / a.cs * kBigM; e += Cfg::threads) {
+      const int i = e / kBigM * a.cs + rank, r = e % kBigM;
+      if (row0 + r >= a.rows) continue;
+      int t = 0;
+      for (int q = 0; q < a.cs; ++q) t += ld_rank(&sums[i * kBigM + r], q);
+      const float v = static_cast<float>(t) * __ldg(a.x_scale + j0 + i) * __ldg(a.w_scale + row0 + r);
+      a.y[(j0 + i) * a.y_stride + row0 + r] = gone ? __uint_as_float(0x7FC00000u) : v;
+    }
+    cluster_barrier();
   }
 }
 
@@ -455,8 +561,8 @@ __global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_str
   dst[8] = q;
 }
 
-// The map of w for boxes of 64 columns x 128 rows.
-cudaError_t map_of(const I8MatmulArgs& a, CUtensorMap* map) {
+// The map of rows of codes for boxes of 64 columns x box_rows rows.
+cudaError_t map_of(const int8_t* p, int64_t stride, int rows, int cols, int box_rows, CUtensorMap* map) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -469,51 +575,64 @@ cudaError_t map_of(const I8MatmulArgs& a, CUtensorMap* map) {
     if (got != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
     __atomic_store_n(&found, fn, __ATOMIC_RELAXED);
   }
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.cols), static_cast<cuuint64_t>(a.rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.cols)};
-  const cuuint32_t box[2] = {kBigK, kBigM}, steps[2] = {1, 1};
-  const CUresult r = reinterpret_cast<Encode>(fn)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(a.w), dims, strides,
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  const cuuint32_t box[2] = {kBigK, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
+  const CUresult r = reinterpret_cast<Encode>(fn)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides,
                                                   box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-constexpr int kFewMost = 32;  // tokens
+constexpr int kRawMost = 64;  // tokens that k_i8_big takes as codes
 
 template <int kTN>
-cudaError_t launch_big(const I8MatmulArgs& a, cudaStream_t st) {
+cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
+  using Cfg = BigCfg<kTN>;
   static unsigned long long done = 0;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_big<kTN>), BigCfg<kTN>::smem, &done);
-  if (e != cudaSuccess) return e;
-  CUtensorMap map;
-  e = map_of(a, &map);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_big<kTN>), Cfg::smem, &done);
   if (e != cudaSuccess) return e;
   const int steps = (a.cols + kBigK - 1) / kBigK, n16 = (a.n + 15) / 16 * 16;
-  const BigArgs b{static_cast<const uint8_t*>(a.scratch), a.x_scale, a.w_scale, a.y, a.y_stride, a.rows, a.n, n16, steps,
-                  (a.rows + kBigM - 1) / kBigM, (a.n + kTN - 1) / kTN};
-  const int64_t threads = static_cast<int64_t>(n16 / 8) * steps * 32, tiles = static_cast<int64_t>(b.row_tiles) * b.token_tiles;
+  BigArgs b{static_cast<const uint8_t*>(a.scratch), a.x_scale, a.w_scale, a.y, a.y_stride, a.rows, a.n, n16, steps,
+            (a.rows + kBigM - 1) / kBigM, (a.n + kTN - 1) / kTN, cs};
+  const int64_t tiles = static_cast<int64_t>(b.row_tiles) * b.token_tiles;
+  CUtensorMap w_map, x_map;
+  e = map_of(a.w, a.cols, a.rows, a.cols, kBigM, &w_map);
+  if (e == cudaSuccess && Cfg::raw_tokens) e = map_of(a.x, a.n > 1 ? a.x_stride : a.cols, a.n, a.cols, kTN, &x_map);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = cs > 1 ? static_cast<unsigned>(tiles * cs) : static_cast<unsigned>(tiles < kSms ? tiles : kSms);
+  if (Cfg::raw_tokens) {
+    void* p[] = {&w_map, &x_map, &b};
+    return launch_clusters(reinterpret_cast<const void*>(k_i8_big<kTN>), cs, grid, Cfg::threads, Cfg::smem, st, p);
+  }
+  x_map = w_map;  // not read
+  const int64_t threads = static_cast<int64_t>(n16 / 8) * steps * 32;
   k_i8_image<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a.x, a.x_stride, a.n, a.cols, n16, steps,
                                                                            static_cast<uint8_t*>(a.scratch));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_i8_big<kTN>, dim3(static_cast<unsigned>(tiles < kBigCtas ? tiles : kBigCtas)), kBigThreads,
-                    BigCfg<kTN>::smem, st, map, b);
+  return launch_pdl_clusters(k_i8_big<kTN>, static_cast<unsigned>(cs), dim3(grid), Cfg::threads, Cfg::smem, st, w_map, x_map, b);
 }
 
 }  // namespace
 
 size_t i8_matmul_scratch_bytes(int rows, int cols, int n) {
-  if (n <= kFewMost) return 0;
+  if (n <= kRawMost) return 0;
   return static_cast<size_t>((n + 15) / 16 * 16) * ((cols + kBigK - 1) / kBigK) * kBigK * 2;
 }
 
 cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
-  if (a.n <= 8) return launch_few<1>(a, st);
-  if (a.n <= 16) return launch_few<2>(a, st);
-  if (a.n <= kFewMost) return launch_few<4>(a, st);
-  if (a.n <= 64) return launch_big<64>(a, st);
-  if (a.n <= 128) return launch_big<128>(a, st);
-  return launch_big<256>(a, st);
+  if (a.n <= kFewMost) return launch_few(a, st);
+  int tn = a.n <= 16 ? 16 : a.n <= 32 ? 32 : a.n <= 64 ? 64 : a.n <= 128 ? 128 : 192, cs = 1;
+  const int64_t tiles = static_cast<int64_t>((a.rows + kBigM - 1) / kBigM) * ((a.n + tn - 1) / tn);
+  const int steps = (a.cols + kBigK - 1) / kBigK;
+  while (cs < 8 && tiles * cs * 2 <= kSms && steps >= cs * 4) cs *= 2;
+  if (const char* f = getenv("BIG")) { int t, c; if (sscanf(f, "%d,%d", &t, &c) == 2 && (t <= 64 || a.n > 64)) tn = t, cs = c; }
+  if (tn == 16) return launch_big<16>(a, cs, st);
+  if (tn == 32) return launch_big<32>(a, cs, st);
+  if (tn == 64) return launch_big<64>(a, cs, st);
+  if (tn == 128) return launch_big<128>(a, cs, st);
+  return launch_big<192>(a, cs, st);
 }
 
 }  // namespace tqd
