@@ -198,39 +198,42 @@ cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
 // ------------------------------------------------------------ 9 tokens and more
 //
 // A CTA per SM makes tiles of 128 rows of w by kTN tokens on the fifth-generation tensor
-// cores.  In a step of 64 columns the rows' codes come by a tensor copy as they are, and
+// cores.  In a step of 128 columns the rows' codes come by a tensor copy as they are, and
 // groups of four warps, a step each in turn, make them f16 and put them into tensor memory as
 // operand A (a lane is a row).  The tokens, operand B, are f16 in shared memory: up to 64 are
 // made so by the same warps, more come by a bulk copy from an image that k_i8_image laid out in the
 // scratch in the order of shared memory.  Other warps take the sums out of tensor memory
-// after every 16 steps (1024 columns) and add them up as whole numbers; they write a tile's results
+// after every 8 steps (1024 columns) and add them up as whole numbers; they write a tile's results
 // while the next one's sums are made.  Where there are few tiles a cluster of cs CTAs shares a
 // tile's steps, and each adds up and writes a part of its tokens.
-constexpr int kBigM = 128, kBigK = 64, kBigRun = 16;
-constexpr uint32_t kBigRaw = kBigM * kBigK;  // bytes of the rows' codes in a stage
+constexpr int kBigM = 128, kImageK = 64;
+constexpr int kConverters = 2;               // groups of four warps
 
 template <int kTN>
 struct BigCfg {
   static constexpr bool raw_tokens = kTN <= 64;
-  static constexpr int converters = kTN <= 128 ? 2 : 1;              // groups of four warps
+  static constexpr int K = raw_tokens ? 128 : kImageK;       // columns of a step
+  static constexpr int run = 1024 / K;                       // steps that the f32 sums hold
   static constexpr int readers = kTN <= 32 ? 4 : kTN <= 128 ? 8 : 16;  // warps that read sums (TN 192: 48 columns each)
-  static constexpr int threads = 32 * (4 + 4 * converters + readers);  // copies, MMAs, two idle; then these
-  static constexpr uint32_t image = kTN * kBigK * 2;                 // bytes of f16 tokens in a stage
-  static constexpr uint32_t raw = raw_tokens ? kTN * kBigK : 0;      // bytes of their codes
-  static constexpr uint32_t stage = kBigRaw + image + raw;
-  static constexpr int stages = kTN == 192 ? 6 : kTN == 128 ? 8 : kTN == 64 ? 10 : 12;
-  static constexpr int a_stages = kTN == 192 ? 4 : stages;  // of operand A, 32 columns each
+  static constexpr int threads = 32 * (4 + 4 * kConverters + readers);  // copies, MMAs, two idle; then these
+  static constexpr uint32_t w_raw = kBigM * K;               // bytes of the rows' codes in a stage
+  static constexpr uint32_t image = kTN * K * 2;                 // bytes of f16 tokens in a stage
+  static constexpr uint32_t raw = raw_tokens ? kTN * K : 0;       // bytes of their codes
+  static constexpr uint32_t stage = w_raw + image + raw;
+  static constexpr int stages = kTN == 192 ? 6 : kTN == 128 ? 8 : kTN == 64 ? 5 : 7;
+  static constexpr int a_stages = kTN == 192 ? 4 : stages;  // of operand A, K / 2 columns each
   static constexpr uint32_t a_col = 2 * kTN;                // behind two accumulators, in turn
   static constexpr size_t smem = stages * stage + 1024;
-  static_assert(a_col + a_stages * 32 <= 512, "tensor memory");
+  static_assert(a_col + a_stages * K / 2 <= 512, "tensor memory");
   static_assert(static_cast<size_t>(kTN) * kBigM * 4 <= stages * stage, "a cluster's sums take the stages' place");
 };
 
+template <int kK>
 __device__ __forceinline__ uint64_t image_desc(const void* p) {
-  // core matrices of 8 tokens x 16 bytes, 128 bytes apart along the columns, 1024 along the tokens
+  // core matrices of 8 tokens x 16 bytes, 128 bytes apart along the columns, kK * 16 along the tokens
   uint64_t d = static_cast<uint64_t>((smem_addr(p) & 0x3FFFFu) >> 4);
   d |= static_cast<uint64_t>(128 >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(kK) << 32;
   return d | (1ull << 46);
 }
 
@@ -263,13 +266,23 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
       : "r"(at)
       : "memory");
 }
-// A box of 64 bytes x 128 rows at (col, row): 16-byte pieces turned as swizzle 64B does.
+// A box of K bytes a row at (col, row): 16-byte pieces turned as swizzle 128B (64B for 64) does.
 __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int col, int row, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           smem_addr(dst)),
       "l"(map), "r"(col), "r"(row), "r"(smem_addr(bar))
       : "memory");
+}
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // True in one lane of a whole warp.
 __device__ __forceinline__ bool elect_one() {
@@ -303,7 +316,7 @@ struct BigArgs {
   const float *x_scale, *w_scale;
   float* y;
   int64_t y_stride;
-  int rows, n, n16, steps, row_tiles, token_tiles, cs;
+  int rows, cols, n, n16, steps, row_tiles, token_tiles, cs;
 };
 
 template <int kTN>
@@ -317,7 +330,7 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
   volatile int* dead = &dead_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* raw = big_smem + (1024u - (smem_addr(big_smem) & 1023u)) % 1024u;  // [stage] codes of the rows,
-  uint8_t* tokens = raw + Cfg::stages * kBigRaw;                             // f16 of the tokens,
+  uint8_t* tokens = raw + Cfg::stages * Cfg::w_raw;                             // f16 of the tokens,
   uint8_t* raw_x = tokens + Cfg::stages * Cfg::image;                        // codes of the tokens
 
   if (threadIdx.x == 0) {
@@ -355,18 +368,18 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
     bool image_there = Cfg::raw_tokens, ok = true;
     for (int tile = first; ok && tile < tiles; tile += stride) {
       const int row0 = tile / a.token_tiles * kBigM, j0 = tile % a.token_tiles * kTN;
-      const uint32_t bytes = Cfg::raw_tokens ? Cfg::raw : min(kTN, a.n16 - j0) * kBigK * 2;
+      const uint32_t bytes = Cfg::raw_tokens ? Cfg::raw : min(kTN, a.n16 - j0) * Cfg::K * 2;
       for (int k = from; k < from + steps; ++k) {
         if (issued >= Cfg::stages) ok = __all_sync(0xFFFFFFFFu, big_wait(&empty[s], phase ^ 1, dead));
         if (!ok) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&full[s], kBigRaw + bytes);
-          copy_box(raw + s * kBigRaw, &w_map, k * kBigK, row0, &full[s]);
+          mbar_arrive_expect_tx(&full[s], Cfg::w_raw + bytes);
+          copy_box(raw + s * Cfg::w_raw, &w_map, k * Cfg::K, row0, &full[s]);
           if (Cfg::raw_tokens) {
-            copy_box(raw_x + s * Cfg::raw, &x_map, k * kBigK, j0, &full[s]);
+            copy_box(raw_x + s * Cfg::raw, &x_map, k * Cfg::K, j0, &full[s]);
           } else {
             if (!image_there) pdl_wait();  // the kernel before this one writes the image
-            bulk_g2s(tokens + s * Cfg::image, a.image + (static_cast<int64_t>(k) * a.n16 + j0) * (kBigK * 2), bytes, &full[s]);
+            bulk_g2s(tokens + s * Cfg::image, a.image + (static_cast<int64_t>(k) * a.n16 + j0) * (Cfg::K * 2), bytes, &full[s]);
           }
         }
         image_there = true;
@@ -382,37 +395,44 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
   } else if (warp == 1) {
     int s = 0, at = 0, run = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true, seen = false;
     for (int tile = first; ok && tile < tiles; tile += stride) {
       const int width = min(kTN, a.n16 - tile % a.token_tiles * kTN);
       const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kBigM >> 4) << 24);
-      for (int k0 = 0; ok && k0 < steps; k0 += kBigRun, ++run) {
+      for (int k0 = 0; ok && k0 < steps; k0 += Cfg::run, ++run) {
         const int b = run & 1;
         if (run >= 2) ok = __all_sync(0xFFFFFFFFu, big_wait(&sums_empty[b], (run / 2 - 1) & 1, dead));
-        const int end = min(steps, k0 + kBigRun);
+        const int end = min(steps, k0 + Cfg::run);
         for (int k = k0; ok && k < end; ++k) {
-          // (ready follows full, but this warp has to see the image's bytes itself)
-          ok = __all_sync(0xFFFFFFFFu, big_wait(&ready[s], phase, dead) && big_wait(&full[s], phase, dead));
+          // (ready follows full: the converting warps waited for that; most often it was seen a step before)
+          if (!seen) ok = __all_sync(0xFFFFFFFFu, big_wait(&ready[s], phase, dead));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const int next = s + 1 == Cfg::stages ? 0 : s + 1;
+          const bool there = mbar_test(&ready[next], phase ^ (next == 0));
           if (elect_one()) {
-            const uint64_t bd = image_desc(tokens + s * Cfg::image);
+            const uint64_t bd = image_desc<Cfg::K>(tokens + s * Cfg::image);
+            const int left = a.cols - (from + k) * Cfg::K;
 #pragma unroll
-            for (int i = 0; i < kBigK / 16; ++i)
-              mma_ts(tmem + b * kTN, tmem + Cfg::a_col + at * 32 + i * 8, bd + i * 16, idesc, k > k0 || i > 0);
+            for (int i = 0; i < Cfg::K / 16; ++i)
+              if (i * 16 < left)
+                mma_ts(tmem + b * kTN, tmem + Cfg::a_col + at * (Cfg::K / 2) + i * 8, bd + i * 16, idesc, k > k0 || i > 0);
             mma_commit(&empty[s]);
             if (k + 1 == end) mma_commit(&sums_full[b]);
           }
-          if (++s == Cfg::stages) s = 0, phase ^= 1;
+          seen = __all_sync(0xFFFFFFFFu, there);
+          phase ^= next == 0;
+          s = next;
           if (++at == Cfg::a_stages) at = 0;
         }
       }
     }
     if (elect_one()) mma_commit(&done);  // tensor memory is given back once every MMA is over
     mbar_wait_warp(&done, 0, kWaitLimitNs / 4);
-  } else if (warp >= 4 && warp < 4 + 4 * Cfg::converters) {
+  } else if (warp >= 4 && warp < 4 + 4 * kConverters) {
     const int quad = warp & 3, row = quad * 32 + lane;
-    const uint32_t turn = ((row >> 1) & 3) * 16;
+    constexpr int kPieces = Cfg::K / 16;  // of 16 codes
+    const uint32_t turn = Cfg::K == 128 ? (row & 7) * 16 : ((row >> 1) & 3) * 16;
     const int total = (tiles - first + stride - 1) / stride * steps;  // (first < tiles)
     int held = -1;  // a stage whose operand is on its way into tensor memory
     auto hand_over = [&]() {
@@ -423,50 +443,56 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
       if (lane == 0) mbar_arrive(&ready[held]);
       held = -1;
     };
-    for (int g = warp / 4 - 1; g < total; g += Cfg::converters) {
+    for (int g = warp / 4 - 1; g < total; g += kConverters) {
       const int s = g % Cfg::stages, at = g % Cfg::a_stages;
       const uint32_t phase = (g / Cfg::stages) & 1;
-      if (held >= 0 && !__all_sync(0xFFFFFFFFu, mbar_try_wait(&full[s], phase))) hand_over();
+      if (held >= 0 && !__all_sync(0xFFFFFFFFu, mbar_test(&full[s], phase))) hand_over();
       if (!__all_sync(0xFFFFFFFFu, big_wait(&full[s], phase, dead))) break;
+      auto piece = [&](int c) { return *reinterpret_cast<const uint4*>(raw + s * Cfg::w_raw + row * Cfg::K + ((c * 16) ^ turn)); };
       uint4 w[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(raw + s * kBigRaw + row * 64 + ((c * 16) ^ turn));
+      for (int c = 0; c < 4; ++c) w[c] = piece(c);
       if (held >= 0) hand_over();
       if (Cfg::a_stages < Cfg::stages && g >= Cfg::a_stages) {  // the operand that stood there has been used
         const int before = g - Cfg::a_stages;
         if (!__all_sync(0xFFFFFFFFu, big_wait(&empty[before % Cfg::stages], (before / Cfg::stages) & 1, dead))) break;
       }
       if (Cfg::raw_tokens) {
-        // 16 codes a thread: token j, piece c of four
+        // 16 codes a thread: token j, piece c of eight
 #pragma unroll
-        for (int q = quad * 32 + lane; q < kTN * 4; q += 128) {
-          const int c = (q >> 3) & 3, j = (q >> 5) * 8 + (q & 7);
-          const uint4 v = *reinterpret_cast<const uint4*>(raw_x + s * Cfg::raw + j * 64 + ((c * 16) ^ (((j >> 1) & 3) * 16)));
+        for (int q = quad * 32 + lane; q < kTN * 8; q += 128) {
+          const int c = (q >> 3) & 7, j = (q >> 6) * 8 + (q & 7);
+          const uint4 v = *reinterpret_cast<const uint4*>(raw_x + s * Cfg::raw + j * 128 + ((c * 16) ^ ((j & 7) * 16)));
           uint4 lo, hi;
           i8x4_to_f16(v.x, lo.x, lo.y);
           i8x4_to_f16(v.y, lo.z, lo.w);
           i8x4_to_f16(v.z, hi.x, hi.y);
           i8x4_to_f16(v.w, hi.z, hi.w);
-          uint4* to = reinterpret_cast<uint4*>(tokens + s * Cfg::image + (j >> 3) * 1024 + c * 256 + (j & 7) * 16);
+          uint4* to = reinterpret_cast<uint4*>(tokens + s * Cfg::image + (j >> 3) * 2048 + c * 256 + (j & 7) * 16);
           to[0] = lo;
           to[8] = hi;
         }
       }
-      uint32_t v[32];
+      const uint32_t operand = tmem + Cfg::a_col + at * (Cfg::K / 2) + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        i8x4_to_f16(w[c].x, v[c * 8], v[c * 8 + 1]);
-        i8x4_to_f16(w[c].y, v[c * 8 + 2], v[c * 8 + 3]);
-        i8x4_to_f16(w[c].z, v[c * 8 + 4], v[c * 8 + 5]);
-        i8x4_to_f16(w[c].w, v[c * 8 + 6], v[c * 8 + 7]);
+      for (int h = 0; h < kPieces / 4; ++h) {
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          i8x4_to_f16(w[c].x, v[c * 8], v[c * 8 + 1]);
+          i8x4_to_f16(w[c].y, v[c * 8 + 2], v[c * 8 + 3]);
+          i8x4_to_f16(w[c].z, v[c * 8 + 4], v[c * 8 + 5]);
+          i8x4_to_f16(w[c].w, v[c * 8 + 6], v[c * 8 + 7]);
+          if (h + 1 < kPieces / 4) w[c] = piece(c + 4);
+        }
+        tmem_st32(operand + h * 32, v);
       }
-      tmem_st32(tmem + Cfg::a_col + at * 32 + (static_cast<uint32_t>(quad * 32) << 16), v);
       held = s;
     }
     if (held >= 0) hand_over();
-  } else if (warp >= 4 + 4 * Cfg::converters) {
+  } else if (warp >= 4 + 4 * kConverters) {
     constexpr int kCols = kTN / (Cfg::readers / 4);  // a warp's columns
-    const int quad = warp & 3, c0 = (warp - 4 - 4 * Cfg::converters) / 4 * kCols;
+    const int quad = warp & 3, c0 = (warp - 4 - 4 * kConverters) / 4 * kCols;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     int run = 0;
     for (int tile = first; tile < tiles; tile += stride) {
@@ -477,7 +503,7 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
 #pragma unroll
       for (int i = 0; i < kCols; ++i) total[i] = 0;
       bool ok = true;
-      for (int k0 = 0; k0 < steps; k0 += kBigRun, ++run) {
+      for (int k0 = 0; k0 < steps; k0 += Cfg::run, ++run) {
         const int b = run & 1;
         ok = __all_sync(0xFFFFFFFFu, big_wait(&sums_full[b], (run / 2) & 1, dead)) && ok;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -543,26 +569,26 @@ __global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_str
                                                   uint8_t* image) {
   pdl_launch_dependents();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int c = static_cast<int>(at & 3), j8 = static_cast<int>((at >> 2) & 7);
+  const int j8 = static_cast<int>(at & 7), c = static_cast<int>((at >> 3) & 3);
   const int64_t rest = at >> 5;  // (token group, step), the step first
   const int k = static_cast<int>(rest % steps);
   const int64_t group = rest / steps;
   if (group * 8 >= n16) return;
   const int64_t j = group * 8 + j8;
-  const int col = k * kBigK + c * 16;
+  const int col = k * kImageK + c * 16;
   uint4 v = make_uint4(0u, 0u, 0u, 0u), p, q;
   if (j < n && col < cols) v = __ldg(reinterpret_cast<const uint4*>(x + j * x_stride + col));
   i8x4_to_f16(v.x, p.x, p.y);
   i8x4_to_f16(v.y, p.z, p.w);
   i8x4_to_f16(v.z, q.x, q.y);
   i8x4_to_f16(v.w, q.z, q.w);
-  uint4* dst = reinterpret_cast<uint4*>(image + (static_cast<int64_t>(k) * n16 + group * 8) * (kBigK * 2) + c * 256 + j8 * 16);
+  uint4* dst = reinterpret_cast<uint4*>(image + (static_cast<int64_t>(k) * n16 + group * 8) * (kImageK * 2) + c * 256 + j8 * 16);
   dst[0] = p;
   dst[8] = q;
 }
 
-// The map of rows of codes for boxes of 64 columns x box_rows rows.
-cudaError_t map_of(const int8_t* p, int64_t stride, int rows, int cols, int box_rows, CUtensorMap* map) {
+// The map of rows of codes for boxes of box_cols (64 or 128) x box_rows.
+cudaError_t map_of(const int8_t* p, int64_t stride, int rows, int cols, int box_cols, int box_rows, CUtensorMap* map) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -577,9 +603,10 @@ cudaError_t map_of(const int8_t* p, int64_t stride, int rows, int cols, int box_
   }
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
-  const cuuint32_t box[2] = {kBigK, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
   const CUresult r = reinterpret_cast<Encode>(fn)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides,
-                                                  box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                                                  box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                                  box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -592,13 +619,13 @@ cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
   static unsigned long long done = 0;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_big<kTN>), Cfg::smem, &done);
   if (e != cudaSuccess) return e;
-  const int steps = (a.cols + kBigK - 1) / kBigK, n16 = (a.n + 15) / 16 * 16;
-  BigArgs b{static_cast<const uint8_t*>(a.scratch), a.x_scale, a.w_scale, a.y, a.y_stride, a.rows, a.n, n16, steps,
+  const int steps = (a.cols + Cfg::K - 1) / Cfg::K, n16 = (a.n + 15) / 16 * 16;
+  BigArgs b{static_cast<const uint8_t*>(a.scratch), a.x_scale, a.w_scale, a.y, a.y_stride, a.rows, a.cols, a.n, n16, steps,
             (a.rows + kBigM - 1) / kBigM, (a.n + kTN - 1) / kTN, cs};
   const int64_t tiles = static_cast<int64_t>(b.row_tiles) * b.token_tiles;
   CUtensorMap w_map, x_map;
-  e = map_of(a.w, a.cols, a.rows, a.cols, kBigM, &w_map);
-  if (e == cudaSuccess && Cfg::raw_tokens) e = map_of(a.x, a.n > 1 ? a.x_stride : a.cols, a.n, a.cols, kTN, &x_map);
+  e = map_of(a.w, a.cols, a.rows, a.cols, Cfg::K, kBigM, &w_map);
+  if (e == cudaSuccess && Cfg::raw_tokens) e = map_of(a.x, a.n > 1 ? a.x_stride : a.cols, a.n, a.cols, Cfg::K, kTN, &x_map);
   if (e != cudaSuccess) return e;
   const unsigned grid = cs > 1 ? static_cast<unsigned>(tiles * cs) : static_cast<unsigned>(tiles < kSms ? tiles : kSms);
   if (Cfg::raw_tokens) {
@@ -618,15 +645,15 @@ cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
 
 size_t i8_matmul_scratch_bytes(int rows, int cols, int n) {
   if (n <= kRawMost) return 0;
-  return static_cast<size_t>((n + 15) / 16 * 16) * ((cols + kBigK - 1) / kBigK) * kBigK * 2;
+  return static_cast<size_t>((n + 15) / 16 * 16) * ((cols + kImageK - 1) / kImageK) * kImageK * 2;
 }
 
 cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
   if (a.n <= kFewMost) return launch_few(a, st);
   int tn = a.n <= 16 ? 16 : a.n <= 32 ? 32 : a.n <= 64 ? 64 : a.n <= 128 ? 128 : 192, cs = 1;
   const int64_t tiles = static_cast<int64_t>((a.rows + kBigM - 1) / kBigM) * ((a.n + tn - 1) / tn);
-  const int steps = (a.cols + kBigK - 1) / kBigK;
-  while (cs < 8 && tiles * cs * 2 <= kSms && steps >= cs * 4) cs *= 2;
+  const int steps = (a.cols + 127) / 128;
+  while (cs < 8 && tiles * cs * 2 <= kSms && steps >= cs * 2) cs *= 2;
   if (const char* f = getenv("BIG")) { int t, c; if (sscanf(f, "%d,%d", &t, &c) == 2 && (t <= 64 || a.n > 64)) tn = t, cs = c; }
   if (tn == 16) return launch_big<16>(a, cs, st);
   if (tn == 32) return launch_big<32>(a, cs, st);
