@@ -438,29 +438,13 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
     constexpr int kPieces = Cfg::K / 16;  // of 16 codes
     const uint32_t turn = Cfg::K == 128 ? (row & 7) * 16 : ((row >> 1) & 3) * 16;
     const int total = (tiles - first + stride - 1) / stride * steps;  // (first < tiles)
-    int held = -1;  // a stage whose operand is on its way into tensor memory
-    auto hand_over = [&]() {
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      if (Cfg::raw_tokens) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ready[held]);
-      held = -1;
-    };
     for (int g = warp / 4 - 1; g < total; g += kConverters) {
       const int s = g % Cfg::stages, at = g % Cfg::a_stages;
-      const uint32_t phase = (g / Cfg::stages) & 1;
-      if (held >= 0 && !__all_sync(0xFFFFFFFFu, mbar_test(&full[s], phase))) hand_over();
-      if (!__all_sync(0xFFFFFFFFu, big_wait(&full[s], phase, dead))) break;
-      auto piece = [&](int c) { return *reinterpret_cast<const uint4*>(raw + s * Cfg::w_raw + row * Cfg::K + ((c * 16) ^ turn)); };
-      uint4 w[4];
+      if (!__all_sync(0xFFFFFFFFu, big_wait(&full[s], (g / Cfg::stages) & 1, dead))) break;
+      const uint8_t* from_w = raw + s * Cfg::w_raw + row * Cfg::K;
+      uint4 w[kPieces];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = piece(c);
-      if (held >= 0) hand_over();
-      if (Cfg::a_stages < Cfg::stages && g >= Cfg::a_stages) {  // the operand that stood there has been used
-        const int before = g - Cfg::a_stages;
-        if (!__all_sync(0xFFFFFFFFu, big_wait(&empty[before % Cfg::stages], (before / Cfg::stages) & 1, dead))) break;
-      }
+      for (int c = 0; c < kPieces; ++c) w[c] = *reinterpret_cast<const uint4*>(from_w + ((c * 16) ^ turn));
       if (Cfg::raw_tokens) {
         // 16 codes a thread: token j, piece c of eight
 #pragma unroll
@@ -476,6 +460,7 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
           to[0] = lo;
           to[8] = hi;
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       const uint32_t operand = tmem + Cfg::a_col + at * (Cfg::K / 2) + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll
@@ -483,17 +468,23 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
         uint32_t v[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          i8x4_to_f16(w[c].x, v[c * 8], v[c * 8 + 1]);
-          i8x4_to_f16(w[c].y, v[c * 8 + 2], v[c * 8 + 3]);
-          i8x4_to_f16(w[c].z, v[c * 8 + 4], v[c * 8 + 5]);
-          i8x4_to_f16(w[c].w, v[c * 8 + 6], v[c * 8 + 7]);
-          if (h + 1 < kPieces / 4) w[c] = piece(c + 4);
+          i8x4_to_f16(w[h * 4 + c].x, v[c * 8], v[c * 8 + 1]);
+          i8x4_to_f16(w[h * 4 + c].y, v[c * 8 + 2], v[c * 8 + 3]);
+          i8x4_to_f16(w[h * 4 + c].z, v[c * 8 + 4], v[c * 8 + 5]);
+          i8x4_to_f16(w[h * 4 + c].w, v[c * 8 + 6], v[c * 8 + 7]);
+        }
+        // (converted before the wait for the operand that stood there to be used)
+        if (h == 0 && Cfg::a_stages < Cfg::stages && g >= Cfg::a_stages) {
+          const int before = g - Cfg::a_stages;
+          __all_sync(0xFFFFFFFFu, big_wait(&empty[before % Cfg::stages], (before / Cfg::stages) & 1, dead));
         }
         tmem_st32(operand + h * 32, v);
       }
-      held = s;
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready[s]);
     }
-    if (held >= 0) hand_over();
   } else if (warp >= 4 + 4 * kConverters) {
     constexpr int kCols = kTN / (Cfg::readers / 4);  // a warp's columns
     const int quad = warp & 3, c0 = (warp - 4 - 4 * kConverters) / 4 * kCols;
