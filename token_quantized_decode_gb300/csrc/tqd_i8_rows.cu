@@ -29,7 +29,15 @@ constexpr float kBand = kKind == kI8Rows ? 0x1p-16f : kKind == kI8Norm ? 0x1p-15
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it leaves the nearest whole number in the low bits
 
-__device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
+// g / (1 + e^-g): the quotient from the approximate reciprocal and one step of Newton's iteration, within a unit.
+// (e^87 is the largest that leaves the reciprocal in range; what is below it counts for nothing in a row that is done here.)
+__device__ __forceinline__ float silu(float g) {
+  const float d = 1.f + expf(fminf(-g, 87.f));
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+  const float q = g * r;
+  return fmaf(fmaf(-d, q, g), r, q);
+}
 
 // silu(g) u to 2^-38, for gates whose e^-g is within f32: of a row whose largest |y| is at least 2^-40
 // and whose |u| are at most 2^40, elements of at least a 2^8th of the largest have g > -62.  The f64 pipe does a
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     }
   }
   fetch(turn % Cfg::ahead, row + Cfg::ahead * step);
-  float top = 0.f, ss = 0.f;  // the largest |y| (a NaN or an infinity is above all), the sum of h^2
+  float top = 0.f, ss = 0.f, ups = 0.f;  // the largest |y| (a NaN or an infinity is above all), the sum of h^2, the largest |up|
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
     const int i = (e * kT + t) * 4;
@@ -268,8 +276,8 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[e][j] = silu(v[e][j]) * w[e][j];
-        if (fabsf(w[e][j]) > 0x1p40f) top = INFINITY;  // silu may be below f32's range, and count: the row in f64
       }
+      ups = max_abs(max_abs(ups, w[e][0], w[e][1]), w[e][2], w[e][3]);
     }
     if (kKind == kI8Norm) {
 #pragma unroll
@@ -294,6 +302,7 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     }
     top = max_abs(max_abs(top, v[e][0], v[e][1]), v[e][2], v[e][3]);
   }
+  if (kKind == kI8Silu && ups > 0x1p40f) top = INFINITY;  // silu may be below f32's range, and count: the row in f64
   uint32_t high = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top) & 0x7FFFFFFFu);
   if (kKind == kI8Norm) ss = warp_sum(ss);
   if (kT > 32) {
