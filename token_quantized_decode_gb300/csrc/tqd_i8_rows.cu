@@ -20,19 +20,26 @@ namespace {
 
 constexpr int kSms = 152;
 
-// The relative errors that reach t, in units of 2^-24, times 127: of y (exact for
-// rows; the product h g, 1; expf 4, 1 + e, the quotient and the product with up 3), of the
-// largest y the same, of 127 / max and of the product with it 1 each.  2 * 127 * 2^-24 =
-// 2^-16, 4 * 127 * 2^-24 = 2^-15, 16 * 127 * 2^-24 = 2^-13.
+// The relative errors that reach t, in units of 2^-24, times 127: of y (exact for rows; the product h g, 1; silu:
+// e^-g 5, 1 + e, the quotient and the product with up 1 each), of the largest y the same, of 127 / max and of
+// the product with it 1 each.  2 * 127 * 2^-24 < 2^-16, 4 * 127 * 2^-24 < 2^-15, 18 * 127 * 2^-24 < 1.125 * 2^-13.
 template <int kKind>
-constexpr float kBand = kKind == kI8Rows ? 0x1p-16f : kKind == kI8Norm ? 0x1p-15f : 0x1p-13f;
+constexpr float kBand = kKind == kI8Rows ? 0x1p-16f : kKind == kI8Norm ? 0x1p-15f : 0x1.2p-13f;
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it leaves the nearest whole number in the low bits
 
+// e^x for x <= 87 within 5 units: 2^t, t = x log2 e rounded, times 1 + ln 2 (x log2 e - t).  (Far below zero 2^t is 0.)
+__device__ __forceinline__ float exp_near(float x) {
+  constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147182f;
+  const float t = x * kLog2e, left = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return fmaf(e * kLn2, left, e);
+}
 // g / (1 + e^-g): the quotient from the approximate reciprocal and one step of Newton's iteration, within a unit.
 // (e^87 is the largest that leaves the reciprocal in range; what is below it counts for nothing in a row that is done here.)
 __device__ __forceinline__ float silu(float g) {
-  const float d = 1.f + expf(fminf(-g, 87.f));
+  const float d = 1.f + exp_near(fminf(-g, 87.f));
   float r;
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
   const float q = g * r;
@@ -105,19 +112,15 @@ __device__ __forceinline__ void load4(const float* p, int i, int n, float (&v)[4
   }
 }
 
-// Elements i to i + 3 of a row into 16 bytes of shared memory, zeros past the row's end.
+// `some` (of four) elements from p on into 16 bytes of shared memory.
 template <bool kVec>
-__device__ __forceinline__ void fetch4(float4* to, const float* p, int i, int n) {
-  const uint32_t dst = smem_addr(to);
+__device__ __forceinline__ void fetch4(uint32_t to, const float* p, int some) {
   if (kVec) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p + (i < n ? i : 0)), "r"(i < n ? 16 : 0)
-                 : "memory");
+    if (some > 0) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * j), "l"(p + (i + j < n ? i + j : 0)),
-                   "r"(i + j < n ? 4 : 0)
-                   : "memory");
+      if (j < some) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * j), "l"(p + j) : "memory");
   }
 }
 
@@ -235,15 +238,21 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
   const int64_t step = static_cast<int64_t>(gridDim.x) * (Cfg::block / kT);
   int64_t row = static_cast<int64_t>(blockIdx.x) * (Cfg::block / kT) + threadIdx.x / kT;
   const bool two = kKind == kI8Silu || (kKind == kI8Norm && a.other);
+  // (past a row's end its places hold zeros from here on: copies leave them)
+#pragma unroll
+  for (int i = 0; i < Cfg::ahead * Cfg::inputs * kE; ++i)
+    if ((i % kE * kT + t) * 4 + 3 >= n) next_rows[i * Cfg::block + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const uint32_t place = smem_addr(next_rows + threadIdx.x);
   auto fetch = [&](int at, int64_t r) {  // (a row past the last: nothing, but a group of its own)
-    float4* to = next_rows + at * (Cfg::inputs * kE * Cfg::block) + threadIdx.x;
     if (r < a.rows) {
+      const uint32_t to = place + at * (Cfg::inputs * kE * Cfg::block * 16);
+      const float* p = a.x + r * a.x_stride + 4 * t;
 #pragma unroll(kVec ? kE : 1)
-      for (int e = 0; e < kE; ++e) fetch4<kVec>(to + e * Cfg::block, a.x + r * a.x_stride, (e * kT + t) * 4, n);
+      for (int e = 0; e < kE; ++e) fetch4<kVec>(to + e * (Cfg::block * 16), p + e * (4 * kT), n - (e * kT + t) * 4);
       if (two) {
+        p = a.other + r * a.other_stride + 4 * t;
 #pragma unroll(kVec ? kE : 1)
-        for (int e = 0; e < kE; ++e)
-          fetch4<kVec>(to + (kE + e) * Cfg::block, a.other + r * a.other_stride, (e * kT + t) * 4, n);
+        for (int e = 0; e < kE; ++e) fetch4<kVec>(to + (kE + e) * (Cfg::block * 16), p + e * (4 * kT), n - (e * kT + t) * 4);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     far = max_abs(max_abs(far, d[0], d[1]), d[2], d[3]);
   }
   // One bit for each element whose quotient is next to a border, and for each that may be the largest (those that
-  // f32 cannot tell from it: silu 7 units each): the codes of the former are taken again below.
+  // f32 cannot tell from it: silu 8 units each): the codes of the former are taken again below.
   uint32_t near = 0u, tops = 0u;
   if (far > 0.5f - kBand<kKind>) {
 #pragma unroll
