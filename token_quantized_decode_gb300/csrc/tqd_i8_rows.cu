@@ -116,7 +116,7 @@ __device__ __forceinline__ void load4(const float* p, int i, int n, float (&v)[4
 template <bool kVec>
 __device__ __forceinline__ void fetch4(uint32_t to, const float* p, int some) {
   if (kVec) {
-    if (some > 0) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+    if (some > 0) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
