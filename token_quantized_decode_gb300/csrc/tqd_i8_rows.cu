@@ -127,6 +127,10 @@ __device__ __forceinline__ void fetch4(uint32_t to, const float* p, int some) {
 // Reductions over the kT threads of a row: one warp, or the whole block.
 template <int kT>
 struct RowGroup {
+  static __device__ __forceinline__ void sync() {
+    if (kT == 32) __syncwarp();
+    else __syncthreads();
+  }
   static __device__ __forceinline__ bool any(bool p) {
     return kT == 32 ? __any_sync(0xFFFFFFFFu, p) : __syncthreads_or(p) != 0;
   }
@@ -143,46 +147,6 @@ struct RowGroup {
     return v;
   }
 };
-
-// The codes of the elements of `near` (bit 4 e + j: group e of the thread, element j) again, in f64.  Rows as they are
-// know their largest value m; of the others it is found among the elements of `tops`, by the whole row's threads.
-template <int kKind, int kT>
-__device__ __noinline__ void codes_again(const I8RowsArgs& a, int64_t row, int t, uint32_t near, uint32_t tops, float m,
-                                         unsigned long long* sh_most) {
-  auto place = [&](uint32_t bits) {
-    const int b = __ffs(bits) - 1;
-    return (b / 4 * kT + t) * 4 + b % 4;
-  };
-  auto element = [&](int i) {
-    double h;
-    if (kKind == kI8Silu) return near_silu(a.x[row * a.x_stride + i], a.other[row * a.other_stride + i]);
-    return exact_element<kKind>(a, row, i, h);
-  };
-  double most = m, y = 0.0;
-  if (near) y = element(place(near));
-  if (kKind != kI8Rows) {
-    most = 0.0;
-    for (; tops; tops &= tops - 1) most = fmax(most, fabs(element(place(tops))));
-    if (kT == 32) {
-      most = RowGroup<kT>::all(most, nullptr, [](double p, double q) { return fmax(p, q); });
-    } else {
-      if (most > 0.0) atomicMax(sh_most, static_cast<unsigned long long>(__double_as_longlong(most)));
-      __syncthreads();
-      most = __longlong_as_double(static_cast<long long>(*sh_most));
-    }
-  }
-  int8_t* q = a.q + row * a.q_stride;
-  while (near) {
-    // the border, and the side of it that 127 y / most lies on (on it: the even code)
-    const int i = place(near);
-    const float low = floorf(static_cast<float>(y) * (127.f / m));
-    const double side = fma(127.0, y, -(low + 0.5) * most);
-    const int c = static_cast<int>(low);
-    q[i] = static_cast<int8_t>(side > 0.0 || (side == 0.0 && (c & 1)) ? c + 1 : c);
-    near &= near - 1;
-    if (near) y = element(place(near));
-  }
-}
 
 // A row in f64 as a whole.
 template <int kKind, int kT>
@@ -211,6 +175,67 @@ __device__ __noinline__ void whole_row(const I8RowsArgs& a, int64_t row, int t, 
   if (t == 0) a.scale[row] = lost ? __uint_as_float(0x7FC00000u) : static_cast<float>(top / 127.0);
 }
 
+// The code next to the border that 127 y / most lies at: by its side, and on it the even one.
+__device__ __forceinline__ int8_t code_at_border(double y, double most) {
+  const float low = floorf(static_cast<float>(y) * (127.f / static_cast<float>(most)));
+  const double side = fma(127.0, y, -(low + 0.5) * most);
+  const int c = static_cast<int>(low);
+  return static_cast<int8_t>(side > 0.0 || (side == 0.0 && (c & 1)) ? c + 1 : c);
+}
+
+// Elements next to borders, and those that may be a row's largest, of up to kWindow rows of a group of threads: they
+// are worked out together, a lane each.  (At once, one lane of a row's threads each, they took 12 of 40 us of
+// 2053 x 8192 silu rows: f64's latency, and two barriers.)
+constexpr int kWindow = 16;
+template <int kT>
+struct Pending {
+  static constexpr int room = kT == 32 ? 64 : 256;
+  uint32_t count, borders, over;   // entries; whether some are at borders; bit r: row r of the window had more than there was room for
+  unsigned long long most[kWindow];  // the largest |y| of each row, as bits
+  uint32_t entry[room];            // row of the window << 16 | largest << 15 | element
+  double y[room];
+
+  __device__ __forceinline__ void clear(int t) {
+    if (t < kWindow) most[t] = 0ull;
+    if (t == 0) count = borders = over = 0u;
+  }
+  __device__ __forceinline__ void add(int r, bool largest, int i) {
+    const uint32_t at = atomicAdd(&count, 1u);
+    if (at < room) entry[at] = static_cast<uint32_t>(r) << 16 | static_cast<uint32_t>(largest) << 15 | static_cast<uint32_t>(i);
+    else atomicOr(&over, 1u << r);
+    if (!largest) borders = 1u;
+  }
+};
+
+template <int kKind, int kT>
+__device__ __noinline__ void settle(const I8RowsArgs& a, Pending<kT>& p, int64_t first, int64_t step, int t, double* sh) {
+  RowGroup<kT>::sync();
+  const int n = static_cast<int>(min(p.count, static_cast<uint32_t>(p.room)));
+  const uint32_t over = p.over, some = p.borders;
+  for (int e = some ? t : n; e < n; e += kT) {
+    const uint32_t x = p.entry[e];
+    const int r = x >> 16, i = x & 0x7FFF;
+    const int64_t row = first + r * step;
+    double h, y;
+    if (kKind == kI8Silu) y = near_silu(a.x[row * a.x_stride + i], a.other[row * a.other_stride + i]);
+    else y = exact_element<kKind>(a, row, i, h);
+    p.y[e] = y;
+    if (x & 0x8000u) atomicMax(&p.most[r], static_cast<unsigned long long>(__double_as_longlong(fabs(y))));
+  }
+  RowGroup<kT>::sync();
+  for (int e = some ? t : n; e < n; e += kT) {
+    const uint32_t x = p.entry[e];
+    const int r = x >> 16, i = x & 0x7FFF;
+    if (!(x & 0x8000u) && !((over >> r) & 1u))
+      a.q[(first + r * step) * a.q_stride + i] = code_at_border(p.y[e], __longlong_as_double(static_cast<long long>(p.most[r])));
+  }
+  for (int r = 0; over && r < kWindow; ++r)
+    if ((over >> r) & 1u) whole_row<kKind, kT>(a, first + r * step, t, sh);
+  if (some) RowGroup<kT>::sync();
+  p.clear(t);  // (a block's next entries come after the next row's barrier)
+  if (kT == 32) __syncwarp();
+}
+
 // How many rows' inputs a thread has under way, and CTAs an SM.
 template <int kKind, int kT, int kE>
 struct RowsCfg {
@@ -233,7 +258,8 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
   __shared__ uint32_t sh_max[2][32];     // the largest |y| of each warp, as bits
   __shared__ float sh_sum[2][32];
   __shared__ double sh_d[32];
-  __shared__ unsigned long long sh_most[2];
+  __shared__ Pending<kT> pending[kKind == kI8Rows ? 1 : Cfg::block / kT];
+  Pending<kT>& later = pending[kKind == kI8Rows ? 0 : threadIdx.x / kT];
   const int t = threadIdx.x % kT, lane = threadIdx.x & 31, n = a.n;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (Cfg::block / kT);
   int64_t row = static_cast<int64_t>(blockIdx.x) * (Cfg::block / kT) + threadIdx.x / kT;
@@ -259,8 +285,14 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
   };
 #pragma unroll
   for (int i = 0; i < Cfg::ahead; ++i) fetch(i, row + i * step);
+  if (kKind != kI8Rows) {
+    later.clear(t);
+    if (kT == 32) __syncwarp();  // (a block's first entries come after the first row's barrier)
+  }
+  int turn = 0;
 #pragma unroll 1
-  for (int turn = 0; row < a.rows; row += step, ++turn) {
+  for (; row < a.rows; row += step, ++turn) {
+  if (kKind != kI8Rows && turn && turn % kWindow == 0) settle<kKind, kT>(a, later, row - kWindow * step, step, t, sh_d);
   const int odd = turn & 1;
   float v[kE][4], w[kE][4];  // y; what else came in (the norm: then h)
   asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::ahead - 1) : "memory");
@@ -318,7 +350,6 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     if (lane == 0) {
       sh_max[odd][threadIdx.x >> 5] = high;
       if (kKind == kI8Norm) sh_sum[odd][threadIdx.x >> 5] = ss;
-      if (kKind != kI8Rows && threadIdx.x == 0) sh_most[odd] = 0ull;
     }
     __syncthreads();
     ss = 0.f;
@@ -350,9 +381,9 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     }
     far = max_abs(max_abs(far, d[0], d[1]), d[2], d[3]);
   }
-  // One bit for each element whose quotient is next to a border, and for each that may be the largest (those that
-  // f32 cannot tell from it: silu 8 units each): the codes of the former are taken again below.
-  uint32_t near = 0u, tops = 0u;
+  // Quotients next to a border: one bit each for rows as they are, which know their largest value; else noted for later,
+  // with the elements that may be the largest (those that f32 cannot tell from it: silu 8 units each).
+  uint32_t near = 0u;
   if (far > 0.5f - kBand<kKind>) {
 #pragma unroll
     for (int e = 0; e < kE; ++e)
@@ -360,12 +391,21 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
       for (int j = 0; j < 4; ++j)
         if (fabsf(fmaf(v[e][j], inv, kMagic - c[e][j])) > 0.5f - kBand<kKind>) near |= 1u << (e * 4 + j);
   }
-  if (kKind != kI8Rows && __float_as_uint(top) >= high - (kKind == kI8Silu ? 32u : 0u)) {
+  auto place = [&](uint32_t bits) {
+    const int b = __ffs(bits) - 1;
+    return (b / 4 * kT + t) * 4 + b % 4;
+  };
+  if (kKind != kI8Rows) {
+    for (; near; near &= near - 1) later.add(turn % kWindow, false, place(near));
+    if (__float_as_uint(top) >= high - (kKind == kI8Silu ? 32u : 0u)) {
+      uint32_t tops = 0u;
 #pragma unroll
-    for (int e = 0; e < kE; ++e)
+      for (int e = 0; e < kE; ++e)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (fabsf(c[e][j] - kMagic) > 126.f) tops |= 1u << (e * 4 + j);
+        for (int j = 0; j < 4; ++j)
+          if (fabsf(c[e][j] - kMagic) > 126.f) tops |= 1u << (e * 4 + j);
+      for (; tops; tops &= tops - 1) later.add(turn % kWindow, true, place(tops));
+    }
   }
   float scale = m / 127.f;
   if (kKind == kI8Norm) scale = m * (1.f / sqrtf(ss / n + a.eps)) / 127.f;
@@ -386,8 +426,16 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     }
   }
   if (t == 0) a.scale[row] = scale;
-  if (kKind == kI8Rows ? near != 0u : RowGroup<kT>::any(near != 0u))
-    codes_again<kKind, kT>(a, row, t, near, tops, m, &sh_most[odd]);
+  if (kKind == kI8Rows) {
+    for (; near; near &= near - 1) {
+      const int i = place(near);
+      q[i] = code_at_border(a.x[row * a.x_stride + i], m);
+    }
+  }
+  }
+  if (kKind != kI8Rows && turn) {
+    const int64_t rows_left = (turn - 1) % kWindow + 1;
+    settle<kKind, kT>(a, later, row - rows_left * step, step, t, sh_d);
   }
 }
 
