@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs
   const int first = blockIdx.x / cs, stride = gridDim.x / cs;
   uint4* ring = few_smem + threadIdx.x;
   const int8_t* x = a.x + min(g, a.n - 1) * a.x_stride;
+  pdl_launch_dependents();
+  pdl_wait();
 
   // the next step to copy: of this CTA's row groups in turn
   int f_group = first, f_step = 0, f_slot = 0;
@@ -152,21 +154,6 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs
   }
 }
 
-cudaError_t launch_clusters(const void* kernel, int cs, unsigned grid, unsigned block, size_t smem, cudaStream_t st, void** args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1] = {};
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
-  return cudaLaunchKernelExC(&cfg, kernel, args);
-}
-
 cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
   constexpr int kMost = kFewDepth * kFewSlot * 16;
   static unsigned long long done = 0;
@@ -189,10 +176,8 @@ cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
   if (const char* f = getenv("FEW")) sscanf(f, "%d,%d", &kw, &cs), groups = (tiles + kFewWarps / kw - 1) / (kFewWarps / kw);
   const int most = kFewCtas / cs, clusters = groups < most ? groups : most;
   const int steps = (pairs + kw * cs - 1) / (kw * cs) * ((groups + clusters - 1) / clusters);
-  I8MatmulArgs args = a;
-  void* p[] = {&args, &kw, &cs, &groups};
-  return launch_clusters(reinterpret_cast<const void*>(k_i8_few), cs, static_cast<unsigned>(clusters * cs), 32 * kFewWarps,
-                         (steps < kFewDepth ? steps : kFewDepth) * kFewSlot * 16, st, p);
+  return launch_pdl_clusters(k_i8_few, static_cast<unsigned>(cs), dim3(static_cast<unsigned>(clusters * cs)), 32 * kFewWarps,
+                             (steps < kFewDepth ? steps : kFewDepth) * kFewSlot * 16, st, a, kw, cs, groups);
 }
 
 // ------------------------------------------------------------ 9 tokens and more
@@ -355,6 +340,9 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_at;
+  // (an image's kernel begins when all before it have ended, so that what is not the image may be read at once)
+  pdl_launch_dependents();
+  if (Cfg::raw_tokens) pdl_wait();
   // this CTA's tiles, and its steps of each
   const int tiles = a.row_tiles * a.token_tiles, rank = blockIdx.x % a.cs, first = blockIdx.x / a.cs, stride = gridDim.x / a.cs;
   const int from = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.cs);
@@ -623,10 +611,8 @@ cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
   if (e == cudaSuccess && Cfg::raw_tokens) e = map_of(a.x, a.n > 1 ? a.x_stride : a.cols, a.n, a.cols, Cfg::K, kTN, &x_map);
   if (e != cudaSuccess) return e;
   const unsigned grid = cs > 1 ? static_cast<unsigned>(tiles * cs) : static_cast<unsigned>(tiles < kSms ? tiles : kSms);
-  if (Cfg::raw_tokens) {
-    void* p[] = {&w_map, &x_map, &b};
-    return launch_clusters(reinterpret_cast<const void*>(k_i8_big<kTN>), cs, grid, Cfg::threads, Cfg::smem, st, p);
-  }
+  if (Cfg::raw_tokens)
+    return launch_pdl_clusters(k_i8_big<kTN>, static_cast<unsigned>(cs), dim3(grid), Cfg::threads, Cfg::smem, st, w_map, x_map, b);
   x_map = w_map;  // not read
   const int64_t threads = static_cast<int64_t>(n16 / 8) * steps * 32;
   k_i8_image<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a.x, a.x_stride, a.n, a.cols, n16, steps,

@@ -242,8 +242,8 @@ struct RowsCfg {
   static constexpr int block = kT < 128 ? 128 : kT;
   static constexpr int inputs = kKind == kI8Rows ? 1 : 2, ahead = kKind == kI8Rows ? 2 : 1;
   static constexpr int smem = block * kE * 16 * inputs * ahead;
-  static constexpr int ctas = kT >= 1024 ? 1 : kT == 512 ? 2 : kT == 256 ? (kE == 4 ? 3 : kKind == kI8Rows ? 5 : 4)
-                              : kE == 4 ? 5 : kKind == kI8Rows ? 8 : 7;
+  static constexpr int ctas = kT >= 1024 ? 1 : kT == 512 ? 2 : kT == 256 ? (kE == 4 ? 3 : kKind == kI8Rows ? 5 : kKind == kI8Norm ? 3 : 4)
+                              : kE == 4 ? 5 : kKind == kI8Rows ? 8 : kKind == kI8Norm ? 6 : 7;
   };
 
 // kT threads a row, kE groups of four elements a thread.  kVec: every row of every tensor
@@ -264,6 +264,8 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
   const int64_t step = static_cast<int64_t>(gridDim.x) * (Cfg::block / kT);
   int64_t row = static_cast<int64_t>(blockIdx.x) * (Cfg::block / kT) + threadIdx.x / kT;
   const bool two = kKind == kI8Silu || (kKind == kI8Norm && a.other);
+  pdl_launch_dependents();
+  pdl_wait();
   // (past a row's end its places hold zeros from here on: copies leave them)
 #pragma unroll
   for (int i = 0; i < Cfg::ahead * Cfg::inputs * kE; ++i)
@@ -449,8 +451,7 @@ cudaError_t launch_rows(const I8RowsArgs& a, bool vec, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   const int per = Cfg::block / kT, blocks = (a.rows + per - 1) / per, most = kSms * Cfg::ctas;
-  kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), Cfg::block, Cfg::smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), Cfg::block, Cfg::smem, st, a);
 }
 
 template <int kKind>
@@ -476,6 +477,8 @@ __global__ void __launch_bounds__(256) k_rows_i8_read(const int8_t* q, int64_t q
                                                       int n, float* out, int64_t out_stride, int groups) {
   // blockIdx.x: kRead groups of four of one row
   constexpr int kRead = 1024;
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t row = blockIdx.x / groups;
   const int first = static_cast<int>(blockIdx.x - row * groups) * kRead;
   const float s = scale[row];
@@ -510,10 +513,8 @@ cudaError_t launch_rows_i8_read(const int8_t* q, int64_t q_stride, const float* 
   const bool vec = n % 4 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                    (rows == 1 || (q_stride % 4 == 0 && out_stride % 4 == 0));
   const int groups = (n + 4095) / 4096;
-  const unsigned grid = static_cast<unsigned>(rows) * groups;
-  if (vec) k_rows_i8_read<true><<<grid, 256, 0, st>>>(q, q_stride, scale, rows, n, out, out_stride, groups);
-  else k_rows_i8_read<false><<<grid, 256, 0, st>>>(q, q_stride, scale, rows, n, out, out_stride, groups);
-  return cudaGetLastError();
+  return launch_pdl(vec ? k_rows_i8_read<true> : k_rows_i8_read<false>, dim3(static_cast<unsigned>(rows) * groups), 256, 0, st, q,
+                    q_stride, scale, rows, n, out, out_stride, groups);
 }
 
 }  // namespace tqd

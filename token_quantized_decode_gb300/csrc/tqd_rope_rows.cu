@@ -23,6 +23,8 @@ template <bool kVec, bool kInter>
 __global__ void __launch_bounds__(256) k_rope_rows(const RopeRowsArgs a, int tokens, int units, int per_head,
                                                    uint32_t mul_units, uint32_t mul_head) {
   constexpr int kAt = 4;
+  pdl_launch_dependents();
+  pdl_wait();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens;
   const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.n - first));
   const int all = here * units, half = a.rotary / 2;
@@ -152,8 +154,7 @@ cudaError_t launch_rope_rows(const RopeRowsArgs& a, bool interleaved, cudaStream
   auto mul = [](int d) { return d > 1 ? static_cast<uint32_t>((1ull << 32) / d + 1) : 0u; };
   const auto kernel = vec ? interleaved ? k_rope_rows<true, true> : k_rope_rows<true, false>
                           : interleaved ? k_rope_rows<false, true> : k_rope_rows<false, false>;
-  kernel<<<grid, 256, 0, st>>>(a, tokens, units, per_head, mul(units), mul(per_head));
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3(grid), 256, 0, st, a, tokens, units, per_head, mul(units), mul(per_head));
 }
 
 }  // namespace tqd
