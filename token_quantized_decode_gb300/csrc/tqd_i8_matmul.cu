@@ -8,8 +8,6 @@
 // they are split, changes nothing.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <stdio.h>
-#include <stdlib.h>
 
 #include "tqd_device.cuh"
 #include "tqd_i8.cuh"
@@ -32,6 +30,14 @@ __device__ __forceinline__ int ld_rank(const int* p, int rank) {
   return v;
 }
 
+__device__ __forceinline__ int4 ld_rank4(const int* p, int rank) {
+  uint32_t at;
+  int4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 // -------------------------------------------------------------- up to 8 tokens
 //
 // A warp takes 16 rows; lane (g, c) = (lane / 4, lane % 4) holds sixteen bytes of rows g and g + 8 and of
@@ -41,11 +47,14 @@ __device__ __forceinline__ int ld_rank(const int* p, int rank) {
 // converted.  Each lane copies its own bytes into a ring of its own, so that no barrier
 // stands between a copy and its use.  A step is 128 columns.  kw warps of a CTA and cs CTAs of a
 // cluster share 16 rows: piece p of the kw cs has the steps p, p + kw cs, ...
-constexpr int kFewMost = 8;
 constexpr int kFewWarps = 8;
-constexpr int kFewCtas = 2 * kSms;
-constexpr int kFewDepth = 4;                     // steps of the ring
-constexpr int kFewSlot = kFewWarps * 32 * 6;     // 16-byte words of one: [half][row g, row g + 8, token][thread]
+// Eight tokens in each of kNT instructions.
+template <int kNT>
+struct FewCfg {
+  static constexpr int lines = 2 + kNT;                     // 16-byte words of a lane and half: rows g and g + 8, tokens g, 8 + g, ...
+  static constexpr int slot = 2 * lines * 32 * kFewWarps;   // of a step: [half][line][thread]
+  static constexpr int depth = kNT == 1 ? 4 : 3;            // steps of the ring
+};
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -54,15 +63,16 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+template <int kNT>
 __global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs a, int kw, int cs, int groups) {
+  using Cfg = FewCfg<kNT>;
   extern __shared__ uint4 few_smem[];
-  __shared__ int sums[kFewWarps][4][32];  // of the warps that share rows
+  __shared__ int sums[kFewWarps][4 * kNT][32];  // of the warps that share rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int share = kFewWarps / kw, part = warp % kw, rank = blockIdx.x % cs, pieces = kw * cs, piece = rank * kw + part;
   const int steps = ((a.cols + 127) / 128 + pieces - 1) / pieces;
   const int first = blockIdx.x / cs, stride = gridDim.x / cs;
   uint4* ring = few_smem + threadIdx.x;
-  const int8_t* x = a.x + min(g, a.n - 1) * a.x_stride;
   pdl_launch_dependents();
   pdl_wait();
 
@@ -73,57 +83,69 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs
       const int r = (f_group * share + warp / kw) * 16 + g, col = (f_step * pieces + piece) * 128 + c * 16;
       const int8_t* w0 = a.w + static_cast<int64_t>(min(r, a.rows - 1)) * a.cols;
       const int8_t* w1 = a.w + static_cast<int64_t>(min(r + 8, a.rows - 1)) * a.cols;
-      uint4* to = ring + f_slot * kFewSlot;
+      uint4* to = ring + f_slot * Cfg::slot;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int at = col + k * 64;
-        const uint32_t size = at < a.cols ? 16 : 0, dst = smem_addr(to + k * (3 * 32 * kFewWarps));
+        const uint32_t size = at < a.cols ? 16 : 0, dst = smem_addr(to + k * (Cfg::lines * 32 * kFewWarps));
         constexpr uint32_t next = 32 * kFewWarps * 16;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(w0 + (size ? at : 0)), "r"(size) : "memory");
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + next), "l"(w1 + (size ? at : 0)), "r"(size) : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 2 * next), "l"(x + (size ? at : 0)),
-                     "r"(g < a.n ? size : 0)
-                     : "memory");
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+          const int j = t * 8 + g;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (2 + t) * next),
+                       "l"(a.x + min(j, a.n - 1) * a.x_stride + (size ? at : 0)), "r"(j < a.n ? size : 0)
+                       : "memory");
+        }
       }
       if (++f_step == steps) f_step = 0, f_group += stride;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (++f_slot == kFewDepth) f_slot = 0;
+    if (++f_slot == Cfg::depth) f_slot = 0;
   };
 #pragma unroll 1
-  for (int i = 0; i < kFewDepth; ++i) fetch();
-  float sx[2];  // scales of this lane's tokens, and (below) of its rows
+  for (int i = 0; i < Cfg::depth; ++i) fetch();
+  float sx[kNT][2];  // scales of this lane's tokens, and (below) of its rows
 #pragma unroll
-  for (int i = 0; i < 2; ++i) sx[i] = __ldg(a.x_scale + min(2 * c + i, a.n - 1));
+  for (int t = 0; t < kNT; ++t)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sx[t][i] = __ldg(a.x_scale + min(t * 8 + 2 * c + i, a.n - 1));
   int slot = 0;
   for (int group = first; group < groups; group += stride) {
     const int r0 = (group * share + warp / kw) * 16 + g;
     const float sw[2] = {__ldg(a.w_scale + min(r0, a.rows - 1)), __ldg(a.w_scale + min(r0 + 8, a.rows - 1))};
-    int total[4] = {0, 0, 0, 0}, other[4] = {0, 0, 0, 0};
+    int total[kNT][4], other[kNT][4];
+#pragma unroll
+    for (int t = 0; t < kNT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) total[t][i] = other[t][i] = 0;
     for (int s = 0; s < steps; ++s) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kFewDepth - 1) : "memory");
-      uint4 v[2][3];
+      asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::depth - 1) : "memory");
+      uint4 v[2][Cfg::lines];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < 3; ++i) v[k][i] = ring[slot * kFewSlot + (k * 3 + i) * 32 * kFewWarps];
-      if (++slot == kFewDepth) slot = 0;
+        for (int i = 0; i < Cfg::lines; ++i) v[k][i] = ring[slot * Cfg::slot + (k * Cfg::lines + i) * 32 * kFewWarps];
+      if (++slot == Cfg::depth) slot = 0;
       fetch();  // into the place just read
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        mma_s8(total, v[k][0].x, v[k][1].x, v[k][0].y, v[k][1].y, v[k][2].x, v[k][2].y);
-        mma_s8(other, v[k][0].z, v[k][1].z, v[k][0].w, v[k][1].w, v[k][2].z, v[k][2].w);
-      }
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+          mma_s8(total[t], v[k][0].x, v[k][1].x, v[k][0].y, v[k][1].y, v[k][2 + t].x, v[k][2 + t].y);
+          mma_s8(other[t], v[k][0].z, v[k][1].z, v[k][0].w, v[k][1].w, v[k][2 + t].z, v[k][2 + t].w);
+        }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) total[e] += other[e];
+    for (int e = 0; e < 4 * kNT; ++e) total[e / 4][e % 4] += other[e / 4][e % 4];
     if (pieces > 1) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sums[warp][e][lane] = total[e];
+      for (int e = 0; e < 4 * kNT; ++e) sums[warp][e][lane] = total[e / 4][e % 4];
       __syncthreads();
       if (cs > 1) {  // the CTA's sums in the place of its first warp's, then the cluster's
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4 * kNT; ++e) {
           if (kw > 1 && e % kw == part) {
             int s = 0;
             for (int w = warp - part; w < warp - part + kw; ++w) s += sums[w][e][lane];
@@ -135,9 +157,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs
     }
     // of the sums of 16 rows, piece p writes every (kw cs)-th
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 4 * kNT; ++e) {
       if (pieces > 1 && e % pieces != piece) continue;
-      int s = total[e];
+      int s = total[e / 4][e % 4];
       if (cs > 1) {
         s = 0;
         for (int q = 0; q < cs; ++q) s += ld_rank(&sums[warp - part][e][lane], q);
@@ -145,8 +167,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs
         s = 0;
         for (int w = warp - part; w < warp - part + kw; ++w) s += sums[w][e][lane];
       }
-      const int r = r0 + (e >> 1) * 8, j = 2 * c + (e & 1);
-      if (r < a.rows && j < a.n) a.y[j * a.y_stride + r] = static_cast<float>(s) * sx[e & 1] * sw[e >> 1];
+      const int r = r0 + ((e & 3) >> 1) * 8, j = (e >> 2) * 8 + 2 * c + (e & 1);
+      if (r < a.rows && j < a.n) a.y[j * a.y_stride + r] = static_cast<float>(s) * sx[e >> 2][e & 1] * sw[(e & 3) >> 1];
     }
     // (no sum is overwritten, nor a CTA's memory gone, while another reads it)
     if (cs > 1) cluster_barrier();
@@ -154,30 +176,32 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs
   }
 }
 
+template <int kNT>
 cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
-  constexpr int kMost = kFewDepth * kFewSlot * 16;
+  using Cfg = FewCfg<kNT>;
+  constexpr int kMost = Cfg::depth * Cfg::slot * 16;
   static unsigned long long done = 0;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_few), kMost, &done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_few<kNT>), kMost, &done);
   if (e != cudaSuccess) return e;
-  // How many warps and CTAs share 16 rows: what makes the busiest CTA's share least.
+  // How many warps and CTAs share 16 rows: what makes the busiest CTA's share least, counted in steps of two CTAs an SM
+  // (an SM's only CTA takes 0.6 of that, a group of rows one more, joining a cluster two).
+  constexpr int kClusters[9] = {0, 304, 152, 97, 74, 58, 46, 38, 36};  // that run at once
   const int tiles = (a.rows + 15) / 16, pairs = (a.cols + 127) / 128;
   int kw = 1, cs = 1, groups = 0;
   float best = 0.f;
-  for (int c = 1; c <= 8; c *= 2) {
-    for (int k = 1; k <= kFewWarps; k *= 2) {
-      const int gr = (tiles + kFewWarps / k - 1) / (kFewWarps / k);
-      const int64_t ctas = static_cast<int64_t>(gr) * c;
-      const int64_t waves = (ctas + kFewCtas / c * c - 1) / (kFewCtas / c * c);
+  for (int c = 1; c <= 8 && c <= pairs; c += c < 4 ? 1 : 2) {
+    for (int k = 1; k <= kFewWarps && (k == 1 || k * c <= pairs); k *= 2) {
+      const int gr = (tiles + kFewWarps / k - 1) / (kFewWarps / k), waves = (gr + kClusters[c] - 1) / kClusters[c];
+      if (c > 1 && waves > 1) break;
       const int steps = (pairs + k * c - 1) / (k * c);
-      const float cost = waves * (steps * (ctas > kFewCtas / 2 ? 1.f : 0.6f) + 1.f) + (c > 1 ? 2.f : 0.f);
+      const float cost = waves * (steps * (static_cast<int64_t>(gr) * c > kSms ? 1.f : 0.6f) + 1.f) + (c > 1 ? 2.f : 0.f);
       if (groups == 0 || cost < best) best = cost, kw = k, cs = c, groups = gr;
     }
   }
-  if (const char* f = getenv("FEW")) sscanf(f, "%d,%d", &kw, &cs), groups = (tiles + kFewWarps / kw - 1) / (kFewWarps / kw);
-  const int most = kFewCtas / cs, clusters = groups < most ? groups : most;
+  const int clusters = groups < kClusters[cs] ? groups : kClusters[cs];
   const int steps = (pairs + kw * cs - 1) / (kw * cs) * ((groups + clusters - 1) / clusters);
-  return launch_pdl_clusters(k_i8_few, static_cast<unsigned>(cs), dim3(static_cast<unsigned>(clusters * cs)), 32 * kFewWarps,
-                             (steps < kFewDepth ? steps : kFewDepth) * kFewSlot * 16, st, a, kw, cs, groups);
+  return launch_pdl_clusters(k_i8_few<kNT>, static_cast<unsigned>(cs), dim3(static_cast<unsigned>(clusters * cs)), 32 * kFewWarps,
+                             (steps < Cfg::depth ? steps : Cfg::depth) * Cfg::slot * 16, st, a, kw, cs, groups);
 }
 
 // ------------------------------------------------------------ 9 tokens and more
@@ -533,14 +557,21 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
     const int row0 = first / a.token_tiles * kBigM, j0 = first % a.token_tiles * kTN, width = min(kTN, a.n - j0);
     int gone = 0;  // a wait ran out in one of the CTAs
     for (int q = 0; q < a.cs; ++q) gone |= ld_rank(&dead_word, q);
-    // token i of the tile by CTA i mod cs: a thread takes one row of it
-    for (int e = threadIdx.x; e < (width - rank + a.cs - 1) / a.cs * kBigM; e += Cfg::threads) {
-      const int i = e / kBigM * a.cs + rank, r = e % kBigM;
-      if (row0 + r >= a.rows) continue;
-      int t = 0;
-      for (int q = 0; q < a.cs; ++q) t += ld_rank(&sums[i * kBigM + r], q);
-      const float v = static_cast<float>(t) * __ldg(a.x_scale + j0 + i) * __ldg(a.w_scale + row0 + r);
-      a.y[(j0 + i) * a.y_stride + row0 + r] = gone ? __uint_as_float(0x7FC00000u) : v;
+    // token i of the tile by CTA i mod cs: a thread takes four rows of it
+    for (int e = threadIdx.x; e < (width - rank + a.cs - 1) / a.cs * (kBigM / 4); e += Cfg::threads) {
+      const int i = e / (kBigM / 4) * a.cs + rank, r = e % (kBigM / 4) * 4;
+      int4 t = ld_rank4(&sums[i * kBigM + r], 0);
+#pragma unroll 4
+      for (int q = 1; q < a.cs; ++q) {
+        const int4 o = ld_rank4(&sums[i * kBigM + r], q);
+        t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
+      }
+      const float sx = gone ? __uint_as_float(0x7FC00000u) : __ldg(a.x_scale + j0 + i);
+      const int v[4] = {t.x, t.y, t.z, t.w};
+      float* y = a.y + (j0 + i) * a.y_stride + row0 + r;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row0 + r + k < a.rows) y[k] = static_cast<float>(v[k]) * sx * __ldg(a.w_scale + row0 + r + k);
     }
     cluster_barrier();
   }
@@ -630,17 +661,36 @@ size_t i8_matmul_scratch_bytes(int rows, int cols, int n) {
 }
 
 cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
-  if (a.n <= kFewMost) return launch_few(a, st);
-  int tn = a.n <= 16 ? 16 : a.n <= 32 ? 32 : a.n <= 64 ? 64 : a.n <= 128 ? 128 : 192, cs = 1;
-  const int64_t tiles = static_cast<int64_t>((a.rows + kBigM - 1) / kBigM) * ((a.n + tn - 1) / tn);
-  const int steps = (a.cols + 127) / 128;
-  while (cs < 8 && tiles * cs * 2 <= kSms && steps >= cs * 2) cs *= 2;
-  if (const char* f = getenv("BIG")) { int t, c; if (sscanf(f, "%d,%d", &t, &c) == 2 && (t <= 64 || a.n > 64)) tn = t, cs = c; }
-  if (tn == 16) return launch_big<16>(a, cs, st);
-  if (tn == 32) return launch_big<32>(a, cs, st);
-  if (tn == 64) return launch_big<64>(a, cs, st);
-  if (tn == 128) return launch_big<128>(a, cs, st);
-  return launch_big<192>(a, cs, st);
+  // Up to 8 tokens: the int8 instructions keep up with memory (151936 x 1024 of 8: 30.3 us, k_i8_big 31.0).  Up to 16 they
+  // do at half the rate, which is faster where a launch and the pipeline's filling are most of the time (4096 x 1024 of 16:
+  // 4.4 and 6.2 us; 5120 x 960 5.9 and 7.0; 4096 x 4096 9.6 and 9.2; 151936 x 1024 45 and 31).
+  if (a.n <= 8) return launch_few<1>(a, st);
+  if (a.n <= 16 && static_cast<int64_t>(a.rows) * a.cols <= (12 << 20)) return launch_few<2>(a, st);
+  // The width of a tile and the CTAs that share one: what takes least by these measured times in ns: 128 columns of a
+  // tile, an image's kernel and a cluster's joining; a tile's beginning and end beside another's steps.
+  constexpr int kWidths[5] = {16, 32, 64, 128, 192}, kStep[5] = {320, 350, 430, 540, 610};
+  constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};  // that run at once
+  const int64_t row_tiles = (a.rows + kBigM - 1) / kBigM, steps = (a.cols + 127) / 128;
+  int64_t best = -1;
+  int way = 0, cs = 1;
+  for (int i = 0; i < 5; ++i) {
+    const int64_t tiles = row_tiles * ((a.n + kWidths[i] - 1) / kWidths[i]);
+    for (int c = 1; c <= 8 && c <= steps; ++c) {
+      if (c > 1 && tiles > kClusters[c]) break;
+      const int64_t waves = (tiles + kClusters[c] - 1) / kClusters[c];
+      const int64_t cost = waves * ((steps + c - 1) / c * kStep[i] + 400) + (kWidths[i] > kRawMost ? 1500 : 0) +
+                           (c > 1 ? 1800 + 8 * kWidths[i] : 0);
+      if (best < 0 || cost < best) best = cost, way = i, cs = c;
+    }
+    if (kWidths[i] >= a.n) break;
+  }
+  switch (way) {
+    case 0: return launch_big<16>(a, cs, st);
+    case 1: return launch_big<32>(a, cs, st);
+    case 2: return launch_big<64>(a, cs, st);
+    case 3: return launch_big<128>(a, cs, st);
+    default: return launch_big<192>(a, cs, st);
+  }
 }
 
 }  // namespace tqd
