@@ -10,6 +10,7 @@ import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libtqd.so")
+CALL_PATH = os.path.join(_HERE, "_build", "_tqd_call.so")
 
 TQD_OK = 0
 STATUS_NAMES = [
@@ -150,6 +151,18 @@ def lib():
         fn.argtypes = args
     _lib = L
     return L
+
+
+def call_module():
+    """The compiled module of the tensor wrappers' common case, not yet bound; raises if it has not been built."""
+    from importlib import machinery, util
+    if not os.path.exists(CALL_PATH):
+        raise ImportError(f"_tqd_call is not built ({CALL_PATH} missing); run __graft_entry__.build() "
+                          "or python token_quantized_decode_gb300/build.py")
+    loader = machinery.ExtensionFileLoader("_tqd_call", CALL_PATH)
+    module = util.module_from_spec(util.spec_from_loader("_tqd_call", loader))
+    loader.exec_module(module)
+    return module
 
 
 def exported_symbols():

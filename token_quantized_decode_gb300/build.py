@@ -10,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtqd.so")
+CALL = os.path.join(BUILD, "_tqd_call.so")
 SYNTH_SRC = os.path.join(ROOT, "synth", "tqd_synth.c")
 
 SOURCES = ["tqd_kernels.cu", "tqd_persist.cu", "tqd_persist_bf16.cu", "tqd_engine.cu", "tqd_ops.cu", "tqd_noalloc.cu", "tqd_batch.cu",
@@ -43,7 +45,7 @@ def _deps_mtime() -> float:
 
 def build(force: bool = False, verbose: bool = False, extra: list | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, CALL)):
         return LIB
     extra = list(extra or [])
     if verbose:
@@ -68,9 +70,21 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
             raise RuntimeError(f"gcc failed for tqd_synth.c:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+    def compile_call():
+        # the tensor wrappers' common case, a CPython module of its own
+        tmp = CALL + f".tmp{os.getpid()}"
+        cmd = ["gcc", "-O2", "-std=gnu11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+               os.path.join(CSRC, "tqd_call.c"), "-o", tmp, "-ldl"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed for tqd_call.c:\n{r.stdout}\n{r.stderr}")
+        return tmp
+
+    with ThreadPoolExecutor(len(SOURCES) + 2) as ex:
         futs = [ex.submit(compile_one, src) for src in SOURCES] + [ex.submit(compile_synth)]
+        call = ex.submit(compile_call)
         results = [f.result() for f in futs]
+        call = call.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -80,6 +94,7 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(call, CALL)
     return LIB
 
 

@@ -5,14 +5,14 @@ from __future__ import annotations
 
 from ctypes import byref
 
-from ._lib import TQDError, check, lib, tqd_kv_q4, tqd_rope_scaling
+from ._lib import LIB_PATH, TQDError, call_module, check, lib, tqd_kv_q4, tqd_rope_scaling
 
 
 torch = None  # bound at the first call (the rest of the package does not need it)
 
 
 def _bind():
-    global torch, _stream_of, _device, _F32, _I32, _U8, _I8
+    global torch, _stream_of, _device, _F32, _I32, _U8, _I8, _call
     import torch as t
     _F32, _I32, _U8, _I8 = t.float32, t.int32, t.uint8, t.int8
     # (without a GPU no tensor is on device 0, and every call is refused)
@@ -20,6 +20,9 @@ def _bind():
     raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
     # the raw handle of the current stream: an eighth of the time that its Stream object takes to make
     _stream_of = raw if raw is not None else lambda d: int(t.cuda.current_stream(d).cuda_stream)
+    lib()  # (says so if it has not been built)
+    _call = call_module()
+    _call.bind(LIB_PATH, _F32, _I32, _U8, _I8, _stream_of, getattr(t._C, "_cuda_getDevice", _device) if t.cuda.is_available() else _device)
     torch = t
 
 
@@ -330,6 +333,9 @@ def tqd_op_logprobs(logits, targets, logprob, entropy, top_ids, top_logprobs, sc
 
 
 # ------------------------------------------------------------------ rows of 8-bit codes, rotation of many rows
+#
+# _call (csrc/tqd_call.c) makes a call whose tensors are of the common form, in half the time that the checks
+# below take; what it does not take, or the library refuses, goes through them.
 
 def _shape(t, where, name):
     """(rows, width) of [rows, width], or of [width] as one row."""
@@ -345,6 +351,10 @@ def _shape(t, where, name):
 
 def tqd_op_rows_i8(x, q, scale, stream=None):
     """Codes of x [rows, n] into q (int8, the same shape), scales into scale [rows]."""
+    if torch is None:
+        _bind()
+    if _call.rows_i8(x, q, scale, stream):
+        return
     where = "tqd_op_rows_i8"
     n, w = _shape(x, where, "x")
     dev = _device()
@@ -359,6 +369,10 @@ def tqd_op_rows_i8(x, q, scale, stream=None):
 def tqd_op_rmsnorm_i8(x, add, g, eps: float, sum_out, q, scale, stream=None):
     """h = x + add [rows, n] (add None: x), kept in sum_out (may be x or add; None: not); codes of its RMSNorm with
     gains g [n] into q, scales into scale."""
+    if torch is None:
+        _bind()
+    if _call.rmsnorm_i8(x, add, g, eps, sum_out, q, scale, stream):
+        return
     where = "tqd_op_rmsnorm_i8"
     n, w = _shape(x, where, "x")
     dev = _device()
@@ -375,6 +389,10 @@ def tqd_op_rmsnorm_i8(x, add, g, eps: float, sum_out, q, scale, stream=None):
 
 def tqd_op_silu_mul_i8(gate, up, q, scale, stream=None):
     """Codes of silu(gate) * up [rows, n] into q, scales into scale (gate and up may be slices of one tensor)."""
+    if torch is None:
+        _bind()
+    if _call.silu_mul_i8(gate, up, q, scale, stream):
+        return
     where = "tqd_op_silu_mul_i8"
     n, w = _shape(gate, where, "gate")
     dev = _device()
@@ -389,6 +407,10 @@ def tqd_op_silu_mul_i8(gate, up, q, scale, stream=None):
 
 def tqd_op_rows_i8_read(q, scale, out, stream=None):
     """The values that rows of codes stand for, f32 [rows, n]."""
+    if torch is None:
+        _bind()
+    if _call.rows_i8_read(q, scale, out, stream):
+        return
     where = "tqd_op_rows_i8_read"
     n, w = _shape(q, where, "q")
     dev = _device()
@@ -407,6 +429,10 @@ def tqd_i8_matmul_scratch_bytes(rows: int, cols: int, n: int) -> int:
 def tqd_op_i8_matmul(w, w_scale, x, x_scale, y, scratch=None, stream=None):
     """y [n, rows] = (x [n, cols] * x_scale [n]) (w [rows, cols] * w_scale [rows])^T over codes.  scratch: uint8 of
     tqd_i8_matmul_scratch_bytes(rows, cols, n) (None where that is 0)."""
+    if torch is None:
+        _bind()
+    if _call.i8_matmul(w, w_scale, x, x_scale, y, scratch, stream):
+        return
     where = "tqd_op_i8_matmul"
     n, cols = _shape(x, where, "x")
     if w.dim() != 2 or w.shape[1] != cols:
@@ -446,6 +472,10 @@ def tqd_op_rope_table_scaled(theta: float, rotary_dim: int, max_pos: int, scalin
 def tqd_op_rope_rows(x, positions, table, head_dim: int, rotary_dim: int, interleaved: bool, out, stream=None):
     """Rotate the first rotary_dim elements of every head of x [n, heads * head_dim] by positions [n] into out (may be
     x).  table: tqd_op_rope_table_scaled's, whole rows of rotary_dim floats."""
+    if torch is None:
+        _bind()
+    if _call.rope_rows(x, positions, table, head_dim, rotary_dim, interleaved, out, stream):
+        return
     where = "tqd_op_rope_rows"
     n, w = _shape(x, where, "x")
     if head_dim <= 0 or w % head_dim or rotary_dim <= 0 or table.numel() % rotary_dim:
