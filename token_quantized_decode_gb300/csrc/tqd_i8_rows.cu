@@ -471,31 +471,51 @@ cudaError_t launch_kind(const I8RowsArgs& a, cudaStream_t st) {
   return launch_rows<kKind, 1024, 4>(a, vec, st);
 }
 
-// The values that rows of codes stand for: four a thread and step.
+// The values that rows of codes stand for: four codes a thread and step, a block's 4096 codes from one row or several
+// short ones (groups: of four codes a row; mul = floor(2^32 / groups) + 1, or 0 for one).
 template <bool kVec>
-__global__ void __launch_bounds__(256) k_rows_i8_read(const int8_t* q, int64_t q_stride, const float* scale, int rows,
-                                                      int n, float* out, int64_t out_stride, int groups) {
-  // blockIdx.x: kRead groups of four of one row
+__global__ void __launch_bounds__(256) k_rows_i8_read(const int8_t* q, int64_t q_stride, const float* scale, int64_t all,
+                                                      int n, float* out, int64_t out_stride, int groups, uint32_t mul) {
   constexpr int kRead = 1024;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t row = blockIdx.x / groups;
-  const int first = static_cast<int>(blockIdx.x - row * groups) * kRead;
-  const float s = scale[row];
-  const int8_t* src = q + row * q_stride;
-  float* dst = out + row * out_stride;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRead, row0 = first / groups;
+  const int skip = static_cast<int>(first - row0 * groups);  // below 4096
+  uint32_t w[kRead / 256];
+  float s[kRead / 256];
 #pragma unroll
   for (int k = 0; k < kRead / 256; ++k) {
-    const int i = (first + k * 256 + static_cast<int>(threadIdx.x)) * 4;
-    if (i >= n) continue;
+    const int f = skip + k * 256 + static_cast<int>(threadIdx.x);
+    const int r = mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(f), mul)) : f;
+    const int64_t row = row0 + r;
+    const int i = (f - r * groups) * 4;
+    if (first + k * 256 + threadIdx.x >= all) continue;
+    s[k] = __ldg(scale + row);
+    const int8_t* src = q + row * q_stride + i;
     if (kVec) {
-      float4 f;
-      i8x4_to_f32(*reinterpret_cast<const uint32_t*>(src + i), f.x, f.y, f.z, f.w);
-      *reinterpret_cast<float4*>(dst + i) = make_float4(f.x * s, f.y * s, f.z * s, f.w * s);
+      w[k] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    } else {
+      w[k] = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < n) w[k] |= static_cast<uint32_t>(static_cast<uint8_t>(src[j])) << (8 * j);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRead / 256; ++k) {
+    const int f = skip + k * 256 + static_cast<int>(threadIdx.x);
+    const int r = mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(f), mul)) : f;
+    const int i = (f - r * groups) * 4;
+    if (first + k * 256 + threadIdx.x >= all) continue;
+    float* dst = out + (row0 + r) * out_stride + i;
+    float v[4];
+    i8x4_to_f32(w[k], v[0], v[1], v[2], v[3]);
+    if (kVec) {
+      *reinterpret_cast<float4*>(dst) = make_float4(v[0] * s[k], v[1] * s[k], v[2] * s[k], v[3] * s[k]);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (i + j < n) dst[i + j] = src[i + j] * s;
+        if (i + j < n) dst[j] = v[j] * s[k];
     }
   }
 }
@@ -512,9 +532,11 @@ cudaError_t launch_rows_i8_read(const int8_t* q, int64_t q_stride, const float* 
                                 int64_t out_stride, cudaStream_t st) {
   const bool vec = n % 4 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                    (rows == 1 || (q_stride % 4 == 0 && out_stride % 4 == 0));
-  const int groups = (n + 4095) / 4096;
-  return launch_pdl(vec ? k_rows_i8_read<true> : k_rows_i8_read<false>, dim3(static_cast<unsigned>(rows) * groups), 256, 0, st, q,
-                    q_stride, scale, rows, n, out, out_stride, groups);
+  const int groups = (n + 3) / 4;
+  const int64_t all = static_cast<int64_t>(rows) * groups;
+  const uint32_t mul = groups > 1 ? static_cast<uint32_t>((1ull << 32) / groups + 1) : 0u;
+  return launch_pdl(vec ? k_rows_i8_read<true> : k_rows_i8_read<false>, dim3(static_cast<unsigned>((all + 1023) / 1024)), 256, 0, st,
+                    q, q_stride, scale, all, n, out, out_stride, groups, mul);
 }
 
 }  // namespace tqd

@@ -15,11 +15,34 @@ __device__ __forceinline__ int div_by(int f, uint32_t mul) {
   return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(f), mul)) : f;
 }
 
-// A unit is eight elements of a head (kVec) or two: two runs of four that turn
-// together (halves), eight neighbours, or what follows the rotated part.  Without
-// kVec: one pair, or one element of the rest.  A block does `tokens` tokens' units,
-// four a thread at a time, so that their loads are under way together.
-template <bool kVec, bool kInter>
+// kW neighbouring floats (of one 4 kW-byte load).
+template <int kW>
+struct Run;
+template <>
+struct Run<4> {
+  using Type = float4;
+};
+template <>
+struct Run<2> {
+  using Type = float2;
+};
+template <>
+struct Run<1> {
+  using Type = float;
+};
+template <int kW>
+__device__ __forceinline__ void get(float (&v)[kW], const float* p) {
+  *reinterpret_cast<typename Run<kW>::Type*>(v) = *reinterpret_cast<const typename Run<kW>::Type*>(p);
+}
+template <int kW>
+__device__ __forceinline__ void put(float* p, const float (&v)[kW]) {
+  *reinterpret_cast<typename Run<kW>::Type*>(p) = *reinterpret_cast<const typename Run<kW>::Type*>(v);
+}
+
+// A unit is 2 kW elements of a head: two runs of kW that turn together (halves), neighbours, or what follows the rotated part
+// (with kW = 1 one element of that).  A block does `tokens` tokens' units, four a thread at a time, so that their loads
+// are under way together.
+template <int kW, bool kInter>
 __global__ void __launch_bounds__(256) k_rope_rows(const RopeRowsArgs a, int tokens, int units, int per_head,
                                                    uint32_t mul_units, uint32_t mul_head) {
   constexpr int kAt = 4;
@@ -42,65 +65,53 @@ __global__ void __launch_bounds__(256) k_rope_rows(const RopeRowsArgs a, int tok
       const int tok = div_by(f, mul_units), u = f - tok * units, head = div_by(u, mul_head), g = u - head * per_head;
       const int pos = a.positions[first + tok];
       if (pos < 0 || pos >= a.max_pos) continue;
-      turn[k] = g < (kVec ? a.rotary / 8 : half);
+      turn[k] = g * kW < half;
       if (!turn[k] && !copies) continue;
       src[k] = a.x + (first + tok) * a.x_stride + static_cast<int64_t>(head) * a.head_dim;
       dst[k] = a.out + (first + tok) * a.out_stride + static_cast<int64_t>(head) * a.head_dim;
-      if (kVec) {
-        i0[k] = turn[k] && !kInter ? 4 * g : 8 * g;
-        i1[k] = turn[k] && !kInter ? half + 4 * g : 8 * g + 4;
+      if (turn[k]) {
+        i0[k] = (kInter ? 2 : 1) * kW * g;
+        i1[k] = kInter ? i0[k] + kW : half + kW * g;
       } else {
-        i0[k] = turn[k] ? (kInter ? 2 * g : g) : half + g;
-        i1[k] = turn[k] ? (kInter ? 2 * g + 1 : half + g) : i0[k];
+        i0[k] = kW == 1 ? half + g : 2 * kW * g;
+        i1[k] = kW == 1 ? i0[k] : i0[k] + kW;
       }
-      // (cos, sin) of the unit's pairs
-      row[k] = reinterpret_cast<const float*>(a.table + static_cast<int64_t>(pos) * half) + (kVec ? 8 : 2) * g;
+      row[k] = reinterpret_cast<const float*>(a.table + static_cast<int64_t>(pos) * half) + 2 * kW * g;  // (cos, sin) of the unit's pairs
     }
-    if (kVec) {
-      float4 p[kAt], q[kAt], c[kAt], s[kAt];
+    float p[kAt][kW], q[kAt][kW], c[kAt][kW], s[kAt][kW];  // c, s: the first and the second half of the pairs
 #pragma unroll
-      for (int k = 0; k < kAt; ++k) {
-        if (!dst[k]) continue;
-        p[k] = *reinterpret_cast<const float4*>(src[k] + i0[k]);
-        q[k] = *reinterpret_cast<const float4*>(src[k] + i1[k]);
-        if (turn[k]) {
-          c[k] = __ldg(reinterpret_cast<const float4*>(row[k]));
-          s[k] = __ldg(reinterpret_cast<const float4*>(row[k]) + 1);
+    for (int k = 0; k < kAt; ++k) {
+      if (!dst[k]) continue;
+      get<kW>(p[k], src[k] + i0[k]);
+      get<kW>(q[k], src[k] + i1[k]);
+      if (turn[k]) {
+        get<kW>(c[k], row[k]);
+        get<kW>(s[k], row[k] + kW);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) {
+      if (!dst[k]) continue;
+      float t[2 * kW], u[kW], w[kW];  // the pairs' (cos, sin); what becomes of p and q
+#pragma unroll
+      for (int i = 0; i < kW; ++i) t[i] = c[k][i], t[kW + i] = s[k][i], u[i] = p[k][i], w[i] = q[k][i];
+      if (turn[k] && (!kInter || kW == 1)) {
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+          u[i] = p[k][i] * t[2 * i] - q[k][i] * t[2 * i + 1];
+          w[i] = q[k][i] * t[2 * i] + p[k][i] * t[2 * i + 1];
+        }
+      } else if (turn[k]) {
+#pragma unroll
+        for (int i = 0; i + 1 < kW; i += 2) {
+          u[i] = p[k][i] * t[i] - p[k][i + 1] * t[i + 1];
+          u[i + 1] = p[k][i + 1] * t[i] + p[k][i] * t[i + 1];
+          w[i] = q[k][i] * t[kW + i] - q[k][i + 1] * t[kW + i + 1];
+          w[i + 1] = q[k][i + 1] * t[kW + i] + q[k][i] * t[kW + i + 1];
         }
       }
-#pragma unroll
-      for (int k = 0; k < kAt; ++k) {
-        if (!dst[k]) continue;
-        float4 u = p[k], w = q[k];
-        if (turn[k] && !kInter) {
-          u = make_float4(p[k].x * c[k].x - q[k].x * c[k].y, p[k].y * c[k].z - q[k].y * c[k].w,
-                          p[k].z * s[k].x - q[k].z * s[k].y, p[k].w * s[k].z - q[k].w * s[k].w);
-          w = make_float4(q[k].x * c[k].x + p[k].x * c[k].y, q[k].y * c[k].z + p[k].y * c[k].w,
-                          q[k].z * s[k].x + p[k].z * s[k].y, q[k].w * s[k].z + p[k].w * s[k].w);
-        } else if (turn[k]) {
-          u = make_float4(p[k].x * c[k].x - p[k].y * c[k].y, p[k].y * c[k].x + p[k].x * c[k].y,
-                          p[k].z * c[k].z - p[k].w * c[k].w, p[k].w * c[k].z + p[k].z * c[k].w);
-          w = make_float4(q[k].x * s[k].x - q[k].y * s[k].y, q[k].y * s[k].x + q[k].x * s[k].y,
-                          q[k].z * s[k].z - q[k].w * s[k].w, q[k].w * s[k].z + q[k].z * s[k].w);
-        }
-        *reinterpret_cast<float4*>(dst[k] + i0[k]) = u;
-        *reinterpret_cast<float4*>(dst[k] + i1[k]) = w;
-      }
-    } else {
-      float p[kAt], q[kAt], c[kAt], s[kAt];
-#pragma unroll
-      for (int k = 0; k < kAt; ++k) {
-        if (!dst[k]) continue;
-        p[k] = src[k][i0[k]];
-        q[k] = src[k][i1[k]];
-        if (turn[k]) c[k] = __ldg(row[k]), s[k] = __ldg(row[k] + 1);
-      }
-#pragma unroll
-      for (int k = 0; k < kAt; ++k) {
-        if (!dst[k]) continue;
-        dst[k][i0[k]] = turn[k] ? p[k] * c[k] - q[k] * s[k] : p[k];
-        if (turn[k]) dst[k][i1[k]] = q[k] * c[k] + p[k] * s[k];
-      }
+      put<kW>(dst[k] + i0[k], u);
+      if (kW > 1 || turn[k]) put<kW>(dst[k] + i1[k], w);
     }
   }
 }
@@ -142,18 +153,23 @@ cudaError_t launch_rope_table_scaled(double theta, int rotary, int max_pos, cons
 }
 
 cudaError_t launch_rope_rows(const RopeRowsArgs& a, bool interleaved, cudaStream_t st) {
-  auto on16 = [&](const float* p, int64_t stride) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.n == 1 || stride % 4 == 0);
+  // the widest run that head sizes, strides and addresses allow
+  auto fits = [&](int w) {
+    auto on = [&](const float* p, int64_t stride) {
+      return reinterpret_cast<uintptr_t>(p) % (4 * w) == 0 && (a.n == 1 || stride % w == 0);
+    };
+    return a.head_dim % (2 * w) == 0 && a.rotary % (2 * w) == 0 && on(a.x, a.x_stride) && on(a.out, a.out_stride) &&
+           reinterpret_cast<uintptr_t>(a.table) % (4 * w) == 0;
   };
-  const bool vec = a.head_dim % 8 == 0 && a.rotary % 8 == 0 && on16(a.x, a.x_stride) && on16(a.out, a.out_stride) &&
-                   reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
-  const int per_head = vec ? a.head_dim / 8 : a.rotary / 2 + (a.head_dim - a.rotary);
+  const int w = fits(4) ? 4 : fits(2) ? 2 : 1;
+  const int per_head = w > 1 ? a.head_dim / (2 * w) : a.rotary / 2 + (a.head_dim - a.rotary);
   const int units = a.heads * per_head;
   const int tokens = units >= 1024 ? 1 : 1024 / units;
   const unsigned grid = static_cast<unsigned>((a.n + tokens - 1) / tokens);
   auto mul = [](int d) { return d > 1 ? static_cast<uint32_t>((1ull << 32) / d + 1) : 0u; };
-  const auto kernel = vec ? interleaved ? k_rope_rows<true, true> : k_rope_rows<true, false>
-                          : interleaved ? k_rope_rows<false, true> : k_rope_rows<false, false>;
+  const auto kernel = w == 4   ? interleaved ? k_rope_rows<4, true> : k_rope_rows<4, false>
+                      : w == 2 ? interleaved ? k_rope_rows<2, true> : k_rope_rows<2, false>
+                               : interleaved ? k_rope_rows<1, true> : k_rope_rows<1, false>;
   return launch_pdl(kernel, dim3(grid), 256, 0, st, a, tokens, units, per_head, mul(units), mul(per_head));
 }
 
