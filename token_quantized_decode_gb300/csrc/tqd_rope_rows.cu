@@ -40,79 +40,61 @@ __device__ __forceinline__ void put(float* p, const float (&v)[kW]) {
 }
 
 // A unit is 2 kW elements of a head: two runs of kW that turn together (halves), neighbours, or what follows the rotated part
-// (with kW = 1 one element of that).  A block does `tokens` tokens' units, four a thread at a time, so that their loads
-// are under way together.
+// (with kW = 1 one element of that).  A thread does one at a time, in few registers, so that an SM holds 2048 threads: that
+// many 16-byte loads are under way (8191 tokens of 20 heads of 128: 28.2 us, 90 % of the copy rate; with four units a
+// thread at once, half as many threads, 34.7).
 template <int kW, bool kInter>
-__global__ void __launch_bounds__(256) k_rope_rows(const RopeRowsArgs a, int tokens, int units, int per_head,
-                                                   uint32_t mul_units, uint32_t mul_head) {
-  constexpr int kAt = 4;
+__global__ void __launch_bounds__(256, 8) k_rope_rows(const RopeRowsArgs a, int tokens, int units, int per_head,
+                                                      uint32_t mul_units, uint32_t mul_head) {
   pdl_launch_dependents();
   pdl_wait();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens;
-  const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.n - first));
-  const int all = here * units, half = a.rotary / 2;
-  const bool copies = a.out != a.x;
-  for (int f0 = threadIdx.x; f0 < all; f0 += 256 * kAt) {
-    const float *src[kAt], *row[kAt];
-    float* dst[kAt];
-    int i0[kAt], i1[kAt];
-    bool turn[kAt];
+  const int all = static_cast<int>(min(static_cast<int64_t>(tokens), a.n - first)) * units, half = a.rotary / 2;
+  for (int f = threadIdx.x; f < all; f += 256) {
+    const int tok = div_by(f, mul_units), u = f - tok * units, head = div_by(u, mul_head), g = u - head * per_head;
+    const bool turn = g * kW < half;
+    if (!turn && a.out == a.x) continue;
+    const int pos = __ldg(a.positions + first + tok);
+    if (pos < 0 || pos >= a.max_pos) continue;
+    // where the unit's two runs begin
+    const int i0 = turn ? (kInter ? 2 : 1) * kW * g : kW == 1 ? half + g : 2 * kW * g;
+    const int i1 = turn ? kInter ? i0 + kW : half + kW * g : kW == 1 ? i0 : i0 + kW;
+    const float* src = a.x + (first + tok) * a.x_stride + head * a.head_dim;
+    float* dst = a.out + (first + tok) * a.out_stride + head * a.head_dim;
+    float p[kW], q[kW], r[kW], w[kW];
+    get<kW>(p, src + i0);
+    get<kW>(q, src + i1);
+    if (turn) {
+      const float* row = reinterpret_cast<const float*>(a.table + static_cast<int64_t>(pos) * half) + 2 * kW * g;
+      float t[2 * kW];  // (cos, sin) of the unit's pairs
 #pragma unroll
-    for (int k = 0; k < kAt; ++k) {
-      const int f = f0 + k * 256;
-      src[k] = nullptr, row[k] = nullptr, dst[k] = nullptr, turn[k] = false, i0[k] = i1[k] = 0;
-      if (f >= all) continue;
-      const int tok = div_by(f, mul_units), u = f - tok * units, head = div_by(u, mul_head), g = u - head * per_head;
-      const int pos = a.positions[first + tok];
-      if (pos < 0 || pos >= a.max_pos) continue;
-      turn[k] = g * kW < half;
-      if (!turn[k] && !copies) continue;
-      src[k] = a.x + (first + tok) * a.x_stride + static_cast<int64_t>(head) * a.head_dim;
-      dst[k] = a.out + (first + tok) * a.out_stride + static_cast<int64_t>(head) * a.head_dim;
-      if (turn[k]) {
-        i0[k] = (kInter ? 2 : 1) * kW * g;
-        i1[k] = kInter ? i0[k] + kW : half + kW * g;
-      } else {
-        i0[k] = kW == 1 ? half + g : 2 * kW * g;
-        i1[k] = kW == 1 ? i0[k] : i0[k] + kW;
+      for (int h = 0; h < 2; ++h) {
+        float c[kW];
+        get<kW>(c, row + h * kW);
+#pragma unroll
+        for (int i = 0; i < kW; ++i) t[h * kW + i] = c[i];
       }
-      row[k] = reinterpret_cast<const float*>(a.table + static_cast<int64_t>(pos) * half) + 2 * kW * g;  // (cos, sin) of the unit's pairs
-    }
-    float p[kAt][kW], q[kAt][kW], c[kAt][kW], s[kAt][kW];  // c, s: the first and the second half of the pairs
-#pragma unroll
-    for (int k = 0; k < kAt; ++k) {
-      if (!dst[k]) continue;
-      get<kW>(p[k], src[k] + i0[k]);
-      get<kW>(q[k], src[k] + i1[k]);
-      if (turn[k]) {
-        get<kW>(c[k], row[k]);
-        get<kW>(s[k], row[k] + kW);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kAt; ++k) {
-      if (!dst[k]) continue;
-      float t[2 * kW], u[kW], w[kW];  // the pairs' (cos, sin); what becomes of p and q
-#pragma unroll
-      for (int i = 0; i < kW; ++i) t[i] = c[k][i], t[kW + i] = s[k][i], u[i] = p[k][i], w[i] = q[k][i];
-      if (turn[k] && (!kInter || kW == 1)) {
+      if (!kInter || kW == 1) {
 #pragma unroll
         for (int i = 0; i < kW; ++i) {
-          u[i] = p[k][i] * t[2 * i] - q[k][i] * t[2 * i + 1];
-          w[i] = q[k][i] * t[2 * i] + p[k][i] * t[2 * i + 1];
+          r[i] = p[i] * t[2 * i] - q[i] * t[2 * i + 1];
+          w[i] = q[i] * t[2 * i] + p[i] * t[2 * i + 1];
         }
-      } else if (turn[k]) {
+      } else {
 #pragma unroll
         for (int i = 0; i + 1 < kW; i += 2) {
-          u[i] = p[k][i] * t[i] - p[k][i + 1] * t[i + 1];
-          u[i + 1] = p[k][i + 1] * t[i] + p[k][i] * t[i + 1];
-          w[i] = q[k][i] * t[kW + i] - q[k][i + 1] * t[kW + i + 1];
-          w[i + 1] = q[k][i + 1] * t[kW + i] + q[k][i] * t[kW + i + 1];
+          r[i] = p[i] * t[i] - p[i + 1] * t[i + 1];
+          r[i + 1] = p[i + 1] * t[i] + p[i] * t[i + 1];
+          w[i] = q[i] * t[kW + i] - q[i + 1] * t[kW + i + 1];
+          w[i + 1] = q[i + 1] * t[kW + i] + q[i] * t[kW + i + 1];
         }
       }
-      put<kW>(dst[k] + i0[k], u);
-      if (kW > 1 || turn[k]) put<kW>(dst[k] + i1[k], w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kW; ++i) r[i] = p[i], w[i] = q[i];
     }
+    put<kW>(dst + i0, r);
+    if (kW > 1 || turn) put<kW>(dst + i1, w);
   }
 }
 
@@ -164,7 +146,7 @@ cudaError_t launch_rope_rows(const RopeRowsArgs& a, bool interleaved, cudaStream
   const int w = fits(4) ? 4 : fits(2) ? 2 : 1;
   const int per_head = w > 1 ? a.head_dim / (2 * w) : a.rotary / 2 + (a.head_dim - a.rotary);
   const int units = a.heads * per_head;
-  const int tokens = units >= 1024 ? 1 : 1024 / units;
+  const int tokens = units >= 256 ? 1 : 256 / units;
   const unsigned grid = static_cast<unsigned>((a.n + tokens - 1) / tokens);
   auto mul = [](int d) { return d > 1 ? static_cast<uint32_t>((1ull << 32) / d + 1) : 0u; };
   const auto kernel = w == 4   ? interleaved ? k_rope_rows<4, true> : k_rope_rows<4, false>
