@@ -215,22 +215,23 @@ cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
 // after every 8 steps (1024 columns) and add them up as whole numbers; they write a tile's results
 // while the next one's sums are made.  Where there are few tiles a cluster of cs CTAs shares a
 // tile's steps, and each adds up and writes a part of its tokens.
-constexpr int kBigM = 128, kImageK = 64;
+constexpr int kBigM = 128, kImageK = 128;
 constexpr int kConverters = 2;               // groups of four warps
 
-template <int kTN>
+template <int kTN, bool kPair>
 struct BigCfg {
   static constexpr bool raw_tokens = kTN <= 64;
   static constexpr int K = raw_tokens ? 128 : kImageK;       // columns of a step
   static constexpr int run = 1024 / K;                       // steps that the f32 sums hold
-  static constexpr int readers = kTN <= 32 ? 4 : kTN <= 128 ? 8 : 16;  // warps that read sums (TN 192: 48 columns each)
+  static constexpr int readers = kTN <= 32 ? 4 : kTN <= 128 ? 8 : 16;  // warps that read sums (TN 160: 48 columns each)
   static constexpr int threads = 32 * (4 + 4 * kConverters + readers);  // copies, MMAs, two idle; then these
   static constexpr uint32_t w_raw = kBigM * K;               // bytes of the rows' codes in a stage
-  static constexpr uint32_t image = kTN * K * 2;                 // bytes of f16 tokens in a stage
+  static constexpr int ctas = kPair ? 2 : 1;                 // that make a tile's products together
+  static constexpr uint32_t image = kTN / ctas * K * 2;                 // bytes of f16 tokens in a stage
   static constexpr uint32_t raw = raw_tokens ? kTN * K : 0;       // bytes of their codes
   static constexpr uint32_t stage = w_raw + image + raw;
-  static constexpr int stages = kTN == 192 ? 6 : kTN == 128 ? 8 : kTN == 64 ? 5 : 7;
-  static constexpr int a_stages = kTN == 192 ? 4 : stages;  // of operand A, K / 2 columns each
+  static constexpr int stages = kPair ? 6 : kTN >= 128 ? 4 : kTN == 64 ? 5 : 7;
+  static constexpr int a_stages = kPair ? 3 : stages;  // of operand A, K / 2 columns each
   static constexpr uint32_t a_col = 2 * kTN;                // behind two accumulators, in turn
   static constexpr size_t smem = stages * stage + 1024;
   static_assert(a_col + a_stages * K / 2 <= 512, "tensor memory");
@@ -246,16 +247,48 @@ __device__ __forceinline__ uint64_t image_desc(const void* p) {
   return d | (1ull << 46);
 }
 
+// The products of 16 columns: operand A in tensor memory, B in shared memory; of a pair of CTAs, each with its own
+// 128 rows of A and sums, and its half of B.
+template <bool kPair>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add)
-      : "memory");
+  if (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
 }
+// An arrival at `bar` (of both CTAs of a pair) once the thread's products so far are over.
+template <bool kPair>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+  if (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc(uint32_t* at) {
+  if (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(at)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(at)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_free(uint32_t at) {
+  if (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(at) : "memory");
+  else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(at) : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&v)[32]) {
   asm volatile(
@@ -267,13 +300,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&v)[32]) 
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at)
-      : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at)
+               : "memory");
 }
 // A box of K bytes a row at (col, row): 16-byte pieces turned as swizzle 128B (64B for 64) does.
 __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int col, int row, uint64_t* bar) {
@@ -284,9 +315,17 @@ __device__ __forceinline__ void copy_box(void* dst, const CUtensorMap* map, int 
       : "memory");
 }
 // Whether a phase is over, without waiting.
+template <bool kPair>
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
+  if (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
       "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_addr(bar)), "r"(parity)
@@ -299,16 +338,35 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+// An arrival at the barrier, of a pair at the first CTA's.
+template <bool kPair>
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+  if (kPair) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(bar)));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+  } else {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+  }
 }
 
 // Wait for a phase; false once any wait of the CTA ran out of time (which *dead says).  The
 // timer takes longer to read than most waits last: it is read after 64 tries, and then every 64.
+// (kPair: what the other CTA did before it arrived is seen too.)
+template <bool kPair = false>
 __device__ __forceinline__ bool big_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    uint32_t ok;
+    if (kPair)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_addr(bar)), "r"(parity)
+          : "memory");
+    else
+      ok = mbar_try_wait(bar, parity);
+    if (ok) return true;
     if (i % 64) continue;
     if (*dead) return false;
     const uint64_t now = global_timer_ns();
@@ -328,10 +386,10 @@ struct BigArgs {
   int rows, cols, n, n16, steps, row_tiles, token_tiles, cs;
 };
 
-template <int kTN>
-__global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
+template <int kTN, bool kPair>
+__global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
     k_i8_big(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map, const BigArgs a) {
-  using Cfg = BigCfg<kTN>;
+  using Cfg = BigCfg<kTN, kPair>;
   extern __shared__ uint8_t big_smem[];
   __shared__ uint64_t full[Cfg::stages], ready[Cfg::stages], empty[Cfg::stages], sums_full[2], sums_empty[2], done;
   __shared__ uint32_t tmem_at;
@@ -345,40 +403,41 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&ready[s], 4);
+      mbar_init(&ready[s], 4 * Cfg::ctas);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sums_full[i], 1);
-      mbar_init(&sums_empty[i], Cfg::readers);
+      mbar_init(&sums_empty[i], Cfg::readers * Cfg::ctas);
     }
     mbar_init(&done, 1);
     dead_word = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_at)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tmem_alloc<kPair>(&tmem_at);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  if (kPair) cluster_barrier();  // the other CTA's barriers too
+  else __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_at;
   // (an image's kernel begins when all before it have ended, so that what is not the image may be read at once)
   pdl_launch_dependents();
   if (Cfg::raw_tokens) pdl_wait();
   // this CTA's tiles, and its steps of each
-  const int tiles = a.row_tiles * a.token_tiles, rank = blockIdx.x % a.cs, first = blockIdx.x / a.cs, stride = gridDim.x / a.cs;
-  const int from = static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.cs);
-  const int steps = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / a.cs) - from;
+  // (of a pair's 256 rows each has 128, and half of the tokens' image; the first one issues the products)
+  const int cluster = kPair ? 2 : a.cs, rank = blockIdx.x % cluster, first = blockIdx.x / cluster, stride = gridDim.x / cluster;
+  const int tiles = a.row_tiles * a.token_tiles, upper = kPair ? rank * kBigM : 0;
+  const int from = kPair ? 0 : static_cast<int>(static_cast<int64_t>(a.steps) * rank / a.cs);
+  const int steps = kPair ? a.steps : static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / a.cs) - from;
 
   if (warp == 0) {
     int s = 0, issued = 0;
     uint32_t phase = 0;
     bool image_there = Cfg::raw_tokens, ok = true;
     for (int tile = first; ok && tile < tiles; tile += stride) {
-      const int row0 = tile / a.token_tiles * kBigM, j0 = tile % a.token_tiles * kTN;
-      const uint32_t bytes = Cfg::raw_tokens ? Cfg::raw : min(kTN, a.n16 - j0) * Cfg::K * 2;
+      const int row0 = tile / a.token_tiles * (kBigM * Cfg::ctas) + upper, j0 = tile % a.token_tiles * kTN;
+      const int share = min(kTN, a.n16 - j0) / Cfg::ctas, mine = j0 + (kPair ? rank * share : 0);  // tokens of the image
+      const uint32_t bytes = Cfg::raw_tokens ? Cfg::raw : share * Cfg::K * 2;
       for (int k = from; k < from + steps; ++k) {
         if (issued >= Cfg::stages) ok = __all_sync(0xFFFFFFFFu, big_wait(&empty[s], phase ^ 1, dead));
         if (!ok) break;
@@ -389,7 +448,7 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
             copy_box(raw_x + s * Cfg::raw, &x_map, k * Cfg::K, j0, &full[s]);
           } else {
             if (!image_there) pdl_wait();  // the kernel before this one writes the image
-            bulk_g2s(tokens + s * Cfg::image, a.image + (static_cast<int64_t>(k) * a.n16 + j0) * (Cfg::K * 2), bytes, &full[s]);
+            bulk_g2s(tokens + s * Cfg::image, a.image + (static_cast<int64_t>(k) * a.n16 + mine) * (Cfg::K * 2), bytes, &full[s]);
           }
         }
         image_there = true;
@@ -405,22 +464,22 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
   } else if (warp == 1) {
     // One thread, which looks for the next stage while this one's MMAs are issued: the tensor cores hold one or two
     // waiting instructions only, so whatever stands between two steps is time that they lack.
-    if (elect_one()) {
+    if ((!kPair || rank == 0) && elect_one()) {
       int s = 0, at = 0, run = 0;
       uint32_t phase = 0;
       bool ok = true, there = false;
       const uint64_t desc = image_desc<Cfg::K>(tokens);
       for (int tile = first; ok && tile < tiles; tile += stride) {
         const int width = min(kTN, a.n16 - tile % a.token_tiles * kTN);
-        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kBigM >> 4) << 24);
+        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kBigM * Cfg::ctas >> 4) << 24);
         int left = (a.cols - from * Cfg::K) / 16;  // instructions of 16 columns (more than this CTA's where others follow)
         for (int k0 = 0; ok && k0 < steps; k0 += Cfg::run, ++run) {
           const uint32_t d = tmem + (run & 1) * kTN;
-          if (run >= 2) ok = big_wait(&sums_empty[run & 1], (run / 2 - 1) & 1, dead);
+          if (run >= 2) ok = big_wait<kPair>(&sums_empty[run & 1], (run / 2 - 1) & 1, dead);
           const int end = min(steps, k0 + Cfg::run);
           for (int k = k0; ok && k < end; ++k, left -= Cfg::K / 16) {
             // (ready follows full: the converting warps waited for that)
-            if (!there && !big_wait(&ready[s], phase, dead)) {
+            if (!there && !big_wait<kPair>(&ready[s], phase, dead)) {
               ok = false;
               break;
             }
@@ -430,19 +489,19 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
             uint64_t* over = &empty[s];
             if (++s == Cfg::stages) s = 0, phase ^= 1;
             if (++at == Cfg::a_stages) at = 0;
-            there = mbar_test(&ready[s], phase);
+            there = mbar_test<kPair>(&ready[s], phase);
             if (left >= Cfg::K / 16) {
 #pragma unroll
-              for (int i = 0; i < Cfg::K / 16; ++i) mma_ts(d, ad + i * 8, bd + i * 16, idesc, k > k0 || i > 0);
+              for (int i = 0; i < Cfg::K / 16; ++i) mma_ts<kPair>(d, ad + i * 8, bd + i * 16, idesc, k > k0 || i > 0);
             } else {
-              for (int i = 0; i < left; ++i) mma_ts(d, ad + i * 8, bd + i * 16, idesc, k > k0 || i > 0);
+              for (int i = 0; i < left; ++i) mma_ts<kPair>(d, ad + i * 8, bd + i * 16, idesc, k > k0 || i > 0);
             }
-            mma_commit(over);
+            mma_commit<kPair>(over);
           }
-          if (ok) mma_commit(&sums_full[run & 1]);
+          if (ok) mma_commit<kPair>(&sums_full[run & 1]);
         }
       }
-      mma_commit(&done);  // tensor memory is given back once every MMA is over
+      mma_commit<kPair>(&done);  // tensor memory is given back once every MMA is over
       mbar_wait_bounded(&done, 0, nullptr, kWaitLimitNs / 4);
     }
   } else if (warp >= 4 && warp < 4 + 4 * kConverters) {
@@ -495,7 +554,7 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ready[s]);
+      if (lane == 0) mbar_arrive<kPair>(&ready[s]);
     }
   } else if (warp >= 4 + 4 * kConverters) {
     constexpr int kCols = kTN / (Cfg::readers / 4);  // a warp's columns
@@ -503,7 +562,7 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     int run = 0;
     for (int tile = first; tile < tiles; tile += stride) {
-      const int row = tile / a.token_tiles * kBigM + quad * 32 + lane, j0 = tile % a.token_tiles * kTN;
+      const int row = tile / a.token_tiles * (kBigM * Cfg::ctas) + upper + quad * 32 + lane, j0 = tile % a.token_tiles * kTN;
       const int width = min(kTN, a.n16 - j0);
       const float sw = row < a.rows ? a.w_scale[row] : 0.f;
       int total[kCols];
@@ -515,19 +574,19 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
         ok = __all_sync(0xFFFFFFFFu, big_wait(&sums_full[b], (run / 2) & 1, dead)) && ok;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
+        for (int c = 0; c < kCols; c += 8) {
           if (c0 + c >= width) continue;
-          uint32_t r[16];
-          tmem_ld16(tmem + b * kTN + c0 + c + lanes, r);
+          uint32_t r[8];
+          tmem_ld8(tmem + b * kTN + c0 + c + lanes, r);
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-          for (int i = 0; i < 16; ++i) total[c + i] += __float2int_rn(__uint_as_float(r[i]));
+          for (int i = 0; i < 8; ++i) total[c + i] += __float2int_rn(__uint_as_float(r[i]));
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sums_empty[b]);
+        if (lane == 0) mbar_arrive<kPair>(&sums_empty[b]);
       }
-      if (a.cs > 1) {  // the stages are done with: the only tile's sums take their place, [token][row]
+      if (!kPair && a.cs > 1) {  // the stages are done with: the only tile's sums take their place, [token][row]
         int* sums = reinterpret_cast<int*>(raw);
 #pragma unroll
         for (int i = 0; i < kCols; ++i) sums[(c0 + i) * kBigM + quad * 32 + lane] = total[i];
@@ -546,12 +605,13 @@ __global__ void __launch_bounds__(BigCfg<kTN>::threads, 1)
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  if (kPair) cluster_barrier();  // (and nothing arrives at a CTA that is gone)
+  else __syncthreads();
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    tmem_free<kPair>(tmem);
   }
-  if (a.cs > 1) {
+  if (!kPair && a.cs > 1) {
     cluster_barrier();
     const int* sums = reinterpret_cast<const int*>(raw);
     const int row0 = first / a.token_tiles * kBigM, j0 = first % a.token_tiles * kTN, width = min(kTN, a.n - j0);
@@ -583,8 +643,8 @@ __global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_str
                                                   uint8_t* image) {
   pdl_launch_dependents();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int j8 = static_cast<int>(at & 7), c = static_cast<int>((at >> 3) & 3);
-  const int64_t rest = at >> 5;  // (token group, step), the step first
+  const int j8 = static_cast<int>(at & 7), c = static_cast<int>((at >> 3) & 7);
+  const int64_t rest = at >> 6;  // (token group, step), the step first
   const int k = static_cast<int>(rest % steps);
   const int64_t group = rest / steps;
   if (group * 8 >= n16) return;
@@ -627,30 +687,31 @@ cudaError_t map_of(const int8_t* p, int64_t stride, int rows, int cols, int box_
 
 constexpr int kRawMost = 64;  // tokens that k_i8_big takes as codes
 
-template <int kTN>
+template <int kTN, bool kPair = false>
 cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
-  using Cfg = BigCfg<kTN>;
+  using Cfg = BigCfg<kTN, kPair>;
   static unsigned long long done = 0;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_big<kTN>), Cfg::smem, &done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_big<kTN, kPair>), Cfg::smem, &done);
   if (e != cudaSuccess) return e;
   const int steps = (a.cols + Cfg::K - 1) / Cfg::K, n16 = (a.n + 15) / 16 * 16;
   BigArgs b{static_cast<const uint8_t*>(a.scratch), a.x_scale, a.w_scale, a.y, a.y_stride, a.rows, a.cols, a.n, n16, steps,
-            (a.rows + kBigM - 1) / kBigM, (a.n + kTN - 1) / kTN, cs};
+            (a.rows + kBigM * Cfg::ctas - 1) / (kBigM * Cfg::ctas), (a.n + kTN - 1) / kTN, cs};
   const int64_t tiles = static_cast<int64_t>(b.row_tiles) * b.token_tiles;
   CUtensorMap w_map, x_map;
   e = map_of(a.w, a.cols, a.rows, a.cols, Cfg::K, kBigM, &w_map);
   if (e == cudaSuccess && Cfg::raw_tokens) e = map_of(a.x, a.n > 1 ? a.x_stride : a.cols, a.n, a.cols, Cfg::K, kTN, &x_map);
   if (e != cudaSuccess) return e;
-  const unsigned grid = cs > 1 ? static_cast<unsigned>(tiles * cs) : static_cast<unsigned>(tiles < kSms ? tiles : kSms);
+  constexpr int kOnce = kSms / Cfg::ctas;  // tiles that are made at once
+  const unsigned grid = static_cast<unsigned>(cs > 1 ? tiles * cs : (tiles < kOnce ? tiles : kOnce) * Cfg::ctas);
   if (Cfg::raw_tokens)
-    return launch_pdl_clusters(k_i8_big<kTN>, static_cast<unsigned>(cs), dim3(grid), Cfg::threads, Cfg::smem, st, w_map, x_map, b);
+    return launch_pdl_clusters(k_i8_big<kTN, kPair>, static_cast<unsigned>(kPair ? 2 : cs), dim3(grid), Cfg::threads, Cfg::smem, st, w_map, x_map, b);
   x_map = w_map;  // not read
-  const int64_t threads = static_cast<int64_t>(n16 / 8) * steps * 32;
+  const int64_t threads = static_cast<int64_t>(n16 / 8) * steps * 64;
   k_i8_image<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a.x, a.x_stride, a.n, a.cols, n16, steps,
                                                                            static_cast<uint8_t*>(a.scratch));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(k_i8_big<kTN>, static_cast<unsigned>(cs), dim3(grid), Cfg::threads, Cfg::smem, st, w_map, x_map, b);
+  return launch_pdl_clusters(k_i8_big<kTN, kPair>, static_cast<unsigned>(kPair ? 2 : cs), dim3(grid), Cfg::threads, Cfg::smem, st, w_map, x_map, b);
 }
 
 }  // namespace
@@ -667,19 +728,20 @@ cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
   if (a.n <= 8) return launch_few<1>(a, st);
   if (a.n <= 16 && static_cast<int64_t>(a.rows) * a.cols <= (12 << 20)) return launch_few<2>(a, st);
   // The width of a tile and the CTAs that share one: what takes least by these measured times in ns: 128 columns of a
-  // tile, an image's kernel and a cluster's joining; a tile's beginning and end beside another's steps.
-  constexpr int kWidths[5] = {16, 32, 64, 128, 192}, kStep[5] = {320, 350, 430, 540, 610};
-  constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};  // that run at once
+  // tile, an image's kernel, a pair's beginning, a cluster's joining; a tile's beginning and end beside another's steps.
+  constexpr int kWidths[5] = {16, 32, 64, 128, 160}, kStep[5] = {320, 350, 430, 460, 430};  // the last: pairs
+  constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};                        // that run at once
   const int64_t row_tiles = (a.rows + kBigM - 1) / kBigM, steps = (a.cols + 127) / 128;
   int64_t best = -1;
   int way = 0, cs = 1;
   for (int i = 0; i < 5; ++i) {
-    const int64_t tiles = row_tiles * ((a.n + kWidths[i] - 1) / kWidths[i]);
-    for (int c = 1; c <= 8 && c <= steps; ++c) {
-      if (c > 1 && tiles > kClusters[c]) break;
-      const int64_t waves = (tiles + kClusters[c] - 1) / kClusters[c];
-      const int64_t cost = waves * ((steps + c - 1) / c * kStep[i] + 400) + (kWidths[i] > kRawMost ? 1500 : 0) +
-                           (c > 1 ? 1800 + 8 * kWidths[i] : 0);
+    const bool pair = i == 4;
+    const int64_t tiles = (pair ? (row_tiles + 1) / 2 : row_tiles) * ((a.n + kWidths[i] - 1) / kWidths[i]);
+    for (int c = 1; c <= (pair ? 1 : 8) && c <= steps; ++c) {
+      const int once = kClusters[pair ? 2 : c];
+      if (c > 1 && tiles > once) break;
+      const int64_t cost = (tiles + once - 1) / once * ((steps + c - 1) / c * kStep[i] + 400) + (kWidths[i] > kRawMost ? 1500 : 0) +
+                           (pair ? 500 : 0) + (c > 1 ? 1800 + 8 * kWidths[i] : 0);
       if (best < 0 || cost < best) best = cost, way = i, cs = c;
     }
     if (kWidths[i] >= a.n) break;
@@ -689,7 +751,7 @@ cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
     case 1: return launch_big<32>(a, cs, st);
     case 2: return launch_big<64>(a, cs, st);
     case 3: return launch_big<128>(a, cs, st);
-    default: return launch_big<192>(a, cs, st);
+    default: return launch_big<160, true>(a, 1, st);
   }
 }
 
