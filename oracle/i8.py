@@ -37,8 +37,8 @@ def silu_rows(gate, up):
 
 
 def matmul(w, w_scale, x, x_scale):
-    """The exact sums, and the f32 result of their stated roundings."""
-    s = x.astype(np.int64) @ w.astype(np.int64).T
+    """The exact sums (of whole numbers below 2^53, so exact in f64), and the f32 result of their stated roundings."""
+    s = x.astype(np.float64) @ w.astype(np.float64).T
     with np.errstate(all="ignore"):
         return s, s.astype(np.float32) * x_scale.astype(np.float32)[:, None] * w_scale.astype(np.float32)[None]
 

@@ -187,6 +187,43 @@ def test_quotients_next_to_borders(ops):
     check_rows(q, s, *i8.norm_rows((x / g).astype(np.float32), None, g, 1e-5)[1:], 33 * U)
 
 
+@pytest.mark.parametrize("n,w", [(700, 300), (64, 2048), (40, 5000)])
+def test_rows_with_more_borders_than_are_kept(ops, n, w):
+    """Products next to borders throughout: more of them than a group of rows has room to note."""
+    rng = np.random.default_rng(w)
+    m = np.abs(rng.normal(size=(n, 1))) + 0.5
+    c = rng.integers(-126, 126, size=(n, w)) + 0.5
+    up = (c * m / 127 / 64 * (1 + rng.integers(-8, 9, size=(n, w)) * 2.0**-23)).astype(np.float32)
+    up[:, 7] = m[:, 0] / 64
+    gate = np.full((n, w), 64, dtype=np.float32)  # silu(64) = 64 to 2^-80
+    q, s = codes_room(n, w), torch.empty(n, device="cuda")
+    ops.tqd_op_silu_mul_i8(dev(gate), dev(up), q, s)
+    check_rows(q, s, *i8.silu_rows(gate, up), 8 * U)
+    ops.tqd_op_rmsnorm_i8(dev(up), None, dev(np.ones(w, dtype=np.float32)), 1e-9, None, q, s)
+    check_rows(q, s, *i8.norm_rows(up, None, np.ones(w, dtype=np.float32), 1e-9)[1:], 33 * U)
+
+
+@pytest.mark.parametrize("n,w", [(100000, 40), (30000, 260), (12000, 1100)])
+def test_many_rows_a_block(ops, n, w):
+    """Blocks that go over more rows than they keep notes of at once."""
+    rng = np.random.default_rng(n)
+    x, z = rng.normal(size=(2, n, w)).astype(np.float32)
+    q, s = codes_room(n, w), torch.empty(n, device="cuda")
+    ops.tqd_op_silu_mul_i8(dev(x), dev(z), q, s)
+    check_rows(q, s, *i8.silu_rows(x, z), 8 * U)
+    g = (1 + 0.1 * rng.normal(size=w)).astype(np.float32)
+    dx = dev(x)
+    ops.tqd_op_rmsnorm_i8(dx, dev(z), dev(g), 1e-6, dx, q, s)
+    h, want_q, want_s = i8.norm_rows(x, z, g, 1e-6)
+    check_rows(q, s, want_q, want_s, 33 * U)
+    assert np.array_equal(dx.cpu().numpy(), h)
+    ops.tqd_op_rows_i8(dev(z), q, s)
+    check_rows(q, s, *i8.rows(z), U)
+    out = torch.empty(n, w, device="cuda")
+    ops.tqd_op_rows_i8_read(q, s, out)
+    assert np.array_equal(out.cpu().numpy(), q.cpu().numpy().astype(np.float32) * s.cpu().numpy()[:, None])
+
+
 # ------------------------------------------------------------------ products
 
 PRODUCTS = [(1, 32, 1), (17, 64, 3), (16, 96, 8), (129, 160, 9), (300, 1056, 17), (1000, 2080, 33), (128, 16384, 2),
@@ -217,6 +254,28 @@ def test_product_is_the_exact_sum(ops, rows, cols, n):
     y = run_product(ops, w, ws, x, xs, place=(3, 1))
     assert np.array_equal(y.cpu().numpy(), i8.matmul(w, ws, x, xs)[1])
     assert bool((torch.as_strided(y, (n, 3), (rows + 3, 1), 1 + rows) == FULL).all())
+
+
+# Sizes at which each way of making a product is taken: tiles of 16 to 128 tokens with and without clusters, and pairs of
+# CTAs, with rows and tokens that end inside a tile, a pair whose second half has no rows, and a pair of few tokens.
+WAYS = [(30000, 512, 10), (9000, 2048, 12), (20000, 640, 30), (20000, 640, 64), (6000, 96, 700), (40000, 64, 170), (4000, 4096, 100),
+        (13000, 1056, 330), (20100, 32, 1000), (20097, 1056, 161), (26112, 160, 1016), (40000, 2080, 150), (38912, 1024, 304)]
+
+
+@pytest.mark.parametrize("rows,cols,n", WAYS)
+def test_every_way_of_a_product(ops, rows, cols, n):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows + n)
+    draw = lambda *s: torch.randint(-128, 128, s, dtype=torch.int8, device="cuda", generator=g)  # noqa: E731
+    w, x = draw(rows, cols), draw(n, cols)
+    w[::5], x[::7] = 127, -128  # sums of one sign past 2^24
+    w[2::5], x[3::7] = -128, 127
+    ws, xs = torch.rand(rows, device="cuda", generator=g), torch.rand(n, device="cuda", generator=g)
+    y = torch.full((n, rows + 3), float(FULL), device="cuda")
+    scratch = torch.full((ops.tqd_i8_matmul_scratch_bytes(rows, cols, n),), 0xFF, dtype=torch.uint8, device="cuda")
+    ops.tqd_op_i8_matmul(w, ws, x, xs, y[:, :rows], scratch)
+    want = (x.double() @ w.double().T).float() * xs[:, None] * ws  # exact in f64
+    assert torch.equal(y[:, :rows], want) and bool((y[:, rows:] == FULL).all())
 
 
 @pytest.mark.parametrize("rows,cols,n", [(40, 16384, 3), (130, 16384, 200), (130, 4096, 40), (260, 8192, 12), (16, 1056, 20)])
@@ -274,7 +333,7 @@ def test_product_of_sliced_codes(ops):
     assert np.array_equal(y.cpu().numpy(), i8.matmul(qw.cpu().numpy(), sw.cpu().numpy(), qx.cpu().numpy(), sx.cpu().numpy())[1])
 
 
-@pytest.mark.parametrize("rows,cols,n", [(4096, 1024, 1), (640, 2048, 40), (1000, 960, 300)])
+@pytest.mark.parametrize("rows,cols,n", [(4096, 1024, 1), (640, 2048, 40), (1000, 960, 300), (20000, 128, 200), (1000, 2048, 12)])
 def test_products_on_two_streams_and_in_graphs(ops, rows, cols, n):
     """Calls on two streams at once, each with its scratch, and a captured call replayed on new codes."""
     rng = np.random.default_rng(n)
