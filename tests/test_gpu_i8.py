@@ -259,7 +259,8 @@ def test_product_is_the_exact_sum(ops, rows, cols, n):
 # Sizes at which each way of making a product is taken: tiles of 16 to 128 tokens with and without clusters, and pairs of
 # CTAs, with rows and tokens that end inside a tile, a pair whose second half has no rows, and a pair of few tokens.
 WAYS = [(30000, 512, 10), (9000, 2048, 12), (20000, 640, 30), (20000, 640, 64), (6000, 96, 700), (40000, 64, 170), (4000, 4096, 100),
-        (13000, 1056, 330), (20100, 32, 1000), (20097, 1056, 161), (26112, 160, 1016), (40000, 2080, 150), (38912, 1024, 304)]
+        (13000, 1056, 330), (20100, 32, 1000), (20097, 1056, 161), (26112, 160, 1016), (40000, 2080, 150), (38912, 1024, 304), (5000, 992, 511),
+        (40000, 2080, 185)]
 
 
 @pytest.mark.parametrize("rows,cols,n", WAYS)

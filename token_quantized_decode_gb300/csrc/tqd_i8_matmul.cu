@@ -215,13 +215,13 @@ cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
 // after every 8 steps (1024 columns) and add them up as whole numbers; they write a tile's results
 // while the next one's sums are made.  Where there are few tiles a cluster of cs CTAs shares a
 // tile's steps, and each adds up and writes a part of its tokens.
-constexpr int kBigM = 128, kImageK = 128;
+constexpr int kBigM = 128;
 constexpr int kConverters = 2;               // groups of four warps
 
 template <int kTN, bool kPair>
 struct BigCfg {
   static constexpr bool raw_tokens = kTN <= 64;
-  static constexpr int K = raw_tokens ? 128 : kImageK;       // columns of a step
+  static constexpr int K = kTN == 192 ? 64 : 128;            // columns of a step
   static constexpr int run = 1024 / K;                       // steps that the f32 sums hold
   static constexpr int readers = kTN <= 32 ? 4 : kTN <= 128 ? 8 : 16;  // warps that read sums (TN 160: 48 columns each)
   static constexpr int threads = 32 * (4 + 4 * kConverters + readers);  // copies, MMAs, two idle; then these
@@ -230,8 +230,8 @@ struct BigCfg {
   static constexpr uint32_t image = kTN / ctas * K * 2;                 // bytes of f16 tokens in a stage
   static constexpr uint32_t raw = raw_tokens ? kTN * K : 0;       // bytes of their codes
   static constexpr uint32_t stage = w_raw + image + raw;
-  static constexpr int stages = kPair ? 6 : kTN >= 128 ? 4 : kTN == 64 ? 5 : 7;
-  static constexpr int a_stages = kPair ? 3 : stages;  // of operand A, K / 2 columns each
+  static constexpr int stages = kTN == 192 ? 10 : kPair ? 6 : kTN >= 128 ? 4 : kTN == 64 ? 5 : 7;
+  static constexpr int a_stages = kTN == 192 ? 4 : kPair ? 3 : stages;  // of operand A, K / 2 columns each
   static constexpr uint32_t a_col = 2 * kTN;                // behind two accumulators, in turn
   static constexpr size_t smem = stages * stage + 1024;
   static_assert(a_col + a_stages * K / 2 <= 512, "tensor memory");
@@ -639,24 +639,25 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
 
 // The tokens' codes as f16 in the order of k_i8_big's shared memory: [step][8 tokens][column / 8][token][8],
 // zeros past the last token and column.  A thread takes 16 codes.
+template <int kK>
 __global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_stride, int n, int cols, int n16, int steps,
                                                   uint8_t* image) {
   pdl_launch_dependents();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int j8 = static_cast<int>(at & 7), c = static_cast<int>((at >> 3) & 7);
-  const int64_t rest = at >> 6;  // (token group, step), the step first
+  const int j8 = static_cast<int>(at & 7), c = static_cast<int>((at >> 3) % (kK / 16));
+  const int64_t rest = at / (kK / 2);  // (token group, step), the step first
   const int k = static_cast<int>(rest % steps);
   const int64_t group = rest / steps;
   if (group * 8 >= n16) return;
   const int64_t j = group * 8 + j8;
-  const int col = k * kImageK + c * 16;
+  const int col = k * kK + c * 16;
   uint4 v = make_uint4(0u, 0u, 0u, 0u), p, q;
   if (j < n && col < cols) v = __ldg(reinterpret_cast<const uint4*>(x + j * x_stride + col));
   i8x4_to_f16(v.x, p.x, p.y);
   i8x4_to_f16(v.y, p.z, p.w);
   i8x4_to_f16(v.z, q.x, q.y);
   i8x4_to_f16(v.w, q.z, q.w);
-  uint4* dst = reinterpret_cast<uint4*>(image + (static_cast<int64_t>(k) * n16 + group * 8) * (kImageK * 2) + c * 256 + j8 * 16);
+  uint4* dst = reinterpret_cast<uint4*>(image + (static_cast<int64_t>(k) * n16 + group * 8) * (kK * 2) + c * 256 + j8 * 16);
   dst[0] = p;
   dst[8] = q;
 }
@@ -706,8 +707,8 @@ cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
   if (Cfg::raw_tokens)
     return launch_pdl_clusters(k_i8_big<kTN, kPair>, static_cast<unsigned>(kPair ? 2 : cs), dim3(grid), Cfg::threads, Cfg::smem, st, w_map, x_map, b);
   x_map = w_map;  // not read
-  const int64_t threads = static_cast<int64_t>(n16 / 8) * steps * 64;
-  k_i8_image<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a.x, a.x_stride, a.n, a.cols, n16, steps,
+  const int64_t threads = static_cast<int64_t>(n16 / 8) * steps * (Cfg::K / 2);
+  k_i8_image<Cfg::K><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a.x, a.x_stride, a.n, a.cols, n16, steps,
                                                                            static_cast<uint8_t*>(a.scratch));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -718,7 +719,7 @@ cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
 
 size_t i8_matmul_scratch_bytes(int rows, int cols, int n) {
   if (n <= kRawMost) return 0;
-  return static_cast<size_t>((n + 15) / 16 * 16) * ((cols + kImageK - 1) / kImageK) * kImageK * 2;
+  return static_cast<size_t>((n + 15) / 16 * 16) * ((cols + 127) / 128) * 128 * 2;
 }
 
 cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
@@ -729,13 +730,14 @@ cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
   if (a.n <= 16 && static_cast<int64_t>(a.rows) * a.cols <= (12 << 20)) return launch_few<2>(a, st);
   // The width of a tile and the CTAs that share one: what takes least by these measured times in ns: 128 columns of a
   // tile, an image's kernel, a pair's beginning, a cluster's joining; a tile's beginning and end beside another's steps.
-  constexpr int kWidths[5] = {16, 32, 64, 128, 160}, kStep[5] = {320, 350, 430, 460, 430};  // the last: pairs
+  constexpr int kWidths[6] = {16, 32, 64, 128, 160, 192}, kStep[6] = {320, 350, 430, 460, 430, 590};  // the last two: pairs
   constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};                        // that run at once
   const int64_t row_tiles = (a.rows + kBigM - 1) / kBigM, steps = (a.cols + 127) / 128;
   int64_t best = -1;
   int way = 0, cs = 1;
-  for (int i = 0; i < 5; ++i) {
-    const bool pair = i == 4;
+  for (int i = 0; i < 6; ++i) {
+    const bool pair = i >= 4;
+    if (kWidths[i] > kRawMost && a.n <= kRawMost) break;  // (there is no scratch for an image)
     const int64_t tiles = (pair ? (row_tiles + 1) / 2 : row_tiles) * ((a.n + kWidths[i] - 1) / kWidths[i]);
     for (int c = 1; c <= (pair ? 1 : 8) && c <= steps; ++c) {
       const int once = kClusters[pair ? 2 : c];
@@ -744,14 +746,14 @@ cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
                            (pair ? 500 : 0) + (c > 1 ? 1800 + 8 * kWidths[i] : 0);
       if (best < 0 || cost < best) best = cost, way = i, cs = c;
     }
-    if (kWidths[i] >= a.n) break;
   }
   switch (way) {
     case 0: return launch_big<16>(a, cs, st);
     case 1: return launch_big<32>(a, cs, st);
     case 2: return launch_big<64>(a, cs, st);
     case 3: return launch_big<128>(a, cs, st);
-    default: return launch_big<160, true>(a, 1, st);
+    case 4: return launch_big<160, true>(a, 1, st);
+    default: return launch_big<192, true>(a, 1, st);
   }
 }
 
