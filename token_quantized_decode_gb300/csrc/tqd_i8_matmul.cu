@@ -1,11 +1,11 @@
 // Products of int8 matrices with a scale for each token and each channel:
 // y[j][r] = x_scale[j] w_scale[r] sum_c x[j][c] w[r][c].
 //
-// The sums are exact.  The int8 tensor instructions of this part run at a sixteenth of the
-// f16 ones' rate, so codes become f16 operands (exact), products are exact in the f32
-// accumulator, and so are sums of up to 1024 of them (128 * 128 * 1024 = 2^24); a run of
-// at most 1024 columns is added to a 32-bit whole number.  So the order of the sums, and how
-// they are split, changes nothing.
+// The sums are exact, so that their order, and how they are split, changes nothing.  The int8
+// tensor instructions of this part (an m16n8k32 in 16.3 clocks an SM) have a quarter of the rate of f16's
+// (an m16n8k16 in 2.0), and the fifth generation's f16 products are 2.6 times as fast again.  Few tokens take them all the same: memory is the bound there.  For more, codes become f16 operands
+// (exact), products are exact in the f32 accumulator, and so are sums of up to 1024 of them
+// (128 * 128 * 1024 = 2^24); a run of at most 1024 columns is added to a 32-bit whole number.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -38,15 +38,19 @@ __device__ __forceinline__ int4 ld_rank4(const int* p, int rank) {
   return v;
 }
 
-// -------------------------------------------------------------- up to 8 tokens
+// ------------------------------------------------------------- up to 16 tokens
 //
 // A warp takes 16 rows; lane (g, c) = (lane / 4, lane % 4) holds sixteen bytes of rows g and g + 8 and of
-// token g, which are its share of two 16 x 8 x 32 int8 instructions (the columns' order within 64 does
-// not matter, as long as both operands have the same).  Eight columns of the instruction are all that is
-// needed here, and its rate, 32 bytes of weights a clock and SM, is above what memory brings (24): nothing is
-// converted.  Each lane copies its own bytes into a ring of its own, so that no barrier
-// stands between a copy and its use.  A step is 128 columns.  kw warps of a CTA and cs CTAs of a
-// cluster share 16 rows: piece p of the kw cs has the steps p, p + kw cs, ...
+// token g (and 8 + g), which are its share of two 16 x 8 x 32 int8 instructions (the columns' order within 64 does
+// not matter, as long as both operands have the same).  The instruction's rate, 32 bytes of weights a clock and
+// SM for eight tokens, is above what memory brings (24): nothing is converted.  Each lane copies its own
+// bytes into a ring of its own, so that no barrier stands between a copy and its use: 4 steps of it, 64 KB a
+// CTA and two CTAs an SM, so that 128 KB an SM are under way.  A step is 128 columns.  kw warps of a CTA and cs CTAs
+// of a cluster share 16 rows: piece p of the kw cs has the steps p, p + kw cs, ...
+//
+// Measured (us, from a graph): 1024 x 1024 of 1 2.1, 4096 x 1024 of 1 2.9 (a launch by itself 1.0), 8192 x 8192 of 1
+// 15.0 (4.5 TB/s), 151936 x 1024 of 1 29.2 (5.3 TB/s, 79 % of the measured copy rate; a plain fill of
+// that many bytes reaches 5.5 TB/s).  Memory and, below 10 MB, one memory latency after another bound it.
 constexpr int kFewWarps = 8;
 // Eight tokens in each of kNT instructions.
 template <int kNT>
@@ -206,24 +210,32 @@ cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
 
 // ------------------------------------------------------------ 9 tokens and more
 //
-// A CTA per SM makes tiles of 128 rows of w by kTN tokens on the fifth-generation tensor
-// cores.  In a step of 128 columns the rows' codes come by a tensor copy as they are, and
-// groups of four warps, a step each in turn, make them f16 and put them into tensor memory as
-// operand A (a lane is a row).  The tokens, operand B, are f16 in shared memory: up to 64 are
-// made so by the same warps, more come by a bulk copy from an image that k_i8_image laid out in the
-// scratch in the order of shared memory.  Other warps take the sums out of tensor memory
-// after every 8 steps (1024 columns) and add them up as whole numbers; they write a tile's results
-// while the next one's sums are made.  Where there are few tiles a cluster of cs CTAs shares a
-// tile's steps, and each adds up and writes a part of its tokens.
+// CTAs, one per SM, make tiles of 128 rows of w by kTN tokens on the fifth-generation tensor cores.  In
+// a step of K columns the rows' codes come by a tensor copy as they are, and groups of four warps, a step
+// each in turn, make them f16 and put them into tensor memory as operand A (a lane is a row).  The tokens, operand
+// B, are f16 in shared memory: up to 64 are made so by the same warps, more come by a bulk copy from an
+// image that k_i8_image laid out in the scratch in the order of shared memory.  Other warps take the sums out of
+// tensor memory after every 1024 columns and add them up as whole numbers; they write a tile's results while the next
+// one's sums are made.
+//
+// Where there are few tiles a cluster of cs CTAs shares a tile's steps, and each adds up and writes a part of
+// its tokens (1024 x 16384 of 40: 13.5 us).
+// What bounds a CTA by itself is what its SM takes in: about 57 bytes a clock were the most, of which a step
+// of 128 x 128 needs 48 KB, 860 clocks of which the products are 512.  So where there are many tiles a pair of CTAs makes
+// 256 rows with one instruction and each brings half of the tokens: 8192 x 8192 of 2048 took 199 us with 128 x 128
+// and takes 165 to 169 with pairs of 160 tokens (85 % of the measured bf16 rate), 16384 x 4096 of 4096 378 and 309 (91 %).  Tensor
+// memory is what limits a pair's width: two accumulators of kTN columns and the slots of A.  192 tokens leave
+// room for four slots of 64 columns only, whose steps are slower for their work (295 ns for 64 columns, 215 for 160 tokens), but 511
+// tokens are three tiles of them and four of 160 (5120 x 960: 13.0 and 15.1 us).
 constexpr int kBigM = 128;
 constexpr int kConverters = 2;               // groups of four warps
 
 template <int kTN, bool kPair>
 struct BigCfg {
   static constexpr bool raw_tokens = kTN <= 64;
-  static constexpr int K = kTN == 192 ? 64 : 128;            // columns of a step
+  static constexpr int K = kTN == 192 ? 64 : 128;                   // columns of a step
   static constexpr int run = 1024 / K;                       // steps that the f32 sums hold
-  static constexpr int readers = kTN <= 32 ? 4 : kTN <= 128 ? 8 : 16;  // warps that read sums (TN 160: 48 columns each)
+  static constexpr int readers = kTN <= 32 ? 4 : kTN <= 128 ? 8 : 16;  // warps that read sums, 16 to 64 columns each
   static constexpr int threads = 32 * (4 + 4 * kConverters + readers);  // copies, MMAs, two idle; then these
   static constexpr uint32_t w_raw = kBigM * K;               // bytes of the rows' codes in a stage
   static constexpr int ctas = kPair ? 2 : 1;                 // that make a tile's products together
@@ -338,7 +350,8 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
-// An arrival at the barrier, of a pair at the first CTA's.
+// An arrival at the barrier, of a pair at the first CTA's.  (At its default scope: with .release.cluster
+// an arrival took 1450 clocks, so 70.  What it tells of is this CTA's tensor memory and finished copies.)
 template <bool kPair>
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   if (kPair) {
@@ -379,11 +392,11 @@ __device__ __forceinline__ bool big_wait(uint64_t* bar, uint32_t parity, volatil
 }
 
 struct BigArgs {
-  const uint8_t* image;  // [steps][tokens up to a multiple of 16][64] f16
+  const uint8_t* image;  // [steps][tokens, whole groups][K] f16
   const float *x_scale, *w_scale;
   float* y;
   int64_t y_stride;
-  int rows, cols, n, n16, steps, row_tiles, token_tiles, cs;
+  int rows, cols, n, padded, steps, row_tiles, token_tiles, cs;
 };
 
 template <int kTN, bool kPair>
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
     bool image_there = Cfg::raw_tokens, ok = true;
     for (int tile = first; ok && tile < tiles; tile += stride) {
       const int row0 = tile / a.token_tiles * (kBigM * Cfg::ctas) + upper, j0 = tile % a.token_tiles * kTN;
-      const int share = min(kTN, a.n16 - j0) / Cfg::ctas, mine = j0 + (kPair ? rank * share : 0);  // tokens of the image
+      const int share = min(kTN, a.padded - j0) / Cfg::ctas, mine = j0 + (kPair ? rank * share : 0);  // tokens of the image
       const uint32_t bytes = Cfg::raw_tokens ? Cfg::raw : share * Cfg::K * 2;
       for (int k = from; k < from + steps; ++k) {
         if (issued >= Cfg::stages) ok = __all_sync(0xFFFFFFFFu, big_wait(&empty[s], phase ^ 1, dead));
@@ -448,7 +461,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
             copy_box(raw_x + s * Cfg::raw, &x_map, k * Cfg::K, j0, &full[s]);
           } else {
             if (!image_there) pdl_wait();  // the kernel before this one writes the image
-            bulk_g2s(tokens + s * Cfg::image, a.image + (static_cast<int64_t>(k) * a.n16 + mine) * (Cfg::K * 2), bytes, &full[s]);
+            bulk_g2s(tokens + s * Cfg::image, a.image + (static_cast<int64_t>(k) * a.padded + mine) * (Cfg::K * 2), bytes, &full[s]);
           }
         }
         image_there = true;
@@ -463,14 +476,15 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
     }
   } else if (warp == 1) {
     // One thread, which looks for the next stage while this one's MMAs are issued: the tensor cores hold one or two
-    // waiting instructions only, so whatever stands between two steps is time that they lack.
+    // waiting instructions only, so whatever stands between two steps is time that they lack.  (The loop stands
+    // inside elect.sync's branch: in one that the thread's number chooses an instruction takes 94 clocks to issue, here 9.)
     if ((!kPair || rank == 0) && elect_one()) {
       int s = 0, at = 0, run = 0;
       uint32_t phase = 0;
       bool ok = true, there = false;
       const uint64_t desc = image_desc<Cfg::K>(tokens);
       for (int tile = first; ok && tile < tiles; tile += stride) {
-        const int width = min(kTN, a.n16 - tile % a.token_tiles * kTN);
+        const int width = min(kTN, a.padded - tile % a.token_tiles * kTN);
         const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(width >> 3) << 17) | (static_cast<uint32_t>(kBigM * Cfg::ctas >> 4) << 24);
         int left = (a.cols - from * Cfg::K) / 16;  // instructions of 16 columns (more than this CTA's where others follow)
         for (int k0 = 0; ok && k0 < steps; k0 += Cfg::run, ++run) {
@@ -563,7 +577,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
     int run = 0;
     for (int tile = first; tile < tiles; tile += stride) {
       const int row = tile / a.token_tiles * (kBigM * Cfg::ctas) + upper + quad * 32 + lane, j0 = tile % a.token_tiles * kTN;
-      const int width = min(kTN, a.n16 - j0);
+      const int width = min(kTN, a.padded - j0);
       const float sw = row < a.rows ? a.w_scale[row] : 0.f;
       int total[kCols];
 #pragma unroll
@@ -638,9 +652,9 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
 }
 
 // The tokens' codes as f16 in the order of k_i8_big's shared memory: [step][8 tokens][column / 8][token][8],
-// zeros past the last token and column.  A thread takes 16 codes.
+// zeros past the last token and column.  A thread takes 16 codes.  (5120 x 960 of 511: 2.1 of the 13.0 us, with its launch.)
 template <int kK>
-__global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_stride, int n, int cols, int n16, int steps,
+__global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_stride, int n, int cols, int padded, int steps,
                                                   uint8_t* image) {
   pdl_launch_dependents();
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -648,7 +662,7 @@ __global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_str
   const int64_t rest = at / (kK / 2);  // (token group, step), the step first
   const int k = static_cast<int>(rest % steps);
   const int64_t group = rest / steps;
-  if (group * 8 >= n16) return;
+  if (group * 8 >= padded) return;
   const int64_t j = group * 8 + j8;
   const int col = k * kK + c * 16;
   uint4 v = make_uint4(0u, 0u, 0u, 0u), p, q;
@@ -657,7 +671,7 @@ __global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_str
   i8x4_to_f16(v.y, p.z, p.w);
   i8x4_to_f16(v.z, q.x, q.y);
   i8x4_to_f16(v.w, q.z, q.w);
-  uint4* dst = reinterpret_cast<uint4*>(image + (static_cast<int64_t>(k) * n16 + group * 8) * (kK * 2) + c * 256 + j8 * 16);
+  uint4* dst = reinterpret_cast<uint4*>(image + (static_cast<int64_t>(k) * padded + group * 8) * (kK * 2) + c * 256 + j8 * 16);
   dst[0] = p;
   dst[8] = q;
 }
@@ -688,14 +702,17 @@ cudaError_t map_of(const int8_t* p, int64_t stride, int rows, int cols, int box_
 
 constexpr int kRawMost = 64;  // tokens that k_i8_big takes as codes
 
+// The tokens that its instructions are for: a CTA's come in sixteens, a pair's in thirty-twos.
+int padded_tokens(int n) { return n <= kRawMost ? (n + 15) / 16 * 16 : (n + 31) / 32 * 32; }
+
 template <int kTN, bool kPair = false>
 cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
   using Cfg = BigCfg<kTN, kPair>;
   static unsigned long long done = 0;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_big<kTN, kPair>), Cfg::smem, &done);
   if (e != cudaSuccess) return e;
-  const int steps = (a.cols + Cfg::K - 1) / Cfg::K, n16 = (a.n + 15) / 16 * 16;
-  BigArgs b{static_cast<const uint8_t*>(a.scratch), a.x_scale, a.w_scale, a.y, a.y_stride, a.rows, a.cols, a.n, n16, steps,
+  const int steps = (a.cols + Cfg::K - 1) / Cfg::K, padded = padded_tokens(a.n);
+  BigArgs b{static_cast<const uint8_t*>(a.scratch), a.x_scale, a.w_scale, a.y, a.y_stride, a.rows, a.cols, a.n, padded, steps,
             (a.rows + kBigM * Cfg::ctas - 1) / (kBigM * Cfg::ctas), (a.n + kTN - 1) / kTN, cs};
   const int64_t tiles = static_cast<int64_t>(b.row_tiles) * b.token_tiles;
   CUtensorMap w_map, x_map;
@@ -707,8 +724,8 @@ cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
   if (Cfg::raw_tokens)
     return launch_pdl_clusters(k_i8_big<kTN, kPair>, static_cast<unsigned>(kPair ? 2 : cs), dim3(grid), Cfg::threads, Cfg::smem, st, w_map, x_map, b);
   x_map = w_map;  // not read
-  const int64_t threads = static_cast<int64_t>(n16 / 8) * steps * (Cfg::K / 2);
-  k_i8_image<Cfg::K><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a.x, a.x_stride, a.n, a.cols, n16, steps,
+  const int64_t threads = static_cast<int64_t>(padded / 8) * steps * (Cfg::K / 2);
+  k_i8_image<Cfg::K><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, st>>>(a.x, a.x_stride, a.n, a.cols, padded, steps,
                                                                            static_cast<uint8_t*>(a.scratch));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -719,7 +736,7 @@ cudaError_t launch_big(const I8MatmulArgs& a, int cs, cudaStream_t st) {
 
 size_t i8_matmul_scratch_bytes(int rows, int cols, int n) {
   if (n <= kRawMost) return 0;
-  return static_cast<size_t>((n + 15) / 16 * 16) * ((cols + 127) / 128) * 128 * 2;
+  return static_cast<size_t>(padded_tokens(n)) * ((cols + 127) / 128) * 128 * 2;
 }
 
 cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
