@@ -187,6 +187,19 @@ def test_quotients_next_to_borders(ops):
     check_rows(q, s, *i8.norm_rows((x / g).astype(np.float32), None, g, 1e-5)[1:], 33 * U)
 
 
+@pytest.mark.parametrize("w", [40, 300, 2048, 5000])
+def test_gates_far_below_zero(ops, w):
+    """Their silu is nothing, however large they are and whatever they meet in up."""
+    rng = np.random.default_rng(w)
+    gate, up = rng.normal(size=(8, w)).astype(np.float32), rng.normal(size=(8, w)).astype(np.float32)
+    for r, far in enumerate((-87.5, -104.0, -1e9, -6e10, -7e10, -1e30, -1e35, -3e38)):
+        gate[r, rng.integers(0, w, size=3)] = far
+        up[r, ::7] *= np.float32(2.0 ** (30 if r < 4 else 3))
+    q, s = codes_room(8, w), torch.empty(8, device="cuda")
+    ops.tqd_op_silu_mul_i8(dev(gate), dev(up), q, s)
+    check_rows(q, s, *i8.silu_rows(gate, up), 8 * U)
+
+
 @pytest.mark.parametrize("n,w", [(700, 300), (64, 2048), (40, 5000)])
 def test_rows_with_more_borders_than_are_kept(ops, n, w):
     """Products next to borders throughout: more of them than a group of rows has room to note."""

@@ -37,7 +37,8 @@ __device__ __forceinline__ float exp_near(float x) {
   return fmaf(e * kLn2, left, e);
 }
 // g / (1 + e^-g): the quotient from the approximate reciprocal and one step of Newton's iteration, within a unit.
-// (e^87 is the largest that leaves the reciprocal in range; what is below it counts for nothing in a row that is done here.)
+// (e^87 is the largest that leaves the reciprocal in range.  Below it the value is too large, by |g| e^-87 at most, 2^-89
+// of gates down to -2^36: nothing beside the largest of a row that is done here.)
 __device__ __forceinline__ float silu(float g) {
   const float d = 1.f + exp_near(fminf(-g, 87.f));
   float r;
@@ -47,7 +48,7 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 // silu(g) u to 2^-38, for gates whose e^-g is within f32: of a row whose largest |y| is at least 2^-40
-// and whose |u| are at most 2^40, elements of at least a 2^8th of the largest have g > -62.  The f64 pipe does a
+// and whose |g| and |u| are at most 2^36, elements of at least a 2^8th of the largest have g > -62.  The f64 pipe does a
 // warp's instruction in 15 clocks, so this takes the reduction to |r| <= ln 2 / 2 with ln 2 in two parts (Cody and
 // Waite), the Taylor series with the terms from r^6 on in f32 (less than 2^-18 of the whole), and one step of
 // Newton's iteration from the f32 reciprocal in place of exp and a division.
@@ -311,16 +312,15 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     }
   }
   fetch(turn % Cfg::ahead, row + Cfg::ahead * step);
-  float top = 0.f, ss = 0.f, ups = 0.f;  // the largest |y| (a NaN or an infinity is above all), the sum of h^2, the largest |up|
+  float top = 0.f, ss = 0.f, ins = 0.f;  // the largest |y| (a NaN or an infinity is above all), the sum of h^2, the largest |gate| and |up|
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
     const int i = (e * kT + t) * 4;
     if (kKind == kI8Silu) {
+      ins = max_abs(max_abs(ins, v[e][0], v[e][1]), v[e][2], v[e][3]);
+      ins = max_abs(max_abs(ins, w[e][0], w[e][1]), w[e][2], w[e][3]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[e][j] = silu(v[e][j]) * w[e][j];
-      }
-      ups = max_abs(max_abs(ups, w[e][0], w[e][1]), w[e][2], w[e][3]);
+      for (int j = 0; j < 4; ++j) v[e][j] = silu(v[e][j]) * w[e][j];
     }
     if (kKind == kI8Norm) {
 #pragma unroll
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     }
     top = max_abs(max_abs(top, v[e][0], v[e][1]), v[e][2], v[e][3]);
   }
-  if (kKind == kI8Silu && ups > 0x1p40f) top = INFINITY;  // silu may be below f32's range, and count: the row in f64
+  if (kKind == kI8Silu && ins > 0x1p36f) top = INFINITY;  // silu may be below f32's range, and count: the row in f64
   uint32_t high = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top) & 0x7FFFFFFFu);
   if (kKind == kI8Norm) ss = warp_sum(ss);
   if (kT > 32) {
