@@ -216,6 +216,25 @@ def test_rows_with_more_borders_than_are_kept(ops, n, w):
     check_rows(q, s, *i8.norm_rows(up, None, np.ones(w, dtype=np.float32), 1e-9)[1:], 33 * U)
 
 
+@pytest.mark.parametrize("n,w", [(700, 300), (64, 2048), (40, 5000)])
+def test_a_row_is_the_same_beside_any_others(ops, n, w):
+    """Rows whose elements are all as large, so that most have no room in a block's list: codes and scales are those of
+    the row by itself."""
+    rng = np.random.default_rng(w)
+    x = (np.exp(rng.normal(size=(n, 1))) * np.sign(rng.normal(size=(n, w)))).astype(np.float32)
+    up, g = np.full((n, w), 1.3, dtype=np.float32), np.ones(w, dtype=np.float32)
+    x[::9] = rng.normal(size=x[::9].shape)
+    dx, du, dg = dev(x), dev(up), dev(g)
+    calls = (lambda i, q, s: ops.tqd_op_rmsnorm_i8(dx[i], None, dg, 1e-6, None, q, s), lambda i, q, s: ops.tqd_op_silu_mul_i8(dx[i], du[i], q, s))
+    for call in calls:
+        q, s = codes_room(n, w), torch.empty(n, device="cuda")
+        one_q, one_s = codes_room(n, w), torch.empty(n, device="cuda")
+        call(slice(0, n), q, s)
+        for i in range(n):
+            call(slice(i, i + 1), one_q[i:i + 1], one_s[i:i + 1])
+        assert torch.equal(q, one_q) and torch.equal(s, one_s)
+
+
 @pytest.mark.parametrize("n,w", [(100000, 40), (30000, 260), (12000, 1100)])
 def test_many_rows_a_block(ops, n, w):
     """Blocks that go over more rows than they keep notes of at once."""

@@ -149,10 +149,11 @@ struct RowGroup {
   }
 };
 
-// A row in f64 as a whole.
+// A row in f64 as a whole, or its codes only.
 template <int kKind, int kT>
-__device__ __noinline__ void whole_row(const I8RowsArgs& a, int64_t row, int t, double* sh) {
+__device__ __noinline__ void whole_row(const I8RowsArgs& a, int64_t row, int t, double* sh, bool codes_only) {
   const int n = a.n;
+  RowGroup<kT>::sync();  // (a sum that was written is read by other threads)
   double most = 0.0, squares = 0.0, h;
   bool lost = false;
   for (int i = t; i < n; i += kT) {
@@ -173,7 +174,7 @@ __device__ __noinline__ void whole_row(const I8RowsArgs& a, int64_t row, int t, 
   int8_t* q = a.q + row * a.q_stride;
   for (int i = t; i < n; i += kT)
     q[i] = lost || most == 0.0 ? 0 : static_cast<int8_t>(exact_code(exact_element<kKind>(a, row, i, h), most));
-  if (t == 0) a.scale[row] = lost ? __uint_as_float(0x7FC00000u) : static_cast<float>(top / 127.0);
+  if (t == 0 && !codes_only) a.scale[row] = lost ? __uint_as_float(0x7FC00000u) : static_cast<float>(top / 127.0);
 }
 
 // The code next to the border that 127 y / most lies at: by its side, and on it the even one.
@@ -231,7 +232,7 @@ __device__ __noinline__ void settle(const I8RowsArgs& a, Pending<kT>& p, int64_t
       a.q[(first + r * step) * a.q_stride + i] = code_at_border(p.y[e], __longlong_as_double(static_cast<long long>(p.most[r])));
   }
   for (int r = 0; over && r < kWindow; ++r)
-    if ((over >> r) & 1u) whole_row<kKind, kT>(a, first + r * step, t, sh);
+    if ((over >> r) & 1u) whole_row<kKind, kT>(a, first + r * step, t, sh, true);  // (its scale depends on no other row)
   if (some) RowGroup<kT>::sync();
   p.clear(t);  // (a block's next entries come after the next row's barrier)
   if (kT == 32) __syncwarp();
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
   if (kKind == kI8Rows && m == 0.f) whole = false;
   if (kKind == kI8Norm) whole = whole || !(ss >= 0x1p-60f && ss <= 0x1p100f);
   if (whole) {
-    whole_row<kKind, kT>(a, row, t, sh_d);
+    whole_row<kKind, kT>(a, row, t, sh_d, false);
     continue;
   }
   const float inv = m > 0.f ? 127.f / m : 0.f;
