@@ -364,10 +364,18 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
   }
   const float m = __uint_as_float(high);
 
-  // (false for NaN; zeros of rows as they are need nothing)
+  // (false for NaN)
   bool whole = !(m >= (kKind == kI8Silu ? 0x1p-40f : 0x1p-60f) && m <= 0x1p60f);
-  if (kKind == kI8Rows && m == 0.f) whole = false;
   if (kKind == kI8Norm) whole = whole || !(ss >= 0x1p-60f && ss <= 0x1p100f);
+  if (m == 0.f) {
+    // a row of zeros (a batch's padding; zeros in up are enough) needs no more; products that vanished do
+    whole = false;
+    if (kKind != kI8Rows) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) whole = whole || max_abs(max_abs(0.f, w[e][0], w[e][1]), w[e][2], w[e][3]) != 0.f;
+      whole = RowGroup<kT>::any(whole);
+    }
+  }
   if (whole) {
     whole_row<kKind, kT>(a, row, t, sh_d, false);
     continue;
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     }
   }
   float scale = m / 127.f;
-  if (kKind == kI8Norm) scale = m * (1.f / sqrtf(ss / n + a.eps)) / 127.f;
+  if (kKind == kI8Norm && m > 0.f) scale = m * (1.f / sqrtf(ss / n + a.eps)) / 127.f;
   int8_t* q = a.q + row * a.q_stride;
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
