@@ -244,11 +244,15 @@ struct RowsCfg {
   static constexpr int block = kT < 128 ? 128 : kT;
   static constexpr int inputs = kKind == kI8Rows ? 1 : 2, ahead = kKind == kI8Rows ? 2 : 1;
   static constexpr int smem = block * kE * 16 * inputs * ahead;
-  static constexpr int ctas = kT >= 1024 ? 1 : kT == 512 ? 2 : kT == 256 ? (kE == 4 ? 3 : kKind == kI8Rows ? 5 : kKind == kI8Norm ? 3 : 4)
+  static constexpr int ctas = kT >= 1024 ? 1 : kT == 512 ? 2 : kT == 256 ? (kE == 4 ? 3 : 5)
                               : kE == 4 ? 5 : kKind == kI8Rows ? 8 : kKind == kI8Norm ? 6 : 7;
   };
 
-// kT threads a row, kE groups of four elements a thread.  kVec: every row of every tensor
+// kT threads a row, kE groups of four elements a thread.  Measured, in TB/s of the bytes that it must move (a copy of
+// as many: 6.8): rows 4099 x 4096 5.2 (16.3 us), norm with a sum that is kept 5.5 (39.4), SwiGLU 5.3
+// (28.6); a single row of 1024 1.2, 2.0 and 2.3 us.  HBM bounds the norm up to 4096 columns; wider rows have two
+// CTAs or one an SM, which wait at a row's barrier together (1500 x 12288 norm 3.8 TB/s); SwiGLU's instructions
+// (2.6 a clock and SM) and its barrier bound it.  kVec: every row of every tensor
 // begins on a 16-byte boundary (codes: 4) and is whole groups of four.  CTAs go from row to
 // row; a thread copies its elements of the next row into its own part of shared memory
 // while it works on this one, so that loads are always under way.
@@ -471,10 +475,15 @@ cudaError_t launch_kind(const I8RowsArgs& a, cudaStream_t st) {
   const bool vec = a.n % 4 == 0 && on16(a.x, a.x_stride) && on16(a.other, a.other_stride) && on16(a.g, 0) &&
                    on16(a.sum, a.sum_stride) && reinterpret_cast<uintptr_t>(a.q) % 4 == 0 &&
                    (a.rows == 1 || a.q_stride % 4 == 0);
+  // Few threads a row where that leaves an SM more rows under way, as a barrier of each row stands between its loads and
+  // its codes; many where a row's elements would not fit the registers.  Measured (us, 8191 x 2048): 128 x 4 and 256 x 2
+  // norm 39.1 and 45.4, SwiGLU 31.7 and 35.6, but rows as they are 17.3 and 15.0, which need few registers.  4099 x 4096,
+  // 256 x 4 and 512 x 2: 39.4 and 54.6, 28.5 and 38.8, 16.3 and 15.8.  8192 x 1024, 128 x 2, 256 x 1 and 64 x 4: norm 23.4, 31.3 and
+  // 22.1, SwiGLU 18.5, 23.9 and 20.2.  8192 x 512, 32 x 4 and 128 x 1: norm 12.2 and 16.5, SwiGLU 11.6 and 13.8, rows 6.0 and 6.7.
   if (a.n <= 128) return launch_rows<kKind, 32, 1>(a, vec, st);
   if (a.n <= 512) return launch_rows<kKind, 32, 4>(a, vec, st);
   if (a.n <= 1024) return launch_rows<kKind, 128, 2>(a, vec, st);
-  if (a.n <= 2048) return launch_rows<kKind, 256, 2>(a, vec, st);
+  if (a.n <= 2048) return launch_rows<kKind, kKind == kI8Rows ? 256 : 128, kKind == kI8Rows ? 2 : 4>(a, vec, st);
   if (a.n <= 4096) return launch_rows<kKind, 256, 4>(a, vec, st);
   if (a.n <= 8192) return launch_rows<kKind, 512, 4>(a, vec, st);
   return launch_rows<kKind, 1024, 4>(a, vec, st);
