@@ -25,6 +25,14 @@ def f(i):
     return P + 4 * i
 
 
+def test_kinds_of_scaling_are_the_package_s():
+    import token_quantized_decode_gb300 as tqd
+    names = ("TQD_ROPE_UNSCALED", "TQD_ROPE_LINEAR", "TQD_ROPE_BY_ROTATIONS", "TQD_ROPE_BY_INDEX")
+    assert [getattr(tqd, name) for name in names] == [0, 1, 2, 3] and set(names) <= set(tqd.__all__)
+    s = ops.rope_scaling(tqd.TQD_ROPE_LINEAR, factor=4.0)
+    assert (s.kind, s.factor, s.attention_factor) == (1, 4.0, 1.0)
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_codes_are_within_half_a_step():

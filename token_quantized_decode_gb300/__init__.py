@@ -12,13 +12,14 @@ import ctypes
 
 import numpy as np
 
-from ._lib import (TQD_KV_F16, TQD_KV_F32, TQD_SCHED_GRAPH, TQD_SCHED_PERSISTENT, TQD_WEIGHT_BF16,
+from ._lib import (TQD_KV_F16, TQD_KV_F32, TQD_ROPE_BY_INDEX, TQD_ROPE_BY_ROTATIONS, TQD_ROPE_LINEAR,
+                   TQD_ROPE_UNSCALED, TQD_SCHED_GRAPH, TQD_SCHED_PERSISTENT, TQD_WEIGHT_BF16,
                    TQD_WEIGHT_Q8_0, TQDError,
                    check, lib, tqd_config, tqd_host_weights, tqd_layer_weights, tqd_sampling)
 
 __all__ = [
     "TQDError", "TQD_SCHED_GRAPH", "TQD_SCHED_PERSISTENT", "TQD_WEIGHT_Q8_0", "TQD_WEIGHT_BF16", "TQD_KV_F32",
-    "TQD_KV_F16",
+    "TQD_KV_F16", "TQD_ROPE_UNSCALED", "TQD_ROPE_LINEAR", "TQD_ROPE_BY_ROTATIONS", "TQD_ROPE_BY_INDEX",
     "make_config", "make_host_weights", "tqd_status_name", "tqd_create", "tqd_destroy", "tqd_reset",
     "tqd_truncate", "tqd_next_pos", "tqd_prefill", "tqd_prefill_batch", "tqd_kv_upload", "tqd_decode_step", "tqd_generate",
     "tqd_decode_step_batch", "tqd_generate_batch", "tqd_sample", "tqd_generate_sampled",
