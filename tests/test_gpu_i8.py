@@ -292,7 +292,7 @@ def test_product_is_the_exact_sum(ops, rows, cols, n):
 # CTAs, with rows and tokens that end inside a tile, a pair whose second half has no rows, and a pair of few tokens.
 WAYS = [(30000, 512, 10), (9000, 2048, 12), (20000, 640, 30), (20000, 640, 64), (6000, 96, 700), (40000, 64, 170), (4000, 4096, 100),
         (13000, 1056, 330), (20100, 32, 1000), (20097, 1056, 161), (26112, 160, 1016), (40000, 2080, 150), (38912, 1024, 304), (5000, 992, 511),
-        (40000, 2080, 185)]
+        (40000, 2080, 185), (1000, 8192, 300), (4090, 4096, 250), (12000, 1984, 1500), (260, 16384, 90), (3900, 2080, 600)]
 
 
 @pytest.mark.parametrize("rows,cols,n", WAYS)
@@ -366,7 +366,8 @@ def test_product_of_sliced_codes(ops):
     assert np.array_equal(y.cpu().numpy(), i8.matmul(qw.cpu().numpy(), sw.cpu().numpy(), qx.cpu().numpy(), sx.cpu().numpy())[1])
 
 
-@pytest.mark.parametrize("rows,cols,n", [(4096, 1024, 1), (640, 2048, 40), (1000, 960, 300), (20000, 128, 200), (1000, 2048, 12)])
+@pytest.mark.parametrize("rows,cols,n", [(4096, 1024, 1), (640, 2048, 40), (1000, 960, 300), (20000, 128, 200), (1000, 2048, 12),
+                                         (1000, 8192, 300)])
 def test_products_on_two_streams_and_in_graphs(ops, rows, cols, n):
     """Calls on two streams at once, each with its scratch, and a captured call replayed on new codes."""
     rng = np.random.default_rng(n)
