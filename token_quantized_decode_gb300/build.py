@@ -12,6 +12,7 @@ import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from importlib import util
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -71,13 +72,18 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
         return obj, r.stderr
 
     def compile_call():
-        # the tensor wrappers' common case, a CPython module of its own
+        # the tensor wrappers' common case, a CPython module of its own (torch's libraries are loaded before it is)
         tmp = CALL + f".tmp{os.getpid()}"
-        cmd = ["gcc", "-O2", "-std=gnu11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-               os.path.join(CSRC, "tqd_call.c"), "-o", tmp, "-ldl"]
+        torch = list(util.find_spec("torch").submodule_search_locations)[0]
+        cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+        cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+               "-isystem", os.path.join(torch, "include"), "-isystem",
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+               os.path.join(CSRC, "tqd_call.cpp"), "-o", tmp, "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda",
+               "-ltorch_cpu", "-ltorch_python", "-ldl"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"gcc failed for tqd_call.c:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"g++ failed for tqd_call.cpp:\n{r.stdout}\n{r.stderr}")
         return tmp
 
     with ThreadPoolExecutor(len(SOURCES) + 2) as ex:

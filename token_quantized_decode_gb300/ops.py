@@ -22,7 +22,7 @@ def _bind():
     _stream_of = raw if raw is not None else lambda d: int(t.cuda.current_stream(d).cuda_stream)
     lib()  # (says so if it has not been built)
     _call = call_module()
-    _call.bind(LIB_PATH, _F32, _I32, _U8, _I8, _stream_of, getattr(t._C, "_cuda_getDevice", _device) if t.cuda.is_available() else _device)
+    _call.bind(LIB_PATH)
     torch = t
 
 
@@ -334,7 +334,7 @@ def tqd_op_logprobs(logits, targets, logprob, entropy, top_ids, top_logprobs, sc
 
 # ------------------------------------------------------------------ rows of 8-bit codes, rotation of many rows
 #
-# _call (csrc/tqd_call.c) makes a call whose tensors are of the common form, in half the time that the checks
+# _call (csrc/tqd_call.cpp) makes a call whose tensors are of the common form, in a fifth of the time that the checks
 # below take; what it does not take, or the library refuses, goes through them.
 
 def _shape(t, where, name):
