@@ -607,6 +607,38 @@ def test_refusals_of_tensors(ops, TQDError):
     torch.cuda.synchronize()
 
 
+def test_common_calls_are_the_module_s(ops):
+    """The compiled module makes the calls of tensors as they come, in strided rows and on a given stream too, and leaves
+    derived classes and refusals to the checks in Python."""
+    ops._bind()
+    call, f = ops._call, lambda *s: torch.ones(*s, device="cuda")
+    c = lambda *s: torch.ones(*s, dtype=torch.int8, device="cuda")  # noqa: E731
+    pos, side = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    x, wide, q, s, room = f(3, 64), f(3, 128)[:, :64], c(3, 64), f(3), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for x in (x, wide):
+        for st in (None, side):
+            assert call.rows_i8(x, q, s, st) is True
+            assert call.rmsnorm_i8(x, None, f(64), 1e-6, None, q, s, st) is True
+            assert call.rmsnorm_i8(x, x, f(64), 1e-6, x, q, s, st) is True
+            assert call.silu_mul_i8(x, x, q, s, st) is True
+            assert call.rows_i8_read(q, s, x, st) is True
+            assert call.i8_matmul(c(64, 64), f(64), q, s, x, None, st) is True
+            assert call.i8_matmul(c(64, 64), f(64), c(70, 64), f(70), f(70, 64), room, st) is True
+            assert call.rope_rows(x, pos, f(5, 32), 32, 32, False, x, st) is True
+    assert call.rows_i8(f(64), c(1, 64), f(1), None) is True
+    torch.cuda.synchronize()
+
+    class Derived(torch.Tensor):
+        pass
+    assert call.rows_i8(f(3, 64).as_subclass(Derived), q, s, None) is None
+    assert call.rows_i8(f(64, 3).t(), q, s, None) is None and call.rows_i8(f(1, 64).expand(3, 64), q, s, None) is None
+    assert call.i8_matmul(c(64, 64), f(64), c(70, 64), f(70), f(70, 64), None, None) is None
+    assert call.i8_matmul(c(64, 64), f(64), c(70, 64), f(70), f(70, 64), room[:100], None) is None
+    assert call.rows_i8(x, q, f(2), None) is None and call.rows_i8(x.double(), q, s, None) is None
+    torch.cuda.synchronize()
+
+
 def test_empty_calls(ops):
     e = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device="cuda")  # noqa: E731
     q, s = e(0, 64, t=torch.int8), e(0)

@@ -25,6 +25,19 @@ def f(i):
     return P + 4 * i
 
 
+def test_calls_that_the_module_does_not_take(L):
+    """The compiled module answers None, and raises nothing, for whatever is not a call on the current device's tensors."""
+    torch = pytest.importorskip("torch")
+    ops._bind()
+    call = ops._call
+    x, q, s = torch.zeros(2, 32), torch.zeros(2, 32, dtype=torch.int8), torch.zeros(2)
+    for f in (call.rows_i8, call.rmsnorm_i8, call.silu_mul_i8, call.rows_i8_read, call.i8_matmul, call.rope_rows):
+        for args in ((), (None,) * 4, (1, "a", 2.0, None), (x, q, s, None), (q, s, x, None), (x, x, q, s, None), (x, x, q, s, 3),
+                     (x, None, s, 1e-6, None, q, s, None), (q, s, q, s, x, None, None), (x, s, x, 32, 32, False, x, None),
+                     (x, s, x, 0, 1 << 80, None, x, "stream")):
+            assert f(*args) is None
+
+
 def test_kinds_of_scaling_are_the_package_s():
     import token_quantized_decode_gb300 as tqd
     names = ("TQD_ROPE_UNSCALED", "TQD_ROPE_LINEAR", "TQD_ROPE_BY_ROTATIONS", "TQD_ROPE_BY_INDEX")

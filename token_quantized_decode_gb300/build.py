@@ -44,9 +44,24 @@ def _deps_mtime() -> float:
     return max(t, os.path.getmtime(__file__), os.path.getmtime(SYNTH_SRC))
 
 
+def _torch() -> str | None:
+    """Where torch is installed: the call module is built against it, and left out where there is none."""
+    spec = util.find_spec("torch")
+    return spec and list(spec.submodule_search_locations)[0]
+
+
+def _newest() -> bool:
+    t = _deps_mtime()
+    if not os.path.exists(LIB) or os.path.getmtime(LIB) < t:
+        return False
+    torch = _torch()
+    return torch is None or (os.path.exists(CALL) and
+                             os.path.getmtime(CALL) >= max(t, os.path.getmtime(os.path.join(torch, "version.py"))))
+
+
 def build(force: bool = False, verbose: bool = False, extra: list | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, CALL)):
+    if not force and _newest():
         return LIB
     extra = list(extra or [])
     if verbose:
@@ -73,8 +88,9 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
 
     def compile_call():
         # the tensor wrappers' common case, a CPython module of its own (torch's libraries are loaded before it is)
-        tmp = CALL + f".tmp{os.getpid()}"
-        torch = list(util.find_spec("torch").submodule_search_locations)[0]
+        tmp, torch = CALL + f".tmp{os.getpid()}", _torch()
+        if torch is None:
+            return None
         cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
         cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
                "-isystem", os.path.join(torch, "include"), "-isystem",
@@ -100,7 +116,8 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    os.replace(call, CALL)
+    if call:
+        os.replace(call, CALL)
     return LIB
 
 
