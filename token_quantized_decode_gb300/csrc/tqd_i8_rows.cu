@@ -243,14 +243,18 @@ template <int kKind, int kT, int kE>
 struct RowsCfg {
   static constexpr int block = kT < 128 ? 128 : kT;
   static constexpr int inputs = kKind == kI8Rows ? 1 : 2, ahead = kKind == kI8Rows ? 2 : 1;
-  static constexpr int smem = block * kE * 16 * inputs * ahead;
+  // The norm's g is kept beside the rows up to 2048 columns (8192 x 1024 23.4 -> 21.2 us, 8191 x 2048 39.7 -> 38.3), and read
+  // again for each wider row, which leaves L1 more room (4099 x 4096 39.7 us and kept 42.2, 2053 x 8192 47.2 and 55.8).
+  static constexpr bool keeps_g = kKind == kI8Norm && kT * kE <= 512;
+  static constexpr int parts = inputs * ahead + keeps_g;  // of kE groups a thread
+  static constexpr int smem = block * kE * 16 * parts;
   static constexpr int ctas = kT >= 1024 ? 1 : kT == 512 ? 2 : kT == 256 ? (kE == 4 ? 3 : 5)
                               : kE == 4 ? 5 : kKind == kI8Rows ? 8 : kKind == kI8Norm ? 6 : 7;
   };
 
 // kT threads a row, kE groups of four elements a thread.  Measured, in TB/s of the bytes that it must move (a copy of
 // as many: 6.8): rows 4099 x 4096 5.2 (16.3 us), norm with a sum that is kept 5.5 (39.4), SwiGLU 5.3
-// (28.6); a single row of 1024 1.2, 2.0 and 2.3 us.  HBM bounds the norm up to 4096 columns; wider rows have two
+// (28.6); a single row of 1024 1.2, 2.0 and 2.1 us.  HBM bounds the norm up to 4096 columns; wider rows have two
 // CTAs or one an SM, which wait at a row's barrier together (1500 x 12288 norm 3.8 TB/s); SwiGLU's instructions
 // (2.6 a clock and SM) and its barrier bound it.  kVec: every row of every tensor
 // begins on a 16-byte boundary (codes: 4) and is whole groups of four.  CTAs go from row to
@@ -260,7 +264,7 @@ template <int kKind, int kT, int kE, bool kVec>
 __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, kT, kE>::ctas)
     k_rows_i8(const __grid_constant__ I8RowsArgs a) {
   using Cfg = RowsCfg<kKind, kT, kE>;
-  extern __shared__ float4 next_rows[];  // [ahead][inputs][kE][block]
+  extern __shared__ float4 next_rows[];  // [ahead][inputs][kE][block], then g, [kE][block]
   __shared__ uint32_t sh_max[2][32];     // the largest |y| of each warp, as bits
   __shared__ float sh_sum[2][32];
   __shared__ double sh_d[32];
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
   pdl_wait();
   // (past a row's end its places hold zeros from here on: copies leave them)
 #pragma unroll
-  for (int i = 0; i < Cfg::ahead * Cfg::inputs * kE; ++i)
+  for (int i = 0; i < Cfg::parts * kE; ++i)
     if ((i % kE * kT + t) * 4 + 3 >= n) next_rows[i * Cfg::block + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
   const uint32_t place = smem_addr(next_rows + threadIdx.x);
   auto fetch = [&](int at, int64_t r) {  // (a row past the last: nothing, but a group of its own)
@@ -291,6 +295,11 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  if (Cfg::keeps_g) {  // g, once for all of its rows (comes with the first)
+#pragma unroll(kVec ? kE : 1)
+    for (int e = 0; e < kE; ++e)
+      fetch4<kVec>(place + (Cfg::inputs * Cfg::ahead * kE + e) * (Cfg::block * 16), a.g + (e * kT + t) * 4, n - (e * kT + t) * 4);
+  }
 #pragma unroll
   for (int i = 0; i < Cfg::ahead; ++i) fetch(i, row + i * step);
   if (kKind != kI8Rows) {
@@ -341,7 +350,12 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
         }
       }
       float g[4];
-      load4<kVec>(a.g, i, n, g);
+      if (Cfg::keeps_g) {
+        const float4 kept = next_rows[(Cfg::inputs * Cfg::ahead * kE + e) * Cfg::block + threadIdx.x];
+        g[0] = kept.x, g[1] = kept.y, g[2] = kept.z, g[3] = kept.w;
+      } else {
+        load4<kVec>(a.g, i, n, g);
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         ss = fmaf(w[e][j], w[e][j], ss);
@@ -458,7 +472,7 @@ template <int kKind, int kT, int kE>
 cudaError_t launch_rows(const I8RowsArgs& a, bool vec, cudaStream_t st) {
   using Cfg = RowsCfg<kKind, kT, kE>;
   const auto kernel = vec ? k_rows_i8<kKind, kT, kE, true> : k_rows_i8<kKind, kT, kE, false>;
-  if (Cfg::smem > 48 * 1024) {
+  if (Cfg::smem > 40 * 1024) {  // (of 48 KB that need no leave, the rest is for what has a fixed place)
     static unsigned long long done[2] = {0, 0};
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Cfg::smem, &done[vec]);
     if (e != cudaSuccess) return e;
