@@ -373,8 +373,9 @@ size_t tqd_attention_scratch_bytes(int32_t n_heads, int32_t n_kv, int32_t head_d
  * waits cannot complete (an mbarrier no thread arrives at, and a counter that
  * nothing increments, polled the way a grid barrier is); each gives up after
  * its 2 s limit, records its error bit and returns.  *err_bits_out receives
- * the bits (1: counter wait, 2: mbarrier wait, and 4 should the lanes of a warp
- * disagree about a wait that ran out in some of them only); the status is
+ * the bits (1: counter wait, 2: mbarrier wait, 4 should the lanes of a warp
+ * disagree about a wait that ran out in some of them only, and 8 should waits that
+ * follow one which ran out be answered as if all were well); the status is
  * TQD_ERR_DEVICE_TIMEOUT when any is set.  The CUDA context stays usable.
  * Takes about 2 s ("One command buffer per token", "The seam": a failed step
  * is reported, not hung on). */

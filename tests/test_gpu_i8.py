@@ -402,6 +402,13 @@ def test_products_on_two_streams_and_in_graphs(ops, rows, cols, n):
             assert np.array_equal(y.cpu().numpy(), want[k])
 
 
+def test_nothing_is_believed_after_a_wait_that_ran_out(ops):
+    """A product's readers wait for two barriers in turn: two runs after the one that never came the parity is that of a
+    phase that is over, and a tile that nobody made would be written as numbers."""
+    status, bits = ops.tqd_op_wait_selftest()
+    assert status != 0 and not bits & 8
+
+
 # ------------------------------------------------------------------ rotation
 
 @pytest.mark.parametrize("kind,factor,original,low,high,att", [(0, 1.0, 0, 1.0, 32.0, 1.0), (1, 4.0, 0, 1.0, 32.0, 1.0),

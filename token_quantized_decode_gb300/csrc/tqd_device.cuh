@@ -100,6 +100,50 @@ __device__ __forceinline__ void mbar_ring_drain(uint64_t* bars, int stages) {
   for (int i = 0; i < 2 * stages; ++i) mbar_wait_warp(&bars[i >> 1], i & 1, kWaitLimitNs / 4);
 }
 
+// Wait for a phase; false once any wait of the CTA ran out of time (which *dead says).  The
+// timer takes longer to read than most waits last: it is read after 64 tries, and then every 64.
+// (kPair: what the other CTA did before it arrived is seen too.)
+template <bool kPair = false>
+__device__ __forceinline__ bool mbar_wait_or_dead(uint64_t* bar, uint32_t parity, volatile int* dead,
+                                                  uint64_t limit_ns = kWaitLimitNs) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    if (kPair)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_addr(bar)), "r"(parity)
+          : "memory");
+    else
+      ok = mbar_try_wait(bar, parity);
+    if (ok) return true;
+    if (i % 64) continue;
+    if (*dead) return false;
+    const uint64_t now = global_timer_ns();
+    if (!t0) t0 = now;
+    if (now - t0 > limit_ns) {
+      *dead = 1;
+      return false;
+    }
+  }
+}
+
+// A warp's waits for what two barriers announce in turn, over all of a CTA's tiles.  After one that
+// ran out nothing is asked for any more: two runs on, the parity is that of the phase before the one that
+// never ended, and the wait would be answered at once.
+struct SumsWait {
+  uint64_t* full;  // [2]
+  volatile int* dead;
+  int run = 0;
+  bool ok = true;
+  __device__ __forceinline__ bool next(uint64_t limit_ns = kWaitLimitNs) {
+    if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_dead(&full[run & 1], (run / 2) & 1, dead, limit_ns));
+    ++run;
+    return ok;
+  }
+};
+
 // Global -> shared bulk copy completing on `bar` (both addresses 16-byte
 // aligned, bytes a multiple of 16).
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes,

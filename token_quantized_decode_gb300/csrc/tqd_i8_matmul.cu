@@ -363,34 +363,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   }
 }
 
-// Wait for a phase; false once any wait of the CTA ran out of time (which *dead says).  The
-// timer takes longer to read than most waits last: it is read after 64 tries, and then every 64.
-// (kPair: what the other CTA did before it arrived is seen too.)
-template <bool kPair = false>
-__device__ __forceinline__ bool big_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    uint32_t ok;
-    if (kPair)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_addr(bar)), "r"(parity)
-          : "memory");
-    else
-      ok = mbar_try_wait(bar, parity);
-    if (ok) return true;
-    if (i % 64) continue;
-    if (*dead) return false;
-    const uint64_t now = global_timer_ns();
-    if (!t0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
-      *dead = 1;
-      return false;
-    }
-  }
-}
-
 struct BigArgs {
   const uint8_t* image;  // [steps][tokens, whole groups][K] f16
   const float *x_scale, *w_scale;
@@ -452,7 +424,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
       const int share = min(kTN, a.padded - j0) / Cfg::ctas, mine = j0 + (kPair ? rank * share : 0);  // tokens of the image
       const uint32_t bytes = Cfg::raw_tokens ? Cfg::raw : share * Cfg::K * 2;
       for (int k = from; k < from + steps; ++k) {
-        if (issued >= Cfg::stages) ok = __all_sync(0xFFFFFFFFu, big_wait(&empty[s], phase ^ 1, dead));
+        if (issued >= Cfg::stages) ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_dead(&empty[s], phase ^ 1, dead));
         if (!ok) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&full[s], Cfg::w_raw + bytes);
@@ -489,11 +461,11 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
         int left = (a.cols - from * Cfg::K) / 16;  // instructions of 16 columns (more than this CTA's where others follow)
         for (int k0 = 0; ok && k0 < steps; k0 += Cfg::run, ++run) {
           const uint32_t d = tmem + (run & 1) * kTN;
-          if (run >= 2) ok = big_wait<kPair>(&sums_empty[run & 1], (run / 2 - 1) & 1, dead);
+          if (run >= 2) ok = mbar_wait_or_dead<kPair>(&sums_empty[run & 1], (run / 2 - 1) & 1, dead);
           const int end = min(steps, k0 + Cfg::run);
           for (int k = k0; ok && k < end; ++k, left -= Cfg::K / 16) {
             // (ready follows full: the converting warps waited for that)
-            if (!there && !big_wait<kPair>(&ready[s], phase, dead)) {
+            if (!there && !mbar_wait_or_dead<kPair>(&ready[s], phase, dead)) {
               ok = false;
               break;
             }
@@ -525,7 +497,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
     const int total = (tiles - first + stride - 1) / stride * steps;  // (first < tiles)
     for (int g = warp / 4 - 1; g < total; g += kConverters) {
       const int s = g % Cfg::stages, at = g % Cfg::a_stages;
-      if (!__all_sync(0xFFFFFFFFu, big_wait(&full[s], (g / Cfg::stages) & 1, dead))) break;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_dead(&full[s], (g / Cfg::stages) & 1, dead))) break;
       const uint8_t* from_w = raw + s * Cfg::w_raw + row * Cfg::K;
       uint4 w[kPieces];
 #pragma unroll
@@ -547,6 +519,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
+      bool there = true;
       const uint32_t operand = tmem + Cfg::a_col + at * (Cfg::K / 2) + (static_cast<uint32_t>(quad * 32) << 16);
 #pragma unroll
       for (int h = 0; h < kPieces / 4; ++h) {
@@ -561,10 +534,12 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
         // (converted before the wait for the operand that stood there to be used)
         if (h == 0 && Cfg::a_stages < Cfg::stages && g >= Cfg::a_stages) {
           const int before = g - Cfg::a_stages;
-          __all_sync(0xFFFFFFFFu, big_wait(&empty[before % Cfg::stages], (before / Cfg::stages) & 1, dead));
+          there = __all_sync(0xFFFFFFFFu, mbar_wait_or_dead(&empty[before % Cfg::stages], (before / Cfg::stages) & 1, dead));
+          if (!there) break;
         }
         tmem_st32(operand + h * 32, v);
       }
+      if (!there) break;  // (an operand that may be in use stays; no sums are made without this one)
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
@@ -574,7 +549,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
     constexpr int kCols = kTN / (Cfg::readers / 4);  // a warp's columns
     const int quad = warp & 3, c0 = (warp - 4 - 4 * kConverters) / 4 * kCols;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    int run = 0;
+    SumsWait sums_there{sums_full, dead};
     for (int tile = first; tile < tiles; tile += stride) {
       const int row = tile / a.token_tiles * (kBigM * Cfg::ctas) + upper + quad * 32 + lane, j0 = tile % a.token_tiles * kTN;
       const int width = min(kTN, a.padded - j0);
@@ -583,9 +558,10 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
 #pragma unroll
       for (int i = 0; i < kCols; ++i) total[i] = 0;
       bool ok = true;
-      for (int k0 = 0; k0 < steps; k0 += Cfg::run, ++run) {
-        const int b = run & 1;
-        ok = __all_sync(0xFFFFFFFFu, big_wait(&sums_full[b], (run / 2) & 1, dead)) && ok;
+      for (int k0 = 0; k0 < steps; k0 += Cfg::run) {
+        const int b = sums_there.run & 1;
+        ok = sums_there.next();
+        if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
         for (int c = 0; c < kCols; c += 8) {
@@ -605,7 +581,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
 #pragma unroll
         for (int i = 0; i < kCols; ++i) sums[(c0 + i) * kBigM + quad * 32 + lane] = total[i];
       } else {
-        // (after a wait that ran out: NaN)
+        // (after a wait that ran out: NaN, in this tile and all that follow)
         const float w_scale = ok ? sw : __uint_as_float(0x7FC00000u);
         float* y = a.y + (j0 + c0) * a.y_stride + row;
 #pragma unroll

@@ -456,16 +456,20 @@ cudaError_t launch_op_argmax(const float* x, int64_t n, int32_t* out, float* can
 // arrives at (the bounded wait the ring and tensor-core kernels use); thread 32
 // polls a counter nothing increments, the way a grid barrier does.  Both give
 // up after kWaitLimitNs, set their error bits and return, and the context
-// stays usable.  Warp 2 checks that a warp's wait has one answer for all lanes.
-constexpr uint32_t kWaitLanes = 4u;
+// stays usable.  Warp 2 checks that a warp's wait has one answer for all lanes, warp 4 that
+// nothing that follows a wait which ran out passes for done.
+constexpr uint32_t kWaitLanes = 4u, kWaitAfter = 8u;
 __device__ uint32_t g_wait_err;
 __device__ unsigned long long g_wait_ctr;  // never incremented
 
 __global__ void k_wait_selftest() {
-  __shared__ __align__(8) uint64_t bar, late[4];
+  __shared__ __align__(8) uint64_t bar, late[4], sums[2];
+  __shared__ int dead;
   if (threadIdx.x == 0) {
     g_wait_err = 0u;
+    dead = 0;
     mbar_init(&bar, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sums[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&late[i], 1);
     fence_mbar_init();
   }
@@ -504,11 +508,21 @@ __global__ void k_wait_selftest() {
       while (global_timer_ns() - t0 < (i + 1) * 200000000ull) __nanosleep(1000000);
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&late[i])) : "memory");
     }
+  } else if (threadIdx.x >= 128) {
+    // a product's reader, one run a tile: runs 0 to 2 are announced, no later one is
+    SumsWait wait{sums, &dead};
+    bool right = true;
+    for (int run = 0; run < 9; ++run) {
+      if (threadIdx.x == 128 && run < 3) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&sums[run & 1])) : "memory");
+      __syncwarp();
+      right = wait.next(1000000ull) == (run < 3) && right;
+    }
+    if (threadIdx.x == 128 && !right) atomicOr(&g_wait_err, kWaitAfter);
   }
 }
 
 cudaError_t run_wait_selftest(uint32_t* err_bits, cudaStream_t st) {
-  k_wait_selftest<<<1, 128, 0, st>>>();
+  k_wait_selftest<<<1, 160, 0, st>>>();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = cudaMemcpyFromSymbolAsync(err_bits, g_wait_err, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, st);
