@@ -402,6 +402,27 @@ def test_products_on_two_streams_and_in_graphs(ops, rows, cols, n):
             assert np.array_equal(y.cpu().numpy(), want[k])
 
 
+@pytest.mark.parametrize("rows,cols,n", [(8192, 512, 400), (40000, 64, 170), (5000, 992, 511), (1000, 2048, 12), (20000, 640, 64)])
+def test_products_one_after_another(ops, rows, cols, n):
+    """Many short products in a row, with row operators between them: a CTA's shared memory serves the next kernel as soon as it
+    is given up."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    draw = lambda *s: torch.randint(-128, 128, s, dtype=torch.int8, device="cuda", generator=g)  # noqa: E731
+    w, X = draw(rows, cols), [draw(n, cols) for _ in range(4)]
+    ws, xs = torch.rand(rows, device="cuda", generator=g), torch.rand(n, device="cuda", generator=g)
+    want = [(x.double() @ w.double().T).float() * xs[:, None] * ws for x in X]
+    scratch = torch.empty(ops.tqd_i8_matmul_scratch_bytes(rows, cols, n), dtype=torch.uint8, device="cuda")
+    Y = [torch.zeros(n, rows, device="cuda") for _ in X]
+    rows_x = torch.randn(n, cols, device="cuda", generator=g)
+    q, s = torch.empty(n, cols, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+    for k in range(100):
+        ops.tqd_op_i8_matmul(w, ws, X[k % 4], xs, Y[k % 4], scratch)
+        if k % 3 == 0:
+            ops.tqd_op_rows_i8(rows_x, q, s)
+    assert all(torch.equal(y, v) for y, v in zip(Y, want))
+
+
 def test_nothing_is_believed_after_a_wait_that_ran_out(ops):
     """A product's readers wait for two barriers in turn: two runs after the one that never came the parity is that of a
     phase that is over, and a tile that nobody made would be written as numbers."""

@@ -276,13 +276,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
 }
-// An arrival at `bar` (of both CTAs of a pair) once the thread's products so far are over.
+// An arrival at `bar` (of a pair's CTAs, those of the mask) once the thread's products so far are over.
 template <bool kPair>
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint16_t ctas = 3) {
   if (kPair)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(ctas)
         : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -441,10 +441,13 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
         if (++s == Cfg::stages) s = 0, phase ^= 1;
       }
     }
-    // whatever the others do, what is still under way lands before the CTA ends
+    // Whatever the others do, what is still under way lands before the CTA ends: copies, and each stage's last arrival at
+    // empty, which a commit makes by itself, in a pair at both CTAs.  (The readers waited for all at sums_full.  After a
+    // wait that ran out there may be none to come.)
     for (int i = 0; i < issued; ++i) {
       if (--s < 0) s = Cfg::stages - 1, phase ^= 1;
       mbar_wait_warp(&full[s], phase, kWaitLimitNs / 4);
+      mbar_wait_warp(&empty[s], phase, *dead ? 1000000ull : kWaitLimitNs / 4);
     }
   } else if (warp == 1) {
     // One thread, which looks for the next stage while this one's MMAs are issued: the tensor cores hold one or two
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
           if (ok) mma_commit<kPair>(&sums_full[run & 1]);
         }
       }
-      mma_commit<kPair>(&done);  // tensor memory is given back once every MMA is over
+      mma_commit<kPair>(&done, 1);  // tensor memory is given back once every MMA is over
       mbar_wait_bounded(&done, 0, nullptr, kWaitLimitNs / 4);
     }
   } else if (warp >= 4 && warp < 4 + 4 * kConverters) {
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  if (kPair) cluster_barrier();  // (and nothing arrives at a CTA that is gone)
+  if (kPair) cluster_barrier();  // (and no thread arrives at a CTA that is gone)
   else __syncthreads();
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
