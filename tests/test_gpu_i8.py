@@ -667,6 +667,37 @@ def test_common_calls_are_the_module_s(ops):
     torch.cuda.synchronize()
 
 
+def test_calls_without_the_call_module(ops, monkeypatch, tmp_path):
+    """What the module makes and what the checks in Python make is the same, to the bit."""
+    from token_quantized_decode_gb300 import _lib
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    f = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    x, add, gain, w, table, pos = f(70, 96), f(70, 96), f(96), f(40, 96), f(9, 32), torch.arange(70, dtype=torch.int32, device="cuda") % 11
+
+    def calls():
+        c = lambda n, w: (torch.zeros(n, w, dtype=torch.int8, device="cuda"), torch.zeros(n, device="cuda"))  # noqa: E731
+        wq, a, b, s, y, back = c(40, 96), c(70, 96), c(70, 96), torch.zeros(70, 96, device="cuda"), torch.zeros(70, 40, device="cuda"), f(70, 96)
+        ops.tqd_op_rows_i8(w, *wq)
+        ops.tqd_op_rmsnorm_i8(x, add, gain, 1e-6, s, *a)
+        ops.tqd_op_silu_mul_i8(x, add, *b)
+        ops.tqd_op_rows_i8_read(*b, back)
+        ops.tqd_op_i8_matmul(*wq, *a, y, torch.zeros(ops.tqd_i8_matmul_scratch_bytes(40, 96, 70), dtype=torch.uint8, device="cuda"))
+        out = x.clone()
+        ops.tqd_op_rope_rows(out, pos, table, 48, 32, True, out)
+        return [*wq, *a, *b, s, y, back, out]
+    ops._bind()
+    fast = calls()
+    monkeypatch.setattr(_lib, "CALL_PATH", str(tmp_path / "none.so"))
+    ops._bind()
+    try:
+        slow = calls()
+    finally:
+        monkeypatch.undo()
+        ops._bind()
+    assert all(torch.equal(a, b) for a, b in zip(fast, slow))
+
+
 def test_empty_calls(ops):
     e = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device="cuda")  # noqa: E731
     q, s = e(0, 64, t=torch.int8), e(0)

@@ -211,3 +211,36 @@ def test_wrappers_refuse_tensors_that_are_not_on_the_device(L):
         with pytest.raises(_lib.TQDError) as e:
             call()
         assert e.value.status == BAD
+
+
+@pytest.fixture
+def without_the_call_module(monkeypatch):
+    """The tensor wrappers as they are where the compiled module cannot be had."""
+    pytest.importorskip("torch")
+
+    def hide(path):
+        monkeypatch.setattr(_lib, "CALL_PATH", str(path))
+        ops._bind()
+    yield hide
+    monkeypatch.undo()
+    ops._bind()
+
+
+@pytest.mark.parametrize("what", ["absent", "not a library"])
+def test_wrappers_go_on_without_the_call_module(L, without_the_call_module, tmp_path, what):
+    """The checks in Python are complete: neither the operators that have a call in the module nor the others need it."""
+    torch = pytest.importorskip("torch")
+    path = tmp_path / "_tqd_call.so"
+    if what == "absent":
+        without_the_call_module(path)
+    else:
+        path.write_bytes(b"no library")
+        with pytest.warns(RuntimeWarning, match="call module"):
+            without_the_call_module(path)
+    test_wrappers_refuse_tensors_that_are_not_on_the_device(L)
+    x = torch.zeros(2, 64)
+    for call in (lambda: ops.tqd_op_q4_0_matvec(torch.zeros(10, dtype=torch.uint8), 2, 64, x, x),
+                 lambda: ops.tqd_op_logprobs(x, torch.zeros(2, dtype=torch.int32), x, x, None, None, x)):
+        with pytest.raises(_lib.TQDError) as e:
+            call()
+        assert e.value.status == BAD

@@ -5,7 +5,7 @@ from __future__ import annotations
 
 from ctypes import byref
 
-from ._lib import LIB_PATH, TQDError, call_module, check, lib, tqd_kv_q4, tqd_rope_scaling
+from ._lib import TQDError, call_module, check, lib, tqd_kv_q4, tqd_rope_scaling
 
 
 torch = None  # bound at the first call (the rest of the package does not need it)
@@ -22,7 +22,6 @@ def _bind():
     _stream_of = raw if raw is not None else lambda d: int(t.cuda.current_stream(d).cuda_stream)
     lib()  # (says so if it has not been built)
     _call = call_module()
-    _call.bind(LIB_PATH)
     torch = t
 
 
@@ -335,7 +334,7 @@ def tqd_op_logprobs(logits, targets, logprob, entropy, top_ids, top_logprobs, sc
 # ------------------------------------------------------------------ rows of 8-bit codes, rotation of many rows
 #
 # _call (csrc/tqd_call.cpp) makes a call whose tensors are of the common form, in a fifth of the time that the checks
-# below take; what it does not take, or the library refuses, goes through them.
+# below take; what it does not take, or the library refuses, goes through them (everything, where there is no such module).
 
 def _shape(t, where, name):
     """(rows, width) of [rows, width], or of [width] as one row."""
