@@ -244,3 +244,37 @@ def test_wrappers_go_on_without_the_call_module(L, without_the_call_module, tmp_
         with pytest.raises(_lib.TQDError) as e:
             call()
         assert e.value.status == BAD
+
+
+@pytest.mark.parametrize("made_for", [None, "torch 1.0 cpython-39-x86_64-linux-gnu"])
+def test_a_call_module_for_another_torch_is_not_loaded(L, without_the_call_module, tmp_path, made_for):
+    """It would read tensors' sizes and pointers at that torch's offsets."""
+    path = tmp_path / "_tqd_call.so"
+    path.write_bytes(open(tqd_build.CALL, "rb").read())
+    if made_for:
+        (tmp_path / "_tqd_call.so.for").write_text(made_for)
+    with pytest.warns(RuntimeWarning, match="built for " + (made_for or "nothing")):
+        without_the_call_module(path)
+    test_wrappers_refuse_tensors_that_are_not_on_the_device(L)
+    (tmp_path / "_tqd_call.so.for").write_text(open(tqd_build.CALL_FOR).read())
+    without_the_call_module(path)
+    assert hasattr(ops._call, "bind")
+
+
+def test_a_call_module_for_another_torch_is_built_again(L, monkeypatch, tmp_path):
+    """Whatever the files' times say."""
+    pytest.importorskip("torch")
+    assert tqd_build._newest()
+    other = tmp_path / "for"
+    other.write_text("torch 1.0 cpython-39-x86_64-linux-gnu")
+    monkeypatch.setattr(tqd_build, "CALL_FOR", str(other))
+    assert not tqd_build._newest()
+
+
+def test_a_call_module_that_does_not_load_is_left_out(L, without_the_call_module, tmp_path):
+    path = tmp_path / "_tqd_call.so"
+    path.write_bytes(b"no library")
+    (tmp_path / "_tqd_call.so.for").write_text(open(tqd_build.CALL_FOR).read())
+    with pytest.warns(RuntimeWarning, match="does not load"):
+        without_the_call_module(path)
+    test_wrappers_refuse_tensors_that_are_not_on_the_device(L)

@@ -158,20 +158,33 @@ class _NoCalls:
     rows_i8 = rmsnorm_i8 = silu_mul_i8 = rows_i8_read = i8_matmul = rope_rows = staticmethod(lambda *args: None)
 
 
-def call_module():
+def call_module(torch_version: str):
     """The compiled module of the tensor wrappers' common case, bound to the library.  Where there is none (a build without
-    torch), or none that loads, the wrappers' checks in Python make every call."""
+    torch), or none that loads and was built for this torch and Python, the wrappers' checks in Python make every call."""
     from importlib import machinery, util
+
+    from .build import call_made_for
     if not os.path.exists(CALL_PATH):
         return _NoCalls
-    loader = machinery.ExtensionFileLoader("_tqd_call", CALL_PATH)
     try:
-        module = util.module_from_spec(util.spec_from_loader("_tqd_call", loader))
-        loader.exec_module(module)
-        module.bind(LIB_PATH)
-    except ImportError as e:
+        with open(CALL_PATH + ".for") as f:
+            made_for = f.read()
+    except OSError:
+        made_for = "nothing that is written beside it"
+    why = None
+    if made_for != call_made_for(torch_version):
+        why = f"was built for {made_for}, this is {call_made_for(torch_version)}; building again makes it anew"
+    else:
+        loader = machinery.ExtensionFileLoader("_tqd_call", CALL_PATH)
+        try:
+            module = util.module_from_spec(util.spec_from_loader("_tqd_call", loader))
+            loader.exec_module(module)
+            module.bind(LIB_PATH)
+        except ImportError as e:
+            why = f"does not load ({e})"
+    if why:
         import warnings
-        warnings.warn(f"the call module {CALL_PATH} does not load ({e}): calls with tensors are marshalled in Python", RuntimeWarning)
+        warnings.warn(f"the call module {CALL_PATH} {why}: calls with tensors are marshalled in Python", RuntimeWarning)
         return _NoCalls
     return module
 

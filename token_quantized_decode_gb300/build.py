@@ -8,6 +8,7 @@ caller's back.
 from __future__ import annotations
 
 import os
+import runpy
 import subprocess
 import sys
 import sysconfig
@@ -21,6 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtqd.so")
 CALL = os.path.join(BUILD, "_tqd_call.so")
+CALL_FOR = CALL + ".for"  # which torch and Python it was compiled against
 SYNTH_SRC = os.path.join(ROOT, "synth", "tqd_synth.c")
 
 SOURCES = ["tqd_kernels.cu", "tqd_persist.cu", "tqd_persist_bf16.cu", "tqd_engine.cu", "tqd_ops.cu", "tqd_noalloc.cu", "tqd_batch.cu",
@@ -50,13 +52,29 @@ def _torch() -> str | None:
     return spec and list(spec.submodule_search_locations)[0]
 
 
+def call_made_for(torch_version: str) -> str:
+    """What a call module compiled now is for: it reads tensors by torch's own layout, so no other torch or Python
+    may load it.  Written beside it."""
+    return f"torch {torch_version} {sysconfig.get_config_var('SOABI')}"
+
+
+def _torch_version(torch: str) -> str:
+    return runpy.run_path(os.path.join(torch, "version.py"))["__version__"]
+
+
 def _newest() -> bool:
     t = _deps_mtime()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < t:
         return False
     torch = _torch()
-    return torch is None or (os.path.exists(CALL) and
-                             os.path.getmtime(CALL) >= max(t, os.path.getmtime(os.path.join(torch, "version.py"))))
+    if torch is None:
+        return True
+    try:
+        with open(CALL_FOR) as f:
+            made_for = f.read()
+    except OSError:
+        return False
+    return made_for == call_made_for(_torch_version(torch)) and os.path.exists(CALL) and os.path.getmtime(CALL) >= t
 
 
 def build(force: bool = False, verbose: bool = False, extra: list | None = None) -> str:
@@ -117,7 +135,12 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if call:
+        if os.path.exists(CALL_FOR):
+            os.remove(CALL_FOR)
         os.replace(call, CALL)
+        with open(CALL_FOR + f".tmp{os.getpid()}", "w") as f:
+            f.write(call_made_for(_torch_version(_torch())))
+        os.replace(CALL_FOR + f".tmp{os.getpid()}", CALL_FOR)
     return LIB
 
 

@@ -21,7 +21,7 @@ def _bind():
     # the raw handle of the current stream: an eighth of the time that its Stream object takes to make
     _stream_of = raw if raw is not None else lambda d: int(t.cuda.current_stream(d).cuda_stream)
     lib()  # (says so if it has not been built)
-    _call = call_module()
+    _call = call_module(t.__version__)
     torch = t
 
 
