@@ -2,6 +2,9 @@
 GPU: the oracle against the definitions, and every refusal that the C ABI and the
 tensor wrappers make before anything is launched."""
 import ctypes
+import importlib.util
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -278,3 +281,54 @@ def test_a_call_module_that_does_not_load_is_left_out(L, without_the_call_module
     with pytest.warns(RuntimeWarning, match="does not load"):
         without_the_call_module(path)
     test_wrappers_refuse_tensors_that_are_not_on_the_device(L)
+
+
+@pytest.fixture
+def pretended_build(monkeypatch, tmp_path):
+    """build() into a folder of its own with compilers that only write their outputs; g++ answers what `answers` says."""
+    pytest.importorskip("torch")
+    ran, answers = [], {"g++": 0}
+    for name in ("LIB", "CALL", "CALL_FOR"):
+        monkeypatch.setattr(tqd_build, name, str(tmp_path / getattr(tqd_build, name).rsplit("/", 1)[1]))
+    monkeypatch.setattr(tqd_build, "BUILD", str(tmp_path))
+
+    def run(cmd, **kw):
+        name = cmd[0].rsplit("/", 1)[-1]
+        ran.append(name)
+        code = answers.get(name, 0)
+        if not code:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, code, "", "no such header" if code else "")
+    monkeypatch.setattr(tqd_build.subprocess, "run", run)
+    return ran, answers
+
+
+def test_the_library_is_built_where_the_call_module_is_not(pretended_build):
+    """Its compiler's errors are told, and leave the library and the wrappers' way in Python; the next build tries the module
+    alone."""
+    ran, answers = pretended_build
+    answers["g++"] = 1
+    with pytest.warns(RuntimeWarning, match="no such header"):
+        assert os.path.exists(tqd_build.build())
+    assert not os.path.exists(tqd_build.CALL) and "nvcc" in ran
+    ran.clear()
+    answers["g++"] = 0
+    tqd_build.build()
+    assert ran == ["g++"] and os.path.exists(tqd_build.CALL)
+    ran.clear()
+    tqd_build.build()
+    assert ran == []
+
+
+def test_a_torch_without_cuda_has_no_call_module(pretended_build, monkeypatch, tmp_path):
+    """There is no libc10_cuda to link it with."""
+    ran, _ = pretended_build
+    (tmp_path / "torch").mkdir()
+    (tmp_path / "torch" / "__init__.py").write_text("")
+    (tmp_path / "torch" / "version.py").write_text("__version__ = '2.0+cpu'")
+    spec = importlib.util.spec_from_file_location("torch", tmp_path / "torch" / "__init__.py", submodule_search_locations=[str(tmp_path / "torch")])
+    monkeypatch.setattr(tqd_build.util, "find_spec", lambda name: spec)
+    assert os.path.exists(tqd_build.build()) and "g++" not in ran
+    ran.clear()
+    tqd_build.build()
+    assert ran == []

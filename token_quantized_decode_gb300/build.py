@@ -12,6 +12,7 @@ import runpy
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 from importlib import util
 
@@ -47,9 +48,11 @@ def _deps_mtime() -> float:
 
 
 def _torch() -> str | None:
-    """Where torch is installed: the call module is built against it, and left out where there is none."""
+    """Where torch is installed: the call module is built against it, and left out where there is none (or one without CUDA,
+    which has not the libraries that it is linked with)."""
     spec = util.find_spec("torch")
-    return spec and list(spec.submodule_search_locations)[0]
+    where = spec and list(spec.submodule_search_locations)[0]
+    return where if where and os.path.exists(os.path.join(where, "lib", "libc10_cuda.so")) else None
 
 
 def call_made_for(torch_version: str) -> str:
@@ -62,10 +65,11 @@ def _torch_version(torch: str) -> str:
     return runpy.run_path(os.path.join(torch, "version.py"))["__version__"]
 
 
-def _newest() -> bool:
-    t = _deps_mtime()
-    if not os.path.exists(LIB) or os.path.getmtime(LIB) < t:
-        return False
+def _lib_newest() -> bool:
+    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime()
+
+
+def _call_newest() -> bool:
     torch = _torch()
     if torch is None:
         return True
@@ -74,13 +78,55 @@ def _newest() -> bool:
             made_for = f.read()
     except OSError:
         return False
-    return made_for == call_made_for(_torch_version(torch)) and os.path.exists(CALL) and os.path.getmtime(CALL) >= t
+    return (made_for == call_made_for(_torch_version(torch)) and os.path.exists(CALL) and
+            os.path.getmtime(CALL) >= _deps_mtime())
+
+
+def _newest() -> bool:
+    return _lib_newest() and _call_newest()
+
+
+def _build_call() -> None:
+    """The tensor wrappers' common case, a CPython module of its own (torch's libraries are loaded before it is).  The
+    wrappers go on without it, so what its compiler refuses is told and stops nothing."""
+    tmp, torch = CALL + f".tmp{os.getpid()}", _torch()
+    if torch is None:
+        return
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(torch, "include"), "-isystem",
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "tqd_call.cpp"), "-o", tmp, "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", "-ldl"]
+    if os.path.exists(CALL_FOR):
+        os.remove(CALL_FOR)  # (one from other sources is not loaded meanwhile, nor if this fails)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.stdout + r.stderr if r.returncode else None
+    except OSError as e:
+        why = str(e)
+    if why is not None:
+        warnings.warn(f"the call module was not built, calls with tensors are marshalled in Python: g++ failed for tqd_call.cpp:\n{why}",
+                      RuntimeWarning)
+        return
+    os.replace(tmp, CALL)
+    with open(CALL_FOR + f".tmp{os.getpid()}", "w") as f:
+        f.write(call_made_for(_torch_version(torch)))
+    os.replace(CALL_FOR + f".tmp{os.getpid()}", CALL_FOR)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    if not force and _newest():
-        return LIB
+    with ThreadPoolExecutor(1) as ex:
+        call = ex.submit(_build_call) if force or not _call_newest() else None
+        if force or not _lib_newest():
+            _build_lib(verbose, extra)
+        if call:
+            call.result()
+    return LIB
+
+
+def _build_lib(verbose: bool, extra: list | None) -> None:
     extra = list(extra or [])
     if verbose:
         extra += ["-Xptxas", "-v"]
@@ -104,27 +150,9 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
             raise RuntimeError(f"gcc failed for tqd_synth.c:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    def compile_call():
-        # the tensor wrappers' common case, a CPython module of its own (torch's libraries are loaded before it is)
-        tmp, torch = CALL + f".tmp{os.getpid()}", _torch()
-        if torch is None:
-            return None
-        cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-        cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-               "-isystem", os.path.join(torch, "include"), "-isystem",
-               os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
-               os.path.join(CSRC, "tqd_call.cpp"), "-o", tmp, "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda",
-               "-ltorch_cpu", "-ltorch_python", "-ldl"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for tqd_call.cpp:\n{r.stdout}\n{r.stderr}")
-        return tmp
-
-    with ThreadPoolExecutor(len(SOURCES) + 2) as ex:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
         futs = [ex.submit(compile_one, src) for src in SOURCES] + [ex.submit(compile_synth)]
-        call = ex.submit(compile_call)
         results = [f.result() for f in futs]
-        call = call.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -134,14 +162,6 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    if call:
-        if os.path.exists(CALL_FOR):
-            os.remove(CALL_FOR)
-        os.replace(call, CALL)
-        with open(CALL_FOR + f".tmp{os.getpid()}", "w") as f:
-            f.write(call_made_for(_torch_version(_torch())))
-        os.replace(CALL_FOR + f".tmp{os.getpid()}", CALL_FOR)
-    return LIB
 
 
 if __name__ == "__main__":
