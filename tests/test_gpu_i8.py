@@ -478,6 +478,24 @@ def test_rope_rows(ops, n, heads, hd, d, inter, pad, lead):
         assert bool((torch.as_strided(dx, (n, pad), (heads * hd + pad, 1), lead + heads * hd) == FULL).all())
 
 
+def test_rotation_of_as_many_tokens_as_an_int_counts(ops):
+    """2^31 - 1 tokens, most of them padding: rows, positions and blocks past 32 bits, in place."""
+    n = 2**31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough memory")
+    x = torch.ones(n, 2, device="cuda")
+    pos = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 1, 255, 256, 2**30 - 1, 2**30, n - 256, n - 255, n - 2, n - 1], device="cuda")
+    pos[at] = 1
+    t = torch.empty(2, 1, 2, device="cuda")
+    ops.tqd_op_rope_table_scaled(1e4, 2, 2, None, t)
+    want, _ = i8.rope_rows(np.ones((1, 2)), 1, np.array([1]), t.cpu().numpy().astype(np.float64), False)
+    ops.tqd_op_rope_rows(x, pos, t, 2, 2, False, x)
+    assert np.all(np.abs(x[at].cpu().numpy() - want) <= 2 * U * 2)
+    x[at] = 1
+    assert bool((x.view(-1)[:2**31] == 1).all()) and bool((x.view(-1)[2**31:] == 1).all())
+
+
 def test_rope_rows_agrees_with_the_rotation_of_one_token(ops):
     x = torch.randn(1, 16 * 128, device="cuda")
     t = torch.empty(50, 64, 2, device="cuda")

@@ -147,7 +147,7 @@ cudaError_t launch_rope_rows(const RopeRowsArgs& a, bool interleaved, cudaStream
   const int per_head = w > 1 ? a.head_dim / (2 * w) : a.rotary / 2 + (a.head_dim - a.rotary);
   const int units = a.heads * per_head;
   const int tokens = units >= 256 ? 1 : 256 / units;
-  const unsigned grid = static_cast<unsigned>((a.n + tokens - 1) / tokens);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.n) + tokens - 1) / tokens);  // (n: up to 2^31 - 1)
   auto mul = [](int d) { return d > 1 ? static_cast<uint32_t>((1ull << 32) / d + 1) : 0u; };
   const auto kernel = w == 4   ? interleaved ? k_rope_rows<4, true> : k_rope_rows<4, false>
                       : w == 2 ? interleaved ? k_rope_rows<2, true> : k_rope_rows<2, false>
