@@ -14,7 +14,14 @@ def rows(y, factor=1.0):
     with np.errstate(all="ignore"):
         most = np.abs(y).max(1, keepdims=True)
         bad = ~(np.isfinite(y).all(1, keepdims=True)) | ~(np.abs(np.float32(most * factor)) <= F32_MAX)
-        q = np.rint(127 * y / np.where(most > 0, most, 1))
+        t = 127 * y / np.where(most > 0, most, 1)
+        q = np.rint(t)
+        low = np.floor(t)
+        # next to a border the quotient's own rounding may decide: there by products, of 56 bits at most where y has 48
+        at = np.nonzero(np.abs(t - low - 0.5) < 1e-9)
+        row_most = np.broadcast_to(most, y.shape)[at].astype(np.longdouble)
+        side = 127 * y[at].astype(np.longdouble) - (low[at] + 0.5) * row_most
+        q[at] = np.where(side == 0, low[at] + (low[at] % 2), low[at] + (side > 0))
         q = np.where(bad, 0, q).astype(np.int8)
         scale = np.where(bad, np.nan, most * factor / 127)
     return q, scale[:, 0]

@@ -187,6 +187,37 @@ def test_quotients_next_to_borders(ops):
     check_rows(q, s, *i8.norm_rows((x / g).astype(np.float32), None, g, 1e-5)[1:], 33 * U)
 
 
+def border_codes(y, most):
+    """rint(127 y / most), ties to even, of whole numbers (Python's, of any size)."""
+    t = 254 * y + most  # 2 most (127 y / most + 1 / 2)
+    low = t // (2 * most)
+    return low - ((t % (2 * most) == 0) & (low % 2 == 1))
+
+
+@pytest.mark.parametrize("w", [100, 509, 1018, 4072])
+@pytest.mark.parametrize("shift", [0, -90])
+@pytest.mark.parametrize("part", [1.0, 0.04])
+def test_norms_at_exact_borders(ops, w, shift, part):
+    """Products h g of 48 bits whose quotient is a border exactly, or beside it by less than 64 bits tell: h = k j with |j| up
+    to 254.  (Shifted by 2^-90 the row is done in 64 bits as a whole; where all odd j stay there are more than are noted.)"""
+    rng = np.random.default_rng(w)
+    n = 64
+    k = rng.integers(20000, 33000, size=(n, 1)) * 2 + 1
+    j = rng.permutation(np.resize(np.arange(-254, 255), w))
+    j = np.where(rng.random(w) < part, j, j // 2 * 2)
+    j[w // 2] = 254
+    h = (k * j).astype(np.int64)
+    one = int(rng.integers(2**22, 2**23)) * 2 + 1
+    for g in (np.full(w, one), one + 2 * rng.integers(-1, 2, size=w)):
+        g[w // 2] = one
+        y = h.astype(object) * g.astype(object)
+        want = border_codes(y, np.abs(y).max(1, keepdims=True)).astype(np.int8)
+        x = np.ldexp(h.astype(np.float64), shift).astype(np.float32)
+        q, s = codes_room(n, w), torch.empty(n, device="cuda")
+        ops.tqd_op_rmsnorm_i8(dev(x), None, dev(np.ldexp(g.astype(np.float64), -23).astype(np.float32)), 1e-6, None, q, s)
+        assert np.array_equal(q.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("w", [40, 300, 2048, 5000])
 def test_gates_far_below_zero(ops, w):
     """Their silu is nothing, however large they are and whatever they meet in up."""

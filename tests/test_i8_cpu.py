@@ -67,6 +67,15 @@ def test_codes_of_ties_and_special_rows():
     assert np.all(np.isnan(s[1:4])) and not q[1:4].any() and list(q[4]) == [127, 0, 0, 0, -127] and s[5] == 0
 
 
+def test_codes_of_products_at_exact_borders():
+    """Ties that a quotient in 64 bits does not see: |h| = k j, j up to 254, times g of 24 bits."""
+    rng = np.random.default_rng(3)
+    j = np.arange(-254, 255)
+    k, g = rng.integers(20000, 33000, size=(40, 1)) * 2 + 1, rng.integers(2**22, 2**23, size=(40, 1)) * 2 + 1
+    q, _ = i8.rows((k * j * g).astype(np.float64))  # 48 bits: exact
+    assert np.array_equal(q, np.broadcast_to(np.rint(j / 2), q.shape))
+
+
 def test_the_norms_scale_makes_rows_of_unit_mean_square():
     rng = np.random.default_rng(2)
     x = rng.normal(size=(3, 4096)).astype(np.float32) * np.float32(7)

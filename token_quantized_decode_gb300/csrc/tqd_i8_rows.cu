@@ -91,8 +91,20 @@ __device__ __noinline__ double exact_element(const I8RowsArgs& a, int64_t row, i
   return x / (1.0 + exp(-static_cast<double>(x))) * u;
 }
 
-// The code of y in a row whose largest value is `most`.
+// The code next to the border between `low` and low + 1: by the side of it that 127 y / most lies on, and on it the even
+// one.  Where y and most are exact (rows: 24 bits; the norm's products: 48) so is the side: the border times most has 56 bits,
+// in two parts.
+__device__ __forceinline__ float code_beside(float low, double y, double most) {
+  const double at = low + 0.5f, p = at * most, side = fma(127.0, y, -p) - fma(at, most, -p);
+  return side > 0.0 || (side == 0.0 && (static_cast<int>(low) & 1)) ? low + 1.f : low;
+}
+
+// The code of y in a row whose largest value is `most`.  (For the norm's products a quotient in f64 tells a border from what
+// lies beside it no more; up to a unit it finds what is below, for which a product with the reciprocal is enough.)
 __device__ __noinline__ float exact_code(double y, double most) { return static_cast<float>(rint(127.0 * y / most)); }
+__device__ __noinline__ float exact_code(double y, double inv, double most) {
+  return code_beside(static_cast<float>(floor(y * inv)), y, most);
+}
 
 // The largest of a and |b|, |c|; NaN where one of them is.
 __device__ __forceinline__ float max_abs(float a, float b, float c) {
@@ -172,17 +184,22 @@ __device__ __noinline__ void whole_row(const I8RowsArgs& a, int64_t row, int t, 
   }
   if (!isfinite(static_cast<float>(top))) lost = true;
   int8_t* q = a.q + row * a.q_stride;
-  for (int i = t; i < n; i += kT)
-    q[i] = lost || most == 0.0 ? 0 : static_cast<int8_t>(exact_code(exact_element<kKind>(a, row, i, h), most));
+  if (kKind == kI8Norm) {
+    const bool none = lost || most == 0.0;
+    const double inv = none ? 0.0 : 127.0 / most;
+    for (int i = t; i < n; i += kT) {
+      q[i] = none ? 0 : static_cast<int8_t>(exact_code(exact_element<kKind>(a, row, i, h), inv, most));
+    }
+  } else {
+    for (int i = t; i < n; i += kT)
+      q[i] = lost || most == 0.0 ? 0 : static_cast<int8_t>(exact_code(exact_element<kKind>(a, row, i, h), most));
+  }
   if (t == 0 && !codes_only) a.scale[row] = lost ? __uint_as_float(0x7FC00000u) : static_cast<float>(top / 127.0);
 }
 
-// The code next to the border that 127 y / most lies at: by its side, and on it the even one.
+// The code of y where 127 y / most is known to lie at a border.
 __device__ __forceinline__ int8_t code_at_border(double y, double most) {
-  const float low = floorf(static_cast<float>(y) * (127.f / static_cast<float>(most)));
-  const double side = fma(127.0, y, -(low + 0.5) * most);
-  const int c = static_cast<int>(low);
-  return static_cast<int8_t>(side > 0.0 || (side == 0.0 && (c & 1)) ? c + 1 : c);
+  return static_cast<int8_t>(code_beside(floorf(static_cast<float>(y) * (127.f / static_cast<float>(most))), y, most));
 }
 
 // Elements next to borders, and those that may be a row's largest, of up to kWindow rows of a group of threads: they
