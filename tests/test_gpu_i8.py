@@ -266,6 +266,39 @@ def test_a_row_is_the_same_beside_any_others(ops, n, w):
         assert torch.equal(q, one_q) and torch.equal(s, one_s)
 
 
+@pytest.mark.parametrize("w,alone", [(300, 4256), (2048, 760), (5000, 304)])
+def test_borders_that_64_bits_hardly_tell_beside_any_rows(ops, w, alone):
+    """SwiGLU products within 2^-41 of a border, where the value that an element is settled by decides: in rows whose block has
+    listed other rows' elements up to its last place before, and by themselves.  (alone: the rows that blocks begin with.)"""
+    rng = np.random.default_rng(w)
+    g0, u0 = np.float64(8), np.float64(np.float32(0.3))
+    silu = lambda g: g / (1 + np.exp(-g))  # noqa: E731
+    most = silu(g0) * u0
+    n = 12_000_000
+    # (e^-g halfway between two powers of two, where a series in what is left is at its worst)
+    g = -np.log(2) * (rng.integers(0, 6, size=n) + 0.5 + rng.uniform(-0.03, 0.03, size=n))
+    g = g.astype(np.float32).astype(np.float64)
+    border = (rng.integers(1, 126, size=n) + 0.5) * most / 127
+    u = -(border / silu(g)).astype(np.float32).astype(np.float64)
+    near = np.nonzero(np.abs(-silu(g) * u / border - 1) < 2.0**-41)[0]
+    assert near.size > 100
+    gate, up = (rng.normal(size=(2, alone, w)) * 0.3).astype(np.float32)
+    gate[:, 3], up[:, 3] = g0, u0
+    for i, k in enumerate(near):
+        r, c = i % alone, 4 + i // alone
+        gate[r, c], up[r, c] = g[k], u[k]
+    q, s = codes_room(alone, w), torch.empty(alone, device="cuda")
+    ops.tqd_op_silu_mul_i8(dev(gate), dev(up), q, s)
+    full = np.concatenate([np.full((alone, w), 1.5, dtype=np.float32), gate]), np.concatenate([np.full((alone, w), 2, dtype=np.float32), up])
+    both, scale = codes_room(2 * alone, w), torch.empty(2 * alone, device="cuda")
+    ops.tqd_op_silu_mul_i8(dev(full[0]), dev(full[1]), both, scale)
+    assert torch.equal(both[alone:], q) and torch.equal(scale[alone:], s)
+    assert bool((both[:alone] == 127).all())
+    # (all codes but those at the borders are the exact ones)
+    differ = np.nonzero(q.cpu().numpy() != i8.silu_rows(gate, up)[0])
+    assert set(zip(*(d.tolist() for d in differ))) <= {(i % alone, 4 + i // alone) for i in range(near.size)}
+
+
 @pytest.mark.parametrize("n,w", [(100000, 40), (30000, 260), (12000, 1100)])
 def test_many_rows_a_block(ops, n, w):
     """Blocks that go over more rows than they keep notes of at once."""

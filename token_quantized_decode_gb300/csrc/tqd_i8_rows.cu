@@ -226,6 +226,29 @@ struct Pending {
   }
 };
 
+// The codes next to borders of a SwiGLU row that had no room in the list: the same elements by the same values as the list's,
+// so that what a row becomes does not depend on what else was in the list.  (The norm's values are exact either way.)
+template <int kT>
+__device__ __noinline__ void settle_silu(const I8RowsArgs& a, int64_t row, int t, double* sh) {
+  const int n = a.n;
+  const float *gate = a.x + row * a.x_stride, *up = a.other + row * a.other_stride;
+  float m = 0.f;
+#pragma unroll 1
+  for (int i = t; i < n; i += kT) m = fmaxf(m, fabsf(silu(gate[i]) * up[i]));
+  auto larger = [](double p, double q) { return fmax(p, q); };
+  const float inv = 127.f / static_cast<float>(RowGroup<kT>::all(m, sh, larger));
+  double most = 0.0;
+#pragma unroll 1
+  for (int i = t; i < n; i += kT)
+    if (fabsf(fmaf(silu(gate[i]) * up[i], inv, kMagic) - kMagic) > 126.f) most = fmax(most, fabs(near_silu(gate[i], up[i])));
+  most = RowGroup<kT>::all(most, sh, larger);
+#pragma unroll 1
+  for (int i = t; i < n; i += kT) {
+    const float v = silu(gate[i]) * up[i], c = fmaf(v, inv, kMagic);
+    if (fabsf(fmaf(v, inv, kMagic - c)) > 0.5f - kBand<kI8Silu>) a.q[row * a.q_stride + i] = code_at_border(near_silu(gate[i], up[i]), most);
+  }
+}
+
 template <int kKind, int kT>
 __device__ __noinline__ void settle(const I8RowsArgs& a, Pending<kT>& p, int64_t first, int64_t step, int t, double* sh) {
   RowGroup<kT>::sync();
@@ -249,7 +272,10 @@ __device__ __noinline__ void settle(const I8RowsArgs& a, Pending<kT>& p, int64_t
       a.q[(first + r * step) * a.q_stride + i] = code_at_border(p.y[e], __longlong_as_double(static_cast<long long>(p.most[r])));
   }
   for (int r = 0; over && r < kWindow; ++r)
-    if ((over >> r) & 1u) whole_row<kKind, kT>(a, first + r * step, t, sh, true);  // (its scale depends on no other row)
+    if ((over >> r) & 1u) {
+      if (kKind == kI8Silu) settle_silu<kT>(a, first + r * step, t, sh);
+      else whole_row<kKind, kT>(a, first + r * step, t, sh, true);  // (its scale depends on no other row)
+    }
   if (some) RowGroup<kT>::sync();
   p.clear(t);  // (a block's next entries come after the next row's barrier)
   if (kT == 32) __syncwarp();
