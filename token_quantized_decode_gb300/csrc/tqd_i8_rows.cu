@@ -265,7 +265,12 @@ __device__ __noinline__ void settle(const I8RowsArgs& a, Pending<kT>& p, int64_t
     if (x & 0x8000u) atomicMax(&p.most[r], static_cast<unsigned long long>(__double_as_longlong(fabs(y))));
   }
   RowGroup<kT>::sync();
-  for (int e = some ? t : n; e < n; e += kT) {
+  if (!some) {  // (nothing to settle, however many may be the largest)
+    p.clear(t);
+    if (kT == 32) __syncwarp();
+    return;
+  }
+  for (int e = t; e < n; e += kT) {
     const uint32_t x = p.entry[e];
     const int r = x >> 16, i = x & 0x7FFF;
     if (!(x & 0x8000u) && !((over >> r) & 1u))
@@ -276,7 +281,7 @@ __device__ __noinline__ void settle(const I8RowsArgs& a, Pending<kT>& p, int64_t
       if (kKind == kI8Silu) settle_silu<kT>(a, first + r * step, t, sh);
       else whole_row<kKind, kT>(a, first + r * step, t, sh, true);  // (its scale depends on no other row)
     }
-  if (some) RowGroup<kT>::sync();
+  RowGroup<kT>::sync();
   p.clear(t);  // (a block's next entries come after the next row's barrier)
   if (kT == 32) __syncwarp();
 }
