@@ -231,6 +231,22 @@ def test_gates_far_below_zero(ops, w):
     check_rows(q, s, *i8.silu_rows(gate, up), 8 * U)
 
 
+@pytest.mark.parametrize("w", [5, 64, 300, 1000, 2048, 4096, 8192, 12288])
+def test_gates_of_zero(ops, w):
+    """Rows of zeros whatever their up values are, but for products that f32 does not hold."""
+    rng = np.random.default_rng(w)
+    gate, up = np.zeros((8, w), dtype=np.float32), rng.normal(size=(8, w)).astype(np.float32)
+    gate[1], gate[2, ::2], up[2, 1::2] = -0.0, 1.0, 0.0
+    up[2, ::2] = 0
+    gate[3, w // 2], up[3, w // 2] = 1e-30, 1e-30
+    gate[4, w - 1], up[4, w - 1] = 1e-3, 1.0
+    up[5, 0] = np.inf
+    up[6, w - 1] = np.nan
+    q, s = codes_room(8, w), torch.empty(8, device="cuda")
+    ops.tqd_op_silu_mul_i8(dev(gate), dev(up), q, s)
+    check_rows(q, s, *i8.silu_rows(gate, up), 8 * U)
+
+
 @pytest.mark.parametrize("n,w", [(700, 300), (64, 2048), (40, 5000)])
 def test_rows_with_more_borders_than_are_kept(ops, n, w):
     """Products next to borders throughout: more of them than a group of rows has room to note."""

@@ -438,7 +438,16 @@ __global__ void __launch_bounds__(RowsCfg<kKind, kT, kE>::block, RowsCfg<kKind, 
     whole = false;
     if (kKind != kI8Rows) {
 #pragma unroll
-      for (int e = 0; e < kE; ++e) whole = whole || max_abs(max_abs(0.f, w[e][0], w[e][1]), w[e][2], w[e][3]) != 0.f;
+      for (int e = 0; e < kE; ++e) {
+        if (kKind == kI8Silu) {  // (w: up; the gates' place has the next row's)
+          float g[4];
+          load4<kVec>(a.x + row * a.x_stride, (e * kT + t) * 4, n, g);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) whole = whole || (g[j] != 0.f && w[e][j] != 0.f);
+        } else {
+          whole = whole || max_abs(max_abs(0.f, w[e][0], w[e][1]), w[e][2], w[e][3]) != 0.f;
+        }
+      }
       whole = RowGroup<kT>::any(whole);
     }
   }
