@@ -612,6 +612,11 @@ int32_t tqd_op_i8_matmul(const int8_t* w, const float* w_scale, int32_t rows, in
                          void* stream);
 size_t tqd_i8_matmul_scratch_bytes(int32_t rows, int32_t cols, int32_t n);
 
+/* How such a product is made, for programs that choose sizes by it (results do not depend on it): way[0] 0 int8 instructions of
+ * warps, 1 tiles of one CTA or a cluster, 2 tiles of a pair of CTAs; [1] tokens of an instruction's columns or a tile; [2] warps
+ * and [3] CTAs that share a row's columns; [4] tiles (0: groups of rows); [5] how many of them one after another. */
+int32_t tqd_i8_matmul_way(int32_t rows, int32_t cols, int32_t n, int64_t* way);
+
 /* How a table's angles are scaled for contexts longer than the training's.  With
  * f_i = theta^(-2 i / rotary_dim) and keep in [0, 1] (limited to it), pair i turns by f_i (keep +
  * (1 - keep) / factor) a position:

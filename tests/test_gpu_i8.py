@@ -391,6 +391,18 @@ def test_every_way_of_a_product(ops, rows, cols, n):
     assert torch.equal(y[:, :rows], want) and bool((y[:, rows:] == FULL).all())
 
 
+# More of the ways: int8 instructions with several groups of rows one after another (a ring that goes on from one to the next), by warps
+# that share columns and by single ones, and what else tests/test_i8_cpu.py asks for.  Rows that end inside a group.
+MORE_WAYS = [(50000, 64, 1), (38970, 32, 8), (151936, 1024, 3), (151930, 96, 5), (60001, 1024, 8), (39901, 416, 2), (100003, 640, 7),
+             (40000, 256, 16), (39580, 32, 9), (150007, 64, 13), (60009, 192, 10), (9800, 1824, 4), (300, 64, 12), (2100, 32, 16),
+             (100, 64, 2500), (240, 96, 2436), (261, 8192, 13)]
+
+
+@pytest.mark.parametrize("rows,cols,n", MORE_WAYS)
+def test_more_ways_of_a_product(ops, rows, cols, n):
+    test_every_way_of_a_product(ops, rows, cols, n)
+
+
 @pytest.mark.parametrize("rows,cols,n", [(40, 16384, 3), (130, 16384, 200), (130, 4096, 40), (260, 8192, 12), (16, 1056, 20)])
 def test_product_of_the_largest_codes(ops, rows, cols, n):
     """Sums far past 2^24, of one sign, of both, and with one odd term: a sum that was rounded on the way differs."""

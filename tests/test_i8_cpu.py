@@ -165,6 +165,31 @@ def test_product_sizes_and_refusals(L):
     refused(L, "tqd_op_i8_matmul", MUL, [dict(y=f(0)), dict(y=f(479)), dict(y=f(2019)), dict(y=f(4071)), dict(y=f(5001))], b"overlap")
 
 
+def test_the_products_sizes_take_every_way(L):
+    """Whatever kernel, width, sharing of columns and number of rounds a size can lead to, some size of the GPU tests leads to."""
+    pytest.importorskip("torch")
+    from tests import test_gpu_i8 as gpu
+
+    def kind(rows, cols, n):
+        kernel, tokens, warps, cluster, tiles, rounds = ops.tqd_i8_matmul_way(rows, cols, n)
+        assert tiles >= 1 and rounds >= 1 and 1 <= cluster <= 8 and warps in (1, 2, 4, 8)
+        return kernel, tokens, warps > 1, cluster > 1, rounds > 1
+    rows = [1, 17, 100, 240, 300, 700, 1300, 2100, 4096, 5120, 9800, 14000, 20000, 30000, 39000, 40000, 60000, 100000, 151936, 400000]
+    cols = [32, 64, 96, 160, 256, 416, 640, 960, 1024, 1824, 2560, 4096, 8192, 16384]
+    tokens = [1, 4, 8, 9, 12, 16, 17, 30, 32, 33, 64, 65, 100, 128, 150, 170, 185, 256, 304, 511, 700, 1000, 1500, 2048, 2436, 3323, 4096]
+    ways = {kind(r, c, n) for r in rows for c in cols for n in tokens}
+    assert len(ways) == 26
+    assert ways == {kind(*size) for size in gpu.PRODUCTS + gpu.WAYS + gpu.MORE_WAYS}
+
+
+def test_ways_of_refused_products(L):
+    way = (ctypes.c_int64 * 6)()
+    for bad in ((0, 96, 3), (20, 100, 3), (20, 16416, 3), (20, 96, 0), (20, 96, (1 << 20) + 1), ((1 << 24) + 1, 96, 3)):
+        assert L.tqd_i8_matmul_way(*bad, way) == BAD and b"tqd_i8_matmul_way" in L.tqd_last_error()
+    assert L.tqd_i8_matmul_way(20, 96, 3, None) == BAD
+    assert L.tqd_i8_matmul_way(1 << 24, 16384, 1 << 20, way) == 0
+
+
 @pytest.mark.parametrize("cols", [32, 96, 1024, 16384])
 def test_a_product_scratch_serves_every_smaller_call(L, cols):
     """The size never falls as rows, columns or tokens grow (a program keeps one for its largest batch)."""

@@ -142,6 +142,7 @@ def lib():
         "tqd_op_rows_i8_read": (i32, [vp, i64, vp, i32, i32, vp, i64, vp]),
         "tqd_op_i8_matmul": (i32, [vp, vp, i32, i32, vp, i64, vp, i32, vp, i64, vp, vp]),
         "tqd_i8_matmul_scratch_bytes": (sz, [i32, i32, i32]),
+        "tqd_i8_matmul_way": (i32, [i32, i32, i32, P(i64)]),
         "tqd_op_rope_table_scaled": (i32, [ctypes.c_float, i32, i32, P(tqd_rope_scaling), vp, vp]),
         "tqd_op_rope_rows": (i32, [vp, i64, vp, i32, i32, i32, vp, i32, i32, i32, vp, i64, vp]),
     }
@@ -204,7 +205,7 @@ def exported_symbols():
         "tqd_attention_q4_scratch_bytes", "tqd_op_q4_0_repack", "tqd_q4_0_matrix_bytes", "tqd_op_q4_0_matvec",
         "tqd_op_logprobs", "tqd_logprobs_scratch_bytes",
         "tqd_op_rows_i8", "tqd_op_rmsnorm_i8", "tqd_op_silu_mul_i8", "tqd_op_rows_i8_read", "tqd_op_i8_matmul",
-        "tqd_i8_matmul_scratch_bytes", "tqd_op_rope_table_scaled", "tqd_op_rope_rows",
+        "tqd_i8_matmul_scratch_bytes", "tqd_i8_matmul_way", "tqd_op_rope_table_scaled", "tqd_op_rope_rows",
     ]
 
 

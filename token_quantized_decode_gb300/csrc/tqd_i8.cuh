@@ -47,6 +47,13 @@ struct I8MatmulArgs {
   int rows, cols, n;
 };
 
+// How a product is made (tqd_i8_matmul_way in tqd.h).
+struct I8Way {
+  int kind, tokens, warps, cluster;
+  int64_t tiles, rounds;
+};
+I8Way i8_matmul_way(int rows, int cols, int n);
+
 // Four codes of a word as f16, exactly: a code's byte with its top bit turned is
 // code + 128, and as the low byte of 0x64xx it makes 1024 + code + 128.  lo holds
 // bytes 0 and 2, hi bytes 1 and 3; both operands of a product are taken apart in

@@ -180,29 +180,34 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2) k_i8_few(const I8MatmulArgs
   }
 }
 
-template <int kNT>
-cudaError_t launch_few(const I8MatmulArgs& a, cudaStream_t st) {
-  using Cfg = FewCfg<kNT>;
-  constexpr int kMost = Cfg::depth * Cfg::slot * 16;
-  static unsigned long long done = 0;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_few<kNT>), kMost, &done);
-  if (e != cudaSuccess) return e;
-  // How many warps and CTAs share 16 rows: what makes the busiest CTA's share least, counted in steps of two CTAs an SM
-  // (an SM's only CTA takes 0.6 of that, a group of rows one more, joining a cluster two).
-  constexpr int kClusters[9] = {0, 304, 152, 97, 74, 58, 46, 38, 36};  // that run at once
-  const int tiles = (a.rows + 15) / 16, pairs = (a.cols + 127) / 128;
-  int kw = 1, cs = 1, groups = 0;
+constexpr int kFewClusters[9] = {0, 304, 152, 97, 74, 58, 46, 38, 36};  // of 0 to 8 CTAs that run at once
+// How many warps and CTAs share 16 rows, and the groups of rows that a CTA or cluster has at a time: what makes the
+// busiest CTA's share least, counted in steps of two CTAs an SM (an SM's only CTA takes 0.6 of that, a group of rows one
+// more, joining a cluster two).
+void few_split(int rows, int cols, int& kw, int& cs, int& groups) {
+  const int tiles = (rows + 15) / 16, pairs = (cols + 127) / 128;
+  kw = cs = 1, groups = 0;
   float best = 0.f;
   for (int c = 1; c <= 8 && c <= pairs; c += c < 4 ? 1 : 2) {
     for (int k = 1; k <= kFewWarps && (k == 1 || k * c <= pairs); k *= 2) {
-      const int gr = (tiles + kFewWarps / k - 1) / (kFewWarps / k), waves = (gr + kClusters[c] - 1) / kClusters[c];
+      const int gr = (tiles + kFewWarps / k - 1) / (kFewWarps / k), waves = (gr + kFewClusters[c] - 1) / kFewClusters[c];
       if (c > 1 && waves > 1) break;
       const int steps = (pairs + k * c - 1) / (k * c);
       const float cost = waves * (steps * (static_cast<int64_t>(gr) * c > kSms ? 1.f : 0.6f) + 1.f) + (c > 1 ? 2.f : 0.f);
       if (groups == 0 || cost < best) best = cost, kw = k, cs = c, groups = gr;
     }
   }
-  const int clusters = groups < kClusters[cs] ? groups : kClusters[cs];
+}
+
+template <int kNT>
+cudaError_t launch_few(const I8MatmulArgs& a, const I8Way& way, cudaStream_t st) {
+  using Cfg = FewCfg<kNT>;
+  constexpr int kMost = Cfg::depth * Cfg::slot * 16;
+  static unsigned long long done = 0;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_i8_few<kNT>), kMost, &done);
+  if (e != cudaSuccess) return e;
+  const int kw = way.warps, cs = way.cluster, groups = static_cast<int>(way.tiles);
+  const int clusters = groups < kFewClusters[cs] ? groups : kFewClusters[cs], pairs = (a.cols + 127) / 128;
   const int steps = (pairs + kw * cs - 1) / (kw * cs) * ((groups + clusters - 1) / clusters);
   return launch_pdl_clusters(k_i8_few<kNT>, static_cast<unsigned>(cs), dim3(static_cast<unsigned>(clusters * cs)), 32 * kFewWarps,
                              (steps < Cfg::depth ? steps : Cfg::depth) * Cfg::slot * 16, st, a, kw, cs, groups);
@@ -718,37 +723,49 @@ size_t i8_matmul_scratch_bytes(int rows, int cols, int n) {
   return static_cast<size_t>(padded_tokens(n)) * ((cols + 127) / 128) * 128 * 2;
 }
 
-cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
+I8Way i8_matmul_way(int rows, int cols, int n) {
+  I8Way way{0, 8, 1, 1, 0, 0};
   // Up to 8 tokens: the int8 instructions keep up with memory (151936 x 1024 of 8: 30.3 us, k_i8_big 31.0).  Up to 16 they
   // do at half the rate, which is faster where a launch and the pipeline's filling are most of the time (4096 x 1024 of 16:
   // 4.4 and 6.2 us; 5120 x 960 5.9 and 7.0; 4096 x 4096 9.6 and 9.2; 151936 x 1024 45 and 31).
-  if (a.n <= 8) return launch_few<1>(a, st);
-  if (a.n <= 16 && static_cast<int64_t>(a.rows) * a.cols <= (12 << 20)) return launch_few<2>(a, st);
+  if (n <= 8 || (n <= 16 && static_cast<int64_t>(rows) * cols <= (12 << 20))) {
+    if (n > 8) way.tokens = 16;
+    int groups;
+    few_split(rows, cols, way.warps, way.cluster, groups);
+    way.tiles = groups, way.rounds = (groups + kFewClusters[way.cluster] - 1) / kFewClusters[way.cluster];
+    return way;
+  }
   // The width of a tile and the CTAs that share one: what takes least by these measured times in ns: 128 columns of a
   // tile, an image's kernel, a pair's beginning, a cluster's joining; a tile's beginning and end beside another's steps.
   constexpr int kWidths[6] = {16, 32, 64, 128, 160, 192}, kStep[6] = {320, 350, 430, 460, 430, 590};  // the last two: pairs
   constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};                        // that run at once
-  const int64_t row_tiles = (a.rows + kBigM - 1) / kBigM, steps = (a.cols + 127) / 128;
+  const int64_t row_tiles = (rows + kBigM - 1) / kBigM, steps = (cols + 127) / 128;
   int64_t best = -1;
-  int way = 0, cs = 1;
   for (int i = 0; i < 6; ++i) {
     const bool pair = i >= 4;
-    if (kWidths[i] > kRawMost && a.n <= kRawMost) break;  // (there is no scratch for an image)
-    const int64_t tiles = (pair ? (row_tiles + 1) / 2 : row_tiles) * ((a.n + kWidths[i] - 1) / kWidths[i]);
+    if (kWidths[i] > kRawMost && n <= kRawMost) break;  // (there is no scratch for an image)
+    const int64_t tiles = (pair ? (row_tiles + 1) / 2 : row_tiles) * ((n + kWidths[i] - 1) / kWidths[i]);
     for (int c = 1; c <= (pair ? 1 : 8) && c <= steps; ++c) {
       const int once = kClusters[pair ? 2 : c];
       if (c > 1 && tiles > once) break;
-      const int64_t cost = (tiles + once - 1) / once * ((steps + c - 1) / c * kStep[i] + 400) + (kWidths[i] > kRawMost ? 1500 : 0) +
+      const int64_t rounds = (tiles + once - 1) / once;
+      const int64_t cost = rounds * ((steps + c - 1) / c * kStep[i] + 400) + (kWidths[i] > kRawMost ? 1500 : 0) +
                            (pair ? 500 : 0) + (c > 1 ? 1800 + 8 * kWidths[i] : 0);
-      if (best < 0 || cost < best) best = cost, way = i, cs = c;
+      if (best < 0 || cost < best) best = cost, way = I8Way{pair ? 2 : 1, kWidths[i], 1, c, tiles, rounds};
     }
   }
-  switch (way) {
-    case 0: return launch_big<16>(a, cs, st);
-    case 1: return launch_big<32>(a, cs, st);
-    case 2: return launch_big<64>(a, cs, st);
-    case 3: return launch_big<128>(a, cs, st);
-    case 4: return launch_big<160, true>(a, 1, st);
+  return way;
+}
+
+cudaError_t launch_i8_matmul(const I8MatmulArgs& a, cudaStream_t st) {
+  const I8Way way = i8_matmul_way(a.rows, a.cols, a.n);
+  switch (way.tokens) {
+    case 8: return launch_few<1>(a, way, st);
+    case 16: return way.kind ? launch_big<16>(a, way.cluster, st) : launch_few<2>(a, way, st);
+    case 32: return launch_big<32>(a, way.cluster, st);
+    case 64: return launch_big<64>(a, way.cluster, st);
+    case 128: return launch_big<128>(a, way.cluster, st);
+    case 160: return launch_big<160, true>(a, 1, st);
     default: return launch_big<192, true>(a, 1, st);
   }
 }

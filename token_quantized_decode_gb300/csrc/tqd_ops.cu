@@ -447,6 +447,15 @@ size_t tqd_i8_matmul_scratch_bytes(int32_t rows, int32_t cols, int32_t n) {
   return i8_matmul_scratch_bytes(rows, cols, n);
 }
 
+int32_t tqd_i8_matmul_way(int32_t rows, int32_t cols, int32_t n, int64_t* way) {
+  if (!way || rows <= 0 || rows > kI8MaxRows || cols <= 0 || cols % 32 || cols > kI8MaxCols || n <= 0 || n > kI8MaxTokens)
+    return refuse("tqd_i8_matmul_way: NULL, or a size that tqd_op_i8_matmul refuses");
+  const I8Way w = i8_matmul_way(rows, cols, n);
+  const int64_t all[6] = {w.kind, w.tokens, w.warps, w.cluster, w.tiles, w.rounds};
+  for (int i = 0; i < 6; ++i) way[i] = all[i];
+  return TQD_OK;
+}
+
 int32_t tqd_op_i8_matmul(const int8_t* w, const float* w_scale, int32_t rows, int32_t cols, const int8_t* x,
                          int64_t x_stride, const float* x_scale, int32_t n, float* y, int64_t y_stride, void* scratch,
                          void* stream) {

@@ -3,7 +3,7 @@ include/tqd.h).  Each call marshals data pointers and the current stream into
 one C call; outputs are written into caller-allocated tensors."""
 from __future__ import annotations
 
-from ctypes import byref
+from ctypes import byref, c_int64
 
 from ._lib import TQDError, call_module, check, lib, tqd_kv_q4, tqd_rope_scaling
 
@@ -423,6 +423,13 @@ def tqd_op_rows_i8_read(q, scale, out, stream=None):
 
 def tqd_i8_matmul_scratch_bytes(rows: int, cols: int, n: int) -> int:
     return int(lib().tqd_i8_matmul_scratch_bytes(rows, cols, n))
+
+
+def tqd_i8_matmul_way(rows: int, cols: int, n: int) -> tuple:
+    """(kind, tokens, warps, cluster, tiles, rounds): how such a product is made."""
+    way = (c_int64 * 6)()
+    check(lib().tqd_i8_matmul_way(rows, cols, n, way), "tqd_i8_matmul_way")
+    return tuple(way)
 
 
 def tqd_op_i8_matmul(w, w_scale, x, x_scale, y, scratch=None, stream=None):
