@@ -447,12 +447,13 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
       }
     }
     // Whatever the others do, what is still under way lands before the CTA ends: copies, and each stage's last arrival at
-    // empty, which a commit makes by itself, in a pair at both CTAs.  (The readers waited for all at sums_full.  After a
-    // wait that ran out there may be none to come.)
+    // empty, which a commit makes by itself, in a pair at both CTAs.  (The oldest first: the last one comes when the
+    // products end.  The readers waited for all at sums_full.  After a wait that ran out there may be none to come.)
+    if (issued < Cfg::stages) s = 0, phase = 1;
     for (int i = 0; i < issued; ++i) {
-      if (--s < 0) s = Cfg::stages - 1, phase ^= 1;
-      mbar_wait_warp(&full[s], phase, kWaitLimitNs / 4);
-      mbar_wait_warp(&empty[s], phase, *dead ? 1000000ull : kWaitLimitNs / 4);
+      mbar_wait_warp(&full[s], phase ^ 1, kWaitLimitNs / 4);
+      mbar_wait_warp(&empty[s], phase ^ 1, *dead ? 1000000ull : kWaitLimitNs / 4);
+      if (++s == Cfg::stages) s = 0, phase ^= 1;
     }
   } else if (warp == 1) {
     // One thread, which looks for the next stage while this one's MMAs are issued: the tensor cores hold one or two
