@@ -572,12 +572,16 @@ size_t tqd_logprobs_scratch_bytes(int32_t rows, int32_t vocab, int32_t top_k);
  * the operators in 4 bits above: refusals before any launch, no rows no
  * launch, capturable, nothing allocated, the same result in every run.
  *
- * A row y of n values is held as scale = f32(max|y| / 127) and codes q = rint(127 y /
- * max|y|), ties to even, of the exact values (for rmsnorm: of h g, as 1 / rms is the
- * same for the whole row): an element stands for q * scale.  A row of zeros has scale 0
- * and codes 0.  A row with a NaN or an infinity, or whose largest value passes the f32
- * range, has scale NaN and codes 0: it stands for NaN, and so does what a product
- * makes of it.  rows <= 2^28, n <= 16384.  Row strides are in elements;
+ * A row y of n values is held as a scale, max|y| / 127 in f32, and codes q = rint(127 y /
+ * max|y|), ties to even: an element stands for q * scale.  The codes are those of the exact
+ * values (for rmsnorm: of h g, as 1 / rms is the same for the whole row); silu_mul knows its
+ * values to 2^-38, so an element that lies that near to a border between codes may fall to
+ * either side.  The scale of rows_i8 is the exact quotient rounded once; rmsnorm sums its
+ * squares, and silu_mul finds its largest value, in f32: relative errors of at most 33 and 9
+ * times 2^-24.  All are the same in every run and whatever other rows a call has.
+ * A row of zeros has scale 0 and codes 0.  A row with a NaN or an infinity, or whose
+ * largest value passes the f32 range, has scale NaN and codes 0: it stands for NaN, and so
+ * does what a product makes of it.  rows <= 2^28, n <= 16384.  Row strides are in elements;
  * outputs may not overlap inputs or one another, but for what is said below.
  * Elements between n and a row's stride are neither read nor written.
  * ------------------------------------------------------------------------ */
@@ -626,7 +630,8 @@ int32_t tqd_i8_matmul_way(int32_t rows, int32_t cols, int32_t n, int64_t* way);
  *                          original_len f_i / 2 pi, the pair's turns over the original length;
  *   TQD_ROPE_BY_INDEX      keep falls linearly over the index i from 1 at `from` to 0 at `to`, the
  *                          indices whose pairs turn high_rotations times (rounded down, not below
- *                          0) and low_rotations times (rounded up, not above rotary_dim - 1).
+ *                          0) and low_rotations times (rounded up, not above rotary_dim - 1);
+ *                          where `to` does not come after `from`, 1 up to `from` and 0 past it.
  * cos and sin are multiplied by attention_factor (1: none). */
 enum { TQD_ROPE_UNSCALED = 0, TQD_ROPE_LINEAR = 1, TQD_ROPE_BY_ROTATIONS = 2, TQD_ROPE_BY_INDEX = 3 };
 typedef struct tqd_rope_scaling {

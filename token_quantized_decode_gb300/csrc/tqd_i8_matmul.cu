@@ -2,10 +2,12 @@
 // y[j][r] = x_scale[j] w_scale[r] sum_c x[j][c] w[r][c].
 //
 // The sums are exact, so that their order, and how they are split, changes nothing.  The int8
-// tensor instructions of this part (an m16n8k32 in 16.3 clocks an SM) have a quarter of the rate of f16's
-// (an m16n8k16 in 2.0), and the fifth generation's f16 products are 2.6 times as fast again.  Few tokens take them all the same: memory is the bound there.  For more, codes become f16 operands
-// (exact), products are exact in the f32 accumulator, and so are sums of up to 1024 of them
-// (128 * 128 * 1024 = 2^24); a run of at most 1024 columns is added to a 32-bit whole number.
+// tensor instructions of this part (an m16n8k32 in 16.3 clocks an SM) have a quarter of the
+// rate of f16's (an m16n8k16 in 2.0), and the fifth generation's f16 products are 2.6 times as
+// fast again.  Few tokens take them all the same: memory is the bound there.  For more, codes
+// become f16 operands (exact), products are exact in the f32 accumulator, and so are sums of
+// up to 1024 of them (128 * 128 * 1024 = 2^24); a run of at most 1024 columns is added to a
+// 32-bit whole number.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -49,7 +51,7 @@ __device__ __forceinline__ int4 ld_rank4(const int* p, int rank) {
 // of a cluster share 16 rows: piece p of the kw cs has the steps p, p + kw cs, ...
 //
 // Measured (us, from a graph): 1024 x 1024 of 1 2.1, 4096 x 1024 of 1 2.9 (a launch by itself 1.0), 8192 x 8192 of 1
-// 15.0 (4.5 TB/s), 151936 x 1024 of 1 29.2 (5.3 TB/s, 79 % of the measured copy rate; a plain fill of
+// 15.1 (4.4 TB/s), 151936 x 1024 of 1 29.6 (5.3 TB/s, 78 % of the measured copy rate; a plain fill of
 // that many bytes reaches 5.5 TB/s).  Memory and, below 10 MB, one memory latency after another bound it.
 constexpr int kFewWarps = 8;
 // Eight tokens in each of kNT instructions.
@@ -228,10 +230,10 @@ cudaError_t launch_few(const I8MatmulArgs& a, const I8Way& way, cudaStream_t st)
 // What bounds a CTA by itself is what its SM takes in: about 57 bytes a clock were the most, of which a step
 // of 128 x 128 needs 48 KB, 860 clocks of which the products are 512.  So where there are many tiles a pair of CTAs makes
 // 256 rows with one instruction and each brings half of the tokens: 8192 x 8192 of 2048 took 199 us with 128 x 128
-// and takes 165 to 169 with pairs of 160 tokens (85 % of the measured bf16 rate), 16384 x 4096 of 4096 378 and 309 (91 %).  Tensor
+// and takes 164 to 169 with pairs of 160 tokens (86 % of the measured bf16 rate), 16384 x 4096 of 4096 378 and 309 (93 %).  Tensor
 // memory is what limits a pair's width: two accumulators of kTN columns and the slots of A.  192 tokens leave
 // room for four slots of 64 columns only, whose steps are slower for their work (295 ns for 64 columns, 215 for 160 tokens), but 511
-// tokens are three tiles of them and four of 160 (5120 x 960: 13.0 and 15.1 us).
+// tokens are three tiles of them and four of 160 (5120 x 960: 12.9 and 15.1 us).
 constexpr int kBigM = 128;
 constexpr int kConverters = 2;               // groups of four warps
 
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(BigCfg<kTN, kPair>::threads, 1)
 }
 
 // The tokens' codes as f16 in the order of k_i8_big's shared memory: [step][8 tokens][column / 8][token][8],
-// zeros past the last token and column.  A thread takes 16 codes.  (5120 x 960 of 511: 2.1 of the 13.0 us, with its launch.)
+// zeros past the last token and column.  A thread takes 16 codes.  (5120 x 960 of 511: 2.1 of the 12.9 us, with its launch.)
 template <int kK>
 __global__ void __launch_bounds__(256) k_i8_image(const int8_t* x, int64_t x_stride, int n, int cols, int padded, int steps,
                                                   uint8_t* image) {

@@ -2,12 +2,16 @@
 // and a code for each element, rint(127 y / max|y|).  Three kinds of row:
 // y = x; the RMSNorm of x + other; silu(gate) * up.  And the way back.
 //
-// The codes are those of the exact values.  In f32 the quotient t = 127 y / max|y| is
-// known to within kBand; where t lies that near to a border between two codes,
-// and only there, it is taken again in f64, with the row's largest value in f64 too.
-// A row whose largest value or sum of squares leaves the middle of the f32 range
-// is done in f64 as a whole, so neither squares nor products overflow or vanish.  The norm's
-// 1 / rms multiplies every element alike: it is in the scale and not in the codes.
+// The codes are those of the exact values (SwiGLU's: of values known to 2^-38).  In f32
+// the quotient t = 127 y / max|y| is known to within kBand; where t lies that near to a
+// border between two codes, and only there, it is taken again in f64, with the row's
+// largest value in f64 too.  A row whose largest value or sum of squares leaves the middle
+// of the f32 range is done in f64 as a whole, so neither squares nor products overflow or
+// vanish.  The norm's 1 / rms multiplies every element alike: it is in the scale and not
+// in the codes.  A scale is found in f32.  Rows: one rounding.  The norm, in units of 2^-24:
+// the sum of squares 52 (chains of 16, a warp's 5 steps, up to 31 warps more), / n and + eps
+// 2, all halved by the root; the root, its reciprocal, the largest h g, its product with
+// that, / 127: 5; 32 in all.  SwiGLU: its largest value 8 (see kBand), / 127: 9.
 #include <cuda_runtime.h>
 #include <float.h>
 
@@ -20,15 +24,17 @@ namespace {
 
 constexpr int kSms = 152;
 
-// The relative errors that reach t, in units of 2^-24, times 127: of y (exact for rows; the product h g, 1; silu:
-// e^-g 5, 1 + e, the quotient and the product with up 1 each), of the largest y the same, of 127 / max and of
-// the product with it 1 each.  2 * 127 * 2^-24 < 2^-16, 4 * 127 * 2^-24 < 2^-15, 18 * 127 * 2^-24 < 1.125 * 2^-13.
+// The relative errors that reach t, in units of 2^-24, times 127: of y (exact for rows; the
+// product h g, 1; silu: e^-g 5, 1 + e, the quotient and the product with up 1 each), of the
+// largest y the same, of 127 / max and of the product with it 1 each.
+// 2 * 127 * 2^-24 < 2^-16, 4 * 127 * 2^-24 < 2^-15, 18 * 127 * 2^-24 < 1.125 * 2^-13.
 template <int kKind>
 constexpr float kBand = kKind == kI8Rows ? 0x1p-16f : kKind == kI8Norm ? 0x1p-15f : 0x1.2p-13f;
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: added, it leaves the nearest whole number in the low bits
 
-// e^x for x <= 87 within 5 units: 2^t, t = x log2 e rounded, times 1 + ln 2 (x log2 e - t).  (Far below zero 2^t is 0.)
+// e^x for x <= 87 within 5 units: 2^t, t = x log2 e rounded, times 1 + ln 2 (x log2 e - t).
+// (Far below zero 2^t is 0.)
 __device__ __forceinline__ float exp_near(float x) {
   constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147182f;
   const float t = x * kLog2e, left = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
@@ -36,9 +42,10 @@ __device__ __forceinline__ float exp_near(float x) {
   asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
   return fmaf(e * kLn2, left, e);
 }
-// g / (1 + e^-g): the quotient from the approximate reciprocal and one step of Newton's iteration, within a unit.
-// (e^87 is the largest that leaves the reciprocal in range.  Below it the value is too large, by |g| e^-87 at most, 2^-89
-// of gates down to -2^36: nothing beside the largest of a row that is done here.)
+// g / (1 + e^-g): the quotient from the approximate reciprocal and one step of Newton's
+// iteration, within a unit.  (e^87 is the largest that leaves the reciprocal in range.  Below
+// it the value is too large, by |g| e^-87 at most, 2^-89 of gates down to -2^36: nothing beside
+// the largest of a row that is done here.)
 __device__ __forceinline__ float silu(float g) {
   const float d = 1.f + exp_near(fminf(-g, 87.f));
   float r;
@@ -47,10 +54,11 @@ __device__ __forceinline__ float silu(float g) {
   return fmaf(fmaf(-d, q, g), r, q);
 }
 
-// silu(g) u to 2^-38, for gates whose e^-g is within f32: of a row whose largest |y| is at least 2^-40
-// and whose |g| and |u| are at most 2^36, elements of at least a 2^8th of the largest have g > -62.  The f64 pipe does a
-// warp's instruction in 15 clocks, so this takes the reduction to |r| <= ln 2 / 2 with ln 2 in two parts (Cody and
-// Waite), the Taylor series with the terms from r^6 on in f32 (less than 2^-18 of the whole), and one step of
+// silu(g) u to 2^-38 (the worst found: 2^-41), for gates whose e^-g is within f32: of a row whose
+// largest |y| is at least 2^-40 and whose |g| and |u| are at most 2^36, elements of at least a
+// 2^8th of the largest have g > -62.  The f64 pipe does a warp's instruction in 15 clocks, so
+// this takes the reduction to |r| <= ln 2 / 2 with ln 2 in two parts (Cody and Waite), the Taylor
+// series with the terms from r^6 on in f32 (less than 2^-18 of the whole), and one step of
 // Newton's iteration from the f32 reciprocal in place of exp and a division.
 constexpr double kLn2High = 0.6931471804855391, kLn2Low = 7.440617110012397e-11;  // 33 bits after the point, and the rest
 __device__ __forceinline__ double near_silu(float g, float u) {
@@ -301,8 +309,8 @@ struct RowsCfg {
   };
 
 // kT threads a row, kE groups of four elements a thread.  Measured, in TB/s of the bytes that it must move (a copy of
-// as many: 6.8): rows 4099 x 4096 5.2 (16.3 us), norm with a sum that is kept 5.5 (39.4), SwiGLU 5.3
-// (28.6); a single row of 1024 1.2, 2.0 and 2.1 us.  HBM bounds the norm up to 4096 columns; wider rows have two
+// as many: 6.8): rows 4099 x 4096 5.1 (16.4 us), norm with a sum that is kept 5.5 (39.6), SwiGLU 5.2
+// (28.8); a single row of 1024 1.2, 2.0 and 2.1 us.  HBM bounds the norm up to 4096 columns; wider rows have two
 // CTAs or one an SM, which wait at a row's barrier together (1500 x 12288 norm 3.8 TB/s); SwiGLU's instructions
 // (2.6 a clock and SM) and its barrier bound it.  kVec: every row of every tensor
 // begins on a 16-byte boundary (codes: 4) and is whole groups of four.  CTAs go from row to
