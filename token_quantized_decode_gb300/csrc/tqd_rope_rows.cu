@@ -41,7 +41,7 @@ __device__ __forceinline__ void put(float* p, const float (&v)[kW]) {
 
 // A unit is 2 kW elements of a head: two runs of kW that turn together (halves), neighbours, or what follows the rotated part
 // (with kW = 1 one element of that).  A thread does one at a time, in few registers, so that an SM holds 2048 threads: that
-// many 16-byte loads are under way (8191 tokens of 20 heads of 128: 28.2 us, 89 % of the copy rate; with four units a
+// many 16-byte loads are under way (8191 tokens of 20 heads of 128: 28.3 us, 89 % of the copy rate; with four units a
 // thread at once, half as many threads, 34.7).
 template <int kW, bool kInter>
 __global__ void __launch_bounds__(256, 8) k_rope_rows(const RopeRowsArgs a, int tokens, int units, int per_head,
